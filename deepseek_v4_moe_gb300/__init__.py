@@ -11,5 +11,9 @@ Besides the block (``MoeFFN.forward``, ``forward_host``), the handle offers the 
 prelude and post of a sublayer (``set_attn_hc``, ``hc_pre``, ``hc_post``: the attention sublayer's,
 or the FFN's on its own), several layers in one captured submission (``forward_layers``), and
 experts in MXFP8 (``set_mxfp8_experts``).
+
+The dense feed-forward sublayer on a plain residual stream needs no handle (``dense``):
+``block_norm`` (the norms around a block with its gate and residual scale) and its gradients.
 """
 from .api import MoeFFN, MoeFFNError, config_from  # noqa: F401
+from .dense import block_norm, block_norm_backward  # noqa: F401

@@ -43,6 +43,25 @@ MXFP8_FIELDS = ["gate_exps", "gate_exps_scale", "up_exps", "up_exps_scale", "dow
 class MoeFfnMxfp8Experts(ctypes.Structure):
     _fields_ = [(n, c_vp) for n in MXFP8_FIELDS]
 
+c_i64, c_sz = ctypes.c_int64, ctypes.c_size_t
+
+TYPE_F32, TYPE_BF16, TYPE_F16 = 0, 1, 2
+GATE_NONE, GATE_VECTOR, GATE_TOKEN = 0, 1, 2
+
+
+class MoeFfnBlockNormArgs(ctypes.Structure):
+    _fields_ = [("rows", c_i32), ("hidden", c_i32), ("stream_type", c_i32), ("block_type", c_i32),
+                ("gate_type", c_i32), ("gate_kind", c_i32), ("rows_per_gate", c_i32), ("residual_scale", c_f32),
+                ("eps", c_f32), ("state", c_vp), ("ld_state", c_i64), ("f", c_vp), ("ld_f", c_i64), ("gate", c_vp),
+                ("norm_f", c_vp), ("norm_next", c_vp), ("out", c_vp), ("ld_out", c_i64), ("y", c_vp), ("ld_y", c_i64)]
+
+
+class MoeFfnBlockNormGrads(ctypes.Structure):
+    _fields_ = [("d_out", c_vp), ("ld_d_out", c_i64), ("d_y", c_vp), ("ld_d_y", c_i64), ("d_state", c_vp),
+                ("ld_d_state", c_i64), ("d_f", c_vp), ("ld_d_f", c_i64), ("d_gate", c_vp), ("d_norm_f", c_vp),
+                ("d_norm_next", c_vp), ("workspace", c_vp), ("workspace_bytes", c_sz)]
+
+
 # return codes and device status bits (include/moe_ffn.h)
 OK, ERR_NULL_PTR, ERR_BAD_CONFIG, ERR_LAYER_RANGE, ERR_ROWS_ZERO, ERR_ROWS_RANGE = 0, -1, -2, -3, -4, -5
 ERR_NO_ROUTING_SOURCE, ERR_ALIAS, ERR_CUDA, ERR_NO_MEMORY, ERR_UNSUPPORTED, ERR_ALIGNMENT, ERR_NO_WEIGHTS = (
@@ -55,7 +74,7 @@ _lib = None
 def declared_functions() -> list[str]:
     """Names of the functions include/moe_ffn.h declares."""
     text = open(HEADER).read()
-    return sorted(set(re.findall(r"^\s*(?:int|void|const char \*)\s*(moe_ffn_\w+)\s*\(", text, re.M)))
+    return sorted(set(re.findall(r"^\s*(?:int|int64_t|void|const char \*)\s*(moe_ffn_\w+)\s*\(", text, re.M)))
 
 
 def load(build: bool = True):
@@ -103,6 +122,13 @@ def load(build: bool = True):
     lib.moe_ffn_hc_post.restype = ctypes.c_int
     lib.moe_ffn_set_fault_injection.argtypes = [vp, i32, ctypes.c_uint32]
     lib.moe_ffn_set_fault_injection.restype = ctypes.c_int
+    norm, grads = ctypes.POINTER(MoeFfnBlockNormArgs), ctypes.POINTER(MoeFfnBlockNormGrads)
+    lib.moe_ffn_block_norm.argtypes = [norm, vp]
+    lib.moe_ffn_block_norm.restype = ctypes.c_int
+    lib.moe_ffn_block_norm_workspace.argtypes = [norm, grads]
+    lib.moe_ffn_block_norm_workspace.restype = c_i64
+    lib.moe_ffn_block_norm_backward.argtypes = [norm, grads, vp]
+    lib.moe_ffn_block_norm_backward.restype = ctypes.c_int
     lib.moe_ffn_last_error.argtypes = [vp]
     lib.moe_ffn_last_error.restype = ctypes.c_char_p
     lib.moe_ffn_destroy.argtypes = [vp]

@@ -1,0 +1,123 @@
+// Loads and stores of eight values of a row, as floats, for the dense sublayer's streaming kernels.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace moe {
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+
+// two floats rounded to a pair of T, the first in the low half
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  const T x = from_f32<T>(a), y = from_f32<T>(b);
+  return (uint32_t)*reinterpret_cast<const uint16_t *>(&x) | (uint32_t)*reinterpret_cast<const uint16_t *>(&y) << 16;
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
+  const __half2 v = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ void unpack2(uint32_t w, float &a, float &b, const __nv_bfloat16 *) {
+  a = bf_lo(w);
+  b = bf_hi(w);
+}
+__device__ __forceinline__ void unpack2(uint32_t w, float &a, float &b, const __half *) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+  a = f.x;
+  b = f.y;
+}
+
+// Eight values of one row that belong to thread t of a group of `n` threads.  VEC: columns 8t .. 8t+7
+// as 16-byte accesses (the row 16-byte aligned, hidden a multiple of 8).  Otherwise columns t, t + n,
+// t + 2n, ...: single accesses that neighbouring threads make side by side.  Columns from `hidden`
+// on read as zero and are not written.
+template <typename T, bool VEC>
+struct Eight {
+  T v[8];
+  __device__ __forceinline__ void load(const T *row, int t, int n, int hidden) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int c = e * n + t;
+      v[e] = c < hidden ? row[c] : from_f32<T>(0.f);
+    }
+  }
+  __device__ __forceinline__ void get(float (&o)[8]) const {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = to_f32(v[e]);
+  }
+  static __device__ __forceinline__ void store(T *row, int t, int n, int hidden, const float (&o)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int c = e * n + t;
+      if (c < hidden) row[c] = from_f32<T>(o[e]);
+    }
+  }
+};
+
+template <typename T>
+struct Eight<T, true> {
+  uint4 w;
+  __device__ __forceinline__ void load(const T *row, int t, int, int hidden) {
+    w = 8 * t < hidden ? *reinterpret_cast<const uint4 *>(row + 8 * t) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  __device__ __forceinline__ void get(float (&o)[8]) const {
+    const T *tag = nullptr;
+    unpack2(w.x, o[0], o[1], tag);
+    unpack2(w.y, o[2], o[3], tag);
+    unpack2(w.z, o[4], o[5], tag);
+    unpack2(w.w, o[6], o[7], tag);
+  }
+  static __device__ __forceinline__ void store(T *row, int t, int, int hidden, const float (&o)[8]) {
+    if (8 * t < hidden)
+      *reinterpret_cast<uint4 *>(row + 8 * t) =
+          make_uint4(pack2<T>(o[0], o[1]), pack2<T>(o[2], o[3]), pack2<T>(o[4], o[5]), pack2<T>(o[6], o[7]));
+  }
+};
+
+template <>
+struct Eight<float, true> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float *row, int t, int, int hidden) {
+    a = b = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (8 * t < hidden) {
+      a = *reinterpret_cast<const float4 *>(row + 8 * t);
+      b = *reinterpret_cast<const float4 *>(row + 8 * t + 4);
+    }
+  }
+  __device__ __forceinline__ void get(float (&o)[8]) const {
+    o[0] = a.x, o[1] = a.y, o[2] = a.z, o[3] = a.w, o[4] = b.x, o[5] = b.y, o[6] = b.z, o[7] = b.w;
+  }
+  static __device__ __forceinline__ void store(float *row, int t, int, int hidden, const float (&o)[8]) {
+    if (8 * t < hidden) {
+      *reinterpret_cast<float4 *>(row + 8 * t) = make_float4(o[0], o[1], o[2], o[3]);
+      *reinterpret_cast<float4 *>(row + 8 * t + 4) = make_float4(o[4], o[5], o[6], o[7]);
+    }
+  }
+};
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void load_eight(const T *row, int t, int n, int hidden, float (&o)[8]) {
+  Eight<T, VEC> e;
+  e.load(row, t, n, hidden);
+  e.get(o);
+}
+
+}  // namespace moe

@@ -1,0 +1,200 @@
+"""Python face of the dense feed-forward sublayer (plain residual stream): argument checks and
+marshalling over the C entry points of include/moe_ffn.h.
+
+Every function enqueues on ``stream`` (default: the tensors' device's current stream) and returns
+device tensors without waiting.  Outputs and workspaces that a call allocates belong to that stream.
+Gradients come from explicit ``*_backward`` calls; nothing is recorded for autograd.  Rows may be
+strided (``stride(-1) == 1``); weights and gates are contiguous.  Refused arguments raise
+``ValueError`` (types, shapes) or ``MoeFFNError`` with the library's code.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+import torch
+
+from . import _lib
+from ._lib import GATE_NONE, GATE_TOKEN, GATE_VECTOR, MoeFfnBlockNormArgs, MoeFfnBlockNormGrads
+from .api import MoeFFNError
+
+_TYPES = {torch.float32: _lib.TYPE_F32, torch.bfloat16: _lib.TYPE_BF16, torch.float16: _lib.TYPE_F16}
+
+
+def _raise(rc: int):
+    raise MoeFFNError(rc, _lib.load().moe_ffn_last_error(None).decode())
+
+
+def _on(device: torch.device, stream: Optional[torch.cuda.Stream]):
+    """The context to run a call in, or None where the current device and stream will do."""
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+        return torch.cuda.stream(stream)
+    if device.index != torch.cuda.current_device():
+        return torch.cuda.device(device)
+    return None
+
+
+def _matrix(name: str, t: torch.Tensor, device, shape, dtype) -> int:
+    """Checks a [rows, columns] tensor; returns the distance between its rows."""
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name} must be of shape {list(shape) if shape is not None else '[rows, columns]'}, "
+                         f"got {list(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _vector(name: str, t: torch.Tensor, device, n: int, dtype=torch.float32):
+    if not t.is_cuda or t.device != device or t.dtype != dtype or tuple(t.shape) != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA {dtype} [{n}] tensor on {device}")
+
+
+def _norm_args(state, f, norm_f, gate, residual_scale, norm_next, eps, block_dtype) -> MoeFfnBlockNormArgs:
+    dev = state.device
+    a = MoeFfnBlockNormArgs()
+    a.ld_state = _matrix("state", state, dev, None, None)
+    rows, hidden = state.shape
+    if state.dtype not in _TYPES or block_dtype not in _TYPES or state.dtype not in (torch.float32, block_dtype):
+        raise ValueError("state must be float32 or of the block's type (float32, bfloat16, float16)")
+    a.rows, a.hidden, a.stream_type, a.block_type = rows, hidden, _TYPES[state.dtype], _TYPES[block_dtype]
+    a.residual_scale, a.eps, a.state = residual_scale, eps, state.data_ptr()
+    if f is not None:
+        a.ld_f = _matrix("f", f, dev, (rows, hidden), None)
+        a.f = f.data_ptr()
+    elif gate is not None or norm_f is not None:
+        raise ValueError("gate and norm_f need f")
+    if norm_f is not None:
+        _vector("norm_f", norm_f, dev, hidden)
+        a.norm_f = norm_f.data_ptr()
+    if norm_next is not None:
+        _vector("norm_next", norm_next, dev, hidden)
+        a.norm_next = norm_next.data_ptr()
+    if gate is not None:
+        if gate.device != dev or gate.dtype not in (torch.float32, block_dtype) or not gate.is_contiguous():
+            raise ValueError("gate must be contiguous, on the state's device, float32 or of the block's type")
+        shape = tuple(gate.shape)
+        if shape == (hidden,):
+            a.gate_kind, a.rows_per_gate = GATE_VECTOR, max(rows, 1)
+        elif len(shape) == 2 and shape[1] == hidden and shape[0] > 0 and rows % shape[0] == 0 and rows > 0:
+            a.gate_kind, a.rows_per_gate = GATE_VECTOR, rows // shape[0]
+        elif shape == (rows, 1):
+            a.gate_kind = GATE_TOKEN
+        else:
+            raise ValueError(f"gate must be [{hidden}], [G, {hidden}] with G dividing {rows}, or [{rows}, 1]; "
+                             f"got {list(shape)}")
+        a.gate_type, a.gate = _TYPES[gate.dtype], gate.data_ptr()
+    else:
+        a.gate_kind = GATE_NONE
+    return a
+
+
+def block_norm(state: torch.Tensor, f: Optional[torch.Tensor] = None, *, norm_f: Optional[torch.Tensor] = None,
+               gate: Optional[torch.Tensor] = None, residual_scale: float = 1.0,
+               norm_next: Optional[torch.Tensor] = None, eps: float = 1e-6, block_dtype: Optional[torch.dtype] = None,
+               out: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+               stream: Optional[torch.cuda.Stream] = None):
+    """The norms before and after a block, with the block's gate and residual scale, in one pass.
+
+        n   = f * rsqrt(mean(f^2) + eps) * norm_f        (n = f without norm_f)
+        out = state + residual_scale * gate * n
+        y   = out * rsqrt(mean(out^2) + eps) * norm_next
+
+    ``state`` [rows, hidden] float32 or of the block's type; ``f`` [rows, hidden], the block's output,
+    float32, bfloat16 or float16; ``norm_f``, ``norm_next`` float32 [hidden]; ``gate`` [hidden],
+    [G, hidden] (each row for rows / G consecutive rows) or [rows, 1].  Without ``f`` only y, the norm of
+    ``state``, is made, in ``block_dtype`` (default: the state's type).  ``out`` may be ``state``.
+    Returns (out, y); y is None without ``norm_next``, out is ``state`` itself without ``f``.
+    """
+    if not state.is_cuda:
+        raise ValueError("state must be a CUDA tensor")
+    ctx = _on(state.device, stream)
+    if ctx is not None:
+        with ctx:
+            return block_norm(state, f, norm_f=norm_f, gate=gate, residual_scale=residual_scale, norm_next=norm_next,
+                              eps=eps, block_dtype=block_dtype, out=out, y=y)
+    bt = f.dtype if f is not None else (block_dtype or state.dtype)
+    if block_dtype is not None and block_dtype != bt:
+        raise ValueError("block_dtype must be f's type")
+    a = _norm_args(state, f, norm_f, gate, residual_scale, norm_next, eps, bt)
+    if f is not None:
+        if out is None:
+            out = torch.empty(state.shape, dtype=state.dtype, device=state.device)
+        a.ld_out = _matrix("out", out, state.device, state.shape, state.dtype)
+        a.out = out.data_ptr()
+    elif out is not None:
+        raise ValueError("out is written only with f")
+    if norm_next is not None:
+        if y is None:
+            y = torch.empty(state.shape, dtype=bt, device=state.device)
+        a.ld_y = _matrix("y", y, state.device, state.shape, bt)
+        a.y = y.data_ptr()
+    elif y is not None:
+        raise ValueError("y is written only with norm_next")
+    rc = _lib.load().moe_ffn_block_norm(ctypes.byref(a), torch.cuda.current_stream().cuda_stream)
+    if rc != 0:
+        _raise(rc)
+    return (out if f is not None else state), y
+
+
+def block_norm_backward(out: torch.Tensor, f: Optional[torch.Tensor] = None, *,
+                        norm_f: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                        residual_scale: float = 1.0, norm_next: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                        d_out: Optional[torch.Tensor] = None, d_y: Optional[torch.Tensor] = None,
+                        stream: Optional[torch.cuda.Stream] = None) -> dict:
+    """Gradients of :func:`block_norm`: ``out`` is what the forward call returned first (the stream after
+    the block; without ``f`` the state), the other arguments are the forward call's.
+
+    ``d_out`` (the stream's type) is the gradient that comes back along the stream, None for zero;
+    ``d_y`` goes with ``norm_next``.  Returns a dict of the gradients of what was given: d_state, d_f,
+    d_gate, d_norm_f and d_norm_next.
+    """
+    if not out.is_cuda:
+        raise ValueError("out must be a CUDA tensor")
+    ctx = _on(out.device, stream)
+    if ctx is not None:
+        with ctx:
+            return block_norm_backward(out, f, norm_f=norm_f, gate=gate, residual_scale=residual_scale,
+                                       norm_next=norm_next, eps=eps, d_out=d_out, d_y=d_y)
+    if f is None and norm_next is None:
+        raise ValueError("neither f nor norm_next is given")
+    if (norm_next is None) != (d_y is None):
+        raise ValueError("d_y goes with norm_next")
+    dev, shape = out.device, out.shape
+    bt = f.dtype if f is not None else d_y.dtype
+    a = _norm_args(out, f, norm_f, gate, residual_scale, norm_next, eps, bt)
+    g, d = MoeFfnBlockNormGrads(), {}
+    if d_out is not None:
+        g.ld_d_out, g.d_out = _matrix("d_out", d_out, dev, shape, out.dtype), d_out.data_ptr()
+    if d_y is not None:
+        g.ld_d_y, g.d_y = _matrix("d_y", d_y, dev, shape, bt), d_y.data_ptr()
+
+    def new(name, like_shape, dtype):
+        d[name] = torch.empty(like_shape, dtype=dtype, device=dev)
+        return d[name].data_ptr()
+
+    g.d_state, g.ld_d_state = new("d_state", shape, out.dtype), shape[1]
+    if f is not None:
+        g.d_f, g.ld_d_f = new("d_f", shape, bt), shape[1]
+    if gate is not None:
+        g.d_gate = new("d_gate", gate.shape, gate.dtype)
+    if norm_f is not None:
+        g.d_norm_f = new("d_norm_f", (shape[1],), torch.float32)
+    if norm_next is not None:
+        g.d_norm_next = new("d_norm_next", (shape[1],), torch.float32)
+    lib = _lib.load()
+    need = lib.moe_ffn_block_norm_workspace(ctypes.byref(a), ctypes.byref(g))
+    if need < 0:
+        _raise(need)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    if need:
+        g.workspace, g.workspace_bytes = ws.data_ptr(), need
+    rc = lib.moe_ffn_block_norm_backward(ctypes.byref(a), ctypes.byref(g), torch.cuda.current_stream().cuda_stream)
+    if rc != 0:
+        _raise(rc)
+    return d

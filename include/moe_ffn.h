@@ -298,6 +298,68 @@ int moe_ffn_set_mxfp8_experts(moe_ffn_handle *h, int32_t layer, const moe_ffn_mx
 #define MOE_FFN_INJECT_GEMM_WAIT 2
 int moe_ffn_set_fault_injection(moe_ffn_handle *h, int32_t which, uint32_t wait_limit_us);
 
+/* ---- The dense feed-forward sublayer on a plain residual stream --------------------------------
+ * The same sublayer without hyper-connections and without routing: a dense layer, a shared expert
+ * on its own, a draft head's layer.  These entry points take no handle.  Tensor arguments are
+ * device pointers of the current device, rows contiguous, consecutive rows `ld_*` elements apart
+ * (ld >= the row's length).  Calls enqueue on `stream` and return without waiting; each call that
+ * needs scratch takes it as `workspace`, which must not be in use by another call meanwhile (give
+ * graphs that may run together workspaces of their own).  They can be captured into CUDA graphs.
+ * All sums are in f32 and no atomics are used: the same call gives the same bits.  On an error
+ * nothing is enqueued, except that a failed launch may leave earlier kernels of the call enqueued;
+ * the message is moe_ffn_last_error(NULL) on the calling thread. */
+#define MOE_FFN_F32 0
+#define MOE_FFN_BF16 1
+#define MOE_FFN_F16 2
+
+#define MOE_FFN_GATE_NONE 0
+#define MOE_FFN_GATE_VECTOR 1 /* [ceil(rows / rows_per_gate), hidden], contiguous: one vector for each rows_per_gate rows */
+#define MOE_FFN_GATE_TOKEN 2  /* [rows]: one value for each row */
+
+/* The norms before and after a block, fused with its gate and residual scale:
+ *   n = f * rsqrt(mean(f^2) + eps) * norm_f      (n = f when norm_f is NULL)
+ *   out = state + residual_scale * gate * n      (rounded to stream_type as it is stored)
+ *   y = out * rsqrt(mean(out^2) + eps) * norm_next
+ * With f NULL there is no block before: y is the norm of state, out is not written. */
+typedef struct moe_ffn_block_norm_args {
+  int32_t rows, hidden;         /* 1 <= hidden <= 8192 */
+  int32_t stream_type;          /* type of state and out: MOE_FFN_F32 or block_type */
+  int32_t block_type;           /* type of f and y */
+  int32_t gate_type;            /* MOE_FFN_F32 or block_type */
+  int32_t gate_kind, rows_per_gate;
+  float residual_scale, eps;
+  const void *state; int64_t ld_state;  /* [rows, hidden] */
+  const void *f; int64_t ld_f;          /* [rows, hidden], or NULL */
+  const void *gate;
+  const float *norm_f, *norm_next;      /* [hidden], either may be NULL; norm_next exactly when y is */
+  void *out; int64_t ld_out;            /* may be state itself (same ld); no other overlap */
+  void *y; int64_t ld_y;
+} moe_ffn_block_norm_args;
+
+/* Returns MOE_FFN_OK, NULL_PTR, ROWS_ZERO, ROWS_RANGE, BAD_CONFIG (hidden, types, gate, ld),
+ * ALIGNMENT (a pointer not aligned to its type), ALIAS, UNSUPPORTED or CUDA. */
+int moe_ffn_block_norm(const moe_ffn_block_norm_args *a, void *stream);
+
+/* Gradients of block_norm.  `a` holds the call's arguments with `state` the stream AFTER the block
+ * (what the forward call wrote to out; with f NULL, its state); a->out and a->y are not read.
+ * d_state is the gradient that goes on to the stream before the block. */
+typedef struct moe_ffn_block_norm_grads {
+  const void *d_out; int64_t ld_d_out;  /* stream_type; NULL: zero */
+  const void *d_y; int64_t ld_d_y;      /* block_type; given exactly when norm_next is */
+  void *d_state; int64_t ld_d_state;    /* stream_type; may be d_out itself (same ld) */
+  void *d_f; int64_t ld_d_f;            /* block_type; given exactly when f is */
+  void *d_gate;                         /* gate_type, the gate's layout; may be NULL */
+  float *d_norm_f, *d_norm_next;        /* [hidden]; may be NULL */
+  void *workspace; size_t workspace_bytes; /* at least moe_ffn_block_norm_workspace, 16-byte aligned */
+} moe_ffn_block_norm_grads;
+
+/* The codes of moe_ffn_block_norm, and NO_MEMORY when the workspace is too small. */
+int moe_ffn_block_norm_backward(const moe_ffn_block_norm_args *a, const moe_ffn_block_norm_grads *g, void *stream);
+
+/* Bytes of workspace that block_norm_backward needs for these arguments (pointers are only compared
+ * with NULL); negative: an error code. */
+int64_t moe_ffn_block_norm_workspace(const moe_ffn_block_norm_args *a, const moe_ffn_block_norm_grads *g);
+
 /* Text of the last error on this handle, or, when h is NULL, of the last failed call made without
  * a handle (init, the allocation-free split, a NULL handle) on the calling thread: that message
  * is kept per thread, so threads that fail at the same time do not overwrite each other's text.

@@ -1,0 +1,76 @@
+"""The dense sublayer's C entry points without a GPU: the argument checks answer before any CUDA call."""
+import ctypes
+
+import pytest
+
+from deepseek_v4_moe_gb300 import _lib
+
+A = 1 << 20  # fake addresses, a MiB apart: never dereferenced, the checks that answer run first
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return _lib.load()
+
+
+def _norm(**kw):
+    base = dict(rows=4, hidden=256, stream_type=_lib.TYPE_F32, block_type=_lib.TYPE_BF16, gate_type=_lib.TYPE_BF16,
+                gate_kind=_lib.GATE_NONE, rows_per_gate=1, residual_scale=1.0, eps=1e-6, state=A, ld_state=256,
+                f=2 * A, ld_f=256, gate=None, norm_f=3 * A, norm_next=4 * A, out=5 * A, ld_out=256, y=6 * A, ld_y=256)
+    base.update(kw)
+    return _lib.MoeFfnBlockNormArgs(**base)
+
+
+NORM_REFUSED = [
+    (dict(rows=0), _lib.ERR_ROWS_ZERO), (dict(rows=-1), _lib.ERR_ROWS_RANGE), (dict(hidden=0), _lib.ERR_BAD_CONFIG),
+    (dict(hidden=8193), _lib.ERR_BAD_CONFIG), (dict(stream_type=_lib.TYPE_F16), _lib.ERR_BAD_CONFIG),
+    (dict(block_type=7), _lib.ERR_BAD_CONFIG), (dict(eps=-1.0), _lib.ERR_BAD_CONFIG),
+    (dict(eps=float("nan")), _lib.ERR_BAD_CONFIG), (dict(state=None), _lib.ERR_NULL_PTR),
+    (dict(f=None, norm_f=None, out=None, norm_next=None, y=None), _lib.ERR_NULL_PTR),
+    (dict(f=None, out=None), _lib.ERR_BAD_CONFIG),            # norm_f without f
+    (dict(ld_state=255), _lib.ERR_BAD_CONFIG), (dict(ld_f=0), _lib.ERR_BAD_CONFIG),
+    (dict(ld_out=255), _lib.ERR_BAD_CONFIG), (dict(ld_y=255), _lib.ERR_BAD_CONFIG),
+    (dict(out=None), _lib.ERR_NULL_PTR), (dict(y=None), _lib.ERR_NULL_PTR),
+    (dict(norm_next=None), _lib.ERR_NULL_PTR),                # y without norm_next
+    (dict(gate_kind=1), _lib.ERR_NULL_PTR), (dict(gate_kind=9, gate=7 * A), _lib.ERR_BAD_CONFIG),
+    (dict(gate_kind=1, gate=7 * A, rows_per_gate=0), _lib.ERR_BAD_CONFIG),
+    (dict(gate_kind=2, gate=7 * A, gate_type=_lib.TYPE_F16), _lib.ERR_BAD_CONFIG),
+    (dict(gate_kind=2, gate=7 * A + 1), _lib.ERR_ALIGNMENT), (dict(state=A + 2), _lib.ERR_ALIGNMENT),
+    (dict(y=6 * A + 1), _lib.ERR_ALIGNMENT), (dict(out=A + 4), _lib.ERR_ALIAS),
+    (dict(out=A, ld_out=260), _lib.ERR_ALIAS),                # the state's memory at another stride
+    (dict(y=2 * A), _lib.ERR_ALIAS), (dict(y=5 * A + 512), _lib.ERR_ALIAS), (dict(out=4 * A), _lib.ERR_ALIAS),
+    (dict(gate_kind=1, gate=5 * A + 16), _lib.ERR_ALIAS),
+]
+
+
+@pytest.mark.parametrize("kw,code", NORM_REFUSED)
+def test_block_norm_refuses(lib, kw, code):
+    assert lib.moe_ffn_block_norm(ctypes.byref(_norm(**kw)), None) == code, lib.moe_ffn_last_error(None)
+
+
+def _grads(**kw):
+    base = dict(d_out=8 * A, ld_d_out=256, d_y=9 * A, ld_d_y=256, d_state=10 * A, ld_d_state=256, d_f=11 * A,
+                ld_d_f=256, d_gate=None, d_norm_f=12 * A, d_norm_next=13 * A, workspace=14 * A, workspace_bytes=0)
+    base.update(kw)
+    return _lib.MoeFfnBlockNormGrads(**base)
+
+
+@pytest.mark.parametrize("kw,gkw,code", [
+    ({}, dict(d_state=None), _lib.ERR_NULL_PTR), ({}, dict(d_f=None), _lib.ERR_NULL_PTR),
+    ({}, dict(d_y=None), _lib.ERR_NULL_PTR), (dict(norm_next=None), {}, _lib.ERR_BAD_CONFIG),
+    ({}, dict(d_gate=15 * A), _lib.ERR_BAD_CONFIG), (dict(norm_f=None), {}, _lib.ERR_BAD_CONFIG),
+    ({}, dict(ld_d_f=100), _lib.ERR_BAD_CONFIG), ({}, dict(ld_d_out=255), _lib.ERR_BAD_CONFIG),
+    ({}, dict(d_state=10 * A + 1), _lib.ERR_ALIGNMENT), ({}, dict(workspace=14 * A + 8), _lib.ERR_ALIGNMENT),
+    ({}, dict(d_state=A), _lib.ERR_ALIAS), ({}, dict(d_f=9 * A), _lib.ERR_ALIAS),
+    ({}, dict(d_f=8 * A), _lib.ERR_ALIAS), ({}, dict(d_norm_f=13 * A + 4), _lib.ERR_ALIAS),
+    ({}, dict(workspace=10 * A, workspace_bytes=64), _lib.ERR_ALIAS),
+])
+def test_block_norm_backward_refuses(lib, kw, gkw, code):
+    rc = lib.moe_ffn_block_norm_backward(ctypes.byref(_norm(**kw)), ctypes.byref(_grads(**gkw)), None)
+    assert rc == code, lib.moe_ffn_last_error(None)
+
+
+def test_block_norm_null(lib):
+    assert lib.moe_ffn_block_norm(None, None) == _lib.ERR_NULL_PTR
+    assert lib.moe_ffn_block_norm_backward(ctypes.byref(_norm()), None, None) == _lib.ERR_NULL_PTR
+    assert lib.moe_ffn_block_norm_workspace(None, None) == _lib.ERR_NULL_PTR
