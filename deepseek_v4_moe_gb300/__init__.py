@@ -13,7 +13,9 @@ or the FFN's on its own), several layers in one captured submission (``forward_l
 experts in MXFP8 (``set_mxfp8_experts``).
 
 The dense feed-forward sublayer on a plain residual stream needs no handle (``dense``):
-``block_norm`` (the norms around a block with its gate and residual scale) and its gradients.
+``block_norm`` (the norms around a block with its gate and residual scale) and ``gated_ffn`` (the
+gated feed-forward block), each with its gradients; ``dense_status`` reads the device status bits.
 """
 from .api import MoeFFN, MoeFFNError, config_from  # noqa: F401
-from .dense import block_norm, block_norm_backward  # noqa: F401
+from .dense import (block_norm, block_norm_backward, dense_status, gated_ffn,  # noqa: F401
+                    gated_ffn_backward)

@@ -62,6 +62,17 @@ class MoeFfnBlockNormGrads(ctypes.Structure):
                 ("d_norm_next", c_vp), ("workspace", c_vp), ("workspace_bytes", c_sz)]
 
 
+ACTIVATIONS = {"silu": 0, "gelu": 1}
+
+
+class MoeFfnGatedArgs(ctypes.Structure):
+    _fields_ = [("rows", c_i32), ("hidden", c_i32), ("inter", c_i32), ("type", c_i32), ("activation", c_i32),
+                ("x", c_vp), ("ld_x", c_i64), ("w_gate", c_vp), ("w_up", c_vp), ("w_down", c_vp), ("y", c_vp),
+                ("ld_y", c_i64), ("gate", c_vp), ("up", c_vp), ("d_y", c_vp), ("ld_d_y", c_i64), ("d_x", c_vp),
+                ("ld_d_x", c_i64), ("d_w_gate", c_vp), ("d_w_up", c_vp), ("d_w_down", c_vp), ("workspace", c_vp),
+                ("workspace_bytes", c_sz)]
+
+
 # return codes and device status bits (include/moe_ffn.h)
 OK, ERR_NULL_PTR, ERR_BAD_CONFIG, ERR_LAYER_RANGE, ERR_ROWS_ZERO, ERR_ROWS_RANGE = 0, -1, -2, -3, -4, -5
 ERR_NO_ROUTING_SOURCE, ERR_ALIAS, ERR_CUDA, ERR_NO_MEMORY, ERR_UNSUPPORTED, ERR_ALIGNMENT, ERR_NO_WEIGHTS = (
@@ -129,6 +140,17 @@ def load(build: bool = True):
     lib.moe_ffn_block_norm_workspace.restype = c_i64
     lib.moe_ffn_block_norm_backward.argtypes = [norm, grads, vp]
     lib.moe_ffn_block_norm_backward.restype = ctypes.c_int
+    gated = ctypes.POINTER(MoeFfnGatedArgs)
+    lib.moe_ffn_gated_forward.argtypes = [gated, vp]
+    lib.moe_ffn_gated_forward.restype = ctypes.c_int
+    lib.moe_ffn_gated_backward.argtypes = [gated, vp]
+    lib.moe_ffn_gated_backward.restype = ctypes.c_int
+    lib.moe_ffn_gated_workspace.argtypes = [gated, i32]
+    lib.moe_ffn_gated_workspace.restype = c_i64
+    lib.moe_ffn_dense_status.argtypes = [vp]
+    lib.moe_ffn_dense_status.restype = ctypes.c_int
+    lib.moe_ffn_dense_fault_injection.argtypes = [i32, ctypes.c_uint32]
+    lib.moe_ffn_dense_fault_injection.restype = ctypes.c_int
     lib.moe_ffn_last_error.argtypes = [vp]
     lib.moe_ffn_last_error.restype = ctypes.c_char_p
     lib.moe_ffn_destroy.argtypes = [vp]

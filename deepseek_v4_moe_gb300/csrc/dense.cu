@@ -90,6 +90,69 @@ int pending(const char *who) {
                           : fail(MOE_FFN_ERR_CUDA, "%s: a CUDA error is pending from earlier work: %s", who, cudaGetErrorString(e));
 }
 
+// ---- what the tensor-core kernels share: status word, wait bound, tensor maps ----
+
+__device__ int g_status;      // device status bits since the last moe_ffn_dense_status
+__device__ int g_status_out;  // what that call reads
+
+__global__ void take_status_kernel() { g_status_out = atomicExch(&g_status, 0); }
+
+std::atomic<int> g_inject{0};
+std::atomic<unsigned> g_wait_us{0};
+
+struct DeviceSide {
+  int *status;
+  uint64_t wait_ns;
+  int inject;
+};
+
+int device_side(const char *who, DeviceSide *d) {
+  static std::atomic<int *> known[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices)
+    return fail(MOE_FFN_ERR_CUDA, "%s: no usable current device", who);
+  d->status = known[dev].load(std::memory_order_acquire);
+  if (!d->status) {
+    void *p = nullptr;
+    const cudaError_t e = cudaGetSymbolAddress(&p, g_status);
+    if (e != cudaSuccess || !p) return fail(MOE_FFN_ERR_CUDA, "%s: cudaGetSymbolAddress: %s", who, cudaGetErrorString(e));
+    d->status = static_cast<int *>(p);
+    known[dev].store(d->status, std::memory_order_release);
+  }
+  const unsigned us = g_wait_us.load(std::memory_order_relaxed);
+  d->wait_ns = us ? (uint64_t)us * 1000u : 2000000000ull;
+  d->inject = g_inject.load(std::memory_order_relaxed);
+  return MOE_FFN_OK;
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn find_encode() {
+  void *p = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+      q == cudaDriverEntryPointSuccess)
+    return reinterpret_cast<EncodeTiledFn>(p);
+  return nullptr;
+}
+
+// A row-major matrix [outer, inner] of 1- or 2-byte elements, rows `ld` elements apart, in boxes of 128
+// bytes x box_outer rows with the 128-byte swizzle; what lies past its ends reads as zeros.
+bool encode_map(CUtensorMap *m, const void *base, int bytes, int64_t inner, int64_t outer, int64_t ld, int box_outer) {
+  static const EncodeTiledFn enc = find_encode();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
+  const cuuint64_t strides[1] = {(cuuint64_t)(ld * bytes)};
+  const cuuint32_t box[2] = {(cuuint32_t)(128 / bytes), (cuuint32_t)box_outer};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(m, bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+             const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // ---- block_norm ----
 
 int check_norm(const char *who, const moe_ffn_block_norm_args *a) {
@@ -194,7 +257,200 @@ moe::NormParams norm_grad_params(const moe_ffn_block_norm_args *a, const moe_ffn
   return p;
 }
 
+// ---- gated block ----
+
+int check_gated(const char *who, const moe_ffn_gated_args *a) {
+  if (!a) return fail(MOE_FFN_ERR_NULL_PTR, "%s: args is NULL", who);
+  if (a->rows == 0) return fail(MOE_FFN_ERR_ROWS_ZERO, "%s: rows must be at least 1", who);
+  if (a->rows < 0 || a->rows > (1 << 24)) return fail(MOE_FFN_ERR_ROWS_RANGE, "%s: rows must be at most 2^24", who);
+  if (a->hidden < 8 || a->hidden % 8 || a->hidden > 65536 || a->inter < 8 || a->inter % 8 || a->inter > 65536)
+    return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: hidden and inter must be multiples of 8 in 8..65536", who);
+  if (a->type != MOE_FFN_BF16 && a->type != MOE_FFN_F16)
+    return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: type must be bf16 or f16", who);
+  if (a->activation != MOE_FFN_ACT_SILU && a->activation != MOE_FFN_ACT_GELU)
+    return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: unknown activation", who);
+  return MOE_FFN_OK;
+}
+
+constexpr int64_t kLdMax = (int64_t)1 << 36;  // a row stride in bytes stays below the tensor maps' 2^40
+
+int check_rows_of(const char *who, const char *name, const void *p, int64_t ld, int64_t cols) {
+  if (!p) return fail(MOE_FFN_ERR_NULL_PTR, "%s: %s is NULL", who, name);
+  if (ld < cols || ld % 8 || ld > kLdMax)
+    return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: the row stride of %s must be a multiple of 8, at least %lld", who, name, (long long)cols);
+  if (!aligned(p, 16)) return fail(MOE_FFN_ERR_ALIGNMENT, "%s: %s is not 16-byte aligned", who, name);
+  return MOE_FFN_OK;
+}
+
+moe::GemmParams gemm_params(const moe_ffn_gated_args *a, const DeviceSide &d, int m, int n, int kb) {
+  moe::GemmParams p = {};
+  p.m = m;
+  p.n = n;
+  p.same = 1;
+  p.kb0 = p.kb = kb;
+  p.act = a->activation;
+  p.f16 = a->type == MOE_FFN_F16;
+  p.status = d.status;
+  p.wait_ns = d.wait_ns;
+  p.inject = d.inject;
+  return p;
+}
+
+// inter columns of a row of the workspace's buffers: h forward; dg, du and h backward
+int64_t gated_workspace(const moe_ffn_gated_args *a, bool backward) {
+  return (int64_t)a->rows * a->inter * 2 * (backward ? 3 : 1);
+}
+
+int kblocks(int k) { return (k + 63) / 64; }
+
 }  // namespace
+
+extern "C" int64_t moe_ffn_gated_workspace(const moe_ffn_gated_args *a, int32_t backward) {
+  const int rc = check_gated("gated_workspace", a);
+  return rc ? rc : gated_workspace(a, backward != 0);
+}
+
+extern "C" int moe_ffn_gated_forward(const moe_ffn_gated_args *a, void *stream) {
+  const char *who = "gated_forward";
+  int rc = check_gated(who, a);
+  if (rc) return rc;
+  const int64_t R = a->rows, H = a->hidden, I = a->inter;
+  if ((rc = check_rows_of(who, "x", a->x, a->ld_x, H)) || (rc = check_rows_of(who, "y", a->y, a->ld_y, H)) ||
+      (rc = check_rows_of(who, "w_gate", a->w_gate, H, H)) || (rc = check_rows_of(who, "w_up", a->w_up, H, H)) ||
+      (rc = check_rows_of(who, "w_down", a->w_down, I, I)) ||
+      (rc = check_rows_of(who, "workspace", a->workspace, I, I)))
+    return rc;
+  if ((a->gate != nullptr) != (a->up != nullptr)) return fail(MOE_FFN_ERR_NULL_PTR, "%s: gate and up go together", who);
+  if (!aligned(a->gate, 16) || !aligned(a->up, 16)) return fail(MOE_FFN_ERR_ALIGNMENT, "%s: gate or up is not 16-byte aligned", who);
+  const int64_t need = gated_workspace(a, false);
+  if (a->workspace_bytes < (size_t)need)
+    return fail(MOE_FFN_ERR_NO_MEMORY, "%s: workspace of %zu bytes, needs %lld", who, a->workspace_bytes, (long long)need);
+  const Span ins[] = {span("x", a->x, R, H, a->ld_x, 2), span("w_gate", a->w_gate, I, H, H, 2),
+                      span("w_up", a->w_up, I, H, H, 2), span("w_down", a->w_down, H, I, I, 2)};
+  const Span outs[] = {span("y", a->y, R, H, a->ld_y, 2), span("gate", a->gate, R, I, I, 2), span("up", a->up, R, I, I, 2),
+                       span("workspace", a->workspace, 1, need, 0, 1)};
+  if ((rc = check_overlaps(who, outs, 4, ins, 4, -1, -1))) return rc;
+  const int sms = current_sms();
+  if (sms < 0) return sms;
+  if ((rc = pending(who))) return rc;
+  DeviceSide dev;
+  if ((rc = device_side(who, &dev))) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+
+  moe::GemmParams up = gemm_params(a, dev, a->rows, a->inter, kblocks(a->hidden));
+  up.c[0] = a->workspace;
+  up.c[1] = a->gate;
+  up.c[2] = a->up;
+  moe::GemmParams down = gemm_params(a, dev, a->rows, a->hidden, kblocks(a->inter));
+  down.c[0] = a->y;
+  down.ldc[0] = a->ld_y;
+  const int bn_up = moe::gemm_pick_bn(moe::kGateUp, up, sms), bn_down = moe::gemm_pick_bn(moe::kDown, down, sms);
+  moe::GemmMaps mu, md;
+  if (!encode_map(&mu.a[0], a->x, 2, H, R, a->ld_x, 128) || !encode_map(&mu.b[0], a->w_gate, 2, H, I, H, bn_up / 2) ||
+      !encode_map(&mu.b[1], a->w_up, 2, H, I, H, bn_up / 2) || !encode_map(&md.a[0], a->workspace, 2, I, R, I, 128) ||
+      !encode_map(&md.b[0], a->w_down, 2, I, H, I, bn_down))
+    return fail(MOE_FFN_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", who);
+  cudaError_t e = moe::launch_dense_gemm(moe::kGateUp, bn_up, mu, up, sms, st);
+  if (e == cudaSuccess) e = moe::launch_dense_gemm(moe::kDown, bn_down, md, down, sms, st);
+  return launched(who, e);
+}
+
+extern "C" int moe_ffn_gated_backward(const moe_ffn_gated_args *a, void *stream) {
+  const char *who = "gated_backward";
+  int rc = check_gated(who, a);
+  if (rc) return rc;
+  const int64_t R = a->rows, H = a->hidden, I = a->inter;
+  const bool weights = a->d_w_gate || a->d_w_up || a->d_w_down;
+  if ((rc = check_rows_of(who, "x", a->x, a->ld_x, H)) || (rc = check_rows_of(who, "w_gate", a->w_gate, H, H)) ||
+      (rc = check_rows_of(who, "w_up", a->w_up, H, H)) || (rc = check_rows_of(who, "w_down", a->w_down, I, I)) ||
+      (rc = check_rows_of(who, "gate", a->gate, I, I)) || (rc = check_rows_of(who, "up", a->up, I, I)) ||
+      (rc = check_rows_of(who, "d_y", a->d_y, a->ld_d_y, H)) ||
+      (rc = check_rows_of(who, "workspace", a->workspace, I, I)) ||
+      (a->d_x && (rc = check_rows_of(who, "d_x", a->d_x, a->ld_d_x, H))) ||
+      (weights && ((rc = check_rows_of(who, "d_w_gate", a->d_w_gate, H, H)) ||
+                   (rc = check_rows_of(who, "d_w_up", a->d_w_up, H, H)) ||
+                   (rc = check_rows_of(who, "d_w_down", a->d_w_down, I, I)))))
+    return rc;
+  if (!a->d_x && !weights) return fail(MOE_FFN_ERR_NULL_PTR, "%s: no gradient is asked for", who);
+  const int64_t need = gated_workspace(a, true);
+  if (a->workspace_bytes < (size_t)need)
+    return fail(MOE_FFN_ERR_NO_MEMORY, "%s: workspace of %zu bytes, needs %lld", who, a->workspace_bytes, (long long)need);
+  const Span ins[] = {span("x", a->x, R, H, a->ld_x, 2),       span("w_gate", a->w_gate, I, H, H, 2),
+                      span("w_up", a->w_up, I, H, H, 2),       span("w_down", a->w_down, H, I, I, 2),
+                      span("gate", a->gate, R, I, I, 2),       span("up", a->up, R, I, I, 2),
+                      span("d_y", a->d_y, R, H, a->ld_d_y, 2)};
+  const Span outs[] = {span("d_x", a->d_x, R, H, a->ld_d_x, 2),       span("d_w_gate", a->d_w_gate, I, H, H, 2),
+                       span("d_w_up", a->d_w_up, I, H, H, 2),         span("d_w_down", a->d_w_down, H, I, I, 2),
+                       span("workspace", a->workspace, 1, need, 0, 1)};
+  if ((rc = check_overlaps(who, outs, 5, ins, 7, -1, -1))) return rc;
+  const int sms = current_sms();
+  if (sms < 0) return sms;
+  if ((rc = pending(who))) return rc;
+  DeviceSide dev;
+  if ((rc = device_side(who, &dev))) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  char *dg = static_cast<char *>(a->workspace), *du = dg + R * I * 2, *h = du + R * I * 2;
+
+  moe::GemmMaps m;
+  moe::GemmParams hid = gemm_params(a, dev, a->rows, a->inter, kblocks(a->hidden));
+  hid.c[0] = dg;
+  hid.c[1] = du;
+  hid.c[2] = h;
+  hid.e[0] = a->gate;
+  hid.e[1] = a->up;
+  if (!encode_map(&m.a[0], a->d_y, 2, H, R, a->ld_d_y, 128) || !encode_map(&m.b[0], a->w_down, 2, I, H, I, 64))
+    return fail(MOE_FFN_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", who);
+  cudaError_t e = moe::launch_dense_gemm(moe::kHiddenGrad, moe::gemm_pick_bn(moe::kHiddenGrad, hid, sms), m, hid, sms, st);
+  if (e == cudaSuccess && a->d_x) {
+    moe::GemmParams p = gemm_params(a, dev, a->rows, a->hidden, 2 * kblocks(a->inter));
+    p.kb0 = kblocks(a->inter);
+    p.c[0] = a->d_x;
+    p.ldc[0] = a->ld_d_x;
+    if (!encode_map(&m.a[0], dg, 2, I, R, I, 128) || !encode_map(&m.a[1], du, 2, I, R, I, 128) ||
+        !encode_map(&m.b[0], a->w_gate, 2, H, I, H, 64) || !encode_map(&m.b[1], a->w_up, 2, H, I, H, 64))
+      return fail(MOE_FFN_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", who);
+    e = moe::launch_dense_gemm(moe::kInputGrad, moe::gemm_pick_bn(moe::kInputGrad, p, sms), m, p, sms, st);
+  }
+  if (e == cudaSuccess && weights) {
+    moe::GemmParams p = gemm_params(a, dev, a->inter, a->hidden, kblocks(a->rows));
+    p.same = 2;
+    p.m_last = a->hidden;
+    p.n_last = a->inter;
+    p.c[0] = a->d_w_gate;
+    p.c[1] = a->d_w_up;
+    p.c[2] = a->d_w_down;
+    p.ldc[0] = p.ldc[1] = H;
+    p.ldc[2] = I;
+    if (!encode_map(&m.a[0], dg, 2, I, R, I, 64) || !encode_map(&m.a[1], du, 2, I, R, I, 64) ||
+        !encode_map(&m.a[2], a->d_y, 2, H, R, a->ld_d_y, 64) || !encode_map(&m.b[0], a->x, 2, H, R, a->ld_x, 64) ||
+        !encode_map(&m.b[2], h, 2, I, R, I, 64))
+      return fail(MOE_FFN_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", who);
+    m.b[1] = m.b[0];
+    e = moe::launch_dense_gemm(moe::kWeightGrad, moe::gemm_pick_bn(moe::kWeightGrad, p, sms), m, p, sms, st);
+  }
+  return launched(who, e);
+}
+
+extern "C" int moe_ffn_dense_status(void *stream) {
+  const char *who = "dense_status";
+  const int sms = current_sms();
+  if (sms < 0) return sms;
+  int rc = pending(who);
+  if (rc) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  take_status_kernel<<<1, 1, 0, st>>>();
+  int bits = 0;
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) e = cudaMemcpyFromSymbolAsync(&bits, g_status_out, sizeof bits, 0, cudaMemcpyDeviceToHost, st);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  return e == cudaSuccess ? bits : fail(MOE_FFN_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
+}
+
+extern "C" int moe_ffn_dense_fault_injection(int32_t enable, uint32_t wait_limit_us) {
+  g_inject.store(enable != 0, std::memory_order_relaxed);
+  g_wait_us.store(wait_limit_us, std::memory_order_relaxed);
+  return MOE_FFN_OK;
+}
 
 extern "C" int moe_ffn_block_norm(const moe_ffn_block_norm_args *a, void *stream) {
   const char *who = "block_norm";

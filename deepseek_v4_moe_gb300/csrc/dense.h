@@ -40,4 +40,30 @@ NormBwdPlan norm_bwd_plan(const NormParams &p, int num_sms);
 cudaError_t launch_block_norm(const NormParams &p, int num_sms, cudaStream_t st);
 cudaError_t launch_block_norm_backward(const NormParams &p, int num_sms, cudaStream_t st);
 
+// ---- the gated block's matrix products (dense_gemm.cu) ----
+
+enum GemmMode : int { kGateUp = 0, kDown = 1, kHiddenGrad = 2, kInputGrad = 3, kWeightGrad = 4 };
+enum Activation : int { kSilu = 0, kGelu = 1 };
+
+struct GemmMaps {
+  CUtensorMap a[3], b[3];
+};
+
+struct GemmParams {
+  int m, n, same;      // output of problems 0 .. same-1
+  int m_last, n_last;  // output of problem `same` (kWeightGrad; zero: there is none)
+  int kb0, kb;         // k blocks of the first pair of matrices, and in all
+  int tiles_m, tiles_n, tiles_m_last, tiles_n_last, tiles;  // set by launch_dense_gemm
+  void *c[3];
+  long long ldc[3];
+  const void *e[2];    // kHiddenGrad: the saved g and u
+  int act, f16;
+  int *status;
+  uint64_t wait_ns;
+  int inject;
+};
+
+int gemm_pick_bn(int mode, const GemmParams &p, int num_sms);
+cudaError_t launch_dense_gemm(int mode, int bn, const GemmMaps &maps, GemmParams p, int num_sms, cudaStream_t st);
+
 }  // namespace moe

@@ -15,7 +15,8 @@ from typing import Optional
 import torch
 
 from . import _lib
-from ._lib import GATE_NONE, GATE_TOKEN, GATE_VECTOR, MoeFfnBlockNormArgs, MoeFfnBlockNormGrads
+from ._lib import (ACTIVATIONS, GATE_NONE, GATE_TOKEN, GATE_VECTOR, MoeFfnBlockNormArgs, MoeFfnBlockNormGrads,
+                   MoeFfnGatedArgs)
 from .api import MoeFFNError
 
 _TYPES = {torch.float32: _lib.TYPE_F32, torch.bfloat16: _lib.TYPE_BF16, torch.float16: _lib.TYPE_F16}
@@ -198,3 +199,110 @@ def block_norm_backward(out: torch.Tensor, f: Optional[torch.Tensor] = None, *,
     if rc != 0:
         _raise(rc)
     return d
+
+
+def _gated_args(x, w_gate, w_up, w_down, activation) -> MoeFfnGatedArgs:
+    dev, dt = x.device, x.dtype
+    if dt not in (torch.bfloat16, torch.float16):
+        raise ValueError("x must be bfloat16 or float16")
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
+    a = MoeFfnGatedArgs()
+    a.ld_x = _matrix("x", x, dev, None, None)
+    rows, hidden = x.shape
+    if w_gate.dim() != 2:
+        raise ValueError("w_gate must be [inter, hidden]")
+    inter = w_gate.shape[0]
+    for name, w, shape in (("w_gate", w_gate, (inter, hidden)), ("w_up", w_up, (inter, hidden)),
+                           ("w_down", w_down, (hidden, inter))):
+        if tuple(w.shape) != shape or w.dtype != dt or w.device != dev or not w.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dt} {list(shape)} tensor on {dev}")
+    a.rows, a.hidden, a.inter, a.type, a.activation = rows, hidden, inter, _TYPES[dt], ACTIVATIONS[activation]
+    a.x, a.w_gate, a.w_up, a.w_down = x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr()
+    return a
+
+
+def _workspace(a: MoeFfnGatedArgs, need: int, device) -> torch.Tensor:
+    if need < 0:
+        _raise(need)
+    ws = torch.empty(need, dtype=torch.uint8, device=device)
+    a.workspace, a.workspace_bytes = ws.data_ptr(), need
+    return ws
+
+
+def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor,
+              activation: str = "silu", save: bool = False, out: Optional[torch.Tensor] = None,
+              stream: Optional[torch.cuda.Stream] = None):
+    """The gated feed-forward block: y = (act(x w_gate^T) * (x w_up^T)) w_down^T.
+
+    ``x`` [rows, hidden] bfloat16 or float16; ``w_gate``, ``w_up`` [inter, hidden] and ``w_down``
+    [hidden, inter] of its type; hidden and inter multiples of 8.  ``activation``: "silu" or "gelu"
+    (tanh form).  Returns y [rows, hidden]; with ``save`` also the pair (g, u) of projections
+    [rows, inter] that :func:`gated_ffn_backward` takes.
+    """
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    ctx = _on(x.device, stream)
+    if ctx is not None:
+        with ctx:
+            return gated_ffn(x, w_gate, w_up, w_down, activation, save, out)
+    a = _gated_args(x, w_gate, w_up, w_down, activation)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    a.ld_y, a.y = _matrix("out", out, x.device, x.shape, x.dtype), out.data_ptr()
+    saved = None
+    if save:
+        saved = tuple(torch.empty((a.rows, a.inter), dtype=x.dtype, device=x.device) for _ in range(2))
+        a.gate, a.up = saved[0].data_ptr(), saved[1].data_ptr()
+    lib = _lib.load()
+    ws = _workspace(a, lib.moe_ffn_gated_workspace(ctypes.byref(a), 0), x.device)  # noqa: F841
+    rc = lib.moe_ffn_gated_forward(ctypes.byref(a), torch.cuda.current_stream().cuda_stream)
+    if rc != 0:
+        _raise(rc)
+    return (out, saved) if save else out
+
+
+def gated_ffn_backward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor, saved,
+                       d_y: torch.Tensor, activation: str = "silu", need_x: bool = True, need_weights: bool = True,
+                       stream: Optional[torch.cuda.Stream] = None) -> dict:
+    """Gradients of :func:`gated_ffn` from what it saved: a dict of d_x, d_w_gate, d_w_up and d_w_down
+    (of the inputs' type), without d_x or the weights' where they are not needed."""
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    ctx = _on(x.device, stream)
+    if ctx is not None:
+        with ctx:
+            return gated_ffn_backward(x, w_gate, w_up, w_down, saved, d_y, activation, need_x, need_weights)
+    a = _gated_args(x, w_gate, w_up, w_down, activation)
+    for name, t in zip(("saved[0]", "saved[1]"), saved):
+        _matrix(name, t, x.device, (a.rows, a.inter), x.dtype)
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    a.gate, a.up = saved[0].data_ptr(), saved[1].data_ptr()
+    a.ld_d_y, a.d_y = _matrix("d_y", d_y, x.device, x.shape, x.dtype), d_y.data_ptr()
+    d = {}
+    if need_x:
+        d["d_x"] = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        a.d_x, a.ld_d_x = d["d_x"].data_ptr(), a.hidden
+    if need_weights:
+        for name, w in (("d_w_gate", w_gate), ("d_w_up", w_up), ("d_w_down", w_down)):
+            d[name] = torch.empty_like(w)
+            setattr(a, name, d[name].data_ptr())
+    lib = _lib.load()
+    ws = _workspace(a, lib.moe_ffn_gated_workspace(ctypes.byref(a), 1), x.device)  # noqa: F841
+    rc = lib.moe_ffn_gated_backward(ctypes.byref(a), torch.cuda.current_stream().cuda_stream)
+    if rc != 0:
+        _raise(rc)
+    return d
+
+
+def dense_status(stream: Optional[torch.cuda.Stream] = None) -> int:
+    """Device status bits that the dense sublayer's kernels set on the current device (the stream's)
+    since the last call, after waiting for the stream; then cleared."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return dense_status()
+    rc = _lib.load().moe_ffn_dense_status(torch.cuda.current_stream().cuda_stream)
+    if rc < 0:
+        _raise(rc)
+    return rc

@@ -360,6 +360,50 @@ int moe_ffn_block_norm_backward(const moe_ffn_block_norm_args *a, const moe_ffn_
  * with NULL); negative: an error code. */
 int64_t moe_ffn_block_norm_workspace(const moe_ffn_block_norm_args *a, const moe_ffn_block_norm_grads *g);
 
+/* The gated feed-forward block:  g = x w_gate^T,  u = x w_up^T,  y = (act(g) * u) w_down^T.
+ * Both projections, the activation and the product are one kernel, the down projection another
+ * (one to four rows: weight-streaming kernels).  Operands are bf16 or f16, sums f32; act(g) * u is
+ * rounded to the operand type before the down projection.
+ * Backward, from the saved g and u (rounded to the type):  dh = d_y w_down;  dg = dh * u * act'(g);
+ *   du = dh * act(g);  d_x = dg w_gate + du w_up;  d_w_gate = dg^T x;  d_w_up = du^T x;
+ *   d_w_down = d_y^T (act(g) * u);  dg, du and act(g) * u are rounded to the type as operands. */
+#define MOE_FFN_ACT_SILU 0
+#define MOE_FFN_ACT_GELU 1 /* 0.5 g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) */
+
+typedef struct moe_ffn_gated_args {
+  int32_t rows, hidden, inter;  /* hidden and inter multiples of 8, at most 65536; rows at most 2^24 */
+  int32_t type;                 /* MOE_FFN_BF16 or MOE_FFN_F16: every tensor below */
+  int32_t activation;
+  const void *x; int64_t ld_x;  /* [rows, hidden] */
+  const void *w_gate, *w_up;    /* [inter, hidden], contiguous */
+  const void *w_down;           /* [hidden, inter], contiguous */
+  void *y; int64_t ld_y;        /* forward: [rows, hidden] */
+  void *gate, *up;              /* [rows, inter], contiguous: forward writes g and u (or both NULL), backward reads them */
+  const void *d_y; int64_t ld_d_y;            /* backward: [rows, hidden] */
+  void *d_x; int64_t ld_d_x;                  /* backward: [rows, hidden], or NULL */
+  void *d_w_gate, *d_w_up, *d_w_down;         /* backward: the weights' layouts; all three or none */
+  void *workspace; size_t workspace_bytes;    /* at least moe_ffn_gated_workspace */
+} moe_ffn_gated_args;
+
+/* Every pointer 16-byte aligned, every ld a multiple of 8.  Returns MOE_FFN_OK, NULL_PTR, ROWS_ZERO,
+ * ROWS_RANGE, BAD_CONFIG (sizes, type, activation, ld), ALIGNMENT, ALIAS (an output or the workspace
+ * overlaps another tensor), NO_MEMORY (workspace too small), UNSUPPORTED or CUDA.  The first call on
+ * each device looks up library memory: make it before any stream capture. */
+int moe_ffn_gated_forward(const moe_ffn_gated_args *a, void *stream);
+int moe_ffn_gated_backward(const moe_ffn_gated_args *a, void *stream);
+
+/* Bytes of workspace that the forward (backward = 0) or backward call needs; negative: an error code. */
+int64_t moe_ffn_gated_workspace(const moe_ffn_gated_args *a, int32_t backward);
+
+/* Device status bits (MOE_FFN_DEV_TIMEOUT) that the dense sublayer's kernels set on the current device
+ * since the previous call, after waiting for `stream`; then cleared.  Or a negative code. */
+int moe_ffn_dense_status(void *stream);
+
+/* Test hook for failure detection, as moe_ffn_set_fault_injection: with enable != 0, CTA 0 of each
+ * tensor-core kernel of the dense sublayer that the process launches from now on first waits for
+ * something that never comes, and wait_limit_us (0: 2 s) bounds every wait. */
+int moe_ffn_dense_fault_injection(int32_t enable, uint32_t wait_limit_us);
+
 /* Text of the last error on this handle, or, when h is NULL, of the last failed call made without
  * a handle (init, the allocation-free split, a NULL handle) on the calling thread: that message
  * is kept per thread, so threads that fail at the same time do not overwrite each other's text.

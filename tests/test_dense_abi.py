@@ -74,3 +74,46 @@ def test_block_norm_null(lib):
     assert lib.moe_ffn_block_norm(None, None) == _lib.ERR_NULL_PTR
     assert lib.moe_ffn_block_norm_backward(ctypes.byref(_norm()), None, None) == _lib.ERR_NULL_PTR
     assert lib.moe_ffn_block_norm_workspace(None, None) == _lib.ERR_NULL_PTR
+
+
+def _gated(**kw):
+    base = dict(rows=4, hidden=256, inter=64, type=_lib.TYPE_BF16, activation=0, x=A, ld_x=256, w_gate=2 * A, w_up=3 * A,
+                w_down=4 * A, y=5 * A, ld_y=256, gate=6 * A, up=7 * A, d_y=8 * A, ld_d_y=256, d_x=9 * A, ld_d_x=256,
+                d_w_gate=10 * A, d_w_up=11 * A, d_w_down=12 * A, workspace=13 * A, workspace_bytes=1536)
+    base.update(kw)
+    return _lib.MoeFfnGatedArgs(**base)
+
+
+BOTH_REFUSED = [
+    (dict(rows=0), _lib.ERR_ROWS_ZERO), (dict(rows=-3), _lib.ERR_ROWS_RANGE), (dict(rows=(1 << 24) + 1), _lib.ERR_ROWS_RANGE),
+    (dict(hidden=0), _lib.ERR_BAD_CONFIG), (dict(hidden=252), _lib.ERR_BAD_CONFIG), (dict(inter=65544), _lib.ERR_BAD_CONFIG),
+    (dict(type=_lib.TYPE_F32), _lib.ERR_BAD_CONFIG), (dict(activation=2), _lib.ERR_BAD_CONFIG),
+    (dict(x=None), _lib.ERR_NULL_PTR), (dict(w_up=None), _lib.ERR_NULL_PTR), (dict(workspace=None), _lib.ERR_NULL_PTR),
+    (dict(ld_x=248), _lib.ERR_BAD_CONFIG), (dict(ld_x=257), _lib.ERR_BAD_CONFIG), (dict(ld_x=1 << 40), _lib.ERR_BAD_CONFIG),
+    (dict(x=A + 8), _lib.ERR_ALIGNMENT), (dict(w_down=4 * A + 2), _lib.ERR_ALIGNMENT), (dict(up=None), _lib.ERR_NULL_PTR),
+    (dict(gate=6 * A + 4), _lib.ERR_ALIGNMENT), (dict(workspace_bytes=100), _lib.ERR_NO_MEMORY),
+    (dict(workspace=A), _lib.ERR_ALIAS),
+]
+
+
+@pytest.mark.parametrize("kw,code", BOTH_REFUSED + [
+    (dict(y=None), _lib.ERR_NULL_PTR), (dict(ld_y=100), _lib.ERR_BAD_CONFIG), (dict(y=A), _lib.ERR_ALIAS),
+    (dict(gate=5 * A), _lib.ERR_ALIAS), (dict(y=13 * A + 16), _lib.ERR_ALIAS)])
+def test_gated_forward_refuses(lib, kw, code):
+    assert lib.moe_ffn_gated_forward(ctypes.byref(_gated(**kw)), None) == code, lib.moe_ffn_last_error(None)
+
+
+@pytest.mark.parametrize("kw,code", BOTH_REFUSED + [
+    (dict(d_y=None), _lib.ERR_NULL_PTR), (dict(d_w_up=None), _lib.ERR_NULL_PTR), (dict(d_x=8 * A), _lib.ERR_ALIAS),
+    (dict(d_x=None, d_w_gate=None, d_w_up=None, d_w_down=None), _lib.ERR_NULL_PTR),
+    (dict(d_w_gate=11 * A), _lib.ERR_ALIAS), (dict(d_x=6 * A), _lib.ERR_ALIAS), (dict(ld_d_x=128), _lib.ERR_BAD_CONFIG),
+    (dict(workspace_bytes=1535), _lib.ERR_NO_MEMORY)])
+def test_gated_backward_refuses(lib, kw, code):
+    assert lib.moe_ffn_gated_backward(ctypes.byref(_gated(**kw)), None) == code, lib.moe_ffn_last_error(None)
+
+
+def test_gated_workspace(lib):
+    assert lib.moe_ffn_gated_workspace(ctypes.byref(_gated()), 0) == 4 * 64 * 2
+    assert lib.moe_ffn_gated_workspace(ctypes.byref(_gated()), 1) == 4 * 64 * 2 * 3
+    assert lib.moe_ffn_gated_workspace(ctypes.byref(_gated(rows=0)), 1) == _lib.ERR_ROWS_ZERO
+    assert lib.moe_ffn_gated_workspace(None, 1) == _lib.ERR_NULL_PTR
