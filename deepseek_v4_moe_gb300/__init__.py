@@ -14,8 +14,10 @@ experts in MXFP8 (``set_mxfp8_experts``).
 
 The dense feed-forward sublayer on a plain residual stream needs no handle (``dense``):
 ``block_norm`` (the norms around a block with its gate and residual scale) and ``gated_ffn`` (the
-gated feed-forward block), each with its gradients; ``dense_status`` reads the device status bits.
+gated feed-forward block), each with its gradients, ``fp8_matmul`` (the product of FP8 operands with
+scales for blocks of 128) and ``fp8_quantise``, which makes its operands; ``dense_status`` reads the
+device status bits.
 """
 from .api import MoeFFN, MoeFFNError, config_from  # noqa: F401
-from .dense import (block_norm, block_norm_backward, dense_status, gated_ffn,  # noqa: F401
-                    gated_ffn_backward)
+from .dense import (block_norm, block_norm_backward, dense_status, fp8_matmul, fp8_quantise,  # noqa: F401
+                    gated_ffn, gated_ffn_backward)

@@ -73,6 +73,20 @@ class MoeFfnGatedArgs(ctypes.Structure):
                 ("workspace_bytes", c_sz)]
 
 
+TYPE_E4M3, TYPE_E5M2 = 0, 1
+
+
+class MoeFfnFp8MatmulArgs(ctypes.Structure):
+    _fields_ = [("rows", c_i32), ("n", c_i32), ("k", c_i32), ("a_type", c_i32), ("b_type", c_i32), ("out_type", c_i32),
+                ("a", c_vp), ("ld_a", c_i64), ("a_scale", c_vp), ("b", c_vp), ("ld_b", c_i64), ("b_scale", c_vp),
+                ("out", c_vp), ("ld_out", c_i64)]
+
+
+class MoeFfnFp8QuantiseArgs(ctypes.Structure):
+    _fields_ = [("rows", c_i32), ("k", c_i32), ("type", c_i32), ("code_type", c_i32), ("block_rows", c_i32),
+                ("pow2", c_i32), ("x", c_vp), ("ld_x", c_i64), ("codes", c_vp), ("ld_codes", c_i64), ("scales", c_vp)]
+
+
 # return codes and device status bits (include/moe_ffn.h)
 OK, ERR_NULL_PTR, ERR_BAD_CONFIG, ERR_LAYER_RANGE, ERR_ROWS_ZERO, ERR_ROWS_RANGE = 0, -1, -2, -3, -4, -5
 ERR_NO_ROUTING_SOURCE, ERR_ALIAS, ERR_CUDA, ERR_NO_MEMORY, ERR_UNSUPPORTED, ERR_ALIGNMENT, ERR_NO_WEIGHTS = (
@@ -151,6 +165,10 @@ def load(build: bool = True):
     lib.moe_ffn_dense_status.restype = ctypes.c_int
     lib.moe_ffn_dense_fault_injection.argtypes = [i32, ctypes.c_uint32]
     lib.moe_ffn_dense_fault_injection.restype = ctypes.c_int
+    lib.moe_ffn_fp8_matmul.argtypes = [ctypes.POINTER(MoeFfnFp8MatmulArgs), vp]
+    lib.moe_ffn_fp8_matmul.restype = ctypes.c_int
+    lib.moe_ffn_fp8_quantise.argtypes = [ctypes.POINTER(MoeFfnFp8QuantiseArgs), vp]
+    lib.moe_ffn_fp8_quantise.restype = ctypes.c_int
     lib.moe_ffn_last_error.argtypes = [vp]
     lib.moe_ffn_last_error.restype = ctypes.c_char_p
     lib.moe_ffn_destroy.argtypes = [vp]

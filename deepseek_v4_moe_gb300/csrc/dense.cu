@@ -431,6 +431,96 @@ extern "C" int moe_ffn_gated_backward(const moe_ffn_gated_args *a, void *stream)
   return launched(who, e);
 }
 
+extern "C" int moe_ffn_fp8_matmul(const moe_ffn_fp8_matmul_args *a, void *stream) {
+  const char *who = "fp8_matmul";
+  if (!a) return fail(MOE_FFN_ERR_NULL_PTR, "%s: args is NULL", who);
+  if (a->rows == 0) return fail(MOE_FFN_ERR_ROWS_ZERO, "%s: rows must be at least 1", who);
+  if (a->rows < 0 || a->rows > (1 << 24)) return fail(MOE_FFN_ERR_ROWS_RANGE, "%s: rows must be at most 2^24", who);
+  if (a->n < 1 || a->n > (1 << 20) || a->k < 16 || a->k % 16 || a->k > (1 << 20))
+    return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: n must be in 1..2^20, k a multiple of 16 in 16..2^20", who);
+  if ((a->a_type != MOE_FFN_E4M3 && a->a_type != MOE_FFN_E5M2) || (a->b_type != MOE_FFN_E4M3 && a->b_type != MOE_FFN_E5M2) ||
+      !is_type(a->out_type))
+    return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: unknown type", who);
+  if (!a->a || !a->a_scale || !a->b || !a->b_scale || !a->out)
+    return fail(MOE_FFN_ERR_NULL_PTR, "%s: a pointer is NULL", who);
+  if (a->ld_a < a->k || a->ld_a % 16 || a->ld_a > kLdMax || a->ld_b < a->k || a->ld_b % 16 || a->ld_b > kLdMax)
+    return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: the row strides of a and b must be multiples of 16, at least k", who);
+  if (a->ld_out < a->n || a->ld_out > kLdMax) return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: the row stride of out is below n", who);
+  const int ob = type_bytes(a->out_type);
+  if (!aligned(a->a, 16) || !aligned(a->b, 16) || !aligned(a->a_scale, 4) || !aligned(a->b_scale, 4) || !aligned(a->out, ob))
+    return fail(MOE_FFN_ERR_ALIGNMENT, "%s: a and b must be 16-byte aligned, the others to their type", who);
+  const int64_t R = a->rows, N = a->n, K = a->k, KB = (K + 127) / 128;
+  const Span ins[] = {span("a", a->a, R, K, a->ld_a, 1), span("a_scale", a->a_scale, R, KB, KB, 4),
+                      span("b", a->b, N, K, a->ld_b, 1), span("b_scale", a->b_scale, (N + 127) / 128, KB, KB, 4)};
+  const Span outs[] = {span("out", a->out, R, N, a->ld_out, ob)};
+  int rc = check_overlaps(who, outs, 1, ins, 4, -1, -1);
+  if (rc) return rc;
+  const int sms = current_sms();
+  if (sms < 0) return sms;
+  if ((rc = pending(who))) return rc;
+  DeviceSide dev;
+  if ((rc = device_side(who, &dev))) return rc;
+  moe::Fp8Params p = {};
+  p.m = a->rows;
+  p.n = a->n;
+  p.kb = (int)KB;
+  p.a_e5m2 = a->a_type == MOE_FFN_E5M2;
+  p.b_e5m2 = a->b_type == MOE_FFN_E5M2;
+  p.out_type = a->out_type;
+  p.a_scale = a->a_scale;
+  p.b_scale = a->b_scale;
+  p.out = a->out;
+  p.ld_out = a->ld_out;
+  p.wide = aligned(a->out, 16) && a->ld_out * ob % 16 == 0;
+  p.status = dev.status;
+  p.wait_ns = dev.wait_ns;
+  p.inject = dev.inject;
+  const int bn = moe::fp8_pick_bn(p, sms);
+  CUtensorMap ma, mb;
+  if (!encode_map(&ma, a->a, 1, K, R, a->ld_a, 128) || !encode_map(&mb, a->b, 1, K, N, a->ld_b, bn))
+    return fail(MOE_FFN_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", who);
+  return launched(who, moe::launch_fp8_matmul(bn, ma, mb, p, sms, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int moe_ffn_fp8_quantise(const moe_ffn_fp8_quantise_args *a, void *stream) {
+  const char *who = "fp8_quantise";
+  if (!a) return fail(MOE_FFN_ERR_NULL_PTR, "%s: args is NULL", who);
+  if (a->rows == 0) return fail(MOE_FFN_ERR_ROWS_ZERO, "%s: rows must be at least 1", who);
+  if (a->rows < 0 || a->rows > (1 << 24)) return fail(MOE_FFN_ERR_ROWS_RANGE, "%s: rows must be at most 2^24", who);
+  if (a->k < 1 || a->k > (1 << 20)) return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: k must be in 1..2^20", who);
+  if (!is_type(a->type) || (a->code_type != MOE_FFN_E4M3 && a->code_type != MOE_FFN_E5M2))
+    return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: unknown type", who);
+  if (a->block_rows != 1 && a->block_rows != 128) return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: block_rows must be 1 or 128", who);
+  if (!a->x || !a->codes || !a->scales) return fail(MOE_FFN_ERR_NULL_PTR, "%s: a pointer is NULL", who);
+  if (a->ld_x < a->k || a->ld_codes < a->k || a->ld_x > kLdMax || a->ld_codes > kLdMax)
+    return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: a row stride is below k", who);
+  const int xb = type_bytes(a->type);
+  if (!aligned(a->x, xb) || !aligned(a->scales, 4)) return fail(MOE_FFN_ERR_ALIGNMENT, "%s: x or scales is misaligned", who);
+  const int64_t R = a->rows, K = a->k, KB = (K + 127) / 128;
+  const Span ins[] = {span("x", a->x, R, K, a->ld_x, xb)};
+  const Span outs[] = {span("codes", a->codes, R, K, a->ld_codes, 1),
+                       span("scales", a->scales, (R + a->block_rows - 1) / a->block_rows, KB, KB, 4)};
+  int rc = check_overlaps(who, outs, 2, ins, 1, -1, -1);
+  if (rc) return rc;
+  const int sms = current_sms();
+  if (sms < 0) return sms;
+  if ((rc = pending(who))) return rc;
+  moe::QuantiseParams p = {};
+  p.rows = a->rows;
+  p.k = a->k;
+  p.type = a->type;
+  p.e5m2 = a->code_type == MOE_FFN_E5M2;
+  p.pow2 = a->pow2 != 0;
+  p.tall = a->block_rows;
+  p.x = a->x;
+  p.ld_x = a->ld_x;
+  p.codes = static_cast<uint8_t *>(a->codes);
+  p.ld_codes = a->ld_codes;
+  p.scales = a->scales;
+  p.wide = a->k % 8 == 0 && aligned(a->x, 16) && a->ld_x * xb % 16 == 0 && aligned(a->codes, 8) && a->ld_codes % 8 == 0;
+  return launched(who, moe::launch_fp8_quantise(p, sms, static_cast<cudaStream_t>(stream)));
+}
+
 extern "C" int moe_ffn_dense_status(void *stream) {
   const char *who = "dense_status";
   const int sms = current_sms();

@@ -66,4 +66,36 @@ struct GemmParams {
 int gemm_pick_bn(int mode, const GemmParams &p, int num_sms);
 cudaError_t launch_dense_gemm(int mode, int bn, const GemmMaps &maps, GemmParams p, int num_sms, cudaStream_t st);
 
+// ---- FP8 with block scales (dense_fp8.cu) ----
+
+constexpr int kScaleBlock = 128;
+
+struct Fp8Params {
+  int m, n, kb;              // kb: blocks of 128 along k
+  int a_e5m2, b_e5m2, out_type;
+  const float *a_scale, *b_scale;  // [m, kb], [ceil(n / 128), kb]
+  void *out;
+  long long ld_out;
+  int wide;                  // out can be written in 16-byte pieces
+  int tiles_m, tiles_n, tiles;  // set by launch_fp8_matmul
+  int *status;
+  uint64_t wait_ns;
+  int inject;
+};
+
+struct QuantiseParams {
+  int rows, k, type, e5m2, pow2, tall;  // tall: rows of a block, 1 or 128
+  const void *x;
+  long long ld_x;
+  uint8_t *codes;
+  long long ld_codes;
+  float *scales;             // [ceil(rows / tall), ceil(k / 128)]
+  int wide;                  // x in 16-byte pieces, codes in 8-byte pieces
+};
+
+int fp8_pick_bn(const Fp8Params &p, int num_sms);
+cudaError_t launch_fp8_matmul(int bn, const CUtensorMap &a, const CUtensorMap &b, Fp8Params p, int num_sms,
+                              cudaStream_t st);
+cudaError_t launch_fp8_quantise(const QuantiseParams &p, int num_sms, cudaStream_t st);
+
 }  // namespace moe

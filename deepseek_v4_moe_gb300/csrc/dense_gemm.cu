@@ -29,14 +29,14 @@
 // MMAs in flight are waited for (bounded) and TMEM is freed.
 #include "common.cuh"
 #include "dense.h"
+#include "dense_tc.cuh"
 #include "dense_vec.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kBM = 128, kBK = 64, kEpiWarps = 8, kThreads = 32 * (2 + kEpiWarps);
+constexpr int kBK = 64;
 constexpr int kABytes = kBM * kBK * 2;
-constexpr int kRingBytes = 227 * 1024 - 3072;  // what the barriers and the alignment leave of a CTA's shared memory
 
 template <int MODE, int BN>
 struct Cfg {
@@ -66,7 +66,6 @@ struct Tile {
   int prob, m0, n0;  // problem (kWeightGrad), first row, first column (kGateUp: of g and of u)
 };
 
-// Tiles in bands of 16 row blocks, so that the CTAs at work at one time share both operands in L2.
 __device__ __forceinline__ Tile tile_of(const GemmParams &p, int t, int cols) {
   Tile r;
   r.prob = 0;
@@ -81,10 +80,9 @@ __device__ __forceinline__ Tile tile_of(const GemmParams &p, int t, int cols) {
     r.prob = t / each;
     t -= r.prob * each;
   }
-  const int band = t / (16 * tn), first = band * 16, height = min(tm - first, 16);
-  t -= band * 16 * tn;
-  r.m0 = (first + t % height) * kBM;
-  r.n0 = (t / height) * cols;
+  band_tile(t, tm, tn, r.m0, r.n0);
+  r.m0 *= kBM;
+  r.n0 *= cols;
   return r;
 }
 

@@ -16,10 +16,11 @@ import torch
 
 from . import _lib
 from ._lib import (ACTIVATIONS, GATE_NONE, GATE_TOKEN, GATE_VECTOR, MoeFfnBlockNormArgs, MoeFfnBlockNormGrads,
-                   MoeFfnGatedArgs)
+                   MoeFfnFp8MatmulArgs, MoeFfnFp8QuantiseArgs, MoeFfnGatedArgs)
 from .api import MoeFFNError
 
 _TYPES = {torch.float32: _lib.TYPE_F32, torch.bfloat16: _lib.TYPE_BF16, torch.float16: _lib.TYPE_F16}
+_FP8 = {torch.float8_e4m3fn: _lib.TYPE_E4M3, torch.float8_e5m2: _lib.TYPE_E5M2}
 
 
 def _raise(rc: int):
@@ -294,6 +295,75 @@ def gated_ffn_backward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor
     if rc != 0:
         _raise(rc)
     return d
+
+
+def fp8_quantise(x: torch.Tensor, block_rows: int = 1, pow2_scales: bool = False,
+                 dtype: torch.dtype = torch.float8_e4m3fn, stream: Optional[torch.cuda.Stream] = None):
+    """Makes an operand of :func:`fp8_matmul`: (codes [rows, k] of ``dtype``, float32 scales
+    [ceil(rows / block_rows), ceil(k / 128)]).
+
+    ``x`` [rows, k] float32, bfloat16 or float16.  ``block_rows`` 1 (activations) or 128 (weights).  A
+    block's scale is its largest magnitude over the largest code, 1 for zeros, at least 2^-126, with
+    ``pow2_scales`` rounded up to a power of two; a code is x / scale rounded to nearest even.
+    """
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    ctx = _on(x.device, stream)
+    if ctx is not None:
+        with ctx:
+            return fp8_quantise(x, block_rows, pow2_scales, dtype)
+    if x.dtype not in _TYPES or dtype not in _FP8:
+        raise ValueError("x must be float32, bfloat16 or float16, dtype float8_e4m3fn or float8_e5m2")
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows must be 1 or 128")
+    ld = _matrix("x", x, x.device, None, None)
+    rows, k = x.shape
+    codes = torch.empty((rows, k), dtype=dtype, device=x.device)
+    scales = torch.empty((-(-rows // block_rows), -(-k // 128)), dtype=torch.float32, device=x.device)
+    a = MoeFfnFp8QuantiseArgs(rows, k, _TYPES[x.dtype], _FP8[dtype], block_rows, bool(pow2_scales), x.data_ptr(), ld,
+                              codes.data_ptr(), k, scales.data_ptr())
+    rc = _lib.load().moe_ffn_fp8_quantise(ctypes.byref(a), torch.cuda.current_stream().cuda_stream)
+    if rc != 0:
+        _raise(rc)
+    return codes, scales
+
+
+def fp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: torch.Tensor,
+               out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
+               stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """a b^T of FP8 operands with float32 scales for blocks of 128: ``a`` [rows, k] with ``a_scale``
+    [rows, ceil(k / 128)], ``b`` [n, k] with ``b_scale`` [ceil(n / 128), ceil(k / 128)] (see
+    :func:`fp8_quantise`; each float8_e4m3fn or float8_e5m2), k a multiple of 16.  Sums are float32; the
+    result is ``out_dtype``: float32, bfloat16 or float16.
+    """
+    if not a.is_cuda:
+        raise ValueError("a must be a CUDA tensor")
+    ctx = _on(a.device, stream)
+    if ctx is not None:
+        with ctx:
+            return fp8_matmul(a, a_scale, b, b_scale, out_dtype, out)
+    dev = a.device
+    if a.dtype not in _FP8 or b.dtype not in _FP8 or out_dtype not in _TYPES:
+        raise ValueError("a and b must be float8_e4m3fn or float8_e5m2, out_dtype float32, bfloat16 or float16")
+    ld_a = _matrix("a", a, dev, None, None)
+    rows, k = a.shape
+    if b.dim() != 2 or b.shape[1] != k:
+        raise ValueError(f"b must be [n, {k}], got {list(b.shape)}")
+    n = b.shape[0]
+    ld_b = _matrix("b", b, dev, None, None)
+    kb = -(-k // 128)
+    for name, t, shape in (("a_scale", a_scale, (rows, kb)), ("b_scale", b_scale, (-(-n // 128), kb))):
+        if tuple(t.shape) != shape or t.dtype != torch.float32 or t.device != dev or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous float32 {list(shape)} tensor on {dev}")
+    if out is None:
+        out = torch.empty((rows, n), dtype=out_dtype, device=dev)
+    ld_out = _matrix("out", out, dev, (rows, n), out_dtype)
+    args = MoeFfnFp8MatmulArgs(rows, n, k, _FP8[a.dtype], _FP8[b.dtype], _TYPES[out_dtype], a.data_ptr(), ld_a,
+                               a_scale.data_ptr(), b.data_ptr(), ld_b, b_scale.data_ptr(), out.data_ptr(), ld_out)
+    rc = _lib.load().moe_ffn_fp8_matmul(ctypes.byref(args), torch.cuda.current_stream().cuda_stream)
+    if rc != 0:
+        _raise(rc)
+    return out
 
 
 def dense_status(stream: Optional[torch.cuda.Stream] = None) -> int:

@@ -395,6 +395,46 @@ int moe_ffn_gated_backward(const moe_ffn_gated_args *a, void *stream);
 /* Bytes of workspace that the forward (backward = 0) or backward call needs; negative: an error code. */
 int64_t moe_ffn_gated_workspace(const moe_ffn_gated_args *a, int32_t backward);
 
+/* Matrix product in 8-bit floating point with a scale for each block of 128:
+ *   out[i, j] = sum_b a_scale[i, b] * b_scale[j / 128, b] * sum over k in block b of a[i, k] * b[j, k]
+ * with blocks of 128 along k, the last of which may be shorter.  Sums are f32.  (The MXFP8 experts
+ * above have a power-of-two scale for each 32 elements instead.) */
+#define MOE_FFN_E4M3 0
+#define MOE_FFN_E5M2 1
+
+typedef struct moe_ffn_fp8_matmul_args {
+  int32_t rows, n, k;            /* k a multiple of 16, at most 2^20; n at most 2^20; rows at most 2^24 */
+  int32_t a_type, b_type;        /* MOE_FFN_E4M3 or MOE_FFN_E5M2 */
+  int32_t out_type;              /* MOE_FFN_F32, _BF16 or _F16 */
+  const void *a; int64_t ld_a;   /* codes [rows, k]; 16-byte aligned, ld a multiple of 16 */
+  const float *a_scale;          /* [rows, ceil(k / 128)], contiguous */
+  const void *b; int64_t ld_b;   /* codes [n, k]; 16-byte aligned, ld a multiple of 16 */
+  const float *b_scale;          /* [ceil(n / 128), ceil(k / 128)], contiguous */
+  void *out; int64_t ld_out;     /* [rows, n], any ld >= n; overlaps no input */
+} moe_ffn_fp8_matmul_args;
+
+/* Returns MOE_FFN_OK, NULL_PTR, ROWS_ZERO, ROWS_RANGE, BAD_CONFIG, ALIGNMENT, ALIAS, UNSUPPORTED or
+ * CUDA.  The first call on each device looks up library memory: make it before any stream capture. */
+int moe_ffn_fp8_matmul(const moe_ffn_fp8_matmul_args *a, void *stream);
+
+/* Makes such an operand: a block is block_rows (1 or 128) rows x 128 columns, those at the ends may be
+ * smaller.  scale = (largest magnitude of the block) / (largest finite code: 448 or 57344), 1 for a
+ * block of zeros, at least 2^-126; with pow2 rounded up to a power of two.  code = x / scale, rounded to
+ * nearest even.  A block with a NaN has the scale NaN, one with an infinity the scale infinity, and
+ * products with either are not finite. */
+typedef struct moe_ffn_fp8_quantise_args {
+  int32_t rows, k;               /* k at most 2^20, rows at most 2^24 */
+  int32_t type;                  /* of x: MOE_FFN_F32, _BF16 or _F16 */
+  int32_t code_type;             /* MOE_FFN_E4M3 or MOE_FFN_E5M2 */
+  int32_t block_rows, pow2;
+  const void *x; int64_t ld_x;   /* [rows, k] */
+  void *codes; int64_t ld_codes; /* [rows, k] */
+  float *scales;                 /* [ceil(rows / block_rows), ceil(k / 128)], contiguous */
+} moe_ffn_fp8_quantise_args;
+
+/* The codes of moe_ffn_fp8_matmul. */
+int moe_ffn_fp8_quantise(const moe_ffn_fp8_quantise_args *a, void *stream);
+
 /* Device status bits (MOE_FFN_DEV_TIMEOUT) that the dense sublayer's kernels set on the current device
  * since the previous call, after waiting for `stream`; then cleared.  Or a negative code. */
 int moe_ffn_dense_status(void *stream);

@@ -117,3 +117,43 @@ def test_gated_workspace(lib):
     assert lib.moe_ffn_gated_workspace(ctypes.byref(_gated()), 1) == 4 * 64 * 2 * 3
     assert lib.moe_ffn_gated_workspace(ctypes.byref(_gated(rows=0)), 1) == _lib.ERR_ROWS_ZERO
     assert lib.moe_ffn_gated_workspace(None, 1) == _lib.ERR_NULL_PTR
+
+
+def _matmul(**kw):
+    base = dict(rows=4, n=200, k=256, a_type=0, b_type=0, out_type=_lib.TYPE_BF16, a=A, ld_a=256, a_scale=2 * A, b=3 * A,
+                ld_b=256, b_scale=4 * A, out=5 * A, ld_out=200)
+    base.update(kw)
+    return _lib.MoeFfnFp8MatmulArgs(**base)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(rows=0), _lib.ERR_ROWS_ZERO), (dict(rows=-1), _lib.ERR_ROWS_RANGE), (dict(n=0), _lib.ERR_BAD_CONFIG),
+    (dict(k=0), _lib.ERR_BAD_CONFIG), (dict(k=40), _lib.ERR_BAD_CONFIG), (dict(a_type=2), _lib.ERR_BAD_CONFIG),
+    (dict(b_type=-1), _lib.ERR_BAD_CONFIG), (dict(out_type=3), _lib.ERR_BAD_CONFIG), (dict(a=None), _lib.ERR_NULL_PTR),
+    (dict(b_scale=None), _lib.ERR_NULL_PTR), (dict(ld_a=264), _lib.ERR_BAD_CONFIG), (dict(ld_b=240), _lib.ERR_BAD_CONFIG),
+    (dict(ld_out=199), _lib.ERR_BAD_CONFIG), (dict(a=A + 8), _lib.ERR_ALIGNMENT), (dict(b_scale=4 * A + 2), _lib.ERR_ALIGNMENT),
+    (dict(out=5 * A + 1), _lib.ERR_ALIGNMENT), (dict(out=A), _lib.ERR_ALIAS), (dict(out=2 * A), _lib.ERR_ALIAS)])
+def test_fp8_matmul_refuses(lib, kw, code):
+    assert lib.moe_ffn_fp8_matmul(ctypes.byref(_matmul(**kw)), None) == code, lib.moe_ffn_last_error(None)
+
+
+def _quantise(**kw):
+    base = dict(rows=4, k=256, type=_lib.TYPE_BF16, code_type=0, block_rows=1, pow2=0, x=A, ld_x=256, codes=2 * A,
+                ld_codes=256, scales=3 * A)
+    base.update(kw)
+    return _lib.MoeFfnFp8QuantiseArgs(**base)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(rows=0), _lib.ERR_ROWS_ZERO), (dict(rows=-1), _lib.ERR_ROWS_RANGE), (dict(k=0), _lib.ERR_BAD_CONFIG),
+    (dict(type=5), _lib.ERR_BAD_CONFIG), (dict(code_type=2), _lib.ERR_BAD_CONFIG), (dict(block_rows=64), _lib.ERR_BAD_CONFIG),
+    (dict(x=None), _lib.ERR_NULL_PTR), (dict(scales=None), _lib.ERR_NULL_PTR), (dict(ld_x=255), _lib.ERR_BAD_CONFIG),
+    (dict(ld_codes=255), _lib.ERR_BAD_CONFIG), (dict(x=A + 1), _lib.ERR_ALIGNMENT), (dict(scales=3 * A + 2), _lib.ERR_ALIGNMENT),
+    (dict(codes=A), _lib.ERR_ALIAS), (dict(scales=2 * A + 16), _lib.ERR_ALIAS)])
+def test_fp8_quantise_refuses(lib, kw, code):
+    assert lib.moe_ffn_fp8_quantise(ctypes.byref(_quantise(**kw)), None) == code, lib.moe_ffn_last_error(None)
+
+
+def test_fp8_null(lib):
+    assert lib.moe_ffn_fp8_matmul(None, None) == _lib.ERR_NULL_PTR
+    assert lib.moe_ffn_fp8_quantise(None, None) == _lib.ERR_NULL_PTR
