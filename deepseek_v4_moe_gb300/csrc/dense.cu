@@ -333,10 +333,32 @@ extern "C" int moe_ffn_gated_forward(const moe_ffn_gated_args *a, void *stream) 
   const int sms = current_sms();
   if (sms < 0) return sms;
   if ((rc = pending(who))) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (a->rows <= moe::kGemvRows) {
+    moe::GemvParams p = {};
+    p.n = a->inter;
+    p.k = a->hidden;
+    p.act = a->activation;
+    p.x = a->x;
+    p.ld_x = a->ld_x;
+    p.w[0] = a->w_gate;
+    p.w[1] = a->w_up;
+    p.out = a->workspace;
+    p.gate = a->gate;
+    p.up = a->up;
+    cudaError_t e = moe::launch_gated_gemv(true, p, a->rows, a->type == MOE_FFN_F16, st);
+    if (e != cudaSuccess) return launched(who, e);
+    p.n = a->hidden;
+    p.k = a->inter;
+    p.x = a->workspace;
+    p.ld_x = I;
+    p.w[0] = a->w_down;
+    p.out = a->y;
+    p.ld_out = a->ld_y;
+    return launched(who, moe::launch_gated_gemv(false, p, a->rows, a->type == MOE_FFN_F16, st));
+  }
   DeviceSide dev;
   if ((rc = device_side(who, &dev))) return rc;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-
   moe::GemmParams up = gemm_params(a, dev, a->rows, a->inter, kblocks(a->hidden));
   up.c[0] = a->workspace;
   up.c[1] = a->gate;
@@ -458,6 +480,23 @@ extern "C" int moe_ffn_fp8_matmul(const moe_ffn_fp8_matmul_args *a, void *stream
   const int sms = current_sms();
   if (sms < 0) return sms;
   if ((rc = pending(who))) return rc;
+  if (a->rows <= moe::kGemvRows) {
+    moe::Fp8GemvParams p = {};
+    p.n = a->n;
+    p.k = a->k;
+    p.kb = (int)KB;
+    p.a_e5m2 = a->a_type == MOE_FFN_E5M2;
+    p.b_e5m2 = a->b_type == MOE_FFN_E5M2;
+    p.a = static_cast<const uint8_t *>(a->a);
+    p.b = static_cast<const uint8_t *>(a->b);
+    p.ld_a = a->ld_a;
+    p.ld_b = a->ld_b;
+    p.a_scale = a->a_scale;
+    p.b_scale = a->b_scale;
+    p.out = a->out;
+    p.ld_out = a->ld_out;
+    return launched(who, moe::launch_fp8_gemv(p, a->rows, a->out_type, static_cast<cudaStream_t>(stream)));
+  }
   DeviceSide dev;
   if ((rc = device_side(who, &dev))) return rc;
   moe::Fp8Params p = {};

@@ -98,4 +98,32 @@ cudaError_t launch_fp8_matmul(int bn, const CUtensorMap &a, const CUtensorMap &b
                               cudaStream_t st);
 cudaError_t launch_fp8_quantise(const QuantiseParams &p, int num_sms, cudaStream_t st);
 
+// ---- products for up to kGemvRows rows on the CUDA cores (dense_gemv.cu) ----
+
+constexpr int kGemvRows = 4;
+
+struct GemvParams {
+  int n, k, splits;          // splits is set by the launch
+  int act;
+  const void *x, *w[2];
+  long long ld_x;
+  void *out, *gate, *up;
+  long long ld_out;
+};
+
+struct Fp8GemvParams {
+  int n, k, kb, splits;
+  int a_e5m2, b_e5m2;
+  const uint8_t *a, *b;
+  long long ld_a, ld_b;
+  const float *a_scale, *b_scale;
+  void *out;
+  long long ld_out;
+};
+
+// up: the gate and up projections with the activation; otherwise the down projection, which starts
+// while the kernel before it on the stream runs
+cudaError_t launch_gated_gemv(bool up, GemvParams p, int rows, bool f16, cudaStream_t st);
+cudaError_t launch_fp8_gemv(Fp8GemvParams p, int rows, int out_type, cudaStream_t st);
+
 }  // namespace moe

@@ -221,8 +221,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int BN>
 cudaError_t launch(const CUtensorMap &a, const CUtensorMap &b, const Fp8Params &p, int num_sms, cudaStream_t st) {
   using C = Fp8Cfg<BN>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(fp8_matmul_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = allow_smem((const void *)fp8_matmul_kernel<BN>, C::kSmem, done);
   if (e != cudaSuccess) return e;
   fp8_matmul_kernel<BN><<<p.tiles < num_sms ? p.tiles : num_sms, kThreads, C::kSmem, st>>>(a, b, p);
   return cudaGetLastError();

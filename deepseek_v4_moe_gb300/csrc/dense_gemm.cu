@@ -86,23 +86,6 @@ __device__ __forceinline__ Tile tile_of(const GemmParams &p, int t, int cols) {
   return r;
 }
 
-// act(g) and, for the backward pass, its derivative
-__device__ __forceinline__ float act_value(int act, float g) {
-  if (act == kSilu) return g * sigmoidf_(g);
-  return 0.5f * g * (1.f + tanhf(0.7978845608028654f * fmaf(0.044715f * g * g, g, g)));
-}
-__device__ __forceinline__ void act_both(int act, float g, float &a, float &da) {
-  if (act == kSilu) {
-    const float s = sigmoidf_(g);
-    a = g * s;
-    da = s * fmaf(g, 1.f - s, 1.f);
-  } else {
-    const float t = tanhf(0.7978845608028654f * fmaf(0.044715f * g * g, g, g));
-    a = 0.5f * g * (1.f + t);
-    da = 0.5f * (1.f + t) + 0.5f * g * (1.f - t * t) * 0.7978845608028654f * fmaf(3.f * 0.044715f * g, g, 1.f);
-  }
-}
-
 // Sixteen consecutive values of a row of T, of which those from column `left` on do not exist (left a
 // multiple of 8; the row 16-byte aligned at these columns).
 template <typename T>
@@ -318,8 +301,8 @@ int cdiv(int a, int b) { return (a + b - 1) / b; }
 template <int MODE, int BN>
 cudaError_t launch(const GemmMaps &maps, const GemmParams &p, int num_sms, cudaStream_t st) {
   using C = Cfg<MODE, BN>;
-  cudaError_t e = cudaFuncSetAttribute(dense_gemm_kernel<MODE, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)C::kSmem);
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = allow_smem((const void *)dense_gemm_kernel<MODE, BN>, C::kSmem, done);
   if (e != cudaSuccess) return e;
   dense_gemm_kernel<MODE, BN><<<p.tiles < num_sms ? p.tiles : num_sms, kThreads, C::kSmem, st>>>(maps, p);
   return cudaGetLastError();

@@ -1,0 +1,227 @@
+// The dense sublayer's products for a few rows (sm_103a): every weight is read once and multiplied on
+// the CUDA cores, which are far from busy at these sizes; the time is the weights' way from memory.
+//
+// A warp takes one output column (a row of the weight matrix; for the gate and up projections the same
+// row of both) and a share of k; lane l of it takes 16 bytes of every 512.  All loads of a warp's share
+// are issued before the first product where they fit 8 rounds, so that a few warps on each SM keep
+// enough bytes in flight.  The columns' shares of k meet in shared memory.
+//
+// The down projection is launched while the gate and up kernel still runs (programmatic dependent
+// launch): its warps fetch their weights first and wait for h then.
+#include "common.cuh"
+#include "dense.h"
+#include "dense_vec.cuh"
+#include "kernels.h"
+
+namespace moe {
+namespace {
+
+constexpr int kWarps = 8, kRounds = 8;  // warps of a CTA; 16-byte loads of a matrix in flight in a lane
+
+template <typename T>
+__device__ __forceinline__ void unpack8(const uint4 w, float (&o)[8]) {
+  const T *tag = nullptr;
+  unpack2(w.x, o[0], o[1], tag);
+  unpack2(w.y, o[2], o[3], tag);
+  unpack2(w.z, o[4], o[5], tag);
+  unpack2(w.w, o[6], o[7], tag);
+}
+
+// the sum over a column's `splits` warps of K values; valid in the column's first warp
+template <int K>
+__device__ __forceinline__ void join_splits(float (&v)[K], int splits, float (*buf)[K]) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int k = 0; k < K; ++k) v[k] = warp_sum(v[k]);
+  if (splits == 1) return;
+  if (lane == 0)
+#pragma unroll
+    for (int k = 0; k < K; ++k) buf[warp][k] = v[k];
+  __syncthreads();
+  if (warp % splits == 0)
+    for (int s = 1; s < splits; ++s)
+#pragma unroll
+      for (int k = 0; k < K; ++k) v[k] += buf[warp + s][k];
+}
+
+// UP: h = act(x w0^T) * (x w1^T), and g and u where they are wanted; otherwise out = x w0^T.
+template <bool UP, int R, typename T>
+__global__ void __launch_bounds__(32 * kWarps) gated_gemv_kernel(const __grid_constant__ GemvParams p) {
+  constexpr int M = UP ? 2 : 1;
+  __shared__ float buf[kWarps][M * R];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int col = blockIdx.x * (kWarps / p.splits) + warp / p.splits, part = warp % p.splits;
+  const bool in = col < p.n;
+  const int step = 256 * p.splits;
+  const T *w[2] = {static_cast<const T *>(p.w[0]) + (size_t)col * p.k,
+                   UP ? static_cast<const T *>(p.w[1]) + (size_t)col * p.k : nullptr};
+  if (UP) pdl_trigger();
+  float sum[M * R];
+#pragma unroll
+  for (int i = 0; i < M * R; ++i) sum[i] = 0.f;
+  bool first = true;
+  for (int k0 = part * 256 + lane * 8; first || k0 < p.k; k0 += step * kRounds) {
+    uint4 f[M][kRounds];
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i)
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+        f[m][i] = in && k0 + i * step < p.k ? ld_stream(w[m] + k0 + i * step) : make_uint4(0u, 0u, 0u, 0u);
+    if (!UP && first) pdl_wait();  // what follows reads the previous kernel's h
+    first = false;
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) {
+      const int k = k0 + i * step;
+      if (k < p.k) {
+        float a[M][8];
+#pragma unroll
+        for (int m = 0; m < M; ++m) unpack8<T>(f[m][i], a[m]);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          float b[8];
+          unpack8<T>(*reinterpret_cast<const uint4 *>(static_cast<const T *>(p.x) + r * p.ld_x + k), b);
+#pragma unroll
+          for (int m = 0; m < M; ++m)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum[m * R + r] = fmaf(a[m][e], b[e], sum[m * R + r]);
+        }
+      }
+    }
+  }
+  join_splits(sum, p.splits, buf);
+  if (!in || part != 0 || lane != 0) return;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    if constexpr (UP) {
+      const size_t at = (size_t)r * p.n + col;
+      const float g = sum[r], u = sum[R + r];
+      if (p.gate) {
+        static_cast<T *>(p.gate)[at] = from_f32<T>(g);
+        static_cast<T *>(p.up)[at] = from_f32<T>(u);
+      }
+      static_cast<T *>(p.out)[at] = from_f32<T>(act_value(p.act, g) * u);
+    } else {
+      static_cast<T *>(p.out)[r * p.ld_out + col] = from_f32<T>(sum[r]);
+    }
+  }
+}
+
+// two FP8 codes in the low 16 bits of w as floats (both formats' values are f16 values)
+__device__ __forceinline__ float2 code_pair(uint32_t w, bool e5m2) {
+  uint32_t h;
+  if (e5m2)  // the high byte of the f16 of the same value
+    h = __byte_perm(w, 0u, 0x1404);
+  else
+    asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %1;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n}" : "=r"(h) : "r"(w));
+  return __half22float2(*reinterpret_cast<const __half2 *>(&h));
+}
+__device__ __forceinline__ void codes16(const uint4 w, bool e5m2, float (&o)[16]) {
+  const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 a = code_pair(q[i], e5m2), b = code_pair(q[i] >> 16, e5m2);
+    o[4 * i] = a.x, o[4 * i + 1] = a.y, o[4 * i + 2] = b.x, o[4 * i + 3] = b.y;
+  }
+}
+
+// FP8 with block scales: eight lanes share a block of 128 codes; a lane's 16 products are summed, then
+// scaled and added.
+template <int R, typename TO>
+__global__ void __launch_bounds__(32 * kWarps) fp8_gemv_kernel(const __grid_constant__ Fp8GemvParams p) {
+  __shared__ float buf[kWarps][R];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int col = blockIdx.x * (kWarps / p.splits) + warp / p.splits, part = warp % p.splits;
+  const bool in = col < p.n;
+  const int step = 512 * p.splits;
+  const uint8_t *w = p.b + (size_t)col * p.ld_b;
+  const float *sb = p.b_scale + (size_t)(col / kScaleBlock) * p.kb;
+  float sum[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) sum[r] = 0.f;
+  for (int k0 = part * 512 + lane * 16; k0 < p.k; k0 += step * kRounds) {
+    uint4 f[kRounds];
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i)
+      f[i] = in && k0 + i * step < p.k ? ld_stream(w + k0 + i * step) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) {
+      const int k = k0 + i * step;
+      if (in && k < p.k) {
+        float b[16];
+        codes16(f[i], p.b_e5m2, b);
+        const int blk = k / kScaleBlock;
+        const float scale = sb[blk];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          float a[16], dot = 0.f;
+          codes16(*reinterpret_cast<const uint4 *>(p.a + r * p.ld_a + k), p.a_e5m2, a);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) dot = fmaf(a[e], b[e], dot);
+          sum[r] = fmaf(dot, scale * p.a_scale[(size_t)r * p.kb + blk], sum[r]);
+        }
+      }
+    }
+  }
+  join_splits(sum, p.splits, buf);
+  if (!in || part != 0 || lane != 0) return;
+#pragma unroll
+  for (int r = 0; r < R; ++r) static_cast<TO *>(p.out)[r * p.ld_out + col] = from_f32<TO>(sum[r]);
+}
+
+// Warps that share a column: as many as leave each kRounds rounds of loads or fewer, so that all are in
+// flight at once.
+int splits_for(int k, int per_round) {
+  int s = 1;
+  while (s < kWarps && k > per_round * kRounds * s) s *= 2;
+  return s;
+}
+
+template <bool UP, int R, typename T>
+cudaError_t launch_rows(const GemvParams &p, cudaStream_t st) {
+  const int cols = kWarps / p.splits, grid = (p.n + cols - 1) / cols;
+  if (UP) {
+    gated_gemv_kernel<UP, R, T><<<grid, 32 * kWarps, 0, st>>>(p);
+    return cudaGetLastError();
+  }
+  return launch_pdl(gated_gemv_kernel<UP, R, T>, dim3(grid), dim3(32 * kWarps), 0, st, p);
+}
+template <bool UP, typename T>
+cudaError_t launch_typed(const GemvParams &p, int rows, cudaStream_t st) {
+  switch (rows) {
+    case 1: return launch_rows<UP, 1, T>(p, st);
+    case 2: return launch_rows<UP, 2, T>(p, st);
+    case 3: return launch_rows<UP, 3, T>(p, st);
+    case 4: return launch_rows<UP, 4, T>(p, st);
+  }
+  return cudaErrorInvalidValue;
+}
+
+template <int R>
+cudaError_t fp8_rows(const Fp8GemvParams &p, int out_type, cudaStream_t st) {
+  const int cols = kWarps / p.splits, grid = (p.n + cols - 1) / cols;
+  if (out_type == kF32) fp8_gemv_kernel<R, float><<<grid, 32 * kWarps, 0, st>>>(p);
+  else if (out_type == kBF16) fp8_gemv_kernel<R, __nv_bfloat16><<<grid, 32 * kWarps, 0, st>>>(p);
+  else fp8_gemv_kernel<R, __half><<<grid, 32 * kWarps, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_gated_gemv(bool up, GemvParams p, int rows, bool f16, cudaStream_t st) {
+  p.splits = splits_for(p.k, 256);
+  if (up) return f16 ? launch_typed<true, __half>(p, rows, st) : launch_typed<true, __nv_bfloat16>(p, rows, st);
+  return f16 ? launch_typed<false, __half>(p, rows, st) : launch_typed<false, __nv_bfloat16>(p, rows, st);
+}
+
+cudaError_t launch_fp8_gemv(Fp8GemvParams p, int rows, int out_type, cudaStream_t st) {
+  p.splits = splits_for(p.k, 512);
+  switch (rows) {
+    case 1: return fp8_rows<1>(p, out_type, st);
+    case 2: return fp8_rows<2>(p, out_type, st);
+    case 3: return fp8_rows<3>(p, out_type, st);
+    case 4: return fp8_rows<4>(p, out_type, st);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace moe

@@ -4,6 +4,7 @@
 #include <cuda_fp16.h>
 
 #include "common.cuh"
+#include "dense.h"
 
 namespace moe {
 
@@ -118,6 +119,23 @@ __device__ __forceinline__ void load_eight(const T *row, int t, int n, int hidde
   Eight<T, VEC> e;
   e.load(row, t, n, hidden);
   e.get(o);
+}
+
+// act(g) and, for the backward pass, its derivative
+__device__ __forceinline__ float act_value(int act, float g) {
+  if (act == kSilu) return g * sigmoidf_(g);
+  return 0.5f * g * (1.f + tanhf(0.7978845608028654f * fmaf(0.044715f * g * g, g, g)));
+}
+__device__ __forceinline__ void act_both(int act, float g, float &a, float &da) {
+  if (act == kSilu) {
+    const float s = sigmoidf_(g);
+    a = g * s;
+    da = s * fmaf(g, 1.f - s, 1.f);
+  } else {
+    const float t = tanhf(0.7978845608028654f * fmaf(0.044715f * g * g, g, g));
+    a = 0.5f * g * (1.f + t);
+    da = 0.5f * (1.f + t) + 0.5f * g * (1.f - t * t) * 0.7978845608028654f * fmaf(3.f * 0.044715f * g, g, 1.f);
+  }
 }
 
 }  // namespace moe

@@ -23,6 +23,12 @@ _TYPES = {torch.float32: _lib.TYPE_F32, torch.bfloat16: _lib.TYPE_BF16, torch.fl
 _FP8 = {torch.float8_e4m3fn: _lib.TYPE_E4M3, torch.float8_e5m2: _lib.TYPE_E5M2}
 
 
+# the current stream's handle of a device, by its index: torch.cuda.current_stream() makes a Stream
+# object for it, which takes longer than the rest of a small call
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _raise(rc: int):
     raise MoeFFNError(rc, _lib.load().moe_ffn_last_error(None).decode())
 
@@ -138,7 +144,7 @@ def block_norm(state: torch.Tensor, f: Optional[torch.Tensor] = None, *, norm_f:
         a.y = y.data_ptr()
     elif y is not None:
         raise ValueError("y is written only with norm_next")
-    rc = _lib.load().moe_ffn_block_norm(ctypes.byref(a), torch.cuda.current_stream().cuda_stream)
+    rc = _lib.load().moe_ffn_block_norm(ctypes.byref(a), _raw_stream(state.device.index))
     if rc != 0:
         _raise(rc)
     return (out if f is not None else state), y
@@ -196,7 +202,7 @@ def block_norm_backward(out: torch.Tensor, f: Optional[torch.Tensor] = None, *,
     ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     if need:
         g.workspace, g.workspace_bytes = ws.data_ptr(), need
-    rc = lib.moe_ffn_block_norm_backward(ctypes.byref(a), ctypes.byref(g), torch.cuda.current_stream().cuda_stream)
+    rc = lib.moe_ffn_block_norm_backward(ctypes.byref(a), ctypes.byref(g), _raw_stream(out.device.index))
     if rc != 0:
         _raise(rc)
     return d
@@ -257,7 +263,7 @@ def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down:
         a.gate, a.up = saved[0].data_ptr(), saved[1].data_ptr()
     lib = _lib.load()
     ws = _workspace(a, lib.moe_ffn_gated_workspace(ctypes.byref(a), 0), x.device)  # noqa: F841
-    rc = lib.moe_ffn_gated_forward(ctypes.byref(a), torch.cuda.current_stream().cuda_stream)
+    rc = lib.moe_ffn_gated_forward(ctypes.byref(a), _raw_stream(x.device.index))
     if rc != 0:
         _raise(rc)
     return (out, saved) if save else out
@@ -291,7 +297,7 @@ def gated_ffn_backward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor
             setattr(a, name, d[name].data_ptr())
     lib = _lib.load()
     ws = _workspace(a, lib.moe_ffn_gated_workspace(ctypes.byref(a), 1), x.device)  # noqa: F841
-    rc = lib.moe_ffn_gated_backward(ctypes.byref(a), torch.cuda.current_stream().cuda_stream)
+    rc = lib.moe_ffn_gated_backward(ctypes.byref(a), _raw_stream(x.device.index))
     if rc != 0:
         _raise(rc)
     return d
@@ -322,7 +328,7 @@ def fp8_quantise(x: torch.Tensor, block_rows: int = 1, pow2_scales: bool = False
     scales = torch.empty((-(-rows // block_rows), -(-k // 128)), dtype=torch.float32, device=x.device)
     a = MoeFfnFp8QuantiseArgs(rows, k, _TYPES[x.dtype], _FP8[dtype], block_rows, bool(pow2_scales), x.data_ptr(), ld,
                               codes.data_ptr(), k, scales.data_ptr())
-    rc = _lib.load().moe_ffn_fp8_quantise(ctypes.byref(a), torch.cuda.current_stream().cuda_stream)
+    rc = _lib.load().moe_ffn_fp8_quantise(ctypes.byref(a), _raw_stream(x.device.index))
     if rc != 0:
         _raise(rc)
     return codes, scales
@@ -360,7 +366,7 @@ def fp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale:
     ld_out = _matrix("out", out, dev, (rows, n), out_dtype)
     args = MoeFfnFp8MatmulArgs(rows, n, k, _FP8[a.dtype], _FP8[b.dtype], _TYPES[out_dtype], a.data_ptr(), ld_a,
                                a_scale.data_ptr(), b.data_ptr(), ld_b, b_scale.data_ptr(), out.data_ptr(), ld_out)
-    rc = _lib.load().moe_ffn_fp8_matmul(ctypes.byref(args), torch.cuda.current_stream().cuda_stream)
+    rc = _lib.load().moe_ffn_fp8_matmul(ctypes.byref(args), _raw_stream(dev.index))
     if rc != 0:
         _raise(rc)
     return out
@@ -372,7 +378,7 @@ def dense_status(stream: Optional[torch.cuda.Stream] = None) -> int:
     if stream is not None:
         with torch.cuda.stream(stream):
             return dense_status()
-    rc = _lib.load().moe_ffn_dense_status(torch.cuda.current_stream().cuda_stream)
+    rc = _lib.load().moe_ffn_dense_status(_raw_stream(torch.cuda.current_device()))
     if rc < 0:
         _raise(rc)
     return rc
