@@ -366,14 +366,15 @@ extern "C" int moe_ffn_gated_forward(const moe_ffn_gated_args *a, void *stream) 
   moe::GemmParams down = gemm_params(a, dev, a->rows, a->hidden, kblocks(a->inter));
   down.c[0] = a->y;
   down.ldc[0] = a->ld_y;
-  const int bn_up = moe::gemm_pick_bn(moe::kGateUp, up, sms), bn_down = moe::gemm_pick_bn(moe::kDown, down, sms);
+  const moe::GemmTile tu = moe::gemm_pick_tile(moe::kGateUp, up, sms), td = moe::gemm_pick_tile(moe::kDown, down, sms);
+  const int bu = tu.b_box(moe::kGateUp), bd = td.b_box(moe::kDown);
   moe::GemmMaps mu, md;
-  if (!encode_map(&mu.a[0], a->x, 2, H, R, a->ld_x, 128) || !encode_map(&mu.b[0], a->w_gate, 2, H, I, H, bn_up / 2) ||
-      !encode_map(&mu.b[1], a->w_up, 2, H, I, H, bn_up / 2) || !encode_map(&md.a[0], a->workspace, 2, I, R, I, 128) ||
-      !encode_map(&md.b[0], a->w_down, 2, I, H, I, bn_down))
+  if (!encode_map(&mu.a[0], a->x, 2, H, R, a->ld_x, 128) || !encode_map(&mu.b[0], a->w_gate, 2, H, I, H, bu) ||
+      !encode_map(&mu.b[1], a->w_up, 2, H, I, H, bu) || !encode_map(&md.a[0], a->workspace, 2, I, R, I, 128) ||
+      !encode_map(&md.b[0], a->w_down, 2, I, H, I, bd))
     return fail(MOE_FFN_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", who);
-  cudaError_t e = moe::launch_dense_gemm(moe::kGateUp, bn_up, mu, up, sms, st);
-  if (e == cudaSuccess) e = moe::launch_dense_gemm(moe::kDown, bn_down, md, down, sms, st);
+  cudaError_t e = moe::launch_dense_gemm(moe::kGateUp, tu, mu, up, sms, st);
+  if (e == cudaSuccess) e = moe::launch_dense_gemm(moe::kDown, td, md, down, sms, st);
   return launched(who, e);
 }
 
@@ -422,7 +423,7 @@ extern "C" int moe_ffn_gated_backward(const moe_ffn_gated_args *a, void *stream)
   hid.e[1] = a->up;
   if (!encode_map(&m.a[0], a->d_y, 2, H, R, a->ld_d_y, 128) || !encode_map(&m.b[0], a->w_down, 2, I, H, I, 64))
     return fail(MOE_FFN_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", who);
-  cudaError_t e = moe::launch_dense_gemm(moe::kHiddenGrad, moe::gemm_pick_bn(moe::kHiddenGrad, hid, sms), m, hid, sms, st);
+  cudaError_t e = moe::launch_dense_gemm(moe::kHiddenGrad, moe::gemm_pick_tile(moe::kHiddenGrad, hid, sms), m, hid, sms, st);
   if (e == cudaSuccess && a->d_x) {
     moe::GemmParams p = gemm_params(a, dev, a->rows, a->hidden, 2 * kblocks(a->inter));
     p.kb0 = kblocks(a->inter);
@@ -431,7 +432,7 @@ extern "C" int moe_ffn_gated_backward(const moe_ffn_gated_args *a, void *stream)
     if (!encode_map(&m.a[0], dg, 2, I, R, I, 128) || !encode_map(&m.a[1], du, 2, I, R, I, 128) ||
         !encode_map(&m.b[0], a->w_gate, 2, H, I, H, 64) || !encode_map(&m.b[1], a->w_up, 2, H, I, H, 64))
       return fail(MOE_FFN_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", who);
-    e = moe::launch_dense_gemm(moe::kInputGrad, moe::gemm_pick_bn(moe::kInputGrad, p, sms), m, p, sms, st);
+    e = moe::launch_dense_gemm(moe::kInputGrad, moe::gemm_pick_tile(moe::kInputGrad, p, sms), m, p, sms, st);
   }
   if (e == cudaSuccess && weights) {
     moe::GemmParams p = gemm_params(a, dev, a->inter, a->hidden, kblocks(a->rows));
@@ -448,7 +449,7 @@ extern "C" int moe_ffn_gated_backward(const moe_ffn_gated_args *a, void *stream)
         !encode_map(&m.b[2], h, 2, I, R, I, 64))
       return fail(MOE_FFN_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", who);
     m.b[1] = m.b[0];
-    e = moe::launch_dense_gemm(moe::kWeightGrad, moe::gemm_pick_bn(moe::kWeightGrad, p, sms), m, p, sms, st);
+    e = moe::launch_dense_gemm(moe::kWeightGrad, moe::gemm_pick_tile(moe::kWeightGrad, p, sms), m, p, sms, st);
   }
   return launched(who, e);
 }

@@ -63,8 +63,14 @@ struct GemmParams {
   int inject;
 };
 
-int gemm_pick_bn(int mode, const GemmParams &p, int num_sms);
-cudaError_t launch_dense_gemm(int mode, int bn, const GemmMaps &maps, GemmParams p, int num_sms, cudaStream_t st);
+// a tile: bn columns (kGateUp: half of them of g, half of u) of 128 rows, or of 256 by a pair of CTAs
+struct GemmTile {
+  int bn;
+  bool pair;
+  int b_box(int mode) const;  // rows of B's boxes
+};
+GemmTile gemm_pick_tile(int mode, const GemmParams &p, int num_sms);
+cudaError_t launch_dense_gemm(int mode, GemmTile tile, const GemmMaps &maps, GemmParams p, int num_sms, cudaStream_t st);
 
 // ---- FP8 with block scales (dense_fp8.cu) ----
 

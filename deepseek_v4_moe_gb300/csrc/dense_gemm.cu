@@ -38,15 +38,16 @@ namespace {
 constexpr int kBK = 64;
 constexpr int kABytes = kBM * kBK * 2;
 
-template <int MODE, int BN>
+template <int MODE, int BN, bool PAIR>
 struct Cfg {
   static constexpr bool kAMn = MODE == kWeightGrad;
   static constexpr bool kBMn = MODE == kHiddenGrad || MODE == kInputGrad || MODE == kWeightGrad;
-  static constexpr int kStage = kABytes + BN * kBK * 2;
+  static constexpr int kBRows = PAIR ? BN / 2 : BN;  // of B in this CTA
+  static constexpr int kStage = kABytes + kBRows * kBK * 2;
   static constexpr int kStages = kRingBytes / kStage;
   static constexpr size_t kSmem = (size_t)kStages * kStage + 1024;
-  static constexpr int kTmemCols = 2 * BN < 32 ? 32 : 2 * BN;
-  static_assert(!kBMn || BN % 64 == 0, "an MN-major operand comes in 64-column boxes");
+  static constexpr int kTmemCols = 2 * BN < 32 ? 32 : 2 * BN > 256 ? 512 : 2 * BN;  // a power of two
+  static_assert(!kBMn || kBRows % 64 == 0, "an MN-major operand comes in 64-column boxes");
 };
 
 // MN-major operand in shared memory, SWIZZLE_128B: 64 columns x 8 k rows make 1024 bytes; the next 8 k
@@ -56,17 +57,17 @@ __device__ __forceinline__ uint64_t smem_desc_mn(uint32_t saddr) {
          (uint64_t)1u << 46 | (uint64_t)2u << 61;
 }
 
-__device__ __forceinline__ uint32_t idesc_16(bool f16, bool a_mn, bool b_mn, int N) {
+__device__ __forceinline__ uint32_t idesc_16(bool f16, bool a_mn, bool b_mn, int M, int N) {
   const uint32_t fmt = f16 ? 0u : 1u;
   return 1u << 4 | fmt << 7 | fmt << 10 | (a_mn ? 1u : 0u) << 15 | (b_mn ? 1u : 0u) << 16 | (uint32_t)(N >> 3) << 17 |
-         (uint32_t)(kBM >> 4) << 24;
+         (uint32_t)(M >> 4) << 24;
 }
 
 struct Tile {
   int prob, m0, n0;  // problem (kWeightGrad), first row, first column (kGateUp: of g and of u)
 };
 
-__device__ __forceinline__ Tile tile_of(const GemmParams &p, int t, int cols) {
+__device__ __forceinline__ Tile tile_of(const GemmParams &p, int t, int rows, int cols) {
   Tile r;
   r.prob = 0;
   int tm = p.tiles_m, tn = p.tiles_n;
@@ -81,7 +82,7 @@ __device__ __forceinline__ Tile tile_of(const GemmParams &p, int t, int cols) {
     t -= r.prob * each;
   }
   band_tile(t, tm, tn, r.m0, r.n0);
-  r.m0 *= kBM;
+  r.m0 *= rows;
   r.n0 *= cols;
   return r;
 }
@@ -155,19 +156,22 @@ __device__ __forceinline__ void epilogue(const GemmParams &p, const Tile &tl, ui
   }
 }
 
-template <int MODE, int BN>
+template <int MODE, int BN, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     dense_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ GemmParams p) {
-  using C = Cfg<MODE, BN>;
+  using C = Cfg<MODE, BN, PAIR>;
   constexpr int kCols = MODE == kGateUp ? BN / 2 : BN;  // output columns of a tile
+  constexpr int kRows = PAIR ? 2 * kBM : kBM;           // output rows of a tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ __align__(8) uint64_t full_bar[C::kStages], empty_bar[C::kStages], tfull_bar[2], tempty_bar[2];
   __shared__ __align__(8) uint64_t mma_done_bar, never_bar;
   __shared__ uint32_t tmem_base;
-  __shared__ int abort_flag;
+  __shared__ int abort_flag, issued;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = PAIR ? cluster_rank() : 0u;
+  const int first_tile = PAIR ? blockIdx.x >> 1 : blockIdx.x, tile_step = PAIR ? gridDim.x >> 1 : gridDim.x;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full_bar[s], 1);
@@ -175,16 +179,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull_bar[b], 1);
-      mbar_init(&tempty_bar[b], kEpiWarps);
+      mbar_init(&tempty_bar[b], PAIR ? 2 * kEpiWarps : kEpiWarps);
     }
     mbar_init(&mma_done_bar, 1);
     mbar_init(&never_bar, 1);
     abort_flag = 0;
+    issued = 0;
     fence_mbar_init();
   }
-  if (warp == 1) tmem_alloc(&tmem_base, C::kTmemCols);
+  if (warp == 1) {
+    if constexpr (PAIR) tmem_alloc_pair(&tmem_base, C::kTmemCols);
+    else tmem_alloc(&tmem_base, C::kTmemCols);
+  }
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync();  // the peer's barriers are initialised
   tc_fence_after();
   const uint32_t tmem = tmem_base;
   volatile int *abort_p = &abort_flag;
@@ -193,8 +202,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------- TMA producer ----------------
     int j = 0;
     bool ok = true;
-    for (int t = blockIdx.x; ok && t < p.tiles; t += gridDim.x) {
-      const Tile tl = tile_of(p, t, kCols);
+    for (int t = first_tile; ok && t < p.tiles; t += tile_step) {
+      const Tile tl = tile_of(p, t, kRows, kCols);
+      const int m0 = tl.m0 + (int)rank * kBM, n0 = tl.n0 + (MODE == kGateUp ? 0 : (int)rank * C::kBRows);
       for (int kb = 0; kb < p.kb; ++kb, ++j) {
         const int s = j % C::kStages;
         if (!mbar_wait_bounded(&empty_bar[s], (uint32_t)((j / C::kStages) & 1) ^ 1u, abort_p, p.status, p.wait_ns)) {
@@ -204,41 +214,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the second pair of matrices follows the first along k (kInputGrad)
         const int src = MODE == kWeightGrad ? tl.prob : (MODE == kInputGrad && kb >= p.kb0 ? 1 : 0);
         const int k0 = (MODE == kInputGrad && kb >= p.kb0 ? kb - p.kb0 : kb) * kBK;
-        uint64_t *fb = &full_bar[s];
-        mbar_arrive_expect_tx(fb, C::kStage);
+        // the leader's barrier counts both CTAs' bytes
+        if (rank == 0) mbar_arrive_expect_tx(&full_bar[s], PAIR ? 2 * C::kStage : C::kStage);
+        const uint32_t fb = PAIR ? in_cta(&full_bar[s], 0) : smem_u32(&full_bar[s]);
+        auto load = [&](uint8_t *dst, const CUtensorMap *map, int c_inner, int c_outer) {
+          if constexpr (PAIR) tma_load_2d_pair(dst, map, fb, c_inner, c_outer);
+          else tma_load_2d(dst, map, &full_bar[s], c_inner, c_outer);
+        };
         uint8_t *a = ring + (size_t)s * C::kStage, *b = a + kABytes;
         if constexpr (C::kAMn) {
-          tma_load_2d(a, &maps.a[src], fb, tl.m0, k0);
-          tma_load_2d(a + kBK * 128, &maps.a[src], fb, tl.m0 + 64, k0);
+          load(a, &maps.a[src], m0, k0);
+          load(a + kBK * 128, &maps.a[src], m0 + 64, k0);
         } else {
-          tma_load_2d(a, &maps.a[src], fb, k0, tl.m0);
+          load(a, &maps.a[src], k0, m0);
         }
         if constexpr (C::kBMn) {
 #pragma unroll
-          for (int i = 0; i < BN / 64; ++i) tma_load_2d(b + i * kBK * 128, &maps.b[src], fb, tl.n0 + 64 * i, k0);
+          for (int i = 0; i < C::kBRows / 64; ++i) load(b + i * kBK * 128, &maps.b[src], n0 + 64 * i, k0);
         } else if constexpr (MODE == kGateUp) {
-          tma_load_2d(b, &maps.b[0], fb, k0, tl.n0);
-          tma_load_2d(b + (BN / 2) * 128, &maps.b[1], fb, k0, tl.n0);
+          if constexpr (PAIR) {  // the leader holds the gate's rows, its peer the up projection's
+            load(b, &maps.b[rank], k0, n0);
+          } else {
+            load(b, &maps.b[0], k0, n0);
+            load(b + (BN / 2) * 128, &maps.b[1], k0, n0);
+          }
         } else {
-          tma_load_2d(b, &maps.b[0], fb, k0, tl.n0);
+          load(b, &maps.b[0], k0, n0);
         }
       }
     }
-    // copies still in flight after an abort land before the CTA may leave (bounded; in a normal run
-    // each has landed long ago)
-    int no_abort = 0;
-    for (int s = 0; s < C::kStages; ++s) {
-      const int n = j / C::kStages + (s < j % C::kStages ? 1 : 0);
-      if (n > 0) (void)mbar_wait_bounded(&full_bar[s], (uint32_t)((n - 1) & 1), &no_abort, p.status, p.wait_ns);
-    }
-  } else if (warp == 1 && lane == 0) {
+    issued = j;
+  } else if (warp == 1 && lane == 0 && rank == 0) {
     // ---------------- MMA issuer ----------------
     if (p.inject && blockIdx.x == 0)  // test hook: a wait that runs out
       (void)mbar_wait_bounded(&never_bar, 0u, abort_p, p.status, p.wait_ns);
-    const uint32_t idesc = idesc_16(p.f16, C::kAMn, C::kBMn, BN);
+    const uint32_t idesc = idesc_16(p.f16, C::kAMn, C::kBMn, kRows, BN);
     int j = 0, it = 0;
     bool ok = true;
-    for (int t = blockIdx.x; ok && t < p.tiles; t += gridDim.x, ++it) {
+    for (int t = first_tile; ok && t < p.tiles; t += tile_step, ++it) {
       const int acc = it & 1;
       if (!mbar_wait_bounded(&tempty_bar[acc], ((uint32_t)(it >> 1) & 1u) ^ 1u, abort_p, p.status, p.wait_ns)) break;
       tc_fence_after();
@@ -256,105 +269,161 @@ __global__ void __launch_bounds__(kThreads, 1)
           // 16 k are 32 bytes of a K-major row, or 16 rows of 128 bytes of an MN-major box
           const uint64_t da = C::kAMn ? smem_desc_mn(a + k * 2048) : smem_desc_sw128(a + k * 32);
           const uint64_t db = C::kBMn ? smem_desc_mn(b + k * 2048) : smem_desc_sw128(b + k * 32);
-          tc_mma_f16(d, da, db, idesc, (kb | k) ? 1u : 0u);
+          if constexpr (PAIR) tc_mma_f16_pair(d, da, db, idesc, (kb | k) ? 1u : 0u);
+          else tc_mma_f16(d, da, db, idesc, (kb | k) ? 1u : 0u);
         }
-        tc_commit(&empty_bar[s]);
+        if constexpr (PAIR) tc_commit_pair(&empty_bar[s]);
+        else tc_commit(&empty_bar[s]);
       }
-      if (ok) tc_commit(&tfull_bar[acc]);
+      if (ok) {
+        if constexpr (PAIR) tc_commit_pair(&tfull_bar[acc]);
+        else tc_commit(&tfull_bar[acc]);
+      }
     }
     // every MMA this thread issued completes before TMEM is freed
-    tc_commit(&mma_done_bar);
+    if constexpr (PAIR) tc_commit_pair_local(&mma_done_bar);
+    else tc_commit(&mma_done_bar);
     int no_abort = 0;
     (void)mbar_wait_bounded(&mma_done_bar, 0u, &no_abort, p.status, p.wait_ns);
   } else if (warp >= 2) {
     // ---------------- epilogue ----------------
     const int q = warp & 3, half = (warp - 2) >> 2;
     int it = 0;
-    for (int t = blockIdx.x; t < p.tiles; t += gridDim.x, ++it) {
+    for (int t = first_tile; t < p.tiles; t += tile_step, ++it) {
       const int acc = it & 1;
       int ready = 0;
       if (lane == 0)
         ready = mbar_wait_bounded(&tfull_bar[acc], (uint32_t)(it >> 1) & 1u, abort_p, p.status, p.wait_ns) ? 1 : 0;
       if (!__shfl_sync(0xffffffffu, ready, 0)) break;
       tc_fence_after();
-      const Tile tl = tile_of(p, t, kCols);
+      const Tile tl = tile_of(p, t, kRows, kCols);
+      const int row = tl.m0 + (int)rank * kBM + q * 32 + lane;
       const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BN);
       if (p.f16)
-        epilogue<MODE, BN, __half>(p, tl, tbase, half, tl.m0 + q * 32 + lane);
+        epilogue<MODE, BN, __half>(p, tl, tbase, half, row);
       else
-        epilogue<MODE, BN, __nv_bfloat16>(p, tl, tbase, half, tl.m0 + q * 32 + lane);
+        epilogue<MODE, BN, __nv_bfloat16>(p, tl, tbase, half, row);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&tempty_bar[acc]);
+      if (lane == 0) {
+        if constexpr (PAIR) mbar_arrive_cluster(in_cta(&tempty_bar[acc], 0));
+        else mbar_arrive(&tempty_bar[acc]);
+      }
     }
   }
+  // Copies still in flight after an abort land before a CTA may leave: the barriers that count them are
+  // waited for (bounded; in a normal run each completed long ago).  A peer may have issued stages whose
+  // arrival the leader still owes.
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync();
+  if (threadIdx.x == 0 && rank == 0) {
+    int j = issued, no_abort = 0;
+    if constexpr (PAIR) {
+      const int theirs = ld_cluster_s32(in_cta(&issued, 1));
+      for (; j < theirs; ++j) mbar_arrive_expect_tx(&full_bar[j % C::kStages], C::kStage);
+    }
+    for (int s = 0; s < C::kStages; ++s) {
+      const int n = j / C::kStages + (s < j % C::kStages ? 1 : 0);
+      if (n > 0) (void)mbar_wait_bounded(&full_bar[s], (uint32_t)((n - 1) & 1), &no_abort, p.status, p.wait_ns);
+    }
+  }
+  __syncthreads();
+  if constexpr (PAIR) cluster_sync();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, C::kTmemCols);
+    if constexpr (PAIR) tmem_dealloc_pair(tmem, C::kTmemCols);
+    else tmem_dealloc(tmem, C::kTmemCols);
   }
 }
 
 int cdiv(int a, int b) { return (a + b - 1) / b; }
 
-template <int MODE, int BN>
+template <int MODE, int BN, bool PAIR>
 cudaError_t launch(const GemmMaps &maps, const GemmParams &p, int num_sms, cudaStream_t st) {
-  using C = Cfg<MODE, BN>;
+  using C = Cfg<MODE, BN, PAIR>;
   static std::atomic<unsigned long long> done{0};
-  const cudaError_t e = allow_smem((const void *)dense_gemm_kernel<MODE, BN>, C::kSmem, done);
+  const cudaError_t e = allow_smem((const void *)dense_gemm_kernel<MODE, BN, PAIR>, C::kSmem, done);
   if (e != cudaSuccess) return e;
-  dense_gemm_kernel<MODE, BN><<<p.tiles < num_sms ? p.tiles : num_sms, kThreads, C::kSmem, st>>>(maps, p);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {PAIR ? 2u : 1u, 1u, 1u};
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = PAIR ? 1 : 0;
+  int units = num_sms;
+  if constexpr (PAIR) {  // pairs that run at one time
+    static std::atomic<int> pairs{0};
+    units = pairs.load(std::memory_order_relaxed);
+    if (!units) {
+      const cudaError_t q = cudaOccupancyMaxActiveClusters(&units, dense_gemm_kernel<MODE, BN, PAIR>, &cfg);
+      if (q != cudaSuccess) return q;
+      if (units < 1 || units > num_sms / 2) units = num_sms / 2;
+      pairs.store(units, std::memory_order_relaxed);
+    }
+  }
+  const int busy = p.tiles < units ? p.tiles : units;
+  cfg.gridDim = dim3(PAIR ? 2 * busy : busy);
+  return cudaLaunchKernelEx(&cfg, dense_gemm_kernel<MODE, BN, PAIR>, maps, p);
+}
+
+long long tiles_of(int mode, const GemmParams &p, GemmTile g) {
+  const int cols = mode == kGateUp ? g.bn / 2 : g.bn, rows = g.pair ? 2 * kBM : kBM;
+  return (long long)cdiv(p.m, rows) * cdiv(p.n, cols) * p.same + (long long)cdiv(p.m_last, rows) * cdiv(p.n_last, cols);
 }
 
 }  // namespace
 
-// The widest tile whose waves over the SMs cost least; a wave costs its tile's columns plus the part
-// of a k block that does not shrink with them.
-int gemm_pick_bn(int mode, const GemmParams &p, int num_sms) {
+int GemmTile::b_box(int mode) const {
+  if (mode == kHiddenGrad || mode == kInputGrad || mode == kWeightGrad) return 64;
+  return mode == kGateUp || pair ? bn / 2 : bn;
+}
+
+// The tile whose waves over the SMs cost least.  A wave's cost in a tile's time, in units of one
+// column of a 128-row tile at the tensor cores' rate: a pair's tile has its operands shared, a single
+// CTA's waits for shared memory below 256 columns, and every k block has a part that does not shrink.
+GemmTile gemm_pick_tile(int mode, const GemmParams &p, int num_sms) {
   const bool b_mn = mode == kHiddenGrad || mode == kInputGrad || mode == kWeightGrad;
-  int best = 0;
-  long long least = 0;
+  GemmTile best = {256, true};
+  const long long pairs = num_sms / 2;
+  double least = (double)((tiles_of(mode, p, best) + pairs - 1) / pairs) * 256;
   for (int bn = 256; bn >= (b_mn ? 64 : 32); bn /= 2) {
-    const long long cols = mode == kGateUp ? bn / 2 : bn;
-    long long tiles = (long long)cdiv(p.m, kBM) * ((p.n + cols - 1) / cols) * p.same;
-    if (p.m_last) tiles += (long long)cdiv(p.m_last, kBM) * ((p.n_last + cols - 1) / cols);
-    const long long cost = (tiles + num_sms - 1) / num_sms * (bn + 32);
-    if (!best || cost < least) {
-      best = bn;
+    const GemmTile g = {bn, false};
+    const double cost = (double)((tiles_of(mode, p, g) + num_sms - 1) / num_sms) * (1.1 * bn + 40);
+    if (cost < least) {
+      best = g;
       least = cost;
     }
   }
   return best;
 }
 
-cudaError_t launch_dense_gemm(int mode, int bn, const GemmMaps &maps, GemmParams p, int num_sms, cudaStream_t st) {
-  const int cols = mode == kGateUp ? bn / 2 : bn;
-  p.tiles_m = cdiv(p.m, kBM);
+cudaError_t launch_dense_gemm(int mode, GemmTile g, const GemmMaps &maps, GemmParams p, int num_sms, cudaStream_t st) {
+  const int cols = mode == kGateUp ? g.bn / 2 : g.bn, rows = g.pair ? 2 * kBM : kBM;
+  p.tiles_m = cdiv(p.m, rows);
   p.tiles_n = cdiv(p.n, cols);
-  p.tiles_m_last = cdiv(p.m_last, kBM);
+  p.tiles_m_last = cdiv(p.m_last, rows);
   p.tiles_n_last = cdiv(p.n_last, cols);
-  p.tiles = p.tiles_m * p.tiles_n * p.same + p.tiles_m_last * p.tiles_n_last;
-#define MOE_LAUNCH(MODE, BN) \
-  if (mode == MODE && bn == BN) return launch<MODE, BN>(maps, p, num_sms, st)
-  MOE_LAUNCH(kGateUp, 256);
-  MOE_LAUNCH(kGateUp, 128);
-  MOE_LAUNCH(kGateUp, 64);
-  MOE_LAUNCH(kGateUp, 32);
-  MOE_LAUNCH(kDown, 256);
-  MOE_LAUNCH(kDown, 128);
-  MOE_LAUNCH(kDown, 64);
-  MOE_LAUNCH(kDown, 32);
-  MOE_LAUNCH(kHiddenGrad, 256);
-  MOE_LAUNCH(kHiddenGrad, 128);
-  MOE_LAUNCH(kHiddenGrad, 64);
-  MOE_LAUNCH(kInputGrad, 256);
-  MOE_LAUNCH(kInputGrad, 128);
-  MOE_LAUNCH(kInputGrad, 64);
-  MOE_LAUNCH(kWeightGrad, 256);
-  MOE_LAUNCH(kWeightGrad, 128);
-  MOE_LAUNCH(kWeightGrad, 64);
+  p.tiles = (int)tiles_of(mode, p, g);
+#define MOE_LAUNCH(MODE, BN, PAIR) \
+  if (mode == MODE && g.bn == BN && g.pair == PAIR) return launch<MODE, BN, PAIR>(maps, p, num_sms, st)
+#define MOE_LAUNCH_ALL(MODE)     \
+  MOE_LAUNCH(MODE, 256, true);   \
+  MOE_LAUNCH(MODE, 256, false);  \
+  MOE_LAUNCH(MODE, 128, false);  \
+  MOE_LAUNCH(MODE, 64, false)
+  MOE_LAUNCH_ALL(kGateUp);
+  MOE_LAUNCH(kGateUp, 32, false);
+  MOE_LAUNCH_ALL(kDown);
+  MOE_LAUNCH(kDown, 32, false);
+  MOE_LAUNCH_ALL(kHiddenGrad);
+  MOE_LAUNCH_ALL(kInputGrad);
+  MOE_LAUNCH_ALL(kWeightGrad);
+#undef MOE_LAUNCH_ALL
 #undef MOE_LAUNCH
   return cudaErrorInvalidValue;
 }

@@ -33,73 +33,83 @@ def _raise(rc: int):
     raise MoeFFNError(rc, _lib.load().moe_ffn_last_error(None).decode())
 
 
-def _on(device: torch.device, stream: Optional[torch.cuda.Stream]):
-    """The context to run a call in, or None where the current device and stream will do."""
+def _on(t: torch.Tensor, name: str, stream: Optional[torch.cuda.Stream]):
+    """The context to run a call on tensor t in, or None where the current device and stream will do."""
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
     if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+        if stream.device.index != index:
+            raise ValueError(f"stream is on {stream.device}, {name} on {t.device}")
         return torch.cuda.stream(stream)
-    if device.index != torch.cuda.current_device():
-        return torch.cuda.device(device)
+    if index != torch.cuda.current_device():
+        return torch.cuda.device(index)
     return None
 
 
-def _matrix(name: str, t: torch.Tensor, device, shape, dtype) -> int:
-    """Checks a [rows, columns] tensor; returns the distance between its rows."""
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be a CUDA tensor on {device}")
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
-        raise ValueError(f"{name} must be of shape {list(shape) if shape is not None else '[rows, columns]'}, "
-                         f"got {list(t.shape)}")
-    if dtype is not None and t.dtype != dtype:
+# The checks below run on every call; they read each property of a tensor once.
+
+def _matrix(name: str, t: torch.Tensor, index: int, shape, dtype) -> int:
+    """Checks a matrix of `shape` on device `index`; returns the distance between its rows."""
+    if t.shape != shape:
+        raise ValueError(f"{name} must be of shape {list(shape)}, got {list(t.shape)}")
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be a CUDA tensor on device {index}")
+    ld, one = t.stride()
+    if one != 1 and shape[1] > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return ld if shape[0] > 1 else shape[1]
 
 
-def _vector(name: str, t: torch.Tensor, device, n: int, dtype=torch.float32):
-    if not t.is_cuda or t.device != device or t.dtype != dtype or tuple(t.shape) != (n,) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA {dtype} [{n}] tensor on {device}")
+def _whole(name: str, t: torch.Tensor, index: int, shape, dtype) -> int:
+    """Checks a contiguous tensor of `shape`; returns its address."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor on device {index}")
+    return t.data_ptr()
 
 
-def _norm_args(state, f, norm_f, gate, residual_scale, norm_next, eps, block_dtype) -> MoeFfnBlockNormArgs:
-    dev = state.device
-    a = MoeFfnBlockNormArgs()
-    a.ld_state = _matrix("state", state, dev, None, None)
-    rows, hidden = state.shape
-    if state.dtype not in _TYPES or block_dtype not in _TYPES or state.dtype not in (torch.float32, block_dtype):
+def _shape2(name: str, t: torch.Tensor):
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be [rows, columns], got {list(shape)}")
+    return shape
+
+
+def _norm_args(index, state, f, norm_f, gate, residual_scale, norm_next, eps, bt) -> MoeFfnBlockNormArgs:
+    shape, ts = _shape2("state", state), state.dtype
+    rows, hidden = shape
+    if ts not in _TYPES or bt not in _TYPES or (ts is not torch.float32 and ts is not bt):
         raise ValueError("state must be float32 or of the block's type (float32, bfloat16, float16)")
-    a.rows, a.hidden, a.stream_type, a.block_type = rows, hidden, _TYPES[state.dtype], _TYPES[block_dtype]
-    a.residual_scale, a.eps, a.state = residual_scale, eps, state.data_ptr()
+    ld_state = _matrix("state", state, index, shape, ts)
+    f_ptr = norm_f_ptr = norm_next_ptr = gate_ptr = None
+    ld_f = gate_type = gate_kind = rows_per_gate = 0
     if f is not None:
-        a.ld_f = _matrix("f", f, dev, (rows, hidden), None)
-        a.f = f.data_ptr()
+        ld_f, f_ptr = _matrix("f", f, index, shape, bt), f.data_ptr()
     elif gate is not None or norm_f is not None:
         raise ValueError("gate and norm_f need f")
     if norm_f is not None:
-        _vector("norm_f", norm_f, dev, hidden)
-        a.norm_f = norm_f.data_ptr()
+        norm_f_ptr = _whole("norm_f", norm_f, index, (hidden,), torch.float32)
     if norm_next is not None:
-        _vector("norm_next", norm_next, dev, hidden)
-        a.norm_next = norm_next.data_ptr()
+        norm_next_ptr = _whole("norm_next", norm_next, index, (hidden,), torch.float32)
     if gate is not None:
-        if gate.device != dev or gate.dtype not in (torch.float32, block_dtype) or not gate.is_contiguous():
+        gs, gt = gate.shape, gate.dtype
+        if gate.get_device() != index or (gt is not torch.float32 and gt is not bt) or not gate.is_contiguous():
             raise ValueError("gate must be contiguous, on the state's device, float32 or of the block's type")
-        shape = tuple(gate.shape)
-        if shape == (hidden,):
-            a.gate_kind, a.rows_per_gate = GATE_VECTOR, max(rows, 1)
-        elif len(shape) == 2 and shape[1] == hidden and shape[0] > 0 and rows % shape[0] == 0 and rows > 0:
-            a.gate_kind, a.rows_per_gate = GATE_VECTOR, rows // shape[0]
-        elif shape == (rows, 1):
-            a.gate_kind = GATE_TOKEN
+        if gs == (hidden,):
+            gate_kind, rows_per_gate = GATE_VECTOR, max(rows, 1)
+        elif len(gs) == 2 and gs[1] == hidden and gs[0] > 0 and rows > 0 and rows % gs[0] == 0:
+            gate_kind, rows_per_gate = GATE_VECTOR, rows // gs[0]
+        elif gs == (rows, 1):
+            gate_kind = GATE_TOKEN
         else:
             raise ValueError(f"gate must be [{hidden}], [G, {hidden}] with G dividing {rows}, or [{rows}, 1]; "
-                             f"got {list(shape)}")
-        a.gate_type, a.gate = _TYPES[gate.dtype], gate.data_ptr()
-    else:
-        a.gate_kind = GATE_NONE
-    return a
+                             f"got {list(gs)}")
+        gate_type, gate_ptr = _TYPES[gt], gate.data_ptr()
+    return MoeFfnBlockNormArgs(rows, hidden, _TYPES[ts], _TYPES[bt], gate_type, gate_kind, rows_per_gate,
+                               residual_scale, eps, state.data_ptr(), ld_state, f_ptr, ld_f, gate_ptr, norm_f_ptr,
+                               norm_next_ptr)
 
 
 def block_norm(state: torch.Tensor, f: Optional[torch.Tensor] = None, *, norm_f: Optional[torch.Tensor] = None,
@@ -119,9 +129,7 @@ def block_norm(state: torch.Tensor, f: Optional[torch.Tensor] = None, *, norm_f:
     ``state``, is made, in ``block_dtype`` (default: the state's type).  ``out`` may be ``state``.
     Returns (out, y); y is None without ``norm_next``, out is ``state`` itself without ``f``.
     """
-    if not state.is_cuda:
-        raise ValueError("state must be a CUDA tensor")
-    ctx = _on(state.device, stream)
+    ctx = _on(state, "state", stream)
     if ctx is not None:
         with ctx:
             return block_norm(state, f, norm_f=norm_f, gate=gate, residual_scale=residual_scale, norm_next=norm_next,
@@ -129,22 +137,26 @@ def block_norm(state: torch.Tensor, f: Optional[torch.Tensor] = None, *, norm_f:
     bt = f.dtype if f is not None else (block_dtype or state.dtype)
     if block_dtype is not None and block_dtype != bt:
         raise ValueError("block_dtype must be f's type")
-    a = _norm_args(state, f, norm_f, gate, residual_scale, norm_next, eps, bt)
+    index = state.get_device()
+    a = _norm_args(index, state, f, norm_f, gate, residual_scale, norm_next, eps, bt)
+    shape = state.shape
     if f is not None:
         if out is None:
-            out = torch.empty(state.shape, dtype=state.dtype, device=state.device)
-        a.ld_out = _matrix("out", out, state.device, state.shape, state.dtype)
+            out, a.ld_out = torch.empty(shape, dtype=state.dtype, device=state.device), shape[1]
+        else:
+            a.ld_out = _matrix("out", out, index, shape, state.dtype)
         a.out = out.data_ptr()
     elif out is not None:
         raise ValueError("out is written only with f")
     if norm_next is not None:
         if y is None:
-            y = torch.empty(state.shape, dtype=bt, device=state.device)
-        a.ld_y = _matrix("y", y, state.device, state.shape, bt)
+            y, a.ld_y = torch.empty(shape, dtype=bt, device=state.device), shape[1]
+        else:
+            a.ld_y = _matrix("y", y, index, shape, bt)
         a.y = y.data_ptr()
     elif y is not None:
         raise ValueError("y is written only with norm_next")
-    rc = _lib.load().moe_ffn_block_norm(ctypes.byref(a), _raw_stream(state.device.index))
+    rc = _lib.load().moe_ffn_block_norm(ctypes.byref(a), _raw_stream(index))
     if rc != 0:
         _raise(rc)
     return (out if f is not None else state), y
@@ -162,9 +174,7 @@ def block_norm_backward(out: torch.Tensor, f: Optional[torch.Tensor] = None, *,
     ``d_y`` goes with ``norm_next``.  Returns a dict of the gradients of what was given: d_state, d_f,
     d_gate, d_norm_f and d_norm_next.
     """
-    if not out.is_cuda:
-        raise ValueError("out must be a CUDA tensor")
-    ctx = _on(out.device, stream)
+    ctx = _on(out, "out", stream)
     if ctx is not None:
         with ctx:
             return block_norm_backward(out, f, norm_f=norm_f, gate=gate, residual_scale=residual_scale,
@@ -173,14 +183,14 @@ def block_norm_backward(out: torch.Tensor, f: Optional[torch.Tensor] = None, *,
         raise ValueError("neither f nor norm_next is given")
     if (norm_next is None) != (d_y is None):
         raise ValueError("d_y goes with norm_next")
-    dev, shape = out.device, out.shape
+    index, dev, shape = out.get_device(), out.device, out.shape
     bt = f.dtype if f is not None else d_y.dtype
-    a = _norm_args(out, f, norm_f, gate, residual_scale, norm_next, eps, bt)
+    a = _norm_args(index, out, f, norm_f, gate, residual_scale, norm_next, eps, bt)
     g, d = MoeFfnBlockNormGrads(), {}
     if d_out is not None:
-        g.ld_d_out, g.d_out = _matrix("d_out", d_out, dev, shape, out.dtype), d_out.data_ptr()
+        g.ld_d_out, g.d_out = _matrix("d_out", d_out, index, shape, out.dtype), d_out.data_ptr()
     if d_y is not None:
-        g.ld_d_y, g.d_y = _matrix("d_y", d_y, dev, shape, bt), d_y.data_ptr()
+        g.ld_d_y, g.d_y = _matrix("d_y", d_y, index, shape, bt), d_y.data_ptr()
 
     def new(name, like_shape, dtype):
         d[name] = torch.empty(like_shape, dtype=dtype, device=dev)
@@ -202,31 +212,24 @@ def block_norm_backward(out: torch.Tensor, f: Optional[torch.Tensor] = None, *,
     ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     if need:
         g.workspace, g.workspace_bytes = ws.data_ptr(), need
-    rc = lib.moe_ffn_block_norm_backward(ctypes.byref(a), ctypes.byref(g), _raw_stream(out.device.index))
+    rc = lib.moe_ffn_block_norm_backward(ctypes.byref(a), ctypes.byref(g), _raw_stream(index))
     if rc != 0:
         _raise(rc)
     return d
 
 
-def _gated_args(x, w_gate, w_up, w_down, activation) -> MoeFfnGatedArgs:
-    dev, dt = x.device, x.dtype
-    if dt not in (torch.bfloat16, torch.float16):
+def _gated_args(index, x, w_gate, w_up, w_down, activation) -> MoeFfnGatedArgs:
+    shape, dt = _shape2("x", x), x.dtype
+    if dt is not torch.bfloat16 and dt is not torch.float16:
         raise ValueError("x must be bfloat16 or float16")
     if activation not in ACTIVATIONS:
         raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
-    a = MoeFfnGatedArgs()
-    a.ld_x = _matrix("x", x, dev, None, None)
-    rows, hidden = x.shape
-    if w_gate.dim() != 2:
-        raise ValueError("w_gate must be [inter, hidden]")
-    inter = w_gate.shape[0]
-    for name, w, shape in (("w_gate", w_gate, (inter, hidden)), ("w_up", w_up, (inter, hidden)),
-                           ("w_down", w_down, (hidden, inter))):
-        if tuple(w.shape) != shape or w.dtype != dt or w.device != dev or not w.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous {dt} {list(shape)} tensor on {dev}")
-    a.rows, a.hidden, a.inter, a.type, a.activation = rows, hidden, inter, _TYPES[dt], ACTIVATIONS[activation]
-    a.x, a.w_gate, a.w_up, a.w_down = x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr()
-    return a
+    rows, hidden = shape
+    inter = _shape2("w_gate", w_gate)[0]
+    return MoeFfnGatedArgs(rows, hidden, inter, _TYPES[dt], ACTIVATIONS[activation], x.data_ptr(),
+                           _matrix("x", x, index, shape, dt), _whole("w_gate", w_gate, index, (inter, hidden), dt),
+                           _whole("w_up", w_up, index, (inter, hidden), dt),
+                           _whole("w_down", w_down, index, (hidden, inter), dt))
 
 
 def _workspace(a: MoeFfnGatedArgs, need: int, device) -> torch.Tensor:
@@ -247,23 +250,24 @@ def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down:
     (tanh form).  Returns y [rows, hidden]; with ``save`` also the pair (g, u) of projections
     [rows, inter] that :func:`gated_ffn_backward` takes.
     """
-    if not x.is_cuda:
-        raise ValueError("x must be a CUDA tensor")
-    ctx = _on(x.device, stream)
+    ctx = _on(x, "x", stream)
     if ctx is not None:
         with ctx:
             return gated_ffn(x, w_gate, w_up, w_down, activation, save, out)
-    a = _gated_args(x, w_gate, w_up, w_down, activation)
+    index = x.get_device()
+    a = _gated_args(index, x, w_gate, w_up, w_down, activation)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    a.ld_y, a.y = _matrix("out", out, x.device, x.shape, x.dtype), out.data_ptr()
+        out, a.ld_y = torch.empty(x.shape, dtype=x.dtype, device=x.device), a.hidden
+    else:
+        a.ld_y = _matrix("out", out, index, x.shape, x.dtype)
+    a.y = out.data_ptr()
     saved = None
     if save:
         saved = tuple(torch.empty((a.rows, a.inter), dtype=x.dtype, device=x.device) for _ in range(2))
         a.gate, a.up = saved[0].data_ptr(), saved[1].data_ptr()
     lib = _lib.load()
     ws = _workspace(a, lib.moe_ffn_gated_workspace(ctypes.byref(a), 0), x.device)  # noqa: F841
-    rc = lib.moe_ffn_gated_forward(ctypes.byref(a), _raw_stream(x.device.index))
+    rc = lib.moe_ffn_gated_forward(ctypes.byref(a), _raw_stream(index))
     if rc != 0:
         _raise(rc)
     return (out, saved) if save else out
@@ -274,19 +278,14 @@ def gated_ffn_backward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor
                        stream: Optional[torch.cuda.Stream] = None) -> dict:
     """Gradients of :func:`gated_ffn` from what it saved: a dict of d_x, d_w_gate, d_w_up and d_w_down
     (of the inputs' type), without d_x or the weights' where they are not needed."""
-    if not x.is_cuda:
-        raise ValueError("x must be a CUDA tensor")
-    ctx = _on(x.device, stream)
+    ctx = _on(x, "x", stream)
     if ctx is not None:
         with ctx:
             return gated_ffn_backward(x, w_gate, w_up, w_down, saved, d_y, activation, need_x, need_weights)
-    a = _gated_args(x, w_gate, w_up, w_down, activation)
-    for name, t in zip(("saved[0]", "saved[1]"), saved):
-        _matrix(name, t, x.device, (a.rows, a.inter), x.dtype)
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    a.gate, a.up = saved[0].data_ptr(), saved[1].data_ptr()
-    a.ld_d_y, a.d_y = _matrix("d_y", d_y, x.device, x.shape, x.dtype), d_y.data_ptr()
+    index = x.get_device()
+    a = _gated_args(index, x, w_gate, w_up, w_down, activation)
+    a.gate, a.up = (_whole("saved", t, index, (a.rows, a.inter), x.dtype) for t in saved)
+    a.ld_d_y, a.d_y = _matrix("d_y", d_y, index, x.shape, x.dtype), d_y.data_ptr()
     d = {}
     if need_x:
         d["d_x"] = torch.empty(x.shape, dtype=x.dtype, device=x.device)
@@ -297,7 +296,7 @@ def gated_ffn_backward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor
             setattr(a, name, d[name].data_ptr())
     lib = _lib.load()
     ws = _workspace(a, lib.moe_ffn_gated_workspace(ctypes.byref(a), 1), x.device)  # noqa: F841
-    rc = lib.moe_ffn_gated_backward(ctypes.byref(a), _raw_stream(x.device.index))
+    rc = lib.moe_ffn_gated_backward(ctypes.byref(a), _raw_stream(index))
     if rc != 0:
         _raise(rc)
     return d
@@ -312,23 +311,22 @@ def fp8_quantise(x: torch.Tensor, block_rows: int = 1, pow2_scales: bool = False
     block's scale is its largest magnitude over the largest code, 1 for zeros, at least 2^-126, with
     ``pow2_scales`` rounded up to a power of two; a code is x / scale rounded to nearest even.
     """
-    if not x.is_cuda:
-        raise ValueError("x must be a CUDA tensor")
-    ctx = _on(x.device, stream)
+    ctx = _on(x, "x", stream)
     if ctx is not None:
         with ctx:
             return fp8_quantise(x, block_rows, pow2_scales, dtype)
+    index = x.get_device()
     if x.dtype not in _TYPES or dtype not in _FP8:
         raise ValueError("x must be float32, bfloat16 or float16, dtype float8_e4m3fn or float8_e5m2")
     if block_rows not in (1, 128):
         raise ValueError("block_rows must be 1 or 128")
-    ld = _matrix("x", x, x.device, None, None)
-    rows, k = x.shape
+    rows, k = shape = _shape2("x", x)
+    ld = _matrix("x", x, index, shape, x.dtype)
     codes = torch.empty((rows, k), dtype=dtype, device=x.device)
     scales = torch.empty((-(-rows // block_rows), -(-k // 128)), dtype=torch.float32, device=x.device)
     a = MoeFfnFp8QuantiseArgs(rows, k, _TYPES[x.dtype], _FP8[dtype], block_rows, bool(pow2_scales), x.data_ptr(), ld,
                               codes.data_ptr(), k, scales.data_ptr())
-    rc = _lib.load().moe_ffn_fp8_quantise(ctypes.byref(a), _raw_stream(x.device.index))
+    rc = _lib.load().moe_ffn_fp8_quantise(ctypes.byref(a), _raw_stream(index))
     if rc != 0:
         _raise(rc)
     return codes, scales
@@ -342,31 +340,26 @@ def fp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale:
     :func:`fp8_quantise`; each float8_e4m3fn or float8_e5m2), k a multiple of 16.  Sums are float32; the
     result is ``out_dtype``: float32, bfloat16 or float16.
     """
-    if not a.is_cuda:
-        raise ValueError("a must be a CUDA tensor")
-    ctx = _on(a.device, stream)
+    ctx = _on(a, "a", stream)
     if ctx is not None:
         with ctx:
             return fp8_matmul(a, a_scale, b, b_scale, out_dtype, out)
-    dev = a.device
-    if a.dtype not in _FP8 or b.dtype not in _FP8 or out_dtype not in _TYPES:
+    index, ta, tb = a.get_device(), a.dtype, b.dtype
+    if ta not in _FP8 or tb not in _FP8 or out_dtype not in _TYPES:
         raise ValueError("a and b must be float8_e4m3fn or float8_e5m2, out_dtype float32, bfloat16 or float16")
-    ld_a = _matrix("a", a, dev, None, None)
-    rows, k = a.shape
-    if b.dim() != 2 or b.shape[1] != k:
-        raise ValueError(f"b must be [n, {k}], got {list(b.shape)}")
-    n = b.shape[0]
-    ld_b = _matrix("b", b, dev, None, None)
+    rows, k = shape = _shape2("a", a)
+    n = _shape2("b", b)[0]
     kb = -(-k // 128)
-    for name, t, shape in (("a_scale", a_scale, (rows, kb)), ("b_scale", b_scale, (-(-n // 128), kb))):
-        if tuple(t.shape) != shape or t.dtype != torch.float32 or t.device != dev or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous float32 {list(shape)} tensor on {dev}")
+    ld_a, ld_b = _matrix("a", a, index, shape, ta), _matrix("b", b, index, (n, k), tb)
+    sa = _whole("a_scale", a_scale, index, (rows, kb), torch.float32)
+    sb = _whole("b_scale", b_scale, index, (-(-n // 128), kb), torch.float32)
     if out is None:
-        out = torch.empty((rows, n), dtype=out_dtype, device=dev)
-    ld_out = _matrix("out", out, dev, (rows, n), out_dtype)
-    args = MoeFfnFp8MatmulArgs(rows, n, k, _FP8[a.dtype], _FP8[b.dtype], _TYPES[out_dtype], a.data_ptr(), ld_a,
-                               a_scale.data_ptr(), b.data_ptr(), ld_b, b_scale.data_ptr(), out.data_ptr(), ld_out)
-    rc = _lib.load().moe_ffn_fp8_matmul(ctypes.byref(args), _raw_stream(dev.index))
+        out, ld_out = torch.empty((rows, n), dtype=out_dtype, device=a.device), n
+    else:
+        ld_out = _matrix("out", out, index, (rows, n), out_dtype)
+    args = MoeFfnFp8MatmulArgs(rows, n, k, _FP8[ta], _FP8[tb], _TYPES[out_dtype], a.data_ptr(), ld_a, sa, b.data_ptr(),
+                               ld_b, sb, out.data_ptr(), ld_out)
+    rc = _lib.load().moe_ffn_fp8_matmul(ctypes.byref(args), _raw_stream(index))
     if rc != 0:
         _raise(rc)
     return out

@@ -97,7 +97,8 @@ def run(x, wg, wu, wd, dy, name):
 
 SIZES = [(1, 8, 8), (1, 64, 64), (2, 72, 136), (3, 128, 128), (4, 1000, 24), (5, 256, 256), (8, 264, 520), (17, 512, 1032),
          (64, 128, 2048), (127, 200, 72), (128, 256, 512), (129, 384, 264), (300, 1000, 1416), (515, 648, 328),
-         (1, 4096, 2048), (2, 2048, 4096), (4, 4096, 2048), (70, 4096, 2048), (1500, 512, 384)]
+         (1, 4096, 2048), (2, 2048, 4096), (4, 4096, 2048), (70, 4096, 2048), (1500, 512, 384),
+         (2049, 1032, 2056), (1100, 4096, 2048)]
 
 
 @pytest.mark.parametrize("rows,hidden,inter", SIZES)
@@ -224,17 +225,18 @@ def test_rows_behind_the_last_stay(cuda_lib):
 
 def test_a_wait_that_runs_out_is_reported(cuda_lib):
     import deepseek_v4_moe_gb300 as m
-    t = make(200, 256, 256, BF16, seed=10)
-    good = m.gated_ffn(*t[:4])
-    assert m.dense_status() == 0
-    assert cuda_lib.moe_ffn_dense_fault_injection(1, 20000) == 0
-    try:
-        m.gated_ffn(*t[:4])
-        assert m.dense_status() == 8
-    finally:
-        cuda_lib.moe_ffn_dense_fault_injection(0, 0)
-    assert torch.equal(m.gated_ffn(*t[:4]), good)
-    assert m.dense_status() == 0
+    for size in ((200, 256, 256), (4096, 2048, 2048)):  # single CTAs, and pairs
+        t = make(*size, BF16, seed=10)
+        good = m.gated_ffn(*t[:4])
+        assert m.dense_status() == 0
+        assert cuda_lib.moe_ffn_dense_fault_injection(1, 20000) == 0
+        try:
+            m.gated_ffn(*t[:4])
+            assert m.dense_status() == 8
+        finally:
+            cuda_lib.moe_ffn_dense_fault_injection(0, 0)
+        assert torch.equal(m.gated_ffn(*t[:4]), good)
+        assert m.dense_status() == 0
 
 
 def test_refusals(cuda_lib):
