@@ -41,16 +41,6 @@ __device__ __forceinline__ uint32_t idesc_f8(bool a_e5m2, bool b_e5m2, int N) {
          (uint32_t)(kBM >> 4) << 24;
 }
 
-__device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                          uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
 template <typename T, int N>
 __device__ __forceinline__ void store_row(T *dst, int left, bool wide, const float (&v)[N]) {
   constexpr int per = 16 / (int)sizeof(T);
@@ -83,9 +73,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ __align__(8) uint64_t full_bar[C::kStages], empty_bar[C::kStages], tfull_bar[C::kAcc], tempty_bar[C::kAcc];
   __shared__ __align__(8) uint64_t mma_done_bar, never_bar;
   __shared__ uint32_t tmem_base;
-  __shared__ int abort_flag;
+  __shared__ int abort_flag, issued;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full_bar[s], 1);
@@ -98,6 +88,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&mma_done_bar, 1);
     mbar_init(&never_bar, 1);
     abort_flag = 0;
+    issued = 0;
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc(&tmem_base, C::kTmemCols);
@@ -107,60 +98,57 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = tmem_base;
   volatile int *abort_p = &abort_flag;
 
-  if (warp == 0 && lane == 0) {
+  if (warp == 0) {
     // ---------------- TMA producer ----------------
+    RingPos<C::kStages> pos;
     int j = 0;
     bool ok = true;
+    const uint32_t ring0 = smem_u32(ring), full0 = smem_u32(full_bar);
     for (int t = blockIdx.x; ok && t < p.tiles; t += gridDim.x) {
       int m, n;
       band_tile(t, p.tiles_m, p.tiles_n, m, n);
-      for (int kb = 0; kb < p.kb; ++kb, ++j) {
-        const int s = j % C::kStages;
-        if (!mbar_wait_bounded(&empty_bar[s], (uint32_t)((j / C::kStages) & 1) ^ 1u, abort_p, p.status, p.wait_ns)) {
+      for (int kb = 0; kb < p.kb; ++kb, ++j, pos.next()) {
+        const int s = pos.slot;
+        if (!warp_wait(&empty_bar[s], pos.round ^ 1u, abort_p, p.status, p.wait_ns)) {
           ok = false;
           break;
         }
-        mbar_arrive_expect_tx(&full_bar[s], C::kStage);
-        uint8_t *a = ring + (size_t)s * C::kStage;
-        tma_load_2d(a, &tm_a, &full_bar[s], kb * kScaleBlock, m * kBM);
-        tma_load_2d(a + C::kABytes, &tm_b, &full_bar[s], kb * kScaleBlock, n * BN);
+        const uint32_t a = ring0 + s * C::kStage, fb = full0 + 8 * s;
+        mbar_expect_one(fb, C::kStage);
+        tma_load_2d_one<false>(a, &tm_a, fb, kb * kScaleBlock, m * kBM);
+        tma_load_2d_one<false>(a + C::kABytes, &tm_b, fb, kb * kScaleBlock, n * BN);
       }
     }
-    // copies still in flight after an abort land before the CTA may leave (bounded)
-    int no_abort = 0;
-    for (int s = 0; s < C::kStages; ++s) {
-      const int n = j / C::kStages + (s < j % C::kStages ? 1 : 0);
-      if (n > 0) (void)mbar_wait_bounded(&full_bar[s], (uint32_t)((n - 1) & 1), &no_abort, p.status, p.wait_ns);
-    }
-  } else if (warp == 1 && lane == 0) {
+    if (lane == 0) issued = j;
+  } else if (warp == 1) {
     // ---------------- MMA issuer ----------------
     if (p.inject && blockIdx.x == 0)  // test hook: a wait that runs out
-      (void)mbar_wait_bounded(&never_bar, 0u, abort_p, p.status, p.wait_ns);
+      (void)warp_wait(&never_bar, 0u, abort_p, p.status, p.wait_ns);
     const uint32_t idesc = idesc_f8(p.a_e5m2, p.b_e5m2, BN);
-    int j = 0;
+    const uint64_t a0 = smem_desc_sw128(0) + (uint64_t)(smem_u32(ring) >> 4), b0 = a0 + (C::kABytes >> 4);
+    RingPos<C::kStages> pos;
+    RingPos<C::kAcc> acc;
     bool ok = true;
     for (int t = blockIdx.x; ok && t < p.tiles; t += gridDim.x) {
-      for (int kb = 0; kb < p.kb; ++kb, ++j) {
-        const int s = j % C::kStages, acc = j % C::kAcc;
-        if (!mbar_wait_bounded(&tempty_bar[acc], (uint32_t)((j / C::kAcc) & 1) ^ 1u, abort_p, p.status, p.wait_ns) ||
-            !mbar_wait_bounded(&full_bar[s], (uint32_t)((j / C::kStages) & 1), abort_p, p.status, p.wait_ns)) {
+      for (int kb = 0; kb < p.kb; ++kb, pos.next(), acc.next()) {
+        if (!warp_wait(&tempty_bar[acc.slot], acc.round ^ 1u, abort_p, p.status, p.wait_ns) ||
+            !warp_wait(&full_bar[pos.slot], pos.round, abort_p, p.status, p.wait_ns)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t a = smem_u32(ring + (size_t)s * C::kStage), b = a + C::kABytes;
+        const uint32_t at = pos.slot * (C::kStage >> 4), d = tmem + (uint32_t)(acc.slot * BN);
 #pragma unroll
         for (int k = 0; k < kScaleBlock / 32; ++k)
-          tc_mma_f8(tmem + (uint32_t)(acc * BN), smem_desc_sw128(a + k * 32), smem_desc_sw128(b + k * 32), idesc,
-                    k ? 1u : 0u);
-        tc_commit(&empty_bar[s]);
-        tc_commit(&tfull_bar[acc]);
+          tc_mma_one<false, true>(d, a0 + (at + k * 2), b0 + (at + k * 2), idesc, k ? 1u : 0u);
+        tc_commit_one<false>(smem_u32(&empty_bar[pos.slot]));
+        tc_commit_one<false>(smem_u32(&tfull_bar[acc.slot]));
       }
     }
-    // every MMA this thread issued completes before TMEM is freed
-    tc_commit(&mma_done_bar);
+    // every MMA this warp issued completes before TMEM is freed
+    tc_commit_one<false>(smem_u32(&mma_done_bar));
     int no_abort = 0;
-    (void)mbar_wait_bounded(&mma_done_bar, 0u, &no_abort, p.status, p.wait_ns);
+    (void)wait_bounded(&mma_done_bar, 0u, &no_abort, p.status, p.wait_ns);
   } else if (warp >= 2) {
     // ---------------- scaled accumulation and output ----------------
     const int q = warp & 3, half = (warp - 2) >> 2;
@@ -181,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float scale = in ? sa[kb] * sb[kb] : 0.f;
         int ready = 0;
         if (lane == 0)
-          ready = mbar_wait_bounded(&tfull_bar[acc], (uint32_t)((j / C::kAcc) & 1), abort_p, p.status, p.wait_ns) ? 1 : 0;
+          ready = wait_bounded(&tfull_bar[acc], (uint32_t)((j / C::kAcc) & 1), abort_p, p.status, p.wait_ns) ? 1 : 0;
         if (!__shfl_sync(0xffffffffu, ready, 0)) {
           ok = false;
           break;
@@ -210,7 +198,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     }
   }
+  // copies still in flight after an abort land before the CTA may leave (bounded; in a normal run each
+  // has landed long ago)
   tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int no_abort = 0;
+    for (int s = 0; s < C::kStages; ++s) {
+      const int n = issued / C::kStages + (s < issued % C::kStages ? 1 : 0);
+      if (n > 0) (void)wait_bounded(&full_bar[s], (uint32_t)((n - 1) & 1), &no_abort, p.status, p.wait_ns);
+    }
+  }
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();

@@ -42,12 +42,13 @@ template <int MODE, int BN, bool PAIR>
 struct Cfg {
   static constexpr bool kAMn = MODE == kWeightGrad;
   static constexpr bool kBMn = MODE == kHiddenGrad || MODE == kInputGrad || MODE == kWeightGrad;
-  static constexpr int kBRows = PAIR ? BN / 2 : BN;  // of B in this CTA
+  // rows of B in this CTA; an MN-major operand comes in whole boxes of 64, of which the last may be used in part
+  static constexpr int kBUsed = PAIR ? BN / 2 : BN, kBRows = kBMn ? (kBUsed + 63) / 64 * 64 : kBUsed;
   static constexpr int kStage = kABytes + kBRows * kBK * 2;
   static constexpr int kStages = kRingBytes / kStage;
   static constexpr size_t kSmem = (size_t)kStages * kStage + 1024;
   static constexpr int kTmemCols = 2 * BN < 32 ? 32 : 2 * BN > 256 ? 512 : 2 * BN;  // a power of two
-  static_assert(!kBMn || kBRows % 64 == 0, "an MN-major operand comes in 64-column boxes");
+  static_assert(BN % 32 == 0 && kBRows % 8 == 0, "whole epilogue chunks and swizzle groups");
 };
 
 // MN-major operand in shared memory, SWIZZLE_128B: 64 columns x 8 k rows make 1024 bytes; the next 8 k
@@ -169,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag, issued;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = PAIR ? cluster_rank() : 0u;
   const int first_tile = PAIR ? blockIdx.x >> 1 : blockIdx.x, tile_step = PAIR ? gridDim.x >> 1 : gridDim.x;
   if (threadIdx.x == 0) {
@@ -198,16 +199,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = tmem_base;
   volatile int *abort_p = &abort_flag;
 
-  if (warp == 0 && lane == 0) {
+  if (warp == 0) {
     // ---------------- TMA producer ----------------
+    RingPos<C::kStages> pos;
     int j = 0;
     bool ok = true;
+    const uint32_t ring0 = smem_u32(ring), full0 = PAIR ? in_cta(full_bar, 0) : smem_u32(full_bar);
     for (int t = first_tile; ok && t < p.tiles; t += tile_step) {
       const Tile tl = tile_of(p, t, kRows, kCols);
-      const int m0 = tl.m0 + (int)rank * kBM, n0 = tl.n0 + (MODE == kGateUp ? 0 : (int)rank * C::kBRows);
-      for (int kb = 0; kb < p.kb; ++kb, ++j) {
-        const int s = j % C::kStages;
-        if (!mbar_wait_bounded(&empty_bar[s], (uint32_t)((j / C::kStages) & 1) ^ 1u, abort_p, p.status, p.wait_ns)) {
+      const int m0 = tl.m0 + (int)rank * kBM, n0 = tl.n0 + (MODE == kGateUp ? 0 : (int)rank * C::kBUsed);
+      for (int kb = 0; kb < p.kb; ++kb, ++j, pos.next()) {
+        const int s = pos.slot;
+        if (!warp_wait(&empty_bar[s], pos.round ^ 1u, abort_p, p.status, p.wait_ns)) {
           ok = false;
           break;
         }
@@ -215,76 +218,68 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int src = MODE == kWeightGrad ? tl.prob : (MODE == kInputGrad && kb >= p.kb0 ? 1 : 0);
         const int k0 = (MODE == kInputGrad && kb >= p.kb0 ? kb - p.kb0 : kb) * kBK;
         // the leader's barrier counts both CTAs' bytes
-        if (rank == 0) mbar_arrive_expect_tx(&full_bar[s], PAIR ? 2 * C::kStage : C::kStage);
-        const uint32_t fb = PAIR ? in_cta(&full_bar[s], 0) : smem_u32(&full_bar[s]);
-        auto load = [&](uint8_t *dst, const CUtensorMap *map, int c_inner, int c_outer) {
-          if constexpr (PAIR) tma_load_2d_pair(dst, map, fb, c_inner, c_outer);
-          else tma_load_2d(dst, map, &full_bar[s], c_inner, c_outer);
-        };
-        uint8_t *a = ring + (size_t)s * C::kStage, *b = a + kABytes;
+        if (rank == 0) mbar_expect_one(full0 + 8 * s, PAIR ? 2 * C::kStage : C::kStage);
+        const uint32_t a = ring0 + s * C::kStage, b = a + kABytes, fb = full0 + 8 * s;
         if constexpr (C::kAMn) {
-          load(a, &maps.a[src], m0, k0);
-          load(a + kBK * 128, &maps.a[src], m0 + 64, k0);
+          tma_load_2d_one<PAIR>(a, &maps.a[src], fb, m0, k0);
+          tma_load_2d_one<PAIR>(a + kBK * 128, &maps.a[src], fb, m0 + 64, k0);
         } else {
-          load(a, &maps.a[src], k0, m0);
+          tma_load_2d_one<PAIR>(a, &maps.a[src], fb, k0, m0);
         }
         if constexpr (C::kBMn) {
 #pragma unroll
-          for (int i = 0; i < C::kBRows / 64; ++i) load(b + i * kBK * 128, &maps.b[src], n0 + 64 * i, k0);
+          for (int i = 0; i < C::kBRows / 64; ++i)
+            tma_load_2d_one<PAIR>(b + i * kBK * 128, &maps.b[src], fb, n0 + 64 * i, k0);
         } else if constexpr (MODE == kGateUp) {
           if constexpr (PAIR) {  // the leader holds the gate's rows, its peer the up projection's
-            load(b, &maps.b[rank], k0, n0);
+            tma_load_2d_one<PAIR>(b, &maps.b[rank], fb, k0, n0);
           } else {
-            load(b, &maps.b[0], k0, n0);
-            load(b + (BN / 2) * 128, &maps.b[1], k0, n0);
+            tma_load_2d_one<PAIR>(b, &maps.b[0], fb, k0, n0);
+            tma_load_2d_one<PAIR>(b + (BN / 2) * 128, &maps.b[1], fb, k0, n0);
           }
         } else {
-          load(b, &maps.b[0], k0, n0);
+          tma_load_2d_one<PAIR>(b, &maps.b[0], fb, k0, n0);
         }
       }
     }
-    issued = j;
-  } else if (warp == 1 && lane == 0 && rank == 0) {
+    if (lane == 0) issued = j;
+  } else if (warp == 1) {
     // ---------------- MMA issuer ----------------
-    if (p.inject && blockIdx.x == 0)  // test hook: a wait that runs out
-      (void)mbar_wait_bounded(&never_bar, 0u, abort_p, p.status, p.wait_ns);
-    const uint32_t idesc = idesc_16(p.f16, C::kAMn, C::kBMn, kRows, BN);
-    int j = 0, it = 0;
-    bool ok = true;
-    for (int t = first_tile; ok && t < p.tiles; t += tile_step, ++it) {
-      const int acc = it & 1;
-      if (!mbar_wait_bounded(&tempty_bar[acc], ((uint32_t)(it >> 1) & 1u) ^ 1u, abort_p, p.status, p.wait_ns)) break;
-      tc_fence_after();
-      const uint32_t d = tmem + (uint32_t)(acc * BN);
-      for (int kb = 0; kb < p.kb; ++kb, ++j) {
-        const int s = j % C::kStages;
-        if (!mbar_wait_bounded(&full_bar[s], (uint32_t)((j / C::kStages) & 1), abort_p, p.status, p.wait_ns)) {
-          ok = false;
-          break;
-        }
+    if (rank == 0) {
+      if (p.inject && blockIdx.x == 0)  // test hook: a wait that runs out
+        (void)warp_wait(&never_bar, 0u, abort_p, p.status, p.wait_ns);
+      const uint32_t idesc = idesc_16(p.f16, C::kAMn, C::kBMn, kRows, BN);
+      // 16 k are 32 bytes of a K-major row, or 16 rows of 128 bytes of an MN-major box
+      const uint64_t ring_d = (uint64_t)(smem_u32(ring) >> 4);
+      const uint64_t a0 = (C::kAMn ? smem_desc_mn(0) : smem_desc_sw128(0)) + ring_d;
+      const uint64_t b0 = (C::kBMn ? smem_desc_mn(0) : smem_desc_sw128(0)) + ring_d + (kABytes >> 4);
+      constexpr int kAStep = (C::kAMn ? 2048 : 32) >> 4, kBStep = (C::kBMn ? 2048 : 32) >> 4;
+      RingPos<C::kStages> pos;
+      RingPos<2> acc;
+      bool ok = true;
+      for (int t = first_tile; ok && t < p.tiles; t += tile_step, acc.next()) {
+        if (!warp_wait(&tempty_bar[acc.slot], acc.round ^ 1u, abort_p, p.status, p.wait_ns)) break;
         tc_fence_after();
-        const uint32_t a = smem_u32(ring + (size_t)s * C::kStage), b = a + kABytes;
+        const uint32_t d = tmem + (uint32_t)(acc.slot * BN);
+        for (int kb = 0; kb < p.kb; ++kb, pos.next()) {
+          if (!warp_wait(&full_bar[pos.slot], pos.round, abort_p, p.status, p.wait_ns)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t at = pos.slot * (C::kStage >> 4);
 #pragma unroll
-        for (int k = 0; k < kBK / 16; ++k) {
-          // 16 k are 32 bytes of a K-major row, or 16 rows of 128 bytes of an MN-major box
-          const uint64_t da = C::kAMn ? smem_desc_mn(a + k * 2048) : smem_desc_sw128(a + k * 32);
-          const uint64_t db = C::kBMn ? smem_desc_mn(b + k * 2048) : smem_desc_sw128(b + k * 32);
-          if constexpr (PAIR) tc_mma_f16_pair(d, da, db, idesc, (kb | k) ? 1u : 0u);
-          else tc_mma_f16(d, da, db, idesc, (kb | k) ? 1u : 0u);
+          for (int k = 0; k < kBK / 16; ++k)
+            tc_mma_one<PAIR, false>(d, a0 + (at + k * kAStep), b0 + (at + k * kBStep), idesc, (kb | k) ? 1u : 0u);
+          tc_commit_one<PAIR>(smem_u32(&empty_bar[pos.slot]));
         }
-        if constexpr (PAIR) tc_commit_pair(&empty_bar[s]);
-        else tc_commit(&empty_bar[s]);
+        if (ok) tc_commit_one<PAIR>(smem_u32(&tfull_bar[acc.slot]));
       }
-      if (ok) {
-        if constexpr (PAIR) tc_commit_pair(&tfull_bar[acc]);
-        else tc_commit(&tfull_bar[acc]);
-      }
+      // every MMA this warp issued completes before TMEM is freed
+      tc_commit_local_one<PAIR>(smem_u32(&mma_done_bar));
+      int no_abort = 0;
+      (void)wait_bounded(&mma_done_bar, 0u, &no_abort, p.status, p.wait_ns);
     }
-    // every MMA this thread issued completes before TMEM is freed
-    if constexpr (PAIR) tc_commit_pair_local(&mma_done_bar);
-    else tc_commit(&mma_done_bar);
-    int no_abort = 0;
-    (void)mbar_wait_bounded(&mma_done_bar, 0u, &no_abort, p.status, p.wait_ns);
   } else if (warp >= 2) {
     // ---------------- epilogue ----------------
     const int q = warp & 3, half = (warp - 2) >> 2;
@@ -293,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int acc = it & 1;
       int ready = 0;
       if (lane == 0)
-        ready = mbar_wait_bounded(&tfull_bar[acc], (uint32_t)(it >> 1) & 1u, abort_p, p.status, p.wait_ns) ? 1 : 0;
+        ready = wait_bounded(&tfull_bar[acc], (uint32_t)(it >> 1) & 1u, abort_p, p.status, p.wait_ns) ? 1 : 0;
       if (!__shfl_sync(0xffffffffu, ready, 0)) break;
       tc_fence_after();
       const Tile tl = tile_of(p, t, kRows, kCols);
@@ -325,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < C::kStages; ++s) {
       const int n = j / C::kStages + (s < j % C::kStages ? 1 : 0);
-      if (n > 0) (void)mbar_wait_bounded(&full_bar[s], (uint32_t)((n - 1) & 1), &no_abort, p.status, p.wait_ns);
+      if (n > 0) (void)wait_bounded(&full_bar[s], (uint32_t)((n - 1) & 1), &no_abort, p.status, p.wait_ns);
     }
   }
   __syncthreads();
@@ -413,6 +408,10 @@ cudaError_t launch_dense_gemm(int mode, GemmTile g, const GemmMaps &maps, GemmPa
   if (mode == MODE && g.bn == BN && g.pair == PAIR) return launch<MODE, BN, PAIR>(maps, p, num_sms, st)
 #define MOE_LAUNCH_ALL(MODE)     \
   MOE_LAUNCH(MODE, 256, true);   \
+  MOE_LAUNCH(MODE, 224, true);   \
+  MOE_LAUNCH(MODE, 192, true);   \
+  MOE_LAUNCH(MODE, 160, true);   \
+  MOE_LAUNCH(MODE, 128, true);   \
   MOE_LAUNCH(MODE, 256, false);  \
   MOE_LAUNCH(MODE, 128, false);  \
   MOE_LAUNCH(MODE, 64, false)

@@ -10,6 +10,18 @@ constexpr int kBM = 128;                             // rows of a tile: the MMA'
 constexpr int kEpiWarps = 8, kThreads = 32 * (2 + kEpiWarps);
 constexpr int kRingBytes = 227 * 1024 - 3072;        // what barriers and alignment leave of a CTA's shared memory
 
+// mbar_wait_bounded, which reads the timer only once a barrier has stayed open for some tries: a try
+// waits a while by itself, and the timer's latency would be added to every wait of a pipeline.
+__device__ __forceinline__ bool wait_bounded(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *dev_status,
+                                             uint64_t limit_ns) {
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+  }
+  return mbar_wait_bounded(bar, parity, abort_flag, dev_status, limit_ns);
+}
+
 // Allows a kernel its dynamic shared memory, once on each device (`done`: one bit a device).
 inline cudaError_t allow_smem(const void *kernel, size_t bytes, std::atomic<unsigned long long> &done) {
   int dev = 0;
@@ -55,36 +67,99 @@ __device__ __forceinline__ int ld_cluster_s32(uint32_t addr) {
   asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
-// a box into this CTA's shared memory, its bytes counted on the barrier at `bar`, of this CTA or its peer
-__device__ __forceinline__ void tma_load_2d_pair(void *smem_dst, const void *tmap, uint32_t bar, int c_inner, int c_outer) {
+// ---- asynchronous operations issued by one lane of a converged warp ----
+// The election is inside the instruction sequence, so the code around it is uniform over the warp and
+// its descriptors and addresses stay in uniform registers: a tcgen05.mma issued from a branch that one
+// lane takes cost 107 to 143 cycles of issue, N = 256 tiles 171 instead of 128; issued like this 57,
+// and 128.  The elected lane is the same every time.
+
+// a box into this CTA's shared memory, its bytes counted on the barrier at `bar` (PAIR: of this CTA or
+// its peer, a shared::cluster address)
+template <bool PAIR>
+__device__ __forceinline__ void tma_load_2d_one(uint32_t dst, const void *tmap, uint32_t bar, int c_inner, int c_outer) {
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, "
+        "{%3, %4}], [%2];\n\t}" ::"r"(dst),
+        "l"(tmap), "r"(bar), "r"(c_inner), "r"(c_outer)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], "
+        "[%2];\n\t}" ::"r"(dst),
+        "l"(tmap), "r"(bar), "r"(c_inner), "r"(c_outer)
+        : "memory");
+}
+__device__ __forceinline__ void mbar_expect_one(uint32_t bar, uint32_t bytes) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%3, "
-      "%4}], [%2];" ::"r"(smem_u32(smem_dst)),
-      "l"(tmap), "r"(bar), "r"(c_inner), "r"(c_outer)
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
+      "r"(bytes)
       : "memory");
 }
-__device__ __forceinline__ void tc_mma_f16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                                uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
+#define MOE_MMA_ONE(GROUP, KIND)                                                    \
+  asm volatile(                                                                     \
+      "{\n\t.reg .pred p, q;\n\telect.sync _|q, 0xffffffff;\n\t"                    \
+      "setp.ne.b32 p, %4, 0;\n\t"                                                   \
+      "@q tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem), \
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)                         \
+      : "memory")
+template <bool PAIR, bool FP8>
+__device__ __forceinline__ void tc_mma_one(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  if constexpr (PAIR && FP8) MOE_MMA_ONE("2", "f8f6f4");
+  else if constexpr (PAIR) MOE_MMA_ONE("2", "f16");
+  else if constexpr (FP8) MOE_MMA_ONE("1", "f8f6f4");
+  else MOE_MMA_ONE("1", "f16");
 }
-// arrives on the barrier at the same place in both CTAs once all MMAs issued before have completed
-__device__ __forceinline__ void tc_commit_pair(uint64_t *bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-          smem_u32(bar)),
-      "h"((uint16_t)3)
-      : "memory");
+#undef MOE_MMA_ONE
+// arrives on the barrier (PAIR: at the same place in both CTAs) once all MMAs issued before have completed
+template <bool PAIR>
+__device__ __forceinline__ void tc_commit_one(uint32_t bar) {
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
+            bar),
+        "h"((uint16_t)3)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+        : "memory");
 }
 // the same for a barrier of this CTA only
-__device__ __forceinline__ void tc_commit_pair_local(uint64_t *bar) {
-  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-               : "memory");
+template <bool PAIR>
+__device__ __forceinline__ void tc_commit_local_one(uint32_t bar) {
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+        : "memory");
+  else
+    tc_commit_one<false>(bar);
 }
+// wait_bounded by a whole warp, with one verdict
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *dev_status,
+                                          uint64_t limit_ns) {
+  return __all_sync(0xffffffffu, wait_bounded(bar, parity, abort_flag, dev_status, limit_ns)) != 0;
+}
+// a ring position: slot and the parity of its round
+template <int SLOTS>
+struct RingPos {
+  int slot = 0;
+  uint32_t round = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == SLOTS) {
+      slot = 0;
+      round ^= 1u;
+    }
+  }
+};
+
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t *smem_dst, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(smem_dst)), "r"(ncols)
                : "memory");
