@@ -290,6 +290,7 @@ moe::GemmParams gemm_params(const moe_ffn_gated_args *a, const DeviceSide &d, in
   p.kb0 = p.kb = kb;
   p.act = a->activation;
   p.f16 = a->type == MOE_FFN_F16;
+  p.a_rows = moe::a_box(m);
   p.status = d.status;
   p.wait_ns = d.wait_ns;
   p.inject = d.inject;
@@ -369,8 +370,8 @@ extern "C" int moe_ffn_gated_forward(const moe_ffn_gated_args *a, void *stream) 
   const moe::GemmTile tu = moe::gemm_pick_tile(moe::kGateUp, up, sms), td = moe::gemm_pick_tile(moe::kDown, down, sms);
   const int bu = tu.b_box(moe::kGateUp), bd = td.b_box(moe::kDown);
   moe::GemmMaps mu, md;
-  if (!encode_map(&mu.a[0], a->x, 2, H, R, a->ld_x, 128) || !encode_map(&mu.b[0], a->w_gate, 2, H, I, H, bu) ||
-      !encode_map(&mu.b[1], a->w_up, 2, H, I, H, bu) || !encode_map(&md.a[0], a->workspace, 2, I, R, I, 128) ||
+  if (!encode_map(&mu.a[0], a->x, 2, H, R, a->ld_x, up.a_rows) || !encode_map(&mu.b[0], a->w_gate, 2, H, I, H, bu) ||
+      !encode_map(&mu.b[1], a->w_up, 2, H, I, H, bu) || !encode_map(&md.a[0], a->workspace, 2, I, R, I, down.a_rows) ||
       !encode_map(&md.b[0], a->w_down, 2, I, H, I, bd))
     return fail(MOE_FFN_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", who);
   cudaError_t e = moe::launch_dense_gemm(moe::kGateUp, tu, mu, up, sms, st);
@@ -421,7 +422,7 @@ extern "C" int moe_ffn_gated_backward(const moe_ffn_gated_args *a, void *stream)
   hid.c[2] = h;
   hid.e[0] = a->gate;
   hid.e[1] = a->up;
-  if (!encode_map(&m.a[0], a->d_y, 2, H, R, a->ld_d_y, 128) || !encode_map(&m.b[0], a->w_down, 2, I, H, I, 64))
+  if (!encode_map(&m.a[0], a->d_y, 2, H, R, a->ld_d_y, hid.a_rows) || !encode_map(&m.b[0], a->w_down, 2, I, H, I, 64))
     return fail(MOE_FFN_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", who);
   cudaError_t e = moe::launch_dense_gemm(moe::kHiddenGrad, moe::gemm_pick_tile(moe::kHiddenGrad, hid, sms), m, hid, sms, st);
   if (e == cudaSuccess && a->d_x) {
@@ -429,7 +430,7 @@ extern "C" int moe_ffn_gated_backward(const moe_ffn_gated_args *a, void *stream)
     p.kb0 = kblocks(a->inter);
     p.c[0] = a->d_x;
     p.ldc[0] = a->ld_d_x;
-    if (!encode_map(&m.a[0], dg, 2, I, R, I, 128) || !encode_map(&m.a[1], du, 2, I, R, I, 128) ||
+    if (!encode_map(&m.a[0], dg, 2, I, R, I, p.a_rows) || !encode_map(&m.a[1], du, 2, I, R, I, p.a_rows) ||
         !encode_map(&m.b[0], a->w_gate, 2, H, I, H, 64) || !encode_map(&m.b[1], a->w_up, 2, H, I, H, 64))
       return fail(MOE_FFN_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", who);
     e = moe::launch_dense_gemm(moe::kInputGrad, moe::gemm_pick_tile(moe::kInputGrad, p, sms), m, p, sms, st);
@@ -437,6 +438,7 @@ extern "C" int moe_ffn_gated_backward(const moe_ffn_gated_args *a, void *stream)
   if (e == cudaSuccess && weights) {
     moe::GemmParams p = gemm_params(a, dev, a->inter, a->hidden, kblocks(a->rows));
     p.same = 2;
+    p.a_rows = 128;
     p.m_last = a->hidden;
     p.n_last = a->inter;
     p.c[0] = a->d_w_gate;

@@ -58,10 +58,16 @@ struct GemmParams {
   long long ldc[3];
   const void *e[2];    // kHiddenGrad: the saved g and u
   int act, f16;
+  int a_rows;          // rows of a K-major A's boxes (128 for an MN-major one); see a_box
   int *status;
   uint64_t wait_ns;
   int inject;
 };
+
+// Rows of a K-major A's boxes.  A single block of fewer rows takes boxes of its own height: rows past the
+// end would be filled with zeros, which costs the copy engine as much time as loading them.  The MMA
+// then reads what lies in shared memory there, into accumulator rows that nothing reads.
+inline int a_box(int m) { return m >= 128 ? 128 : (m + 7) / 8 * 8; }
 
 // a tile: bn columns (kGateUp: half of them of g, half of u) of 128 rows, or of 256 by a pair of CTAs
 struct GemmTile {

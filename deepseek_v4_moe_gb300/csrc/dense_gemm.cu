@@ -37,6 +37,7 @@ namespace {
 
 constexpr int kBK = 64;
 constexpr int kABytes = kBM * kBK * 2;
+constexpr int kStageBuf = 32 * 64;  // see piece_at
 
 template <int MODE, int BN, bool PAIR>
 struct Cfg {
@@ -45,8 +46,9 @@ struct Cfg {
   // rows of B in this CTA; an MN-major operand comes in whole boxes of 64, of which the last may be used in part
   static constexpr int kBUsed = PAIR ? BN / 2 : BN, kBRows = kBMn ? (kBUsed + 63) / 64 * 64 : kBUsed;
   static constexpr int kStage = kABytes + kBRows * kBK * 2;
-  static constexpr int kStages = kRingBytes / kStage;
-  static constexpr size_t kSmem = (size_t)kStages * kStage + 1024;
+  static constexpr int kBufBytes = kEpiWarps * kStageBuf;
+  static constexpr int kStages = (kRingBytes - kBufBytes) / kStage;
+  static constexpr size_t kSmem = (size_t)kStages * kStage + kBufBytes + 1024;
   static constexpr int kTmemCols = 2 * BN < 32 ? 32 : 2 * BN > 256 ? 512 : 2 * BN;  // a power of two
   static_assert(BN % 32 == 0 && kBRows % 8 == 0, "whole epilogue chunks and swizzle groups");
 };
@@ -88,71 +90,169 @@ __device__ __forceinline__ Tile tile_of(const GemmParams &p, int t, int rows, in
   return r;
 }
 
-// Sixteen consecutive values of a row of T, of which those from column `left` on do not exist (left a
-// multiple of 8; the row 16-byte aligned at these columns).
-template <typename T>
-__device__ __forceinline__ void store16(T *dst, int left, const float (&v)[16]) {
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-    if (8 * h < left)
-      *reinterpret_cast<uint4 *>(dst + 8 * h) =
-          make_uint4(pack2<T>(v[8 * h], v[8 * h + 1]), pack2<T>(v[8 * h + 2], v[8 * h + 3]),
-                     pack2<T>(v[8 * h + 4], v[8 * h + 5]), pack2<T>(v[8 * h + 6], v[8 * h + 7]));
+// A warp's staging buffer: 32 rows x 32 values of a 16-bit type, 64 bytes a row in four pieces, piece c of
+// row r at place c ^ (r / 2 % 4), so that both a warp writing one piece of every row and a warp writing
+// whole rows side by side meet every bank once.
+__device__ __forceinline__ uint32_t piece_at(int r, int c) { return r * 64 + ((c ^ (r >> 1)) & 3) * 16; }
+__device__ __forceinline__ void sts128(uint32_t a, const uint4 w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
 }
-template <typename T>
-__device__ __forceinline__ void load16(const T *src, int left, float (&v)[16]) {
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint4 w = make_uint4(0u, 0u, 0u, 0u);
-    if (8 * h < left) w = *reinterpret_cast<const uint4 *>(src + 8 * h);
-    unpack2(w.x, v[8 * h], v[8 * h + 1], src);
-    unpack2(w.y, v[8 * h + 2], v[8 * h + 3], src);
-    unpack2(w.z, v[8 * h + 4], v[8 * h + 5], src);
-    unpack2(w.w, v[8 * h + 6], v[8 * h + 7], src);
-  }
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 w;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(a) : "memory");
+  return w;
 }
 
-// one thread's row of a finished tile: columns [16 * half, BN) in steps of 32
+// A warp's 32 rows of a tile: its columns [32 * half, kCols) in steps of 64, 32 at a time.  A thread of
+// the TMEM loads has a row; rows lie far apart in memory, so what is stored (and kHiddenGrad's g and u)
+// passes through shared memory, and four neighbouring threads move the 64 bytes of a row: a store that
+// took 32 lines takes 8.  begin() runs while the tile's products are still made: it fetches g and u of
+// the first step; each step then fetches the next one's.  The loop is kept rolled: unrolled, its code no
+// longer fits the instruction caches and a tile of 256 columns took 15 us more.
 template <int MODE, int BN, typename T>
-__device__ __forceinline__ void epilogue(const GemmParams &p, const Tile &tl, uint32_t tbase, int half, int row) {
-  const bool last = tl.prob == p.same;
-  const int m = last ? p.m_last : p.m, n = last ? p.n_last : p.n;
-  const bool in = row < m;
-  constexpr int kCols = MODE == kGateUp ? BN / 2 : BN;
-  for (int c0 = half * 16; c0 < kCols; c0 += 32) {
-    __syncwarp();  // the TMEM loads take the whole warp
-    float v[16], w[16];
-    tmem_ld16(tbase + c0, v);
-    if constexpr (MODE == kGateUp) tmem_ld16(tbase + BN / 2 + c0, w);
-    const int col = tl.n0 + c0, left = n - col;
-    if (!in || left <= 0) continue;
-    if constexpr (MODE == kGateUp) {
-      const size_t at = (size_t)row * n + col;
-      if (p.c[1]) {
-        store16(static_cast<T *>(p.c[1]) + at, left, v);
-        store16(static_cast<T *>(p.c[2]) + at, left, w);
+struct Epilogue {
+  static constexpr int kCols = MODE == kGateUp ? BN / 2 : BN;
+  uint4 g[4], u[4];  // kHiddenGrad: the next step's, as they are fetched
+  int row0, m, n, half;
+  uint32_t buf;      // the warp's staging buffer
+  Tile tl;
+  // thread l moves piece l % 4 of rows l / 4 + 8 i
+  __device__ __forceinline__ bool mine(int i, int c0, size_t ld, size_t &at) const {
+    const int lane = threadIdx.x & 31, row = row0 + 8 * i + (lane >> 2), c = c0 + 8 * (lane & 3);
+    at = (size_t)row * ld + tl.n0 + c;
+    return row < m && c < kCols && tl.n0 + c < n;
+  }
+  __device__ __forceinline__ void fetch(const GemmParams &p, int c0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      size_t at;
+      g[i] = u[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (mine(i, c0, n, at)) {
+        g[i] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(p.e[0]) + at);
+        u[i] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(p.e[1]) + at);
+      }
+    }
+  }
+  __device__ __forceinline__ void begin(const GemmParams &p, const Tile &tile, int half_, int row0_, uint32_t buf_) {
+    tl = tile;
+    row0 = row0_;
+    half = half_;
+    buf = buf_;
+    const bool last = tl.prob == p.same;
+    m = last ? p.m_last : p.m;
+    n = last ? p.n_last : p.n;
+    if constexpr (MODE == kHiddenGrad) fetch(p, half * 32);
+  }
+  // sixteen values as eight words of pairs
+  static __device__ __forceinline__ void pack16(const float (&v)[16], uint32_t *w) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = pack2<T>(v[2 * i], v[2 * i + 1]);
+  }
+  static __device__ __forceinline__ void unpack16(const uint32_t *w, float (&v)[16]) {
+    const T *tag = nullptr;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) unpack2(w[i], v[2 * i], v[2 * i + 1], tag);
+  }
+  // what fetch() brought, handed to the threads that have the rows
+  __device__ __forceinline__ void hand_over(const uint4 (&f)[4], uint32_t (&w)[16]) const {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sts128(buf + piece_at(8 * i + (lane >> 2), lane & 3), f[i]);
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const uint4 q = lds128(buf + piece_at(lane, c));
+      w[4 * c] = q.x, w[4 * c + 1] = q.y, w[4 * c + 2] = q.z, w[4 * c + 3] = q.w;
+    }
+    __syncwarp();
+  }
+  // each thread's 32 values of its row to `out`
+  __device__ __forceinline__ void emit(const uint32_t (&w)[16], void *out, size_t ld, int c0) const {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) sts128(buf + piece_at(lane, c), make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]));
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      size_t at;
+      if (mine(i, c0, ld, at))
+        *reinterpret_cast<uint4 *>(static_cast<T *>(out) + at) = lds128(buf + piece_at(8 * i + (lane >> 2), lane & 3));
+    }
+    __syncwarp();
+  }
+  __device__ __forceinline__ void finish(const GemmParams &p, uint32_t tbase) {
+#pragma unroll 1
+    for (int c0 = half * 32; c0 < kCols; c0 += 64) {
+      uint32_t x[16], y[16], z[16];
+      if constexpr (MODE == kHiddenGrad) {
+        hand_over(g, x);
+        hand_over(u, y);
+        fetch(p, c0 + 64);
       }
 #pragma unroll
-      for (int j = 0; j < 16; ++j) v[j] = act_value(p.act, v[j]) * w[j];
-      store16(static_cast<T *>(p.c[0]) + at, left, v);
-    } else if constexpr (MODE == kHiddenGrad) {
-      const size_t at = (size_t)row * n + col;
-      float g[16], u[16];
-      load16(static_cast<const T *>(p.e[0]) + at, left, g);
-      load16(static_cast<const T *>(p.e[1]) + at, left, u);
+      for (int s = 0; s < 2; ++s) {
+        if (c0 + 16 * s >= kCols) break;  // TMEM ends here (the words left over are not stored)
+        float v[16], w[16];
+        tmem_ld16(tbase + c0 + 16 * s, v);
+        if constexpr (MODE == kGateUp) {
+          tmem_ld16(tbase + BN / 2 + c0 + 16 * s, w);
+          pack16(v, y + 8 * s);
+          pack16(w, z + 8 * s);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        float a, da;
-        act_both(p.act, g[j], a, da);
-        g[j] = v[j] * u[j] * da;  // dg
-        w[j] = a * u[j];          // h
-        v[j] *= a;                // du
+          for (int j = 0; j < 16; ++j) v[j] = act_value(p.act, v[j]) * w[j];
+          pack16(v, x + 8 * s);
+        } else if constexpr (MODE == kHiddenGrad) {
+          float a[16], b[16];
+          unpack16(x + 8 * s, a);
+          unpack16(y + 8 * s, b);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            float act, slope;
+            act_both(p.act, a[j], act, slope);
+            a[j] = v[j] * b[j] * slope;  // dg
+            w[j] = act * b[j];           // h
+            v[j] *= act;                 // du
+          }
+          pack16(a, x + 8 * s);
+          pack16(v, y + 8 * s);
+          pack16(w, z + 8 * s);
+        } else {
+          pack16(v, x + 8 * s);
+        }
       }
-      store16(static_cast<T *>(p.c[0]) + at, left, g);
-      store16(static_cast<T *>(p.c[1]) + at, left, v);
-      store16(static_cast<T *>(p.c[2]) + at, left, w);
-    } else {
-      store16(static_cast<T *>(p.c[tl.prob]) + (size_t)row * p.ldc[tl.prob] + col, left, v);
+      if constexpr (MODE == kGateUp || MODE == kHiddenGrad) {
+        emit(x, p.c[0], n, c0);
+        if (p.c[1]) {
+          emit(y, p.c[1], n, c0);
+          emit(z, p.c[2], n, c0);
+        }
+      } else {
+        emit(x, p.c[tl.prob], p.ldc[tl.prob], c0);
+      }
+    }
+  }
+};
+
+// the epilogue warps' loop over the tiles, for one type
+template <int MODE, int BN, bool PAIR, typename T>
+__device__ __forceinline__ void epilogue_loop(const GemmParams &p, uint32_t tmem, uint32_t rank, int warp, int lane,
+                                              int first_tile, int tile_step, uint64_t *tfull_bar, uint64_t *tempty_bar,
+                                              uint32_t buf, volatile int *abort_p) {
+  constexpr int kCols = MODE == kGateUp ? BN / 2 : BN, kRows = PAIR ? 2 * kBM : kBM;
+  const int q = warp & 3, half = (warp - 2) >> 2;
+  RingPos<2> acc;
+  Epilogue<MODE, BN, T> e;
+  for (int t = first_tile; t < p.tiles; t += tile_step, acc.next()) {
+    const Tile tl = tile_of(p, t, kRows, kCols);
+    e.begin(p, tl, half, tl.m0 + (int)rank * kBM + q * 32, buf);
+    if (!warp_wait(&tfull_bar[acc.slot], acc.round, abort_p, p.status, p.wait_ns)) break;
+    tc_fence_after();
+    e.finish(p, tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc.slot * BN));
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) {
+      if constexpr (PAIR) mbar_arrive_cluster(in_cta(&tempty_bar[acc.slot], 0));
+      else mbar_arrive(&tempty_bar[acc.slot]);
     }
   }
 }
@@ -204,6 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     RingPos<C::kStages> pos;
     int j = 0;
     bool ok = true;
+    const uint32_t stage_bytes = C::kStage - (kBM - p.a_rows) * kBK * 2;
     const uint32_t ring0 = smem_u32(ring), full0 = PAIR ? in_cta(full_bar, 0) : smem_u32(full_bar);
     for (int t = first_tile; ok && t < p.tiles; t += tile_step) {
       const Tile tl = tile_of(p, t, kRows, kCols);
@@ -218,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int src = MODE == kWeightGrad ? tl.prob : (MODE == kInputGrad && kb >= p.kb0 ? 1 : 0);
         const int k0 = (MODE == kInputGrad && kb >= p.kb0 ? kb - p.kb0 : kb) * kBK;
         // the leader's barrier counts both CTAs' bytes
-        if (rank == 0) mbar_expect_one(full0 + 8 * s, PAIR ? 2 * C::kStage : C::kStage);
+        if (rank == 0) mbar_expect_one(full0 + 8 * s, PAIR ? 2 * stage_bytes : stage_bytes);
         const uint32_t a = ring0 + s * C::kStage, b = a + kABytes, fb = full0 + 8 * s;
         if constexpr (C::kAMn) {
           tma_load_2d_one<PAIR>(a, &maps.a[src], fb, m0, k0);
@@ -282,29 +383,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= 2) {
     // ---------------- epilogue ----------------
-    const int q = warp & 3, half = (warp - 2) >> 2;
-    int it = 0;
-    for (int t = first_tile; t < p.tiles; t += tile_step, ++it) {
-      const int acc = it & 1;
-      int ready = 0;
-      if (lane == 0)
-        ready = wait_bounded(&tfull_bar[acc], (uint32_t)(it >> 1) & 1u, abort_p, p.status, p.wait_ns) ? 1 : 0;
-      if (!__shfl_sync(0xffffffffu, ready, 0)) break;
-      tc_fence_after();
-      const Tile tl = tile_of(p, t, kRows, kCols);
-      const int row = tl.m0 + (int)rank * kBM + q * 32 + lane;
-      const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BN);
-      if (p.f16)
-        epilogue<MODE, BN, __half>(p, tl, tbase, half, row);
-      else
-        epilogue<MODE, BN, __nv_bfloat16>(p, tl, tbase, half, row);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if constexpr (PAIR) mbar_arrive_cluster(in_cta(&tempty_bar[acc], 0));
-        else mbar_arrive(&tempty_bar[acc]);
-      }
-    }
+    const uint32_t buf = smem_u32(ring) + C::kStages * C::kStage + (warp - 2) * kStageBuf;
+    if (p.f16)
+      epilogue_loop<MODE, BN, PAIR, __half>(p, tmem, rank, warp, lane, first_tile, tile_step, tfull_bar, tempty_bar, buf,
+                                            abort_p);
+    else
+      epilogue_loop<MODE, BN, PAIR, __nv_bfloat16>(p, tmem, rank, warp, lane, first_tile, tile_step, tfull_bar, tempty_bar,
+                                                   buf, abort_p);
   }
   // Copies still in flight after an abort land before a CTA may leave: the barriers that count them are
   // waited for (bounded; in a normal run each completed long ago).  A peer may have issued stages whose
@@ -316,7 +401,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int j = issued, no_abort = 0;
     if constexpr (PAIR) {
       const int theirs = ld_cluster_s32(in_cta(&issued, 1));
-      for (; j < theirs; ++j) mbar_arrive_expect_tx(&full_bar[j % C::kStages], C::kStage);
+      for (; j < theirs; ++j)
+        mbar_arrive_expect_tx(&full_bar[j % C::kStages], C::kStage - (kBM - p.a_rows) * kBK * 2);
     }
     for (int s = 0; s < C::kStages; ++s) {
       const int n = j / C::kStages + (s < j % C::kStages ? 1 : 0);
@@ -378,20 +464,33 @@ int GemmTile::b_box(int mode) const {
   return mode == kGateUp || pair ? bn / 2 : bn;
 }
 
-// The tile whose waves over the SMs cost least.  A wave's cost in a tile's time, in units of one
-// column of a 128-row tile at the tensor cores' rate: a pair's tile has its operands shared, a single
-// CTA's waits for shared memory below 256 columns, and every k block has a part that does not shrink.
+// The tile that takes the least time by what tiles measured (us, 2048 to 4096 k, bf16): a k block of 64
+// with 256, 128, 64 and 32 columns 0.339, 0.200, 0.157 and 0.147 on a CTA by itself (few columns: the
+// time to issue four MMAs), 0.045 + 0.00092 for each column on a pair; an epilogue 0.010 for each column
+// of a plain result, 0.022 of kGateUp and 0.032 of kHiddenGrad, hidden under the next tile's products
+// but for the last; a launch with its prologue 3.8, of pairs 5.8.  Tiles go in waves over the SMs, so
+// the widest tile is not always the fastest: 4096 x 4096 columns by 4096 took 83.1 us in 256 tiles of
+// 256 columns (3.4 waves of 76 pairs), 75.6 in 304 of 224 (4.0), and 1024 rows 29.4 in one wave of
+// pairs, 34.8 in two of 128 columns.
 GemmTile gemm_pick_tile(int mode, const GemmParams &p, int num_sms) {
   const bool b_mn = mode == kHiddenGrad || mode == kInputGrad || mode == kWeightGrad;
-  GemmTile best = {256, true};
-  const long long pairs = num_sms / 2;
-  double least = (double)((tiles_of(mode, p, best) + pairs - 1) / pairs) * 256;
-  for (int bn = 256; bn >= (b_mn ? 64 : 32); bn /= 2) {
-    const GemmTile g = {bn, false};
-    const double cost = (double)((tiles_of(mode, p, g) + num_sms - 1) / num_sms) * (1.1 * bn + 40);
-    if (cost < least) {
-      best = g;
-      least = cost;
+  const double per_col = mode == kGateUp ? 0.022 : mode == kHiddenGrad ? 0.032 : 0.010;
+  const struct {
+    GemmTile tile;
+    double k_block;
+  } all[] = {{{256, true}, 0.280}, {{224, true}, 0.251}, {{192, true}, 0.222}, {{128, true}, 0.163},
+             {{256, false}, 0.339}, {{128, false}, 0.200}, {{64, false}, 0.157}, {{32, false}, 0.147}};
+  GemmTile best = {0, false};
+  double least = 0;
+  for (const auto &c : all) {
+    if (b_mn && c.tile.bn < 64) continue;
+    const long long units = c.tile.pair ? num_sms / 2 : num_sms;
+    const long long waves = (tiles_of(mode, p, c.tile) + units - 1) / units;
+    const double epilogue = per_col * c.tile.bn, products = c.k_block * p.kb;
+    const double time = (c.tile.pair ? 5.8 : 3.8) + waves * (products > epilogue ? products : epilogue) + epilogue;
+    if (best.bn == 0 || time < least) {
+      best = c.tile;
+      least = time;
     }
   }
   return best;
@@ -410,7 +509,6 @@ cudaError_t launch_dense_gemm(int mode, GemmTile g, const GemmMaps &maps, GemmPa
   MOE_LAUNCH(MODE, 256, true);   \
   MOE_LAUNCH(MODE, 224, true);   \
   MOE_LAUNCH(MODE, 192, true);   \
-  MOE_LAUNCH(MODE, 160, true);   \
   MOE_LAUNCH(MODE, 128, true);   \
   MOE_LAUNCH(MODE, 256, false);  \
   MOE_LAUNCH(MODE, 128, false);  \

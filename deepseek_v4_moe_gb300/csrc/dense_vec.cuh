@@ -121,21 +121,21 @@ __device__ __forceinline__ void load_eight(const T *row, int t, int n, int hidde
   e.get(o);
 }
 
-// act(g) and, for the backward pass, its derivative
+// 1 / (1 + exp(-x)) by the fast exponential and division: a few units of 2^-22, well below the 16-bit
+// types that what is made of it is rounded to; 0 and 1 far out, where exp(-x) overflows or vanishes.
+__device__ __forceinline__ float fast_sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+
+// act(g) and, for the backward pass, its derivative.  The tanh form of gelu is g * sigmoid(2 z) with
+// z = sqrt(2 / pi) (g + 0.044715 g^3), as (1 + tanh(z)) / 2 = sigmoid(2 z).
+constexpr float kGelu2 = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 __device__ __forceinline__ float act_value(int act, float g) {
-  if (act == kSilu) return g * sigmoidf_(g);
-  return 0.5f * g * (1.f + tanhf(0.7978845608028654f * fmaf(0.044715f * g * g, g, g)));
+  return g * fast_sigmoid(act == kSilu ? g : kGelu2 * fmaf(0.044715f * g * g, g, g));
 }
 __device__ __forceinline__ void act_both(int act, float g, float &a, float &da) {
-  if (act == kSilu) {
-    const float s = sigmoidf_(g);
-    a = g * s;
-    da = s * fmaf(g, 1.f - s, 1.f);
-  } else {
-    const float t = tanhf(0.7978845608028654f * fmaf(0.044715f * g * g, g, g));
-    a = 0.5f * g * (1.f + t);
-    da = 0.5f * (1.f + t) + 0.5f * g * (1.f - t * t) * 0.7978845608028654f * fmaf(3.f * 0.044715f * g, g, 1.f);
-  }
+  const float s = fast_sigmoid(act == kSilu ? g : kGelu2 * fmaf(0.044715f * g * g, g, g));
+  const float slope = act == kSilu ? 1.f : kGelu2 * fmaf(3.f * 0.044715f * g, g, 1.f);
+  a = g * s;
+  da = fmaf(a * (1.f - s), slope, s);
 }
 
 }  // namespace moe
