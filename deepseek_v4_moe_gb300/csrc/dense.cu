@@ -367,8 +367,8 @@ extern "C" int moe_ffn_gated_forward(const moe_ffn_gated_args *a, void *stream) 
   moe::GemmParams down = gemm_params(a, dev, a->rows, a->hidden, kblocks(a->inter));
   down.c[0] = a->y;
   down.ldc[0] = a->ld_y;
-  const moe::GemmTile tu = moe::gemm_pick_tile(moe::kGateUp, up, sms), td = moe::gemm_pick_tile(moe::kDown, down, sms);
-  const int bu = tu.b_box(moe::kGateUp), bd = td.b_box(moe::kDown);
+  const moe::DenseTile tu = moe::gemm_pick_tile(moe::kGateUp, up, sms), td = moe::gemm_pick_tile(moe::kDown, down, sms);
+  const int bu = moe::gemm_b_box(moe::kGateUp, tu), bd = moe::gemm_b_box(moe::kDown, td);
   moe::GemmMaps mu, md;
   if (!encode_map(&mu.a[0], a->x, 2, H, R, a->ld_x, up.a_rows) || !encode_map(&mu.b[0], a->w_gate, 2, H, I, H, bu) ||
       !encode_map(&mu.b[1], a->w_up, 2, H, I, H, bu) || !encode_map(&md.a[0], a->workspace, 2, I, R, I, down.a_rows) ||
@@ -517,11 +517,13 @@ extern "C" int moe_ffn_fp8_matmul(const moe_ffn_fp8_matmul_args *a, void *stream
   p.status = dev.status;
   p.wait_ns = dev.wait_ns;
   p.inject = dev.inject;
-  const int bn = moe::fp8_pick_bn(p, sms);
+  p.a_rows = moe::a_box(a->rows);
+  const moe::DenseTile t = moe::fp8_pick_tile(p, sms);
   CUtensorMap ma, mb;
-  if (!encode_map(&ma, a->a, 1, K, R, a->ld_a, 128) || !encode_map(&mb, a->b, 1, K, N, a->ld_b, bn))
+  if (!encode_map(&ma, a->a, 1, K, R, a->ld_a, p.a_rows) ||
+      !encode_map(&mb, a->b, 1, K, N, a->ld_b, t.pair ? t.bn / 2 : t.bn))
     return fail(MOE_FFN_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", who);
-  return launched(who, moe::launch_fp8_matmul(bn, ma, mb, p, sms, static_cast<cudaStream_t>(stream)));
+  return launched(who, moe::launch_fp8_matmul(t, ma, mb, p, sms, static_cast<cudaStream_t>(stream)));
 }
 
 extern "C" int moe_ffn_fp8_quantise(const moe_ffn_fp8_quantise_args *a, void *stream) {

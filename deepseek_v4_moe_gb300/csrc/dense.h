@@ -70,13 +70,13 @@ struct GemmParams {
 inline int a_box(int m) { return m >= 128 ? 128 : (m + 7) / 8 * 8; }
 
 // a tile: bn columns (kGateUp: half of them of g, half of u) of 128 rows, or of 256 by a pair of CTAs
-struct GemmTile {
+struct DenseTile {
   int bn;
   bool pair;
-  int b_box(int mode) const;  // rows of B's boxes
 };
-GemmTile gemm_pick_tile(int mode, const GemmParams &p, int num_sms);
-cudaError_t launch_dense_gemm(int mode, GemmTile tile, const GemmMaps &maps, GemmParams p, int num_sms, cudaStream_t st);
+int gemm_b_box(int mode, DenseTile tile);  // rows of B's boxes
+DenseTile gemm_pick_tile(int mode, const GemmParams &p, int num_sms);
+cudaError_t launch_dense_gemm(int mode, DenseTile tile, const GemmMaps &maps, GemmParams p, int num_sms, cudaStream_t st);
 
 // ---- FP8 with block scales (dense_fp8.cu) ----
 
@@ -89,6 +89,7 @@ struct Fp8Params {
   void *out;
   long long ld_out;
   int wide;                  // out can be written in 16-byte pieces
+  int a_rows;                // rows of A's boxes (see a_box)
   int tiles_m, tiles_n, tiles;  // set by launch_fp8_matmul
   int *status;
   uint64_t wait_ns;
@@ -105,8 +106,8 @@ struct QuantiseParams {
   int wide;                  // x in 16-byte pieces, codes in 8-byte pieces
 };
 
-int fp8_pick_bn(const Fp8Params &p, int num_sms);
-cudaError_t launch_fp8_matmul(int bn, const CUtensorMap &a, const CUtensorMap &b, Fp8Params p, int num_sms,
+DenseTile fp8_pick_tile(const Fp8Params &p, int num_sms);
+cudaError_t launch_fp8_matmul(DenseTile tile, const CUtensorMap &a, const CUtensorMap &b, Fp8Params p, int num_sms,
                               cudaStream_t st);
 cudaError_t launch_fp8_quantise(const QuantiseParams &p, int num_sms, cudaStream_t st);
 

@@ -6,11 +6,13 @@
 // The codes' products accumulate over one block of 128 k in f32 in TMEM (four tcgen05.mma kind::f8f6f4
 // of 32 k each); the epilogue warps then take the block's sums, multiply them by the block's two scales
 // and add them to f32 sums in registers.  So scales may be any f32 values, and no more than 128 products
-// are added before a scale is applied.  Several TMEM buffers let the MMAs of the next blocks run
-// meanwhile.
+// are added before a scale is applied.  Two or more TMEM buffers let the MMAs of the next blocks run
+// meanwhile: a block of a 256 x 256 tile takes the tensor cores 512 cycles, its 128 x 256 sums a CTA's
+// multiply-adds 256 and its share of shared memory's bandwidth all of it, as 256 x 256 by a pair of CTAs
+// is the widest tile.
 //
-// A CTA (one per SM, persistent over tiles of 128 x BN, BN dividing 128 so that a tile has one b_scale):
-//   warp 0     TMA producer: a ring of blocks (A 128 rows, B BN rows, 128 bytes of k each)
+// A CTA (one per SM, persistent over tiles of 128 x BN; a pair of CTAs: 256 x BN):
+//   warp 0     TMA producer: a ring of blocks (A 128 rows, B BN rows or half of them, 128 bytes of k each)
 //   warp 1     TMEM allocator and MMA issuer
 //   warps 2-9  scaled accumulation and the output: two warps for each TMEM lane quarter, half the
 //              columns each
@@ -25,49 +27,130 @@
 namespace moe {
 namespace {
 
-template <int BN>
+template <int BN, bool PAIR>
 struct Fp8Cfg {
   static constexpr int kABytes = kBM * kScaleBlock;
-  static constexpr int kStage = kABytes + BN * kScaleBlock;
-  static constexpr int kStages = kRingBytes / kStage;
-  static constexpr size_t kSmem = (size_t)kStages * kStage + 1024;
-  static constexpr int kAcc = 4;  // TMEM buffers, one block's sums each
-  static constexpr int kTmemCols = kAcc * BN < 32 ? 32 : kAcc * BN;
-  static constexpr int kPer = BN / 2;  // columns of one epilogue warp
+  static constexpr int kBRows = PAIR ? BN / 2 : BN;  // of B in this CTA
+  static constexpr int kStage = kABytes + kBRows * kScaleBlock;
+  static constexpr int kBufBytes = kEpiWarps * kStageBuf;
+  static constexpr int kStages = (kRingBytes - kBufBytes) / kStage;
+  static constexpr size_t kSmem = (size_t)kStages * kStage + kBufBytes + 1024;
+  static constexpr int kAcc = BN > 128 ? 2 : 4;  // TMEM buffers, one block's sums each
+  static constexpr int kTmemCols = BN > 64 ? 512 : kAcc * BN;  // a power of two
+  static constexpr int kPer = BN / 2;            // columns of one epilogue warp
+  static constexpr int kChunk = kPer % 32 ? 16 : 32;  // columns of one TMEM load
+  static_assert(kBRows % 8 == 0 && kPer % 16 == 0 && kAcc * BN <= kTmemCols, "whole swizzle groups and chunks");
 };
 
-__device__ __forceinline__ uint32_t idesc_f8(bool a_e5m2, bool b_e5m2, int N) {
+__device__ __forceinline__ uint32_t idesc_f8(bool a_e5m2, bool b_e5m2, int M, int N) {
   return 1u << 4 | (a_e5m2 ? 1u : 0u) << 7 | (b_e5m2 ? 1u : 0u) << 10 | (uint32_t)(N >> 3) << 17 |
-         (uint32_t)(kBM >> 4) << 24;
+         (uint32_t)(M >> 4) << 24;
 }
 
-template <typename T, int N>
-__device__ __forceinline__ void store_row(T *dst, int left, bool wide, const float (&v)[N]) {
-  constexpr int per = 16 / (int)sizeof(T);
-  if (wide && left >= N) {
+// columns of TMEM for a whole warp, without the wait
+template <int N>
+__device__ __forceinline__ void tmem_ld_start(uint32_t taddr, float (&v)[N]) {
+  static_assert(N == 16 || N == 32, "");
+  if constexpr (N == 16)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+        : "r"(taddr));
+  else
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+          "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+          "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(taddr));
+}
+// waits for the loads before it; v passes through, so that nothing reads it earlier
+template <int N>
+__device__ __forceinline__ void tmem_ld_wait(float (&v)[N]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-    for (int i = 0; i < N; i += per) {
+  for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
+}
+// (a0, a1) += s * (v0, v1), one instruction
+__device__ __forceinline__ void fma2(float &a0, float &a1, uint64_t s, float v0, float v1) {
+  uint64_t a, v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(a0), "f"(a1));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(v0), "f"(v1));
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(a) : "l"(s), "l"(v));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a0), "=f"(a1) : "l"(a));
+}
+__device__ __forceinline__ uint64_t both(float s) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(s));
+  return r;
+}
+
+// A warp's 32 rows of N sums each to `out` from row row0 and column col on; the rows' pieces of 64 bytes
+// pass through the warp's staging buffer, so that four threads store a row's piece together.
+template <typename T, int N>
+__device__ __forceinline__ void store_rows(const Fp8Params &p, int row0, int col, uint32_t buf, const float (&v)[N]) {
+  const int lane = threadIdx.x & 31;
+  T *out = static_cast<T *>(p.out);
+  if (!p.wide) {
+    if (row0 + lane < p.m) {
+      T *dst = out + (size_t)(row0 + lane) * p.ld_out + col;
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (col + i < p.n) dst[i] = from_f32<T>(v[i]);
+    }
+    return;
+  }
+  constexpr int kPiece = 16 / (int)sizeof(T);  // values in 16 bytes; a row's 64 bytes are four of them
+#pragma unroll
+  for (int c0 = 0; c0 < N; c0 += 4 * kPiece) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int i = c0 + c * kPiece;
+      if (i >= N) break;
       uint4 w;
       if constexpr (sizeof(T) == 4)
-        w = make_uint4(__float_as_uint(v[i]), __float_as_uint(v[i + 1]), __float_as_uint(v[i + 2]),
-                       __float_as_uint(v[i + 3]));
+        w = make_uint4(__float_as_uint(v[i]), __float_as_uint(v[i + 1]), __float_as_uint(v[i + 2]), __float_as_uint(v[i + 3]));
       else
         w = make_uint4(pack2<T>(v[i], v[i + 1]), pack2<T>(v[i + 2], v[i + 3]), pack2<T>(v[i + 4], v[i + 5]),
                        pack2<T>(v[i + 6], v[i + 7]));
-      *reinterpret_cast<uint4 *>(dst + i) = w;
+      sts128(buf + piece_at(lane, c), w);
     }
-  } else {
+    __syncwarp();
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (i < left) dst[i] = from_f32<T>(v[i]);
+    for (int i = 0; i < 4; ++i) {
+      const int r = 8 * i + (lane >> 2), c = c0 + (lane & 3) * kPiece, left = p.n - (col + c);
+      if (row0 + r < p.m && c < N && left > 0) {
+        T *dst = out + (size_t)(row0 + r) * p.ld_out + col + c;
+        const uint4 w = lds128(buf + piece_at(r, lane & 3));
+        if (left >= kPiece) {
+          *reinterpret_cast<uint4 *>(dst) = w;
+        } else {
+          const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int e = 0; e < kPiece; ++e)
+            if (e < left) {
+              if constexpr (sizeof(T) == 4)
+                reinterpret_cast<uint32_t *>(dst)[e] = q[e];
+              else
+                reinterpret_cast<uint16_t *>(dst)[e] = (uint16_t)(q[e / 2] >> (16 * (e & 1)));
+            }
+        }
+      }
+    }
+    __syncwarp();
   }
 }
 
-template <int BN>
+template <int BN, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_matmul_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                       const __grid_constant__ Fp8Params p) {
-  using C = Fp8Cfg<BN>;
+  using C = Fp8Cfg<BN, PAIR>;
+  constexpr int kRows = PAIR ? 2 * kBM : kBM;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ __align__(8) uint64_t full_bar[C::kStages], empty_bar[C::kStages], tfull_bar[C::kAcc], tempty_bar[C::kAcc];
@@ -76,6 +159,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ int abort_flag, issued;
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const uint32_t rank = PAIR ? cluster_rank() : 0u;
+  const int first_tile = PAIR ? blockIdx.x >> 1 : blockIdx.x, tile_step = PAIR ? gridDim.x >> 1 : gridDim.x;
+  const uint32_t stage_bytes = C::kStage - (kBM - p.a_rows) * kScaleBlock;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full_bar[s], 1);
@@ -83,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < C::kAcc; ++b) {
       mbar_init(&tfull_bar[b], 1);
-      mbar_init(&tempty_bar[b], kEpiWarps);
+      mbar_init(&tempty_bar[b], PAIR ? 2 * kEpiWarps : kEpiWarps);
     }
     mbar_init(&mma_done_bar, 1);
     mbar_init(&never_bar, 1);
@@ -91,9 +177,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     issued = 0;
     fence_mbar_init();
   }
-  if (warp == 1) tmem_alloc(&tmem_base, C::kTmemCols);
+  if (warp == 1) {
+    if constexpr (PAIR) tmem_alloc_pair(&tmem_base, C::kTmemCols);
+    else tmem_alloc(&tmem_base, C::kTmemCols);
+  }
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync();  // the peer's barriers are initialised
   tc_fence_after();
   const uint32_t tmem = tmem_base;
   volatile int *abort_p = &abort_flag;
@@ -103,10 +193,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     RingPos<C::kStages> pos;
     int j = 0;
     bool ok = true;
-    const uint32_t ring0 = smem_u32(ring), full0 = smem_u32(full_bar);
-    for (int t = blockIdx.x; ok && t < p.tiles; t += gridDim.x) {
+    const uint32_t ring0 = smem_u32(ring), full0 = PAIR ? in_cta(full_bar, 0) : smem_u32(full_bar);
+    for (int t = first_tile; ok && t < p.tiles; t += tile_step) {
       int m, n;
       band_tile(t, p.tiles_m, p.tiles_n, m, n);
+      const int m0 = m * kRows + (int)rank * kBM, n0 = n * BN + (int)rank * C::kBRows;
       for (int kb = 0; kb < p.kb; ++kb, ++j, pos.next()) {
         const int s = pos.slot;
         if (!warp_wait(&empty_bar[s], pos.round ^ 1u, abort_p, p.status, p.wait_ns)) {
@@ -114,116 +205,137 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         const uint32_t a = ring0 + s * C::kStage, fb = full0 + 8 * s;
-        mbar_expect_one(fb, C::kStage);
-        tma_load_2d_one<false>(a, &tm_a, fb, kb * kScaleBlock, m * kBM);
-        tma_load_2d_one<false>(a + C::kABytes, &tm_b, fb, kb * kScaleBlock, n * BN);
+        if (rank == 0) mbar_expect_one(fb, PAIR ? 2 * stage_bytes : stage_bytes);  // both CTAs' bytes
+        tma_load_2d_one<PAIR>(a, &tm_a, fb, kb * kScaleBlock, m0);
+        tma_load_2d_one<PAIR>(a + C::kABytes, &tm_b, fb, kb * kScaleBlock, n0);
       }
     }
     if (lane == 0) issued = j;
   } else if (warp == 1) {
     // ---------------- MMA issuer ----------------
-    if (p.inject && blockIdx.x == 0)  // test hook: a wait that runs out
-      (void)warp_wait(&never_bar, 0u, abort_p, p.status, p.wait_ns);
-    const uint32_t idesc = idesc_f8(p.a_e5m2, p.b_e5m2, BN);
-    const uint64_t a0 = smem_desc_sw128(0) + (uint64_t)(smem_u32(ring) >> 4), b0 = a0 + (C::kABytes >> 4);
-    RingPos<C::kStages> pos;
-    RingPos<C::kAcc> acc;
-    bool ok = true;
-    for (int t = blockIdx.x; ok && t < p.tiles; t += gridDim.x) {
-      for (int kb = 0; kb < p.kb; ++kb, pos.next(), acc.next()) {
-        if (!warp_wait(&tempty_bar[acc.slot], acc.round ^ 1u, abort_p, p.status, p.wait_ns) ||
-            !warp_wait(&full_bar[pos.slot], pos.round, abort_p, p.status, p.wait_ns)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t at = pos.slot * (C::kStage >> 4), d = tmem + (uint32_t)(acc.slot * BN);
+    if (rank == 0) {
+      if (p.inject && blockIdx.x == 0)  // test hook: a wait that runs out
+        (void)warp_wait(&never_bar, 0u, abort_p, p.status, p.wait_ns);
+      const uint32_t idesc = idesc_f8(p.a_e5m2, p.b_e5m2, kRows, BN);
+      const uint64_t a0 = smem_desc_sw128(0) + (uint64_t)(smem_u32(ring) >> 4), b0 = a0 + (C::kABytes >> 4);
+      RingPos<C::kStages> pos;
+      RingPos<C::kAcc> acc;
+      bool ok = true;
+      for (int t = first_tile; ok && t < p.tiles; t += tile_step) {
+        for (int kb = 0; kb < p.kb; ++kb, pos.next(), acc.next()) {
+          if (!warp_wait(&tempty_bar[acc.slot], acc.round ^ 1u, abort_p, p.status, p.wait_ns) ||
+              !warp_wait(&full_bar[pos.slot], pos.round, abort_p, p.status, p.wait_ns)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t at = pos.slot * (C::kStage >> 4), d = tmem + (uint32_t)(acc.slot * BN);
 #pragma unroll
-        for (int k = 0; k < kScaleBlock / 32; ++k)
-          tc_mma_one<false, true>(d, a0 + (at + k * 2), b0 + (at + k * 2), idesc, k ? 1u : 0u);
-        tc_commit_one<false>(smem_u32(&empty_bar[pos.slot]));
-        tc_commit_one<false>(smem_u32(&tfull_bar[acc.slot]));
+          for (int k = 0; k < kScaleBlock / 32; ++k)
+            tc_mma_one<PAIR, true>(d, a0 + (at + k * 2), b0 + (at + k * 2), idesc, k ? 1u : 0u);
+          tc_commit_one<PAIR>(smem_u32(&empty_bar[pos.slot]));
+          tc_commit_one<PAIR>(smem_u32(&tfull_bar[acc.slot]));
+        }
       }
+      // every MMA this warp issued completes before TMEM is freed
+      tc_commit_local_one<PAIR>(smem_u32(&mma_done_bar));
+      int no_abort = 0;
+      (void)wait_bounded(&mma_done_bar, 0u, &no_abort, p.status, p.wait_ns);
     }
-    // every MMA this warp issued completes before TMEM is freed
-    tc_commit_one<false>(smem_u32(&mma_done_bar));
-    int no_abort = 0;
-    (void)wait_bounded(&mma_done_bar, 0u, &no_abort, p.status, p.wait_ns);
-  } else if (warp >= 2) {
+  } else {
     // ---------------- scaled accumulation and output ----------------
     const int q = warp & 3, half = (warp - 2) >> 2;
-    int j = 0;
+    const uint32_t buf = smem_u32(ring) + C::kStages * C::kStage + (warp - 2) * kStageBuf;
+    const uint32_t tempty0 = PAIR ? in_cta(tempty_bar, 0) : smem_u32(tempty_bar);
+    RingPos<C::kAcc> acc;
     bool ok = true;
-    for (int t = blockIdx.x; t < p.tiles; t += gridDim.x) {
+    for (int t = first_tile; t < p.tiles; t += tile_step) {
       int m, n;
       band_tile(t, p.tiles_m, p.tiles_n, m, n);
-      const int row = m * kBM + q * 32 + lane;
-      const float *sa = p.a_scale + (size_t)row * p.kb;
-      const float *sb = p.b_scale + (size_t)(n * BN / kScaleBlock) * p.kb;
-      const bool in = row < p.m;
+      const int row0 = m * kRows + (int)rank * kBM + q * 32, col = n * BN + half * C::kPer;
+      // the columns span at most two blocks of b_scale; the second begins at column `edge` of them
+      const int blk = min(col, p.n - 1) / kScaleBlock, edge = (col / kScaleBlock + 1) * kScaleBlock - col;
+      const bool two = edge < C::kPer && col + edge < p.n;
+      const bool in = row0 + lane < p.m;
+      const float *sa = p.a_scale + (size_t)(in ? row0 + lane : 0) * p.kb;
+      const float *sb = p.b_scale + (size_t)blk * p.kb, *sb2 = two ? sb + p.kb : sb;
       float sum[C::kPer];
 #pragma unroll
       for (int i = 0; i < C::kPer; ++i) sum[i] = 0.f;
-      for (int kb = 0; kb < p.kb; ++kb, ++j) {
-        const int acc = j % C::kAcc;
-        const float scale = in ? sa[kb] * sb[kb] : 0.f;
-        int ready = 0;
-        if (lane == 0)
-          ready = wait_bounded(&tfull_bar[acc], (uint32_t)((j / C::kAcc) & 1), abort_p, p.status, p.wait_ns) ? 1 : 0;
-        if (!__shfl_sync(0xffffffffu, ready, 0)) {
+      float next_a = sa[0], next_b = sb[0], next_b2 = sb2[0];
+      for (int kb = 0; kb < p.kb; ++kb, acc.next()) {
+        const uint64_t s1 = both(next_a * next_b), s2 = both(next_a * next_b2);
+        if (kb + 1 < p.kb) {
+          next_a = sa[kb + 1];
+          next_b = sb[kb + 1];
+          next_b2 = sb2[kb + 1];
+        }
+        if (!warp_wait(&tfull_bar[acc.slot], acc.round, abort_p, p.status, p.wait_ns)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BN + half * C::kPer);
+        const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc.slot * BN + half * C::kPer);
+        constexpr int N = C::kPer / C::kChunk;
+        float v[2][C::kChunk];
+        tmem_ld_start(tb, v[0]);
 #pragma unroll
-        for (int c = 0; c < C::kPer; c += 16) {
-          float v[16];
-          tmem_ld16(tb + c, v);
+        for (int c = 0; c < N; ++c) {
+          tmem_ld_wait(v[c & 1]);
+          if (c + 1 < N) {
+            tmem_ld_start(tb + (c + 1) * C::kChunk, v[(c + 1) & 1]);
+          } else {  // everything is in registers: the buffer is free
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if constexpr (PAIR) mbar_arrive_cluster(tempty0 + 8 * acc.slot);
+              else mbar_arrive(&tempty_bar[acc.slot]);
+            }
+          }
+          const uint64_t s = c * C::kChunk < edge ? s1 : s2;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) sum[c + i] = fmaf(scale, v[i], sum[c + i]);
+          for (int i = 0; i < C::kChunk; i += 2)
+            fma2(sum[c * C::kChunk + i], sum[c * C::kChunk + i + 1], s, v[c & 1][i], v[c & 1][i + 1]);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&tempty_bar[acc]);
       }
       if (!ok) break;
-      const int col = n * BN + half * C::kPer, left = p.n - col;
-      if (in && left > 0) {
-        const size_t at = (size_t)row * p.ld_out + col;
-        if (p.out_type == kF32) store_row(static_cast<float *>(p.out) + at, left, p.wide, sum);
-        else if (p.out_type == kBF16) store_row(static_cast<__nv_bfloat16 *>(p.out) + at, left, p.wide, sum);
-        else store_row(static_cast<__half *>(p.out) + at, left, p.wide, sum);
-      }
+      if (p.out_type == kF32) store_rows<float>(p, row0, col, buf, sum);
+      else if (p.out_type == kBF16) store_rows<__nv_bfloat16>(p, row0, col, buf, sum);
+      else store_rows<__half>(p, row0, col, buf, sum);
       __syncwarp();
     }
   }
-  // copies still in flight after an abort land before the CTA may leave (bounded; in a normal run each
-  // has landed long ago)
+  // Copies still in flight after an abort land before a CTA may leave (bounded; in a normal run each has
+  // landed long ago).  A peer may have issued stages whose arrival the leader still owes.
   tc_fence_before();
   __syncthreads();
-  if (threadIdx.x == 0) {
-    int no_abort = 0;
+  if constexpr (PAIR) cluster_sync();
+  if (threadIdx.x == 0 && rank == 0) {
+    int j = issued, no_abort = 0;
+    if constexpr (PAIR) {
+      const int theirs = ld_cluster_s32(in_cta(&issued, 1));
+      for (; j < theirs; ++j) mbar_arrive_expect_tx(&full_bar[j % C::kStages], stage_bytes);
+    }
     for (int s = 0; s < C::kStages; ++s) {
-      const int n = issued / C::kStages + (s < issued % C::kStages ? 1 : 0);
+      const int n = j / C::kStages + (s < j % C::kStages ? 1 : 0);
       if (n > 0) (void)wait_bounded(&full_bar[s], (uint32_t)((n - 1) & 1), &no_abort, p.status, p.wait_ns);
     }
   }
   __syncthreads();
+  if constexpr (PAIR) cluster_sync();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, C::kTmemCols);
+    if constexpr (PAIR) tmem_dealloc_pair(tmem, C::kTmemCols);
+    else tmem_dealloc(tmem, C::kTmemCols);
   }
 }
 
-template <int BN>
+template <int BN, bool PAIR>
 cudaError_t launch(const CUtensorMap &a, const CUtensorMap &b, const Fp8Params &p, int num_sms, cudaStream_t st) {
-  using C = Fp8Cfg<BN>;
+  using C = Fp8Cfg<BN, PAIR>;
   static std::atomic<unsigned long long> done{0};
-  const cudaError_t e = allow_smem((const void *)fp8_matmul_kernel<BN>, C::kSmem, done);
-  if (e != cudaSuccess) return e;
-  fp8_matmul_kernel<BN><<<p.tiles < num_sms ? p.tiles : num_sms, kThreads, C::kSmem, st>>>(a, b, p);
-  return cudaGetLastError();
+  static std::atomic<int> pairs{0};
+  return launch_tiles<PAIR>(fp8_matmul_kernel<BN, PAIR>, C::kSmem, done, pairs, p.tiles, num_sms, st, a, b, p);
 }
 
 // ---- quantiser ----
@@ -344,31 +456,43 @@ cudaError_t quantise_typed(const QuantiseParams &p, int num_sms, cudaStream_t st
   return cudaGetLastError();
 }
 
+long long fp8_tiles(const Fp8Params &p, DenseTile t) {
+  const int rows = t.pair ? 2 * kBM : kBM;
+  return (long long)((p.m + rows - 1) / rows) * ((p.n + t.bn - 1) / t.bn);
+}
+
 }  // namespace
 
-// The widest tile whose waves over the SMs cost least (see gemm_pick_bn).
-int fp8_pick_bn(const Fp8Params &p, int num_sms) {
-  int best = 0;
-  long long least = 0;
-  for (int bn = 128; bn >= 32; bn /= 2) {
-    const long long tiles = (long long)((p.m + kBM - 1) / kBM) * ((p.n + bn - 1) / bn);
-    const long long cost = (tiles + num_sms - 1) / num_sms * (bn + 32);
-    if (!best || cost < least) {
-      best = bn;
-      least = cost;
+// The tile that takes the least time (see gemm_pick_tile).
+DenseTile fp8_pick_tile(const Fp8Params &p, int num_sms) {
+  const struct {
+    DenseTile tile;
+    double k_block;
+  } all[] = {{{256, true}, 0.300}, {{224, true}, 0.270}, {{128, false}, 0.250}, {{64, false}, 0.200}, {{32, false}, 0.180}};
+  DenseTile best = {0, false};
+  double least = 0;
+  for (const auto &c : all) {
+    const long long units = c.tile.pair ? num_sms / 2 : num_sms;
+    const long long waves = (fp8_tiles(p, c.tile) + units - 1) / units;
+    const double time = (c.tile.pair ? 5.8 : 3.8) + waves * c.k_block * p.kb + 0.01 * c.tile.bn;
+    if (best.bn == 0 || time < least) {
+      best = c.tile;
+      least = time;
     }
   }
   return best;
 }
 
-cudaError_t launch_fp8_matmul(int bn, const CUtensorMap &a, const CUtensorMap &b, Fp8Params p, int num_sms,
+cudaError_t launch_fp8_matmul(DenseTile t, const CUtensorMap &a, const CUtensorMap &b, Fp8Params p, int num_sms,
                               cudaStream_t st) {
-  p.tiles_m = (p.m + kBM - 1) / kBM;
-  p.tiles_n = (p.n + bn - 1) / bn;
+  p.tiles_m = (p.m + (t.pair ? 2 : 1) * kBM - 1) / ((t.pair ? 2 : 1) * kBM);
+  p.tiles_n = (p.n + t.bn - 1) / t.bn;
   p.tiles = p.tiles_m * p.tiles_n;
-  if (bn == 128) return launch<128>(a, b, p, num_sms, st);
-  if (bn == 64) return launch<64>(a, b, p, num_sms, st);
-  if (bn == 32) return launch<32>(a, b, p, num_sms, st);
+  if (t.bn == 256 && t.pair) return launch<256, true>(a, b, p, num_sms, st);
+  if (t.bn == 224 && t.pair) return launch<224, true>(a, b, p, num_sms, st);
+  if (t.bn == 128) return launch<128, false>(a, b, p, num_sms, st);
+  if (t.bn == 64) return launch<64, false>(a, b, p, num_sms, st);
+  if (t.bn == 32) return launch<32, false>(a, b, p, num_sms, st);
   return cudaErrorInvalidValue;
 }
 

@@ -37,7 +37,6 @@ namespace {
 
 constexpr int kBK = 64;
 constexpr int kABytes = kBM * kBK * 2;
-constexpr int kStageBuf = 32 * 64;  // see piece_at
 
 template <int MODE, int BN, bool PAIR>
 struct Cfg {
@@ -88,19 +87,6 @@ __device__ __forceinline__ Tile tile_of(const GemmParams &p, int t, int rows, in
   r.m0 *= rows;
   r.n0 *= cols;
   return r;
-}
-
-// A warp's staging buffer: 32 rows x 32 values of a 16-bit type, 64 bytes a row in four pieces, piece c of
-// row r at place c ^ (r / 2 % 4), so that both a warp writing one piece of every row and a warp writing
-// whole rows side by side meet every bank once.
-__device__ __forceinline__ uint32_t piece_at(int r, int c) { return r * 64 + ((c ^ (r >> 1)) & 3) * 16; }
-__device__ __forceinline__ void sts128(uint32_t a, const uint4 w) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
-}
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 w;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(a) : "memory");
-  return w;
 }
 
 // A warp's 32 rows of a tile: its columns [32 * half, kCols) in steps of 64, 32 at a time.  A thread of
@@ -424,44 +410,20 @@ template <int MODE, int BN, bool PAIR>
 cudaError_t launch(const GemmMaps &maps, const GemmParams &p, int num_sms, cudaStream_t st) {
   using C = Cfg<MODE, BN, PAIR>;
   static std::atomic<unsigned long long> done{0};
-  const cudaError_t e = allow_smem((const void *)dense_gemm_kernel<MODE, BN, PAIR>, C::kSmem, done);
-  if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim = {PAIR ? 2u : 1u, 1u, 1u};
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = C::kSmem;
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = PAIR ? 1 : 0;
-  int units = num_sms;
-  if constexpr (PAIR) {  // pairs that run at one time
-    static std::atomic<int> pairs{0};
-    units = pairs.load(std::memory_order_relaxed);
-    if (!units) {
-      const cudaError_t q = cudaOccupancyMaxActiveClusters(&units, dense_gemm_kernel<MODE, BN, PAIR>, &cfg);
-      if (q != cudaSuccess) return q;
-      if (units < 1 || units > num_sms / 2) units = num_sms / 2;
-      pairs.store(units, std::memory_order_relaxed);
-    }
-  }
-  const int busy = p.tiles < units ? p.tiles : units;
-  cfg.gridDim = dim3(PAIR ? 2 * busy : busy);
-  return cudaLaunchKernelEx(&cfg, dense_gemm_kernel<MODE, BN, PAIR>, maps, p);
+  static std::atomic<int> pairs{0};
+  return launch_tiles<PAIR>(dense_gemm_kernel<MODE, BN, PAIR>, C::kSmem, done, pairs, p.tiles, num_sms, st, maps, p);
 }
 
-long long tiles_of(int mode, const GemmParams &p, GemmTile g) {
+long long tiles_of(int mode, const GemmParams &p, DenseTile g) {
   const int cols = mode == kGateUp ? g.bn / 2 : g.bn, rows = g.pair ? 2 * kBM : kBM;
   return (long long)cdiv(p.m, rows) * cdiv(p.n, cols) * p.same + (long long)cdiv(p.m_last, rows) * cdiv(p.n_last, cols);
 }
 
 }  // namespace
 
-int GemmTile::b_box(int mode) const {
+int gemm_b_box(int mode, DenseTile t) {
   if (mode == kHiddenGrad || mode == kInputGrad || mode == kWeightGrad) return 64;
-  return mode == kGateUp || pair ? bn / 2 : bn;
+  return mode == kGateUp || t.pair ? t.bn / 2 : t.bn;
 }
 
 // The tile that takes the least time by what tiles measured (us, 2048 to 4096 k, bf16): a k block of 64
@@ -472,15 +434,15 @@ int GemmTile::b_box(int mode) const {
 // the widest tile is not always the fastest: 4096 x 4096 columns by 4096 took 83.1 us in 256 tiles of
 // 256 columns (3.4 waves of 76 pairs), 75.6 in 304 of 224 (4.0), and 1024 rows 29.4 in one wave of
 // pairs, 34.8 in two of 128 columns.
-GemmTile gemm_pick_tile(int mode, const GemmParams &p, int num_sms) {
+DenseTile gemm_pick_tile(int mode, const GemmParams &p, int num_sms) {
   const bool b_mn = mode == kHiddenGrad || mode == kInputGrad || mode == kWeightGrad;
   const double per_col = mode == kGateUp ? 0.022 : mode == kHiddenGrad ? 0.032 : 0.010;
   const struct {
-    GemmTile tile;
+    DenseTile tile;
     double k_block;
   } all[] = {{{256, true}, 0.280}, {{224, true}, 0.251}, {{192, true}, 0.222}, {{128, true}, 0.163},
              {{256, false}, 0.339}, {{128, false}, 0.200}, {{64, false}, 0.157}, {{32, false}, 0.147}};
-  GemmTile best = {0, false};
+  DenseTile best = {0, false};
   double least = 0;
   for (const auto &c : all) {
     if (b_mn && c.tile.bn < 64) continue;
@@ -496,7 +458,7 @@ GemmTile gemm_pick_tile(int mode, const GemmParams &p, int num_sms) {
   return best;
 }
 
-cudaError_t launch_dense_gemm(int mode, GemmTile g, const GemmMaps &maps, GemmParams p, int num_sms, cudaStream_t st) {
+cudaError_t launch_dense_gemm(int mode, DenseTile g, const GemmMaps &maps, GemmParams p, int num_sms, cudaStream_t st) {
   const int cols = mode == kGateUp ? g.bn / 2 : g.bn, rows = g.pair ? 2 * kBM : kBM;
   p.tiles_m = cdiv(p.m, rows);
   p.tiles_n = cdiv(p.n, cols);

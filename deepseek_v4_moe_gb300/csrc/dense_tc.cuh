@@ -169,4 +169,49 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
+// A warp's staging buffer: 32 rows x 64 bytes, a row's in four pieces, piece c of
+// row r at place c ^ (r / 2 % 4), so that both a warp writing one piece of every row and a warp writing
+// whole rows side by side meet every bank once.
+constexpr int kStageBuf = 32 * 64;
+__device__ __forceinline__ uint32_t piece_at(int r, int c) { return r * 64 + ((c ^ (r >> 1)) & 3) * 16; }
+__device__ __forceinline__ void sts128(uint32_t a, const uint4 w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 w;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(a) : "memory");
+  return w;
+}
+
+// Launches a kernel over `tiles` tiles: one CTA, or one pair of CTAs, on each SM (pair) that has work.
+template <bool PAIR, typename... KArgs, typename... Args>
+cudaError_t launch_tiles(void (*kernel)(KArgs...), size_t smem, std::atomic<unsigned long long> &done,
+                         std::atomic<int> &pairs, int tiles, int num_sms, cudaStream_t st, const Args &...args) {
+  const cudaError_t e = allow_smem((const void *)kernel, smem, done);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {PAIR ? 2u : 1u, 1u, 1u};
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = PAIR ? 1 : 0;
+  int units = num_sms;
+  if constexpr (PAIR) {  // pairs that run at one time
+    units = pairs.load(std::memory_order_relaxed);
+    if (!units) {
+      const cudaError_t q = cudaOccupancyMaxActiveClusters(&units, kernel, &cfg);
+      if (q != cudaSuccess) return q;
+      if (units < 1 || units > num_sms / 2) units = num_sms / 2;
+      pairs.store(units, std::memory_order_relaxed);
+    }
+  }
+  const int busy = tiles < units ? tiles : units;
+  cfg.gridDim = dim3(PAIR ? 2 * busy : busy);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 }  // namespace moe

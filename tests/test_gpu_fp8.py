@@ -44,7 +44,7 @@ def check(a, sa, b, sb, out):
 
 SIZES = [(1, 1, 16), (1, 129, 128), (2, 64, 144), (3, 1000, 256), (4, 4096, 4096), (5, 127, 384), (16, 200, 1040),
          (33, 1031, 2000), (128, 128, 128), (129, 257, 512), (200, 77, 4112), (300, 520, 272), (1000, 640, 1024),
-         (1, 2048, 8192), (64, 8192, 512)]
+         (1, 2048, 8192), (64, 8192, 512), (2100, 4000, 272), (1033, 2055, 640), (4096, 1031, 144)]
 
 
 @pytest.mark.parametrize("rows,n,k", SIZES)
@@ -204,17 +204,19 @@ def test_another_stream_and_a_graph(cuda_lib):
 def test_a_wait_that_runs_out_is_reported(cuda_lib):
     import deepseek_v4_moe_gb300 as m
     gen = torch.Generator(device="cuda").manual_seed(9)
-    a, sa = operand(200, 512, 1, E4, gen)
-    b, sb = operand(256, 512, 128, E4, gen)
-    good = m.fp8_matmul(a, sa, b, sb)
-    assert m.dense_status() == 0
-    assert cuda_lib.moe_ffn_dense_fault_injection(1, 20000) == 0
-    try:
-        m.fp8_matmul(a, sa, b, sb)
-        assert m.dense_status() == 8
-    finally:
-        cuda_lib.moe_ffn_dense_fault_injection(0, 0)
-    assert torch.equal(m.fp8_matmul(a, sa, b, sb), good)
+    for rows, n, k in ((200, 256, 512), (4096, 4096, 1024)):  # single CTAs, and pairs
+        a, sa = operand(rows, k, 1, E4, gen)
+        b, sb = operand(n, k, 128, E4, gen)
+        good = m.fp8_matmul(a, sa, b, sb)
+        assert m.dense_status() == 0
+        assert cuda_lib.moe_ffn_dense_fault_injection(1, 20000) == 0
+        try:
+            m.fp8_matmul(a, sa, b, sb)
+            assert m.dense_status() == 8
+        finally:
+            cuda_lib.moe_ffn_dense_fault_injection(0, 0)
+        assert torch.equal(m.fp8_matmul(a, sa, b, sb), good)
+        assert m.dense_status() == 0
 
 
 def test_refusals(cuda_lib):
