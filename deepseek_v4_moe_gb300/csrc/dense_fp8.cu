@@ -18,6 +18,7 @@
 //              columns each
 // Rows and k past an operand's end read as zeros; outputs past the end are not stored.
 #include <cuda_fp8.h>
+#include <string.h>
 
 #include "common.cuh"
 #include "dense.h"
@@ -89,21 +90,28 @@ __device__ __forceinline__ uint64_t both(float s) {
   return r;
 }
 
+// one value of a staging buffer
+template <typename T>
+__device__ __forceinline__ T staged(uint32_t a) {
+  T v;
+  if constexpr (sizeof(T) == 4) {
+    uint32_t w;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(a) : "memory");
+    memcpy(&v, &w, 4);
+  } else {
+    uint16_t w;
+    asm volatile("ld.shared.b16 %0, [%1];" : "=h"(w) : "r"(a) : "memory");
+    memcpy(&v, &w, 2);
+  }
+  return v;
+}
+
 // A warp's 32 rows of N sums each to `out` from row row0 and column col on; the rows' pieces of 64 bytes
 // pass through the warp's staging buffer, so that four threads store a row's piece together.
 template <typename T, int N>
 __device__ __forceinline__ void store_rows(const Fp8Params &p, int row0, int col, uint32_t buf, const float (&v)[N]) {
   const int lane = threadIdx.x & 31;
   T *out = static_cast<T *>(p.out);
-  if (!p.wide) {
-    if (row0 + lane < p.m) {
-      T *dst = out + (size_t)(row0 + lane) * p.ld_out + col;
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (col + i < p.n) dst[i] = from_f32<T>(v[i]);
-    }
-    return;
-  }
   constexpr int kPiece = 16 / (int)sizeof(T);  // values in 16 bytes; a row's 64 bytes are four of them
 #pragma unroll
   for (int c0 = 0; c0 < N; c0 += 4 * kPiece) {
@@ -120,6 +128,18 @@ __device__ __forceinline__ void store_rows(const Fp8Params &p, int row0, int col
       sts128(buf + piece_at(lane, c), w);
     }
     __syncwarp();
+    if (!p.wide) {  // single values, neighbouring threads side by side in a row
+      constexpr int kRow = 4 * kPiece, kAtOnce = 32 / kRow;
+      const int c = lane % kRow;
+      const bool there = c0 + c < N && col + c0 + c < p.n;
+#pragma unroll 4
+      for (int r = lane / kRow; r < 32; r += kAtOnce)
+        if (there && row0 + r < p.m)
+          out[(size_t)(row0 + r) * p.ld_out + col + c0 + c] =
+              staged<T>(buf + piece_at(r, c / kPiece) + (c % kPiece) * (int)sizeof(T));
+      __syncwarp();
+      continue;
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = 8 * i + (lane >> 2), c = c0 + (lane & 3) * kPiece, left = p.n - (col + c);
@@ -341,7 +361,8 @@ cudaError_t launch(const CUtensorMap &a, const CUtensorMap &b, const Fp8Params &
 // ---- quantiser ----
 // A block's scale is its largest magnitude over the largest code (448 or 57344); 1 for a block of
 // zeros, at least 2^-126 so that it is a normal number, and with pow2 rounded up to a power of two.  A
-// code is x / scale rounded to nearest even.  The magnitudes are compared as integers, so that a NaN
+// code is x times the scale's reciprocal (a division for each value made the kernel arithmetic-bound:
+// 18.9 us for 4096 x 4096 bf16) rounded to nearest even.  The magnitudes are compared as integers, so that a NaN
 // counts as the largest and makes the scale NaN.
 
 __device__ __forceinline__ float block_scale(uint32_t amax, bool e5m2, bool pow2) {
@@ -353,10 +374,10 @@ __device__ __forceinline__ float block_scale(uint32_t amax, bool e5m2, bool pow2
   return s;
 }
 
-__device__ __forceinline__ uint32_t codes4(const float *v, float s, bool e5m2) {
+__device__ __forceinline__ uint32_t codes4(const float *v, float r, bool e5m2) {
   const __nv_fp8_interpretation_t f = e5m2 ? __NV_E5M2 : __NV_E4M3;
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(v[0], s), __fdiv_rn(v[1], s)), __NV_SATFINITE, f);
-  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(v[2], s), __fdiv_rn(v[3], s)), __NV_SATFINITE, f);
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[0] * r, v[1] * r), __NV_SATFINITE, f);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[2] * r, v[3] * r), __NV_SATFINITE, f);
   return lo | hi << 16;
 }
 
@@ -376,10 +397,10 @@ __device__ __forceinline__ void load_part(const QuantiseParams &p, int row, int 
   }
 }
 template <bool WIDE>
-__device__ __forceinline__ void store_part(const QuantiseParams &p, int row, int col, float s, const float (&v)[8]) {
+__device__ __forceinline__ void store_part(const QuantiseParams &p, int row, int col, float r, const float (&v)[8]) {
   if (row >= p.rows || col >= p.k) return;
   uint8_t *dst = p.codes + (size_t)row * p.ld_codes + col;
-  const uint32_t a = codes4(v, s, p.e5m2), b = codes4(v + 4, s, p.e5m2);
+  const uint32_t a = codes4(v, r, p.e5m2), b = codes4(v + 4, r, p.e5m2);
   if constexpr (WIDE) {
     *reinterpret_cast<uint2 *>(dst) = make_uint2(a, b);
   } else {
@@ -395,24 +416,42 @@ __device__ __forceinline__ uint32_t largest(const float (&v)[8]) {
   return m;
 }
 
+constexpr int kQuantBlocks = 4;  // neighbouring blocks of a row that 16 lanes take at a time: their loads overlap
+
 template <typename T, bool WIDE>
 __global__ void __launch_bounds__(256) quantise_rows_kernel(const __grid_constant__ QuantiseParams p) {
-  const int blocks = (p.k + kScaleBlock - 1) / kScaleBlock;
-  const long long total = (long long)p.rows * blocks, step = (long long)gridDim.x * 16;
-  const int part = threadIdx.x & 15;
+  const int blocks = (p.k + kScaleBlock - 1) / kScaleBlock, per_row = (blocks + kQuantBlocks - 1) / kQuantBlocks;
+  const int part = threadIdx.x & 15, step = gridDim.x * 16;
+  // where this half warp begins, and by how much it moves on: rows and groups of blocks
+  const long long first = (long long)blockIdx.x * 16 + (threadIdx.x >> 4);
+  long long row = first / per_row;
+  int group = (int)(first % per_row);
+  const int rows_on = step / per_row, groups_on = step % per_row;
   // whole warps stay in the loop for the shuffles: a half warp past the end works on nothing
-  for (long long base = (long long)blockIdx.x * 16 + (threadIdx.x >> 5) * 2; base < total; base += step) {
-    const long long i = base + ((threadIdx.x >> 4) & 1);
-    const bool in = i < total;
-    const int row = in ? (int)(i / blocks) : p.rows, b = in ? (int)(i % blocks) : 0, col = b * kScaleBlock + part * 8;
-    float v[8];
-    load_part<T, WIDE>(p, row, col, v);
-    uint32_t m = largest(v);
+  while (__any_sync(0xffffffffu, row < p.rows)) {
+    const int r = row < p.rows ? (int)row : p.rows, b0 = group * kQuantBlocks;
+    float v[kQuantBlocks][8];
+    uint32_t m[kQuantBlocks];
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float s = block_scale(m, p.e5m2, p.pow2);
-    store_part<WIDE>(p, row, col, s, v);
-    if (in && part == 0) p.scales[i] = s;
+    for (int i = 0; i < kQuantBlocks; ++i) load_part<T, WIDE>(p, r, (b0 + i) * kScaleBlock + part * 8, v[i]);
+#pragma unroll
+    for (int i = 0; i < kQuantBlocks; ++i) m[i] = largest(v[i]);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < kQuantBlocks; ++i) m[i] = max(m[i], __shfl_xor_sync(0xffffffffu, m[i], o));
+#pragma unroll
+    for (int i = 0; i < kQuantBlocks; ++i) {
+      const float s = block_scale(m[i], p.e5m2, p.pow2);
+      store_part<WIDE>(p, r, (b0 + i) * kScaleBlock + part * 8, __frcp_rn(s), v[i]);
+      if (part == 0 && r < p.rows && b0 + i < blocks) p.scales[(size_t)r * blocks + b0 + i] = s;
+    }
+    row += rows_on;
+    group += groups_on;
+    if (group >= per_row) {
+      group -= per_row;
+      ++row;
+    }
   }
 }
 
@@ -434,9 +473,9 @@ __global__ void __launch_bounds__(256) quantise_tiles_kernel(const __grid_consta
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = max(m, largest_of[i]);
-  const float s = block_scale(m, p.e5m2, p.pow2);
+  const float s = block_scale(m, p.e5m2, p.pow2), r = __frcp_rn(s);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) store_part<WIDE>(p, row + 16 * i, col, s, v[i]);
+  for (int i = 0; i < 8; ++i) store_part<WIDE>(p, row + 16 * i, col, r, v[i]);
   if (threadIdx.x == 0) p.scales[blockIdx.x] = s;
 }
 
@@ -444,7 +483,8 @@ template <typename T>
 cudaError_t quantise_typed(const QuantiseParams &p, int num_sms, cudaStream_t st) {
   const long long blocks = (p.k + kScaleBlock - 1) / kScaleBlock;
   if (p.tall == 1) {
-    const long long ctas = (p.rows * blocks + 15) / 16, most = (long long)num_sms * 8 * 4;
+    const long long per_row = (blocks + kQuantBlocks - 1) / kQuantBlocks;
+    const long long ctas = (p.rows * per_row + 15) / 16, most = (long long)num_sms * 8;
     const int grid = (int)(ctas < most ? ctas : most);
     if (p.wide) quantise_rows_kernel<T, true><<<grid, 256, 0, st>>>(p);
     else quantise_rows_kernel<T, false><<<grid, 256, 0, st>>>(p);
@@ -463,18 +503,22 @@ long long fp8_tiles(const Fp8Params &p, DenseTile t) {
 
 }  // namespace
 
-// The tile that takes the least time (see gemm_pick_tile).
+// The tile that takes the least time (see gemm_pick_tile), from what they measured at 4096 x 4096 (us): a k
+// block with 256, 224 and 128 columns on a pair 0.47, 0.42 and 0.28, with 128, 64 and 32 on a CTA by
+// itself 0.305, 0.265 and 0.26.  4096 rows took 59.4 in 224 columns (four waves), 66.0 in 256, 73.3 in
+// single CTAs' 128.
 DenseTile fp8_pick_tile(const Fp8Params &p, int num_sms) {
   const struct {
     DenseTile tile;
     double k_block;
-  } all[] = {{{256, true}, 0.300}, {{224, true}, 0.270}, {{128, false}, 0.250}, {{64, false}, 0.200}, {{32, false}, 0.180}};
+  } all[] = {{{256, true}, 0.47},   {{224, true}, 0.42},  {{128, true}, 0.28},
+             {{128, false}, 0.305}, {{64, false}, 0.265}, {{32, false}, 0.26}};
   DenseTile best = {0, false};
   double least = 0;
   for (const auto &c : all) {
     const long long units = c.tile.pair ? num_sms / 2 : num_sms;
     const long long waves = (fp8_tiles(p, c.tile) + units - 1) / units;
-    const double time = (c.tile.pair ? 5.8 : 3.8) + waves * c.k_block * p.kb + 0.01 * c.tile.bn;
+    const double time = (c.tile.pair ? 4.0 : 3.5) + waves * c.k_block * p.kb + 0.012 * c.tile.bn;
     if (best.bn == 0 || time < least) {
       best = c.tile;
       least = time;
@@ -490,6 +534,7 @@ cudaError_t launch_fp8_matmul(DenseTile t, const CUtensorMap &a, const CUtensorM
   p.tiles = p.tiles_m * p.tiles_n;
   if (t.bn == 256 && t.pair) return launch<256, true>(a, b, p, num_sms, st);
   if (t.bn == 224 && t.pair) return launch<224, true>(a, b, p, num_sms, st);
+  if (t.bn == 128 && t.pair) return launch<128, true>(a, b, p, num_sms, st);
   if (t.bn == 128) return launch<128, false>(a, b, p, num_sms, st);
   if (t.bn == 64) return launch<64, false>(a, b, p, num_sms, st);
   if (t.bn == 32) return launch<32, false>(a, b, p, num_sms, st);

@@ -19,7 +19,10 @@
 // the row is a warp butterfly and one exchange through shared memory.  The backward pass sums the
 // weights' gradients over its rows in registers, writes one partial row for each group, and a
 // second kernel adds the partial rows in a fixed order: no atomics, the same bits every run.
+#include <string.h>
+
 #include "dense.h"
+#include "dense_tc.cuh"
 #include "dense_vec.cuh"
 #include "kernels.h"
 
@@ -131,66 +134,151 @@ __device__ __forceinline__ void store_gate(const NormParams &p, size_t at, int t
     Eight<TB, VEC>::store(static_cast<TB *>(p.d_gate) + at, t, n, p.hidden, v);
 }
 
+// A worker's place in its rows: row i of the lap-th of its chunks.
+struct Place {
+  int lap = 0, i = 0;
+  __device__ __forceinline__ void next(const NormBwdPlan &pl) {
+    if (++i == pl.chunk_rows) {
+      i = 0;
+      ++lap;
+    }
+  }
+  __device__ __forceinline__ int chunk(const NormBwdPlan &pl, int worker) const { return lap * pl.workers + worker; }
+  // the row, or -1 where the chunk (the last of a gate row may be shorter) has none
+  __device__ __forceinline__ int row(const NormParams &p, const NormBwdPlan &pl, int worker) const {
+    const int c = chunk(pl, worker);
+    if (c >= pl.chunks) return -1;
+    const int gate_row = c / pl.chunks_per_gate;
+    const int r = gate_row * p.rows_per_gate + (c % pl.chunks_per_gate) * pl.chunk_rows + i;
+    return r < min((gate_row + 1) * p.rows_per_gate, p.rows) ? r : -1;
+  }
+};
+
+// Rows on their way: each thread copies its own columns of the next DEPTH - 1 rows into its own places in
+// shared memory (cp.async) and reads them back itself, so no barrier guards the ring.
+template <typename TS, typename TB, int DEPTH>
+struct RowRing {
+  static constexpr int kS = sizeof(TS) / 2, kB = sizeof(TB) / 2;  // 16-byte pieces of eight values
+  static constexpr int kPieces = 2 * kS + 2 * kB;                 // state, d_out, d_y, f: sizeof(TS) + sizeof(TB)
+  uint32_t base;  // this thread's first piece; pieces lie blockDim.x * 16 bytes apart
+  __device__ __forceinline__ uint32_t at(int stage, int piece) const {
+    return base + (uint32_t)(stage * kPieces + piece) * blockDim.x * 16u;
+  }
+  template <typename T>
+  __device__ __forceinline__ void copy(int stage, int piece, const T *src) const {
+#pragma unroll
+    for (int k = 0; k < (int)sizeof(T) / 2; ++k)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at(stage, piece + k)), "l"(src + k * (16 / sizeof(T)))
+                   : "memory");
+  }
+  template <typename T>
+  __device__ __forceinline__ void get(int stage, int piece, float (&v)[8]) const {
+    Eight<T, true> e;
+    uint4 w[sizeof(T) / 2];
+#pragma unroll
+    for (int k = 0; k < (int)sizeof(T) / 2; ++k)
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[k].x), "=r"(w[k].y), "=r"(w[k].z), "=r"(w[k].w)
+                   : "r"(at(stage, piece + k))
+                   : "memory");
+    memcpy(&e, w, sizeof e);
+    e.get(v);
+  }
+  __device__ __forceinline__ void fetch(const NormParams &p, int stage, int row, int t) const {
+    if (row >= 0 && 8 * t < p.hidden) {
+      if (p.w_next) copy(stage, 0, static_cast<const TS *>(p.state) + row * p.ld_state + 8 * t);
+      if (p.d_out) copy(stage, kS, static_cast<const TS *>(p.d_out) + row * p.ld_d_out + 8 * t);
+      if (p.w_next) copy(stage, 2 * kS, static_cast<const TB *>(p.d_y) + row * p.ld_d_y + 8 * t);
+      if (p.f) copy(stage, 2 * kS + kB, static_cast<const TB *>(p.f) + row * p.ld_f + 8 * t);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+};
+
+// Rows in flight in the ring: three, or what a CTA's shared memory holds at 1024 threads; 0: no ring.
+template <typename TS, typename TB, int MAXT>
+constexpr int kRingFit = 220 * 1024 / (MAXT * 16 * (int)(sizeof(TS) + sizeof(TB)));
+template <typename TS, typename TB, bool VEC, int MAXT>
+constexpr int kRingDepth = !VEC ? 0 : kRingFit<TS, TB, MAXT> < 3 ? kRingFit<TS, TB, MAXT> : 3;
+
 template <typename TS, typename TB, bool VEC, int MAXT>
 __global__ void __launch_bounds__(MAXT)
     block_norm_backward_kernel(const __grid_constant__ NormParams p, const __grid_constant__ NormBwdPlan pl) {
+  constexpr int DEPTH = kRingDepth<TS, TB, VEC, MAXT>;
   __shared__ float buf[2 * kSumBuf];
+  extern __shared__ uint4 ring_smem[];
+  RowRing<TS, TB, DEPTH> ring;
+  ring.base = smem_u32(ring_smem + threadIdx.x);
   const int n = pl.threads, t = threadIdx.x & (n - 1), group = threadIdx.x / n;
   const int worker = blockIdx.x * pl.groups + group;
   const float inv = 1.f / (float)p.hidden;
+  const bool there = VEC ? 8 * t < p.hidden : true;
   int turn = 0;
   float a_next[8], a_post[8], a_gate[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) a_next[e] = a_post[e] = a_gate[e] = 0.f;
   // the same number of steps for every thread of the grid: the reductions are CTA-wide
-  const int laps = (pl.chunks + pl.workers - 1) / pl.workers;
-  for (int lap = 0; lap < laps; ++lap) {
-    const int chunk = lap * pl.workers + worker;
-    const int gate_row = chunk / pl.chunks_per_gate;
-    const int first = gate_row * p.rows_per_gate + (chunk % pl.chunks_per_gate) * pl.chunk_rows;
-    const int end = min(min(first + pl.chunk_rows, (gate_row + 1) * p.rows_per_gate), p.rows);
-    const bool live = chunk < pl.chunks;
-    for (int i = 0; i < pl.chunk_rows; ++i) {
-      const int row = first + i;
-      const bool in = live && row < end;
-      float ds[8], s[8], gy[8], f[8], g[8];
+  const int steps = (pl.chunks + pl.workers - 1) / pl.workers * pl.chunk_rows;
+  Place here, ahead;
+  if constexpr (VEC)
+    for (int s = 0; s < DEPTH - 1; ++s, ahead.next(pl)) ring.fetch(p, s, s < steps ? ahead.row(p, pl, worker) : -1, t);
+  int stage = 0;
+  for (int step = 0; step < steps; ++step, here.next(pl)) {
+    const int row = here.row(p, pl, worker);
+    const bool in = row >= 0;
+    float ds[8], s[8], gy[8], f[8], g[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ds[e] = s[e] = gy[e] = f[e] = g[e] = 0.f;
-      if (in) {
-        if (p.d_out) load_eight<TS, VEC>(static_cast<const TS *>(p.d_out) + row * p.ld_d_out, t, n, p.hidden, ds);
+    for (int e = 0; e < 8; ++e) ds[e] = s[e] = gy[e] = f[e] = g[e] = 0.f;
+    if constexpr (VEC) {
+      const int put = stage == 0 ? DEPTH - 1 : stage - 1;  // the stage that the step before freed
+      ring.fetch(p, put, step + DEPTH - 1 < steps ? ahead.row(p, pl, worker) : -1, t);
+      ahead.next(pl);
+      if (in && p.f) gate_eight<TB, VEC>(p, row, t, n, g);
+      asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
+      if (in && there) {
+        if (p.d_out) ring.template get<TS>(stage, ring.kS, ds);
         if (p.w_next) {
-          load_eight<TS, VEC>(static_cast<const TS *>(p.state) + row * p.ld_state, t, n, p.hidden, s);
-          load_eight<TB, VEC>(static_cast<const TB *>(p.d_y) + row * p.ld_d_y, t, n, p.hidden, gy);
+          ring.template get<TS>(stage, 0, s);
+          ring.template get<TB>(stage, 2 * ring.kS, gy);
         }
-        if (p.f) {
-          load_eight<TB, VEC>(static_cast<const TB *>(p.f) + row * p.ld_f, t, n, p.hidden, f);
-          gate_eight<TB, VEC>(p, row, t, n, g);
-        }
+        if (p.f) ring.template get<TB>(stage, 2 * ring.kS + ring.kB, f);
       }
-      float w[8], sums[3] = {0.f, 0.f, 0.f};
-      if (p.w_next) load_eight<float, VEC>(p.w_next, t, n, p.hidden, w);
-      else
+      stage = stage + 1 == DEPTH ? 0 : stage + 1;
+    } else if (in) {
+      if (p.d_out) load_eight<TS, VEC>(static_cast<const TS *>(p.d_out) + row * p.ld_d_out, t, n, p.hidden, ds);
+      if (p.w_next) {
+        load_eight<TS, VEC>(static_cast<const TS *>(p.state) + row * p.ld_state, t, n, p.hidden, s);
+        load_eight<TB, VEC>(static_cast<const TB *>(p.d_y) + row * p.ld_d_y, t, n, p.hidden, gy);
+      }
+      if (p.f) {
+        load_eight<TB, VEC>(static_cast<const TB *>(p.f) + row * p.ld_f, t, n, p.hidden, f);
+        gate_eight<TB, VEC>(p, row, t, n, g);
+      }
+    }
+    float w[8], sums[3] = {0.f, 0.f, 0.f};
+    if (p.w_next) load_eight<float, VEC>(p.w_next, t, n, p.hidden, w);
+    else
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = 0.f;
+      for (int e = 0; e < 8; ++e) w[e] = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      w[e] *= gy[e];
+      sums[0] = fmaf(s[e], s[e], sums[0]);
+      sums[1] = fmaf(w[e], s[e], sums[1]);
+      sums[2] = fmaf(f[e], f[e], sums[2]);
+    }
+    group_sums(sums, n, buf, turn);
+    const float rf = p.w_post ? rsqrtf(fmaf(sums[2], inv, p.eps)) : 1.f;
+    if (p.w_next) {
+      const float rs = rsqrtf(fmaf(sums[0], inv, p.eps)), c = rs * rs * (sums[1] * inv);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        w[e] *= gy[e];
-        sums[0] = fmaf(s[e], s[e], sums[0]);
-        sums[1] = fmaf(w[e], s[e], sums[1]);
-        sums[2] = fmaf(f[e], f[e], sums[2]);
+        a_next[e] = fmaf(gy[e], s[e] * rs, a_next[e]);
+        ds[e] = fmaf(rs, fmaf(-s[e], c, w[e]), ds[e]);
       }
-      group_sums(sums, n, buf, turn);
-      const float rf = p.w_post ? rsqrtf(fmaf(sums[2], inv, p.eps)) : 1.f;
-      if (p.w_next) {
-        const float rs = rsqrtf(fmaf(sums[0], inv, p.eps)), c = rs * rs * (sums[1] * inv);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          a_next[e] = fmaf(gy[e], s[e] * rs, a_next[e]);
-          ds[e] = fmaf(rs, fmaf(-s[e], c, w[e]), ds[e]);
-        }
-      }
-      if (in) Eight<TS, VEC>::store(static_cast<TS *>(p.d_state) + row * p.ld_d_state, t, n, p.hidden, ds);
-      if (!p.f) continue;
+    }
+    if (in) Eight<TS, VEC>::store(static_cast<TS *>(p.d_state) + row * p.ld_d_state, t, n, p.hidden, ds);
+    if (p.f) {
       if (p.w_post) load_eight<float, VEC>(p.w_post, t, n, p.hidden, w);
       else
 #pragma unroll
@@ -224,14 +312,17 @@ __global__ void __launch_bounds__(MAXT)
         }
       }
     }
-    if (p.gate_kind == kGateVector && p.d_gate && live) {
-      if (pl.chunks_per_gate == 1)
-        store_gate<TB, VEC>(p, (size_t)gate_row * p.hidden, t, n, a_gate);
-      else
-        Eight<float, VEC>::store(p.part + pl.gate_part + (size_t)chunk * p.hidden, t, n, p.hidden, a_gate);
-    }
+    if (here.i == pl.chunk_rows - 1) {  // the chunk's part of the gate's gradient is complete
+      const int chunk = here.chunk(pl, worker);
+      if (p.gate_kind == kGateVector && p.d_gate && chunk < pl.chunks) {
+        if (pl.chunks_per_gate == 1)
+          store_gate<TB, VEC>(p, (size_t)(chunk / pl.chunks_per_gate) * p.hidden, t, n, a_gate);
+        else
+          Eight<float, VEC>::store(p.part + pl.gate_part + (size_t)chunk * p.hidden, t, n, p.hidden, a_gate);
+      }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) a_gate[e] = 0.f;
+      for (int e = 0; e < 8; ++e) a_gate[e] = 0.f;
+    }
   }
   if (p.d_w_next) Eight<float, VEC>::store(p.part + (size_t)worker * p.hidden, t, n, p.hidden, a_next);
   if (p.d_w_post)
@@ -308,19 +399,25 @@ cudaError_t forward_typed(const NormParams &p, int num_sms, cudaStream_t st) {
   return cudaGetLastError();
 }
 
+template <typename TS, typename TB, bool VEC, int MAXT>
+cudaError_t backward_launch(const NormParams &p, const NormBwdPlan &pl, cudaStream_t st) {
+  static std::atomic<unsigned long long> done{0};
+  const int threads = pl.threads * pl.groups;
+  const size_t per_thread = (size_t)kRingDepth<TS, TB, VEC, MAXT> * (sizeof(TS) + sizeof(TB)) * 16;
+  const cudaError_t e =
+      allow_smem((const void *)block_norm_backward_kernel<TS, TB, VEC, MAXT>, per_thread * MAXT, done);
+  if (e != cudaSuccess) return e;
+  block_norm_backward_kernel<TS, TB, VEC, MAXT><<<pl.ctas, threads, per_thread * threads, st>>>(p, pl);
+  return cudaGetLastError();
+}
+
 template <typename TS, typename TB>
 cudaError_t backward_typed(const NormParams &p, int num_sms, cudaStream_t st) {
   const NormBwdPlan pl = norm_bwd_plan(p, num_sms);
   const int threads = pl.threads * pl.groups;
-  const bool v = all_wide(p);
-  if (threads <= 512) {
-    if (v) block_norm_backward_kernel<TS, TB, true, 512><<<pl.ctas, threads, 0, st>>>(p, pl);
-    else block_norm_backward_kernel<TS, TB, false, 512><<<pl.ctas, threads, 0, st>>>(p, pl);
-  } else {
-    if (v) block_norm_backward_kernel<TS, TB, true, 1024><<<pl.ctas, threads, 0, st>>>(p, pl);
-    else block_norm_backward_kernel<TS, TB, false, 1024><<<pl.ctas, threads, 0, st>>>(p, pl);
-  }
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e;
+  if (all_wide(p)) e = threads <= 512 ? backward_launch<TS, TB, true, 512>(p, pl, st) : backward_launch<TS, TB, true, 1024>(p, pl, st);
+  else e = threads <= 512 ? backward_launch<TS, TB, false, 512>(p, pl, st) : backward_launch<TS, TB, false, 1024>(p, pl, st);
   if (e != cudaSuccess || pl.floats == 0) return e;
   const int jobs = 2 + (pl.floats > pl.gate_part ? pl.chunks / pl.chunks_per_gate : 0);
   const dim3 grid((p.hidden + 31) / 32, jobs < 1024 ? jobs : 1024);

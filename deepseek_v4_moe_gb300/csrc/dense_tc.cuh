@@ -59,8 +59,11 @@ __device__ __forceinline__ uint32_t in_cta(const void *p, uint32_t rank) {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
+// Arrives at a barrier of another CTA.  What it orders are TMEM loads, by the tcgen05 fences around it;
+// a release at cluster scope would first wait for every memory access in flight, 1.5 us of the round
+// trip of a TMEM buffer.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 __device__ __forceinline__ int ld_cluster_s32(uint32_t addr) {
   int v;

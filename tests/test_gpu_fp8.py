@@ -5,8 +5,8 @@ in 4 steps of 32, each off by at most 2^-23 of the magnitudes' sum for the runni
 products' alignment; the scales' product and the f32 multiply-adds over the blocks add 2^-24 of it each.  So
 the sum over KB blocks is off by at most (8 + 8 + KB) 2^-23 M, M the sum of the magnitudes of all terms, and
 the stored value by half a step of its type more.  fp8_quantise: the scale is one correctly rounded division
-(2^-24); a code is the nearest to x / scale, and x / scale is itself rounded once in f32 (2^-24): away from
-the border between two codes by that much, the code is the nearest one."""
+(2^-24); a code is the nearest to x * (1 / scale), whose reciprocal and product are rounded in f32 (2^-24
+each): away from the border between two codes by 2^-23, the code is the one nearest to x / scale."""
 import pytest
 import torch
 
