@@ -14,11 +14,13 @@
 // All arithmetic is in f32; a value is rounded once, where it is stored.  The norm of s takes s as
 // stored, so that the backward pass, which reads s, differentiates what the forward pass computed.
 //
-// Both kernels are bound by memory: each row is read once into registers and written once.  A
-// group of n threads (a power of two, one thread for each 8 columns) holds a row; a reduction over
-// the row is a warp butterfly and one exchange through shared memory.  The backward pass sums the
-// weights' gradients over its rows in registers, writes one partial row for each group, and a
-// second kernel adds the partial rows in a fixed order: no atomics, the same bits every run.
+// Both kernels move each row once.  A group of n threads (a power of two, one thread for each two sets
+// of 8 columns) holds a row; a reduction over the row is a warp butterfly and one exchange through
+// shared memory.  What bounds them then is instructions and the barriers of the reductions, so a row
+// takes few threads and several CTAs share an SM: one CTA of 512 threads for a row of 4096 took 114 us
+// for the backward pass of 4096 rows, whatever it had in flight.  The backward pass sums the weights'
+// gradients over its rows in registers, writes one partial row for each group, and a second kernel adds
+// the partial rows in a fixed order: no atomics, the same bits every run.
 #include <string.h>
 
 #include "dense.h"
@@ -50,33 +52,47 @@ __device__ __forceinline__ void group_sums(float (&v)[K], int n, float *buf, int
     for (int k = 0; k < K; ++k) b[warp * K + k] = v[k];
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    v[k] = lane < per ? b[(first + lane) * K + k] : 0.f;
+  for (int k = 0; k < K; ++k) v[k] = b[(first + (lane & (per - 1))) * K + k];
+  for (int o = per >> 1; o > 0; o >>= 1)
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-  }
+    for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
 }
 
-// the gate's eight values for a row: its vector, or one value for the whole row
+// Set v of a thread's columns: columns 8 (v n + t) .. + 7, or (not VEC) v 8 n + t, + n, + 2n, ...: the
+// thread's place among the n kSets that Eight takes.
+constexpr int kSets = 2;
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void load_set(const T *row, int v, int t, int n, int hidden, float (&o)[8]) {
+  if constexpr (VEC) load_eight<T, true>(row, v * n + t, n, hidden, o);
+  else load_eight<T, false>(row + v * 8 * n, t, n, hidden - v * 8 * n, o);
+}
+template <typename T, bool VEC>
+__device__ __forceinline__ void store_set(T *row, int v, int t, int n, int hidden, const float (&o)[8]) {
+  if constexpr (VEC) Eight<T, true>::store(row, v * n + t, n, hidden, o);
+  else Eight<T, false>::store(row + v * 8 * n, t, n, hidden - v * 8 * n, o);
+}
+
+// the gate's values for a set of a row: its vector's, or one value for the whole row
 template <typename TB, bool VEC>
-__device__ __forceinline__ void gate_eight(const NormParams &p, int row, int t, int n, float (&g)[8]) {
+__device__ __forceinline__ void gate_set(const NormParams &p, int row, int v, int t, int n, float (&g)[8]) {
   if (p.gate_kind == kGateVector) {
     const size_t at = (size_t)(row / p.rows_per_gate) * p.hidden;
     if (p.gate_type == kF32)
-      load_eight<float, VEC>(static_cast<const float *>(p.gate) + at, t, n, p.hidden, g);
+      load_set<float, VEC>(static_cast<const float *>(p.gate) + at, v, t, n, p.hidden, g);
     else
-      load_eight<TB, VEC>(static_cast<const TB *>(p.gate) + at, t, n, p.hidden, g);
+      load_set<TB, VEC>(static_cast<const TB *>(p.gate) + at, v, t, n, p.hidden, g);
   } else {
-    float v = 1.f;
+    float x = 1.f;
     if (p.gate_kind == kGateToken)
-      v = p.gate_type == kF32 ? static_cast<const float *>(p.gate)[row] : to_f32(static_cast<const TB *>(p.gate)[row]);
+      x = p.gate_type == kF32 ? static_cast<const float *>(p.gate)[row] : to_f32(static_cast<const TB *>(p.gate)[row]);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) g[e] = v;
+    for (int e = 0; e < 8; ++e) g[e] = x;
   }
 }
 
 template <typename TS, typename TB, bool VEC>
-__global__ void __launch_bounds__(1024) block_norm_kernel(const __grid_constant__ NormParams p, int n) {
+__global__ void __launch_bounds__(512) block_norm_kernel(const __grid_constant__ NormParams p, int n) {
   __shared__ float buf[2 * kSumBuf];
   const int t = threadIdx.x & (n - 1), group = threadIdx.x / n, groups = blockDim.x / n;
   const float inv = 1.f / (float)p.hidden;
@@ -85,248 +101,305 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const __grid_constant_
   for (int base = blockIdx.x * groups; base < p.rows; base += step) {
     const int row = base + group;
     const bool in = row < p.rows;
-    float s[8];
+    const size_t r = in ? row : 0;  // a group without a row reads the first one and stores nothing
+    float s[kSets][8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s[e] = 0.f;
-    if (in) load_eight<TS, VEC>(static_cast<const TS *>(p.state) + row * p.ld_state, t, n, p.hidden, s);
+    for (int v = 0; v < kSets; ++v)
+      load_set<TS, VEC>(static_cast<const TS *>(p.state) + r * p.ld_state, v, t, n, p.hidden, s[v]);
     if (p.f) {
-      float f[8], g[8];
+      float f[kSets][8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = g[e] = 0.f;
-      if (in) {
-        load_eight<TB, VEC>(static_cast<const TB *>(p.f) + row * p.ld_f, t, n, p.hidden, f);
-        gate_eight<TB, VEC>(p, row, t, n, g);
-      }
+      for (int v = 0; v < kSets; ++v)
+        load_set<TB, VEC>(static_cast<const TB *>(p.f) + r * p.ld_f, v, t, n, p.hidden, f[v]);
+      float scale = p.scale;
       if (p.w_post) {
-        float w[8], ss[1] = {0.f};
-        load_eight<float, VEC>(p.w_post, t, n, p.hidden, w);
+        float ss[1] = {0.f};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss[0] = fmaf(f[e], f[e], ss[0]);
+        for (int v = 0; v < kSets; ++v)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) ss[0] = fmaf(f[v][e], f[v][e], ss[0]);
         group_sums(ss, n, buf, turn);
-        const float r = rsqrtf(fmaf(ss[0], inv, p.eps));
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] *= r * w[e];
+        scale *= rsqrtf(fmaf(ss[0], inv, p.eps));
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s[e] = to_f32(from_f32<TS>(fmaf(p.scale * g[e], f[e], s[e])));
-      if (in) Eight<TS, VEC>::store(static_cast<TS *>(p.out) + row * p.ld_out, t, n, p.hidden, s);
+      for (int v = 0; v < kSets; ++v) {
+        float w[8];
+        gate_set<TB, VEC>(p, (int)r, v, t, n, w);
+        if (p.w_post) {
+          float wp[8];
+          load_set<float, VEC>(p.w_post, v, t, n, p.hidden, wp);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) w[e] *= wp[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[v][e] = to_f32(from_f32<TS>(fmaf(scale * w[e], f[v][e], s[v][e])));
+        if (in) store_set<TS, VEC>(static_cast<TS *>(p.out) + r * p.ld_out, v, t, n, p.hidden, s[v]);
+      }
     }
     if (p.w_next) {
-      float w[8], ss[1] = {0.f};
-      load_eight<float, VEC>(p.w_next, t, n, p.hidden, w);
+      float ss[1] = {0.f};
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss[0] = fmaf(s[e], s[e], ss[0]);
+      for (int v = 0; v < kSets; ++v)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss[0] = fmaf(s[v][e], s[v][e], ss[0]);
       group_sums(ss, n, buf, turn);
-      const float r = rsqrtf(fmaf(ss[0], inv, p.eps));
+      const float rs = rsqrtf(fmaf(ss[0], inv, p.eps));
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s[e] *= r * w[e];
-      if (in) Eight<TB, VEC>::store(static_cast<TB *>(p.y) + row * p.ld_y, t, n, p.hidden, s);
+      for (int v = 0; v < kSets; ++v) {
+        float w[8];
+        load_set<float, VEC>(p.w_next, v, t, n, p.hidden, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] *= s[v][e] * rs;
+        if (in) store_set<TB, VEC>(static_cast<TB *>(p.y) + r * p.ld_y, v, t, n, p.hidden, w);
+      }
     }
   }
 }
 
-// writes a gate row's gradient in the gate's type
+// writes a set of a gate row's gradient in the gate's type
 template <typename TB, bool VEC>
-__device__ __forceinline__ void store_gate(const NormParams &p, size_t at, int t, int n, const float (&v)[8]) {
+__device__ __forceinline__ void store_gate(const NormParams &p, size_t at, int v, int t, int n, const float (&g)[8]) {
   if (p.gate_type == kF32)
-    Eight<float, VEC>::store(static_cast<float *>(p.d_gate) + at, t, n, p.hidden, v);
+    store_set<float, VEC>(static_cast<float *>(p.d_gate) + at, v, t, n, p.hidden, g);
   else
-    Eight<TB, VEC>::store(static_cast<TB *>(p.d_gate) + at, t, n, p.hidden, v);
+    store_set<TB, VEC>(static_cast<TB *>(p.d_gate) + at, v, t, n, p.hidden, g);
 }
 
-// A worker's place in its rows: row i of the lap-th of its chunks.
+// A worker's place in its rows: row `first + i` of its lap-th chunk, while that is below `end` (the last
+// chunk of a gate row may be shorter, and a worker's last lap may have none).
 struct Place {
-  int lap = 0, i = 0;
-  __device__ __forceinline__ void next(const NormBwdPlan &pl) {
-    if (++i == pl.chunk_rows) {
-      i = 0;
-      ++lap;
-    }
+  int lap, i, first, end, gate_row;
+  __device__ __forceinline__ void enter(const NormParams &p, const NormBwdPlan &pl, int worker, int lap_) {
+    lap = lap_;
+    i = 0;
+    const int c = lap * pl.workers + worker;
+    gate_row = c / pl.chunks_per_gate;
+    first = gate_row * p.rows_per_gate + (c - gate_row * pl.chunks_per_gate) * pl.chunk_rows;
+    end = c < pl.chunks ? min((gate_row + 1) * p.rows_per_gate, p.rows) : 0;
   }
-  __device__ __forceinline__ int chunk(const NormBwdPlan &pl, int worker) const { return lap * pl.workers + worker; }
-  // the row, or -1 where the chunk (the last of a gate row may be shorter) has none
-  __device__ __forceinline__ int row(const NormParams &p, const NormBwdPlan &pl, int worker) const {
-    const int c = chunk(pl, worker);
-    if (c >= pl.chunks) return -1;
-    const int gate_row = c / pl.chunks_per_gate;
-    const int r = gate_row * p.rows_per_gate + (c % pl.chunks_per_gate) * pl.chunk_rows + i;
-    return r < min((gate_row + 1) * p.rows_per_gate, p.rows) ? r : -1;
+  __device__ __forceinline__ void next(const NormParams &p, const NormBwdPlan &pl, int worker) {
+    if (++i == pl.chunk_rows) enter(p, pl, worker, lap + 1);
   }
+  __device__ __forceinline__ int row() const { return first + i < end ? first + i : -1; }
 };
 
-// Rows on their way: each thread copies its own columns of the next DEPTH - 1 rows into its own places in
-// shared memory (cp.async) and reads them back itself, so no barrier guards the ring.
-template <typename TS, typename TB, int DEPTH>
-struct RowRing {
-  static constexpr int kS = sizeof(TS) / 2, kB = sizeof(TB) / 2;  // 16-byte pieces of eight values
-  static constexpr int kPieces = 2 * kS + 2 * kB;                 // state, d_out, d_y, f: sizeof(TS) + sizeof(TB)
+// The rows that the backward pass reads.  VEC: each thread copies its own columns of the next DEPTH - 1
+// rows into its own places in shared memory (cp.async) and reads them back itself, as often as it needs
+// them, so no barrier guards the ring and few of a row's values have to stay in registers.  Otherwise
+// the values are read from memory each time (the second time from the caches).
+template <typename TS, typename TB, bool VEC, int DEPTH>
+struct Rows {
+  static constexpr int kS = sizeof(TS) / 2, kB = sizeof(TB) / 2;  // 16-byte pieces of a set
+  static constexpr int kState = 0, kDOut = kS, kDY = 2 * kS, kF = 2 * kS + kB, kPieces = 2 * kS + 2 * kB;
   uint32_t base;  // this thread's first piece; pieces lie blockDim.x * 16 bytes apart
-  __device__ __forceinline__ uint32_t at(int stage, int piece) const {
-    return base + (uint32_t)(stage * kPieces + piece) * blockDim.x * 16u;
+  int t, n, stage, row;
+  __device__ __forceinline__ uint32_t at(int st, int v, int piece) const {
+    return base + (uint32_t)((st * kSets + v) * kPieces + piece) * blockDim.x * 16u;
   }
   template <typename T>
-  __device__ __forceinline__ void copy(int stage, int piece, const T *src) const {
+  __device__ __forceinline__ void copy(int st, int v, int piece, const T *src) const {
 #pragma unroll
     for (int k = 0; k < (int)sizeof(T) / 2; ++k)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at(stage, piece + k)), "l"(src + k * (16 / sizeof(T)))
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at(st, v, piece + k)), "l"(src + k * (16 / sizeof(T)))
                    : "memory");
   }
-  template <typename T>
-  __device__ __forceinline__ void get(int stage, int piece, float (&v)[8]) const {
-    Eight<T, true> e;
-    uint4 w[sizeof(T) / 2];
+  __device__ __forceinline__ void fetch(const NormParams &p, int st, int r) const {
+    if (r >= 0)
 #pragma unroll
-    for (int k = 0; k < (int)sizeof(T) / 2; ++k)
-      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(w[k].x), "=r"(w[k].y), "=r"(w[k].z), "=r"(w[k].w)
-                   : "r"(at(stage, piece + k))
-                   : "memory");
-    memcpy(&e, w, sizeof e);
-    e.get(v);
-  }
-  __device__ __forceinline__ void fetch(const NormParams &p, int stage, int row, int t) const {
-    if (row >= 0 && 8 * t < p.hidden) {
-      if (p.w_next) copy(stage, 0, static_cast<const TS *>(p.state) + row * p.ld_state + 8 * t);
-      if (p.d_out) copy(stage, kS, static_cast<const TS *>(p.d_out) + row * p.ld_d_out + 8 * t);
-      if (p.w_next) copy(stage, 2 * kS, static_cast<const TB *>(p.d_y) + row * p.ld_d_y + 8 * t);
-      if (p.f) copy(stage, 2 * kS + kB, static_cast<const TB *>(p.f) + row * p.ld_f + 8 * t);
-    }
+      for (int v = 0; v < kSets; ++v) {
+        const int col = 8 * (v * n + t);
+        if (col < p.hidden) {
+          if (p.w_next) copy(st, v, kState, static_cast<const TS *>(p.state) + r * p.ld_state + col);
+          if (p.d_out) copy(st, v, kDOut, static_cast<const TS *>(p.d_out) + r * p.ld_d_out + col);
+          if (p.w_next) copy(st, v, kDY, static_cast<const TB *>(p.d_y) + r * p.ld_d_y + col);
+          if (p.f) copy(st, v, kF, static_cast<const TB *>(p.f) + r * p.ld_f + col);
+        }
+      }
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
+  // set v of the row at work; zeros past the row's end
+  template <typename T, int PIECE>
+  __device__ __forceinline__ void get(const NormParams &p, const void *src, long long ld, int v, float (&o)[8]) const {
+    if constexpr (VEC) {
+      if (8 * (v * n + t) < p.hidden) {
+        Eight<T, true> e;
+        uint4 w[sizeof(T) / 2];
+#pragma unroll
+        for (int k = 0; k < (int)sizeof(T) / 2; ++k)
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(w[k].x), "=r"(w[k].y), "=r"(w[k].z), "=r"(w[k].w)
+                       : "r"(at(stage, v, PIECE + k))
+                       : "memory");
+        memcpy(&e, w, sizeof e);
+        e.get(o);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = 0.f;
+      }
+    } else {
+      load_set<T, false>(static_cast<const T *>(src) + row * ld, v, t, n, p.hidden, o);
+    }
+  }
 };
 
-// Rows in flight in the ring: three, or what a CTA's shared memory holds at 1024 threads; 0: no ring.
-template <typename TS, typename TB, int MAXT>
-constexpr int kRingFit = 220 * 1024 / (MAXT * 16 * (int)(sizeof(TS) + sizeof(TB)));
-template <typename TS, typename TB, bool VEC, int MAXT>
-constexpr int kRingDepth = !VEC ? 0 : kRingFit<TS, TB, MAXT> < 3 ? kRingFit<TS, TB, MAXT> : 3;
+// Rows of the ring: what lets two CTAs of up to 256 threads, or one of 512, stay on an SM; 0: no ring.
+template <typename TS, typename TB>
+constexpr int kRingFit = 208 * 1024 / (512 * 16 * kSets * (int)(sizeof(TS) + sizeof(TB)));
+template <typename TS, typename TB, bool VEC>
+constexpr int kRingDepth = !VEC ? 0 : kRingFit<TS, TB> < 3 ? kRingFit<TS, TB> : 3;
 
-template <typename TS, typename TB, bool VEC, int MAXT>
-__global__ void __launch_bounds__(MAXT)
+template <typename TS, typename TB, bool VEC>
+__global__ void __launch_bounds__(512)
     block_norm_backward_kernel(const __grid_constant__ NormParams p, const __grid_constant__ NormBwdPlan pl) {
-  constexpr int DEPTH = kRingDepth<TS, TB, VEC, MAXT>;
+  constexpr int DEPTH = kRingDepth<TS, TB, VEC>;
+  using R = Rows<TS, TB, VEC, DEPTH>;
   __shared__ float buf[2 * kSumBuf];
   extern __shared__ uint4 ring_smem[];
-  RowRing<TS, TB, DEPTH> ring;
-  ring.base = smem_u32(ring_smem + threadIdx.x);
   const int n = pl.threads, t = threadIdx.x & (n - 1), group = threadIdx.x / n;
   const int worker = blockIdx.x * pl.groups + group;
+  R rows;
+  rows.base = smem_u32(ring_smem + threadIdx.x);
+  rows.t = t;
+  rows.n = n;
+  rows.stage = 0;
   const float inv = 1.f / (float)p.hidden;
-  const bool there = VEC ? 8 * t < p.hidden : true;
+  const bool gates = p.gate_kind == kGateVector && p.d_gate, token = p.gate_kind == kGateToken && p.d_gate;
   int turn = 0;
-  float a_next[8], a_post[8], a_gate[8];
+  float a_next[kSets][8], a_post[kSets][8], a_gate[kSets][8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) a_next[e] = a_post[e] = a_gate[e] = 0.f;
+  for (int v = 0; v < kSets; ++v)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) a_next[v][e] = a_post[v][e] = a_gate[v][e] = 0.f;
   // the same number of steps for every thread of the grid: the reductions are CTA-wide
   const int steps = (pl.chunks + pl.workers - 1) / pl.workers * pl.chunk_rows;
   Place here, ahead;
+  here.enter(p, pl, worker, 0);
+  ahead.enter(p, pl, worker, 0);
   if constexpr (VEC)
-    for (int s = 0; s < DEPTH - 1; ++s, ahead.next(pl)) ring.fetch(p, s, s < steps ? ahead.row(p, pl, worker) : -1, t);
-  int stage = 0;
-  for (int step = 0; step < steps; ++step, here.next(pl)) {
-    const int row = here.row(p, pl, worker);
+    for (int s = 0; s < DEPTH - 1; ++s, ahead.next(p, pl, worker)) rows.fetch(p, s, s < steps ? ahead.row() : -1);
+#pragma unroll 1
+  for (int step = 0; step < steps; ++step) {
+    const int row = here.row();
     const bool in = row >= 0;
-    float ds[8], s[8], gy[8], f[8], g[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) ds[e] = s[e] = gy[e] = f[e] = g[e] = 0.f;
     if constexpr (VEC) {
-      const int put = stage == 0 ? DEPTH - 1 : stage - 1;  // the stage that the step before freed
-      ring.fetch(p, put, step + DEPTH - 1 < steps ? ahead.row(p, pl, worker) : -1, t);
-      ahead.next(pl);
-      if (in && p.f) gate_eight<TB, VEC>(p, row, t, n, g);
-      asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
-      if (in && there) {
-        if (p.d_out) ring.template get<TS>(stage, ring.kS, ds);
-        if (p.w_next) {
-          ring.template get<TS>(stage, 0, s);
-          ring.template get<TB>(stage, 2 * ring.kS, gy);
-        }
-        if (p.f) ring.template get<TB>(stage, 2 * ring.kS + ring.kB, f);
-      }
-      stage = stage + 1 == DEPTH ? 0 : stage + 1;
-    } else if (in) {
-      if (p.d_out) load_eight<TS, VEC>(static_cast<const TS *>(p.d_out) + row * p.ld_d_out, t, n, p.hidden, ds);
+      // into the stage that the step before freed
+      rows.fetch(p, rows.stage == 0 ? DEPTH - 1 : rows.stage - 1, step + DEPTH - 1 < steps ? ahead.row() : -1);
+      ahead.next(p, pl, worker);
+      asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH > 0 ? DEPTH - 1 : 0) : "memory");
+    } else {
+      rows.row = in ? row : 0;
+    }
+    // A group without a row this time works on what it finds and keeps nothing of it: its sums are its
+    // own.
+    float sums[3] = {0.f, 0.f, 0.f};
+#pragma unroll
+    for (int v = 0; v < kSets; ++v) {
       if (p.w_next) {
-        load_eight<TS, VEC>(static_cast<const TS *>(p.state) + row * p.ld_state, t, n, p.hidden, s);
-        load_eight<TB, VEC>(static_cast<const TB *>(p.d_y) + row * p.ld_d_y, t, n, p.hidden, gy);
+        float s[8], gy[8], w[8];
+        rows.template get<TS, R::kState>(p, p.state, p.ld_state, v, s);
+        rows.template get<TB, R::kDY>(p, p.d_y, p.ld_d_y, v, gy);
+        load_set<float, VEC>(p.w_next, v, t, n, p.hidden, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          sums[0] = fmaf(s[e], s[e], sums[0]);
+          sums[1] = fmaf(w[e] * gy[e], s[e], sums[1]);
+        }
       }
-      if (p.f) {
-        load_eight<TB, VEC>(static_cast<const TB *>(p.f) + row * p.ld_f, t, n, p.hidden, f);
-        gate_eight<TB, VEC>(p, row, t, n, g);
+      if (p.w_post) {
+        float f[8];
+        rows.template get<TB, R::kF>(p, p.f, p.ld_f, v, f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sums[2] = fmaf(f[e], f[e], sums[2]);
       }
     }
-    float w[8], sums[3] = {0.f, 0.f, 0.f};
-    if (p.w_next) load_eight<float, VEC>(p.w_next, t, n, p.hidden, w);
-    else
-#pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] = 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      w[e] *= gy[e];
-      sums[0] = fmaf(s[e], s[e], sums[0]);
-      sums[1] = fmaf(w[e], s[e], sums[1]);
-      sums[2] = fmaf(f[e], f[e], sums[2]);
-    }
-    group_sums(sums, n, buf, turn);
+    if (p.w_next || p.w_post) group_sums(sums, n, buf, turn);
+    const float rs = rsqrtf(fmaf(sums[0], inv, p.eps)), cs = rs * rs * (sums[1] * inv);
     const float rf = p.w_post ? rsqrtf(fmaf(sums[2], inv, p.eps)) : 1.f;
-    if (p.w_next) {
-      const float rs = rsqrtf(fmaf(sums[0], inv, p.eps)), c = rs * rs * (sums[1] * inv);
+    float two[2] = {0.f, 0.f};
+    float dn[kSets][8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        a_next[e] = fmaf(gy[e], s[e] * rs, a_next[e]);
-        ds[e] = fmaf(rs, fmaf(-s[e], c, w[e]), ds[e]);
-      }
-    }
-    if (in) Eight<TS, VEC>::store(static_cast<TS *>(p.d_state) + row * p.ld_d_state, t, n, p.hidden, ds);
-    if (p.f) {
-      if (p.w_post) load_eight<float, VEC>(p.w_post, t, n, p.hidden, w);
+    for (int v = 0; v < kSets; ++v) {
+      float ds[8];
+      if (p.d_out) rows.template get<TS, R::kDOut>(p, p.d_out, p.ld_d_out, v, ds);
       else
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = 1.f;
-      float two[2] = {0.f, 0.f};
+        for (int e = 0; e < 8; ++e) ds[e] = 0.f;
+      if (p.w_next) {
+        float s[8], gy[8], w[8];
+        rows.template get<TS, R::kState>(p, p.state, p.ld_state, v, s);
+        rows.template get<TB, R::kDY>(p, p.d_y, p.ld_d_y, v, gy);
+        load_set<float, VEC>(p.w_next, v, t, n, p.hidden, w);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float nh = f[e] * rf;                // the normalised branch without its weight
-        const float sd = p.scale * ds[e];
-        const float gn = sd * nh * w[e];           // the gate's gradient
-        const float dn = sd * g[e];
-        a_gate[e] += gn;
-        a_post[e] = fmaf(dn, nh, a_post[e]);
-        g[e] = dn * w[e];
-        two[0] = fmaf(g[e], f[e], two[0]);
-        two[1] += gn;
+        for (int e = 0; e < 8; ++e) {
+          if (in) a_next[v][e] = fmaf(gy[e], s[e] * rs, a_next[v][e]);
+          ds[e] = fmaf(rs, fmaf(-s[e], cs, w[e] * gy[e]), ds[e]);
+        }
       }
-      if (p.w_post || (p.gate_kind == kGateToken && p.d_gate)) group_sums(two, n, buf, turn);
-      if (p.w_post) {
-        const float c = rf * rf * (two[0] * inv);
+      if (in) store_set<TS, VEC>(static_cast<TS *>(p.d_state) + row * p.ld_d_state, v, t, n, p.hidden, ds);
+      if (p.f) {
+        float f[8], g[8], w[8];
+        rows.template get<TB, R::kF>(p, p.f, p.ld_f, v, f);
+        gate_set<TB, VEC>(p, in ? row : 0, v, t, n, g);
+        if (p.w_post) load_set<float, VEC>(p.w_post, v, t, n, p.hidden, w);
+        else
 #pragma unroll
-        for (int e = 0; e < 8; ++e) g[e] = rf * fmaf(-f[e], c, g[e]);
-      }
-      if (in) {
-        Eight<TB, VEC>::store(static_cast<TB *>(p.d_f) + row * p.ld_d_f, t, n, p.hidden, g);
-        if (p.gate_kind == kGateToken && p.d_gate && t == 0) {
-          if (p.gate_type == kF32)
-            static_cast<float *>(p.d_gate)[row] = two[1];
-          else
-            static_cast<TB *>(p.d_gate)[row] = from_f32<TB>(two[1]);
+          for (int e = 0; e < 8; ++e) w[e] = 1.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float sd = p.scale * ds[e], nh = f[e] * rf;  // nh: the normalised branch without its weight
+          const float gn = sd * nh * w[e], d = sd * g[e];    // the gate's gradient, and the branch's
+          if (in) {
+            a_gate[v][e] += gn;
+            a_post[v][e] = fmaf(d, nh, a_post[v][e]);
+          }
+          dn[v][e] = d * w[e];
+          two[0] = fmaf(dn[v][e], f[e], two[0]);
+          two[1] += gn;
         }
       }
     }
-    if (here.i == pl.chunk_rows - 1) {  // the chunk's part of the gate's gradient is complete
-      const int chunk = here.chunk(pl, worker);
-      if (p.gate_kind == kGateVector && p.d_gate && chunk < pl.chunks) {
-        if (pl.chunks_per_gate == 1)
-          store_gate<TB, VEC>(p, (size_t)(chunk / pl.chunks_per_gate) * p.hidden, t, n, a_gate);
-        else
-          Eight<float, VEC>::store(p.part + pl.gate_part + (size_t)chunk * p.hidden, t, n, p.hidden, a_gate);
-      }
+    if (p.f) {
+      if (p.w_post || token) group_sums(two, n, buf, turn);
+      const float cf = p.w_post ? rf * rf * (two[0] * inv) : 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) a_gate[e] = 0.f;
+      for (int v = 0; v < kSets; ++v) {
+        float f[8];
+        rows.template get<TB, R::kF>(p, p.f, p.ld_f, v, f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = p.w_post ? rf * fmaf(-f[e], cf, dn[v][e]) : dn[v][e];
+        if (in) store_set<TB, VEC>(static_cast<TB *>(p.d_f) + row * p.ld_d_f, v, t, n, p.hidden, f);
+      }
+      if (in && token && t == 0) {
+        if (p.gate_type == kF32)
+          static_cast<float *>(p.d_gate)[row] = two[1];
+        else
+          static_cast<TB *>(p.d_gate)[row] = from_f32<TB>(two[1]);
+      }
     }
+    if (gates && here.i == pl.chunk_rows - 1) {  // the chunk's part of the gate's gradient is complete
+      const int chunk = here.lap * pl.workers + worker;
+#pragma unroll
+      for (int v = 0; v < kSets; ++v) {
+        if (chunk < pl.chunks) {
+          if (pl.chunks_per_gate == 1)
+            store_gate<TB, VEC>(p, (size_t)here.gate_row * p.hidden, v, t, n, a_gate[v]);
+          else
+            store_set<float, VEC>(p.part + pl.gate_part + (size_t)chunk * p.hidden, v, t, n, p.hidden, a_gate[v]);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a_gate[v][e] = 0.f;
+      }
+    }
+    here.next(p, pl, worker);
+    rows.stage = rows.stage + 1 >= DEPTH ? 0 : rows.stage + 1;
   }
-  if (p.d_w_next) Eight<float, VEC>::store(p.part + (size_t)worker * p.hidden, t, n, p.hidden, a_next);
-  if (p.d_w_post)
-    Eight<float, VEC>::store(p.part + ((size_t)(p.d_w_next ? pl.workers : 0) + worker) * p.hidden, t, n, p.hidden, a_post);
+#pragma unroll
+  for (int v = 0; v < kSets; ++v) {
+    if (p.d_w_next) store_set<float, VEC>(p.part + (size_t)worker * p.hidden, v, t, n, p.hidden, a_next[v]);
+    if (p.d_w_post)
+      store_set<float, VEC>(p.part + ((size_t)(p.d_w_next ? pl.workers : 0) + worker) * p.hidden, v, t, n, p.hidden,
+                            a_post[v]);
+  }
 }
 
 // Adds the partial rows: job 0 and 1 the norm weights' over the workers, job 2 + i gate row i's over
@@ -366,8 +439,8 @@ __global__ void __launch_bounds__(1024)
 
 int group_threads(int hidden) {
   int n = 32;
-  while (n * 8 < hidden) n *= 2;
-  return n;
+  while (n * 8 * kSets < hidden) n *= 2;
+  return n;  // at most 512: kNormHiddenMax
 }
 
 size_t type_bytes(int t) { return t == kF32 ? 4 : 2; }
@@ -390,7 +463,7 @@ bool all_wide(const NormParams &p) {
 template <typename TS, typename TB>
 cudaError_t forward_typed(const NormParams &p, int num_sms, cudaStream_t st) {
   const int n = group_threads(p.hidden), threads = n < 256 ? 256 : n, groups = threads / n;
-  const int blocks = (p.rows + groups - 1) / groups, most = num_sms * (2048 / threads);
+  const int blocks = (p.rows + groups - 1) / groups, most = num_sms * (1024 / threads);
   const int grid = blocks < most ? blocks : most;
   if (all_wide(p))
     block_norm_kernel<TS, TB, true><<<grid, threads, 0, st>>>(p, n);
@@ -399,25 +472,21 @@ cudaError_t forward_typed(const NormParams &p, int num_sms, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-template <typename TS, typename TB, bool VEC, int MAXT>
+template <typename TS, typename TB, bool VEC>
 cudaError_t backward_launch(const NormParams &p, const NormBwdPlan &pl, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
   const int threads = pl.threads * pl.groups;
-  const size_t per_thread = (size_t)kRingDepth<TS, TB, VEC, MAXT> * (sizeof(TS) + sizeof(TB)) * 16;
-  const cudaError_t e =
-      allow_smem((const void *)block_norm_backward_kernel<TS, TB, VEC, MAXT>, per_thread * MAXT, done);
+  const size_t per_thread = (size_t)kRingDepth<TS, TB, VEC> * kSets * (sizeof(TS) + sizeof(TB)) * 16;
+  const cudaError_t e = allow_smem((const void *)block_norm_backward_kernel<TS, TB, VEC>, per_thread * 512, done);
   if (e != cudaSuccess) return e;
-  block_norm_backward_kernel<TS, TB, VEC, MAXT><<<pl.ctas, threads, per_thread * threads, st>>>(p, pl);
+  block_norm_backward_kernel<TS, TB, VEC><<<pl.ctas, threads, per_thread * threads, st>>>(p, pl);
   return cudaGetLastError();
 }
 
 template <typename TS, typename TB>
 cudaError_t backward_typed(const NormParams &p, int num_sms, cudaStream_t st) {
   const NormBwdPlan pl = norm_bwd_plan(p, num_sms);
-  const int threads = pl.threads * pl.groups;
-  cudaError_t e;
-  if (all_wide(p)) e = threads <= 512 ? backward_launch<TS, TB, true, 512>(p, pl, st) : backward_launch<TS, TB, true, 1024>(p, pl, st);
-  else e = threads <= 512 ? backward_launch<TS, TB, false, 512>(p, pl, st) : backward_launch<TS, TB, false, 1024>(p, pl, st);
+  const cudaError_t e = all_wide(p) ? backward_launch<TS, TB, true>(p, pl, st) : backward_launch<TS, TB, false>(p, pl, st);
   if (e != cudaSuccess || pl.floats == 0) return e;
   const int jobs = 2 + (pl.floats > pl.gate_part ? pl.chunks / pl.chunks_per_gate : 0);
   const dim3 grid((p.hidden + 31) / 32, jobs < 1024 ? jobs : 1024);
@@ -435,7 +504,7 @@ NormBwdPlan norm_bwd_plan(const NormParams &p, int num_sms) {
   const bool gates = p.f && p.gate_kind == kGateVector;
   const int per = gates ? p.rows_per_gate : p.rows;
   const int n_gates = (p.rows + per - 1) / per;
-  // one CTA of 512 threads or more for each SM, two of 256
+  // two CTAs of 256 threads for each SM, or one of 512
   const int most = num_sms * (threads <= 256 ? 2 : 1) * pl.groups;
   int chunk = (int)(((long long)n_gates * per + most - 1) / most);
   pl.chunk_rows = chunk < 1 ? 1 : chunk > per ? per : chunk;
