@@ -561,7 +561,7 @@ extern "C" int moe_ffn_fp8_quantise(const moe_ffn_fp8_quantise_args *a, void *st
   p.codes = static_cast<uint8_t *>(a->codes);
   p.ld_codes = a->ld_codes;
   p.scales = a->scales;
-  p.wide = a->k % 8 == 0 && aligned(a->x, 16) && a->ld_x * xb % 16 == 0 && aligned(a->codes, 8) && a->ld_codes % 8 == 0;
+  p.wide = a->k % 8 == 0 && aligned(a->x, 8 * xb) && a->ld_x % 8 == 0 && aligned(a->codes, 8) && a->ld_codes % 8 == 0;
   return launched(who, moe::launch_fp8_quantise(p, sms, static_cast<cudaStream_t>(stream)));
 }
 
@@ -627,8 +627,8 @@ extern "C" int moe_ffn_block_norm_backward(const moe_ffn_block_norm_args *a, con
   if (rc) return rc;
   const int sb = type_bytes(a->stream_type), bb = type_bytes(a->block_type), gb = type_bytes(a->gate_type);
   if (!aligned(g->d_out, sb) || !aligned(g->d_y, bb) || !aligned(g->d_state, sb) || !aligned(g->d_f, bb) ||
-      !aligned(g->d_gate, gb) || !aligned(g->d_norm_f, 4) || !aligned(g->d_norm_next, 4) || !aligned(g->workspace, 16))
-    return fail(MOE_FFN_ERR_ALIGNMENT, "%s: a pointer is not aligned to its type (workspace: 16 bytes)", who);
+      !aligned(g->d_gate, gb) || !aligned(g->d_norm_f, 4) || !aligned(g->d_norm_next, 4) || !aligned(g->workspace, 32))
+    return fail(MOE_FFN_ERR_ALIGNMENT, "%s: a pointer is not aligned to its type (workspace: 32 bytes)", who);
   const bool vec = a->gate_kind == MOE_FFN_GATE_VECTOR;
   const int64_t R = a->rows, H = a->hidden;
   Span ins[7], outs[6] = {span("d_state", g->d_state, R, H, g->ld_d_state, sb), span("d_f", g->d_f, R, H, g->ld_d_f, bb),

@@ -34,7 +34,9 @@ struct NormParams {
 // chunk_rows rows, none of which crosses a gate row.
 struct NormBwdPlan {
   int threads, groups, ctas, workers, chunk_rows, chunks_per_gate, chunks;
-  size_t gate_part, floats;  // offset of the gate's partials, and the workspace's size
+  int one_gate, jobs;          // a gate of one row, a chunk of it for each worker; sums over partial rows
+  int depth;                   // rows of the ring; set by the launch
+  size_t gate_part, floats;    // offset of the gate's partials, and the workspace's size
 };
 NormBwdPlan norm_bwd_plan(const NormParams &p, int num_sms);
 cudaError_t launch_block_norm(const NormParams &p, int num_sms, cudaStream_t st);

@@ -16,12 +16,20 @@
 //
 // Both kernels move each row once.  A group of n threads (a power of two, one thread for each two sets
 // of 8 columns) holds a row; a reduction over the row is a warp butterfly and one exchange through
-// shared memory.  What bounds them then is instructions and the barriers of the reductions, so a row
-// takes few threads and several CTAs share an SM: one CTA of 512 threads for a row of 4096 took 114 us
-// for the backward pass of 4096 rows, whatever it had in flight.  The backward pass sums the weights'
-// gradients over its rows in registers, writes one partial row for each group, and a second kernel adds
-// the partial rows in a fixed order: no atomics, the same bits every run.
+// shared memory, with a barrier of the group's own.
+//
+// The backward pass needs the mean of dn w_post f, which contains ds and with it the row's first sums.
+// It is linear in them: with q = gate w_post f and gw = d_y w_next,
+//   sum(q ds) = sum(q d_out) + r_s sum(q gw) - r_s^3 mean(gw s) sum(q s),
+// so that one reduction of six sums serves a row.  Its time is instructions and latency rather than
+// bytes: with two reductions, a CTA-wide barrier each and the weights read through the L1 that a large
+// ring leaves (28 KB), 4096 rows of 4096 took 103 to 124 us.  So the weights lie in shared memory beside
+// the ring, arithmetic is on pairs, and the groups of a CTA run on their own.  The weights' gradients are
+// summed over a group's rows in registers, one partial row for each group goes to memory, and a second
+// kernel adds the partial rows in a fixed order: no atomics, the same bits every run.
 #include <string.h>
+
+#include <type_traits>
 
 #include "dense.h"
 #include "dense_tc.cuh"
@@ -31,11 +39,9 @@
 namespace moe {
 namespace {
 
-// Sums v[0..K-1] over a group of n threads (n a power of two, >= 32), every thread getting the
-// sums.  `buf` holds two buffers of kSumBuf floats used in turn, so one barrier a call is enough: a
-// buffer is written again two calls later, with a barrier in between.  Every thread of the CTA must
-// call it.
-constexpr int kSumBuf = 32 * 3;
+// Sums v[0..K-1] over a group of n threads (n a power of two, >= 32), every thread getting the sums.
+// `buf` holds two buffers used in turn, so one barrier a call is enough: a buffer is written again two
+// calls later, with a barrier in between.  The group's threads call it together; no other group waits.
 template <int K>
 __device__ __forceinline__ void group_sums(float (&v)[K], int n, float *buf, int &turn) {
 #pragma unroll
@@ -44,13 +50,12 @@ __device__ __forceinline__ void group_sums(float (&v)[K], int n, float *buf, int
     for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
   if (n == 32) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, per = n >> 5, first = warp & ~(per - 1);
-  static_assert(32 * K <= kSumBuf, "sums of one call");
-  float *b = buf + turn * kSumBuf;
+  float *b = buf + turn * (16 * K);  // at most 16 warps
   turn ^= 1;
   if (lane == 0)
 #pragma unroll
     for (int k = 0; k < K; ++k) b[warp * K + k] = v[k];
-  __syncthreads();
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + threadIdx.x / n), "r"(n) : "memory");
 #pragma unroll
   for (int k = 0; k < K; ++k) v[k] = b[(first + (lane & (per - 1))) * K + k];
   for (int o = per >> 1; o > 0; o >>= 1)
@@ -58,42 +63,83 @@ __device__ __forceinline__ void group_sums(float (&v)[K], int n, float *buf, int
     for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
 }
 
+// Eight values as four pairs: the arithmetic below takes two values an instruction.
+struct Pairs {
+  float2 v[4];
+};
+__device__ __forceinline__ float2 pair(float x) { return make_float2(x, x); }
+__device__ __forceinline__ Pairs splat(float x) { return Pairs{{pair(x), pair(x), pair(x), pair(x)}}; }
+__device__ __forceinline__ Pairs mul(const Pairs &a, const Pairs &b) {
+  Pairs r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.v[i] = __fmul2_rn(a.v[i], b.v[i]);
+  return r;
+}
+__device__ __forceinline__ Pairs mul(const Pairs &a, float b) {
+  Pairs r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.v[i] = __fmul2_rn(a.v[i], pair(b));
+  return r;
+}
+// a * b + c
+__device__ __forceinline__ Pairs fma(const Pairs &a, const Pairs &b, const Pairs &c) {
+  Pairs r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.v[i] = __ffma2_rn(a.v[i], b.v[i], c.v[i]);
+  return r;
+}
+__device__ __forceinline__ Pairs fma(const Pairs &a, float b, const Pairs &c) {
+  Pairs r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.v[i] = __ffma2_rn(a.v[i], pair(b), c.v[i]);
+  return r;
+}
+// adds the products to a running pair of sums
+__device__ __forceinline__ void dot(const Pairs &a, const Pairs &b, float2 &sum) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) sum = __ffma2_rn(a.v[i], b.v[i], sum);
+}
+__device__ __forceinline__ void add(const Pairs &a, float2 &sum) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) sum = __fadd2_rn(a.v[i], sum);
+}
+__device__ __forceinline__ float (&flat(Pairs &p))[8] { return reinterpret_cast<float(&)[8]>(p); }
+__device__ __forceinline__ const float (&flat(const Pairs &p))[8] { return reinterpret_cast<const float(&)[8]>(p); }
+
 // Set v of a thread's columns: columns 8 (v n + t) .. + 7, or (not VEC) v 8 n + t, + n, + 2n, ...: the
 // thread's place among the n kSets that Eight takes.
 constexpr int kSets = 2;
 
 template <typename T, bool VEC>
-__device__ __forceinline__ void load_set(const T *row, int v, int t, int n, int hidden, float (&o)[8]) {
-  if constexpr (VEC) load_eight<T, true>(row, v * n + t, n, hidden, o);
-  else load_eight<T, false>(row + v * 8 * n, t, n, hidden - v * 8 * n, o);
+__device__ __forceinline__ Pairs load_set(const T *row, int v, int t, int n, int hidden) {
+  Pairs o;
+  if constexpr (VEC) load_eight<T, true>(row, v * n + t, n, hidden, flat(o));
+  else load_eight<T, false>(row + v * 8 * n, t, n, hidden - v * 8 * n, flat(o));
+  return o;
 }
 template <typename T, bool VEC>
-__device__ __forceinline__ void store_set(T *row, int v, int t, int n, int hidden, const float (&o)[8]) {
-  if constexpr (VEC) Eight<T, true>::store(row, v * n + t, n, hidden, o);
-  else Eight<T, false>::store(row + v * 8 * n, t, n, hidden - v * 8 * n, o);
+__device__ __forceinline__ void store_set(T *row, int v, int t, int n, int hidden, const Pairs &o) {
+  if constexpr (VEC) Eight<T, true>::store(row, v * n + t, n, hidden, flat(o));
+  else Eight<T, false>::store(row + v * 8 * n, t, n, hidden - v * 8 * n, flat(o));
 }
 
 // the gate's values for a set of a row: its vector's, or one value for the whole row
 template <typename TB, bool VEC>
-__device__ __forceinline__ void gate_set(const NormParams &p, int row, int v, int t, int n, float (&g)[8]) {
+__device__ __forceinline__ Pairs gate_set(const NormParams &p, int row, int gate_row, int v, int t, int n) {
   if (p.gate_kind == kGateVector) {
-    const size_t at = (size_t)(row / p.rows_per_gate) * p.hidden;
-    if (p.gate_type == kF32)
-      load_set<float, VEC>(static_cast<const float *>(p.gate) + at, v, t, n, p.hidden, g);
-    else
-      load_set<TB, VEC>(static_cast<const TB *>(p.gate) + at, v, t, n, p.hidden, g);
-  } else {
-    float x = 1.f;
-    if (p.gate_kind == kGateToken)
-      x = p.gate_type == kF32 ? static_cast<const float *>(p.gate)[row] : to_f32(static_cast<const TB *>(p.gate)[row]);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) g[e] = x;
+    const size_t at = (size_t)gate_row * p.hidden;
+    if (p.gate_type == kF32) return load_set<float, VEC>(static_cast<const float *>(p.gate) + at, v, t, n, p.hidden);
+    return load_set<TB, VEC>(static_cast<const TB *>(p.gate) + at, v, t, n, p.hidden);
   }
+  float x = 1.f;
+  if (p.gate_kind == kGateToken)
+    x = p.gate_type == kF32 ? static_cast<const float *>(p.gate)[row] : to_f32(static_cast<const TB *>(p.gate)[row]);
+  return splat(x);
 }
 
 template <typename TS, typename TB, bool VEC>
 __global__ void __launch_bounds__(512) block_norm_kernel(const __grid_constant__ NormParams p, int n) {
-  __shared__ float buf[2 * kSumBuf];
+  __shared__ float buf[2 * 16];
   const int t = threadIdx.x & (n - 1), group = threadIdx.x / n, groups = blockDim.x / n;
   const float inv = 1.f / (float)p.hidden;
   int turn = 0;
@@ -102,55 +148,46 @@ __global__ void __launch_bounds__(512) block_norm_kernel(const __grid_constant__
     const int row = base + group;
     const bool in = row < p.rows;
     const size_t r = in ? row : 0;  // a group without a row reads the first one and stores nothing
-    float s[kSets][8];
+    Pairs s[kSets];
 #pragma unroll
     for (int v = 0; v < kSets; ++v)
-      load_set<TS, VEC>(static_cast<const TS *>(p.state) + r * p.ld_state, v, t, n, p.hidden, s[v]);
+      s[v] = load_set<TS, VEC>(static_cast<const TS *>(p.state) + r * p.ld_state, v, t, n, p.hidden);
     if (p.f) {
-      float f[kSets][8];
+      Pairs f[kSets];
 #pragma unroll
       for (int v = 0; v < kSets; ++v)
-        load_set<TB, VEC>(static_cast<const TB *>(p.f) + r * p.ld_f, v, t, n, p.hidden, f[v]);
+        f[v] = load_set<TB, VEC>(static_cast<const TB *>(p.f) + r * p.ld_f, v, t, n, p.hidden);
       float scale = p.scale;
       if (p.w_post) {
-        float ss[1] = {0.f};
+        float2 ss = pair(0.f);
 #pragma unroll
-        for (int v = 0; v < kSets; ++v)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) ss[0] = fmaf(f[v][e], f[v][e], ss[0]);
-        group_sums(ss, n, buf, turn);
-        scale *= rsqrtf(fmaf(ss[0], inv, p.eps));
+        for (int v = 0; v < kSets; ++v) dot(f[v], f[v], ss);
+        float sums[1] = {ss.x + ss.y};
+        group_sums(sums, n, buf, turn);
+        scale *= rsqrtf(fmaf(sums[0], inv, p.eps));
       }
+      const int gate_row = p.gate_kind == kGateVector ? (int)r / p.rows_per_gate : 0;
 #pragma unroll
       for (int v = 0; v < kSets; ++v) {
-        float w[8];
-        gate_set<TB, VEC>(p, (int)r, v, t, n, w);
-        if (p.w_post) {
-          float wp[8];
-          load_set<float, VEC>(p.w_post, v, t, n, p.hidden, wp);
+        Pairs w = gate_set<TB, VEC>(p, (int)r, gate_row, v, t, n);
+        if (p.w_post) w = mul(w, load_set<float, VEC>(p.w_post, v, t, n, p.hidden));
+        s[v] = fma(mul(w, scale), f[v], s[v]);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) w[e] *= wp[e];
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s[v][e] = to_f32(from_f32<TS>(fmaf(scale * w[e], f[v][e], s[v][e])));
+        for (int e = 0; e < 8; ++e) flat(s[v])[e] = to_f32(from_f32<TS>(flat(s[v])[e]));
         if (in) store_set<TS, VEC>(static_cast<TS *>(p.out) + r * p.ld_out, v, t, n, p.hidden, s[v]);
       }
     }
     if (p.w_next) {
-      float ss[1] = {0.f};
+      float2 ss = pair(0.f);
 #pragma unroll
-      for (int v = 0; v < kSets; ++v)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss[0] = fmaf(s[v][e], s[v][e], ss[0]);
-      group_sums(ss, n, buf, turn);
-      const float rs = rsqrtf(fmaf(ss[0], inv, p.eps));
+      for (int v = 0; v < kSets; ++v) dot(s[v], s[v], ss);
+      float sums[1] = {ss.x + ss.y};
+      group_sums(sums, n, buf, turn);
+      const float rs = rsqrtf(fmaf(sums[0], inv, p.eps));
 #pragma unroll
       for (int v = 0; v < kSets; ++v) {
-        float w[8];
-        load_set<float, VEC>(p.w_next, v, t, n, p.hidden, w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] *= s[v][e] * rs;
-        if (in) store_set<TB, VEC>(static_cast<TB *>(p.y) + r * p.ld_y, v, t, n, p.hidden, w);
+        const Pairs w = load_set<float, VEC>(p.w_next, v, t, n, p.hidden);
+        if (in) store_set<TB, VEC>(static_cast<TB *>(p.y) + r * p.ld_y, v, t, n, p.hidden, mul(w, mul(s[v], rs)));
       }
     }
   }
@@ -158,269 +195,360 @@ __global__ void __launch_bounds__(512) block_norm_kernel(const __grid_constant__
 
 // writes a set of a gate row's gradient in the gate's type
 template <typename TB, bool VEC>
-__device__ __forceinline__ void store_gate(const NormParams &p, size_t at, int v, int t, int n, const float (&g)[8]) {
+__device__ __forceinline__ void store_gate(const NormParams &p, size_t at, int v, int t, int n, const Pairs &g) {
   if (p.gate_type == kF32)
     store_set<float, VEC>(static_cast<float *>(p.d_gate) + at, v, t, n, p.hidden, g);
   else
     store_set<TB, VEC>(static_cast<TB *>(p.d_gate) + at, v, t, n, p.hidden, g);
 }
 
-// A worker's place in its rows: row `first + i` of its lap-th chunk, while that is below `end` (the last
-// chunk of a gate row may be shorter, and a worker's last lap may have none).
+// A worker's place in its rows: row `first + i` of its lap-th chunk; end 0 after its last chunk.
 struct Place {
-  int lap, i, first, end, gate_row;
+  int lap, row, end, gate_row;
   __device__ __forceinline__ void enter(const NormParams &p, const NormBwdPlan &pl, int worker, int lap_) {
-    lap = lap_;
-    i = 0;
-    const int c = lap * pl.workers + worker;
-    gate_row = c / pl.chunks_per_gate;
-    first = gate_row * p.rows_per_gate + (c - gate_row * pl.chunks_per_gate) * pl.chunk_rows;
-    end = c < pl.chunks ? min((gate_row + 1) * p.rows_per_gate, p.rows) : 0;
+    for (lap = lap_;; ++lap) {
+      const int c = lap * pl.workers + worker;
+      row = end = 0;
+      if (c >= pl.chunks) return;
+      gate_row = c / pl.chunks_per_gate;
+      row = gate_row * p.rows_per_gate + (c - gate_row * pl.chunks_per_gate) * pl.chunk_rows;
+      end = min(min(row + pl.chunk_rows, (gate_row + 1) * p.rows_per_gate), p.rows);
+      if (row < end) return;  // the last gate row's chunks may have no rows left
+    }
   }
+  __device__ __forceinline__ bool has() const { return row < end; }
   __device__ __forceinline__ void next(const NormParams &p, const NormBwdPlan &pl, int worker) {
-    if (++i == pl.chunk_rows) enter(p, pl, worker, lap + 1);
+    if (++row == end) enter(p, pl, worker, lap + 1);
   }
-  __device__ __forceinline__ int row() const { return first + i < end ? first + i : -1; }
 };
 
-// The rows that the backward pass reads.  VEC: each thread copies its own columns of the next DEPTH - 1
-// rows into its own places in shared memory (cp.async) and reads them back itself, as often as it needs
-// them, so no barrier guards the ring and few of a row's values have to stay in registers.  Otherwise
-// the values are read from memory each time (the second time from the caches).
-template <typename TS, typename TB, bool VEC, int DEPTH>
+// The rows that the backward pass reads.  VEC: each thread copies its own columns of the next rows into
+// its own places in shared memory (cp.async) and reads them back itself, as often as it needs them, so no
+// barrier guards the ring and none of a row's values stays in registers over the reduction.  The places of
+// columns past the row's end, and of what is not given, hold zeros from the start.  Otherwise the values
+// are read from memory each time (the second time from the caches).
+constexpr int kBwdThreads = 512;
+
+template <typename TS, typename TB, bool VEC>
 struct Rows {
   static constexpr int kS = sizeof(TS) / 2, kB = sizeof(TB) / 2;  // 16-byte pieces of a set
   static constexpr int kState = 0, kDOut = kS, kDY = 2 * kS, kF = 2 * kS + kB, kPieces = 2 * kS + 2 * kB;
-  uint32_t base;  // this thread's first piece; pieces lie blockDim.x * 16 bytes apart
-  int t, n, stage, row;
-  __device__ __forceinline__ uint32_t at(int st, int v, int piece) const {
-    return base + (uint32_t)((st * kSets + v) * kPieces + piece) * blockDim.x * 16u;
+  static constexpr uint32_t kPitch = kBwdThreads * 16, kRow = kSets * kPieces * kPitch;  // a row of every group
+  uint32_t base;   // this thread's first piece; pieces lie kPitch bytes apart
+  uint32_t stage;  // the row at work, in bytes from base
+  int t, n, row;
+  bool has[kSets];
+  __device__ __forceinline__ void clear(int depth) const {
+    for (uint32_t at = 0; at < depth * kRow; at += kPitch) sts128(base + at, make_uint4(0u, 0u, 0u, 0u));
   }
-  template <typename T>
-  __device__ __forceinline__ void copy(int st, int v, int piece, const T *src) const {
-#pragma unroll
-    for (int k = 0; k < (int)sizeof(T) / 2; ++k)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at(st, v, piece + k)), "l"(src + k * (16 / sizeof(T)))
-                   : "memory");
-  }
-  __device__ __forceinline__ void fetch(const NormParams &p, int st, int r) const {
-    if (r >= 0)
-#pragma unroll
-      for (int v = 0; v < kSets; ++v) {
-        const int col = 8 * (v * n + t);
-        if (col < p.hidden) {
-          if (p.w_next) copy(st, v, kState, static_cast<const TS *>(p.state) + r * p.ld_state + col);
-          if (p.d_out) copy(st, v, kDOut, static_cast<const TS *>(p.d_out) + r * p.ld_d_out + col);
-          if (p.w_next) copy(st, v, kDY, static_cast<const TB *>(p.d_y) + r * p.ld_d_y + col);
-          if (p.f) copy(st, v, kF, static_cast<const TB *>(p.f) + r * p.ld_f + col);
-        }
-      }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  }
-  // set v of the row at work; zeros past the row's end
   template <typename T, int PIECE>
-  __device__ __forceinline__ void get(const NormParams &p, const void *src, long long ld, int v, float (&o)[8]) const {
-    if constexpr (VEC) {
-      if (8 * (v * n + t) < p.hidden) {
-        Eight<T, true> e;
-        uint4 w[sizeof(T) / 2];
+  __device__ __forceinline__ void copy(uint32_t st, const void *src, long long ld, int r) const {
+    const T *from = static_cast<const T *>(src) + r * ld + 8 * t;
+#pragma unroll
+    for (int v = 0; v < kSets; ++v, from += 8 * n)
+      if (has[v])
 #pragma unroll
         for (int k = 0; k < (int)sizeof(T) / 2; ++k)
-          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(w[k].x), "=r"(w[k].y), "=r"(w[k].z), "=r"(w[k].w)
-                       : "r"(at(stage, v, PIECE + k))
-                       : "memory");
-        memcpy(&e, w, sizeof e);
-        e.get(o);
-      } else {
+          if constexpr (sizeof(T) == 4)  // by way of L1: neighbouring threads' pieces share sectors
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(base + st + (v * kPieces + PIECE + k) * kPitch),
+                         "l"(from + k * (16 / sizeof(T)))
+                         : "memory");
+          else
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(base + st + (v * kPieces + PIECE + k) * kPitch),
+                         "l"(from + k * (16 / sizeof(T)))
+                         : "memory");
+  }
+  __device__ __forceinline__ void fetch(const NormParams &p, uint32_t st, const Place &to) const {
+    if (to.has()) {
+      if (p.w_next) copy<TS, kState>(st, p.state, p.ld_state, to.row);
+      if (p.d_out) copy<TS, kDOut>(st, p.d_out, p.ld_d_out, to.row);
+      if (p.w_next) copy<TB, kDY>(st, p.d_y, p.ld_d_y, to.row);
+      if (p.f) copy<TB, kF>(st, p.f, p.ld_f, to.row);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  template <typename T, int PIECE>
+  __device__ __forceinline__ Pairs get(const void *src, long long ld, int hidden, int v) const {
+    if constexpr (VEC) {
+      Pairs o;
+      Eight<T, true> e;
+      uint4 w[sizeof(T) / 2];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = 0.f;
-      }
+      for (int k = 0; k < (int)sizeof(T) / 2; ++k) w[k] = lds128(base + stage + (v * kPieces + PIECE + k) * kPitch);
+      memcpy(&e, w, sizeof e);
+      e.get(flat(o));
+      return o;
     } else {
-      load_set<T, false>(static_cast<const T *>(src) + row * ld, v, t, n, p.hidden, o);
+      return src ? load_set<T, false>(static_cast<const T *>(src) + row * ld, v, t, n, hidden) : splat(0.f);
+    }
+  }
+  __device__ __forceinline__ Pairs state(const NormParams &p, int v) const {
+    return get<TS, kState>(p.w_next ? p.state : nullptr, p.ld_state, p.hidden, v);
+  }
+  __device__ __forceinline__ Pairs d_out(const NormParams &p, int v) const {
+    return get<TS, kDOut>(p.d_out, p.ld_d_out, p.hidden, v);
+  }
+  __device__ __forceinline__ Pairs d_y(const NormParams &p, int v) const {
+    return get<TB, kDY>(p.d_y, p.ld_d_y, p.hidden, v);
+  }
+  __device__ __forceinline__ Pairs f(const NormParams &p, int v) const { return get<TB, kF>(p.f, p.ld_f, p.hidden, v); }
+};
+
+// The norms' weights.  WSMEM: in shared memory, in 16-byte pieces as the threads of a group read them, zeros
+// past the row's end.
+template <bool VEC, bool WSMEM>
+struct Weights {
+  uint32_t base;  // this thread's first piece
+  int t, n;
+  __device__ __forceinline__ void fill(const float *w, int which, int hidden, float absent) const {
+    if (threadIdx.x >= n) return;
+#pragma unroll
+    for (int v = 0; v < kSets; ++v)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int col = 8 * (v * n + t) + 4 * k;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (col < hidden) x = w ? *reinterpret_cast<const float4 *>(w + col) : make_float4(absent, absent, absent, absent);
+        sts128(base + ((which * kSets + v) * 2 + k) * n * 16, make_uint4(__float_as_uint(x.x), __float_as_uint(x.y),
+                                                                          __float_as_uint(x.z), __float_as_uint(x.w)));
+      }
+  }
+  __device__ __forceinline__ Pairs get(const float *w, int which, int hidden, float absent, int v) const {
+    if constexpr (WSMEM) {
+      Pairs o;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint4 x = lds128(base + ((which * kSets + v) * 2 + k) * n * 16);
+        o.v[2 * k] = make_float2(__uint_as_float(x.x), __uint_as_float(x.y));
+        o.v[2 * k + 1] = make_float2(__uint_as_float(x.z), __uint_as_float(x.w));
+      }
+      return o;
+    } else {
+      return w ? load_set<float, VEC>(w, v, t, n, hidden) : splat(absent);
     }
   }
 };
 
-// Rows of the ring: what lets two CTAs of up to 256 threads, or one of 512, stay on an SM; 0: no ring.
-template <typename TS, typename TB>
-constexpr int kRingFit = 208 * 1024 / (512 * 16 * kSets * (int)(sizeof(TS) + sizeof(TB)));
-template <typename TS, typename TB, bool VEC>
-constexpr int kRingDepth = !VEC ? 0 : kRingFit<TS, TB> < 3 ? kRingFit<TS, TB> : 3;
-
-template <typename TS, typename TB, bool VEC>
-__global__ void __launch_bounds__(512)
-    block_norm_backward_kernel(const __grid_constant__ NormParams p, const __grid_constant__ NormBwdPlan pl) {
-  constexpr int DEPTH = kRingDepth<TS, TB, VEC>;
-  using R = Rows<TS, TB, VEC, DEPTH>;
-  __shared__ float buf[2 * kSumBuf];
-  extern __shared__ uint4 ring_smem[];
-  const int n = pl.threads, t = threadIdx.x & (n - 1), group = threadIdx.x / n;
-  const int worker = blockIdx.x * pl.groups + group;
-  R rows;
-  rows.base = smem_u32(ring_smem + threadIdx.x);
-  rows.t = t;
-  rows.n = n;
-  rows.stage = 0;
-  const float inv = 1.f / (float)p.hidden;
-  const bool gates = p.gate_kind == kGateVector && p.d_gate, token = p.gate_kind == kGateToken && p.d_gate;
-  int turn = 0;
-  float a_next[kSets][8], a_post[kSets][8], a_gate[kSets][8];
+// A CTA's partial row: its groups' sums added in shared memory (the ring's, which is done with).
+template <bool VEC>
+__device__ __forceinline__ void store_sums(const NormParams &p, const Pairs (&a)[kSets], int n, int t, float *part) {
+  extern __shared__ uint4 dyn_smem[];
+  float *row = part + (size_t)blockIdx.x * p.hidden;
+  if (n == kBwdThreads) {
+#pragma unroll
+    for (int v = 0; v < kSets; ++v) store_set<float, VEC>(row, v, t, n, p.hidden, a[v]);
+    return;
+  }
+  float4 *sums = reinterpret_cast<float4 *>(dyn_smem);
+  __syncthreads();
 #pragma unroll
   for (int v = 0; v < kSets; ++v)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) a_next[v][e] = a_post[v][e] = a_gate[v][e] = 0.f;
-  // the same number of steps for every thread of the grid: the reductions are CTA-wide
-  const int steps = (pl.chunks + pl.workers - 1) / pl.workers * pl.chunk_rows;
-  Place here, ahead;
-  here.enter(p, pl, worker, 0);
-  ahead.enter(p, pl, worker, 0);
-  if constexpr (VEC)
-    for (int s = 0; s < DEPTH - 1; ++s, ahead.next(p, pl, worker)) rows.fetch(p, s, s < steps ? ahead.row() : -1);
-#pragma unroll 1
-  for (int step = 0; step < steps; ++step) {
-    const int row = here.row();
-    const bool in = row >= 0;
-    if constexpr (VEC) {
-      // into the stage that the step before freed
-      rows.fetch(p, rows.stage == 0 ? DEPTH - 1 : rows.stage - 1, step + DEPTH - 1 < steps ? ahead.row() : -1);
-      ahead.next(p, pl, worker);
-      asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH > 0 ? DEPTH - 1 : 0) : "memory");
-    } else {
-      rows.row = in ? row : 0;
+    for (int k = 0; k < 2; ++k)
+      sums[(v * 2 + k) * kBwdThreads + threadIdx.x] =
+          make_float4(a[v].v[2 * k].x, a[v].v[2 * k].y, a[v].v[2 * k + 1].x, a[v].v[2 * k + 1].y);
+  __syncthreads();
+  for (int i = threadIdx.x; i < n * kSets * 2; i += kBwdThreads) {
+    const int tt = i & (n - 1), vk = i / n, v = vk >> 1, k = vk & 1;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int g = 0; g < kBwdThreads; g += n) {
+      const float4 x = sums[vk * kBwdThreads + g + tt];
+      s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
     }
-    // A group without a row this time works on what it finds and keeps nothing of it: its sums are its
-    // own.
-    float sums[3] = {0.f, 0.f, 0.f};
+    const float o[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
-    for (int v = 0; v < kSets; ++v) {
-      if (p.w_next) {
-        float s[8], gy[8], w[8];
-        rows.template get<TS, R::kState>(p, p.state, p.ld_state, v, s);
-        rows.template get<TB, R::kDY>(p, p.d_y, p.ld_d_y, v, gy);
-        load_set<float, VEC>(p.w_next, v, t, n, p.hidden, w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          sums[0] = fmaf(s[e], s[e], sums[0]);
-          sums[1] = fmaf(w[e] * gy[e], s[e], sums[1]);
-        }
-      }
-      if (p.w_post) {
-        float f[8];
-        rows.template get<TB, R::kF>(p, p.f, p.ld_f, v, f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sums[2] = fmaf(f[e], f[e], sums[2]);
-      }
+    for (int e = 0; e < 4; ++e) {
+      const int col = VEC ? 8 * (v * n + tt) + 4 * k + e : (v * 8 + 4 * k + e) * n + tt;
+      if (col < p.hidden) row[col] = o[e];
     }
-    if (p.w_next || p.w_post) group_sums(sums, n, buf, turn);
-    const float rs = rsqrtf(fmaf(sums[0], inv, p.eps)), cs = rs * rs * (sums[1] * inv);
-    const float rf = p.w_post ? rsqrtf(fmaf(sums[2], inv, p.eps)) : 1.f;
-    float two[2] = {0.f, 0.f};
-    float dn[kSets][8];
-#pragma unroll
-    for (int v = 0; v < kSets; ++v) {
-      float ds[8];
-      if (p.d_out) rows.template get<TS, R::kDOut>(p, p.d_out, p.ld_d_out, v, ds);
-      else
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ds[e] = 0.f;
-      if (p.w_next) {
-        float s[8], gy[8], w[8];
-        rows.template get<TS, R::kState>(p, p.state, p.ld_state, v, s);
-        rows.template get<TB, R::kDY>(p, p.d_y, p.ld_d_y, v, gy);
-        load_set<float, VEC>(p.w_next, v, t, n, p.hidden, w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (in) a_next[v][e] = fmaf(gy[e], s[e] * rs, a_next[v][e]);
-          ds[e] = fmaf(rs, fmaf(-s[e], cs, w[e] * gy[e]), ds[e]);
-        }
-      }
-      if (in) store_set<TS, VEC>(static_cast<TS *>(p.d_state) + row * p.ld_d_state, v, t, n, p.hidden, ds);
-      if (p.f) {
-        float f[8], g[8], w[8];
-        rows.template get<TB, R::kF>(p, p.f, p.ld_f, v, f);
-        gate_set<TB, VEC>(p, in ? row : 0, v, t, n, g);
-        if (p.w_post) load_set<float, VEC>(p.w_post, v, t, n, p.hidden, w);
-        else
-#pragma unroll
-          for (int e = 0; e < 8; ++e) w[e] = 1.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float sd = p.scale * ds[e], nh = f[e] * rf;  // nh: the normalised branch without its weight
-          const float gn = sd * nh * w[e], d = sd * g[e];    // the gate's gradient, and the branch's
-          if (in) {
-            a_gate[v][e] += gn;
-            a_post[v][e] = fmaf(d, nh, a_post[v][e]);
-          }
-          dn[v][e] = d * w[e];
-          two[0] = fmaf(dn[v][e], f[e], two[0]);
-          two[1] += gn;
-        }
-      }
-    }
-    if (p.f) {
-      if (p.w_post || token) group_sums(two, n, buf, turn);
-      const float cf = p.w_post ? rf * rf * (two[0] * inv) : 0.f;
-#pragma unroll
-      for (int v = 0; v < kSets; ++v) {
-        float f[8];
-        rows.template get<TB, R::kF>(p, p.f, p.ld_f, v, f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = p.w_post ? rf * fmaf(-f[e], cf, dn[v][e]) : dn[v][e];
-        if (in) store_set<TB, VEC>(static_cast<TB *>(p.d_f) + row * p.ld_d_f, v, t, n, p.hidden, f);
-      }
-      if (in && token && t == 0) {
-        if (p.gate_type == kF32)
-          static_cast<float *>(p.d_gate)[row] = two[1];
-        else
-          static_cast<TB *>(p.d_gate)[row] = from_f32<TB>(two[1]);
-      }
-    }
-    if (gates && here.i == pl.chunk_rows - 1) {  // the chunk's part of the gate's gradient is complete
-      const int chunk = here.lap * pl.workers + worker;
-#pragma unroll
-      for (int v = 0; v < kSets; ++v) {
-        if (chunk < pl.chunks) {
-          if (pl.chunks_per_gate == 1)
-            store_gate<TB, VEC>(p, (size_t)here.gate_row * p.hidden, v, t, n, a_gate[v]);
-          else
-            store_set<float, VEC>(p.part + pl.gate_part + (size_t)chunk * p.hidden, v, t, n, p.hidden, a_gate[v]);
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) a_gate[v][e] = 0.f;
-      }
-    }
-    here.next(p, pl, worker);
-    rows.stage = rows.stage + 1 >= DEPTH ? 0 : rows.stage + 1;
-  }
-#pragma unroll
-  for (int v = 0; v < kSets; ++v) {
-    if (p.d_w_next) store_set<float, VEC>(p.part + (size_t)worker * p.hidden, v, t, n, p.hidden, a_next[v]);
-    if (p.d_w_post)
-      store_set<float, VEC>(p.part + ((size_t)(p.d_w_next ? pl.workers : 0) + worker) * p.hidden, v, t, n, p.hidden,
-                            a_post[v]);
   }
 }
 
-// Adds the partial rows: job 0 and 1 the norm weights' over the workers, job 2 + i gate row i's over
-// its chunks.  A CTA takes 32 columns; its 32 warps take every 32nd partial row, and the first warp
+// TG: the type of a vector gate; NoGate: the gate is no vector
+struct NoGate {};
+template <typename TS, typename TB, bool VEC, bool WSMEM, typename TG>
+__global__ void __launch_bounds__(kBwdThreads)
+    block_norm_backward_kernel(const __grid_constant__ NormParams p, const __grid_constant__ NormBwdPlan pl) {
+  using R = Rows<TS, TB, VEC>;
+  constexpr bool GATEV = !std::is_same<TG, NoGate>::value;
+  using GateEight = Eight<typename std::conditional<GATEV, TG, float>::type, VEC>;
+  __shared__ float buf[2 * 16 * 6];
+  extern __shared__ uint4 dyn_smem[];
+  const int n = pl.threads, t = threadIdx.x & (n - 1), worker = threadIdx.x / n * gridDim.x + blockIdx.x;
+  R rows;
+  rows.base = smem_u32(dyn_smem + threadIdx.x);
+  rows.t = t;
+  rows.n = n;
+  rows.stage = 0;
+#pragma unroll
+  for (int v = 0; v < kSets; ++v) rows.has[v] = 8 * (v * n + t) < p.hidden;
+  Weights<VEC, WSMEM> weights;
+  weights.base = smem_u32(dyn_smem) + pl.depth * R::kRow + t * 16;  // behind the ring
+  weights.t = t;
+  weights.n = n;
+  if constexpr (VEC) rows.clear(pl.depth);
+  if constexpr (WSMEM) {
+    weights.fill(p.w_next, 0, p.hidden, 0.f);
+    weights.fill(p.w_post, 1, p.hidden, 1.f);
+    __syncthreads();
+  }
+  const float inv = 1.f / (float)p.hidden;
+  int turn = 0;
+  // A column's gate and weight are the same over a chunk's rows, so one sum of scale ds f r_f serves both
+  // their gradients: times the gate it is w_post's, times w_post the gate's.  Without a vector gate it is
+  // w_post's.
+  Pairs a_next[kSets], a_post[kSets], branch[kSets];
+#pragma unroll
+  for (int v = 0; v < kSets; ++v) a_next[v] = a_post[v] = branch[v] = splat(0.f);
+  Place here, ahead;
+  here.enter(p, pl, worker, 0);
+  ahead = here;
+  // the gate's values stay in registers; a 16-bit gate's of the next chunk are fetched a row ahead
+  constexpr bool kAhead = GATEV && sizeof(TG) == 2;
+  GateEight gate[kSets], gate_next[kSets];
+  auto load_gate = [&](GateEight &to, int gate_row, int v) {
+    if constexpr (GATEV)
+      to.load(static_cast<const TG *>(p.gate) + (size_t)gate_row * p.hidden + (VEC ? 0 : v * 8 * n), VEC ? v * n + t : t, n,
+              VEC ? p.hidden : p.hidden - v * 8 * n);
+  };
+  auto gate_pairs = [&](const GateEight &from) {
+    Pairs o;
+    from.get(flat(o));
+    return o;
+  };
+  if constexpr (GATEV) {
+#pragma unroll
+    for (int v = 0; v < kSets; ++v) {
+      load_gate(gate[v], here.has() ? here.gate_row : 0, v);
+      gate_next[v] = gate[v];
+    }
+  }
+  if constexpr (VEC) {
+    for (int s = 0; s < pl.depth - 1; ++s) {
+      rows.fetch(p, s * R::kRow, ahead);
+      if (ahead.has()) ahead.next(p, pl, worker);
+    }
+  }
+  while (here.has()) {
+    if constexpr (VEC) {
+      rows.fetch(p, rows.stage == 0 ? (pl.depth - 1) * R::kRow : rows.stage - R::kRow, ahead);  // freed by the row before
+      if (ahead.has()) ahead.next(p, pl, worker);
+      if (pl.depth == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
+      else if (pl.depth == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
+      else asm volatile("cp.async.wait_group 0;" ::: "memory");
+    } else {
+      rows.row = here.row;
+    }
+    Place after = here;
+    after.next(p, pl, worker);
+    if constexpr (kAhead) {
+      if (after.has() && after.gate_row != here.gate_row)
+#pragma unroll
+        for (int v = 0; v < kSets; ++v) load_gate(gate_next[v], after.gate_row, v);
+    }
+    const int row = here.row;
+    // a gate value of the whole row stays out of q, so that its own gradient is a sum of q ds
+    const float token = p.gate_kind != kGateToken ? 1.f
+                        : p.gate_type == kF32     ? static_cast<const float *>(p.gate)[row]
+                                                  : to_f32(static_cast<const TB *>(p.gate)[row]);
+    float2 ss = pair(0.f), sw = pair(0.f), sf = pair(0.f), qo = pair(0.f), qg = pair(0.f), qs = pair(0.f);
+#pragma unroll
+    for (int v = 0; v < kSets; ++v) {
+      const Pairs s = rows.state(p, v), gw = mul(rows.d_y(p, v), weights.get(p.w_next, 0, p.hidden, 0.f, v));
+      Pairs q = rows.f(p, v);
+      dot(s, s, ss);
+      dot(gw, s, sw);
+      dot(q, q, sf);
+      q = mul(q, weights.get(p.w_post, 1, p.hidden, 1.f, v));
+      if constexpr (GATEV) q = mul(q, gate_pairs(gate[v]));
+      dot(q, rows.d_out(p, v), qo);
+      dot(q, gw, qg);
+      dot(q, s, qs);
+    }
+    float sums[6] = {ss.x + ss.y, sw.x + sw.y, sf.x + sf.y, qo.x + qo.y, qg.x + qg.y, qs.x + qs.y};
+    group_sums(sums, n, buf, turn);
+    const float rs = p.w_next ? rsqrtf(fmaf(sums[0], inv, p.eps)) : 0.f, cs = rs * rs * rs * (sums[1] * inv);
+    const float rf = p.w_post ? rsqrtf(fmaf(sums[2], inv, p.eps)) : 1.f;
+    const float q_ds = fmaf(-cs, sums[5], fmaf(rs, sums[4], sums[3]));
+    const float scale = p.scale * token, cf = p.w_post ? scale * (rf * rf * rf) * (q_ds * inv) : 0.f;
+#pragma unroll
+    for (int v = 0; v < kSets; ++v) {
+      const Pairs s = rows.state(p, v), gy = mul(rows.d_y(p, v), rs);
+      a_next[v] = fma(gy, s, a_next[v]);
+      const Pairs ds = fma(s, -cs, fma(weights.get(p.w_next, 0, p.hidden, 0.f, v), gy, rows.d_out(p, v)));
+      store_set<TS, VEC>(static_cast<TS *>(p.d_state) + row * p.ld_d_state, v, t, n, p.hidden, ds);
+      if (p.f) {
+        // nh: the normalised branch without its weight; d: the branch's gradient
+        const Pairs f = rows.f(p, v), nh = mul(f, rf), sd = mul(ds, scale), w = weights.get(p.w_post, 1, p.hidden, 1.f, v);
+        Pairs d = sd;
+        if constexpr (GATEV) {
+          d = mul(sd, gate_pairs(gate[v]));
+          branch[v] = fma(sd, nh, branch[v]);
+        } else {
+          a_post[v] = fma(sd, nh, a_post[v]);
+        }
+        store_set<TB, VEC>(static_cast<TB *>(p.d_f) + row * p.ld_d_f, v, t, n, p.hidden, fma(f, -cf, mul(mul(d, w), rf)));
+      }
+    }
+    if (p.gate_kind == kGateToken && p.d_gate && t == 0) {
+      const float d = p.scale * rf * q_ds;
+      if (p.gate_type == kF32)
+        static_cast<float *>(p.d_gate)[row] = d;
+      else
+        static_cast<TB *>(p.d_gate)[row] = from_f32<TB>(d);
+    }
+    if constexpr (GATEV) {
+      if (row + 1 == here.end) {  // the chunk's part of the gate's gradient is complete
+#pragma unroll
+        for (int v = 0; v < kSets; ++v) {
+          a_post[v] = fma(gate_pairs(gate[v]), branch[v], a_post[v]);
+          if (p.d_gate) branch[v] = mul(branch[v], weights.get(p.w_post, 1, p.hidden, 1.f, v));
+          if (pl.one_gate) continue;  // this was the worker's only chunk: stored at the end
+          if (p.d_gate) {
+            if (pl.chunks_per_gate == 1)
+              store_gate<TB, VEC>(p, (size_t)here.gate_row * p.hidden, v, t, n, branch[v]);
+            else
+              store_set<float, VEC>(p.part + pl.gate_part + (size_t)(here.lap * pl.workers + worker) * p.hidden, v, t, n,
+                                    p.hidden, branch[v]);
+          }
+          branch[v] = splat(0.f);
+          if constexpr (kAhead) gate[v] = gate_next[v];
+          else if (after.has()) load_gate(gate[v], after.gate_row, v);
+        }
+      }
+    }
+    here = after;
+    if constexpr (VEC) rows.stage = rows.stage + R::kRow >= pl.depth * R::kRow ? 0 : rows.stage + R::kRow;
+  }
+  if (p.d_w_next) store_sums<VEC>(p, a_next, n, t, p.part);
+  if (p.d_w_post) store_sums<VEC>(p, a_post, n, t, p.part + (size_t)(p.d_w_next ? pl.ctas : 0) * p.hidden);
+  if (GATEV && p.d_gate && pl.one_gate) store_sums<VEC>(p, branch, n, t, p.part + pl.gate_part);
+}
+
+// Adds the partial rows: job 0 and 1 the norm weights' over the CTAs, job 2 + i gate row i's over its
+// chunks (a gate of one row: over the CTAs).  A CTA takes 32 columns; its 32 warps take every 32nd partial row, and the first warp
 // adds their 32 sums in order.
 template <typename TB>
 __global__ void __launch_bounds__(1024)
     norm_partials_kernel(const __grid_constant__ NormParams p, const __grid_constant__ NormBwdPlan pl) {
   __shared__ float buf[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
-  for (int job = blockIdx.y; job < 2 + (pl.floats > pl.gate_part ? pl.chunks / pl.chunks_per_gate : 0); job += gridDim.y) {
+  pdl_wait();  // launched while the kernel that writes the partial rows runs
+  for (int job = blockIdx.y; job < pl.jobs; job += gridDim.y) {
     if ((job == 0 && !p.d_w_next) || (job == 1 && !p.d_w_post)) continue;
     const float *src = p.part;
-    int count = pl.workers;
-    if (job == 1) src += (size_t)(p.d_w_next ? pl.workers : 0) * p.hidden;
-    if (job >= 2) {
+    int count = pl.ctas;
+    if (job == 1) src += (size_t)(p.d_w_next ? pl.ctas : 0) * p.hidden;
+    if (job == 2 && pl.one_gate) {
+      src += pl.gate_part;
+    } else if (job >= 2) {
       src += pl.gate_part + (size_t)(job - 2) * pl.chunks_per_gate * p.hidden;
-      count = pl.chunks_per_gate;
+      // the last gate row may have fewer rows than the others
+      count = (min(p.rows_per_gate, p.rows - (job - 2) * p.rows_per_gate) + pl.chunk_rows - 1) / pl.chunk_rows;
     }
     float a = 0.f;
     if (col < p.hidden)
+#pragma unroll 8
       for (int i = warp; i < count; i += 32) a += src[(size_t)i * p.hidden + col];
     __syncthreads();
     buf[warp][lane] = a;
@@ -445,9 +573,10 @@ int group_threads(int hidden) {
 
 size_t type_bytes(int t) { return t == kF32 ? 4 : 2; }
 
-// a row can be read and written in 16-byte pieces: address and row stride are multiples of 16 bytes
+// a row can be read and written eight values at a time: address and row stride are multiples of their bytes
 bool wide(const void *q, long long ld, int type) {
-  return !q || ((reinterpret_cast<uintptr_t>(q) & 15u) == 0 && (ld * (long long)type_bytes(type)) % 16 == 0);
+  const int bytes = 8 * (int)type_bytes(type);
+  return !q || (reinterpret_cast<uintptr_t>(q) % bytes == 0 && (ld * (long long)type_bytes(type)) % bytes == 0);
 }
 
 bool all_wide(const NormParams &p) {
@@ -472,26 +601,41 @@ cudaError_t forward_typed(const NormParams &p, int num_sms, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-template <typename TS, typename TB, bool VEC>
-cudaError_t backward_launch(const NormParams &p, const NormBwdPlan &pl, cudaStream_t st) {
-  static std::atomic<unsigned long long> done{0};
-  const int threads = pl.threads * pl.groups;
-  const size_t per_thread = (size_t)kRingDepth<TS, TB, VEC> * kSets * (sizeof(TS) + sizeof(TB)) * 16;
-  const cudaError_t e = allow_smem((const void *)block_norm_backward_kernel<TS, TB, VEC>, per_thread * 512, done);
-  if (e != cudaSuccess) return e;
-  block_norm_backward_kernel<TS, TB, VEC><<<pl.ctas, threads, per_thread * threads, st>>>(p, pl);
-  return cudaGetLastError();
+// The ring takes up to three rows of every group.  The weights go beside it unless that leaves less than
+// two rows.
+constexpr size_t kBwdSmem = 224 * 1024;
+
+template <typename TS, typename TB, bool VEC, bool WSMEM>
+cudaError_t backward_launch(const NormParams &p, NormBwdPlan pl, cudaStream_t st) {
+  using R = Rows<TS, TB, VEC>;
+  const size_t weights = WSMEM ? 2 * kSets * 2 * (size_t)pl.threads * 16 : 0, room = (kBwdSmem - weights) / R::kRow;
+  // no more rows than a worker has
+  const int most = (int)(room < 3 ? room : 3), its = (pl.chunks + pl.workers - 1) / pl.workers * pl.chunk_rows;
+  pl.depth = !VEC ? 0 : its < most ? its : most;
+  const size_t ring = pl.depth * (size_t)R::kRow, sums = kBwdThreads * kSets * 32;  // at the end the groups' sums
+  const size_t smem = (ring > sums ? ring : sums) + weights;
+  auto go = [&](auto kernel, std::atomic<unsigned long long> &done) {
+    const cudaError_t e = allow_smem((const void *)kernel, kBwdSmem, done);
+    if (e != cudaSuccess) return e;
+    kernel<<<pl.ctas, kBwdThreads, smem, st>>>(p, pl);
+    return cudaGetLastError();
+  };
+  static std::atomic<unsigned long long> done[3];
+  if (!p.f || p.gate_kind != kGateVector) return go(block_norm_backward_kernel<TS, TB, VEC, WSMEM, NoGate>, done[0]);
+  if (p.gate_type == kF32) return go(block_norm_backward_kernel<TS, TB, VEC, WSMEM, float>, done[1]);
+  return go(block_norm_backward_kernel<TS, TB, VEC, WSMEM, TB>, done[2]);
 }
 
 template <typename TS, typename TB>
 cudaError_t backward_typed(const NormParams &p, int num_sms, cudaStream_t st) {
   const NormBwdPlan pl = norm_bwd_plan(p, num_sms);
-  const cudaError_t e = all_wide(p) ? backward_launch<TS, TB, true>(p, pl, st) : backward_launch<TS, TB, false>(p, pl, st);
+  const bool beside = kBwdSmem - 2 * kSets * 2 * (size_t)pl.threads * 16 >= 2 * (size_t)Rows<TS, TB, true>::kRow;
+  const cudaError_t e = !all_wide(p) ? backward_launch<TS, TB, false, false>(p, pl, st)
+                        : beside     ? backward_launch<TS, TB, true, true>(p, pl, st)
+                                     : backward_launch<TS, TB, true, false>(p, pl, st);
   if (e != cudaSuccess || pl.floats == 0) return e;
-  const int jobs = 2 + (pl.floats > pl.gate_part ? pl.chunks / pl.chunks_per_gate : 0);
-  const dim3 grid((p.hidden + 31) / 32, jobs < 1024 ? jobs : 1024);
-  norm_partials_kernel<TB><<<grid, 1024, 0, st>>>(p, pl);
-  return cudaGetLastError();
+  const dim3 grid((p.hidden + 31) / 32, pl.jobs < 1024 ? pl.jobs : 1024);
+  return launch_pdl(norm_partials_kernel<TB>, grid, dim3(1024), 0, st, p, pl);
 }
 
 }  // namespace
@@ -499,24 +643,28 @@ cudaError_t backward_typed(const NormParams &p, int num_sms, cudaStream_t st) {
 NormBwdPlan norm_bwd_plan(const NormParams &p, int num_sms) {
   NormBwdPlan pl = {};
   pl.threads = group_threads(p.hidden);
-  const int threads = pl.threads < 256 ? 256 : pl.threads;
-  pl.groups = threads / pl.threads;
+  pl.groups = kBwdThreads / pl.threads;
   const bool gates = p.f && p.gate_kind == kGateVector;
   const int per = gates ? p.rows_per_gate : p.rows;
   const int n_gates = (p.rows + per - 1) / per;
-  // two CTAs of 256 threads for each SM, or one of 512
-  const int most = num_sms * (threads <= 256 ? 2 : 1) * pl.groups;
+  const int most = num_sms * pl.groups;  // one CTA for each SM
   int chunk = (int)(((long long)n_gates * per + most - 1) / most);
   pl.chunk_rows = chunk < 1 ? 1 : chunk > per ? per : chunk;
   pl.chunks_per_gate = (per + pl.chunk_rows - 1) / pl.chunk_rows;
   pl.chunks = n_gates * pl.chunks_per_gate;
-  const int workers = pl.chunks < most ? pl.chunks : most;
-  pl.ctas = (workers + pl.groups - 1) / pl.groups;
+  pl.ctas = pl.chunks < num_sms ? pl.chunks : num_sms;
   pl.workers = pl.ctas * pl.groups;
   const size_t norms = (p.d_w_next ? 1 : 0) + (p.d_w_post ? 1 : 0);
-  pl.gate_part = norms * pl.workers * p.hidden;
+  pl.gate_part = norms * pl.ctas * p.hidden;
   pl.floats = pl.gate_part;
-  if (gates && p.d_gate && pl.chunks_per_gate > 1) pl.floats += (size_t)pl.chunks * p.hidden;
+  pl.jobs = 2;
+  if (gates && p.d_gate) {
+    pl.one_gate = n_gates == 1 && pl.chunks <= pl.workers;
+    if (pl.one_gate || pl.chunks_per_gate > 1) {
+      pl.floats += (size_t)(pl.one_gate ? pl.ctas : pl.chunks) * p.hidden;
+      pl.jobs += n_gates;
+    }
+  }
   return pl;
 }
 

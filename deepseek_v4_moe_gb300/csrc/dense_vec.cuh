@@ -47,7 +47,7 @@ __device__ __forceinline__ void unpack2(uint32_t w, float &a, float &b, const __
 }
 
 // Eight values of one row that belong to thread t of a group of `n` threads.  VEC: columns 8t .. 8t+7
-// as 16-byte accesses (the row 16-byte aligned, hidden a multiple of 8).  Otherwise columns t, t + n,
+// as one access (the row aligned to eight values, hidden a multiple of 8).  Otherwise columns t, t + n,
 // t + 2n, ...: single accesses that neighbouring threads make side by side.  Columns from `hidden`
 // on read as zero and are not written.
 template <typename T, bool VEC>
@@ -93,24 +93,30 @@ struct Eight<T, true> {
   }
 };
 
+// f32: one 32-byte access (the row 32-byte aligned); two of 16 bytes each would use half of every sector
+// they touch
 template <>
 struct Eight<float, true> {
-  float4 a, b;
+  float v[8];
   __device__ __forceinline__ void load(const float *row, int t, int, int hidden) {
-    a = b = make_float4(0.f, 0.f, 0.f, 0.f);
     if (8 * t < hidden) {
-      a = *reinterpret_cast<const float4 *>(row + 8 * t);
-      b = *reinterpret_cast<const float4 *>(row + 8 * t + 4);
+      asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                   : "l"(row + 8 * t));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = 0.f;
     }
   }
   __device__ __forceinline__ void get(float (&o)[8]) const {
-    o[0] = a.x, o[1] = a.y, o[2] = a.z, o[3] = a.w, o[4] = b.x, o[5] = b.y, o[6] = b.z, o[7] = b.w;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = v[e];
   }
   static __device__ __forceinline__ void store(float *row, int t, int, int hidden, const float (&o)[8]) {
-    if (8 * t < hidden) {
-      *reinterpret_cast<float4 *>(row + 8 * t) = make_float4(o[0], o[1], o[2], o[3]);
-      *reinterpret_cast<float4 *>(row + 8 * t + 4) = make_float4(o[4], o[5], o[6], o[7]);
-    }
+    if (8 * t < hidden)
+      asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(row + 8 * t), "f"(o[0]), "f"(o[1]),
+                   "f"(o[2]), "f"(o[3]), "f"(o[4]), "f"(o[5]), "f"(o[6]), "f"(o[7])
+                   : "memory");
   }
 };
 

@@ -350,7 +350,7 @@ typedef struct moe_ffn_block_norm_grads {
   void *d_f; int64_t ld_d_f;            /* block_type; given exactly when f is */
   void *d_gate;                         /* gate_type, the gate's layout; may be NULL */
   float *d_norm_f, *d_norm_next;        /* [hidden]; may be NULL */
-  void *workspace; size_t workspace_bytes; /* at least moe_ffn_block_norm_workspace, 16-byte aligned */
+  void *workspace; size_t workspace_bytes; /* at least moe_ffn_block_norm_workspace, 32-byte aligned */
 } moe_ffn_block_norm_grads;
 
 /* The codes of moe_ffn_block_norm, and NO_MEMORY when the workspace is too small. */
