@@ -521,7 +521,7 @@ extern "C" int moe_ffn_fp8_matmul(const moe_ffn_fp8_matmul_args *a, void *stream
   const moe::DenseTile t = moe::fp8_pick_tile(p, sms);
   CUtensorMap ma, mb;
   if (!encode_map(&ma, a->a, 1, K, R, a->ld_a, p.a_rows) ||
-      !encode_map(&mb, a->b, 1, K, N, a->ld_b, t.pair ? t.bn / 2 : t.bn))
+      !encode_map(&mb, a->b, 1, K, N, a->ld_b, t.kind == moe::kPairTile ? t.bn / 2 : t.bn))
     return fail(MOE_FFN_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", who);
   return launched(who, moe::launch_fp8_matmul(t, ma, mb, p, sms, static_cast<cudaStream_t>(stream)));
 }

@@ -55,6 +55,7 @@ struct GemmParams {
   int m, n, same;      // output of problems 0 .. same-1
   int m_last, n_last;  // output of problem `same` (kWeightGrad; zero: there is none)
   int kb0, kb;         // k blocks of the first pair of matrices, and in all
+  int splits;          // CTAs that share a tile's k; set by launch_dense_gemm
   int tiles_m, tiles_n, tiles_m_last, tiles_n_last, tiles;  // set by launch_dense_gemm
   void *c[3];
   long long ldc[3];
@@ -71,10 +72,12 @@ struct GemmParams {
 // then reads what lies in shared memory there, into accumulator rows that nothing reads.
 inline int a_box(int m) { return m >= 128 ? 128 : (m + 7) / 8 * 8; }
 
-// a tile: bn columns (kGateUp: half of them of g, half of u) of 128 rows, or of 256 by a pair of CTAs
+// A tile: bn columns (kGateUp: half of them of g, half of u) of 128 rows by one CTA, of 256 by a pair, or of
+// 128 by `splits` CTAs that share its k.
+enum TileKind : int { kOneTile = 0, kPairTile = 1, kSplitTile = 2 };
+constexpr int kSplitMax = 4;
 struct DenseTile {
-  int bn;
-  bool pair;
+  int bn, kind, splits;
 };
 int gemm_b_box(int mode, DenseTile tile);  // rows of B's boxes
 DenseTile gemm_pick_tile(int mode, const GemmParams &p, int num_sms);

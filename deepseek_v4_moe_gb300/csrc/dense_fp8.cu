@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (p.inject && blockIdx.x == 0)  // test hook: a wait that runs out
         (void)warp_wait(&never_bar, 0u, abort_p, p.status, p.wait_ns);
       const uint32_t idesc = idesc_f8(p.a_e5m2, p.b_e5m2, kRows, BN);
-      const uint64_t a0 = smem_desc_sw128(0) + (uint64_t)(smem_u32(ring) >> 4), b0 = a0 + (C::kABytes >> 4);
+      const uint64_t a0 = smem_desc_sw128(smem_u32(ring)), b0 = a0 + (C::kABytes >> 4);
       RingPos<C::kStages> pos;
       RingPos<C::kAcc> acc;
       bool ok = true;
@@ -497,7 +497,7 @@ cudaError_t quantise_typed(const QuantiseParams &p, int num_sms, cudaStream_t st
 }
 
 long long fp8_tiles(const Fp8Params &p, DenseTile t) {
-  const int rows = t.pair ? 2 * kBM : kBM;
+  const int rows = t.kind == kPairTile ? 2 * kBM : kBM;
   return (long long)((p.m + rows - 1) / rows) * ((p.n + t.bn - 1) / t.bn);
 }
 
@@ -511,14 +511,14 @@ DenseTile fp8_pick_tile(const Fp8Params &p, int num_sms) {
   const struct {
     DenseTile tile;
     double k_block;
-  } all[] = {{{256, true}, 0.47},   {{224, true}, 0.42},  {{128, true}, 0.28},
-             {{128, false}, 0.305}, {{64, false}, 0.265}, {{32, false}, 0.26}};
-  DenseTile best = {0, false};
+  } all[] = {{{256, kPairTile, 1}, 0.47}, {{224, kPairTile, 1}, 0.42}, {{128, kPairTile, 1}, 0.28},
+             {{128, kOneTile, 1}, 0.305}, {{64, kOneTile, 1}, 0.265}, {{32, kOneTile, 1}, 0.26}};
+  DenseTile best = {0, kOneTile, 1};
   double least = 0;
   for (const auto &c : all) {
-    const long long units = c.tile.pair ? num_sms / 2 : num_sms;
+    const long long units = c.tile.kind == kPairTile ? num_sms / 2 : num_sms;
     const long long waves = (fp8_tiles(p, c.tile) + units - 1) / units;
-    const double time = (c.tile.pair ? 4.0 : 3.5) + waves * c.k_block * p.kb + 0.012 * c.tile.bn;
+    const double time = (c.tile.kind == kPairTile ? 4.0 : 3.5) + waves * c.k_block * p.kb + 0.012 * c.tile.bn;
     if (best.bn == 0 || time < least) {
       best = c.tile;
       least = time;
@@ -529,12 +529,12 @@ DenseTile fp8_pick_tile(const Fp8Params &p, int num_sms) {
 
 cudaError_t launch_fp8_matmul(DenseTile t, const CUtensorMap &a, const CUtensorMap &b, Fp8Params p, int num_sms,
                               cudaStream_t st) {
-  p.tiles_m = (p.m + (t.pair ? 2 : 1) * kBM - 1) / ((t.pair ? 2 : 1) * kBM);
+  p.tiles_m = (p.m + (t.kind == kPairTile ? 2 : 1) * kBM - 1) / ((t.kind == kPairTile ? 2 : 1) * kBM);
   p.tiles_n = (p.n + t.bn - 1) / t.bn;
   p.tiles = p.tiles_m * p.tiles_n;
-  if (t.bn == 256 && t.pair) return launch<256, true>(a, b, p, num_sms, st);
-  if (t.bn == 224 && t.pair) return launch<224, true>(a, b, p, num_sms, st);
-  if (t.bn == 128 && t.pair) return launch<128, true>(a, b, p, num_sms, st);
+  if (t.bn == 256 && t.kind == kPairTile) return launch<256, true>(a, b, p, num_sms, st);
+  if (t.bn == 224 && t.kind == kPairTile) return launch<224, true>(a, b, p, num_sms, st);
+  if (t.bn == 128 && t.kind == kPairTile) return launch<128, true>(a, b, p, num_sms, st);
   if (t.bn == 128) return launch<128, false>(a, b, p, num_sms, st);
   if (t.bn == 64) return launch<64, false>(a, b, p, num_sms, st);
   if (t.bn == 32) return launch<32, false>(a, b, p, num_sms, st);

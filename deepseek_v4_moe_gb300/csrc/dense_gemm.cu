@@ -38,16 +38,21 @@ namespace {
 constexpr int kBK = 64;
 constexpr int kABytes = kBM * kBK * 2;
 
-template <int MODE, int BN, bool PAIR>
+// How the CTAs of a cluster share a tile: not at all; a pair makes 256 rows of it (cta_group::2); or each
+// takes a part of k, for few tiles with a long k.
+template <int MODE, int BN, int KIND>
 struct Cfg {
+  static constexpr bool PAIR = KIND == kPairTile, SPLIT = KIND == kSplitTile;
   static constexpr bool kAMn = MODE == kWeightGrad;
   static constexpr bool kBMn = MODE == kHiddenGrad || MODE == kInputGrad || MODE == kWeightGrad;
   // rows of B in this CTA; an MN-major operand comes in whole boxes of 64, of which the last may be used in part
   static constexpr int kBUsed = PAIR ? BN / 2 : BN, kBRows = kBMn ? (kBUsed + 63) / 64 * 64 : kBUsed;
   static constexpr int kStage = kABytes + kBRows * kBK * 2;
   static constexpr int kBufBytes = kEpiWarps * kStageBuf;
-  static constexpr int kStages = (kRingBytes - kBufBytes) / kStage;
-  static constexpr size_t kSmem = (size_t)kStages * kStage + kBufBytes + 1024;
+  // what the other CTAs send of this CTA's rows: at most (kSplitMax - 1) parts of a lane quarter's rows
+  static constexpr int kPartBytes = SPLIT ? (kSplitMax - 1) * 32 * BN * 4 : 0;
+  static constexpr int kStages = (kRingBytes - kBufBytes - kPartBytes) / kStage;
+  static constexpr size_t kSmem = (size_t)kStages * kStage + kBufBytes + kPartBytes + 1024;
   static constexpr int kTmemCols = 2 * BN < 32 ? 32 : 2 * BN > 256 ? 512 : 2 * BN;  // a power of two
   static_assert(BN % 32 == 0 && kBRows % 8 == 0, "whole epilogue chunks and swizzle groups");
 };
@@ -101,6 +106,7 @@ struct Epilogue {
   uint4 g[4], u[4];  // kHiddenGrad: the next step's, as they are fetched
   int row0, m, n, half;
   uint32_t buf;      // the warp's staging buffer
+  uint32_t parts;    // the other CTAs' sums of this warp's rows, p.splits - 1 times 32 rows x BN
   Tile tl;
   // thread l moves piece l % 4 of rows l / 4 + 8 i
   __device__ __forceinline__ bool mine(int i, int c0, size_t ld, size_t &at) const {
@@ -166,6 +172,26 @@ struct Epilogue {
     }
     __syncwarp();
   }
+  // sixteen columns of the accumulator, with the other CTAs' parts added in order
+  template <bool SPLIT>
+  __device__ __forceinline__ void take(const GemmParams &p, uint32_t tbase, int col, float (&v)[16]) const {
+    tmem_ld16(tbase + col, v);
+    if constexpr (SPLIT)
+      for (int s = 0; s < p.splits - 1; ++s)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 w = lds128(parts + part_at(s, col / 4 + i));
+          v[4 * i] += __uint_as_float(w.x);
+          v[4 * i + 1] += __uint_as_float(w.y);
+          v[4 * i + 2] += __uint_as_float(w.z);
+          v[4 * i + 3] += __uint_as_float(w.w);
+        }
+  }
+  // four columns of this lane's row in part s
+  static __device__ __forceinline__ uint32_t part_at(int s, int four) {
+    return ((s * (BN / 4) + four) * 32 + (threadIdx.x & 31)) * 16;
+  }
+  template <bool SPLIT>
   __device__ __forceinline__ void finish(const GemmParams &p, uint32_t tbase) {
 #pragma unroll 1
     for (int c0 = half * 32; c0 < kCols; c0 += 64) {
@@ -179,9 +205,9 @@ struct Epilogue {
       for (int s = 0; s < 2; ++s) {
         if (c0 + 16 * s >= kCols) break;  // TMEM ends here (the words left over are not stored)
         float v[16], w[16];
-        tmem_ld16(tbase + c0 + 16 * s, v);
+        take<SPLIT>(p, tbase, c0 + 16 * s, v);
         if constexpr (MODE == kGateUp) {
-          tmem_ld16(tbase + BN / 2 + c0 + 16 * s, w);
+          take<SPLIT>(p, tbase, BN / 2 + c0 + 16 * s, w);
           pack16(v, y + 8 * s);
           pack16(w, z + 8 * s);
 #pragma unroll
@@ -233,7 +259,7 @@ __device__ __forceinline__ void epilogue_loop(const GemmParams &p, uint32_t tmem
     e.begin(p, tl, half, tl.m0 + (int)rank * kBM + q * 32, buf);
     if (!warp_wait(&tfull_bar[acc.slot], acc.round, abort_p, p.status, p.wait_ns)) break;
     tc_fence_after();
-    e.finish(p, tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc.slot * BN));
+    e.template finish<false>(p, tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc.slot * BN));
     tc_fence_before();
     __syncwarp();
     if (lane == 0) {
@@ -243,10 +269,43 @@ __device__ __forceinline__ void epilogue_loop(const GemmParams &p, uint32_t tmem
   }
 }
 
-template <int MODE, int BN, bool PAIR>
+// The epilogue of a tile whose k the cluster's CTAs share (p.splits: two or four): lane quarter q of the
+// rows belongs to CTA q * splits / 4, which gets the others' sums of it and finishes it.
+template <int MODE, int BN, typename T>
+__device__ __forceinline__ void epilogue_split(const GemmParams &p, uint32_t tmem, int rank, int warp, int tile,
+                                               uint64_t *tfull_bar, uint32_t buf, uint32_t parts0, volatile int *abort_p) {
+  constexpr int kCols = MODE == kGateUp ? BN / 2 : BN;
+  const int q = warp & 3, half = (warp - 2) >> 2, owner = q * p.splits / 4;
+  const int first_q = owner * 4 / p.splits;  // the owner's first quarter
+  const uint32_t parts = parts0 + (q - first_q) * (p.splits - 1) * 32 * BN * 4;
+  const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16);
+  const Tile tl = tile_of(p, tile, kBM, kCols);
+  Epilogue<MODE, BN, T> e;
+  e.parts = parts;
+  if (owner == rank) e.begin(p, tl, half, tl.m0 + q * 32, buf);
+  const bool ok = warp_wait(tfull_bar, 0u, abort_p, p.status, p.wait_ns);
+  tc_fence_after();
+  if (ok && owner != rank) {
+    const uint32_t to = in_cta_of(parts, owner);
+    const int slot = rank < owner ? rank : rank - 1;
+#pragma unroll 1
+    for (int c0 = half * (BN / 2); c0 < (half + 1) * (BN / 2); c0 += 16) {
+      float v[16];
+      tmem_ld16(tbase + c0, v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        st_cluster_128(to + e.part_at(slot, c0 / 4 + i), v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    }
+  }
+  cluster_sync();  // every part has arrived
+  if (ok && owner == rank) e.template finish<true>(p, tbase);
+}
+
+template <int MODE, int BN, int KIND>
 __global__ void __launch_bounds__(kThreads, 1)
     dense_gemm_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ GemmParams p) {
-  using C = Cfg<MODE, BN, PAIR>;
+  using C = Cfg<MODE, BN, KIND>;
+  constexpr bool PAIR = C::PAIR, SPLIT = C::SPLIT;
   constexpr int kCols = MODE == kGateUp ? BN / 2 : BN;  // output columns of a tile
   constexpr int kRows = PAIR ? 2 * kBM : kBM;           // output rows of a tile
   extern __shared__ uint8_t smem_raw[];
@@ -257,8 +316,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ int abort_flag, issued;
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const uint32_t rank = PAIR ? cluster_rank() : 0u;
-  const int first_tile = PAIR ? blockIdx.x >> 1 : blockIdx.x, tile_step = PAIR ? gridDim.x >> 1 : gridDim.x;
+  const uint32_t rank = PAIR ? cluster_rank() : 0u;  // in the pair
+  const int part = SPLIT ? (int)cluster_rank() : 0;  // of k
+  const int first_tile = PAIR ? blockIdx.x >> 1 : SPLIT ? blockIdx.x / p.splits : blockIdx.x;
+  const int tile_step = PAIR ? gridDim.x >> 1 : SPLIT ? p.tiles : gridDim.x;
+  const int kb_first = SPLIT ? part * p.kb / p.splits : 0, kb_end = SPLIT ? (part + 1) * p.kb / p.splits : p.kb;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full_bar[s], 1);
@@ -280,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if constexpr (PAIR) cluster_sync();  // the peer's barriers are initialised
+  if constexpr (PAIR || SPLIT) cluster_sync();  // the other CTAs run, and their barriers are initialised
   tc_fence_after();
   const uint32_t tmem = tmem_base;
   volatile int *abort_p = &abort_flag;
@@ -295,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int t = first_tile; ok && t < p.tiles; t += tile_step) {
       const Tile tl = tile_of(p, t, kRows, kCols);
       const int m0 = tl.m0 + (int)rank * kBM, n0 = tl.n0 + (MODE == kGateUp ? 0 : (int)rank * C::kBUsed);
-      for (int kb = 0; kb < p.kb; ++kb, ++j, pos.next()) {
+      for (int kb = kb_first; kb < kb_end; ++kb, ++j, pos.next()) {
         const int s = pos.slot;
         if (!warp_wait(&empty_bar[s], pos.round ^ 1u, abort_p, p.status, p.wait_ns)) {
           ok = false;
@@ -337,7 +399,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         (void)warp_wait(&never_bar, 0u, abort_p, p.status, p.wait_ns);
       const uint32_t idesc = idesc_16(p.f16, C::kAMn, C::kBMn, kRows, BN);
       // 16 k are 32 bytes of a K-major row, or 16 rows of 128 bytes of an MN-major box
-      const uint64_t ring_d = (uint64_t)(smem_u32(ring) >> 4);
+      // (an address of shared memory carries the CTA's rank in its cluster above the 18 bits that count)
+      const uint64_t ring_d = (smem_u32(ring) >> 4) & 0x3FFFu;
       const uint64_t a0 = (C::kAMn ? smem_desc_mn(0) : smem_desc_sw128(0)) + ring_d;
       const uint64_t b0 = (C::kBMn ? smem_desc_mn(0) : smem_desc_sw128(0)) + ring_d + (kABytes >> 4);
       constexpr int kAStep = (C::kAMn ? 2048 : 32) >> 4, kBStep = (C::kBMn ? 2048 : 32) >> 4;
@@ -348,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!warp_wait(&tempty_bar[acc.slot], acc.round ^ 1u, abort_p, p.status, p.wait_ns)) break;
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)(acc.slot * BN);
-        for (int kb = 0; kb < p.kb; ++kb, pos.next()) {
+        for (int kb = kb_first; kb < kb_end; ++kb, pos.next()) {
           if (!warp_wait(&full_bar[pos.slot], pos.round, abort_p, p.status, p.wait_ns)) {
             ok = false;
             break;
@@ -357,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t at = pos.slot * (C::kStage >> 4);
 #pragma unroll
           for (int k = 0; k < kBK / 16; ++k)
-            tc_mma_one<PAIR, false>(d, a0 + (at + k * kAStep), b0 + (at + k * kBStep), idesc, (kb | k) ? 1u : 0u);
+            tc_mma_one<PAIR, false>(d, a0 + (at + k * kAStep), b0 + (at + k * kBStep), idesc, (kb > kb_first || k > 0) ? 1u : 0u);
           tc_commit_one<PAIR>(smem_u32(&empty_bar[pos.slot]));
         }
         if (ok) tc_commit_one<PAIR>(smem_u32(&tfull_bar[acc.slot]));
@@ -370,12 +433,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= 2) {
     // ---------------- epilogue ----------------
     const uint32_t buf = smem_u32(ring) + C::kStages * C::kStage + (warp - 2) * kStageBuf;
-    if (p.f16)
+    if constexpr (SPLIT) {
+      const uint32_t parts = smem_u32(ring) + C::kStages * C::kStage + C::kBufBytes;
+      if (p.f16) epilogue_split<MODE, BN, __half>(p, tmem, part, warp, first_tile, tfull_bar, buf, parts, abort_p);
+      else epilogue_split<MODE, BN, __nv_bfloat16>(p, tmem, part, warp, first_tile, tfull_bar, buf, parts, abort_p);
+    } else if (p.f16) {
       epilogue_loop<MODE, BN, PAIR, __half>(p, tmem, rank, warp, lane, first_tile, tile_step, tfull_bar, tempty_bar, buf,
                                             abort_p);
-    else
+    } else {
       epilogue_loop<MODE, BN, PAIR, __nv_bfloat16>(p, tmem, rank, warp, lane, first_tile, tile_step, tfull_bar, tempty_bar,
                                                    buf, abort_p);
+    }
+  }
+  if constexpr (SPLIT) {
+    if (warp < 2) cluster_sync();  // the epilogue warps' barrier counts every thread
   }
   // Copies still in flight after an abort land before a CTA may leave: the barriers that count them are
   // waited for (bounded; in a normal run each completed long ago).  A peer may have issued stages whose
@@ -406,16 +477,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 int cdiv(int a, int b) { return (a + b - 1) / b; }
 
-template <int MODE, int BN, bool PAIR>
+template <int MODE, int BN, int KIND>
 cudaError_t launch(const GemmMaps &maps, const GemmParams &p, int num_sms, cudaStream_t st) {
-  using C = Cfg<MODE, BN, PAIR>;
+  using C = Cfg<MODE, BN, KIND>;
   static std::atomic<unsigned long long> done{0};
   static std::atomic<int> pairs{0};
-  return launch_tiles<PAIR>(dense_gemm_kernel<MODE, BN, PAIR>, C::kSmem, done, pairs, p.tiles, num_sms, st, maps, p);
+  if constexpr (C::SPLIT)
+    return launch_clusters(dense_gemm_kernel<MODE, BN, KIND>, C::kSmem, done, p.tiles, p.splits, kThreads, st, maps, p);
+  else
+    return launch_tiles<C::PAIR>(dense_gemm_kernel<MODE, BN, KIND>, C::kSmem, done, pairs, p.tiles, num_sms, st,
+                                 maps, p);
 }
 
 long long tiles_of(int mode, const GemmParams &p, DenseTile g) {
-  const int cols = mode == kGateUp ? g.bn / 2 : g.bn, rows = g.pair ? 2 * kBM : kBM;
+  const int cols = mode == kGateUp ? g.bn / 2 : g.bn, rows = g.kind == kPairTile ? 2 * kBM : kBM;
   return (long long)cdiv(p.m, rows) * cdiv(p.n, cols) * p.same + (long long)cdiv(p.m_last, rows) * cdiv(p.n_last, cols);
 }
 
@@ -423,7 +498,7 @@ long long tiles_of(int mode, const GemmParams &p, DenseTile g) {
 
 int gemm_b_box(int mode, DenseTile t) {
   if (mode == kHiddenGrad || mode == kInputGrad || mode == kWeightGrad) return 64;
-  return mode == kGateUp || t.pair ? t.bn / 2 : t.bn;
+  return mode == kGateUp || t.kind == kPairTile ? t.bn / 2 : t.bn;
 }
 
 // The tile that takes the least time by what tiles measured (us, 2048 to 4096 k, bf16): a k block of 64
@@ -434,22 +509,33 @@ int gemm_b_box(int mode, DenseTile t) {
 // the widest tile is not always the fastest: 4096 x 4096 columns by 4096 took 83.1 us in 256 tiles of
 // 256 columns (3.4 waves of 76 pairs), 75.6 in 304 of 224 (4.0), and 1024 rows 29.4 in one wave of
 // pairs, 34.8 in two of 128 columns.
+//
+// Few tiles with a long k leave SMs idle; then clusters of two or four CTAs share a tile's k (64 columns) and
+// exchange their sums, for 2.2 more at the start and the end.  8 rows, hidden 4096, inter 2048: the gate and
+// up projections 14.7 in single CTAs, 12.4 in clusters of two; the backward pass's first product 15.5 and, in
+// clusters of four, 11.6.
 DenseTile gemm_pick_tile(int mode, const GemmParams &p, int num_sms) {
   const bool b_mn = mode == kHiddenGrad || mode == kInputGrad || mode == kWeightGrad;
   const double per_col = mode == kGateUp ? 0.022 : mode == kHiddenGrad ? 0.032 : 0.010;
   const struct {
     DenseTile tile;
     double k_block;
-  } all[] = {{{256, true}, 0.280}, {{224, true}, 0.251}, {{192, true}, 0.222}, {{128, true}, 0.163},
-             {{256, false}, 0.339}, {{128, false}, 0.200}, {{64, false}, 0.157}, {{32, false}, 0.147}};
-  DenseTile best = {0, false};
+  } all[] = {{{256, kPairTile, 1}, 0.280}, {{224, kPairTile, 1}, 0.251}, {{192, kPairTile, 1}, 0.222},
+             {{128, kPairTile, 1}, 0.163}, {{256, kOneTile, 1}, 0.339},  {{128, kOneTile, 1}, 0.200},
+             {{64, kOneTile, 1}, 0.157},   {{32, kOneTile, 1}, 0.147},   {{64, kSplitTile, 2}, 0.157},
+             {{64, kSplitTile, 4}, 0.157}};
+  DenseTile best = {0, kOneTile, 1};
   double least = 0;
   for (const auto &c : all) {
     if (b_mn && c.tile.bn < 64) continue;
-    const long long units = c.tile.pair ? num_sms / 2 : num_sms;
+    const int splits = c.tile.splits;
+    if (splits > p.kb) continue;
+    // pairs lie on the two SMs of a pair; not every SM can be in a cluster of four
+    const long long units = c.tile.kind == kPairTile || splits == 2 ? num_sms / 2 : splits == 4 ? num_sms * 36 / 152 : num_sms;
     const long long waves = (tiles_of(mode, p, c.tile) + units - 1) / units;
-    const double epilogue = per_col * c.tile.bn, products = c.k_block * p.kb;
-    const double time = (c.tile.pair ? 5.8 : 3.8) + waves * (products > epilogue ? products : epilogue) + epilogue;
+    const double epilogue = per_col * c.tile.bn, products = c.k_block * ((p.kb + splits - 1) / splits);
+    const double time = (c.tile.kind == kPairTile ? 5.8 : c.tile.kind == kSplitTile ? 6.0 : 3.8) +
+                        waves * (products > epilogue ? products : epilogue) + epilogue;
     if (best.bn == 0 || time < least) {
       best = c.tile;
       least = time;
@@ -459,26 +545,28 @@ DenseTile gemm_pick_tile(int mode, const GemmParams &p, int num_sms) {
 }
 
 cudaError_t launch_dense_gemm(int mode, DenseTile g, const GemmMaps &maps, GemmParams p, int num_sms, cudaStream_t st) {
-  const int cols = mode == kGateUp ? g.bn / 2 : g.bn, rows = g.pair ? 2 * kBM : kBM;
+  const int cols = mode == kGateUp ? g.bn / 2 : g.bn, rows = g.kind == kPairTile ? 2 * kBM : kBM;
+  p.splits = g.splits;
   p.tiles_m = cdiv(p.m, rows);
   p.tiles_n = cdiv(p.n, cols);
   p.tiles_m_last = cdiv(p.m_last, rows);
   p.tiles_n_last = cdiv(p.n_last, cols);
   p.tiles = (int)tiles_of(mode, p, g);
-#define MOE_LAUNCH(MODE, BN, PAIR) \
-  if (mode == MODE && g.bn == BN && g.pair == PAIR) return launch<MODE, BN, PAIR>(maps, p, num_sms, st)
-#define MOE_LAUNCH_ALL(MODE)     \
-  MOE_LAUNCH(MODE, 256, true);   \
-  MOE_LAUNCH(MODE, 224, true);   \
-  MOE_LAUNCH(MODE, 192, true);   \
-  MOE_LAUNCH(MODE, 128, true);   \
-  MOE_LAUNCH(MODE, 256, false);  \
-  MOE_LAUNCH(MODE, 128, false);  \
-  MOE_LAUNCH(MODE, 64, false)
+#define MOE_LAUNCH(MODE, BN, KIND) \
+  if (mode == MODE && g.bn == BN && g.kind == KIND) return launch<MODE, BN, KIND>(maps, p, num_sms, st)
+#define MOE_LAUNCH_ALL(MODE)         \
+  MOE_LAUNCH(MODE, 256, kPairTile);  \
+  MOE_LAUNCH(MODE, 224, kPairTile);  \
+  MOE_LAUNCH(MODE, 192, kPairTile);  \
+  MOE_LAUNCH(MODE, 128, kPairTile);  \
+  MOE_LAUNCH(MODE, 256, kOneTile);   \
+  MOE_LAUNCH(MODE, 128, kOneTile);   \
+  MOE_LAUNCH(MODE, 64, kOneTile);    \
+  MOE_LAUNCH(MODE, 64, kSplitTile)
   MOE_LAUNCH_ALL(kGateUp);
-  MOE_LAUNCH(kGateUp, 32, false);
+  MOE_LAUNCH(kGateUp, 32, kOneTile);
   MOE_LAUNCH_ALL(kDown);
-  MOE_LAUNCH(kDown, 32, false);
+  MOE_LAUNCH(kDown, 32, kOneTile);
   MOE_LAUNCH_ALL(kHiddenGrad);
   MOE_LAUNCH_ALL(kInputGrad);
   MOE_LAUNCH_ALL(kWeightGrad);

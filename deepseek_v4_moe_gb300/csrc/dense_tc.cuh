@@ -56,6 +56,14 @@ __device__ __forceinline__ uint32_t in_cta(const void *p, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
   return a;
 }
+__device__ __forceinline__ uint32_t in_cta_of(uint32_t shared_addr, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(shared_addr), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ void st_cluster_128(uint32_t addr, float a, float b, float c, float d) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
+}
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
@@ -214,6 +222,25 @@ cudaError_t launch_tiles(void (*kernel)(KArgs...), size_t smem, std::atomic<unsi
   }
   const int busy = tiles < units ? tiles : units;
   cfg.gridDim = dim3(PAIR ? 2 * busy : busy);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Launches a kernel with a cluster of `ctas` CTAs for each tile.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_clusters(void (*kernel)(KArgs...), size_t smem, std::atomic<unsigned long long> &done, int tiles,
+                            int ctas, int threads, cudaStream_t st, const Args &...args) {
+  const cudaError_t e = allow_smem((const void *)kernel, smem, done);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {(unsigned)ctas, 1u, 1u};
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(tiles * ctas);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
