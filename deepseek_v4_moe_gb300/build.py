@@ -4,7 +4,8 @@
 
 Each translation unit compiles in parallel into _build/, then one shared library is linked with the
 static CUDA runtime (the driver API is reached through cudaGetDriverEntryPointByVersion, so no
-libcuda link is needed).
+libcuda link is needed).  The Python binding of the dense sublayer, _native.so, is compiled beside
+them against PyTorch's headers and linked to the library.
 """
 from __future__ import annotations
 
@@ -13,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -20,6 +22,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe_ffn.so")
+NATIVE = os.path.join(PKG, "_native.so")
 SOURCES = ["moe_ffn.cu", "prelude.cu", "decode.cu", "decode_tc.cu", "dispatch.cu", "gemm_tc.cu", "splitgemm.cu",
            "noalloc.cu", "dense.cu", "dense_norm.cu", "dense_gemm.cu",
            "dense_fp8.cu", "dense_gemv.cu"]
@@ -35,11 +38,42 @@ def nvcc() -> str:
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(NATIVE):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(NATIVE))
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
     return any(os.path.getmtime(p) > t for p in deps)
+
+
+def _torch_dir() -> str:
+    import torch
+    return os.path.dirname(torch.__file__)
+
+
+def _compile_binding(cc: str) -> str:
+    import torch
+    t = os.path.join(_torch_dir(), "include")
+    inc = [INCLUDE, t, os.path.join(t, "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"],
+           os.path.join(os.path.dirname(os.path.dirname(cc)), "include")]
+    obj = os.path.join(BUILD, "binding.o")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[a for p in inc for a in ("-I" if p == INCLUDE else "-isystem", p)],
+           "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    tmp = NATIVE + f".{os.getpid()}.tmp"
+    r = subprocess.run(["g++", "-shared", "-o", tmp, obj, "-L", PKG, "-l:libmoe_ffn.so", "-Wl,-rpath,$ORIGIN",
+                        "-L", os.path.join(_torch_dir(), "lib"), "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu",
+                        "-ltorch_python"], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of the binding failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, NATIVE)
 
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
@@ -59,13 +93,16 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
             print(r.stdout + r.stderr, file=sys.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        native = ex.submit(_compile_binding, cc)
         objs = list(ex.map(compile_one, SOURCES))
+        binding = native.result()
     tmp = LIB + f".{os.getpid()}.tmp"
     r = subprocess.run([cc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_binding(binding)
     return LIB
 
 
