@@ -355,7 +355,7 @@ cudaError_t launch(const CUtensorMap &a, const CUtensorMap &b, const Fp8Params &
   using C = Fp8Cfg<BN, PAIR>;
   static std::atomic<unsigned long long> done{0};
   static std::atomic<int> pairs{0};
-  return launch_tiles<PAIR>(fp8_matmul_kernel<BN, PAIR>, C::kSmem, done, pairs, p.tiles, num_sms, st, a, b, p);
+  return launch_tiles<PAIR>(fp8_matmul_kernel<BN, PAIR>, C::kSmem, done, pairs, p.tiles, num_sms, false, st, a, b, p);
 }
 
 // ---- quantiser ----

@@ -346,6 +346,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_base;
   volatile int *abort_p = &abort_flag;
+  pdl_trigger();
+  pdl_wait();  // from here on what the kernel before it wrote is read
 
   if (warp == 0) {
     // ---------------- TMA producer ----------------
@@ -483,10 +485,11 @@ cudaError_t launch(const GemmMaps &maps, const GemmParams &p, int num_sms, cudaS
   static std::atomic<unsigned long long> done{0};
   static std::atomic<int> pairs{0};
   if constexpr (C::SPLIT)
-    return launch_clusters(dense_gemm_kernel<MODE, BN, KIND>, C::kSmem, done, p.tiles, p.splits, kThreads, st, maps, p);
+    return launch_clusters(dense_gemm_kernel<MODE, BN, KIND>, C::kSmem, done, p.tiles, p.splits, kThreads, p.early != 0, st,
+                           maps, p);
   else
-    return launch_tiles<C::PAIR>(dense_gemm_kernel<MODE, BN, KIND>, C::kSmem, done, pairs, p.tiles, num_sms, st,
-                                 maps, p);
+    return launch_tiles<C::PAIR>(dense_gemm_kernel<MODE, BN, KIND>, C::kSmem, done, pairs, p.tiles, num_sms,
+                                 p.early != 0, st, maps, p);
 }
 
 long long tiles_of(int mode, const GemmParams &p, DenseTile g) {

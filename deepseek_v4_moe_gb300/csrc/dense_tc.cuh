@@ -195,21 +195,24 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
 }
 
 // Launches a kernel over `tiles` tiles: one CTA, or one pair of CTAs, on each SM (pair) that has work.
+// early: its CTAs may start, and wait in pdl_wait, while the kernel before it on the stream ends.
 template <bool PAIR, typename... KArgs, typename... Args>
 cudaError_t launch_tiles(void (*kernel)(KArgs...), size_t smem, std::atomic<unsigned long long> &done,
-                         std::atomic<int> &pairs, int tiles, int num_sms, cudaStream_t st, const Args &...args) {
+                         std::atomic<int> &pairs, int tiles, int num_sms, bool early, cudaStream_t st, const Args &...args) {
   const cudaError_t e = allow_smem((const void *)kernel, smem, done);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim = {PAIR ? 2u : 1u, 1u, 1u};
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = attr;
-  cfg.numAttrs = PAIR ? 1 : 0;
+  cfg.numAttrs = 1;
   int units = num_sms;
   if constexpr (PAIR) {  // pairs that run at one time
     units = pairs.load(std::memory_order_relaxed);
@@ -222,25 +225,28 @@ cudaError_t launch_tiles(void (*kernel)(KArgs...), size_t smem, std::atomic<unsi
   }
   const int busy = tiles < units ? tiles : units;
   cfg.gridDim = dim3(PAIR ? 2 * busy : busy);
+  cfg.numAttrs = early ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 // Launches a kernel with a cluster of `ctas` CTAs for each tile.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_clusters(void (*kernel)(KArgs...), size_t smem, std::atomic<unsigned long long> &done, int tiles,
-                            int ctas, int threads, cudaStream_t st, const Args &...args) {
+                            int ctas, int threads, bool early, cudaStream_t st, const Args &...args) {
   const cudaError_t e = allow_smem((const void *)kernel, smem, done);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim = {(unsigned)ctas, 1u, 1u};
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(tiles * ctas);
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = early ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
