@@ -3,7 +3,7 @@
 //
 // A warp takes one output column (a row of the weight matrix; for the gate and up projections the same
 // row of both) and a share of k; lane l of it takes 16 bytes of every 512.  All loads of a warp's share
-// are issued before the first product where they fit 8 rounds, so that a few warps on each SM keep
+// are issued before the first product where they fit kRounds rounds, so that a few warps on each SM keep
 // enough bytes in flight.  The columns' shares of k meet in shared memory.
 //
 // The down projection is launched while the gate and up kernel still runs (programmatic dependent
@@ -16,15 +16,18 @@
 namespace moe {
 namespace {
 
-constexpr int kWarps = 8, kRounds = 8;  // warps of a CTA; 16-byte loads of a matrix in flight in a lane
+// Warps of a CTA, and 16-byte loads of a matrix in flight in a lane.  Eight of each took 15.4 us for the gated
+// block on one token (hidden 4096, inter 2048), where registers left the SMs half their warps; four of each
+// 13.5.
+constexpr int kWarps = 4, kRounds = 4;
 
 template <typename T>
-__device__ __forceinline__ void unpack8(const uint4 w, float (&o)[8]) {
+__device__ __forceinline__ void unpack8(const uint4 w, float2 (&o)[4]) {
   const T *tag = nullptr;
-  unpack2(w.x, o[0], o[1], tag);
-  unpack2(w.y, o[2], o[3], tag);
-  unpack2(w.z, o[4], o[5], tag);
-  unpack2(w.w, o[6], o[7], tag);
+  unpack2(w.x, o[0].x, o[0].y, tag);
+  unpack2(w.y, o[1].x, o[1].y, tag);
+  unpack2(w.z, o[2].x, o[2].y, tag);
+  unpack2(w.w, o[3].x, o[3].y, tag);
 }
 
 // the sum over a column's `splits` warps of K values; valid in the column's first warp
@@ -56,9 +59,9 @@ __global__ void __launch_bounds__(32 * kWarps) gated_gemv_kernel(const __grid_co
   const T *w[2] = {static_cast<const T *>(p.w[0]) + (size_t)col * p.k,
                    UP ? static_cast<const T *>(p.w[1]) + (size_t)col * p.k : nullptr};
   if (UP) pdl_trigger();
-  float sum[M * R];
+  float2 sums[M * R];  // two running sums of each product: an instruction takes a pair
 #pragma unroll
-  for (int i = 0; i < M * R; ++i) sum[i] = 0.f;
+  for (int i = 0; i < M * R; ++i) sums[i] = make_float2(0.f, 0.f);
   bool first = true;
   for (int k0 = part * 256 + lane * 8; first || k0 < p.k; k0 += step * kRounds) {
     uint4 f[M][kRounds];
@@ -73,21 +76,24 @@ __global__ void __launch_bounds__(32 * kWarps) gated_gemv_kernel(const __grid_co
     for (int i = 0; i < kRounds; ++i) {
       const int k = k0 + i * step;
       if (k < p.k) {
-        float a[M][8];
+        float2 a[M][4];
 #pragma unroll
         for (int m = 0; m < M; ++m) unpack8<T>(f[m][i], a[m]);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-          float b[8];
+          float2 b[4];
           unpack8<T>(*reinterpret_cast<const uint4 *>(static_cast<const T *>(p.x) + r * p.ld_x + k), b);
 #pragma unroll
           for (int m = 0; m < M; ++m)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sum[m * R + r] = fmaf(a[m][e], b[e], sum[m * R + r]);
+            for (int e = 0; e < 4; ++e) sums[m * R + r] = __ffma2_rn(a[m][e], b[e], sums[m * R + r]);
         }
       }
     }
   }
+  float sum[M * R];
+#pragma unroll
+  for (int i = 0; i < M * R; ++i) sum[i] = sums[i].x + sums[i].y;
   join_splits(sum, p.splits, buf);
   if (!in || part != 0 || lane != 0) return;
 #pragma unroll
@@ -115,12 +121,12 @@ __device__ __forceinline__ float2 code_pair(uint32_t w, bool e5m2) {
     asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %1;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n}" : "=r"(h) : "r"(w));
   return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
-__device__ __forceinline__ void codes16(const uint4 w, bool e5m2, float (&o)[16]) {
+__device__ __forceinline__ void codes16(const uint4 w, bool e5m2, float2 (&o)[8]) {
   const uint32_t q[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 a = code_pair(q[i], e5m2), b = code_pair(q[i] >> 16, e5m2);
-    o[4 * i] = a.x, o[4 * i + 1] = a.y, o[4 * i + 2] = b.x, o[4 * i + 3] = b.y;
+    o[2 * i] = code_pair(q[i], e5m2);
+    o[2 * i + 1] = code_pair(q[i] >> 16, e5m2);
   }
 }
 
@@ -147,17 +153,17 @@ __global__ void __launch_bounds__(32 * kWarps) fp8_gemv_kernel(const __grid_cons
     for (int i = 0; i < kRounds; ++i) {
       const int k = k0 + i * step;
       if (in && k < p.k) {
-        float b[16];
+        float2 b[8];
         codes16(f[i], p.b_e5m2, b);
         const int blk = k / kScaleBlock;
         const float scale = sb[blk];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-          float a[16], dot = 0.f;
+          float2 a[8], dot = make_float2(0.f, 0.f);
           codes16(*reinterpret_cast<const uint4 *>(p.a + r * p.ld_a + k), p.a_e5m2, a);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) dot = fmaf(a[e], b[e], dot);
-          sum[r] = fmaf(dot, scale * p.a_scale[(size_t)r * p.kb + blk], sum[r]);
+          for (int e = 0; e < 8; ++e) dot = __ffma2_rn(a[e], b[e], dot);
+          sum[r] = fmaf(dot.x + dot.y, scale * p.a_scale[(size_t)r * p.kb + blk], sum[r]);
         }
       }
     }
