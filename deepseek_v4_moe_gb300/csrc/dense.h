@@ -96,7 +96,7 @@ struct Fp8Params {
   long long ld_out;
   int wide;                  // out can be written in 16-byte pieces
   int a_rows;                // rows of A's boxes (see a_box)
-  int tiles_m, tiles_n, tiles;  // set by launch_fp8_matmul
+  int tiles_m, tiles_n, tiles, splits;  // set by launch_fp8_matmul
   int *status;
   uint64_t wait_ns;
   int inject;

@@ -28,14 +28,17 @@
 namespace moe {
 namespace {
 
-template <int BN, bool PAIR>
+template <int BN, int KIND>
 struct Fp8Cfg {
+  static constexpr bool PAIR = KIND == kPairTile, SPLIT = KIND == kSplitTile;
   static constexpr int kABytes = kBM * kScaleBlock;
   static constexpr int kBRows = PAIR ? BN / 2 : BN;  // of B in this CTA
   static constexpr int kStage = kABytes + kBRows * kScaleBlock;
   static constexpr int kBufBytes = kEpiWarps * kStageBuf;
-  static constexpr int kStages = (kRingBytes - kBufBytes) / kStage;
-  static constexpr size_t kSmem = (size_t)kStages * kStage + kBufBytes + 1024;
+  // what the other CTAs of a split tile send of this CTA's rows
+  static constexpr int kPartBytes = SPLIT ? (kSplitMax - 1) * 32 * BN * 4 : 0;
+  static constexpr int kStages = (kRingBytes - kBufBytes - kPartBytes) / kStage;
+  static constexpr size_t kSmem = (size_t)kStages * kStage + kBufBytes + kPartBytes + 1024;
   static constexpr int kAcc = BN > 128 ? 2 : 4;  // TMEM buffers, one block's sums each
   static constexpr int kTmemCols = BN > 64 ? 512 : kAcc * BN;  // a power of two
   static constexpr int kPer = BN / 2;            // columns of one epilogue warp
@@ -165,11 +168,12 @@ __device__ __forceinline__ void store_rows(const Fp8Params &p, int row0, int col
   }
 }
 
-template <int BN, bool PAIR>
+template <int BN, int KIND>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_matmul_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                       const __grid_constant__ Fp8Params p) {
-  using C = Fp8Cfg<BN, PAIR>;
+  using C = Fp8Cfg<BN, KIND>;
+  constexpr bool PAIR = C::PAIR, SPLIT = C::SPLIT;
   constexpr int kRows = PAIR ? 2 * kBM : kBM;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -179,8 +183,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ int abort_flag, issued;
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const uint32_t rank = PAIR ? cluster_rank() : 0u;
-  const int first_tile = PAIR ? blockIdx.x >> 1 : blockIdx.x, tile_step = PAIR ? gridDim.x >> 1 : gridDim.x;
+  const uint32_t rank = PAIR ? cluster_rank() : 0u;  // in the pair
+  const int share = SPLIT ? (int)cluster_rank() : 0;  // of k
+  const int first_tile = PAIR ? blockIdx.x >> 1 : SPLIT ? blockIdx.x / p.splits : blockIdx.x;
+  const int tile_step = PAIR ? gridDim.x >> 1 : SPLIT ? p.tiles : gridDim.x;
+  const int kb_first = SPLIT ? share * p.kb / p.splits : 0, kb_end = SPLIT ? (share + 1) * p.kb / p.splits : p.kb;
   const uint32_t stage_bytes = C::kStage - (kBM - p.a_rows) * kScaleBlock;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
@@ -203,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if constexpr (PAIR) cluster_sync();  // the peer's barriers are initialised
+  if constexpr (PAIR || SPLIT) cluster_sync();  // the other CTAs run, and their barriers are initialised
   tc_fence_after();
   const uint32_t tmem = tmem_base;
   volatile int *abort_p = &abort_flag;
@@ -218,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int m, n;
       band_tile(t, p.tiles_m, p.tiles_n, m, n);
       const int m0 = m * kRows + (int)rank * kBM, n0 = n * BN + (int)rank * C::kBRows;
-      for (int kb = 0; kb < p.kb; ++kb, ++j, pos.next()) {
+      for (int kb = kb_first; kb < kb_end; ++kb, ++j, pos.next()) {
         const int s = pos.slot;
         if (!warp_wait(&empty_bar[s], pos.round ^ 1u, abort_p, p.status, p.wait_ns)) {
           ok = false;
@@ -242,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       RingPos<C::kAcc> acc;
       bool ok = true;
       for (int t = first_tile; ok && t < p.tiles; t += tile_step) {
-        for (int kb = 0; kb < p.kb; ++kb, pos.next(), acc.next()) {
+        for (int kb = kb_first; kb < kb_end; ++kb, pos.next(), acc.next()) {
           if (!warp_wait(&tempty_bar[acc.slot], acc.round ^ 1u, abort_p, p.status, p.wait_ns) ||
               !warp_wait(&full_bar[pos.slot], pos.round, abort_p, p.status, p.wait_ns)) {
             ok = false;
@@ -282,10 +289,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       float sum[C::kPer];
 #pragma unroll
       for (int i = 0; i < C::kPer; ++i) sum[i] = 0.f;
-      float next_a = sa[0], next_b = sb[0], next_b2 = sb2[0];
-      for (int kb = 0; kb < p.kb; ++kb, acc.next()) {
+      float next_a = sa[kb_first], next_b = sb[kb_first], next_b2 = sb2[kb_first];
+      for (int kb = kb_first; kb < kb_end; ++kb, acc.next()) {
         const uint64_t s1 = both(next_a * next_b), s2 = both(next_a * next_b2);
-        if (kb + 1 < p.kb) {
+        if (kb + 1 < kb_end) {
           next_a = sa[kb + 1];
           next_b = sb[kb + 1];
           next_b2 = sb2[kb + 1];
@@ -318,12 +325,41 @@ __global__ void __launch_bounds__(kThreads, 1)
             fma2(sum[c * C::kChunk + i], sum[c * C::kChunk + i + 1], s, v[c & 1][i], v[c & 1][i + 1]);
         }
       }
+      if constexpr (SPLIT) {
+        // Lane quarter q of the rows belongs to CTA q * splits / 4: it adds the others' sums to its own, in
+        // the order of their ranks.
+        const int owner = q * p.splits / 4, first_q = owner * 4 / p.splits;
+        const uint32_t parts = smem_u32(ring) + C::kStages * C::kStage + C::kBufBytes +
+                               (q - first_q) * (p.splits - 1) * 32 * BN * 4;
+        auto part_at = [&](int s, int four) { return ((s * (BN / 4) + half * (C::kPer / 4) + four) * 32 + lane) * 16; };
+        if (ok && owner != share) {
+          const uint32_t to = in_cta_of(parts, owner);
+#pragma unroll
+          for (int i = 0; i < C::kPer / 4; ++i)
+            st_cluster_128(to + part_at(share < owner ? share : share - 1, i), sum[4 * i], sum[4 * i + 1], sum[4 * i + 2],
+                           sum[4 * i + 3]);
+        }
+        cluster_sync();  // every part has arrived
+        if (owner != share) break;
+        for (int s = 0; s < p.splits - 1; ++s)
+#pragma unroll
+          for (int i = 0; i < C::kPer / 4; ++i) {
+            const uint4 w = lds128(parts + part_at(s, i));
+            sum[4 * i] += __uint_as_float(w.x);
+            sum[4 * i + 1] += __uint_as_float(w.y);
+            sum[4 * i + 2] += __uint_as_float(w.z);
+            sum[4 * i + 3] += __uint_as_float(w.w);
+          }
+      }
       if (!ok) break;
       if (p.out_type == kF32) store_rows<float>(p, row0, col, buf, sum);
       else if (p.out_type == kBF16) store_rows<__nv_bfloat16>(p, row0, col, buf, sum);
       else store_rows<__half>(p, row0, col, buf, sum);
       __syncwarp();
     }
+  }
+  if constexpr (SPLIT) {
+    if (warp < 2) cluster_sync();  // the epilogue warps' barrier counts every thread
   }
   // Copies still in flight after an abort land before a CTA may leave (bounded; in a normal run each has
   // landed long ago).  A peer may have issued stages whose arrival the leader still owes.
@@ -350,12 +386,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int BN, bool PAIR>
+template <int BN, int KIND>
 cudaError_t launch(const CUtensorMap &a, const CUtensorMap &b, const Fp8Params &p, int num_sms, cudaStream_t st) {
-  using C = Fp8Cfg<BN, PAIR>;
+  using C = Fp8Cfg<BN, KIND>;
   static std::atomic<unsigned long long> done{0};
   static std::atomic<int> pairs{0};
-  return launch_tiles<PAIR>(fp8_matmul_kernel<BN, PAIR>, C::kSmem, done, pairs, p.tiles, num_sms, false, st, a, b, p);
+  if constexpr (C::SPLIT)
+    return launch_clusters(fp8_matmul_kernel<BN, KIND>, C::kSmem, done, p.tiles, p.splits, kThreads, false, st, a, b, p);
+  else
+    return launch_tiles<C::PAIR>(fp8_matmul_kernel<BN, KIND>, C::kSmem, done, pairs, p.tiles, num_sms, false, st, a, b, p);
 }
 
 // ---- quantiser ----
@@ -512,13 +551,17 @@ DenseTile fp8_pick_tile(const Fp8Params &p, int num_sms) {
     DenseTile tile;
     double k_block;
   } all[] = {{{256, kPairTile, 1}, 0.47}, {{224, kPairTile, 1}, 0.42}, {{128, kPairTile, 1}, 0.28},
-             {{128, kOneTile, 1}, 0.305}, {{64, kOneTile, 1}, 0.265}, {{32, kOneTile, 1}, 0.26}};
+             {{128, kOneTile, 1}, 0.305}, {{64, kOneTile, 1}, 0.265}, {{32, kOneTile, 1}, 0.26},
+             {{64, kSplitTile, 2}, 0.265}, {{64, kSplitTile, 4}, 0.265}};
   DenseTile best = {0, kOneTile, 1};
   double least = 0;
   for (const auto &c : all) {
-    const long long units = c.tile.kind == kPairTile ? num_sms / 2 : num_sms;
+    const int splits = c.tile.splits;
+    if (splits > p.kb) continue;
+    const long long units = c.tile.kind == kPairTile || splits == 2 ? num_sms / 2 : splits == 4 ? num_sms * 36 / 152 : num_sms;
     const long long waves = (fp8_tiles(p, c.tile) + units - 1) / units;
-    const double time = (c.tile.kind == kPairTile ? 4.0 : 3.5) + waves * c.k_block * p.kb + 0.012 * c.tile.bn;
+    const double time = (c.tile.kind == kPairTile ? 4.0 : c.tile.kind == kSplitTile ? 5.5 : 3.5) +
+                        waves * c.k_block * ((p.kb + splits - 1) / splits) + 0.012 * c.tile.bn;
     if (best.bn == 0 || time < least) {
       best = c.tile;
       least = time;
@@ -532,12 +575,17 @@ cudaError_t launch_fp8_matmul(DenseTile t, const CUtensorMap &a, const CUtensorM
   p.tiles_m = (p.m + (t.kind == kPairTile ? 2 : 1) * kBM - 1) / ((t.kind == kPairTile ? 2 : 1) * kBM);
   p.tiles_n = (p.n + t.bn - 1) / t.bn;
   p.tiles = p.tiles_m * p.tiles_n;
-  if (t.bn == 256 && t.kind == kPairTile) return launch<256, true>(a, b, p, num_sms, st);
-  if (t.bn == 224 && t.kind == kPairTile) return launch<224, true>(a, b, p, num_sms, st);
-  if (t.bn == 128 && t.kind == kPairTile) return launch<128, true>(a, b, p, num_sms, st);
-  if (t.bn == 128) return launch<128, false>(a, b, p, num_sms, st);
-  if (t.bn == 64) return launch<64, false>(a, b, p, num_sms, st);
-  if (t.bn == 32) return launch<32, false>(a, b, p, num_sms, st);
+  p.splits = t.splits;
+#define MOE_LAUNCH(BN, KIND) \
+  if (t.bn == BN && t.kind == KIND) return launch<BN, KIND>(a, b, p, num_sms, st)
+  MOE_LAUNCH(256, kPairTile);
+  MOE_LAUNCH(224, kPairTile);
+  MOE_LAUNCH(128, kPairTile);
+  MOE_LAUNCH(128, kOneTile);
+  MOE_LAUNCH(64, kOneTile);
+  MOE_LAUNCH(32, kOneTile);
+  MOE_LAUNCH(64, kSplitTile);
+#undef MOE_LAUNCH
   return cudaErrorInvalidValue;
 }
 
