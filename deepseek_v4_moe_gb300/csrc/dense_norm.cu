@@ -526,12 +526,14 @@ __global__ void __launch_bounds__(kBwdThreads)
 }
 
 // Adds the partial rows: job 0 and 1 the norm weights' over the CTAs, job 2 + i gate row i's over its
-// chunks (a gate of one row: over the CTAs).  A CTA takes 32 columns; its 32 warps take every 32nd partial row, and the first warp
-// adds their 32 sums in order.
+// chunks (a gate of one row: over the CTAs).  A CTA takes 32 columns; its warps take every kPartWarps-th
+// partial row, and the first warp adds their sums in order.  (Of 32 warps, few CTAs fit on an SM: 9 us where
+// these take 4.)
+constexpr int kPartWarps = 8;
 template <typename TB>
-__global__ void __launch_bounds__(1024)
+__global__ void __launch_bounds__(32 * kPartWarps)
     norm_partials_kernel(const __grid_constant__ NormParams p, const __grid_constant__ NormBwdPlan pl) {
-  __shared__ float buf[32][33];
+  __shared__ float buf[kPartWarps][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
   pdl_wait();  // launched while the kernel that writes the partial rows runs
   for (int job = blockIdx.y; job < pl.jobs; job += gridDim.y) {
@@ -549,14 +551,14 @@ __global__ void __launch_bounds__(1024)
     float a = 0.f;
     if (col < p.hidden)
 #pragma unroll 8
-      for (int i = warp; i < count; i += 32) a += src[(size_t)i * p.hidden + col];
+      for (int i = warp; i < count; i += kPartWarps) a += src[(size_t)i * p.hidden + col];
     __syncthreads();
     buf[warp][lane] = a;
     __syncthreads();
     if (warp == 0 && col < p.hidden) {
       a = 0.f;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) a += buf[i][lane];
+      for (int i = 0; i < kPartWarps; ++i) a += buf[i][lane];
       if (job == 0) p.d_w_next[col] = a;
       else if (job == 1) p.d_w_post[col] = a;
       else if (p.gate_type == kF32) static_cast<float *>(p.d_gate)[(size_t)(job - 2) * p.hidden + col] = a;
@@ -635,7 +637,7 @@ cudaError_t backward_typed(const NormParams &p, int num_sms, cudaStream_t st) {
                                      : backward_launch<TS, TB, true, false>(p, pl, st);
   if (e != cudaSuccess || pl.floats == 0) return e;
   const dim3 grid((p.hidden + 31) / 32, pl.jobs < 1024 ? pl.jobs : 1024);
-  return launch_pdl(norm_partials_kernel<TB>, grid, dim3(1024), 0, st, p, pl);
+  return launch_pdl(norm_partials_kernel<TB>, grid, dim3(32 * kPartWarps), 0, st, p, pl);
 }
 
 }  // namespace
