@@ -523,7 +523,7 @@ cudaError_t quantise_typed(const QuantiseParams &p, int num_sms, cudaStream_t st
   const long long blocks = (p.k + kScaleBlock - 1) / kScaleBlock;
   if (p.tall == 1) {
     const long long per_row = (blocks + kQuantBlocks - 1) / kQuantBlocks;
-    const long long ctas = (p.rows * per_row + 15) / 16, most = (long long)num_sms * 8;
+    const long long ctas = (p.rows * per_row + 15) / 16, most = (long long)num_sms * 3;  // those that an SM holds
     const int grid = (int)(ctas < most ? ctas : most);
     if (p.wide) quantise_rows_kernel<T, true><<<grid, 256, 0, st>>>(p);
     else quantise_rows_kernel<T, false><<<grid, 256, 0, st>>>(p);
