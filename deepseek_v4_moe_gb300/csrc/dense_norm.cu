@@ -306,11 +306,14 @@ struct Weights {
     for (int v = 0; v < kSets; ++v)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const int col = 8 * (v * n + t) + 4 * k;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (col < hidden) x = w ? *reinterpret_cast<const float4 *>(w + col) : make_float4(absent, absent, absent, absent);
-        sts128(base + ((which * kSets + v) * 2 + k) * n * 16, make_uint4(__float_as_uint(x.x), __float_as_uint(x.y),
-                                                                          __float_as_uint(x.z), __float_as_uint(x.w)));
+        float x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int col = VEC ? 8 * (v * n + t) + 4 * k + e : (v * 8 + 4 * k + e) * n + t;
+          x[e] = col >= hidden ? 0.f : w ? w[col] : absent;
+        }
+        sts128(base + ((which * kSets + v) * 2 + k) * n * 16, make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]),
+                                                                          __float_as_uint(x[2]), __float_as_uint(x[3])));
       }
   }
   __device__ __forceinline__ Pairs get(const float *w, int which, int hidden, float absent, int v) const {
@@ -632,7 +635,7 @@ template <typename TS, typename TB>
 cudaError_t backward_typed(const NormParams &p, int num_sms, cudaStream_t st) {
   const NormBwdPlan pl = norm_bwd_plan(p, num_sms);
   const bool beside = kBwdSmem - 2 * kSets * 2 * (size_t)pl.threads * 16 >= 2 * (size_t)Rows<TS, TB, true>::kRow;
-  const cudaError_t e = !all_wide(p) ? backward_launch<TS, TB, false, false>(p, pl, st)
+  const cudaError_t e = !all_wide(p) ? backward_launch<TS, TB, false, true>(p, pl, st)
                         : beside     ? backward_launch<TS, TB, true, true>(p, pl, st)
                                      : backward_launch<TS, TB, true, false>(p, pl, st);
   if (e != cudaSuccess || pl.floats == 0) return e;

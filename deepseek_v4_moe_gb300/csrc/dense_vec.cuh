@@ -54,10 +54,16 @@ template <typename T, bool VEC>
 struct Eight {
   T v[8];
   __device__ __forceinline__ void load(const T *row, int t, int n, int hidden) {
+    const T *q = row + t;
+    if (7 * n + t < hidden) {  // most threads' columns all exist
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int c = e * n + t;
-      v[e] = c < hidden ? row[c] : from_f32<T>(0.f);
+      for (int e = 0; e < 8; ++e, q += n) v[e] = *q;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int c = e * n + t;
+        v[e] = c < hidden ? row[c] : from_f32<T>(0.f);
+      }
     }
   }
   __device__ __forceinline__ void get(float (&o)[8]) const {
@@ -65,10 +71,16 @@ struct Eight {
     for (int e = 0; e < 8; ++e) o[e] = to_f32(v[e]);
   }
   static __device__ __forceinline__ void store(T *row, int t, int n, int hidden, const float (&o)[8]) {
+    T *q = row + t;
+    if (7 * n + t < hidden) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int c = e * n + t;
-      if (c < hidden) row[c] = from_f32<T>(o[e]);
+      for (int e = 0; e < 8; ++e, q += n) *q = from_f32<T>(o[e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int c = e * n + t;
+        if (c < hidden) row[c] = from_f32<T>(o[e]);
+      }
     }
   }
 };
