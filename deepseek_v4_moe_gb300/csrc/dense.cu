@@ -47,20 +47,25 @@ int current_sms() {
   return sms;
 }
 
-// A tensor argument's memory: `rows` rows of `cols` elements, `ld` elements apart.
+// A tensor argument's memory: `rows` rows of `cols` elements, `ld` elements apart; width and pitch in bytes.
 struct Span {
   const void *p;
-  uintptr_t end;
+  uintptr_t end, width, pitch;
   int64_t ld;
   const char *name;
 };
 Span span(const char *name, const void *p, int64_t rows, int64_t cols, int64_t ld, int bytes) {
   const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-  return Span{p, p && rows > 0 ? a + (uintptr_t)((rows - 1) * ld + cols) * bytes : a, ld, name};
+  return Span{p, p && rows > 0 ? a + (uintptr_t)((rows - 1) * ld + cols) * bytes : a, (uintptr_t)cols * bytes,
+              (uintptr_t)ld * bytes, ld, name};
 }
 bool overlap(const Span &a, const Span &b) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-  return a.p && b.p && x < b.end && y < a.end;
+  if (!(a.p && b.p && x < b.end && y < a.end)) return false;
+  if (a.pitch != b.pitch || a.pitch == 0) return true;
+  // rows at the same distance, as of two column ranges of one tensor: b's begin this far into a's pitch
+  const uintptr_t into = y >= x ? (y - x) % a.pitch : (a.pitch - (x - y) % a.pitch) % a.pitch;
+  return into < a.width || into + b.width > a.pitch;
 }
 // An output may overlap no input and no other output, but for the one input it may be itself.
 int check_overlaps(const char *who, const Span *outs, int n_outs, const Span *ins, int n_ins, int same_out, int same_in) {

@@ -302,7 +302,7 @@ int moe_ffn_set_fault_injection(moe_ffn_handle *h, int32_t which, uint32_t wait_
  * The same sublayer without hyper-connections and without routing: a dense layer, a shared expert
  * on its own, a draft head's layer.  These entry points take no handle.  Tensor arguments are
  * device pointers of the current device, rows contiguous, consecutive rows `ld_*` elements apart
- * (ld >= the row's length).  Calls enqueue on `stream` and return without waiting; each call that
+ * (ld >= the row's length; column ranges of one tensor do not overlap).  Calls enqueue on `stream` and return without waiting; each call that
  * needs scratch takes it as `workspace`, which must not be in use by another call meanwhile (give
  * graphs that may run together workspaces of their own).  They can be captured into CUDA graphs.
  * All sums are in f32 and no atomics are used: the same call gives the same bits.  On an error

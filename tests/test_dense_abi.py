@@ -157,3 +157,27 @@ def test_fp8_quantise_refuses(lib, kw, code):
 def test_fp8_null(lib):
     assert lib.moe_ffn_fp8_matmul(None, None) == _lib.ERR_NULL_PTR
     assert lib.moe_ffn_fp8_quantise(None, None) == _lib.ERR_NULL_PTR
+
+
+# ---- column ranges of one tensor are apart, though their rows lie between one another ----
+
+@pytest.mark.parametrize("kw", [
+    dict(), dict(state=A + 1024, out=A), dict(y=A + 4096 - 512), dict(state=A + 4096 + 2048, out=A, y=A + 1024)])
+def test_column_ranges_of_one_tensor(lib, kw):
+    # bytes: state f32 of 1024 in a pitch of 4096, out behind it, y of 512 behind that; nothing refuses them, and
+    # the call ends where its device would have to be looked up
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("would launch on addresses that are not memory")
+    args = dict(rows=4, ld_state=1024, state=A, out=A + 1024, ld_out=1024, y=A + 2048, ld_y=2048)
+    args.update(kw)
+    assert lib.moe_ffn_block_norm(ctypes.byref(_norm(**args)), None) in (_lib.ERR_CUDA, _lib.ERR_UNSUPPORTED)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(out=A + 1020), dict(out=A + 4), dict(out=A + 4096 - 1020), dict(out=A + 4096 + 4), dict(out=A - 4),
+    dict(y=A + 1022), dict(y=A + 2046), dict(y=A + 4096 - 510)])
+def test_column_ranges_that_overlap(lib, kw):
+    args = dict(rows=4, ld_state=1024, state=A, out=A + 1024, ld_out=1024, y=A + 2048, ld_y=2048)
+    args.update(kw)
+    assert lib.moe_ffn_block_norm(ctypes.byref(_norm(**args)), None) == _lib.ERR_ALIAS
