@@ -163,7 +163,8 @@ bool encode_map(CUtensorMap *m, const void *base, int bytes, int64_t inner, int6
 int check_norm(const char *who, const moe_ffn_block_norm_args *a) {
   if (!a) return fail(MOE_FFN_ERR_NULL_PTR, "%s: args is NULL", who);
   if (a->rows == 0) return fail(MOE_FFN_ERR_ROWS_ZERO, "%s: rows must be at least 1", who);
-  if (a->rows < 0) return fail(MOE_FFN_ERR_ROWS_RANGE, "%s: rows is negative", who);
+  // a group of rows past the last, or the rows of all CTAs, added to a row's number stay below 2^31
+  if (a->rows < 0 || a->rows > (1 << 30)) return fail(MOE_FFN_ERR_ROWS_RANGE, "%s: rows must be at most 2^30", who);
   if (a->hidden < 1 || a->hidden > moe::kNormHiddenMax)
     return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: hidden must be in 1..%d", who, moe::kNormHiddenMax);
   if (!is_type(a->block_type) || (a->stream_type != MOE_FFN_F32 && a->stream_type != a->block_type))

@@ -181,3 +181,9 @@ def test_column_ranges_that_overlap(lib, kw):
     args = dict(rows=4, ld_state=1024, state=A, out=A + 1024, ld_out=1024, y=A + 2048, ld_y=2048)
     args.update(kw)
     assert lib.moe_ffn_block_norm(ctypes.byref(_norm(**args)), None) == _lib.ERR_ALIAS
+
+
+def test_block_norm_rows_past_the_limit(lib):
+    for rows in (2 ** 30 + 1, 2 ** 31 - 1):
+        assert lib.moe_ffn_block_norm(ctypes.byref(_norm(rows=rows)), None) == _lib.ERR_ROWS_RANGE
+        assert lib.moe_ffn_block_norm_workspace(ctypes.byref(_norm(rows=rows)), ctypes.byref(_grads())) == _lib.ERR_ROWS_RANGE
