@@ -5,6 +5,7 @@
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/utils/pybind.h>
 
 #include <optional>
@@ -26,6 +27,7 @@ PyObject *g_error = nullptr;  // MoeFFNError
 
 void check(int64_t rc) {
   if (rc >= 0) return;
+  if (!g_error) throw std::runtime_error(moe_ffn_last_error(nullptr));
   const py::object e = py::reinterpret_borrow<py::object>(g_error)(rc, moe_ffn_last_error(nullptr));
   PyErr_SetObject(g_error, e.ptr());
   throw py::error_already_set();
@@ -367,12 +369,13 @@ Tensor fp8_matmul(const Tensor &a, const Tensor &a_scale, const Tensor &b, const
 
 }  // namespace
 
+// wrap_pybind_function: errors of PyTorch's own (a failed allocation) keep their Python types
 PYBIND11_MODULE(_native, m) {
   m.def("set_error", [](py::object cls) { g_error = cls.release().ptr(); });
-  m.def("block_norm", &block_norm);
-  m.def("block_norm_backward", &block_norm_backward);
-  m.def("gated_ffn", &gated_ffn);
-  m.def("gated_ffn_backward", &gated_ffn_backward);
-  m.def("fp8_quantise", &fp8_quantise);
-  m.def("fp8_matmul", &fp8_matmul);
+  m.def("block_norm", torch::wrap_pybind_function(&block_norm));
+  m.def("block_norm_backward", torch::wrap_pybind_function(&block_norm_backward));
+  m.def("gated_ffn", torch::wrap_pybind_function(&gated_ffn));
+  m.def("gated_ffn_backward", torch::wrap_pybind_function(&gated_ffn_backward));
+  m.def("fp8_quantise", torch::wrap_pybind_function(&fp8_quantise));
+  m.def("fp8_matmul", torch::wrap_pybind_function(&fp8_matmul));
 }

@@ -6,6 +6,7 @@
 #include <stdio.h>
 
 #include <atomic>
+#include <mutex>
 
 #include "dense.h"
 #include "kernels.h"
@@ -581,6 +582,11 @@ extern "C" int moe_ffn_dense_status(void *stream) {
   int rc = pending(who);
   if (rc) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(st, &capture) == cudaSuccess && capture != cudaStreamCaptureStatusNone)
+    return fail(MOE_FFN_ERR_UNSUPPORTED, "%s: the stream is being captured", who);
+  static std::mutex one_at_a_time;  // g_status_out holds one call's bits until they are copied
+  const std::lock_guard<std::mutex> lock(one_at_a_time);
   take_status_kernel<<<1, 1, 0, st>>>();
   int bits = 0;
   cudaError_t e = cudaGetLastError();

@@ -20,8 +20,8 @@
 //
 // A CTA (one per SM, persistent over the tiles) makes tiles of 128 x BN:
 //   warp 0     TMA producer: a ring of 64-wide k blocks of A (128 rows) and B (BN rows)
-//   warp 1     TMEM allocator and MMA issuer (one thread)
-//   warps 2-9  epilogue: two warps for each TMEM lane quarter, each every other 16 columns; the
+//   warp 1     TMEM allocator and MMA issuer
+//   warps 2-9  epilogue: two warps for each TMEM lane quarter, each every other 32 columns; the
 //              accumulator is double buffered, so the next tile's MMAs run under it
 // kGateUp makes BN / 2 columns of g and the same of u side by side in one accumulator, so the
 // activation and the product need no second pass.

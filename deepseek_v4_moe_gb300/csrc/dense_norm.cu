@@ -470,10 +470,12 @@ __global__ void __launch_bounds__(kBwdThreads)
     }
     float sums[6] = {ss.x + ss.y, sw.x + sw.y, sf.x + sf.y, qo.x + qo.y, qg.x + qg.y, qs.x + qs.y};
     group_sums(sums, n, buf, turn);
-    const float rs = p.w_next ? rsqrtf(fmaf(sums[0], inv, p.eps)) : 0.f, cs = rs * rs * rs * (sums[1] * inv);
+    // (rs and rf are multiplied to the sums one at a time: a cube of theirs leaves f32's range where rows of
+    // 1e13 or, with a small eps, 1e-13 do not)
+    const float rs = p.w_next ? rsqrtf(fmaf(sums[0], inv, p.eps)) : 0.f, cs = rs * (rs * (rs * (sums[1] * inv)));
     const float rf = p.w_post ? rsqrtf(fmaf(sums[2], inv, p.eps)) : 1.f;
     const float q_ds = fmaf(-cs, sums[5], fmaf(rs, sums[4], sums[3]));
-    const float scale = p.scale * token, cf = p.w_post ? scale * (rf * rf * rf) * (q_ds * inv) : 0.f;
+    const float scale = p.scale * token, cf = p.w_post ? scale * (rf * (rf * (rf * (q_ds * inv)))) : 0.f;
 #pragma unroll
     for (int v = 0; v < kSets; ++v) {
       const Pairs s = rows.state(p, v), gy = mul(rows.d_y(p, v), rs);

@@ -2,7 +2,8 @@
 include/moe_ffn.h; the checks and the marshalling are in the compiled binding (csrc/binding.cpp).
 
 Every function enqueues on ``stream`` (default: the tensors' device's current stream) and returns
-device tensors without waiting.  Outputs and workspaces that a call allocates belong to that stream.
+device tensors without waiting.  Outputs and workspaces that a call allocates belong to that stream;
+inputs that belong to another one stay with the caller until the call's kernels have run.
 Gradients come from explicit ``*_backward`` calls; nothing is recorded for autograd.  Rows may be
 strided (``stride(-1) == 1``); weights and gates are contiguous.  Refused arguments raise
 ``ValueError`` (types, shapes), ``TypeError`` (no tensor) or ``MoeFFNError`` with the library's code.
@@ -91,7 +92,8 @@ def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down:
     """The gated feed-forward block: y = (act(x w_gate^T) * (x w_up^T)) w_down^T.
 
     ``x`` [rows, hidden] bfloat16 or float16; ``w_gate``, ``w_up`` [inter, hidden] and ``w_down``
-    [hidden, inter] of its type; hidden and inter multiples of 8.  ``activation``: "silu" or "gelu"
+    [hidden, inter] of its type; hidden and inter multiples of 8, every tensor 16-byte aligned and row
+    strides multiples of 8.  ``activation``: "silu" or "gelu"
     (tanh form).  Returns y [rows, hidden]; with ``save`` also the pair (g, u) of projections
     [rows, inter] that :func:`gated_ffn_backward` takes.
     """
@@ -134,7 +136,8 @@ def fp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale:
                stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """a b^T of FP8 operands with float32 scales for blocks of 128: ``a`` [rows, k] with ``a_scale``
     [rows, ceil(k / 128)], ``b`` [n, k] with ``b_scale`` [ceil(n / 128), ceil(k / 128)] (see
-    :func:`fp8_quantise`; each float8_e4m3fn or float8_e5m2), k a multiple of 16.  Sums are float32; the
+    :func:`fp8_quantise`; each float8_e4m3fn or float8_e5m2), k and both row strides multiples of 16, both
+    16-byte aligned.  Sums are float32; the
     result is ``out_dtype``: float32, bfloat16 or float16.
     """
     if stream is not None:

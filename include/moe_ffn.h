@@ -387,8 +387,7 @@ typedef struct moe_ffn_gated_args {
 
 /* Every pointer 16-byte aligned, every ld a multiple of 8.  Returns MOE_FFN_OK, NULL_PTR, ROWS_ZERO,
  * ROWS_RANGE, BAD_CONFIG (sizes, type, activation, ld), ALIGNMENT, ALIAS (an output or the workspace
- * overlaps another tensor), NO_MEMORY (workspace too small), UNSUPPORTED or CUDA.  The first call on
- * each device looks up library memory: make it before any stream capture. */
+ * overlaps another tensor), NO_MEMORY (workspace too small), UNSUPPORTED or CUDA. */
 int moe_ffn_gated_forward(const moe_ffn_gated_args *a, void *stream);
 int moe_ffn_gated_backward(const moe_ffn_gated_args *a, void *stream);
 
@@ -414,7 +413,7 @@ typedef struct moe_ffn_fp8_matmul_args {
 } moe_ffn_fp8_matmul_args;
 
 /* Returns MOE_FFN_OK, NULL_PTR, ROWS_ZERO, ROWS_RANGE, BAD_CONFIG, ALIGNMENT, ALIAS, UNSUPPORTED or
- * CUDA.  The first call on each device looks up library memory: make it before any stream capture. */
+ * CUDA. */
 int moe_ffn_fp8_matmul(const moe_ffn_fp8_matmul_args *a, void *stream);
 
 /* Makes such an operand: a block is block_rows (1 or 128) rows x 128 columns, those at the ends may be
@@ -436,7 +435,8 @@ typedef struct moe_ffn_fp8_quantise_args {
 int moe_ffn_fp8_quantise(const moe_ffn_fp8_quantise_args *a, void *stream);
 
 /* Device status bits (MOE_FFN_DEV_TIMEOUT) that the dense sublayer's kernels set on the current device
- * since the previous call, after waiting for `stream`; then cleared.  Or a negative code. */
+ * since the previous call, after waiting for `stream` (which must not be under capture); then cleared.
+ * Each set of bits is reported to one caller.  Or a negative code. */
 int moe_ffn_dense_status(void *stream);
 
 /* Test hook for failure detection, as moe_ffn_set_fault_injection: with enable != 0, CTA 0 of each
