@@ -69,7 +69,7 @@ def _compile_binding(cc: str) -> str:
 def _link_binding(obj: str) -> None:
     tmp = NATIVE + f".{os.getpid()}.tmp"
     r = subprocess.run(["g++", "-shared", "-o", tmp, obj, "-L", PKG, "-l:libmoe_ffn.so", "-Wl,-rpath,$ORIGIN",
-                        "-L", os.path.join(_torch_dir(), "lib"), "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu",
+                        "-L", os.path.join(_torch_dir(), "lib"), "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_cuda",
                         "-ltorch_python"], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link of the binding failed:\n{r.stdout}\n{r.stderr}")

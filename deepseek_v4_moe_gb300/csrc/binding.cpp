@@ -2,6 +2,7 @@
 // the tensors, outputs and workspaces from PyTorch's allocator, the current stream, and the call.  The
 // checks take a few tenths of a microsecond here; through ctypes they took longer than a token's kernels.
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -103,7 +104,7 @@ int32_t size32(const char *name, int64_t n) {
 }
 
 Tensor fresh(const Where &w, at::IntArrayRef shape, ScalarType type) {
-  return at::empty(shape, at::TensorOptions().dtype(type).device(w.device));
+  return Tensor(at::detail::empty_cuda(shape, at::TensorOptions().dtype(type).device(w.device)));
 }
 
 // ---- block_norm ----

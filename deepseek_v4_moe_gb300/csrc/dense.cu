@@ -372,7 +372,6 @@ extern "C" int moe_ffn_gated_forward(const moe_ffn_gated_args *a, void *stream) 
   up.c[1] = a->gate;
   up.c[2] = a->up;
   moe::GemmParams down = gemm_params(a, dev, a->rows, a->hidden, kblocks(a->inter));
-  down.early = 1;
   down.c[0] = a->y;
   down.ldc[0] = a->ld_y;
   const moe::DenseTile tu = moe::gemm_pick_tile(moe::kGateUp, up, sms), td = moe::gemm_pick_tile(moe::kDown, down, sms);
@@ -435,7 +434,6 @@ extern "C" int moe_ffn_gated_backward(const moe_ffn_gated_args *a, void *stream)
   cudaError_t e = moe::launch_dense_gemm(moe::kHiddenGrad, moe::gemm_pick_tile(moe::kHiddenGrad, hid, sms), m, hid, sms, st);
   if (e == cudaSuccess && a->d_x) {
     moe::GemmParams p = gemm_params(a, dev, a->rows, a->hidden, 2 * kblocks(a->inter));
-    p.early = 1;
     p.kb0 = kblocks(a->inter);
     p.c[0] = a->d_x;
     p.ldc[0] = a->ld_d_x;
@@ -446,7 +444,6 @@ extern "C" int moe_ffn_gated_backward(const moe_ffn_gated_args *a, void *stream)
   }
   if (e == cudaSuccess && weights) {
     moe::GemmParams p = gemm_params(a, dev, a->inter, a->hidden, kblocks(a->rows));
-    p.early = 1;
     p.same = 2;
     p.a_rows = 128;
     p.m_last = a->hidden;

@@ -61,7 +61,6 @@ struct GemmParams {
   long long ldc[3];
   const void *e[2];    // kHiddenGrad: the saved g and u
   int act, f16;
-  int early;           // follows another of these kernels, which it reads
   int a_rows;          // rows of a K-major A's boxes (128 for an MN-major one); see a_box
   int *status;
   uint64_t wait_ns;

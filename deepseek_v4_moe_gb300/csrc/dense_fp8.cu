@@ -24,6 +24,7 @@
 #include "dense.h"
 #include "dense_tc.cuh"
 #include "dense_vec.cuh"
+#include "kernels.h"
 
 namespace moe {
 namespace {
@@ -214,6 +215,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_base;
   volatile int *abort_p = &abort_flag;
+  pdl_trigger();
+  pdl_wait();  // from here on what the kernel before it wrote is read
 
   if (warp == 0) {
     // ---------------- TMA producer ----------------
@@ -392,9 +395,9 @@ cudaError_t launch(const CUtensorMap &a, const CUtensorMap &b, const Fp8Params &
   static std::atomic<unsigned long long> done{0};
   static std::atomic<int> pairs{0};
   if constexpr (C::SPLIT)
-    return launch_clusters(fp8_matmul_kernel<BN, KIND>, C::kSmem, done, p.tiles, p.splits, kThreads, false, st, a, b, p);
+    return launch_clusters(fp8_matmul_kernel<BN, KIND>, C::kSmem, done, p.tiles, p.splits, kThreads, st, a, b, p);
   else
-    return launch_tiles<C::PAIR>(fp8_matmul_kernel<BN, KIND>, C::kSmem, done, pairs, p.tiles, num_sms, false, st, a, b, p);
+    return launch_tiles<C::PAIR>(fp8_matmul_kernel<BN, KIND>, C::kSmem, done, pairs, p.tiles, num_sms, st, a, b, p);
 }
 
 // ---- quantiser ----
@@ -466,6 +469,7 @@ __global__ void __launch_bounds__(256) quantise_rows_kernel(const __grid_constan
   long long row = first / per_row;
   int group = (int)(first % per_row);
   const int rows_on = step / per_row, groups_on = step % per_row;
+  pdl_wait();
   // whole warps stay in the loop for the shuffles: a half warp past the end works on nothing
   while (__any_sync(0xffffffffu, row < p.rows)) {
     const int r = row < p.rows ? (int)row : p.rows, b0 = group * kQuantBlocks;
@@ -502,6 +506,7 @@ __global__ void __launch_bounds__(256) quantise_tiles_kernel(const __grid_consta
   const int row = tile_row * kScaleBlock + (threadIdx.x >> 4), col = b * kScaleBlock + (threadIdx.x & 15) * 8;
   float v[8][8];
   uint32_t m = 0u;
+  pdl_wait();
 #pragma unroll
   for (int i = 0; i < 8; ++i) load_part<T, WIDE>(p, row + 16 * i, col, v[i]);
 #pragma unroll
@@ -525,14 +530,10 @@ cudaError_t quantise_typed(const QuantiseParams &p, int num_sms, cudaStream_t st
     const long long per_row = (blocks + kQuantBlocks - 1) / kQuantBlocks;
     const long long ctas = (p.rows * per_row + 15) / 16, most = (long long)num_sms * 3;  // those that an SM holds
     const int grid = (int)(ctas < most ? ctas : most);
-    if (p.wide) quantise_rows_kernel<T, true><<<grid, 256, 0, st>>>(p);
-    else quantise_rows_kernel<T, false><<<grid, 256, 0, st>>>(p);
-  } else {
-    const int grid = (int)((p.rows + kScaleBlock - 1) / kScaleBlock * blocks);
-    if (p.wide) quantise_tiles_kernel<T, true><<<grid, 256, 0, st>>>(p);
-    else quantise_tiles_kernel<T, false><<<grid, 256, 0, st>>>(p);
+    return launch_pdl(p.wide ? quantise_rows_kernel<T, true> : quantise_rows_kernel<T, false>, dim3(grid), dim3(256), 0, st, p);
   }
-  return cudaGetLastError();
+  const int grid = (int)((p.rows + kScaleBlock - 1) / kScaleBlock * blocks);
+  return launch_pdl(p.wide ? quantise_tiles_kernel<T, true> : quantise_tiles_kernel<T, false>, dim3(grid), dim3(256), 0, st, p);
 }
 
 long long fp8_tiles(const Fp8Params &p, DenseTile t) {

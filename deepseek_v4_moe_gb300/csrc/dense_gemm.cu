@@ -485,11 +485,10 @@ cudaError_t launch(const GemmMaps &maps, const GemmParams &p, int num_sms, cudaS
   static std::atomic<unsigned long long> done{0};
   static std::atomic<int> pairs{0};
   if constexpr (C::SPLIT)
-    return launch_clusters(dense_gemm_kernel<MODE, BN, KIND>, C::kSmem, done, p.tiles, p.splits, kThreads, p.early != 0, st,
-                           maps, p);
+    return launch_clusters(dense_gemm_kernel<MODE, BN, KIND>, C::kSmem, done, p.tiles, p.splits, kThreads, st, maps, p);
   else
-    return launch_tiles<C::PAIR>(dense_gemm_kernel<MODE, BN, KIND>, C::kSmem, done, pairs, p.tiles, num_sms,
-                                 p.early != 0, st, maps, p);
+    return launch_tiles<C::PAIR>(dense_gemm_kernel<MODE, BN, KIND>, C::kSmem, done, pairs, p.tiles, num_sms, st,
+                                 maps, p);
 }
 
 long long tiles_of(int mode, const GemmParams &p, DenseTile g) {

@@ -58,7 +58,10 @@ __global__ void __launch_bounds__(32 * kWarps) gated_gemv_kernel(const __grid_co
   const int step = 256 * p.splits;
   const T *w[2] = {static_cast<const T *>(p.w[0]) + (size_t)col * p.k,
                    UP ? static_cast<const T *>(p.w[1]) + (size_t)col * p.k : nullptr};
-  if (UP) pdl_trigger();
+  if (UP) {
+    pdl_trigger();  // the down projection's CTAs come and fetch their weights
+    pdl_wait();
+  }
   float2 sums[M * R];  // two running sums of each product: an instruction takes a pair
 #pragma unroll
   for (int i = 0; i < M * R; ++i) sums[i] = make_float2(0.f, 0.f);
@@ -144,6 +147,7 @@ __global__ void __launch_bounds__(32 * kWarps) fp8_gemv_kernel(const __grid_cons
   float sum[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) sum[r] = 0.f;
+  pdl_wait();
   for (int k0 = part * 512 + lane * 16; k0 < p.k; k0 += step * kRounds) {
     uint4 f[kRounds];
 #pragma unroll
@@ -185,10 +189,6 @@ int splits_for(int k, int per_round) {
 template <bool UP, int R, typename T>
 cudaError_t launch_rows(const GemvParams &p, cudaStream_t st) {
   const int cols = kWarps / p.splits, grid = (p.n + cols - 1) / cols;
-  if (UP) {
-    gated_gemv_kernel<UP, R, T><<<grid, 32 * kWarps, 0, st>>>(p);
-    return cudaGetLastError();
-  }
   return launch_pdl(gated_gemv_kernel<UP, R, T>, dim3(grid), dim3(32 * kWarps), 0, st, p);
 }
 template <bool UP, typename T>
@@ -205,10 +205,10 @@ cudaError_t launch_typed(const GemvParams &p, int rows, cudaStream_t st) {
 template <int R>
 cudaError_t fp8_rows(const Fp8GemvParams &p, int out_type, cudaStream_t st) {
   const int cols = kWarps / p.splits, grid = (p.n + cols - 1) / cols;
-  if (out_type == kF32) fp8_gemv_kernel<R, float><<<grid, 32 * kWarps, 0, st>>>(p);
-  else if (out_type == kBF16) fp8_gemv_kernel<R, __nv_bfloat16><<<grid, 32 * kWarps, 0, st>>>(p);
-  else fp8_gemv_kernel<R, __half><<<grid, 32 * kWarps, 0, st>>>(p);
-  return cudaGetLastError();
+  auto kernel = out_type == kF32    ? fp8_gemv_kernel<R, float>
+                : out_type == kBF16 ? fp8_gemv_kernel<R, __nv_bfloat16>
+                                    : fp8_gemv_kernel<R, __half>;
+  return launch_pdl(kernel, dim3(grid), dim3(32 * kWarps), 0, st, p);
 }
 
 }  // namespace

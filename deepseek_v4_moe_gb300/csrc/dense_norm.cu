@@ -144,6 +144,7 @@ __global__ void __launch_bounds__(512) block_norm_kernel(const __grid_constant__
   const float inv = 1.f / (float)p.hidden;
   int turn = 0;
   const int step = gridDim.x * groups;
+  pdl_wait();
   for (int base = blockIdx.x * groups; base < p.rows; base += step) {
     const int row = base + group;
     const bool in = row < p.rows;
@@ -390,6 +391,7 @@ __global__ void __launch_bounds__(kBwdThreads)
   weights.t = t;
   weights.n = n;
   if constexpr (VEC) rows.clear(pl.depth);
+  pdl_wait();
   if constexpr (WSMEM) {
     weights.fill(p.w_next, 0, p.hidden, 0.f);
     weights.fill(p.w_post, 1, p.hidden, 1.f);
@@ -601,11 +603,8 @@ cudaError_t forward_typed(const NormParams &p, int num_sms, cudaStream_t st) {
   const int n = group_threads(p.hidden), threads = n < 256 ? 256 : n, groups = threads / n;
   const int blocks = (p.rows + groups - 1) / groups, most = num_sms * (1024 / threads);
   const int grid = blocks < most ? blocks : most;
-  if (all_wide(p))
-    block_norm_kernel<TS, TB, true><<<grid, threads, 0, st>>>(p, n);
-  else
-    block_norm_kernel<TS, TB, false><<<grid, threads, 0, st>>>(p, n);
-  return cudaGetLastError();
+  return launch_pdl(all_wide(p) ? block_norm_kernel<TS, TB, true> : block_norm_kernel<TS, TB, false>, dim3(grid),
+                    dim3(threads), 0, st, p, n);
 }
 
 // The ring takes up to three rows of every group.  The weights go beside it unless that leaves less than
@@ -624,8 +623,7 @@ cudaError_t backward_launch(const NormParams &p, NormBwdPlan pl, cudaStream_t st
   auto go = [&](auto kernel, std::atomic<unsigned long long> &done) {
     const cudaError_t e = allow_smem((const void *)kernel, kBwdSmem, done);
     if (e != cudaSuccess) return e;
-    kernel<<<pl.ctas, kBwdThreads, smem, st>>>(p, pl);
-    return cudaGetLastError();
+    return launch_pdl(kernel, dim3(pl.ctas), dim3(kBwdThreads), smem, st, p, pl);
   };
   static std::atomic<unsigned long long> done[3];
   if (!p.f || p.gate_kind != kGateVector) return go(block_norm_backward_kernel<TS, TB, VEC, WSMEM, NoGate>, done[0]);

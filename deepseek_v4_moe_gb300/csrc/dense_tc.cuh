@@ -195,10 +195,10 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
 }
 
 // Launches a kernel over `tiles` tiles: one CTA, or one pair of CTAs, on each SM (pair) that has work.
-// early: its CTAs may start, and wait in pdl_wait, while the kernel before it on the stream ends.
+// Its CTAs may start, and wait in pdl_wait, while the kernel before it on the stream ends.
 template <bool PAIR, typename... KArgs, typename... Args>
 cudaError_t launch_tiles(void (*kernel)(KArgs...), size_t smem, std::atomic<unsigned long long> &done,
-                         std::atomic<int> &pairs, int tiles, int num_sms, bool early, cudaStream_t st, const Args &...args) {
+                         std::atomic<int> &pairs, int tiles, int num_sms, cudaStream_t st, const Args &...args) {
   const cudaError_t e = allow_smem((const void *)kernel, smem, done);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
@@ -225,14 +225,14 @@ cudaError_t launch_tiles(void (*kernel)(KArgs...), size_t smem, std::atomic<unsi
   }
   const int busy = tiles < units ? tiles : units;
   cfg.gridDim = dim3(PAIR ? 2 * busy : busy);
-  cfg.numAttrs = early ? 2 : 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 // Launches a kernel with a cluster of `ctas` CTAs for each tile.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_clusters(void (*kernel)(KArgs...), size_t smem, std::atomic<unsigned long long> &done, int tiles,
-                            int ctas, int threads, bool early, cudaStream_t st, const Args &...args) {
+                            int ctas, int threads, cudaStream_t st, const Args &...args) {
   const cudaError_t e = allow_smem((const void *)kernel, smem, done);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
@@ -246,7 +246,7 @@ cudaError_t launch_clusters(void (*kernel)(KArgs...), size_t smem, std::atomic<u
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = attr;
-  cfg.numAttrs = early ? 2 : 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 

@@ -280,3 +280,63 @@ def test_memory_that_is_not_there(cuda_lib):
     with pytest.raises(torch.cuda.OutOfMemoryError):
         m.gated_ffn(x, wg, wg, wd, save=True)
     assert not m.gated_ffn(x[:64], wg, wg, wd).any() and m.dense_status() == 0
+
+
+def test_what_comes_before_and_after_on_the_stream(cuda_lib):
+    """Kernels start while the one before them ends: each still reads what copies, fills, kernels and other
+    streams' work before it wrote, and is done before what follows it writes."""
+    import deepseek_v4_moe_gb300 as m
+    rows, h = 2048, 2048
+    host = [torch.randn(rows, h, generator=torch.Generator().manual_seed(i)).to(BF16).pin_memory() for i in range(3)]
+    _, wg, wu, wd, _ = tg.make(1, h, 512, BF16, seed=1)
+    w = torch.ones(h, device="cuda")
+
+    def ops(x):
+        s, y = m.block_norm(x, norm_next=w)
+        few = m.gated_ffn(x[:2], wg, wu, wd)
+        f = m.gated_ffn(y, wg, wu, wd)
+        q = m.fp8_quantise(f)
+        return [few, f, *q, m.fp8_matmul(*q, *m.fp8_quantise(wg, block_rows=128)),
+                *m.block_norm_backward(s, norm_next=w, d_y=f).values()]
+
+    want = [[t.clone() for t in ops(t.cuda())] for t in host]
+    torch.cuda.synchronize()
+    x, x2 = torch.empty(2, rows, h, device="cuda", dtype=BF16).unbind()
+    side = torch.cuda.Stream()
+
+    def chain():
+        got = []
+        for i, t in enumerate(host):
+            x.copy_(t, non_blocking=True)          # a copy before
+            got.append((i, ops(x)))
+            x.zero_()                              # a fill after
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):          # a kernel of another stream before, joined by an event
+                x2.copy_(t, non_blocking=True)
+                x2.mul_(1.0)
+            torch.cuda.current_stream().wait_stream(side)
+            got.append((i, ops(x2)))
+            x2.fill_(float("nan"))
+            x2.copy_(x)                            # zeros, by a kernel
+            x.copy_(host[(i + 1) % 3], non_blocking=True)
+            got.append(((i + 1) % 3, ops(x)))
+        return got
+
+    def check(got):
+        torch.cuda.synchronize()
+        for i, g in got:
+            assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(g, want[i])), i
+
+    for _ in range(3):
+        check(chain())
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = chain()
+    for _ in range(3):
+        for _, t in got:
+            for v in t:
+                v.view(torch.uint8).zero_()
+        g.replay()
+        check(got)
+    assert m.dense_status() == 0
