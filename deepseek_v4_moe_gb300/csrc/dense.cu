@@ -289,19 +289,19 @@ int check_rows_of(const char *who, const char *name, const void *p, int64_t ld, 
   return MOE_FFN_OK;
 }
 
-moe::GemmParams gemm_params(const moe_ffn_gated_args *a, const DeviceSide &d, int m, int n, int kb) {
+moe::GemmParams gemm_params(const moe_ffn_gated_args *a, const DeviceSide &d) {
   moe::GemmParams p = {};
-  p.m = m;
-  p.n = n;
-  p.same = 1;
-  p.kb0 = p.kb = kb;
   p.act = a->activation;
   p.f16 = a->type == MOE_FFN_F16;
-  p.a_rows = moe::a_box(m);
+  p.a_rows = moe::a_box(a->rows);
+  p.odd_rows = a->hidden % 64 != 0 || a->inter % 64 != 0 || a->ld_x % 64 != 0;
   p.status = d.status;
   p.wait_ns = d.wait_ns;
   p.inject = d.inject;
   return p;
+}
+void add_problem(moe::GemmParams &p, int m, int n, int kb0, int kb, int a, int b, bool a_mn, void *c, int64_t ldc) {
+  p.problem[p.problems++] = moe::GemmProblem{m, n, kb0, kb, a, b, a_mn, 0, 0, 0, c, ldc};
 }
 
 // inter columns of a row of the workspace's buffers: h forward; dg, du and h backward
@@ -367,14 +367,15 @@ extern "C" int moe_ffn_gated_forward(const moe_ffn_gated_args *a, void *stream) 
   }
   DeviceSide dev;
   if ((rc = device_side(who, &dev))) return rc;
-  moe::GemmParams up = gemm_params(a, dev, a->rows, a->inter, kblocks(a->hidden));
-  up.c[0] = a->workspace;
-  up.c[1] = a->gate;
-  up.c[2] = a->up;
-  moe::GemmParams down = gemm_params(a, dev, a->rows, a->hidden, kblocks(a->inter));
-  down.c[0] = a->y;
-  down.ldc[0] = a->ld_y;
-  const moe::DenseTile tu = moe::gemm_pick_tile(moe::kGateUp, up, sms), td = moe::gemm_pick_tile(moe::kDown, down, sms);
+  const int kh = kblocks(a->hidden), ki = kblocks(a->inter);
+  moe::GemmParams up = gemm_params(a, dev), down = up;
+  add_problem(up, a->rows, a->inter, kh, kh, 0, 0, false, nullptr, 0);
+  up.out[0] = a->workspace;
+  up.out[1] = a->gate;
+  up.out[2] = a->up;
+  add_problem(down, a->rows, a->hidden, ki, ki, 0, 0, false, a->y, a->ld_y);
+  double t;
+  const moe::DenseTile tu = moe::gemm_pick_tile(moe::kGateUp, up, sms, &t), td = moe::gemm_pick_tile(moe::kDown, down, sms, &t);
   const int bu = moe::gemm_b_box(moe::kGateUp, tu), bd = moe::gemm_b_box(moe::kDown, td);
   moe::GemmMaps mu, md;
   if (!encode_map(&mu.a[0], a->x, 2, H, R, a->ld_x, up.a_rows) || !encode_map(&mu.b[0], a->w_gate, 2, H, I, H, bu) ||
@@ -422,45 +423,44 @@ extern "C" int moe_ffn_gated_backward(const moe_ffn_gated_args *a, void *stream)
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   char *dg = static_cast<char *>(a->workspace), *du = dg + R * I * 2, *h = du + R * I * 2;
 
-  moe::GemmMaps m;
-  moe::GemmParams hid = gemm_params(a, dev, a->rows, a->inter, kblocks(a->hidden));
-  hid.c[0] = dg;
-  hid.c[1] = du;
-  hid.c[2] = h;
+  const int kh = kblocks(a->hidden), ki = kblocks(a->inter), kr = kblocks(a->rows);
+  moe::GemmMaps mh, mg;
+  moe::GemmParams hid = gemm_params(a, dev), all = hid, dx = hid, dw = hid;
+  add_problem(hid, a->rows, a->inter, kh, kh, 0, 0, false, nullptr, 0);
+  hid.out[0] = dg;
+  hid.out[1] = du;
+  hid.out[2] = h;
   hid.e[0] = a->gate;
   hid.e[1] = a->up;
-  if (!encode_map(&m.a[0], a->d_y, 2, H, R, a->ld_d_y, hid.a_rows) || !encode_map(&m.b[0], a->w_down, 2, I, H, I, 64))
+  double t, t_all, t_dx, t_dw;
+  const moe::DenseTile th = moe::gemm_pick_tile(moe::kHiddenGrad, hid, sms, &t);
+  if (!encode_map(&mh.a[0], a->d_y, 2, H, R, a->ld_d_y, hid.a_rows) || !encode_map(&mh.b[0], a->w_down, 2, I, H, I, 64) ||
+      !encode_map(&mg.a[0], dg, 2, I, R, I, hid.a_rows) || !encode_map(&mg.a[1], du, 2, I, R, I, hid.a_rows) ||
+      !encode_map(&mg.a[2], dg, 2, I, R, I, 64) || !encode_map(&mg.a[3], du, 2, I, R, I, 64) ||
+      !encode_map(&mg.a[4], a->d_y, 2, H, R, a->ld_d_y, 64) || !encode_map(&mg.b[0], a->w_gate, 2, H, I, H, 64) ||
+      !encode_map(&mg.b[1], a->w_up, 2, H, I, H, 64) || !encode_map(&mg.b[2], a->x, 2, H, R, a->ld_x, 64) ||
+      !encode_map(&mg.b[3], h, 2, I, R, I, 64))
     return fail(MOE_FFN_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", who);
-  cudaError_t e = moe::launch_dense_gemm(moe::kHiddenGrad, moe::gemm_pick_tile(moe::kHiddenGrad, hid, sms), m, hid, sms, st);
-  if (e == cudaSuccess && a->d_x) {
-    moe::GemmParams p = gemm_params(a, dev, a->rows, a->hidden, 2 * kblocks(a->inter));
-    p.kb0 = kblocks(a->inter);
-    p.c[0] = a->d_x;
-    p.ldc[0] = a->ld_d_x;
-    if (!encode_map(&m.a[0], dg, 2, I, R, I, p.a_rows) || !encode_map(&m.a[1], du, 2, I, R, I, p.a_rows) ||
-        !encode_map(&m.b[0], a->w_gate, 2, H, I, H, 64) || !encode_map(&m.b[1], a->w_up, 2, H, I, H, 64))
-      return fail(MOE_FFN_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", who);
-    e = moe::launch_dense_gemm(moe::kInputGrad, moe::gemm_pick_tile(moe::kInputGrad, p, sms), m, p, sms, st);
+  if (a->d_x) add_problem(dx, a->rows, a->hidden, ki, 2 * ki, 0, 0, false, a->d_x, a->ld_d_x);
+  dw.a_rows = 128;  // its A is MN-major
+  if (weights) {
+    add_problem(dw, a->inter, a->hidden, kr, kr, 2, 2, true, a->d_w_gate, H);
+    add_problem(dw, a->inter, a->hidden, kr, kr, 3, 2, true, a->d_w_up, H);
+    add_problem(dw, a->hidden, a->inter, kr, kr, 4, 3, true, a->d_w_down, I);
   }
-  if (e == cudaSuccess && weights) {
-    moe::GemmParams p = gemm_params(a, dev, a->inter, a->hidden, kblocks(a->rows));
-    p.same = 2;
-    p.a_rows = 128;
-    p.m_last = a->hidden;
-    p.n_last = a->inter;
-    p.c[0] = a->d_w_gate;
-    p.c[1] = a->d_w_up;
-    p.c[2] = a->d_w_down;
-    p.ldc[0] = p.ldc[1] = H;
-    p.ldc[2] = I;
-    if (!encode_map(&m.a[0], dg, 2, I, R, I, 64) || !encode_map(&m.a[1], du, 2, I, R, I, 64) ||
-        !encode_map(&m.a[2], a->d_y, 2, H, R, a->ld_d_y, 64) || !encode_map(&m.b[0], a->x, 2, H, R, a->ld_x, 64) ||
-        !encode_map(&m.b[2], h, 2, I, R, I, 64))
-      return fail(MOE_FFN_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", who);
-    m.b[1] = m.b[0];
-    e = moe::launch_dense_gemm(moe::kWeightGrad, moe::gemm_pick_tile(moe::kWeightGrad, p, sms), m, p, sms, st);
+  // one launch for all, the tiles with more k first, unless two take less time
+  for (const moe::GemmParams *p : {2 * ki >= kr ? &dx : &dw, 2 * ki >= kr ? &dw : &dx})
+    for (int i = 0; i < p->problems; ++i) all.problem[all.problems++] = p->problem[i];
+  const moe::DenseTile ta = moe::gemm_pick_tile(moe::kGrads, all, sms, &t_all);
+  cudaError_t e = moe::launch_dense_gemm(moe::kHiddenGrad, th, mh, hid, sms, st);
+  if (e == cudaSuccess && dx.problems && dw.problems) {
+    const moe::DenseTile tx = moe::gemm_pick_tile(moe::kGrads, dx, sms, &t_dx), tw = moe::gemm_pick_tile(moe::kGrads, dw, sms, &t_dw);
+    if (t_dx + t_dw < t_all) {
+      e = moe::launch_dense_gemm(moe::kGrads, tx, mg, dx, sms, st);
+      return launched(who, e == cudaSuccess ? moe::launch_dense_gemm(moe::kGrads, tw, mg, dw, sms, st) : e);
+    }
   }
-  return launched(who, e);
+  return launched(who, e == cudaSuccess ? moe::launch_dense_gemm(moe::kGrads, ta, mg, all, sms, st) : e);
 }
 
 extern "C" int moe_ffn_fp8_matmul(const moe_ffn_fp8_matmul_args *a, void *stream) {

@@ -44,24 +44,33 @@ cudaError_t launch_block_norm_backward(const NormParams &p, int num_sms, cudaStr
 
 // ---- the gated block's matrix products (dense_gemm.cu) ----
 
-enum GemmMode : int { kGateUp = 0, kDown = 1, kHiddenGrad = 2, kInputGrad = 3, kWeightGrad = 4 };
+enum GemmMode : int { kGateUp = 0, kDown = 1, kHiddenGrad = 2, kGrads = 3 };
 enum Activation : int { kSilu = 0, kGelu = 1 };
 
 struct GemmMaps {
-  CUtensorMap a[3], b[3];
+  CUtensorMap a[5], b[4];
 };
 
+// A product of a launch: c [m, n] = the sum over its pairs of matrices, a[a] b[b] over k blocks 0 .. kb0 - 1,
+// a[a + 1] b[b + 1] over those from kb0 on.
+struct GemmProblem {
+  int m, n, kb0, kb, a, b;
+  int a_mn;                   // A is MN-major (kGrads)
+  int tiles_m, tiles_n, end;  // set by launch_dense_gemm; end: its last tile's number plus one
+  void *c;
+  long long ldc;
+};
+constexpr int kMaxProblems = 4;
+
 struct GemmParams {
-  int m, n, same;      // output of problems 0 .. same-1
-  int m_last, n_last;  // output of problem `same` (kWeightGrad; zero: there is none)
-  int kb0, kb;         // k blocks of the first pair of matrices, and in all
-  int splits;          // CTAs that share a tile's k; set by launch_dense_gemm
-  int tiles_m, tiles_n, tiles_m_last, tiles_n_last, tiles;  // set by launch_dense_gemm
-  void *c[3];
-  long long ldc[3];
-  const void *e[2];    // kHiddenGrad: the saved g and u
+  GemmProblem problem[kMaxProblems];
+  int problems, tiles;  // tiles: set by launch_dense_gemm
+  int splits;           // CTAs that share a tile's k; set by launch_dense_gemm
+  void *out[3];         // kGateUp: h, g, u; kHiddenGrad: dg, du, h
+  const void *e[2];     // kHiddenGrad: the saved g and u
   int act, f16;
-  int a_rows;          // rows of a K-major A's boxes (128 for an MN-major one); see a_box
+  int a_rows;           // rows of a K-major A's boxes; see a_box
+  int odd_rows;         // a matrix has rows that are no multiple of 128 bytes
   int *status;
   uint64_t wait_ns;
   int inject;
@@ -80,7 +89,8 @@ struct DenseTile {
   int bn, kind, splits;
 };
 int gemm_b_box(int mode, DenseTile tile);  // rows of B's boxes
-DenseTile gemm_pick_tile(int mode, const GemmParams &p, int num_sms);
+// the fastest tile for a launch, and the time that it should take in us
+DenseTile gemm_pick_tile(int mode, const GemmParams &p, int num_sms, double *time);
 cudaError_t launch_dense_gemm(int mode, DenseTile tile, const GemmMaps &maps, GemmParams p, int num_sms, cudaStream_t st);
 
 // ---- FP8 with block scales (dense_fp8.cu) ----

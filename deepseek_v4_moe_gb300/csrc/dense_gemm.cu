@@ -4,8 +4,7 @@
 //   forward    g = x Wg^T, u = x Wu^T, h = act(g) u                        kGateUp
 //              y = h Wd^T                                                  kDown
 //   backward   dh = dy Wd;  dg = dh u act'(g), du = dh act(g), h again     kHiddenGrad
-//              dx = dg Wg + du Wu                                          kInputGrad
-//              dWg = dg^T x, dWu = du^T x, dWd = dy^T h  (one launch)      kWeightGrad
+//              dx = dg Wg + du Wu;  dWg = dg^T x, dWu = du^T x, dWd = dy^T h     kGrads
 //
 // Every operand is read from the caller's row-major matrices by TMA as it lies: a matrix whose
 // contraction runs along its rows' elements is a K-major operand (boxes of 64 k x 128 bytes), one
@@ -24,9 +23,12 @@
 //   warps 2-9  epilogue: two warps for each TMEM lane quarter, each every other 32 columns; the
 //              accumulator is double buffered, so the next tile's MMAs run under it
 // kGateUp makes BN / 2 columns of g and the same of u side by side in one accumulator, so the
-// activation and the product need no second pass.
+// activation and the product need no second pass.  kGrads runs up to four products in one launch: its
+// tiles are those of one after another, whose A is K-major (dx) or MN-major (the weights' gradients).
 // Every wait is bounded; on expiry the CTA sets the device timeout bit, all roles leave, copies and
 // MMAs in flight are waited for (bounded) and TMEM is freed.
+#include <algorithm>
+
 #include "common.cuh"
 #include "dense.h"
 #include "dense_tc.cuh"
@@ -43,8 +45,7 @@ constexpr int kABytes = kBM * kBK * 2;
 template <int MODE, int BN, int KIND>
 struct Cfg {
   static constexpr bool PAIR = KIND == kPairTile, SPLIT = KIND == kSplitTile;
-  static constexpr bool kAMn = MODE == kWeightGrad;
-  static constexpr bool kBMn = MODE == kHiddenGrad || MODE == kInputGrad || MODE == kWeightGrad;
+  static constexpr bool kBMn = MODE == kHiddenGrad || MODE == kGrads;
   // rows of B in this CTA; an MN-major operand comes in whole boxes of 64, of which the last may be used in part
   static constexpr int kBUsed = PAIR ? BN / 2 : BN, kBRows = kBMn ? (kBUsed + 63) / 64 * 64 : kBUsed;
   static constexpr int kStage = kABytes + kBRows * kBK * 2;
@@ -71,24 +72,19 @@ __device__ __forceinline__ uint32_t idesc_16(bool f16, bool a_mn, bool b_mn, int
 }
 
 struct Tile {
-  int prob, m0, n0;  // problem (kWeightGrad), first row, first column (kGateUp: of g and of u)
+  int prob, m0, n0;  // problem, first row, first column (kGateUp: of g and of u)
 };
 
+template <int MODE>
 __device__ __forceinline__ Tile tile_of(const GemmParams &p, int t, int rows, int cols) {
   Tile r;
   r.prob = 0;
-  int tm = p.tiles_m, tn = p.tiles_n;
-  const int each = tm * tn;
-  if (t >= each * p.same) {
-    t -= each * p.same;
-    r.prob = p.same;
-    tm = p.tiles_m_last;
-    tn = p.tiles_n_last;
-  } else {
-    r.prob = t / each;
-    t -= r.prob * each;
+  if constexpr (MODE == kGrads) {
+    int begin = 0;
+    while (t >= p.problem[r.prob].end) begin = p.problem[r.prob++].end;
+    t -= begin;
   }
-  band_tile(t, tm, tn, r.m0, r.n0);
+  band_tile(t, p.problem[r.prob].tiles_m, p.problem[r.prob].tiles_n, r.m0, r.n0);
   r.m0 *= rows;
   r.n0 *= cols;
   return r;
@@ -130,9 +126,8 @@ struct Epilogue {
     row0 = row0_;
     half = half_;
     buf = buf_;
-    const bool last = tl.prob == p.same;
-    m = last ? p.m_last : p.m;
-    n = last ? p.n_last : p.n;
+    m = p.problem[tl.prob].m;
+    n = p.problem[tl.prob].n;
     if constexpr (MODE == kHiddenGrad) fetch(p, half * 32);
   }
   // sixteen values as eight words of pairs
@@ -233,13 +228,13 @@ struct Epilogue {
         }
       }
       if constexpr (MODE == kGateUp || MODE == kHiddenGrad) {
-        emit(x, p.c[0], n, c0);
-        if (p.c[1]) {
-          emit(y, p.c[1], n, c0);
-          emit(z, p.c[2], n, c0);
+        emit(x, p.out[0], n, c0);
+        if (p.out[1]) {
+          emit(y, p.out[1], n, c0);
+          emit(z, p.out[2], n, c0);
         }
       } else {
-        emit(x, p.c[tl.prob], p.ldc[tl.prob], c0);
+        emit(x, p.problem[tl.prob].c, p.problem[tl.prob].ldc, c0);
       }
     }
   }
@@ -255,7 +250,7 @@ __device__ __forceinline__ void epilogue_loop(const GemmParams &p, uint32_t tmem
   RingPos<2> acc;
   Epilogue<MODE, BN, T> e;
   for (int t = first_tile; t < p.tiles; t += tile_step, acc.next()) {
-    const Tile tl = tile_of(p, t, kRows, kCols);
+    const Tile tl = tile_of<MODE>(p, t, kRows, kCols);
     e.begin(p, tl, half, tl.m0 + (int)rank * kBM + q * 32, buf);
     if (!warp_wait(&tfull_bar[acc.slot], acc.round, abort_p, p.status, p.wait_ns)) break;
     tc_fence_after();
@@ -279,7 +274,7 @@ __device__ __forceinline__ void epilogue_split(const GemmParams &p, uint32_t tme
   const int first_q = owner * 4 / p.splits;  // the owner's first quarter
   const uint32_t parts = parts0 + (q - first_q) * (p.splits - 1) * 32 * BN * 4;
   const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16);
-  const Tile tl = tile_of(p, tile, kBM, kCols);
+  const Tile tl = tile_of<MODE>(p, tile, kBM, kCols);
   Epilogue<MODE, BN, T> e;
   e.parts = parts;
   if (owner == rank) e.begin(p, tl, half, tl.m0 + q * 32, buf);
@@ -320,7 +315,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int part = SPLIT ? (int)cluster_rank() : 0;  // of k
   const int first_tile = PAIR ? blockIdx.x >> 1 : SPLIT ? blockIdx.x / p.splits : blockIdx.x;
   const int tile_step = PAIR ? gridDim.x >> 1 : SPLIT ? p.tiles : gridDim.x;
-  const int kb_first = SPLIT ? part * p.kb / p.splits : 0, kb_end = SPLIT ? (part + 1) * p.kb / p.splits : p.kb;
+  // this CTA's k blocks of a tile of problem q
+  auto kb_first = [&](const GemmProblem &q) { return SPLIT ? part * q.kb / p.splits : 0; };
+  auto kb_end = [&](const GemmProblem &q) { return SPLIT ? (part + 1) * q.kb / p.splits : q.kb; };
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full_bar[s], 1);
@@ -354,33 +351,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     RingPos<C::kStages> pos;
     int j = 0;
     bool ok = true;
-    const uint32_t stage_bytes = C::kStage - (kBM - p.a_rows) * kBK * 2;
     const uint32_t ring0 = smem_u32(ring), full0 = PAIR ? in_cta(full_bar, 0) : smem_u32(full_bar);
     for (int t = first_tile; ok && t < p.tiles; t += tile_step) {
-      const Tile tl = tile_of(p, t, kRows, kCols);
+      const Tile tl = tile_of<MODE>(p, t, kRows, kCols);
+      const GemmProblem &q = p.problem[tl.prob];
+      const bool a_mn = MODE == kGrads && q.a_mn;
+      const uint32_t stage_bytes = a_mn ? C::kStage : C::kStage - (kBM - p.a_rows) * kBK * 2;
       const int m0 = tl.m0 + (int)rank * kBM, n0 = tl.n0 + (MODE == kGateUp ? 0 : (int)rank * C::kBUsed);
-      for (int kb = kb_first; kb < kb_end; ++kb, ++j, pos.next()) {
+      const int last = kb_end(q);
+      for (int kb = kb_first(q); kb < last; ++kb, ++j, pos.next()) {
         const int s = pos.slot;
         if (!warp_wait(&empty_bar[s], pos.round ^ 1u, abort_p, p.status, p.wait_ns)) {
           ok = false;
           break;
         }
-        // the second pair of matrices follows the first along k (kInputGrad)
-        const int src = MODE == kWeightGrad ? tl.prob : (MODE == kInputGrad && kb >= p.kb0 ? 1 : 0);
-        const int k0 = (MODE == kInputGrad && kb >= p.kb0 ? kb - p.kb0 : kb) * kBK;
+        const int second = MODE == kGrads && kb >= q.kb0, k0 = (second ? kb - q.kb0 : kb) * kBK;
+        const CUtensorMap *ma = &maps.a[MODE == kGrads ? q.a + second : 0], *mb = &maps.b[MODE == kGrads ? q.b + second : 0];
         // the leader's barrier counts both CTAs' bytes
         if (rank == 0) mbar_expect_one(full0 + 8 * s, PAIR ? 2 * stage_bytes : stage_bytes);
         const uint32_t a = ring0 + s * C::kStage, b = a + kABytes, fb = full0 + 8 * s;
-        if constexpr (C::kAMn) {
-          tma_load_2d_one<PAIR>(a, &maps.a[src], fb, m0, k0);
-          tma_load_2d_one<PAIR>(a + kBK * 128, &maps.a[src], fb, m0 + 64, k0);
+        if (a_mn) {
+          tma_load_2d_one<PAIR>(a, ma, fb, m0, k0);
+          tma_load_2d_one<PAIR>(a + kBK * 128, ma, fb, m0 + 64, k0);
         } else {
-          tma_load_2d_one<PAIR>(a, &maps.a[src], fb, k0, m0);
+          tma_load_2d_one<PAIR>(a, ma, fb, k0, m0);
         }
         if constexpr (C::kBMn) {
 #pragma unroll
           for (int i = 0; i < C::kBRows / 64; ++i)
-            tma_load_2d_one<PAIR>(b + i * kBK * 128, &maps.b[src], fb, n0 + 64 * i, k0);
+            tma_load_2d_one<PAIR>(b + i * kBK * 128, mb, fb, n0 + 64 * i, k0);
         } else if constexpr (MODE == kGateUp) {
           if constexpr (PAIR) {  // the leader holds the gate's rows, its peer the up projection's
             tma_load_2d_one<PAIR>(b, &maps.b[rank], fb, k0, n0);
@@ -389,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_2d_one<PAIR>(b + (BN / 2) * 128, &maps.b[1], fb, k0, n0);
           }
         } else {
-          tma_load_2d_one<PAIR>(b, &maps.b[0], fb, k0, n0);
+          tma_load_2d_one<PAIR>(b, mb, fb, k0, n0);
         }
       }
     }
@@ -399,21 +398,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (rank == 0) {
       if (p.inject && blockIdx.x == 0)  // test hook: a wait that runs out
         (void)warp_wait(&never_bar, 0u, abort_p, p.status, p.wait_ns);
-      const uint32_t idesc = idesc_16(p.f16, C::kAMn, C::kBMn, kRows, BN);
       // 16 k are 32 bytes of a K-major row, or 16 rows of 128 bytes of an MN-major box
       // (an address of shared memory carries the CTA's rank in its cluster above the 18 bits that count)
       const uint64_t ring_d = (smem_u32(ring) >> 4) & 0x3FFFu;
-      const uint64_t a0 = (C::kAMn ? smem_desc_mn(0) : smem_desc_sw128(0)) + ring_d;
       const uint64_t b0 = (C::kBMn ? smem_desc_mn(0) : smem_desc_sw128(0)) + ring_d + (kABytes >> 4);
-      constexpr int kAStep = (C::kAMn ? 2048 : 32) >> 4, kBStep = (C::kBMn ? 2048 : 32) >> 4;
+      constexpr int kBStep = (C::kBMn ? 2048 : 32) >> 4;
       RingPos<C::kStages> pos;
       RingPos<2> acc;
       bool ok = true;
       for (int t = first_tile; ok && t < p.tiles; t += tile_step, acc.next()) {
+        const GemmProblem &q = p.problem[MODE == kGrads ? tile_of<MODE>(p, t, kRows, kCols).prob : 0];
+        const bool a_mn = MODE == kGrads && q.a_mn;
+        const uint32_t idesc = idesc_16(p.f16, a_mn, C::kBMn, kRows, BN);
+        const uint64_t a0 = (a_mn ? smem_desc_mn(0) : smem_desc_sw128(0)) + ring_d;
+        const int a_step = (a_mn ? 2048 : 32) >> 4, begin = kb_first(q), last = kb_end(q);
         if (!warp_wait(&tempty_bar[acc.slot], acc.round ^ 1u, abort_p, p.status, p.wait_ns)) break;
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)(acc.slot * BN);
-        for (int kb = kb_first; kb < kb_end; ++kb, pos.next()) {
+        for (int kb = begin; kb < last; ++kb, pos.next()) {
           if (!warp_wait(&full_bar[pos.slot], pos.round, abort_p, p.status, p.wait_ns)) {
             ok = false;
             break;
@@ -422,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t at = pos.slot * (C::kStage >> 4);
 #pragma unroll
           for (int k = 0; k < kBK / 16; ++k)
-            tc_mma_one<PAIR, false>(d, a0 + (at + k * kAStep), b0 + (at + k * kBStep), idesc, (kb > kb_first || k > 0) ? 1u : 0u);
+            tc_mma_one<PAIR, false>(d, a0 + (at + k * a_step), b0 + (at + k * kBStep), idesc, (kb > begin || k > 0) ? 1u : 0u);
           tc_commit_one<PAIR>(smem_u32(&empty_bar[pos.slot]));
         }
         if (ok) tc_commit_one<PAIR>(smem_u32(&tfull_bar[acc.slot]));
@@ -460,8 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int j = issued, no_abort = 0;
     if constexpr (PAIR) {
       const int theirs = ld_cluster_s32(in_cta(&issued, 1));
-      for (; j < theirs; ++j)
-        mbar_arrive_expect_tx(&full_bar[j % C::kStages], C::kStage - (kBM - p.a_rows) * kBK * 2);
+      for (; j < theirs; ++j) mbar_arrive_expect_tx(&full_bar[j % C::kStages], C::kStage);
     }
     for (int s = 0; s < C::kStages; ++s) {
       const int n = j / C::kStages + (s < j % C::kStages ? 1 : 0);
@@ -491,34 +492,43 @@ cudaError_t launch(const GemmMaps &maps, const GemmParams &p, int num_sms, cudaS
                                  maps, p);
 }
 
-long long tiles_of(int mode, const GemmParams &p, DenseTile g) {
-  const int cols = mode == kGateUp ? g.bn / 2 : g.bn, rows = g.kind == kPairTile ? 2 * kBM : kBM;
-  return (long long)cdiv(p.m, rows) * cdiv(p.n, cols) * p.same + (long long)cdiv(p.m_last, rows) * cdiv(p.n_last, cols);
+// rows and columns of a tile's results
+int tile_rows(DenseTile g) { return g.kind == kPairTile ? 2 * kBM : kBM; }
+int tile_cols(int mode, DenseTile g) { return mode == kGateUp ? g.bn / 2 : g.bn; }
+long long tiles_of(int mode, const GemmProblem &q, DenseTile g) {
+  return (long long)cdiv(q.m, tile_rows(g)) * cdiv(q.n, tile_cols(mode, g));
 }
 
 }  // namespace
 
 int gemm_b_box(int mode, DenseTile t) {
-  if (mode == kHiddenGrad || mode == kInputGrad || mode == kWeightGrad) return 64;
+  if (mode == kHiddenGrad || mode == kGrads) return 64;
   return mode == kGateUp || t.kind == kPairTile ? t.bn / 2 : t.bn;
 }
 
-// The tile that takes the least time by what tiles measured (us, 2048 to 4096 k, bf16): a k block of 64
-// with 256, 128, 64 and 32 columns 0.339, 0.200, 0.157 and 0.147 on a CTA by itself (few columns: the
-// time to issue four MMAs), 0.045 + 0.00092 for each column on a pair; an epilogue 0.010 for each column
-// of a plain result, 0.022 of kGateUp and 0.032 of kHiddenGrad, hidden under the next tile's products
-// but for the last; a launch with its prologue 3.8, of pairs 5.8.  Tiles go in waves over the SMs, so
-// the widest tile is not always the fastest: 4096 x 4096 columns by 4096 took 83.1 us in 256 tiles of
-// 256 columns (3.4 waves of 76 pairs), 75.6 in 304 of 224 (4.0), and 1024 rows 29.4 in one wave of
-// pairs, 34.8 in two of 128 columns.
+// The tile that takes the least time by what tiles measured (us, bf16): a k block of 64 with 256, 128, 64
+// and 32 columns 0.339, 0.200, 0.157 and 0.147 on a CTA by itself (few columns: the time to issue four
+// MMAs), 0.045 + 0.00092 for each column on a pair; the epilogue of a tile 0.25 + 0.0085 for each column
+// of a plain result, 0.45 + 0.0078 of kGateUp, and 0.032 a column of kHiddenGrad, whose ten bytes for each
+// value are memory's; of the two the longer, and together no less than 0.8 of their sum; a launch with its
+// prologue 3.8, of pairs 5.8.  Rows that are no multiple of 128 bytes make each 128 bytes of a box two
+// lines, 0.0014 for each.  Tiles go in waves over the SMs, so the widest tile is not always the fastest:
+// 4096 x 4096 columns by 4096 took 83.1 us in 256 tiles of 256 columns (3.4 waves of 76 pairs), 75.6 in 304
+// of 224 (4.0), and 1024 rows 29.4 in one wave of pairs, 34.8 in two of 128 columns.
 //
 // Few tiles with a long k leave SMs idle; then clusters of two or four CTAs share a tile's k (64 columns) and
-// exchange their sums, for 2.2 more at the start and the end.  8 rows, hidden 4096, inter 2048: the gate and
-// up projections 14.7 in single CTAs, 12.4 in clusters of two; the backward pass's first product 15.5 and, in
-// clusters of four, 11.6.
-DenseTile gemm_pick_tile(int mode, const GemmParams &p, int num_sms) {
-  const bool b_mn = mode == kHiddenGrad || mode == kInputGrad || mode == kWeightGrad;
-  const double per_col = mode == kGateUp ? 0.022 : mode == kHiddenGrad ? 0.032 : 0.010;
+// exchange their sums, for 2.2 more at the start and the end, and 4.2 for each further wave, as these CTAs
+// make one tile each.  8 rows, hidden 4096, inter 2048: the gate and up projections 14.7 in single CTAs, 12.4
+// in clusters of two; the backward pass's first product 15.5 and, in clusters of four, 11.6.
+//
+// Several products in one launch save a launch and share its last wave, but also the tile.  The backward
+// pass of 1016 rows, hidden 224, inter 424 took 21.0 with two launches for kGrads, 13.9 with one; 4096 rows,
+// hidden 4096, inter 2048 MERGED_LARGE; 8 rows, hidden 4096, inter 2048, whose dx wants clusters, 40.9 with
+// two, 45.7 with one.
+DenseTile gemm_pick_tile(int mode, const GemmParams &p, int num_sms, double *time) {
+  const bool b_mn = mode == kHiddenGrad || mode == kGrads;
+  const double per_col = mode == kGateUp ? 0.0078 : mode == kHiddenGrad ? 0.032 : 0.0085;
+  const double per_tile = mode == kGateUp ? 0.45 : mode == kHiddenGrad ? 0.0 : 0.25;
   const struct {
     DenseTile tile;
     double k_block;
@@ -527,33 +537,52 @@ DenseTile gemm_pick_tile(int mode, const GemmParams &p, int num_sms) {
              {{64, kOneTile, 1}, 0.157},   {{32, kOneTile, 1}, 0.147},   {{64, kSplitTile, 2}, 0.157},
              {{64, kSplitTile, 4}, 0.157}};
   DenseTile best = {0, kOneTile, 1};
-  double least = 0;
   for (const auto &c : all) {
-    if (b_mn && c.tile.bn < 64) continue;
     const int splits = c.tile.splits;
-    if (splits > p.kb) continue;
+    bool fits = !(b_mn && c.tile.bn < 64);
+    for (int i = 0; i < p.problems; ++i) fits = fits && splits <= p.problem[i].kb;
+    // a pair's boxes have one height, whose bytes a barrier of the other CTA counts
+    if (!fits || (c.tile.kind == kPairTile && p.a_rows < kBM)) continue;
     // pairs lie on the two SMs of a pair; not every SM can be in a cluster of four
     const long long units = c.tile.kind == kPairTile || splits == 2 ? num_sms / 2 : splits == 4 ? num_sms * 36 / 152 : num_sms;
-    const long long waves = (tiles_of(mode, p, c.tile) + units - 1) / units;
-    const double epilogue = per_col * c.tile.bn, products = c.k_block * ((p.kb + splits - 1) / splits);
-    const double time = (c.tile.kind == kPairTile ? 5.8 : c.tile.kind == kSplitTile ? 6.0 : 3.8) +
-                        waves * (products > epilogue ? products : epilogue) + epilogue;
-    if (best.bn == 0 || time < least) {
+    const double epilogue = per_tile + per_col * c.tile.bn;
+    const double lines = p.odd_rows ? 0.0014 * (p.a_rows + (c.tile.kind == kPairTile ? c.tile.bn / 2 : c.tile.bn)) : 0.0;
+    const double k_block = c.k_block > lines ? c.k_block : lines;
+    double us = (c.tile.kind == kPairTile ? 5.8 : c.tile.kind == kSplitTile ? 6.0 : 3.8) + epilogue;
+    long long tiles = 0, waves = 0;
+    double work = 0.0, longest = 0.0, shortest = 0.0;
+    for (int i = 0; i < p.problems; ++i) {  // longest k first
+      const long long own = tiles_of(mode, p.problem[i], c.tile), upto = (tiles += own, (tiles + units - 1) / units);
+      const double products = k_block * ((p.problem[i].kb + splits - 1) / splits);
+      if (c.tile.kind == kSplitTile) {
+        shortest = products + 4.2;
+        longest = longest > shortest ? longest : shortest;
+        work += own * shortest;
+      } else {  // a wave takes as long as its first tile
+        us += (upto - waves) * std::max({products, epilogue, 0.8 * (products + epilogue)});
+        waves = upto;
+      }
+    }
+    if (c.tile.kind == kSplitTile)  // a cluster for each tile, the next as one ends
+      us += (tiles <= units ? longest : p.problems == 1 ? (tiles + units - 1) / units * longest
+                                                        : std::max(longest, work / units + shortest)) - 4.2;
+    if (best.bn == 0 || us < *time) {
       best = c.tile;
-      least = time;
+      *time = us;
     }
   }
   return best;
 }
 
 cudaError_t launch_dense_gemm(int mode, DenseTile g, const GemmMaps &maps, GemmParams p, int num_sms, cudaStream_t st) {
-  const int cols = mode == kGateUp ? g.bn / 2 : g.bn, rows = g.kind == kPairTile ? 2 * kBM : kBM;
   p.splits = g.splits;
-  p.tiles_m = cdiv(p.m, rows);
-  p.tiles_n = cdiv(p.n, cols);
-  p.tiles_m_last = cdiv(p.m_last, rows);
-  p.tiles_n_last = cdiv(p.n_last, cols);
-  p.tiles = (int)tiles_of(mode, p, g);
+  p.tiles = 0;
+  for (int i = 0; i < p.problems; ++i) {
+    GemmProblem &q = p.problem[i];
+    q.tiles_m = cdiv(q.m, tile_rows(g));
+    q.tiles_n = cdiv(q.n, tile_cols(mode, g));
+    q.end = p.tiles += (int)tiles_of(mode, q, g);
+  }
 #define MOE_LAUNCH(MODE, BN, KIND) \
   if (mode == MODE && g.bn == BN && g.kind == KIND) return launch<MODE, BN, KIND>(maps, p, num_sms, st)
 #define MOE_LAUNCH_ALL(MODE)         \
@@ -570,8 +599,7 @@ cudaError_t launch_dense_gemm(int mode, DenseTile g, const GemmMaps &maps, GemmP
   MOE_LAUNCH_ALL(kDown);
   MOE_LAUNCH(kDown, 32, kOneTile);
   MOE_LAUNCH_ALL(kHiddenGrad);
-  MOE_LAUNCH_ALL(kInputGrad);
-  MOE_LAUNCH_ALL(kWeightGrad);
+  MOE_LAUNCH_ALL(kGrads);
 #undef MOE_LAUNCH_ALL
 #undef MOE_LAUNCH
   return cudaErrorInvalidValue;

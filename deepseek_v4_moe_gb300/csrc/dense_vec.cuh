@@ -139,9 +139,15 @@ __device__ __forceinline__ void load_eight(const T *row, int t, int n, int hidde
   e.get(o);
 }
 
-// 1 / (1 + exp(-x)) by the fast exponential and division: a few units of 2^-22, well below the 16-bit
-// types that what is made of it is rounded to; 0 and 1 far out, where exp(-x) overflows or vanishes.
-__device__ __forceinline__ float fast_sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+// 1 / (1 + exp(-x)) by the approximate base-2 exponential and reciprocal: a few units of 2^-22, well below
+// the 16-bit types that what is made of it is rounded to; 0 and 1 far out, where exp(-x) overflows or
+// vanishes.  (With subnormals, which change nothing here, each takes several instructions more.)
+__device__ __forceinline__ float fast_sigmoid(float x) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return r;
+}
 
 // act(g) and, for the backward pass, its derivative.  The tanh form of gelu is g * sigmoid(2 z) with
 // z = sqrt(2 / pi) (g + 0.044715 g^3), as (1 + tanh(z)) / 2 = sigmoid(2 z).
