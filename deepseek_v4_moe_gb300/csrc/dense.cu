@@ -342,7 +342,7 @@ extern "C" int moe_ffn_gated_forward(const moe_ffn_gated_args *a, void *stream) 
   if (sms < 0) return sms;
   if ((rc = pending(who))) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (a->rows <= moe::kGemvRows) {
+  if (moe::gated_gemv(a->rows, a->hidden, a->inter)) {
     moe::GemvParams p = {};
     p.n = a->inter;
     p.k = a->hidden;
@@ -490,7 +490,7 @@ extern "C" int moe_ffn_fp8_matmul(const moe_ffn_fp8_matmul_args *a, void *stream
   const int sms = current_sms();
   if (sms < 0) return sms;
   if ((rc = pending(who))) return rc;
-  if (a->rows <= moe::kGemvRows) {
+  if (moe::fp8_gemv(a->rows, a->n, a->k)) {
     moe::Fp8GemvParams p = {};
     p.n = a->n;
     p.k = a->k;
@@ -505,7 +505,7 @@ extern "C" int moe_ffn_fp8_matmul(const moe_ffn_fp8_matmul_args *a, void *stream
     p.b_scale = a->b_scale;
     p.out = a->out;
     p.ld_out = a->ld_out;
-    return launched(who, moe::launch_fp8_gemv(p, a->rows, a->out_type, static_cast<cudaStream_t>(stream)));
+    return launched(who, moe::launch_fp8_gemv(p, a->rows, sms, a->out_type, static_cast<cudaStream_t>(stream)));
   }
   DeviceSide dev;
   if ((rc = device_side(who, &dev))) return rc;

@@ -126,12 +126,14 @@ cudaError_t launch_fp8_matmul(DenseTile tile, const CUtensorMap &a, const CUtens
                               cudaStream_t st);
 cudaError_t launch_fp8_quantise(const QuantiseParams &p, int num_sms, cudaStream_t st);
 
-// ---- products for up to kGemvRows rows on the CUDA cores (dense_gemv.cu) ----
+// ---- products for a few rows on the CUDA cores (dense_gemv.cu) ----
 
-constexpr int kGemvRows = 4;
+bool gated_gemv(int rows, int hidden, int inter);  // these kernels are the faster ones
+bool fp8_gemv(int rows, int n, int k);
 
 struct GemvParams {
-  int n, k, splits;          // splits is set by the launch
+  int n, k;
+  int rows, splits;          // set by the launch
   int act;
   const void *x, *w[2];
   long long ld_x;
@@ -140,7 +142,7 @@ struct GemvParams {
 };
 
 struct Fp8GemvParams {
-  int n, k, kb, splits;
+  int n, k, kb, splits;      // splits is set by the launch
   int a_e5m2, b_e5m2;
   const uint8_t *a, *b;
   long long ld_a, ld_b;
@@ -152,6 +154,6 @@ struct Fp8GemvParams {
 // up: the gate and up projections with the activation; otherwise the down projection, which starts
 // while the kernel before it on the stream runs
 cudaError_t launch_gated_gemv(bool up, GemvParams p, int rows, bool f16, cudaStream_t st);
-cudaError_t launch_fp8_gemv(Fp8GemvParams p, int rows, int out_type, cudaStream_t st);
+cudaError_t launch_fp8_gemv(const Fp8GemvParams &p, int rows, int num_sms, int out_type, cudaStream_t st);
 
 }  // namespace moe

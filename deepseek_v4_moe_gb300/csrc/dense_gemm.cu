@@ -523,7 +523,7 @@ int gemm_b_box(int mode, DenseTile t) {
 //
 // Several products in one launch save a launch and share its last wave, but also the tile.  The backward
 // pass of 1016 rows, hidden 224, inter 424 took 21.0 with two launches for kGrads, 13.9 with one; 4096 rows,
-// hidden 4096, inter 2048 MERGED_LARGE; 8 rows, hidden 4096, inter 2048, whose dx wants clusters, 40.9 with
+// hidden 4096, inter 2048 268 and 247; 8 rows, hidden 4096, inter 2048, whose dx wants clusters, 40.9 with
 // two, 45.7 with one.
 DenseTile gemm_pick_tile(int mode, const GemmParams &p, int num_sms, double *time) {
   const bool b_mn = mode == kHiddenGrad || mode == kGrads;

@@ -47,7 +47,7 @@ __device__ __forceinline__ void join_splits(float (&v)[K], int splits, float (*b
       for (int k = 0; k < K; ++k) v[k] += buf[warp + s][k];
 }
 
-// UP: h = act(x w0^T) * (x w1^T), and g and u where they are wanted; otherwise out = x w0^T.
+// R rows; 8: five to eight.  UP: h = act(x w0^T) * (x w1^T), and g and u where they are wanted; otherwise out = x w0^T.
 template <bool UP, int R, typename T>
 __global__ void __launch_bounds__(32 * kWarps) gated_gemv_kernel(const __grid_constant__ GemvParams p) {
   constexpr int M = UP ? 2 : 1;
@@ -85,7 +85,8 @@ __global__ void __launch_bounds__(32 * kWarps) gated_gemv_kernel(const __grid_co
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           float2 b[4];
-          unpack8<T>(*reinterpret_cast<const uint4 *>(static_cast<const T *>(p.x) + r * p.ld_x + k), b);
+          const int row = R <= 4 ? r : min(r, p.rows - 1);  // no branch between the rows' loads
+          unpack8<T>(*reinterpret_cast<const uint4 *>(static_cast<const T *>(p.x) + row * p.ld_x + k), b);
 #pragma unroll
           for (int m = 0; m < M; ++m)
 #pragma unroll
@@ -101,6 +102,7 @@ __global__ void __launch_bounds__(32 * kWarps) gated_gemv_kernel(const __grid_co
   if (!in || part != 0 || lane != 0) return;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
+    if (R > 4 && r >= p.rows) break;
     if constexpr (UP) {
       const size_t at = (size_t)r * p.n + col;
       const float g = sum[r], u = sum[R + r];
@@ -134,55 +136,73 @@ __device__ __forceinline__ void codes16(const uint4 w, bool e5m2, float2 (&o)[8]
 }
 
 // FP8 with block scales: eight lanes share a block of 128 codes; a lane's 16 products are summed, then
-// scaled and added.
-template <int R, typename TO>
+// scaled and added.  A warp takes C neighbouring columns (of one block of b_scale), so that the conversion
+// of a's codes serves C columns: 4096 x 4096 took 6.6 us with one column a warp, 5.8 with four; on four
+// tokens 11.5 and 8.7.
+// Rounds of 512 codes whose loads are in flight: four 16-byte loads in a lane, eight where registers allow it
+// (four tokens leave none: 10.1 us for 8.7).
+template <int R, int C>
+constexpr int kFp8Rounds = C == 1 ? 4 : R <= 3 ? 8 / C : 4 / C;
+
+template <int R, int C, typename TO>
 __global__ void __launch_bounds__(32 * kWarps) fp8_gemv_kernel(const __grid_constant__ Fp8GemvParams p) {
-  __shared__ float buf[kWarps][R];
+  constexpr int kDeep = kFp8Rounds<R, C>;
+  __shared__ float buf[kWarps][C * R];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int col = blockIdx.x * (kWarps / p.splits) + warp / p.splits, part = warp % p.splits;
-  const bool in = col < p.n;
+  const int col = (blockIdx.x * (kWarps / p.splits) + warp / p.splits) * C, part = warp % p.splits;
   const int step = 512 * p.splits;
   const uint8_t *w = p.b + (size_t)col * p.ld_b;
   const float *sb = p.b_scale + (size_t)(col / kScaleBlock) * p.kb;
-  float sum[R];
+  float sum[C * R];
 #pragma unroll
-  for (int r = 0; r < R; ++r) sum[r] = 0.f;
+  for (int i = 0; i < C * R; ++i) sum[i] = 0.f;
   pdl_wait();
-  for (int k0 = part * 512 + lane * 16; k0 < p.k; k0 += step * kRounds) {
-    uint4 f[kRounds];
+  for (int k0 = part * 512 + lane * 16; k0 < p.k; k0 += step * kDeep) {
+    uint4 f[kDeep][C];
 #pragma unroll
-    for (int i = 0; i < kRounds; ++i)
-      f[i] = in && k0 + i * step < p.k ? ld_stream(w + k0 + i * step) : make_uint4(0u, 0u, 0u, 0u);
+    for (int i = 0; i < kDeep; ++i)
 #pragma unroll
-    for (int i = 0; i < kRounds; ++i) {
+      for (int c = 0; c < C; ++c)
+        f[i][c] = col + c < p.n && k0 + i * step < p.k ? ld_stream(w + c * p.ld_b + k0 + i * step) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int i = 0; i < kDeep; ++i) {
       const int k = k0 + i * step;
-      if (in && k < p.k) {
-        float2 b[8];
-        codes16(f[i], p.b_e5m2, b);
+      if (col < p.n && k < p.k) {
         const int blk = k / kScaleBlock;
         const float scale = sb[blk];
+        float2 b[C][8];
+#pragma unroll
+        for (int c = 0; c < C; ++c) codes16(f[i][c], p.b_e5m2, b[c]);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-          float2 a[8], dot = make_float2(0.f, 0.f);
+          float2 a[8];
           codes16(*reinterpret_cast<const uint4 *>(p.a + r * p.ld_a + k), p.a_e5m2, a);
+          const float both = scale * p.a_scale[(size_t)r * p.kb + blk];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) dot = __ffma2_rn(a[e], b[e], dot);
-          sum[r] = fmaf(dot.x + dot.y, scale * p.a_scale[(size_t)r * p.kb + blk], sum[r]);
+          for (int c = 0; c < C; ++c) {
+            float2 dot = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dot = __ffma2_rn(a[e], b[c][e], dot);
+            sum[r * C + c] = fmaf(dot.x + dot.y, both, sum[r * C + c]);
+          }
         }
       }
     }
   }
   join_splits(sum, p.splits, buf);
-  if (!in || part != 0 || lane != 0) return;
+  if (part != 0 || lane != 0) return;
 #pragma unroll
-  for (int r = 0; r < R; ++r) static_cast<TO *>(p.out)[r * p.ld_out + col] = from_f32<TO>(sum[r]);
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      if (col + c < p.n) static_cast<TO *>(p.out)[r * p.ld_out + col + c] = from_f32<TO>(sum[r * C + c]);
 }
 
-// Warps that share a column: as many as leave each kRounds rounds of loads or fewer, so that all are in
+// Warps that share a column: as many as leave each `rounds` rounds of loads or fewer, so that all are in
 // flight at once.
-int splits_for(int k, int per_round) {
+int splits_for(int k, int per_round, int rounds) {
   int s = 1;
-  while (s < kWarps && k > per_round * kRounds * s) s *= 2;
+  while (s < kWarps && k > per_round * rounds * s) s *= 2;
   return s;
 }
 
@@ -199,33 +219,54 @@ cudaError_t launch_typed(const GemvParams &p, int rows, cudaStream_t st) {
     case 3: return launch_rows<UP, 3, T>(p, st);
     case 4: return launch_rows<UP, 4, T>(p, st);
   }
-  return cudaErrorInvalidValue;
+  return launch_rows<UP, 8, T>(p, st);
 }
 
-template <int R>
-cudaError_t fp8_rows(const Fp8GemvParams &p, int out_type, cudaStream_t st) {
-  const int cols = kWarps / p.splits, grid = (p.n + cols - 1) / cols;
-  auto kernel = out_type == kF32    ? fp8_gemv_kernel<R, float>
-                : out_type == kBF16 ? fp8_gemv_kernel<R, __nv_bfloat16>
-                                    : fp8_gemv_kernel<R, __half>;
+template <int R, int C>
+cudaError_t fp8_typed(Fp8GemvParams p, int out_type, cudaStream_t st) {
+  p.splits = splits_for(p.k, 512, kFp8Rounds<R, C>);
+  const int cols = kWarps / p.splits * C, grid = (p.n + cols - 1) / cols;
+  auto kernel = out_type == kF32    ? fp8_gemv_kernel<R, C, float>
+                : out_type == kBF16 ? fp8_gemv_kernel<R, C, __nv_bfloat16>
+                                    : fp8_gemv_kernel<R, C, __half>;
   return launch_pdl(kernel, dim3(grid), dim3(32 * kWarps), 0, st, p);
+}
+template <int R>
+cudaError_t fp8_rows(const Fp8GemvParams &p, int num_sms, int out_type, cudaStream_t st) {
+  constexpr int C = 4;
+  // one column a warp where four would leave the SMs few warps (512 x 7168: 3.6 us, 4.8 with four)
+  const bool wide = (long long)p.n / C * splits_for(p.k, 512, kFp8Rounds<R, C>) >= 16 * num_sms;
+  return wide ? fp8_typed<R, C>(p, out_type, st) : fp8_typed<R, 1>(p, out_type, st);
 }
 
 }  // namespace
 
+// Up to four rows the weights' way from memory bounds these kernels as it does the tensor cores' (hidden
+// 4096, inter 2048: 12.8 us for one row, 18.1 for four; tiles 20.7).  Rows beyond cost their arithmetic, which
+// small weights have time for (hidden 2048, inter 512, 8 rows: 7.7 for 11.1).
+bool gated_gemv(int rows, int hidden, int inter) {
+  return rows <= 4 || (rows <= 8 && (long long)rows * hidden * inter <= 1 << 24);
+}
+
+// Here the conversions of the codes grow with the rows: 16384 x 1024 took 4.9, 6.0, 7.7 and 9.3 us for 1 to 4
+// rows, tiles 5.9; 2048 x 2048 3.3 to 4.5, tiles 5.7.
+bool fp8_gemv(int rows, int n, int k) {
+  return rows == 1 || (rows <= 4 && (long long)rows * n * k <= 1 << 25);
+}
+
 cudaError_t launch_gated_gemv(bool up, GemvParams p, int rows, bool f16, cudaStream_t st) {
-  p.splits = splits_for(p.k, 256);
+  p.rows = rows;
+  p.splits = splits_for(p.k, 256, kRounds);
   if (up) return f16 ? launch_typed<true, __half>(p, rows, st) : launch_typed<true, __nv_bfloat16>(p, rows, st);
   return f16 ? launch_typed<false, __half>(p, rows, st) : launch_typed<false, __nv_bfloat16>(p, rows, st);
 }
 
-cudaError_t launch_fp8_gemv(Fp8GemvParams p, int rows, int out_type, cudaStream_t st) {
-  p.splits = splits_for(p.k, 512);
+cudaError_t launch_fp8_gemv(const Fp8GemvParams &p, int rows, int num_sms, int out_type, cudaStream_t st) {
   switch (rows) {
-    case 1: return fp8_rows<1>(p, out_type, st);
-    case 2: return fp8_rows<2>(p, out_type, st);
-    case 3: return fp8_rows<3>(p, out_type, st);
-    case 4: return fp8_rows<4>(p, out_type, st);
+    case 1: return fp8_rows<1>(p, num_sms, out_type, st);
+    case 2: return fp8_rows<2>(p, num_sms, out_type, st);
+    case 3: return fp8_rows<3>(p, num_sms, out_type, st);
+    case 4: return fp8_rows<4>(p, num_sms, out_type, st);
   }
   return cudaErrorInvalidValue;
 }

@@ -301,21 +301,21 @@ template <bool VEC, bool WSMEM>
 struct Weights {
   uint32_t base;  // this thread's first piece
   int t, n;
-  __device__ __forceinline__ void fill(const float *w, int which, int hidden, float absent) const {
+  // all loads before the first store, which nothing passes
+  __device__ __forceinline__ void fill(const float *w_next, const float *w_post, int hidden) const {
     if (threadIdx.x >= n) return;
+    Pairs x[2][kSets];
 #pragma unroll
-    for (int v = 0; v < kSets; ++v)
+    for (int v = 0; v < kSets; ++v) {
+      x[0][v] = w_next ? load_set<float, VEC>(w_next, v, t, n, hidden) : splat(0.f);
+      x[1][v] = w_post ? load_set<float, VEC>(w_post, v, t, n, hidden) : splat(1.f);
+    }
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float x[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int col = VEC ? 8 * (v * n + t) + 4 * k + e : (v * 8 + 4 * k + e) * n + t;
-          x[e] = col >= hidden ? 0.f : w ? w[col] : absent;
-        }
-        sts128(base + ((which * kSets + v) * 2 + k) * n * 16, make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]),
-                                                                          __float_as_uint(x[2]), __float_as_uint(x[3])));
-      }
+    for (int i = 0; i < 2 * kSets * 2; ++i) {
+      const float2 *y = x[i / (2 * kSets)][i / 2 % kSets].v + 2 * (i & 1);
+      sts128(base + i * n * 16, make_uint4(__float_as_uint(y[0].x), __float_as_uint(y[0].y), __float_as_uint(y[1].x),
+                                           __float_as_uint(y[1].y)));
+    }
   }
   __device__ __forceinline__ Pairs get(const float *w, int which, int hidden, float absent, int v) const {
     if constexpr (WSMEM) {
@@ -392,11 +392,6 @@ __global__ void __launch_bounds__(kBwdThreads)
   weights.n = n;
   if constexpr (VEC) rows.clear(pl.depth);
   pdl_wait();
-  if constexpr (WSMEM) {
-    weights.fill(p.w_next, 0, p.hidden, 0.f);
-    weights.fill(p.w_post, 1, p.hidden, 1.f);
-    __syncthreads();
-  }
   const float inv = 1.f / (float)p.hidden;
   int turn = 0;
   // A column's gate and weight are the same over a chunk's rows, so one sum of scale ds f r_f serves both
@@ -408,6 +403,16 @@ __global__ void __launch_bounds__(kBwdThreads)
   Place here, ahead;
   here.enter(p, pl, worker, 0);
   ahead = here;
+  if constexpr (VEC) {
+    for (int s = 0; s < pl.depth - 1; ++s) {
+      rows.fetch(p, s * R::kRow, ahead);
+      if (ahead.has()) ahead.next(p, pl, worker);
+    }
+  }
+  if constexpr (WSMEM) {
+    weights.fill(p.w_next, p.w_post, p.hidden);
+    __syncthreads();
+  }
   // the gate's values stay in registers; a 16-bit gate's of the next chunk are fetched a row ahead
   constexpr bool kAhead = GATEV && sizeof(TG) == 2;
   GateEight gate[kSets], gate_next[kSets];
@@ -426,12 +431,6 @@ __global__ void __launch_bounds__(kBwdThreads)
     for (int v = 0; v < kSets; ++v) {
       load_gate(gate[v], here.has() ? here.gate_row : 0, v);
       gate_next[v] = gate[v];
-    }
-  }
-  if constexpr (VEC) {
-    for (int s = 0; s < pl.depth - 1; ++s) {
-      rows.fetch(p, s * R::kRow, ahead);
-      if (ahead.has()) ahead.next(p, pl, worker);
     }
   }
   while (here.has()) {

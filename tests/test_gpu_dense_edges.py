@@ -340,3 +340,22 @@ def test_what_comes_before_and_after_on_the_stream(cuda_lib):
         g.replay()
         check(got)
     assert m.dense_status() == 0
+
+
+# the same for the backward pass's products in one launch and in two (both ways of every size), and the rest
+MORE_TILES = [(5, 32, 2088), (5, 5544, 392), (5, 2544, 2904), (665, 264, 920), (937, 1752, 136), (2491, 984, 648),
+              (3394, 5376, 32), (1583, 32, 3752), (756, 32, 72), (1045, 2896, 584), (555, 1936, 2472), (4245, 936, 1472),
+              (804, 856, 4184), (513, 1888, 6128), (513, 1976, 7168)]
+
+
+@pytest.mark.parametrize("rows,hidden,inter", MORE_TILES)
+def test_gradients_together_and_apart(cuda_lib, rows, hidden, inter):
+    import deepseek_v4_moe_gb300 as m
+    dtype, name = ((BF16, "silu"), (F16, "gelu"))[(rows + inter // 8) % 2]
+    t = tg.make(rows, hidden, inter, dtype, seed=rows)
+    y, saved, d = tg.run(*t, name)
+    tg.check(*t, name, y, saved, d)
+    apart = m.gated_ffn_backward(*t[:4], saved, t[4], activation=name, need_weights=False)
+    apart.update(m.gated_ffn_backward(*t[:4], saved, t[4], activation=name, need_x=False))
+    tg.check(*t, name, y, saved, apart)
+    assert m.dense_status() == 0
