@@ -133,14 +133,20 @@ __device__ __forceinline__ void store_rows(const Fp8Params &p, int row0, int col
     }
     __syncwarp();
     if (!p.wide) {  // single values, neighbouring threads side by side in a row
-      constexpr int kRow = 4 * kPiece, kAtOnce = 32 / kRow;
-      const int c = lane % kRow;
+      constexpr int kRow = 4 * kPiece, kAtOnce = 32 / kRow, kBatch = 8;  // loads before the first store
+      const int c = lane % kRow, left = p.m - row0;
       const bool there = c0 + c < N && col + c0 + c < p.n;
-#pragma unroll 4
-      for (int r = lane / kRow; r < 32; r += kAtOnce)
-        if (there && row0 + r < p.m)
-          out[(size_t)(row0 + r) * p.ld_out + col + c0 + c] =
-              staged<T>(buf + piece_at(r, c / kPiece) + (c % kPiece) * (int)sizeof(T));
+      const uint32_t from = buf + (c % kPiece) * (int)sizeof(T);
+      T *dst = out + (size_t)(row0 + lane / kRow) * p.ld_out + col + c0 + c;
+#pragma unroll 1
+      for (int r0 = lane / kRow; r0 < 32 && r0 - lane / kRow < left; r0 += kBatch * kAtOnce) {
+        T x[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) x[i] = staged<T>(from + piece_at(r0 + i * kAtOnce, c / kPiece));
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i, dst += kAtOnce * p.ld_out)
+          if (there && r0 + i * kAtOnce < left) *dst = x[i];
+      }
       __syncwarp();
       continue;
     }
