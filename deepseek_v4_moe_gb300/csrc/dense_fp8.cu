@@ -551,7 +551,8 @@ long long fp8_tiles(const Fp8Params &p, DenseTile t) {
 
 // The tile that takes the least time (see gemm_pick_tile), from what they measured at 4096 x 4096 (us): a k
 // block with 256, 224 and 128 columns on a pair 0.47, 0.42 and 0.28, with 128, 64 and 32 on a CTA by
-// itself 0.305, 0.265 and 0.26.  4096 rows took 59.4 in 224 columns (four waves), 66.0 in 256, 73.3 in
+// itself 0.305, 0.265 and 0.26; a launch 3.5 to 4.4, a further wave 0.4 and, of clusters that share a tile's
+// k, which make one tile each, 4.2.  4096 rows took 59.4 in 224 columns (four waves), 66.0 in 256, 73.3 in
 // single CTAs' 128.
 DenseTile fp8_pick_tile(const Fp8Params &p, int num_sms) {
   const struct {
@@ -567,8 +568,9 @@ DenseTile fp8_pick_tile(const Fp8Params &p, int num_sms) {
     if (splits > p.kb) continue;
     const long long units = c.tile.kind == kPairTile || splits == 2 ? num_sms / 2 : splits == 4 ? num_sms * 36 / 152 : num_sms;
     const long long waves = (fp8_tiles(p, c.tile) + units - 1) / units;
-    const double time = (c.tile.kind == kPairTile ? 4.0 : c.tile.kind == kSplitTile ? 5.5 : 3.5) +
-                        waves * c.k_block * ((p.kb + splits - 1) / splits) + 0.012 * c.tile.bn;
+    const bool split = c.tile.kind == kSplitTile;
+    const double time = (c.tile.kind == kPairTile ? 4.0 : split ? 4.4 : 3.5) + 0.012 * c.tile.bn +
+                        waves * c.k_block * ((p.kb + splits - 1) / splits) + (waves - 1) * (split ? 4.2 : 0.4);
     if (best.bn == 0 || time < least) {
       best = c.tile;
       least = time;
