@@ -268,32 +268,41 @@ struct Rows {
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
+  // a set of the row at work as it was read
   template <typename T, int PIECE>
-  __device__ __forceinline__ Pairs get(const void *src, long long ld, int hidden, int v) const {
+  __device__ __forceinline__ Eight<T, VEC> get(const void *src, long long ld, int hidden, int v) const {
+    Eight<T, VEC> e;
     if constexpr (VEC) {
-      Pairs o;
-      Eight<T, true> e;
       uint4 w[sizeof(T) / 2];
 #pragma unroll
       for (int k = 0; k < (int)sizeof(T) / 2; ++k) w[k] = lds128(base + stage + (v * kPieces + PIECE + k) * kPitch);
       memcpy(&e, w, sizeof e);
-      e.get(flat(o));
-      return o;
+    } else if (src) {
+      e.load(static_cast<const T *>(src) + row * ld + v * 8 * n, t, n, hidden - v * 8 * n);
     } else {
-      return src ? load_set<T, false>(static_cast<const T *>(src) + row * ld, v, t, n, hidden) : splat(0.f);
+      memset(&e, 0, sizeof e);
     }
+    return e;
   }
-  __device__ __forceinline__ Pairs state(const NormParams &p, int v) const {
+  __device__ __forceinline__ Eight<TS, VEC> state(const NormParams &p, int v) const {
     return get<TS, kState>(p.w_next ? p.state : nullptr, p.ld_state, p.hidden, v);
   }
-  __device__ __forceinline__ Pairs d_out(const NormParams &p, int v) const {
+  __device__ __forceinline__ Eight<TS, VEC> d_out(const NormParams &p, int v) const {
     return get<TS, kDOut>(p.d_out, p.ld_d_out, p.hidden, v);
   }
-  __device__ __forceinline__ Pairs d_y(const NormParams &p, int v) const {
+  __device__ __forceinline__ Eight<TB, VEC> d_y(const NormParams &p, int v) const {
     return get<TB, kDY>(p.d_y, p.ld_d_y, p.hidden, v);
   }
-  __device__ __forceinline__ Pairs f(const NormParams &p, int v) const { return get<TB, kF>(p.f, p.ld_f, p.hidden, v); }
+  __device__ __forceinline__ Eight<TB, VEC> f(const NormParams &p, int v) const {
+    return get<TB, kF>(p.f, p.ld_f, p.hidden, v);
+  }
 };
+template <typename E>
+__device__ __forceinline__ Pairs pairs(const E &e) {
+  Pairs o;
+  e.get(flat(o));
+  return o;
+}
 
 // The norms' weights.  WSMEM: in shared memory, in 16-byte pieces as the threads of a group read them, zeros
 // past the row's end.
@@ -301,15 +310,20 @@ template <bool VEC, bool WSMEM>
 struct Weights {
   uint32_t base;  // this thread's first piece
   int t, n;
-  // all loads before the first store, which nothing passes
-  __device__ __forceinline__ void fill(const float *w_next, const float *w_post, int hidden) const {
+  // all loads before the first store, which nothing passes; with a gate row, w_post times it
+  template <typename TB>
+  __device__ __forceinline__ void fill(const NormParams &p, bool gate) const {
     if (threadIdx.x >= n) return;
-    Pairs x[2][kSets];
+    Pairs x[2][kSets], g[kSets];
 #pragma unroll
     for (int v = 0; v < kSets; ++v) {
-      x[0][v] = w_next ? load_set<float, VEC>(w_next, v, t, n, hidden) : splat(0.f);
-      x[1][v] = w_post ? load_set<float, VEC>(w_post, v, t, n, hidden) : splat(1.f);
+      x[0][v] = p.w_next ? load_set<float, VEC>(p.w_next, v, t, n, p.hidden) : splat(0.f);
+      x[1][v] = p.w_post ? load_set<float, VEC>(p.w_post, v, t, n, p.hidden) : splat(1.f);
+      if (gate) g[v] = gate_set<TB, VEC>(p, 0, 0, v, t, n);
     }
+    if (gate)
+#pragma unroll
+      for (int v = 0; v < kSets; ++v) x[1][v] = mul(x[1][v], g[v]);
 #pragma unroll
     for (int i = 0; i < 2 * kSets * 2; ++i) {
       const float2 *y = x[i / (2 * kSets)][i / 2 % kSets].v + 2 * (i & 1);
@@ -368,7 +382,9 @@ __device__ __forceinline__ void store_sums(const NormParams &p, const Pairs (&a)
   }
 }
 
-// TG: the type of a vector gate; NoGate: the gate is no vector
+// TG: the type of a vector gate of several rows.  NoGate: the gate is no vector, or one row (and WSMEM),
+// which lies multiplied to w_post: fewer registers and accesses to shared memory, whose pipe was 57 % busy
+// (4096 x 4096, f32 stream, 67.6 -> 63.8 us; bf16 53.3 -> 47.0).
 struct NoGate {};
 template <typename TS, typename TB, bool VEC, bool WSMEM, typename TG>
 __global__ void __launch_bounds__(kBwdThreads)
@@ -396,7 +412,7 @@ __global__ void __launch_bounds__(kBwdThreads)
   int turn = 0;
   // A column's gate and weight are the same over a chunk's rows, so one sum of scale ds f r_f serves both
   // their gradients: times the gate it is w_post's, times w_post the gate's.  Without a vector gate it is
-  // w_post's.
+  // w_post's.  (NoGate: the sum is a_post until the end.)
   Pairs a_next[kSets], a_post[kSets], branch[kSets];
 #pragma unroll
   for (int v = 0; v < kSets; ++v) a_next[v] = a_post[v] = branch[v] = splat(0.f);
@@ -410,7 +426,7 @@ __global__ void __launch_bounds__(kBwdThreads)
     }
   }
   if constexpr (WSMEM) {
-    weights.fill(p.w_next, p.w_post, p.hidden);
+    weights.template fill<TB>(p, !GATEV && p.gate_kind == kGateVector);
     __syncthreads();
   }
   // the gate's values stay in registers; a 16-bit gate's of the next chunk are fetched a row ahead
@@ -421,11 +437,6 @@ __global__ void __launch_bounds__(kBwdThreads)
       to.load(static_cast<const TG *>(p.gate) + (size_t)gate_row * p.hidden + (VEC ? 0 : v * 8 * n), VEC ? v * n + t : t, n,
               VEC ? p.hidden : p.hidden - v * 8 * n);
   };
-  auto gate_pairs = [&](const GateEight &from) {
-    Pairs o;
-    from.get(flat(o));
-    return o;
-  };
   if constexpr (GATEV) {
 #pragma unroll
     for (int v = 0; v < kSets; ++v) {
@@ -433,6 +444,7 @@ __global__ void __launch_bounds__(kBwdThreads)
       gate_next[v] = gate[v];
     }
   }
+  const bool any = here.has();
   while (here.has()) {
     if constexpr (VEC) {
       rows.fetch(p, rows.stage == 0 ? (pl.depth - 1) * R::kRow : rows.stage - R::kRow, ahead);  // freed by the row before
@@ -455,17 +467,25 @@ __global__ void __launch_bounds__(kBwdThreads)
     const float token = p.gate_kind != kGateToken ? 1.f
                         : p.gate_type == kF32     ? static_cast<const float *>(p.gate)[row]
                                                   : to_f32(static_cast<const TB *>(p.gate)[row]);
+    // Single values stay in registers from the first pass over the row to the second (4096 x 1001, no gate: 28.1
+    // -> 24.5 us); from the ring they are read again (kept, 2048 x 8192 f32 spilled: 68.0 -> 73.5).
+    constexpr bool KEEP = !GATEV && !VEC;
+    Eight<TB, VEC> keep_f[kSets], keep_dy[kSets];
+    Eight<TS, VEC> keep_do[kSets];
     float2 ss = pair(0.f), sw = pair(0.f), sf = pair(0.f), qo = pair(0.f), qg = pair(0.f), qs = pair(0.f);
 #pragma unroll
     for (int v = 0; v < kSets; ++v) {
-      const Pairs s = rows.state(p, v), gw = mul(rows.d_y(p, v), weights.get(p.w_next, 0, p.hidden, 0.f, v));
-      Pairs q = rows.f(p, v);
+      keep_f[v] = rows.f(p, v);
+      keep_dy[v] = rows.d_y(p, v);
+      keep_do[v] = rows.d_out(p, v);
+      const Pairs s = pairs(rows.state(p, v)), gw = mul(pairs(keep_dy[v]), weights.get(p.w_next, 0, p.hidden, 0.f, v));
+      Pairs q = pairs(keep_f[v]);
       dot(s, s, ss);
       dot(gw, s, sw);
       dot(q, q, sf);
       q = mul(q, weights.get(p.w_post, 1, p.hidden, 1.f, v));
-      if constexpr (GATEV) q = mul(q, gate_pairs(gate[v]));
-      dot(q, rows.d_out(p, v), qo);
+      if constexpr (GATEV) q = mul(q, pairs(gate[v]));
+      dot(q, pairs(keep_do[v]), qo);
       dot(q, gw, qg);
       dot(q, s, qs);
     }
@@ -479,16 +499,21 @@ __global__ void __launch_bounds__(kBwdThreads)
     const float scale = p.scale * token, cf = p.w_post ? scale * (rf * (rf * (rf * (q_ds * inv)))) : 0.f;
 #pragma unroll
     for (int v = 0; v < kSets; ++v) {
-      const Pairs s = rows.state(p, v), gy = mul(rows.d_y(p, v), rs);
+      if constexpr (!KEEP) {
+        keep_f[v] = rows.f(p, v);
+        keep_dy[v] = rows.d_y(p, v);
+        keep_do[v] = rows.d_out(p, v);
+      }
+      const Pairs s = pairs(rows.state(p, v)), gy = mul(pairs(keep_dy[v]), rs);
       a_next[v] = fma(gy, s, a_next[v]);
-      const Pairs ds = fma(s, -cs, fma(weights.get(p.w_next, 0, p.hidden, 0.f, v), gy, rows.d_out(p, v)));
+      const Pairs ds = fma(s, -cs, fma(weights.get(p.w_next, 0, p.hidden, 0.f, v), gy, pairs(keep_do[v])));
       store_set<TS, VEC>(static_cast<TS *>(p.d_state) + row * p.ld_d_state, v, t, n, p.hidden, ds);
       if (p.f) {
         // nh: the normalised branch without its weight; d: the branch's gradient
-        const Pairs f = rows.f(p, v), nh = mul(f, rf), sd = mul(ds, scale), w = weights.get(p.w_post, 1, p.hidden, 1.f, v);
+        const Pairs f = pairs(keep_f[v]), nh = mul(f, rf), sd = mul(ds, scale), w = weights.get(p.w_post, 1, p.hidden, 1.f, v);
         Pairs d = sd;
         if constexpr (GATEV) {
-          d = mul(sd, gate_pairs(gate[v]));
+          d = mul(sd, pairs(gate[v]));
           branch[v] = fma(sd, nh, branch[v]);
         } else {
           a_post[v] = fma(sd, nh, a_post[v]);
@@ -507,7 +532,7 @@ __global__ void __launch_bounds__(kBwdThreads)
       if (row + 1 == here.end) {  // the chunk's part of the gate's gradient is complete
 #pragma unroll
         for (int v = 0; v < kSets; ++v) {
-          a_post[v] = fma(gate_pairs(gate[v]), branch[v], a_post[v]);
+          a_post[v] = fma(pairs(gate[v]), branch[v], a_post[v]);
           if (p.d_gate) branch[v] = mul(branch[v], weights.get(p.w_post, 1, p.hidden, 1.f, v));
           if (pl.one_gate) continue;  // this was the worker's only chunk: stored at the end
           if (p.d_gate) {
@@ -526,9 +551,16 @@ __global__ void __launch_bounds__(kBwdThreads)
     here = after;
     if constexpr (VEC) rows.stage = rows.stage + R::kRow >= pl.depth * R::kRow ? 0 : rows.stage + R::kRow;
   }
+  if (!GATEV && p.f && p.gate_kind == kGateVector && any) {
+#pragma unroll
+    for (int v = 0; v < kSets; ++v) {
+      branch[v] = p.w_post ? mul(a_post[v], load_set<float, VEC>(p.w_post, v, t, n, p.hidden)) : a_post[v];
+      a_post[v] = mul(a_post[v], gate_set<TB, VEC>(p, 0, 0, v, t, n));
+    }
+  }
   if (p.d_w_next) store_sums<VEC>(p, a_next, n, t, p.part);
   if (p.d_w_post) store_sums<VEC>(p, a_post, n, t, p.part + (size_t)(p.d_w_next ? pl.ctas : 0) * p.hidden);
-  if (GATEV && p.d_gate && pl.one_gate) store_sums<VEC>(p, branch, n, t, p.part + pl.gate_part);
+  if (p.gate_kind == kGateVector && p.d_gate && pl.one_gate) store_sums<VEC>(p, branch, n, t, p.part + pl.gate_part);
 }
 
 // Adds the partial rows: job 0 and 1 the norm weights' over the CTAs, job 2 + i gate row i's over its
@@ -625,7 +657,7 @@ cudaError_t backward_launch(const NormParams &p, NormBwdPlan pl, cudaStream_t st
     return launch_pdl(kernel, dim3(pl.ctas), dim3(kBwdThreads), smem, st, p, pl);
   };
   static std::atomic<unsigned long long> done[3];
-  if (!p.f || p.gate_kind != kGateVector) return go(block_norm_backward_kernel<TS, TB, VEC, WSMEM, NoGate>, done[0]);
+  if (!p.f || p.gate_kind != kGateVector || (WSMEM && pl.one_gate)) return go(block_norm_backward_kernel<TS, TB, VEC, WSMEM, NoGate>, done[0]);
   if (p.gate_type == kF32) return go(block_norm_backward_kernel<TS, TB, VEC, WSMEM, float>, done[1]);
   return go(block_norm_backward_kernel<TS, TB, VEC, WSMEM, TB>, done[2]);
 }
@@ -662,8 +694,8 @@ NormBwdPlan norm_bwd_plan(const NormParams &p, int num_sms) {
   pl.gate_part = norms * pl.ctas * p.hidden;
   pl.floats = pl.gate_part;
   pl.jobs = 2;
+  pl.one_gate = gates && n_gates == 1 && pl.chunks <= pl.workers;
   if (gates && p.d_gate) {
-    pl.one_gate = n_gates == 1 && pl.chunks <= pl.workers;
     if (pl.one_gate || pl.chunks_per_gate > 1) {
       pl.floats += (size_t)(pl.one_gate ? pl.ctas : pl.chunks) * p.hidden;
       pl.jobs += n_gates;
