@@ -221,8 +221,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_base;
   volatile int *abort_p = &abort_flag;
-  pdl_trigger();
-  pdl_wait();  // from here on what the kernel before it wrote is read
+  pdl_wait();     // from here on what the kernel before it wrote is read
+  pdl_trigger();  // the next one may come: not earlier, as it may read before its own wait what this one waited for
 
   if (warp == 0) {
     // ---------------- TMA producer ----------------

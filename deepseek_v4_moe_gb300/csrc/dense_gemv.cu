@@ -7,7 +7,7 @@
 // enough bytes in flight.  The columns' shares of k meet in shared memory.
 //
 // The down projection is launched while the gate and up kernel still runs (programmatic dependent
-// launch): its warps fetch their weights first and wait for h then.
+// launch): its warps fetch their weights first, which nothing writes any more, and wait for h then.
 #include "common.cuh"
 #include "dense.h"
 #include "dense_vec.cuh"
@@ -59,8 +59,10 @@ __global__ void __launch_bounds__(32 * kWarps) gated_gemv_kernel(const __grid_co
   const T *w[2] = {static_cast<const T *>(p.w[0]) + (size_t)col * p.k,
                    UP ? static_cast<const T *>(p.w[1]) + (size_t)col * p.k : nullptr};
   if (UP) {
-    pdl_trigger();  // the down projection's CTAs come and fetch their weights
     pdl_wait();
+    // The down projection's CTAs may come and fetch their weights: not earlier, as what the wait was for may
+    // write them.
+    pdl_trigger();
   }
   float2 sums[M * R];  // two running sums of each product: an instruction takes a pair
 #pragma unroll

@@ -359,3 +359,45 @@ def test_gradients_together_and_apart(cuda_lib, rows, hidden, inter):
     apart.update(m.gated_ffn_backward(*t[:4], saved, t[4], activation=name, need_x=False))
     tg.check(*t, name, y, saved, apart)
     assert m.dense_status() == 0
+
+
+@pytest.mark.parametrize("rows", [1, 4, 8, 40])
+def test_weights_that_the_kernel_before_makes(cuda_lib, rows):
+    """Each weight of the gated block comes from a kernel just before it on the stream, after others that
+    started early: nothing is read before it is written."""
+    import deepseek_v4_moe_gb300 as m
+    h, inter = 512, 256
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    x, wg, wu, _, _ = tg.make(rows, h, inter, BF16, seed=rows)
+    pairs = [(m.fp8_quantise(torch.randn(h, 4096, generator=gen, device="cuda") / 64),
+              m.fp8_quantise(torch.randn(inter, 4096, generator=gen, device="cuda"), block_rows=128)) for _ in range(3)]
+    made = [m.fp8_matmul(*a, *b) for a, b in pairs]
+    want = [m.gated_ffn(x, wg, wu, w) for w in made]
+    torch.cuda.synchronize()
+    wd = torch.empty(h, inter, device="cuda", dtype=BF16)
+
+    def chain():
+        got = []
+        for i in range(12):
+            (a, b), w = pairs[i % 3], made[(i + 1) % 3]
+            m.fp8_matmul(*a, *b, out=wd)
+            got.append((i % 3, m.gated_ffn(x, wg, wu, wd)))
+            m.block_norm(w, norm_next=torch.ones(inter, device="cuda"), y=wd)
+            wd.copy_(w)
+            m.fp8_quantise(x)
+            got.append(((i + 1) % 3, m.gated_ffn(x, wg, wu, wd)))
+        return got
+
+    for _ in range(5):
+        got = chain()
+        torch.cuda.synchronize()
+        assert all(torch.equal(y, want[i]) for i, y in got)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = chain()
+    for _ in range(5):
+        wd.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(y, want[i]) for i, y in got)
+    assert m.dense_status() == 0
