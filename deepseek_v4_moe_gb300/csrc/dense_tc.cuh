@@ -8,7 +8,7 @@ namespace moe {
 
 constexpr int kBM = 128;                             // rows of a tile: the MMA's M
 constexpr int kEpiWarps = 8, kThreads = 32 * (2 + kEpiWarps);
-constexpr int kRingBytes = 227 * 1024 - 3072;        // what barriers and alignment leave of a CTA's shared memory
+constexpr int kRingBytes = 224 * 1024;  // what barriers and alignment leave of a CTA's shared memory
 
 // mbar_wait_bounded, which reads the timer only once a barrier has stayed open for some tries: a try
 // waits a while by itself, and the timer's latency would be added to every wait of a pipeline.

@@ -362,7 +362,7 @@ int64_t moe_ffn_block_norm_workspace(const moe_ffn_block_norm_args *a, const moe
 
 /* The gated feed-forward block:  g = x w_gate^T,  u = x w_up^T,  y = (act(g) * u) w_down^T.
  * Both projections, the activation and the product are one kernel, the down projection another
- * (one to four rows: weight-streaming kernels).  Operands are bf16 or f16, sums f32; act(g) * u is
+ * (a few rows: weight-streaming kernels).  Operands are bf16 or f16, sums f32; act(g) * u is
  * rounded to the operand type before the down projection.
  * Backward, from the saved g and u (rounded to the type):  dh = d_y w_down;  dg = dh * u * act'(g);
  *   du = dh * act(g);  d_x = dg w_gate + du w_up;  d_w_gate = dg^T x;  d_w_up = du^T x;
