@@ -451,6 +451,7 @@ extern "C" int moe_ffn_gated_backward(const moe_ffn_gated_args *a, void *stream)
   // one launch for all, the tiles with more k first, unless two take less time
   for (const moe::GemmParams *p : {2 * ki >= kr ? &dx : &dw, 2 * ki >= kr ? &dw : &dx})
     for (int i = 0; i < p->problems; ++i) all.problem[all.problems++] = p->problem[i];
+  if (!dx.problems) all.a_rows = dw.a_rows;
   const moe::DenseTile ta = moe::gemm_pick_tile(moe::kGrads, all, sms, &t_all);
   cudaError_t e = moe::launch_dense_gemm(moe::kHiddenGrad, th, mh, hid, sms, st);
   if (e == cudaSuccess && dx.problems && dw.problems) {

@@ -401,3 +401,28 @@ def test_weights_that_the_kernel_before_makes(cuda_lib, rows):
         torch.cuda.synchronize()
         assert all(torch.equal(y, want[i]) for i, y in got)
     assert m.dense_status() == 0
+
+
+@pytest.mark.parametrize("ts,tb", [(F32, F32), (F32, BF16), (BF16, BF16)])
+@pytest.mark.parametrize("rows,hidden", [(3, 8192), (700, 8192), (310, 8184), (5, 8190)])
+@pytest.mark.parametrize("gate", ["vector", "group", "token"])
+def test_the_longest_rows(cuda_lib, ts, tb, rows, hidden, gate):
+    """Rows whose ring leaves the weights no shared memory, or holds one row."""
+    if gate == "group" and rows % max(1, rows // 3):
+        rows += -rows % 3
+    c = tn.make(rows, hidden, ts, tb, gate, True, True, seed=hidden)
+    if gate == "group":
+        c["gate"] = c["gate"][:3].contiguous()
+    out, y, d = tn.both(c)
+    tn.check_forward(c, out, y)
+    tn.check_backward(c, out, d)
+
+
+@pytest.mark.parametrize("rows,hidden,inter", [(9, 2048, 1024), (100, 1024, 2048), (127, 4096, 512)])
+def test_only_the_weights_gradients_of_few_rows(cuda_lib, rows, hidden, inter):
+    import deepseek_v4_moe_gb300 as m
+    t = tg.make(rows, hidden, inter, BF16, seed=rows)
+    y, saved, d = tg.run(*t, "silu")
+    d = m.gated_ffn_backward(*t[:4], saved, t[4], need_x=False)
+    assert set(d) == {"d_w_gate", "d_w_up", "d_w_down"}
+    tg.check(*t, "silu", y, saved, d)
