@@ -85,9 +85,14 @@ int type_bytes(int t) { return t == MOE_FFN_F32 ? 4 : 2; }
 bool is_type(int t) { return t == MOE_FFN_F32 || t == MOE_FFN_BF16 || t == MOE_FFN_F16; }
 bool aligned(const void *p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
-int launched(const char *who, cudaError_t e) {
-  return e == cudaSuccess ? MOE_FFN_OK : fail(MOE_FFN_ERR_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));
+// A CUDA call of this one failed.  The caller learns of it here, so the runtime forgets it: an error that stayed
+// recorded for the thread would be reported by its next calls too, whose work has nothing to do with it.  (One
+// that the context does not recover from comes back by itself.)
+int cuda_failed(const char *who, const char *what, cudaError_t e) {
+  cudaGetLastError();
+  return fail(MOE_FFN_ERR_CUDA, "%s: %s: %s", who, what, cudaGetErrorString(e));
 }
+int launched(const char *who, cudaError_t e) { return e == cudaSuccess ? MOE_FFN_OK : cuda_failed(who, "launch", e); }
 
 // an error left by earlier work is reported with nothing enqueued
 int pending(const char *who) {
@@ -115,13 +120,15 @@ struct DeviceSide {
 int device_side(const char *who, DeviceSide *d) {
   static std::atomic<int *> known[kMaxDevices];
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices)
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+    cudaGetLastError();
     return fail(MOE_FFN_ERR_CUDA, "%s: no usable current device", who);
+  }
   d->status = known[dev].load(std::memory_order_acquire);
   if (!d->status) {
     void *p = nullptr;
     const cudaError_t e = cudaGetSymbolAddress(&p, g_status);
-    if (e != cudaSuccess || !p) return fail(MOE_FFN_ERR_CUDA, "%s: cudaGetSymbolAddress: %s", who, cudaGetErrorString(e));
+    if (e != cudaSuccess || !p) return cuda_failed(who, "cudaGetSymbolAddress", e);
     d->status = static_cast<int *>(p);
     known[dev].store(d->status, std::memory_order_release);
   }
@@ -141,6 +148,7 @@ EncodeTiledFn find_encode() {
   if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
       q == cudaDriverEntryPointSuccess)
     return reinterpret_cast<EncodeTiledFn>(p);
+  cudaGetLastError();
   return nullptr;
 }
 
@@ -581,16 +589,18 @@ extern "C" int moe_ffn_dense_status(void *stream) {
   if (rc) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
-  if (cudaStreamIsCapturing(st, &capture) == cudaSuccess && capture != cudaStreamCaptureStatusNone)
+  cudaError_t e = cudaStreamIsCapturing(st, &capture);
+  if (e != cudaSuccess) return cuda_failed(who, "cudaStreamIsCapturing", e);
+  if (capture != cudaStreamCaptureStatusNone)
     return fail(MOE_FFN_ERR_UNSUPPORTED, "%s: the stream is being captured", who);
   static std::mutex one_at_a_time;  // g_status_out holds one call's bits until they are copied
   const std::lock_guard<std::mutex> lock(one_at_a_time);
   take_status_kernel<<<1, 1, 0, st>>>();
   int bits = 0;
-  cudaError_t e = cudaGetLastError();
+  e = cudaGetLastError();
   if (e == cudaSuccess) e = cudaMemcpyFromSymbolAsync(&bits, g_status_out, sizeof bits, 0, cudaMemcpyDeviceToHost, st);
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-  return e == cudaSuccess ? bits : fail(MOE_FFN_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
+  return e == cudaSuccess ? bits : cuda_failed(who, "reading the status", e);
 }
 
 extern "C" int moe_ffn_dense_fault_injection(int32_t enable, uint32_t wait_limit_us) {

@@ -307,7 +307,8 @@ int moe_ffn_set_fault_injection(moe_ffn_handle *h, int32_t which, uint32_t wait_
  * graphs that may run together workspaces of their own).  They can be captured into CUDA graphs.
  * All sums are in f32 and no atomics are used: the same call gives the same bits.  On an error
  * nothing is enqueued, except that a failed launch may leave earlier kernels of the call enqueued;
- * the message is moe_ffn_last_error(NULL) on the calling thread. */
+ * the message is moe_ffn_last_error(NULL) on the calling thread.  A failure that CUDA recovers from
+ * (a capture that became invalid, memory for a kernel's code) is reported by this call only. */
 #define MOE_FFN_F32 0
 #define MOE_FFN_BF16 1
 #define MOE_FFN_F16 2
