@@ -5,8 +5,8 @@
 //
 // The codes' products accumulate over one block of 128 k in f32 in TMEM (four tcgen05.mma kind::f8f6f4
 // of 32 k each); the epilogue warps then take the block's sums, multiply them by the block's two scales
-// and add them to f32 sums in registers.  So scales may be any f32 values, and no more than 128 products
-// are added before a scale is applied.  Two or more TMEM buffers let the MMAs of the next blocks run
+// and add them to f32 sums in registers.  So scales may be any f32 values (a block whose scales' product is no
+// normal f32 value takes them one at a time), and no more than 128 products are added before a scale is applied.  Two or more TMEM buffers let the MMAs of the next blocks run
 // meanwhile: a block of a 256 x 256 tile takes the tensor cores 512 cycles, its 128 x 256 sums a CTA's
 // multiply-adds 256 and its share of shared memory's bandwidth all of it, as 256 x 256 by a pair of CTAs
 // is the widest tile.
@@ -300,7 +300,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < C::kPer; ++i) sum[i] = 0.f;
       float next_a = sa[kb_first], next_b = sb[kb_first], next_b2 = sb2[kb_first];
       for (int kb = kb_first; kb < kb_end; ++kb, acc.next()) {
-        const uint64_t s1 = both(next_a * next_b), s2 = both(next_a * next_b2);
+        const float product = next_a * next_b, product2 = next_a * next_b2;
+        const uint64_t s1 = both(product), s2 = both(product2);
+        const bool apart = __any_sync(0xffffffffu, !scales_multiply(next_a, next_b, product) ||
+                                                       !scales_multiply(next_a, next_b2, product2));
         if (kb + 1 < kb_end) {
           next_a = sa[kb + 1];
           next_b = sb[kb + 1];
@@ -312,6 +315,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc.slot * BN + half * C::kPer);
+        if (apart) {  // rare, and so kept out of the registers of what follows: the scales are read again
+#pragma unroll
+          for (int c = 0; c < C::kPer; c += 16) {
+            const ScalePair f = scales_apart(sa[kb], (c < edge ? sb : sb2)[kb]);
+            float v[16];
+            tmem_ld16(tb + c, v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sum[c + i] = fmaf(v[i] * f.first, f.then, sum[c + i]);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if constexpr (PAIR) mbar_arrive_cluster(tempty0 + 8 * acc.slot);
+            else mbar_arrive(&tempty_bar[acc.slot]);
+          }
+          continue;
+        }
         constexpr int N = C::kPer / C::kChunk;
         float v[2][C::kChunk];
         tmem_ld_start(tb, v[0]);

@@ -179,13 +179,13 @@ __global__ void __launch_bounds__(32 * kWarps) fp8_gemv_kernel(const __grid_cons
         for (int r = 0; r < R; ++r) {
           float2 a[8];
           codes16(*reinterpret_cast<const uint4 *>(p.a + r * p.ld_a + k), p.a_e5m2, a);
-          const float both = scale * p.a_scale[(size_t)r * p.kb + blk];
+          const ScalePair s = scales_apart(scale, p.a_scale[(size_t)r * p.kb + blk]);
 #pragma unroll
           for (int c = 0; c < C; ++c) {
             float2 dot = make_float2(0.f, 0.f);
 #pragma unroll
             for (int e = 0; e < 8; ++e) dot = __ffma2_rn(a[e], b[c][e], dot);
-            sum[r * C + c] = fmaf(dot.x + dot.y, both, sum[r * C + c]);
+            sum[r * C + c] = fmaf((dot.x + dot.y) * s.first, s.then, sum[r * C + c]);
           }
         }
       }

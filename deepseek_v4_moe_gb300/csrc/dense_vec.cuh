@@ -139,6 +139,22 @@ __device__ __forceinline__ void load_eight(const T *row, int t, int n, int hidde
   e.get(o);
 }
 
+// A block's sum is multiplied by its two scales a and b.  Their product serves where it is a normal f32 value
+// (or 0, as one of them is); elsewhere it has lost bits, or is 0 or infinite, where the sum times both need not
+// be.  Then the sum is multiplied by one after the other, first by the one that leads away from the end of the
+// range at which the product lies: no step is less exact than the result.
+__device__ __forceinline__ bool scales_multiply(float a, float b, float product) {
+  return (__float_as_uint(product) & 0x7FFFFFFFu) - 0x00800000u < 0x7F000000u || a == 0.f || b == 0.f;
+}
+struct ScalePair {
+  float first, then;
+};
+__device__ __forceinline__ ScalePair scales_apart(float a, float b) {
+  const float product = a * b;
+  if (scales_multiply(a, b, product)) return ScalePair{1.f, product};
+  return (fabsf(a) < fabsf(b)) == (fabsf(product) > 1.f) ? ScalePair{a, b} : ScalePair{b, a};
+}
+
 // 1 / (1 + exp(-x)) by the approximate base-2 exponential and reciprocal: a few units of 2^-22, well below
 // the 16-bit types that what is made of it is rounded to; 0 and 1 far out, where exp(-x) overflows or
 // vanishes.  (With subnormals, which change nothing here, each takes several instructions more.)

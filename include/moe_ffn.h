@@ -397,7 +397,8 @@ int64_t moe_ffn_gated_workspace(const moe_ffn_gated_args *a, int32_t backward);
 
 /* Matrix product in 8-bit floating point with a scale for each block of 128:
  *   out[i, j] = sum_b a_scale[i, b] * b_scale[j / 128, b] * sum over k in block b of a[i, k] * b[j, k]
- * with blocks of 128 along k, the last of which may be shorter.  Sums are f32.  (The MXFP8 experts
+ * with blocks of 128 along k, the last of which may be shorter.  Sums are f32; scales may be any f32 values, and
+ * their product may leave f32's range where the block's result does not.  (The MXFP8 experts
  * above have a power-of-two scale for each 32 elements instead.) */
 #define MOE_FFN_E4M3 0
 #define MOE_FFN_E5M2 1
