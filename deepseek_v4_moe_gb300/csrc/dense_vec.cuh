@@ -173,7 +173,8 @@ __device__ __forceinline__ float act_value(int act, float g) {
 }
 __device__ __forceinline__ void act_both(int act, float g, float &a, float &da) {
   const float s = fast_sigmoid(act == kSilu ? g : kGelu2 * fmaf(0.044715f * g * g, g, g));
-  const float slope = act == kSilu ? 1.f : kGelu2 * fmaf(3.f * 0.044715f * g, g, 1.f);
+  // (finite: past 4e19, where its square leaves f32, what it is multiplied by is 0)
+  const float slope = act == kSilu ? 1.f : fminf(kGelu2 * fmaf(3.f * 0.044715f * g, g, 1.f), 3e38f);
   a = g * s;
   da = fmaf(a * (1.f - s), slope, s);
 }
