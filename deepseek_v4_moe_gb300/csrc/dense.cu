@@ -169,6 +169,15 @@ bool encode_map(CUtensorMap *m, const void *base, int bytes, int64_t inner, int6
 
 // ---- block_norm ----
 
+// A row stride holds a row, and the last row's place in memory stays far inside 64 bits: of the fewest rows
+// strides may be as large as memory, of 2^30 rows 2^30 elements.
+int check_stride(const char *who, const char *name, int64_t ld, int64_t rows, int64_t cols) {
+  if (ld < cols) return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: the row stride of %s is below hidden", who, name);
+  if (ld > ((int64_t)1 << 60) / rows)
+    return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: the row stride of %s is too large for %lld rows", who, name, (long long)rows);
+  return MOE_FFN_OK;
+}
+
 int check_norm(const char *who, const moe_ffn_block_norm_args *a) {
   if (!a) return fail(MOE_FFN_ERR_NULL_PTR, "%s: args is NULL", who);
   if (a->rows == 0) return fail(MOE_FFN_ERR_ROWS_ZERO, "%s: rows must be at least 1", who);
@@ -194,8 +203,9 @@ int check_norm(const char *who, const moe_ffn_block_norm_args *a) {
     if (!aligned(a->gate, type_bytes(a->gate_type))) return fail(MOE_FFN_ERR_ALIGNMENT, "%s: gate is misaligned", who);
   }
   const int sb = type_bytes(a->stream_type), bb = type_bytes(a->block_type);
-  if (a->ld_state < a->hidden || (a->f && a->ld_f < a->hidden))
-    return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: a row stride is below hidden", who);
+  int rc = check_stride(who, "state", a->ld_state, a->rows, a->hidden);
+  if (!rc && a->f) rc = check_stride(who, "f", a->ld_f, a->rows, a->hidden);
+  if (rc) return rc;
   if (!aligned(a->state, sb) || !aligned(a->f, bb) || !aligned(a->norm_f, 4) || !aligned(a->norm_next, 4))
     return fail(MOE_FFN_ERR_ALIGNMENT, "%s: a pointer is not aligned to its type", who);
   return MOE_FFN_OK;
@@ -249,9 +259,12 @@ int check_norm_grads(const char *who, const moe_ffn_block_norm_args *a, const mo
   if ((!a->norm_next && (g->d_y || g->d_norm_next)) || (!a->f && g->d_f) || (!a->norm_f && g->d_norm_f) ||
       (a->gate_kind == MOE_FFN_GATE_NONE && g->d_gate))
     return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: a gradient of something that is not given", who);
-  if ((g->d_out && g->ld_d_out < a->hidden) || (g->d_y && g->ld_d_y < a->hidden) || g->ld_d_state < a->hidden ||
-      (g->d_f && g->ld_d_f < a->hidden))
-    return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: a row stride is below hidden", who);
+  const int64_t R = a->rows, H = a->hidden;
+  if ((g->d_out && (rc = check_stride(who, "d_out", g->ld_d_out, R, H))) ||
+      (g->d_y && (rc = check_stride(who, "d_y", g->ld_d_y, R, H))) ||
+      (rc = check_stride(who, "d_state", g->ld_d_state, R, H)) ||
+      (g->d_f && (rc = check_stride(who, "d_f", g->ld_d_f, R, H))))
+    return rc;
   return MOE_FFN_OK;
 }
 
@@ -615,8 +628,9 @@ extern "C" int moe_ffn_block_norm(const moe_ffn_block_norm_args *a, void *stream
   if (rc) return rc;
   if ((a->f != nullptr) != (a->out != nullptr)) return fail(MOE_FFN_ERR_NULL_PTR, "%s: out goes with f", who);
   if ((a->norm_next != nullptr) != (a->y != nullptr)) return fail(MOE_FFN_ERR_NULL_PTR, "%s: y goes with norm_next", who);
-  if ((a->out && a->ld_out < a->hidden) || (a->y && a->ld_y < a->hidden))
-    return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: a row stride is below hidden", who);
+  if ((a->out && (rc = check_stride(who, "out", a->ld_out, a->rows, a->hidden))) ||
+      (a->y && (rc = check_stride(who, "y", a->ld_y, a->rows, a->hidden))))
+    return rc;
   const int sb = type_bytes(a->stream_type), bb = type_bytes(a->block_type);
   if (!aligned(a->out, sb) || !aligned(a->y, bb))
     return fail(MOE_FFN_ERR_ALIGNMENT, "%s: a pointer is not aligned to its type", who);

@@ -323,7 +323,7 @@ int moe_ffn_set_fault_injection(moe_ffn_handle *h, int32_t which, uint32_t wait_
  *   y = out * rsqrt(mean(out^2) + eps) * norm_next
  * With f NULL there is no block before: y is the norm of state, out is not written. */
 typedef struct moe_ffn_block_norm_args {
-  int32_t rows, hidden;         /* 1 <= hidden <= 8192, rows at most 2^30 */
+  int32_t rows, hidden;         /* 1 <= hidden <= 8192, rows at most 2^30, rows times any ld at most 2^60 */
   int32_t stream_type;          /* type of state and out: MOE_FFN_F32 or block_type */
   int32_t block_type;           /* type of f and y */
   int32_t gate_type;            /* MOE_FFN_F32 or block_type */
