@@ -94,6 +94,7 @@ ERR_NO_ROUTING_SOURCE, ERR_ALIAS, ERR_CUDA, ERR_NO_MEMORY, ERR_UNSUPPORTED, ERR_
 DEV_TOKEN_RANGE, DEV_ROUTE_RANGE, DEV_NONFINITE, DEV_TIMEOUT = 0x1, 0x2, 0x4, 0x8
 
 _lib = None
+build_error = None  # why load() could not build what was missing or out of date, where it went on without
 
 
 def declared_functions() -> list[str]:
@@ -104,14 +105,16 @@ def declared_functions() -> list[str]:
 
 def load(build: bool = True):
     """Loads the library, building it first when it is missing or older than its sources."""
-    global _lib
+    global _lib, build_error
     if _lib is not None:
         return _lib
     if build:
         from . import build as _build
         try:
             _build.build()
-        except RuntimeError:
+            build_error = None
+        except RuntimeError as e:
+            build_error = e
             if not os.path.exists(LIB_PATH):
                 raise
     if not os.path.exists(LIB_PATH):

@@ -5,11 +5,13 @@
 Each translation unit compiles in parallel into _build/, then one shared library is linked with the
 static CUDA runtime (the driver API is reached through cudaGetDriverEntryPointByVersion, so no
 libcuda link is needed).  The Python binding of the dense sublayer, _native.so, is compiled beside
-them against PyTorch's headers and linked to the library.
+them against PyTorch's headers and linked to the library; what it was compiled for is noted beside the
+objects, and a binding made for something else is built anew.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import hashlib
 import os
 import shutil
 import subprocess
@@ -23,6 +25,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe_ffn.so")
 NATIVE = os.path.join(PKG, "_native.so")
+NATIVE_KEY = os.path.join(BUILD, "native.key")
+NATIVE_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden"]
 SOURCES = ["moe_ffn.cu", "prelude.cu", "decode.cu", "decode_tc.cu", "dispatch.cu", "gemm_tc.cu", "splitgemm.cu",
            "noalloc.cu", "dense.cu", "dense_norm.cu", "dense_gemm.cu",
            "dense_fp8.cu", "dense_gemv.cu"]
@@ -42,7 +46,29 @@ def _stale() -> bool:
         return True
     t = min(os.path.getmtime(LIB), os.path.getmtime(NATIVE))
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
-    return any(os.path.getmtime(p) > t for p in deps)
+    return any(os.path.getmtime(p) > t for p in deps) or not native_fits()
+
+
+def native_key() -> str:
+    """What the binding depends on besides the sources' times: PyTorch (its inline code, types and C++ ABI),
+    Python, the compiler's flags, and the interface between the binding and the library."""
+    import torch
+    digest = hashlib.sha256()
+    for path in (os.path.join(INCLUDE, "moe_ffn.h"), os.path.join(CSRC, "binding.cpp")):
+        with open(path, "rb") as f:
+            digest.update(f.read())
+    return "\n".join([f"torch {torch.__version__}", f"cuda {torch.version.cuda}",
+                      f"cxx11 abi {int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"python {sysconfig.get_config_var('SOABI')}",
+                      " ".join(NATIVE_FLAGS), digest.hexdigest()])
+
+
+def native_fits() -> bool:
+    """There is a binding, and it was made for this PyTorch, Python and interface."""
+    try:
+        with open(NATIVE_KEY) as f:
+            return os.path.exists(NATIVE) and f.read() == native_key()
+    except OSError:
+        return False
 
 
 def _torch_dir() -> str:
@@ -56,7 +82,7 @@ def _compile_binding(cc: str) -> str:
     inc = [INCLUDE, t, os.path.join(t, "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"],
            os.path.join(os.path.dirname(os.path.dirname(cc)), "include")]
     obj = os.path.join(BUILD, "binding.o")
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+    cmd = ["g++", *NATIVE_FLAGS,
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            *[a for p in inc for a in ("-I" if p == INCLUDE else "-isystem", p)],
            "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
@@ -73,7 +99,13 @@ def _link_binding(obj: str) -> None:
                         "-ltorch_python"], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link of the binding failed:\n{r.stdout}\n{r.stderr}")
+    if os.path.exists(NATIVE_KEY):  # never the note of one binding beside another
+        os.remove(NATIVE_KEY)
     os.replace(tmp, NATIVE)
+    tmp = NATIVE_KEY + f".{os.getpid()}.tmp"
+    with open(tmp, "w") as f:
+        f.write(native_key())
+    os.replace(tmp, NATIVE_KEY)
 
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:

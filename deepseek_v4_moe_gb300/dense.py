@@ -25,7 +25,11 @@ _n = None  # the binding, once loaded
 def _native():
     global _n
     if _n is None:
+        from . import build
         _lib.load()  # builds what is missing
+        if not build.native_fits():
+            raise RuntimeError(f"{build.NATIVE} is missing or was built for another PyTorch, Python or interface, and "
+                               f"was not built anew") from _lib.build_error
         n = importlib.import_module("._native", __package__)
         n.set_error(MoeFFNError)
         _n = n
