@@ -107,6 +107,12 @@ Tensor fresh(const Where &w, at::IntArrayRef shape, ScalarType type) {
   return Tensor(at::detail::empty_cuda(shape, at::TensorOptions().dtype(type).device(w.device)));
 }
 
+// The call has written into a tensor that the caller gave: a gradient that autograd would take of what was in it
+// is refused, as after PyTorch's own in-place operations.
+void written(const Maybe &t) {
+  if (t && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+}
+
 // ---- block_norm ----
 
 moe_ffn_block_norm_args norm_args(const Where &w, const Tensor &state, const Maybe &f, const Maybe &norm_f, const Maybe &gate,
@@ -166,6 +172,7 @@ py::tuple block_norm(const Tensor &state, const Maybe &f, const Maybe &norm_f, c
   if (!block_dtype.is_none() && dtype_of(block_dtype) != block) refuse("block_dtype must be f's type");
   moe_ffn_block_norm_args a = norm_args(w, state, f, norm_f, gate, scale, norm_next, eps, block);
   const auto shape = state.sizes();
+  const Maybe given_out = out, given_y = y;
   if (f) {
     if (!out) out = fresh(w, shape, state.scalar_type());
     a.ld_out = matrix(w, "out", *out, shape, state.scalar_type());
@@ -181,6 +188,8 @@ py::tuple block_norm(const Tensor &state, const Maybe &f, const Maybe &norm_f, c
     refuse("y is written only with norm_next");
   }
   check(moe_ffn_block_norm(&a, w.stream));
+  written(given_out);
+  written(given_y);
   return py::make_tuple(f ? *out : state, y ? py::cast(*y) : py::none());
 }
 
@@ -265,6 +274,7 @@ py::object gated_ffn(const Tensor &x, const Tensor &w_gate, const Tensor &w_up, 
   const Where w("x", x);
   moe_ffn_gated_args a = gated_args(w, x, w_gate, w_up, w_down, activation);
   const ScalarType t = x.scalar_type();
+  const Maybe given = out;
   if (!out) out = fresh(w, x.sizes(), t);
   a.ld_y = matrix(w, "out", *out, x.sizes(), t);
   a.y = out->data_ptr();
@@ -277,6 +287,7 @@ py::object gated_ffn(const Tensor &x, const Tensor &w_gate, const Tensor &w_up, 
   }
   const Tensor ws = gated_workspace(w, a, 0);
   check(moe_ffn_gated_forward(&a, w.stream));
+  written(given);
   if (save) return py::make_tuple(*out, py::make_tuple(g, u));
   return py::cast(*out);
 }
@@ -361,10 +372,12 @@ Tensor fp8_matmul(const Tensor &a, const Tensor &a_scale, const Tensor &b, const
   p.b = b.data_ptr();
   p.a_scale = static_cast<float *>(whole(w, "a_scale", a_scale, {rows, kb}, ScalarType::Float));
   p.b_scale = static_cast<float *>(whole(w, "b_scale", b_scale, {(n + 127) / 128, kb}, ScalarType::Float));
+  const Maybe given = out;
   if (!out) out = fresh(w, {rows, n}, type);
   p.ld_out = matrix(w, "out", *out, {rows, n}, type);
   p.out = out->data_ptr();
   check(moe_ffn_fp8_matmul(&p, w.stream));
+  written(given);
   return *out;
 }
 

@@ -4,7 +4,8 @@ include/moe_ffn.h; the checks and the marshalling are in the compiled binding (c
 Every function enqueues on ``stream`` (default: the tensors' device's current stream) and returns
 device tensors without waiting.  Outputs and workspaces that a call allocates belong to that stream;
 inputs that belong to another one stay with the caller until the call's kernels have run.
-Gradients come from explicit ``*_backward`` calls; nothing is recorded for autograd.  Rows may be
+Gradients come from explicit ``*_backward`` calls; nothing is recorded for autograd, also where an argument
+requires a gradient.  Tensors given for a call to write into count as changed in place.  Rows may be
 strided (``stride(-1) == 1``); weights and gates are contiguous.  Refused arguments raise
 ``ValueError`` (types, shapes), ``TypeError`` (no tensor) or ``MoeFFNError`` with the library's code.
 """
