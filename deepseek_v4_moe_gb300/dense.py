@@ -39,6 +39,8 @@ def _native():
 
 def _on(t: torch.Tensor, stream: torch.cuda.Stream):
     """The context to run a call on tensor t on another stream in."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"a torch.Tensor is needed, got {type(t).__name__}")
     if stream.device != t.device:
         raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
     return torch.cuda.stream(stream)
