@@ -74,6 +74,7 @@ class MoeFfnGatedArgs(ctypes.Structure):
 
 
 TYPE_E4M3, TYPE_E5M2 = 0, 1
+TILES_FORWARD, TILES_BACKWARD, TILES_BACKWARD_X, TILES_BACKWARD_WEIGHTS, TILES_FP8 = range(5)
 
 
 class MoeFfnFp8MatmulArgs(ctypes.Structure):
@@ -168,6 +169,8 @@ def load(build: bool = True):
     lib.moe_ffn_dense_status.restype = ctypes.c_int
     lib.moe_ffn_dense_fault_injection.argtypes = [i32, ctypes.c_uint32]
     lib.moe_ffn_dense_fault_injection.restype = ctypes.c_int
+    lib.moe_ffn_dense_tiles.argtypes = [i32, i32, i32, i32, i32, ctypes.POINTER(i32)]
+    lib.moe_ffn_dense_tiles.restype = ctypes.c_int
     lib.moe_ffn_fp8_matmul.argtypes = [ctypes.POINTER(MoeFfnFp8MatmulArgs), vp]
     lib.moe_ffn_fp8_matmul.restype = ctypes.c_int
     lib.moe_ffn_fp8_quantise.argtypes = [ctypes.POINTER(MoeFfnFp8QuantiseArgs), vp]

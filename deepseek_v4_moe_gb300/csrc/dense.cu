@@ -332,6 +332,72 @@ int64_t gated_workspace(const moe_ffn_gated_args *a, bool backward) {
 
 int kblocks(int k) { return (k + 63) / 64; }
 
+// A launch of a call: its products, and the tile that they take on a GPU of so many SMs.
+struct Launch {
+  int mode;
+  moe::GemmParams p;
+  moe::DenseTile tile;
+};
+void pick(Launch &l, int sms) {
+  double t;
+  l.tile = moe::gemm_pick_tile(l.mode, l.p, sms, &t);
+}
+
+void forward_launches(const moe_ffn_gated_args *a, const DeviceSide &dev, int sms, Launch (&l)[2]) {
+  const int kh = kblocks(a->hidden), ki = kblocks(a->inter);
+  Launch &up = l[0], &down = l[1];
+  up.mode = moe::kGateUp;
+  down.mode = moe::kDown;
+  up.p = down.p = gemm_params(a, dev);
+  add_problem(up.p, a->rows, a->inter, kh, kh, 0, 0, false, nullptr, 0);
+  up.p.out[0] = a->workspace;
+  up.p.out[1] = a->gate;
+  up.p.out[2] = a->up;
+  add_problem(down.p, a->rows, a->hidden, ki, ki, 0, 0, false, a->y, a->ld_y);
+  pick(up, sms);
+  pick(down, sms);
+}
+
+// The backward pass's launches, two or three; `x`, `weights`: which gradients are wanted.
+int backward_launches(const moe_ffn_gated_args *a, bool x, bool weights, const DeviceSide &dev, int sms, Launch (&l)[3]) {
+  const int kh = kblocks(a->hidden), ki = kblocks(a->inter), kr = kblocks(a->rows);
+  const int64_t H = a->hidden, I = a->inter;
+  Launch &hid = l[0];
+  hid.mode = moe::kHiddenGrad;
+  hid.p = gemm_params(a, dev);
+  moe::GemmParams all = hid.p, dx = all, dw = all;
+  char *dg = static_cast<char *>(a->workspace);
+  add_problem(hid.p, a->rows, a->inter, kh, kh, 0, 0, false, nullptr, 0);
+  hid.p.out[0] = dg;
+  hid.p.out[1] = dg + a->rows * I * 2;
+  hid.p.out[2] = dg + a->rows * I * 4;
+  hid.p.e[0] = a->gate;
+  hid.p.e[1] = a->up;
+  pick(hid, sms);
+  if (x) add_problem(dx, a->rows, a->hidden, ki, 2 * ki, 0, 0, false, a->d_x, a->ld_d_x);
+  dw.a_rows = 128;  // its A is MN-major
+  if (weights) {
+    add_problem(dw, a->inter, a->hidden, kr, kr, 2, 2, true, a->d_w_gate, H);
+    add_problem(dw, a->inter, a->hidden, kr, kr, 3, 2, true, a->d_w_up, H);
+    add_problem(dw, a->hidden, a->inter, kr, kr, 4, 3, true, a->d_w_down, I);
+  }
+  // one launch for all, the tiles with more k first, unless two take less time
+  for (const moe::GemmParams *p : {2 * ki >= kr ? &dx : &dw, 2 * ki >= kr ? &dw : &dx})
+    for (int i = 0; i < p->problems; ++i) all.problem[all.problems++] = p->problem[i];
+  if (!x) all.a_rows = dw.a_rows;
+  double t_all, t_dx, t_dw;
+  l[1] = Launch{moe::kGrads, all, moe::gemm_pick_tile(moe::kGrads, all, sms, &t_all)};
+  if (x && weights) {
+    const moe::DenseTile tx = moe::gemm_pick_tile(moe::kGrads, dx, sms, &t_dx), tw = moe::gemm_pick_tile(moe::kGrads, dw, sms, &t_dw);
+    if (t_dx + t_dw < t_all) {
+      l[1] = Launch{moe::kGrads, dx, tx};
+      l[2] = Launch{moe::kGrads, dw, tw};
+      return 3;
+    }
+  }
+  return 2;
+}
+
 }  // namespace
 
 extern "C" int64_t moe_ffn_gated_workspace(const moe_ffn_gated_args *a, int32_t backward) {
@@ -388,23 +454,17 @@ extern "C" int moe_ffn_gated_forward(const moe_ffn_gated_args *a, void *stream) 
   }
   DeviceSide dev;
   if ((rc = device_side(who, &dev))) return rc;
-  const int kh = kblocks(a->hidden), ki = kblocks(a->inter);
-  moe::GemmParams up = gemm_params(a, dev), down = up;
-  add_problem(up, a->rows, a->inter, kh, kh, 0, 0, false, nullptr, 0);
-  up.out[0] = a->workspace;
-  up.out[1] = a->gate;
-  up.out[2] = a->up;
-  add_problem(down, a->rows, a->hidden, ki, ki, 0, 0, false, a->y, a->ld_y);
-  double t;
-  const moe::DenseTile tu = moe::gemm_pick_tile(moe::kGateUp, up, sms, &t), td = moe::gemm_pick_tile(moe::kDown, down, sms, &t);
-  const int bu = moe::gemm_b_box(moe::kGateUp, tu), bd = moe::gemm_b_box(moe::kDown, td);
+  Launch l[2];
+  forward_launches(a, dev, sms, l);
+  const Launch &up = l[0], &down = l[1];
+  const int bu = moe::gemm_b_box(moe::kGateUp, up.tile), bd = moe::gemm_b_box(moe::kDown, down.tile);
   moe::GemmMaps mu, md;
-  if (!encode_map(&mu.a[0], a->x, 2, H, R, a->ld_x, up.a_rows) || !encode_map(&mu.b[0], a->w_gate, 2, H, I, H, bu) ||
-      !encode_map(&mu.b[1], a->w_up, 2, H, I, H, bu) || !encode_map(&md.a[0], a->workspace, 2, I, R, I, down.a_rows) ||
+  if (!encode_map(&mu.a[0], a->x, 2, H, R, a->ld_x, up.p.a_rows) || !encode_map(&mu.b[0], a->w_gate, 2, H, I, H, bu) ||
+      !encode_map(&mu.b[1], a->w_up, 2, H, I, H, bu) || !encode_map(&md.a[0], a->workspace, 2, I, R, I, down.p.a_rows) ||
       !encode_map(&md.b[0], a->w_down, 2, I, H, I, bd))
     return fail(MOE_FFN_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", who);
-  cudaError_t e = moe::launch_dense_gemm(moe::kGateUp, tu, mu, up, sms, st);
-  if (e == cudaSuccess) e = moe::launch_dense_gemm(moe::kDown, td, md, down, sms, st);
+  cudaError_t e = moe::launch_dense_gemm(up.mode, up.tile, mu, up.p, sms, st);
+  if (e == cudaSuccess) e = moe::launch_dense_gemm(down.mode, down.tile, md, down.p, sms, st);
   return launched(who, e);
 }
 
@@ -444,45 +504,20 @@ extern "C" int moe_ffn_gated_backward(const moe_ffn_gated_args *a, void *stream)
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   char *dg = static_cast<char *>(a->workspace), *du = dg + R * I * 2, *h = du + R * I * 2;
 
-  const int kh = kblocks(a->hidden), ki = kblocks(a->inter), kr = kblocks(a->rows);
+  Launch l[3];
+  const int launches = backward_launches(a, a->d_x != nullptr, weights, dev, sms, l), box = l[0].p.a_rows;
   moe::GemmMaps mh, mg;
-  moe::GemmParams hid = gemm_params(a, dev), all = hid, dx = hid, dw = hid;
-  add_problem(hid, a->rows, a->inter, kh, kh, 0, 0, false, nullptr, 0);
-  hid.out[0] = dg;
-  hid.out[1] = du;
-  hid.out[2] = h;
-  hid.e[0] = a->gate;
-  hid.e[1] = a->up;
-  double t, t_all, t_dx, t_dw;
-  const moe::DenseTile th = moe::gemm_pick_tile(moe::kHiddenGrad, hid, sms, &t);
-  if (!encode_map(&mh.a[0], a->d_y, 2, H, R, a->ld_d_y, hid.a_rows) || !encode_map(&mh.b[0], a->w_down, 2, I, H, I, 64) ||
-      !encode_map(&mg.a[0], dg, 2, I, R, I, hid.a_rows) || !encode_map(&mg.a[1], du, 2, I, R, I, hid.a_rows) ||
+  if (!encode_map(&mh.a[0], a->d_y, 2, H, R, a->ld_d_y, box) || !encode_map(&mh.b[0], a->w_down, 2, I, H, I, 64) ||
+      !encode_map(&mg.a[0], dg, 2, I, R, I, box) || !encode_map(&mg.a[1], du, 2, I, R, I, box) ||
       !encode_map(&mg.a[2], dg, 2, I, R, I, 64) || !encode_map(&mg.a[3], du, 2, I, R, I, 64) ||
       !encode_map(&mg.a[4], a->d_y, 2, H, R, a->ld_d_y, 64) || !encode_map(&mg.b[0], a->w_gate, 2, H, I, H, 64) ||
       !encode_map(&mg.b[1], a->w_up, 2, H, I, H, 64) || !encode_map(&mg.b[2], a->x, 2, H, R, a->ld_x, 64) ||
       !encode_map(&mg.b[3], h, 2, I, R, I, 64))
     return fail(MOE_FFN_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", who);
-  if (a->d_x) add_problem(dx, a->rows, a->hidden, ki, 2 * ki, 0, 0, false, a->d_x, a->ld_d_x);
-  dw.a_rows = 128;  // its A is MN-major
-  if (weights) {
-    add_problem(dw, a->inter, a->hidden, kr, kr, 2, 2, true, a->d_w_gate, H);
-    add_problem(dw, a->inter, a->hidden, kr, kr, 3, 2, true, a->d_w_up, H);
-    add_problem(dw, a->hidden, a->inter, kr, kr, 4, 3, true, a->d_w_down, I);
-  }
-  // one launch for all, the tiles with more k first, unless two take less time
-  for (const moe::GemmParams *p : {2 * ki >= kr ? &dx : &dw, 2 * ki >= kr ? &dw : &dx})
-    for (int i = 0; i < p->problems; ++i) all.problem[all.problems++] = p->problem[i];
-  if (!dx.problems) all.a_rows = dw.a_rows;
-  const moe::DenseTile ta = moe::gemm_pick_tile(moe::kGrads, all, sms, &t_all);
-  cudaError_t e = moe::launch_dense_gemm(moe::kHiddenGrad, th, mh, hid, sms, st);
-  if (e == cudaSuccess && dx.problems && dw.problems) {
-    const moe::DenseTile tx = moe::gemm_pick_tile(moe::kGrads, dx, sms, &t_dx), tw = moe::gemm_pick_tile(moe::kGrads, dw, sms, &t_dw);
-    if (t_dx + t_dw < t_all) {
-      e = moe::launch_dense_gemm(moe::kGrads, tx, mg, dx, sms, st);
-      return launched(who, e == cudaSuccess ? moe::launch_dense_gemm(moe::kGrads, tw, mg, dw, sms, st) : e);
-    }
-  }
-  return launched(who, e == cudaSuccess ? moe::launch_dense_gemm(moe::kGrads, ta, mg, all, sms, st) : e);
+  cudaError_t e = cudaSuccess;
+  for (int i = 0; i < launches && e == cudaSuccess; ++i)
+    e = moe::launch_dense_gemm(l[i].mode, l[i].tile, i ? mg : mh, l[i].p, sms, st);
+  return launched(who, e);
 }
 
 extern "C" int moe_ffn_fp8_matmul(const moe_ffn_fp8_matmul_args *a, void *stream) {
@@ -614,6 +649,52 @@ extern "C" int moe_ffn_dense_status(void *stream) {
   if (e == cudaSuccess) e = cudaMemcpyFromSymbolAsync(&bits, g_status_out, sizeof bits, 0, cudaMemcpyDeviceToHost, st);
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
   return e == cudaSuccess ? bits : cuda_failed(who, "reading the status", e);
+}
+
+extern "C" int moe_ffn_dense_tiles(int32_t call, int32_t rows, int32_t n, int32_t k, int32_t num_sms, int32_t *tiles) {
+  const char *who = "dense_tiles";
+  if (!tiles) return fail(MOE_FFN_ERR_NULL_PTR, "%s: tiles is NULL", who);
+  if (num_sms < 8 || num_sms > 4096) return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: num_sms must be in 8..4096", who);
+  int count = 0;
+  auto add = [&](int product, moe::DenseTile t) {
+    *tiles++ = product;
+    *tiles++ = t.bn;
+    *tiles++ = t.kind;
+    ++count;
+  };
+  if (call == MOE_FFN_TILES_FP8) {
+    if (rows < 1 || rows > (1 << 24) || n < 1 || n > (1 << 20) || k < 16 || k % 16 || k > (1 << 20))
+      return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: rows, n or k is not one of an fp8_matmul", who);
+    if (moe::fp8_gemv(rows, n, k)) return 0;
+    moe::Fp8Params p = {};
+    p.m = rows;
+    p.n = n;
+    p.kb = (k + 127) / 128;
+    add(4, moe::fp8_pick_tile(p, num_sms));
+    return count;
+  }
+  moe_ffn_gated_args a = {};
+  a.rows = rows;
+  a.hidden = k;
+  a.inter = n;
+  a.type = MOE_FFN_BF16;
+  a.ld_x = k;
+  int rc = check_gated(who, &a);
+  if (rc) return rc;
+  if (call == MOE_FFN_TILES_FORWARD) {
+    if (moe::gated_gemv(rows, k, n)) return 0;
+    Launch l[2];
+    forward_launches(&a, DeviceSide{}, num_sms, l);
+    for (const Launch &x : l) add(x.mode, x.tile);
+    return count;
+  }
+  if (call != MOE_FFN_TILES_BACKWARD && call != MOE_FFN_TILES_BACKWARD_X && call != MOE_FFN_TILES_BACKWARD_WEIGHTS)
+    return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: unknown call", who);
+  Launch l[3];
+  const int launches = backward_launches(&a, call != MOE_FFN_TILES_BACKWARD_WEIGHTS, call != MOE_FFN_TILES_BACKWARD_X,
+                                         DeviceSide{}, num_sms, l);
+  for (int i = 0; i < launches; ++i) add(l[i].mode, l[i].tile);
+  return count;
 }
 
 extern "C" int moe_ffn_dense_fault_injection(int32_t enable, uint32_t wait_limit_us) {

@@ -446,6 +446,18 @@ int moe_ffn_dense_status(void *stream);
  * something that never comes, and wait_limit_us (0: 2 s) bounds every wait. */
 int moe_ffn_dense_fault_injection(int32_t enable, uint32_t wait_limit_us);
 
+/* Test hook: the tiles that a call with these sizes (contiguous rows) takes on a GPU of num_sms SMs, three
+ * numbers for each of its tensor-core launches in order: the product (0 gate and up, 1 down, 2 hidden gradient,
+ * 3 gradients, 4 FP8), the tile's columns, and how CTAs share it (0 one CTA, 1 a pair, 2 a cluster that shares
+ * k).  Returns the number of launches, at most 3, 0 where the weight-streaming kernels serve the call, or a
+ * negative code.  n and k: inter and hidden of the gated block. */
+#define MOE_FFN_TILES_FORWARD 0
+#define MOE_FFN_TILES_BACKWARD 1
+#define MOE_FFN_TILES_BACKWARD_X 2
+#define MOE_FFN_TILES_BACKWARD_WEIGHTS 3
+#define MOE_FFN_TILES_FP8 4
+int moe_ffn_dense_tiles(int32_t call, int32_t rows, int32_t n, int32_t k, int32_t num_sms, int32_t *tiles);
+
 /* Text of the last error on this handle, or, when h is NULL, of the last failed call made without
  * a handle (init, the allocation-free split, a NULL handle) on the calling thread: that message
  * is kept per thread, so threads that fail at the same time do not overwrite each other's text.
