@@ -429,9 +429,12 @@ cudaError_t launch(const CUtensorMap &a, const CUtensorMap &b, const Fp8Params &
 // ---- quantiser ----
 // A block's scale is its largest magnitude over the largest code (448 or 57344); 1 for a block of
 // zeros, at least 2^-126 so that it is a normal number, and with pow2 rounded up to a power of two.  A
-// code is x times the scale's reciprocal (a division for each value made the kernel arithmetic-bound:
-// 18.9 us for 4096 x 4096 bf16) rounded to nearest even.  The magnitudes are compared as integers, so that a NaN
-// counts as the largest and makes the scale NaN.
+// code is the quotient x / scale rounded to nearest even.  (A division for each value made the kernel
+// arithmetic-bound: 18.9 us for 4096 x 4096 bf16.)  With the scale's reciprocal r, correctly rounded, q = x r is
+// off by a last place at most, its remainder q s - x is exact in one multiply-add, and q - r (q s - x) is the
+// correctly rounded quotient, with the sign of a zero (P. Markstein, "Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990); of values below 2^-100, whose remainders may lie below f32's range, q may stay as it is.
+// The magnitudes are compared as integers, so that a NaN counts as the largest and makes the scale NaN.
 
 __device__ __forceinline__ float block_scale(uint32_t amax, bool e5m2, bool pow2) {
   if (amax == 0u) return 1.f;
@@ -442,11 +445,21 @@ __device__ __forceinline__ float block_scale(uint32_t amax, bool e5m2, bool pow2
   return s;
 }
 
-__device__ __forceinline__ uint32_t codes4(const float *v, float r, bool e5m2) {
-  const __nv_fp8_interpretation_t f = e5m2 ? __NV_E5M2 : __NV_E4M3;
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[0] * r, v[1] * r), __NV_SATFINITE, f);
-  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[2] * r, v[3] * r), __NV_SATFINITE, f);
-  return lo | hi << 16;
+struct Divisor {
+  float r, s;
+};
+// (an infinite scale: every finite value's quotient is 0)
+__device__ __forceinline__ Divisor divisor(float scale) {
+  return Divisor{__frcp_rn(scale), __float_as_uint(scale) == 0x7F800000u ? 0.f : scale};
+}
+__device__ __forceinline__ uint32_t codes2(float a, float b, const Divisor &d, bool e5m2) {
+  const float2 q = __fmul2_rn(make_float2(a, b), make_float2(d.r, d.r));
+  const float2 rest = __ffma2_rn(q, make_float2(d.s, d.s), make_float2(-a, -b));
+  return __nv_cvt_float2_to_fp8x2(__ffma2_rn(rest, make_float2(-d.r, -d.r), q), __NV_SATFINITE,
+                                  e5m2 ? __NV_E5M2 : __NV_E4M3);
+}
+__device__ __forceinline__ uint32_t codes4(const float *v, const Divisor &d, bool e5m2) {
+  return codes2(v[0], v[1], d, e5m2) | codes2(v[2], v[3], d, e5m2) << 16;
 }
 
 // Sixteen lanes take the 128 values of a row's block, eight consecutive ones each.
@@ -465,10 +478,10 @@ __device__ __forceinline__ void load_part(const QuantiseParams &p, int row, int 
   }
 }
 template <bool WIDE>
-__device__ __forceinline__ void store_part(const QuantiseParams &p, int row, int col, float r, const float (&v)[8]) {
+__device__ __forceinline__ void store_part(const QuantiseParams &p, int row, int col, const Divisor &d, const float (&v)[8]) {
   if (row >= p.rows || col >= p.k) return;
   uint8_t *dst = p.codes + (size_t)row * p.ld_codes + col;
-  const uint32_t a = codes4(v, r, p.e5m2), b = codes4(v + 4, r, p.e5m2);
+  const uint32_t a = codes4(v, d, p.e5m2), b = codes4(v + 4, d, p.e5m2);
   if constexpr (WIDE) {
     *reinterpret_cast<uint2 *>(dst) = make_uint2(a, b);
   } else {
@@ -512,7 +525,7 @@ __global__ void __launch_bounds__(256) quantise_rows_kernel(const __grid_constan
 #pragma unroll
     for (int i = 0; i < kQuantBlocks; ++i) {
       const float s = block_scale(m[i], p.e5m2, p.pow2);
-      store_part<WIDE>(p, r, (b0 + i) * kScaleBlock + part * 8, __frcp_rn(s), v[i]);
+      store_part<WIDE>(p, r, (b0 + i) * kScaleBlock + part * 8, divisor(s), v[i]);
       if (part == 0 && r < p.rows && b0 + i < blocks) p.scales[(size_t)r * blocks + b0 + i] = s;
     }
     row += rows_on;
@@ -543,9 +556,10 @@ __global__ void __launch_bounds__(256) quantise_tiles_kernel(const __grid_consta
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = max(m, largest_of[i]);
-  const float s = block_scale(m, p.e5m2, p.pow2), r = __frcp_rn(s);
+  const float s = block_scale(m, p.e5m2, p.pow2);
+  const Divisor d = divisor(s);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) store_part<WIDE>(p, row + 16 * i, col, r, v[i]);
+  for (int i = 0; i < 8; ++i) store_part<WIDE>(p, row + 16 * i, col, d, v[i]);
   if (threadIdx.x == 0) p.scales[blockIdx.x] = s;
 }
 

@@ -130,7 +130,7 @@ def fp8_quantise(x: torch.Tensor, block_rows: int = 1, pow2_scales: bool = False
 
     ``x`` [rows, k] float32, bfloat16 or float16.  ``block_rows`` 1 (activations) or 128 (weights).  A
     block's scale is its largest magnitude over the largest code, 1 for zeros, at least 2^-126, with
-    ``pow2_scales`` rounded up to a power of two; a code is x * (1 / scale) rounded to nearest even.
+    ``pow2_scales`` rounded up to a power of two; a code is the quotient x / scale rounded to nearest even.
     """
     if stream is not None:
         with _on(x, stream):

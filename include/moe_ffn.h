@@ -420,8 +420,9 @@ int moe_ffn_fp8_matmul(const moe_ffn_fp8_matmul_args *a, void *stream);
 
 /* Makes such an operand: a block is block_rows (1 or 128) rows x 128 columns, those at the ends may be
  * smaller.  scale = (largest magnitude of the block) / (largest finite code: 448 or 57344), 1 for a
- * block of zeros, at least 2^-126; with pow2 rounded up to a power of two.  code = x * (1 / scale), the
- * reciprocal and the product in f32, rounded to nearest even.  A block with a NaN has the scale NaN, one with an infinity the scale infinity, and
+ * block of zeros, at least 2^-126; with pow2 rounded up to a power of two.  code = x / scale, the quotient
+ * in f32, rounded to nearest even.  (The f32 quotient of a value below 2^-100 may be off by a last place.)
+ * A block with a NaN has the scale NaN, one with an infinity the scale infinity, and
  * products with either are not finite. */
 typedef struct moe_ffn_fp8_quantise_args {
   int32_t rows, k;               /* k at most 2^20, rows at most 2^24 */
