@@ -143,8 +143,11 @@ __device__ __forceinline__ void load_eight(const T *row, int t, int n, int hidde
 // (or 0, as one of them is); elsewhere it has lost bits, or is 0 or infinite, where the sum times both need not
 // be.  Then the sum is multiplied by one after the other, first by the one that leads away from the end of the
 // range at which the product lies: no step is less exact than the result.
+__device__ __forceinline__ bool normal_f32(float x) {
+  return (__float_as_uint(x) & 0x7FFFFFFFu) - 0x00800000u < 0x7F000000u;
+}
 __device__ __forceinline__ bool scales_multiply(float a, float b, float product) {
-  return (__float_as_uint(product) & 0x7FFFFFFFu) - 0x00800000u < 0x7F000000u || a == 0.f || b == 0.f;
+  return normal_f32(product) || a == 0.f || b == 0.f;
 }
 struct ScalePair {
   float first, then;
@@ -155,9 +158,9 @@ __device__ __forceinline__ ScalePair scales_apart(float a, float b) {
   return (fabsf(a) < fabsf(b)) == (fabsf(product) > 1.f) ? ScalePair{a, b} : ScalePair{b, a};
 }
 
-// 1 / (1 + exp(-x)) by the approximate base-2 exponential and reciprocal: a few units of 2^-22, well below
-// the 16-bit types that what is made of it is rounded to; 0 and 1 far out, where exp(-x) overflows or
-// vanishes.  (With subnormals, which change nothing here, each takes several instructions more.)
+// 1 / (1 + exp(-x)) by the approximate base-2 exponential and reciprocal: a few units of 2^-22, and |x| 2^-23
+// more where it is small, as the exponent's rounding counts (2^-17 at -80); well below the 16-bit types that what is
+// made of it is rounded to; 0 and 1 far out, where exp(-x) overflows or vanishes.  (With subnormals, which change nothing here, each takes several instructions more.)
 __device__ __forceinline__ float fast_sigmoid(float x) {
   float e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
