@@ -7,9 +7,10 @@
 // of 32 k each); the epilogue warps then take the block's sums, multiply them by the block's two scales
 // and add them to f32 sums in registers.  So scales may be any f32 values (a block whose scales' product is no
 // normal f32 value takes them one at a time), and no more than 128 products are added before a scale is applied.  Two or more TMEM buffers let the MMAs of the next blocks run
-// meanwhile: a block of a 256 x 256 tile takes the tensor cores 512 cycles, its 128 x 256 sums a CTA's
-// multiply-adds 256 and its share of shared memory's bandwidth all of it, as 256 x 256 by a pair of CTAs
-// is the widest tile.
+// meanwhile: a block of a 256 x 256 tile by a pair of CTAs, the widest, takes the tensor cores 512 cycles, its
+// 128 x 256 sums a CTA's multiply-adds 256 and its share of shared memory's bandwidth all of it.  The epilogue
+// has 168 registers a thread at 320 threads: 128 sums and two chunks of 32 columns in flight do not fit, 112
+// and two of 16 do, and 256 x 224 is the tile at work at 4096 x 4096 x 4096 (times at fp8_pick_tile).
 //
 // A CTA (one per SM, persistent over tiles of 128 x BN; a pair of CTAs: 256 x BN):
 //   warp 0     TMA producer: a ring of blocks (A 128 rows, B BN rows or half of them, 128 bytes of k each)
@@ -315,7 +316,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc.slot * BN + half * C::kPer);
-        if (apart) {  // rare, and so kept out of the registers of what follows: the scales are read again
+        // rare, and so kept out of the registers of what follows (in that loop it spilled 324 bytes of the 256-column
+        // tile's): the scales are read again
+        if (apart) {
 #pragma unroll
           for (int c = 0; c < C::kPer; c += 16) {
             const ScalePair f = scales_apart(sa[kb], (c < edge ? sb : sb2)[kb]);
@@ -432,9 +435,11 @@ cudaError_t launch(const CUtensorMap &a, const CUtensorMap &b, const Fp8Params &
 // code is the quotient x / scale rounded to nearest even.  (A division for each value made the kernel
 // arithmetic-bound: 18.9 us for 4096 x 4096 bf16.)  With the scale's reciprocal r, correctly rounded, q = x r is
 // off by a last place at most, its remainder q s - x is exact in one multiply-add, and q - r (q s - x) is the
-// correctly rounded quotient, with the sign of a zero (P. Markstein, "Computation of elementary functions on the IBM RISC System/6000
-// processor", 1990); of values below 2^-100, whose remainders may lie below f32's range, q may stay as it is.
-// The magnitudes are compared as integers, so that a NaN counts as the largest and makes the scale NaN.
+// correctly rounded quotient, with the sign of a zero (P. Markstein, "Computation of elementary functions on the
+// IBM RISC System/6000 processor", 1990); of values below 2^-100, whose remainders may lie below f32's range, q
+// may stay as it is.  4096 x 4096 bf16 takes 12.3 us, 11.9 with q alone, which gave 3 to 6 of 10^4 bf16 values
+// another code.  The magnitudes are compared as integers, so that a NaN counts as the largest and makes the
+// scale NaN.
 
 __device__ __forceinline__ float block_scale(uint32_t amax, bool e5m2, bool pow2) {
   if (amax == 0u) return 1.f;
@@ -568,7 +573,7 @@ cudaError_t quantise_typed(const QuantiseParams &p, int num_sms, cudaStream_t st
   const long long blocks = (p.k + kScaleBlock - 1) / kScaleBlock;
   if (p.tall == 1) {
     const long long per_row = (blocks + kQuantBlocks - 1) / kQuantBlocks;
-    const long long ctas = (p.rows * per_row + 15) / 16, most = (long long)num_sms * 3;  // those that an SM holds
+    const long long ctas = (p.rows * per_row + 15) / 16, most = (long long)num_sms * 3;  // three for each SM (by registers four fit)
     const int grid = (int)(ctas < most ? ctas : most);
     return launch_pdl(p.wide ? quantise_rows_kernel<T, true> : quantise_rows_kernel<T, false>, dim3(grid), dim3(256), 0, st, p);
   }
@@ -586,8 +591,8 @@ long long fp8_tiles(const Fp8Params &p, DenseTile t) {
 // The tile that takes the least time (see gemm_pick_tile), from what they measured at 4096 x 4096 (us): a k
 // block with 256, 224 and 128 columns on a pair 0.47, 0.42 and 0.28, with 128, 64 and 32 on a CTA by
 // itself 0.305, 0.265 and 0.26; a launch 3.5 to 4.4, a further wave 0.4 and, of clusters that share a tile's
-// k, which make one tile each, 4.2.  4096 rows took 59.4 in 224 columns (four waves), 66.0 in 256, 73.3 in
-// single CTAs' 128.
+// k, which make one tile each, 4.2.  4096 rows took 59.4 in 224 columns (four waves; 60.6 since
+// scales that do not multiply are told apart), 66.0 in 256, 73.3 in single CTAs' 128.
 DenseTile fp8_pick_tile(const Fp8Params &p, int num_sms) {
   const struct {
     DenseTile tile;

@@ -506,9 +506,9 @@ int gemm_b_box(int mode, DenseTile t) {
   return mode == kGateUp || t.kind == kPairTile ? t.bn / 2 : t.bn;
 }
 
-// The tile that takes the least time by what tiles measured (us, bf16): a k block of 64 with 256, 128, 64
-// and 32 columns 0.339, 0.200, 0.157 and 0.147 on a CTA by itself (few columns: the time to issue four
-// MMAs), 0.045 + 0.00092 for each column on a pair; the epilogue of a tile 0.25 + 0.0085 for each column
+// The tile that takes the least time by what tiles measured (us on the GPU, launches replayed in a graph, bf16):
+// a k block of 64 with 256, 128, 64 and 32 columns 0.339, 0.200, 0.157 and 0.147 on a CTA by itself (few columns:
+// the time to issue four MMAs), 0.045 + 0.00092 for each column on a pair; the epilogue of a tile 0.25 + 0.0085 for each column
 // of a plain result, 0.45 + 0.0078 of kGateUp, and 0.032 a column of kHiddenGrad, whose ten bytes for each
 // value are memory's; of the two the longer, and together no less than 0.8 of their sum; a launch with its
 // prologue 3.8, of pairs 5.8.  Rows that are no multiple of 128 bytes make each 128 bytes of a box two
@@ -524,7 +524,7 @@ int gemm_b_box(int mode, DenseTile t) {
 // Several products in one launch save a launch and share its last wave, but also the tile.  The backward
 // pass of 1016 rows, hidden 224, inter 424 took 21.0 with two launches for kGrads, 13.9 with one; 4096 rows,
 // hidden 4096, inter 2048 268 and 247; 8 rows, hidden 4096, inter 2048, whose dx wants clusters, 40.9 with
-// two, 45.7 with one.
+// two and 45.7 with one, where the model puts one ahead all the same (30.5 for 31.7 of these launches).
 DenseTile gemm_pick_tile(int mode, const GemmParams &p, int num_sms, double *time) {
   const bool b_mn = mode == kHiddenGrad || mode == kGrads;
   const double per_col = mode == kGateUp ? 0.0078 : mode == kHiddenGrad ? 0.032 : 0.0085;

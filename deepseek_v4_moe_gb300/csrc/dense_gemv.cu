@@ -112,6 +112,7 @@ __global__ void __launch_bounds__(32 * kWarps) gated_gemv_kernel(const __grid_co
         static_cast<T *>(p.gate)[at] = from_f32<T>(g);
         static_cast<T *>(p.up)[at] = from_f32<T>(u);
       }
+      // rounded as the tensor cores' operand is: a row's result does not take more bits for being one of few
       static_cast<T *>(p.out)[at] = from_f32<T>(act_value(p.act, g) * u);
     } else {
       static_cast<T *>(p.out)[r * p.ld_out + col] = from_f32<T>(sum[r]);
@@ -139,8 +140,8 @@ __device__ __forceinline__ void codes16(const uint4 w, bool e5m2, float2 (&o)[8]
 
 // FP8 with block scales: eight lanes share a block of 128 codes; a lane's 16 products are summed, then
 // scaled and added.  A warp takes C neighbouring columns (of one block of b_scale), so that the conversion
-// of a's codes serves C columns: 4096 x 4096 took 6.6 us with one column a warp, 5.8 with four; on four
-// tokens 11.5 and 8.7.
+// of a's codes serves C columns: 4096 x 4096 took 6.6 us with one column a warp, 5.8 with four (6.0 since
+// it looks at the scales' product); on four tokens 11.5 and 8.7.
 // Rounds of 512 codes whose loads are in flight: four 16-byte loads in a lane, eight where registers allow it
 // (four tokens leave none: 10.1 us for 8.7).
 template <int R, int C>
@@ -294,8 +295,8 @@ bool gated_gemv(int rows, int hidden, int inter) {
   return rows <= 4 || (rows <= 8 && (long long)rows * hidden * inter <= 1 << 24);
 }
 
-// Here the conversions of the codes grow with the rows: 16384 x 1024 took 4.9, 6.0, 7.7 and 9.3 us for 1 to 4
-// rows, tiles 5.9; 2048 x 2048 3.3 to 4.5, tiles 5.7.
+// Here the conversions of the codes grow with the rows: 16384 x 1024 took 5.0, 6.1, 7.7 and 9.3 us for 1 to 4
+// rows, tiles 5.9; 2048 x 2048 3.2 to 4.5, tiles 5.7.
 bool fp8_gemv(int rows, int n, int k) {
   return rows == 1 || (rows <= 4 && (long long)rows * n * k <= 1 << 25);
 }

@@ -6,7 +6,8 @@ device tensors without waiting.  Outputs and workspaces that a call allocates be
 inputs that belong to another one stay with the caller until the call's kernels have run.
 Gradients come from explicit ``*_backward`` calls; nothing is recorded for autograd, also where an argument
 requires a gradient.  Tensors given for a call to write into count as changed in place.  Rows may be
-strided (``stride(-1) == 1``); weights and gates are contiguous.  Refused arguments raise
+strided (``stride(-1) == 1``) but not lie in one another, as an expanded tensor's do; weights and gates are
+contiguous.  Refused arguments raise
 ``ValueError`` (types, shapes), ``TypeError`` (no tensor) or ``MoeFFNError`` with the library's code.
 """
 from __future__ import annotations
@@ -101,7 +102,8 @@ def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down:
     ``x`` [rows, hidden] bfloat16 or float16; ``w_gate``, ``w_up`` [inter, hidden] and ``w_down``
     [hidden, inter] of its type; hidden and inter multiples of 8, every tensor 16-byte aligned and row
     strides multiples of 8.  ``activation``: "silu" or "gelu"
-    (tanh form).  Returns y [rows, hidden]; with ``save`` also the pair (g, u) of projections
+    (tanh form).  Sums are float32; the activated product is rounded to x's type before the down projection (in
+    float16 past 65504 to infinity), while the routed block keeps its own in two parts.  Returns y [rows, hidden]; with ``save`` also the pair (g, u) of projections
     [rows, inter] that :func:`gated_ffn_backward` takes.
     """
     if stream is not None:
@@ -114,7 +116,8 @@ def gated_ffn_backward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor
                        d_y: torch.Tensor, activation: str = "silu", need_x: bool = True, need_weights: bool = True,
                        stream: Optional[torch.cuda.Stream] = None) -> dict:
     """Gradients of :func:`gated_ffn` from what it saved: a dict of d_x, d_w_gate, d_w_up and d_w_down
-    (of the inputs' type), without d_x or the weights' where they are not needed."""
+    (of the inputs' type), without d_x or the weights' where they are not needed.  The gradients of the two
+    projections and the activated product are rounded to that type on the way."""
     if stream is not None:
         with _on(x, stream):
             return (_n or _native()).gated_ffn_backward(x, w_gate, w_up, w_down, saved[0], saved[1], d_y,
