@@ -19,5 +19,5 @@ scales for blocks of 128) and ``fp8_quantise``, which makes its operands; ``dens
 device status bits.
 """
 from .api import MoeFFN, MoeFFNError, config_from  # noqa: F401
-from .dense import (block_norm, block_norm_backward, dense_status, fp8_matmul, fp8_quantise,  # noqa: F401
-                    gated_ffn, gated_ffn_backward)
+from .dense import (block_norm, block_norm_backward, block_norm_fp8, dense_status, fp8_matmul,  # noqa: F401
+                    fp8_quantise, gated_ffn, gated_ffn_backward, gated_quantise)

@@ -88,6 +88,15 @@ class MoeFfnFp8QuantiseArgs(ctypes.Structure):
                 ("pow2", c_i32), ("x", c_vp), ("ld_x", c_i64), ("codes", c_vp), ("ld_codes", c_i64), ("scales", c_vp)]
 
 
+class MoeFfnFp8Out(ctypes.Structure):
+    _fields_ = [("code_type", c_i32), ("pow2", c_i32), ("codes", c_vp), ("ld_codes", c_i64), ("scales", c_vp)]
+
+
+class MoeFfnGatedQuantiseArgs(ctypes.Structure):
+    _fields_ = [("rows", c_i32), ("columns", c_i32), ("type", c_i32), ("activation", c_i32), ("gate", c_vp),
+                ("ld_gate", c_i64), ("up", c_vp), ("ld_up", c_i64)]
+
+
 # return codes and device status bits (include/moe_ffn.h)
 OK, ERR_NULL_PTR, ERR_BAD_CONFIG, ERR_LAYER_RANGE, ERR_ROWS_ZERO, ERR_ROWS_RANGE = 0, -1, -2, -3, -4, -5
 ERR_NO_ROUTING_SOURCE, ERR_ALIAS, ERR_CUDA, ERR_NO_MEMORY, ERR_UNSUPPORTED, ERR_ALIGNMENT, ERR_NO_WEIGHTS = (
@@ -175,6 +184,11 @@ def load(build: bool = True):
     lib.moe_ffn_fp8_matmul.restype = ctypes.c_int
     lib.moe_ffn_fp8_quantise.argtypes = [ctypes.POINTER(MoeFfnFp8QuantiseArgs), vp]
     lib.moe_ffn_fp8_quantise.restype = ctypes.c_int
+    out8 = ctypes.POINTER(MoeFfnFp8Out)
+    lib.moe_ffn_block_norm_fp8.argtypes = [norm, out8, vp]
+    lib.moe_ffn_block_norm_fp8.restype = ctypes.c_int
+    lib.moe_ffn_gated_quantise.argtypes = [ctypes.POINTER(MoeFfnGatedQuantiseArgs), out8, vp]
+    lib.moe_ffn_gated_quantise.restype = ctypes.c_int
     lib.moe_ffn_last_error.argtypes = [vp]
     lib.moe_ffn_last_error.restype = ctypes.c_char_p
     lib.moe_ffn_destroy.argtypes = [vp]

@@ -193,6 +193,62 @@ py::tuple block_norm(const Tensor &state, const Maybe &f, const Maybe &norm_f, c
   return py::make_tuple(f ? *out : state, y ? py::cast(*y) : py::none());
 }
 
+// codes [rows, k] and scales [rows, ceil(k / 128)] of a call's result
+moe_ffn_fp8_out fp8_out(const Where &w, int64_t rows, int64_t k, py::object dtype, bool pow2, Tensor &codes, Tensor &scales) {
+  const ScalarType type = dtype_of(dtype);
+  if (fp8_code(type) < 0) refuse("dtype must be float8_e4m3fn or float8_e5m2");
+  codes = fresh(w, {rows, k}, type);
+  scales = fresh(w, {rows, (k + 127) / 128}, ScalarType::Float);
+  moe_ffn_fp8_out o = {};
+  o.code_type = fp8_code(type);
+  o.pow2 = pow2;
+  o.codes = codes.data_ptr();
+  o.ld_codes = k;
+  o.scales = static_cast<float *>(scales.data_ptr());
+  return o;
+}
+
+py::tuple block_norm_fp8(const Tensor &state, const Maybe &f, const Maybe &norm_f, const Maybe &gate, double scale,
+                         const Tensor &norm_next, double eps, bool pow2, py::object dtype, Maybe out) {
+  const Where w("state", state);
+  const ScalarType block = f ? f->scalar_type() : state.scalar_type();
+  moe_ffn_block_norm_args a = norm_args(w, state, f, norm_f, gate, scale, norm_next, eps, block);
+  const auto shape = state.sizes();
+  const Maybe given = out;
+  if (f) {
+    if (!out) out = fresh(w, shape, state.scalar_type());
+    a.ld_out = matrix(w, "out", *out, shape, state.scalar_type());
+    a.out = out->data_ptr();
+  } else if (out) {
+    refuse("out is written only with f");
+  }
+  Tensor codes, scales;
+  const moe_ffn_fp8_out o = fp8_out(w, shape[0], shape[1], dtype, pow2, codes, scales);
+  check(moe_ffn_block_norm_fp8(&a, &o, w.stream));
+  written(given);
+  return py::make_tuple(f ? *out : state, codes, scales);
+}
+
+py::tuple gated_quantise(const Tensor &gate, const Tensor &up, int activation, bool pow2, py::object dtype) {
+  const Where w("gate", gate);
+  const ScalarType t = gate.scalar_type();
+  if (t != ScalarType::BFloat16 && t != ScalarType::Half) refuse("gate must be bfloat16 or float16");
+  two("gate", gate);
+  moe_ffn_gated_quantise_args a = {};
+  a.rows = size32("rows", gate.size(0));
+  a.columns = size32("columns", gate.size(1));
+  a.type = type_code(t);
+  a.activation = activation;
+  a.ld_gate = matrix(w, "gate", gate, gate.sizes(), t);
+  a.gate = gate.data_ptr();
+  a.ld_up = matrix(w, "up", up, gate.sizes(), t);
+  a.up = up.data_ptr();
+  Tensor codes, scales;
+  const moe_ffn_fp8_out o = fp8_out(w, gate.size(0), gate.size(1), dtype, pow2, codes, scales);
+  check(moe_ffn_gated_quantise(&a, &o, w.stream));
+  return py::make_tuple(codes, scales);
+}
+
 py::dict block_norm_backward(const Tensor &out, const Maybe &f, const Maybe &norm_f, const Maybe &gate, double scale,
                              const Maybe &norm_next, double eps, const Maybe &d_out, const Maybe &d_y) {
   const Where w("out", out);
@@ -387,6 +443,8 @@ Tensor fp8_matmul(const Tensor &a, const Tensor &a_scale, const Tensor &b, const
 PYBIND11_MODULE(_native, m) {
   m.def("set_error", [](py::object cls) { g_error = cls.release().ptr(); });
   m.def("block_norm", torch::wrap_pybind_function(&block_norm));
+  m.def("block_norm_fp8", torch::wrap_pybind_function(&block_norm_fp8));
+  m.def("gated_quantise", torch::wrap_pybind_function(&gated_quantise));
   m.def("block_norm_backward", torch::wrap_pybind_function(&block_norm_backward));
   m.def("gated_ffn", torch::wrap_pybind_function(&gated_ffn));
   m.def("gated_ffn_backward", torch::wrap_pybind_function(&gated_ffn_backward));

@@ -9,97 +9,13 @@
 #include <mutex>
 
 #include "dense.h"
+#include "entry.h"
 #include "kernels.h"
 #include "moe_ffn.h"
 
 namespace {
 
-constexpr int kMaxDevices = 64;
-
-int fail(int code, const char *fmt, ...) {
-  char buf[256];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof buf, fmt, ap);
-  va_end(ap);
-  moe::set_global_error(buf);
-  return code;
-}
-
-// SMs of the current device; a negative code where it is no sm_103 device
-int current_sms() {
-  static std::atomic<int> known[kMaxDevices];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
-    cudaGetLastError();
-    return fail(MOE_FFN_ERR_CUDA, "no usable current device");
-  }
-  int sms = known[dev].load(std::memory_order_relaxed);
-  if (sms) return sms;
-  int major = 0, minor = 0;
-  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-    cudaGetLastError();
-    return fail(MOE_FFN_ERR_CUDA, "cannot query device %d", dev);
-  }
-  if (major != 10 || minor != 3) return fail(MOE_FFN_ERR_UNSUPPORTED, "needs an sm_103 device, found sm_%d%d", major, minor);
-  known[dev].store(sms, std::memory_order_relaxed);
-  return sms;
-}
-
-// A tensor argument's memory: `rows` rows of `cols` elements, `ld` elements apart; width and pitch in bytes.
-struct Span {
-  const void *p;
-  uintptr_t end, width, pitch;
-  int64_t ld;
-  const char *name;
-};
-Span span(const char *name, const void *p, int64_t rows, int64_t cols, int64_t ld, int bytes) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-  return Span{p, p && rows > 0 ? a + (uintptr_t)((rows - 1) * ld + cols) * bytes : a, (uintptr_t)cols * bytes,
-              (uintptr_t)ld * bytes, ld, name};
-}
-bool overlap(const Span &a, const Span &b) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-  if (!(a.p && b.p && x < b.end && y < a.end)) return false;
-  if (a.pitch != b.pitch || a.pitch == 0) return true;
-  // rows at the same distance, as of two column ranges of one tensor: b's begin this far into a's pitch
-  const uintptr_t into = y >= x ? (y - x) % a.pitch : (a.pitch - (x - y) % a.pitch) % a.pitch;
-  return into < a.width || into + b.width > a.pitch;
-}
-// An output may overlap no input and no other output, but for the one input it may be itself.
-int check_overlaps(const char *who, const Span *outs, int n_outs, const Span *ins, int n_ins, int same_out, int same_in) {
-  for (int i = 0; i < n_outs; ++i) {
-    for (int j = 0; j < n_ins; ++j)
-      if (overlap(outs[i], ins[j]) &&
-          !(i == same_out && j == same_in && outs[i].p == ins[j].p && outs[i].ld == ins[j].ld))
-        return fail(MOE_FFN_ERR_ALIAS, "%s: %s overlaps %s", who, outs[i].name, ins[j].name);
-    for (int j = 0; j < i; ++j)
-      if (overlap(outs[i], outs[j])) return fail(MOE_FFN_ERR_ALIAS, "%s: %s overlaps %s", who, outs[i].name, outs[j].name);
-  }
-  return MOE_FFN_OK;
-}
-
-int type_bytes(int t) { return t == MOE_FFN_F32 ? 4 : 2; }
-bool is_type(int t) { return t == MOE_FFN_F32 || t == MOE_FFN_BF16 || t == MOE_FFN_F16; }
-bool aligned(const void *p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
-
-// A CUDA call of this one failed.  The caller learns of it here, so the runtime forgets it: an error that stayed
-// recorded for the thread would be reported by its next calls too, whose work has nothing to do with it.  (One
-// that the context does not recover from comes back by itself.)
-int cuda_failed(const char *who, const char *what, cudaError_t e) {
-  cudaGetLastError();
-  return fail(MOE_FFN_ERR_CUDA, "%s: %s: %s", who, what, cudaGetErrorString(e));
-}
-int launched(const char *who, cudaError_t e) { return e == cudaSuccess ? MOE_FFN_OK : cuda_failed(who, "launch", e); }
-
-// an error left by earlier work is reported with nothing enqueued
-int pending(const char *who) {
-  const cudaError_t e = cudaPeekAtLastError();
-  return e == cudaSuccess ? MOE_FFN_OK
-                          : fail(MOE_FFN_ERR_CUDA, "%s: a CUDA error is pending from earlier work: %s", who, cudaGetErrorString(e));
-}
+using namespace moe::entry;
 
 // ---- what the tensor-core kernels share: status word, wait bound, tensor maps ----
 
@@ -168,15 +84,6 @@ bool encode_map(CUtensorMap *m, const void *base, int bytes, int64_t inner, int6
 }
 
 // ---- block_norm ----
-
-// A row stride holds a row, and the last row's place in memory stays far inside 64 bits: of the fewest rows
-// strides may be as large as memory, of 2^30 rows 2^30 elements.
-int check_stride(const char *who, const char *name, int64_t ld, int64_t rows, int64_t cols) {
-  if (ld < cols) return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: the row stride of %s is below hidden", who, name);
-  if (ld > ((int64_t)1 << 60) / rows)
-    return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: the row stride of %s is too large for %lld rows", who, name, (long long)rows);
-  return MOE_FFN_OK;
-}
 
 int check_norm(const char *who, const moe_ffn_block_norm_args *a) {
   if (!a) return fail(MOE_FFN_ERR_NULL_PTR, "%s: args is NULL", who);
@@ -299,8 +206,6 @@ int check_gated(const char *who, const moe_ffn_gated_args *a) {
     return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: unknown activation", who);
   return MOE_FFN_OK;
 }
-
-constexpr int64_t kLdMax = (int64_t)1 << 36;  // a row stride in bytes stays below the tensor maps' 2^40
 
 int check_rows_of(const char *who, const char *name, const void *p, int64_t ld, int64_t cols) {
   if (!p) return fail(MOE_FFN_ERR_NULL_PTR, "%s: %s is NULL", who, name);
@@ -703,22 +608,33 @@ extern "C" int moe_ffn_dense_fault_injection(int32_t enable, uint32_t wait_limit
   return MOE_FFN_OK;
 }
 
-extern "C" int moe_ffn_block_norm(const moe_ffn_block_norm_args *a, void *stream) {
-  const char *who = "block_norm";
+namespace {
+
+// block_norm, with y in its type or (o) as FP8 codes and scales
+int block_norm(const char *who, const moe_ffn_block_norm_args *a, const moe_ffn_fp8_out *o, void *stream) {
   int rc = check_norm(who, a);
   if (rc) return rc;
   if ((a->f != nullptr) != (a->out != nullptr)) return fail(MOE_FFN_ERR_NULL_PTR, "%s: out goes with f", who);
-  if ((a->norm_next != nullptr) != (a->y != nullptr)) return fail(MOE_FFN_ERR_NULL_PTR, "%s: y goes with norm_next", who);
+  if (o) {
+    if (!a->norm_next || !o->codes || !o->scales) return fail(MOE_FFN_ERR_NULL_PTR, "%s: norm_next, codes or scales is NULL", who);
+    if (a->y) return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: y is not written", who);
+    if (o->code_type != MOE_FFN_E4M3 && o->code_type != MOE_FFN_E5M2) return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: unknown type", who);
+    if ((rc = check_stride(who, "codes", o->ld_codes, a->rows, a->hidden))) return rc;
+  } else if ((a->norm_next != nullptr) != (a->y != nullptr)) {
+    return fail(MOE_FFN_ERR_NULL_PTR, "%s: y goes with norm_next", who);
+  }
   if ((a->out && (rc = check_stride(who, "out", a->ld_out, a->rows, a->hidden))) ||
       (a->y && (rc = check_stride(who, "y", a->ld_y, a->rows, a->hidden))))
     return rc;
   const int sb = type_bytes(a->stream_type), bb = type_bytes(a->block_type);
-  if (!aligned(a->out, sb) || !aligned(a->y, bb))
+  if (!aligned(a->out, sb) || !aligned(a->y, bb) || (o && !aligned(o->scales, 4)))
     return fail(MOE_FFN_ERR_ALIGNMENT, "%s: a pointer is not aligned to its type", who);
-  Span ins[5], outs[2] = {span("out", a->out, a->rows, a->hidden, a->ld_out, sb),
-                          span("y", a->y, a->rows, a->hidden, a->ld_y, bb)};
+  const int64_t blocks = (a->hidden + moe::kScaleBlock - 1) / moe::kScaleBlock;
+  Span ins[5], outs[4] = {span("out", a->out, a->rows, a->hidden, a->ld_out, sb), span("y", a->y, a->rows, a->hidden, a->ld_y, bb),
+                          span("codes", o ? o->codes : nullptr, a->rows, a->hidden, o ? o->ld_codes : 0, 1),
+                          span("scales", o ? o->scales : nullptr, a->rows, blocks, blocks, 4)};
   const int n_ins = norm_inputs(a, ins);
-  if ((rc = check_overlaps(who, outs, 2, ins, n_ins, 0, 0))) return rc;
+  if ((rc = check_overlaps(who, outs, 4, ins, n_ins, 0, 0))) return rc;
   const int sms = current_sms();
   if (sms < 0) return sms;
   if ((rc = pending(who))) return rc;
@@ -727,7 +643,70 @@ extern "C" int moe_ffn_block_norm(const moe_ffn_block_norm_args *a, void *stream
   p.ld_out = a->ld_out;
   p.y = a->y;
   p.ld_y = a->ld_y;
+  if (o) {
+    p.codes = static_cast<uint8_t *>(o->codes);
+    p.ld_codes = o->ld_codes;
+    p.scales = o->scales;
+    p.e5m2 = o->code_type == MOE_FFN_E5M2;
+    p.pow2 = o->pow2 != 0;
+  }
   return launched(who, moe::launch_block_norm(p, sms, static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" int moe_ffn_block_norm(const moe_ffn_block_norm_args *a, void *stream) {
+  return block_norm("block_norm", a, nullptr, stream);
+}
+
+extern "C" int moe_ffn_block_norm_fp8(const moe_ffn_block_norm_args *a, const moe_ffn_fp8_out *o, void *stream) {
+  const char *who = "block_norm_fp8";
+  if (!o) return fail(MOE_FFN_ERR_NULL_PTR, "%s: out is NULL", who);
+  return block_norm(who, a, o, stream);
+}
+
+extern "C" int moe_ffn_gated_quantise(const moe_ffn_gated_quantise_args *a, const moe_ffn_fp8_out *o, void *stream) {
+  const char *who = "gated_quantise";
+  if (!a || !o) return fail(MOE_FFN_ERR_NULL_PTR, "%s: args or out is NULL", who);
+  if (a->rows == 0) return fail(MOE_FFN_ERR_ROWS_ZERO, "%s: rows must be at least 1", who);
+  if (a->rows < 0 || a->rows > (1 << 24)) return fail(MOE_FFN_ERR_ROWS_RANGE, "%s: rows must be at most 2^24", who);
+  if (a->columns < 1 || a->columns > (1 << 20)) return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: columns must be in 1..2^20", who);
+  if ((a->type != MOE_FFN_BF16 && a->type != MOE_FFN_F16) || (o->code_type != MOE_FFN_E4M3 && o->code_type != MOE_FFN_E5M2))
+    return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: unknown type", who);
+  if (a->activation != MOE_FFN_ACT_SILU && a->activation != MOE_FFN_ACT_GELU)
+    return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: unknown activation", who);
+  if (!a->gate || !a->up || !o->codes || !o->scales) return fail(MOE_FFN_ERR_NULL_PTR, "%s: a pointer is NULL", who);
+  if (a->ld_gate < a->columns || a->ld_up < a->columns || o->ld_codes < a->columns || a->ld_gate > kLdMax ||
+      a->ld_up > kLdMax || o->ld_codes > kLdMax)
+    return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: a row stride is below the columns", who);
+  if (!aligned(a->gate, 2) || !aligned(a->up, 2) || !aligned(o->scales, 4))
+    return fail(MOE_FFN_ERR_ALIGNMENT, "%s: gate, up or scales is misaligned", who);
+  const int64_t R = a->rows, K = a->columns, KB = (K + 127) / 128;
+  const Span ins[] = {span("gate", a->gate, R, K, a->ld_gate, 2), span("up", a->up, R, K, a->ld_up, 2)};
+  const Span outs[] = {span("codes", o->codes, R, K, o->ld_codes, 1), span("scales", o->scales, R, KB, KB, 4)};
+  int rc = check_overlaps(who, outs, 2, ins, 2, -1, -1);
+  if (rc) return rc;
+  const int sms = current_sms();
+  if (sms < 0) return sms;
+  if ((rc = pending(who))) return rc;
+  moe::GatedQuantiseParams p = {};
+  p.q.rows = a->rows;
+  p.q.k = a->columns;
+  p.q.type = a->type;
+  p.q.e5m2 = o->code_type == MOE_FFN_E5M2;
+  p.q.pow2 = o->pow2 != 0;
+  p.q.tall = 1;
+  p.q.x = a->gate;
+  p.q.ld_x = a->ld_gate;
+  p.q.codes = static_cast<uint8_t *>(o->codes);
+  p.q.ld_codes = o->ld_codes;
+  p.q.scales = o->scales;
+  p.q.wide = K % 8 == 0 && aligned(a->gate, 16) && a->ld_gate % 8 == 0 && aligned(a->up, 16) && a->ld_up % 8 == 0 &&
+             aligned(o->codes, 8) && o->ld_codes % 8 == 0;
+  p.up = a->up;
+  p.ld_up = a->ld_up;
+  p.act = a->activation;
+  return launched(who, moe::launch_gated_quantise(p, sms, static_cast<cudaStream_t>(stream)));
 }
 
 extern "C" int64_t moe_ffn_block_norm_workspace(const moe_ffn_block_norm_args *a, const moe_ffn_block_norm_grads *g) {

@@ -8,6 +8,7 @@ namespace moe {
 
 enum DenseType : int { kF32 = 0, kBF16 = 1, kF16 = 2 };
 constexpr int kNormHiddenMax = 8192;
+constexpr int kScaleBlock = 128;  // columns that share a scale in FP8
 
 enum GateKind : int { kGateNone = 0, kGateVector = 1, kGateToken = 2 };
 
@@ -21,6 +22,10 @@ struct NormParams {
   // forward
   void *out, *y;
   long long ld_out, ld_y;
+  uint8_t *codes;                // y as FP8 codes and scales [rows, ceil(hidden / 128)] instead
+  long long ld_codes;
+  float *scales;
+  int e5m2, pow2;
   // backward
   const void *d_out, *d_y;
   long long ld_d_out, ld_d_y;
@@ -95,8 +100,6 @@ cudaError_t launch_dense_gemm(int mode, DenseTile tile, const GemmMaps &maps, Ge
 
 // ---- FP8 with block scales (dense_fp8.cu) ----
 
-constexpr int kScaleBlock = 128;
-
 struct Fp8Params {
   int m, n, kb;              // kb: blocks of 128 along k
   int a_e5m2, b_e5m2, out_type;
@@ -121,10 +124,19 @@ struct QuantiseParams {
   int wide;                  // x in 16-byte pieces, codes in 8-byte pieces
 };
 
+// act(gate) up as codes and scales of a row's blocks
+struct GatedQuantiseParams {
+  QuantiseParams q;          // x: gate; type bf16 or f16, tall 1
+  const void *up;
+  long long ld_up;
+  int act;
+};
+
 DenseTile fp8_pick_tile(const Fp8Params &p, int num_sms);
 cudaError_t launch_fp8_matmul(DenseTile tile, const CUtensorMap &a, const CUtensorMap &b, Fp8Params p, int num_sms,
                               cudaStream_t st);
 cudaError_t launch_fp8_quantise(const QuantiseParams &p, int num_sms, cudaStream_t st);
+cudaError_t launch_gated_quantise(const GatedQuantiseParams &p, int num_sms, cudaStream_t st);
 
 // ---- products for a few rows on the CUDA cores (dense_gemv.cu) ----
 

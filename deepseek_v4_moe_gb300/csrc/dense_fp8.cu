@@ -24,6 +24,7 @@
 #include "common.cuh"
 #include "dense.h"
 #include "dense_tc.cuh"
+#include "dense_quant.cuh"
 #include "dense_vec.cuh"
 #include "kernels.h"
 
@@ -430,42 +431,7 @@ cudaError_t launch(const CUtensorMap &a, const CUtensorMap &b, const Fp8Params &
 }
 
 // ---- quantiser ----
-// A block's scale is its largest magnitude over the largest code (448 or 57344); 1 for a block of
-// zeros, at least 2^-126 so that it is a normal number, and with pow2 rounded up to a power of two.  A
-// code is the quotient x / scale rounded to nearest even.  (A division for each value made the kernel
-// arithmetic-bound: 18.9 us for 4096 x 4096 bf16.)  With the scale's reciprocal r, correctly rounded, q = x r is
-// off by a last place at most, its remainder q s - x is exact in one multiply-add, and q - r (q s - x) is the
-// correctly rounded quotient, with the sign of a zero (P. Markstein, "Computation of elementary functions on the
-// IBM RISC System/6000 processor", 1990); of values below 2^-100, whose remainders may lie below f32's range, q
-// may stay as it is.  4096 x 4096 bf16 takes 12.3 us, 11.9 with q alone, which gave 3 to 6 of 10^4 bf16 values
-// another code.  The magnitudes are compared as integers, so that a NaN counts as the largest and makes the
-// scale NaN.
-
-__device__ __forceinline__ float block_scale(uint32_t amax, bool e5m2, bool pow2) {
-  if (amax == 0u) return 1.f;
-  float s = __fdiv_rn(__uint_as_float(amax), e5m2 ? 57344.f : 448.f);
-  if (s < 1.17549435e-38f) s = 1.17549435e-38f;
-  const uint32_t u = __float_as_uint(s);
-  if (pow2 && (u & 0x7FFFFFu) && u < 0x7F800000u) s = __uint_as_float((u & 0x7F800000u) + 0x800000u);
-  return s;
-}
-
-struct Divisor {
-  float r, s;
-};
-// (an infinite scale: every finite value's quotient is 0)
-__device__ __forceinline__ Divisor divisor(float scale) {
-  return Divisor{__frcp_rn(scale), __float_as_uint(scale) == 0x7F800000u ? 0.f : scale};
-}
-__device__ __forceinline__ uint32_t codes2(float a, float b, const Divisor &d, bool e5m2) {
-  const float2 q = __fmul2_rn(make_float2(a, b), make_float2(d.r, d.r));
-  const float2 rest = __ffma2_rn(q, make_float2(d.s, d.s), make_float2(-a, -b));
-  return __nv_cvt_float2_to_fp8x2(__ffma2_rn(rest, make_float2(-d.r, -d.r), q), __NV_SATFINITE,
-                                  e5m2 ? __NV_E5M2 : __NV_E4M3);
-}
-__device__ __forceinline__ uint32_t codes4(const float *v, const Divisor &d, bool e5m2) {
-  return codes2(v[0], v[1], d, e5m2) | codes2(v[2], v[3], d, e5m2) << 16;
-}
+// Scales and codes: dense_quant.cuh.
 
 // Sixteen lanes take the 128 values of a row's block, eight consecutive ones each.
 template <typename T, bool WIDE>
@@ -495,13 +461,6 @@ __device__ __forceinline__ void store_part(const QuantiseParams &p, int row, int
       if (col + e < p.k) dst[e] = (uint8_t)((e < 4 ? a : b) >> (8 * (e & 3)));
   }
 }
-__device__ __forceinline__ uint32_t largest(const float (&v)[8]) {
-  uint32_t m = 0u;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(v[e]) & 0x7FFFFFFFu);
-  return m;
-}
-
 constexpr int kQuantBlocks = 4;  // neighbouring blocks of a row that 16 lanes take at a time: their loads overlap
 
 template <typename T, bool WIDE>
@@ -581,6 +540,65 @@ cudaError_t quantise_typed(const QuantiseParams &p, int num_sms, cudaStream_t st
   return launch_pdl(p.wide ? quantise_tiles_kernel<T, true> : quantise_tiles_kernel<T, false>, dim3(grid), dim3(256), 0, st, p);
 }
 
+// act(gate) up of a row's blocks as codes and scales: the operand of a gated block's second FP8 product, from what
+// the first left.  The product is formed and quantised in f32: through memory in 16 bits it would be rounded once more,
+// and cost four bytes a value on the way out and in again.  Bound by the bytes of gate and up.
+constexpr int kGatedBlocks = 2;
+
+template <typename T, bool WIDE>
+__global__ void __launch_bounds__(256) gated_quantise_kernel(const __grid_constant__ GatedQuantiseParams p) {
+  const int blocks = (p.q.k + kScaleBlock - 1) / kScaleBlock, per_row = (blocks + kGatedBlocks - 1) / kGatedBlocks;
+  const int part = threadIdx.x & 15, step = gridDim.x * 16;
+  const long long first = (long long)blockIdx.x * 16 + (threadIdx.x >> 4);
+  long long row = first / per_row;
+  int group = (int)(first % per_row);
+  const int rows_on = step / per_row, groups_on = step % per_row;
+  QuantiseParams up = p.q;
+  up.x = p.up;
+  up.ld_x = p.ld_up;
+  pdl_wait();
+  while (__any_sync(0xffffffffu, row < p.q.rows)) {
+    const int r = row < p.q.rows ? (int)row : p.q.rows, b0 = group * kGatedBlocks;
+    float g[kGatedBlocks][8], u[kGatedBlocks][8];
+    uint32_t m[kGatedBlocks];
+#pragma unroll
+    for (int i = 0; i < kGatedBlocks; ++i) {
+      load_part<T, WIDE>(p.q, r, (b0 + i) * kScaleBlock + part * 8, g[i]);
+      load_part<T, WIDE>(up, r, (b0 + i) * kScaleBlock + part * 8, u[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kGatedBlocks; ++i) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) g[i][e] = act_value(p.act, g[i][e]) * u[i][e];
+      m[i] = largest(g[i]);
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < kGatedBlocks; ++i) m[i] = max(m[i], __shfl_xor_sync(0xffffffffu, m[i], o));
+#pragma unroll
+    for (int i = 0; i < kGatedBlocks; ++i) {
+      const float s = block_scale(m[i], p.q.e5m2, p.q.pow2);
+      store_part<WIDE>(p.q, r, (b0 + i) * kScaleBlock + part * 8, divisor(s), g[i]);
+      if (part == 0 && r < p.q.rows && b0 + i < blocks) p.q.scales[(size_t)r * blocks + b0 + i] = s;
+    }
+    row += rows_on;
+    group += groups_on;
+    if (group >= per_row) {
+      group -= per_row;
+      ++row;
+    }
+  }
+}
+
+template <typename T>
+cudaError_t gated_quantise_typed(const GatedQuantiseParams &p, int num_sms, cudaStream_t st) {
+  const long long blocks = (p.q.k + kScaleBlock - 1) / kScaleBlock, per_row = (blocks + kGatedBlocks - 1) / kGatedBlocks;
+  const long long ctas = (p.q.rows * per_row + 15) / 16, most = (long long)num_sms * 4;
+  const int grid = (int)(ctas < most ? ctas : most);
+  return launch_pdl(p.q.wide ? gated_quantise_kernel<T, true> : gated_quantise_kernel<T, false>, dim3(grid), dim3(256), 0, st, p);
+}
+
 long long fp8_tiles(const Fp8Params &p, DenseTile t) {
   const int rows = t.kind == kPairTile ? 2 * kBM : kBM;
   return (long long)((p.m + rows - 1) / rows) * ((p.n + t.bn - 1) / t.bn);
@@ -641,6 +659,11 @@ cudaError_t launch_fp8_quantise(const QuantiseParams &p, int num_sms, cudaStream
   if (p.type == kF32) return quantise_typed<float>(p, num_sms, st);
   if (p.type == kBF16) return quantise_typed<__nv_bfloat16>(p, num_sms, st);
   return quantise_typed<__half>(p, num_sms, st);
+}
+
+cudaError_t launch_gated_quantise(const GatedQuantiseParams &p, int num_sms, cudaStream_t st) {
+  if (p.q.type == kBF16) return gated_quantise_typed<__nv_bfloat16>(p, num_sms, st);
+  return gated_quantise_typed<__half>(p, num_sms, st);
 }
 
 }  // namespace moe

@@ -32,6 +32,7 @@
 #include <type_traits>
 
 #include "dense.h"
+#include "dense_quant.cuh"
 #include "dense_tc.cuh"
 #include "dense_vec.cuh"
 #include "kernels.h"
@@ -139,9 +140,73 @@ __device__ __forceinline__ Pairs gate_set(const NormParams &p, int row, int gate
 
 // (Single values: 64 registers and 32 warps on an SM, some of them spilled, in place of 124 and 16 warps: 2000 x 4001
 // bf16 39 -> 28 us, 4096 x 3001 f32 57 -> 44.)
-template <typename TS, typename TB, bool VEC>
+// Writes y as FP8 codes with a scale for each block of 128 columns, of its f32 values.  VEC: a block of a set is 16
+// neighbouring lanes' eight columns each.  Otherwise (columns t + n e) a warp's columns of one e lie in one block,
+// several warps' in the same one: their maxima meet in shared memory (`amax`, one word for each block, zeros on entry
+// and on return), by integer atomics, whose order changes nothing.
+template <bool VEC>
+__device__ __forceinline__ void store_codes(const NormParams &p, size_t r, bool in, int t, int n, uint32_t *amax, const Pairs (&y)[kSets]) {
+  const int blocks = (p.hidden + kScaleBlock - 1) / kScaleBlock;
+  uint8_t *codes = p.codes + r * p.ld_codes;
+  float *scales = p.scales + r * blocks;
+  if constexpr (VEC) {
+    uint32_t m[kSets];
+#pragma unroll
+    for (int v = 0; v < kSets; ++v) m[v] = largest(flat(y[v]));
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+      for (int v = 0; v < kSets; ++v) m[v] = max(m[v], __shfl_xor_sync(0xffffffffu, m[v], o));
+#pragma unroll
+    for (int v = 0; v < kSets; ++v) {
+      const int col = 8 * (v * n + t);
+      if (!in || col >= p.hidden) continue;
+      const float s = block_scale(m[v], p.e5m2, p.pow2);
+      const Divisor d = divisor(s);
+      *reinterpret_cast<uint2 *>(codes + col) = make_uint2(codes4(flat(y[v]), d, p.e5m2), codes4(flat(y[v]) + 4, d, p.e5m2));
+      if (t % 16 == 0) scales[col / kScaleBlock] = s;
+    }
+  } else {
+    auto meet = [&] {  // the group's threads
+      if (n == 32) __syncwarp();
+      else asm volatile("bar.sync %0, %1;" ::"r"(1 + threadIdx.x / n), "r"(n) : "memory");
+    };
+#pragma unroll
+    for (int v = 0; v < kSets; ++v)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(flat(y[v])[e]) & 0x7FFFFFFFu);
+        const int col = (8 * v + e) * n + (t & ~31);
+        if (t % 32 == 0 && col < p.hidden) atomicMax(&amax[col / kScaleBlock], m);
+      }
+    meet();
+    if (in) {
+#pragma unroll
+      for (int v = 0; v < kSets; ++v)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int col = (8 * v + e) * n + t;
+          if (col >= p.hidden) continue;
+          const float s = block_scale(amax[col / kScaleBlock], p.e5m2, p.pow2);
+          codes[col] = (uint8_t)codes2(flat(y[v])[e], 0.f, divisor(s), p.e5m2);
+          if (col % kScaleBlock == 0) scales[col / kScaleBlock] = s;
+        }
+    }
+    meet();
+    for (int b = t; b < blocks; b += n) amax[b] = 0u;
+    meet();
+  }
+}
+
+// OUT8: y goes out as FP8 codes and scales.
+template <typename TS, typename TB, bool VEC, bool OUT8>
 __global__ void __launch_bounds__(512, VEC ? 1 : 2) block_norm_kernel(const __grid_constant__ NormParams p, int n) {
   __shared__ float buf[2 * 16];
+  __shared__ uint32_t amax[OUT8 && !VEC ? kNormHiddenMax / kScaleBlock : 1];
+  if constexpr (OUT8 && !VEC) {
+    for (int i = threadIdx.x; i < (int)(sizeof amax / sizeof *amax); i += blockDim.x) amax[i] = 0u;
+    __syncthreads();
+  }
   const int t = threadIdx.x & (n - 1), group = threadIdx.x / n, groups = blockDim.x / n;
   const float inv = 1.f / (float)p.hidden;
   int turn = 0;
@@ -190,8 +255,11 @@ __global__ void __launch_bounds__(512, VEC ? 1 : 2) block_norm_kernel(const __gr
 #pragma unroll
       for (int v = 0; v < kSets; ++v) {
         const Pairs w = load_set<float, VEC>(p.w_next, v, t, n, p.hidden);
-        if (in) store_set<TB, VEC>(static_cast<TB *>(p.y) + r * p.ld_y, v, t, n, p.hidden, mul(w, mul(s[v], rs)));
+        if constexpr (OUT8) s[v] = mul(w, mul(s[v], rs));
+        else if (in) store_set<TB, VEC>(static_cast<TB *>(p.y) + r * p.ld_y, v, t, n, p.hidden, mul(w, mul(s[v], rs)));
       }
+      // a group's blocks: of all groups together at most kNormHiddenMax / kScaleBlock
+      if constexpr (OUT8) store_codes<VEC>(p, r, in, t, n, amax + group * (n * 8 * kSets / kScaleBlock), s);
     }
   }
 }
@@ -628,7 +696,8 @@ bool all_wide(const NormParams &p) {
          wide(p.d_out, p.ld_d_out, p.stream_type) && wide(p.d_y, p.ld_d_y, p.block_type) &&
          wide(p.d_state, p.ld_d_state, p.stream_type) && wide(p.d_f, p.ld_d_f, p.block_type) &&
          (p.gate_kind != kGateVector || (wide(p.gate, p.hidden, p.gate_type) && wide(p.d_gate, p.hidden, p.gate_type))) &&
-         wide(p.w_post, 0, kF32) && wide(p.w_next, 0, kF32) && wide(p.part, 0, kF32);
+         wide(p.w_post, 0, kF32) && wide(p.w_next, 0, kF32) && wide(p.part, 0, kF32) &&
+         reinterpret_cast<uintptr_t>(p.codes) % 8 == 0 && p.ld_codes % 8 == 0;
 }
 
 template <typename TS, typename TB>
@@ -636,8 +705,10 @@ cudaError_t forward_typed(const NormParams &p, int num_sms, cudaStream_t st) {
   const int n = group_threads(p.hidden), threads = n < 256 ? 256 : n, groups = threads / n;
   const int blocks = (p.rows + groups - 1) / groups, most = num_sms * (1024 / threads);
   const int grid = blocks < most ? blocks : most;
-  return launch_pdl(all_wide(p) ? block_norm_kernel<TS, TB, true> : block_norm_kernel<TS, TB, false>, dim3(grid),
-                    dim3(threads), 0, st, p, n);
+  const bool vec = all_wide(p);
+  auto kernel = p.codes ? (vec ? block_norm_kernel<TS, TB, true, true> : block_norm_kernel<TS, TB, false, true>)
+                        : (vec ? block_norm_kernel<TS, TB, true, false> : block_norm_kernel<TS, TB, false, false>);
+  return launch_pdl(kernel, dim3(grid), dim3(threads), 0, st, p, n);
 }
 
 // The ring takes up to three rows of every group.  The weights go beside it unless that leaves less than

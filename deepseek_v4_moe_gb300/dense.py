@@ -76,6 +76,23 @@ def block_norm(state: torch.Tensor, f: Optional[torch.Tensor] = None, *, norm_f:
     return (_n or _native()).block_norm(state, f, norm_f, gate, residual_scale, norm_next, eps, block_dtype, out, y)
 
 
+def block_norm_fp8(state: torch.Tensor, f: Optional[torch.Tensor] = None, *, norm_next: torch.Tensor,
+                   norm_f: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                   residual_scale: float = 1.0, eps: float = 1e-6, pow2_scales: bool = False,
+                   dtype: torch.dtype = torch.float8_e4m3fn, out: Optional[torch.Tensor] = None,
+                   stream: Optional[torch.cuda.Stream] = None):
+    """:func:`block_norm` whose y is an operand of :func:`fp8_matmul`: y's float32 values as codes and scales, as
+    :func:`fp8_quantise` makes them of rows (``block_rows`` 1), without a rounding to the block's type between.
+
+    Returns (out, codes [rows, hidden] of ``dtype``, float32 scales [rows, ceil(hidden / 128)]); out is ``state``
+    itself without ``f``.
+    """
+    if stream is not None:
+        with _on(state, stream):
+            return (_n or _native()).block_norm_fp8(state, f, norm_f, gate, residual_scale, norm_next, eps, pow2_scales, dtype, out)
+    return (_n or _native()).block_norm_fp8(state, f, norm_f, gate, residual_scale, norm_next, eps, pow2_scales, dtype, out)
+
+
 def block_norm_backward(out: torch.Tensor, f: Optional[torch.Tensor] = None, *,
                         norm_f: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
                         residual_scale: float = 1.0, norm_next: Optional[torch.Tensor] = None, eps: float = 1e-6,
@@ -124,6 +141,20 @@ def gated_ffn_backward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor
                                                         _activation(activation), need_x, need_weights)
     return (_n or _native()).gated_ffn_backward(x, w_gate, w_up, w_down, saved[0], saved[1], d_y,
                                                 _activation(activation), need_x, need_weights)
+
+
+def gated_quantise(gate: torch.Tensor, up: torch.Tensor, activation: str = "silu", pow2_scales: bool = False,
+                   dtype: torch.dtype = torch.float8_e4m3fn, stream: Optional[torch.cuda.Stream] = None):
+    """The gated block's product as an operand of its second FP8 product: act(gate) * up, formed in float32, as codes
+    and scales of rows (see :func:`fp8_quantise`, ``block_rows`` 1).
+
+    ``gate``, ``up`` [rows, inter] bfloat16 or float16, also as column ranges of one tensor.  ``activation``: "silu"
+    or "gelu" (tanh form).  Returns (codes [rows, inter] of ``dtype``, float32 scales [rows, ceil(inter / 128)]).
+    """
+    if stream is not None:
+        with _on(gate, stream):
+            return (_n or _native()).gated_quantise(gate, up, _activation(activation), pow2_scales, dtype)
+    return (_n or _native()).gated_quantise(gate, up, _activation(activation), pow2_scales, dtype)
 
 
 def fp8_quantise(x: torch.Tensor, block_rows: int = 1, pow2_scales: bool = False,

@@ -437,6 +437,31 @@ typedef struct moe_ffn_fp8_quantise_args {
 /* The codes of moe_ffn_fp8_matmul. */
 int moe_ffn_fp8_quantise(const moe_ffn_fp8_quantise_args *a, void *stream);
 
+/* Where block_norm_fp8 and gated_quantise write codes and scales: as fp8_quantise makes them with block_rows 1. */
+typedef struct moe_ffn_fp8_out {
+  int32_t code_type, pow2;       /* MOE_FFN_E4M3 or MOE_FFN_E5M2 */
+  void *codes; int64_t ld_codes; /* [rows, columns] */
+  float *scales;                 /* [rows, ceil(columns / 128)], contiguous */
+} moe_ffn_fp8_out;
+
+/* block_norm with y as an operand of the FP8 product: the f32 values out * rsqrt(mean(out^2) + eps) * norm_next,
+ * quantised without being rounded to block_type first.  norm_next is given and y NULL; block_type is f's type (any
+ * with f NULL, which writes no out).  The codes of moe_ffn_block_norm. */
+int moe_ffn_block_norm_fp8(const moe_ffn_block_norm_args *a, const moe_ffn_fp8_out *o, void *stream);
+
+/* The gated block's product as an operand of its second FP8 product: act(gate) * up in f32, quantised.
+ * gate and up may be column ranges of one tensor, as one product of both projections leaves them. */
+typedef struct moe_ffn_gated_quantise_args {
+  int32_t rows, columns;         /* columns at most 2^20, rows at most 2^24 */
+  int32_t type;                  /* of gate and up: MOE_FFN_BF16 or _F16 */
+  int32_t activation;
+  const void *gate; int64_t ld_gate;  /* [rows, columns] */
+  const void *up; int64_t ld_up;
+} moe_ffn_gated_quantise_args;
+
+/* The codes of moe_ffn_fp8_matmul. */
+int moe_ffn_gated_quantise(const moe_ffn_gated_quantise_args *a, const moe_ffn_fp8_out *o, void *stream);
+
 /* Device status bits (MOE_FFN_DEV_TIMEOUT) that the dense sublayer's kernels set on the current device
  * since the previous call, after waiting for `stream` (which must not be under capture); then cleared.
  * Each set of bits is reported to one caller.  Or a negative code. */
