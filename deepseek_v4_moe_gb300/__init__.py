@@ -16,8 +16,13 @@ The dense feed-forward sublayer on a plain residual stream needs no handle (``de
 ``block_norm`` (the norms around a block with its gate and residual scale) and ``gated_ffn`` (the
 gated feed-forward block), each with its gradients, ``fp8_matmul`` (the product of FP8 operands with
 scales for blocks of 128) and ``fp8_quantise``, which makes its operands; ``dense_status`` reads the
-device status bits.
+device status bits.  ``block_norm_fp8`` and ``gated_quantise`` write such operands themselves.
+
+For serving a few tokens there are products with 4-bit weights (``int4_matmul``, with ``int4_quantise`` and
+``int4_widen``; ``Int4``) and a whole mixture-of-experts layer on a plain residual stream (``routed_ffn``), with
+experts in 16 or 4 bits (``few``).
 """
 from .api import MoeFFN, MoeFFNError, config_from  # noqa: F401
 from .dense import (block_norm, block_norm_backward, block_norm_fp8, dense_status, fp8_matmul,  # noqa: F401
                     fp8_quantise, gated_ffn, gated_ffn_backward, gated_quantise)
+from .few import Int4, int4_matmul, int4_quantise, int4_widen, routed_ffn  # noqa: F401

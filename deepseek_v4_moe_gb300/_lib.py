@@ -97,6 +97,31 @@ class MoeFfnGatedQuantiseArgs(ctypes.Structure):
                 ("ld_gate", c_i64), ("up", c_vp), ("ld_up", c_i64)]
 
 
+class MoeFfnInt4WeightsArgs(ctypes.Structure):
+    _fields_ = [("n", c_i32), ("k", c_i32), ("group", c_i32), ("scale_type", c_i32), ("codes", c_vp), ("scales", c_vp),
+                ("zeros", c_vp)]
+
+
+class MoeFfnInt4MatmulArgs(ctypes.Structure):
+    _fields_ = [("rows", c_i32), ("n", c_i32), ("k", c_i32), ("type", c_i32), ("group", c_i32), ("x", c_vp),
+                ("ld_x", c_i64), ("codes", c_vp), ("scales", c_vp), ("zeros", c_vp), ("out", c_vp), ("ld_out", c_i64)]
+
+
+SCORES = {"sigmoid": 0, "softmax": 1}
+
+
+class MoeFfnMatrices(ctypes.Structure):
+    _fields_ = [("w", c_vp), ("scales", c_vp), ("zeros", c_vp)]
+
+
+class MoeFfnRoutedArgs(ctypes.Structure):
+    _fields_ = [(n, c_i32) for n in ("rows", "hidden", "inter", "experts", "top_k", "shared", "type", "router_type", "bits",
+                                     "group", "score", "normalise", "activation")] + [
+        ("route_scale", c_f32), ("x", c_vp), ("ld_x", c_i64), ("router", c_vp), ("bias", c_vp),
+        *[(n, MoeFfnMatrices) for n in ("gate", "up", "down", "shared_gate", "shared_up", "shared_down")],
+        ("y", c_vp), ("ld_y", c_i64), ("indices", c_vp), ("weights", c_vp), ("workspace", c_vp), ("workspace_bytes", c_sz)]
+
+
 # return codes and device status bits (include/moe_ffn.h)
 OK, ERR_NULL_PTR, ERR_BAD_CONFIG, ERR_LAYER_RANGE, ERR_ROWS_ZERO, ERR_ROWS_RANGE = 0, -1, -2, -3, -4, -5
 ERR_NO_ROUTING_SOURCE, ERR_ALIAS, ERR_CUDA, ERR_NO_MEMORY, ERR_UNSUPPORTED, ERR_ALIGNMENT, ERR_NO_WEIGHTS = (
@@ -189,6 +214,17 @@ def load(build: bool = True):
     lib.moe_ffn_block_norm_fp8.restype = ctypes.c_int
     lib.moe_ffn_gated_quantise.argtypes = [ctypes.POINTER(MoeFfnGatedQuantiseArgs), out8, vp]
     lib.moe_ffn_gated_quantise.restype = ctypes.c_int
+    int4 = ctypes.POINTER(MoeFfnInt4WeightsArgs)
+    lib.moe_ffn_int4_quantise.argtypes = [int4, vp, i32, c_i64, vp]
+    lib.moe_ffn_int4_quantise.restype = ctypes.c_int
+    lib.moe_ffn_int4_widen.argtypes = [int4, vp, c_i64, vp]
+    lib.moe_ffn_int4_widen.restype = ctypes.c_int
+    lib.moe_ffn_int4_matmul.argtypes = [ctypes.POINTER(MoeFfnInt4MatmulArgs), vp]
+    lib.moe_ffn_int4_matmul.restype = ctypes.c_int
+    lib.moe_ffn_routed_forward.argtypes = [ctypes.POINTER(MoeFfnRoutedArgs), vp]
+    lib.moe_ffn_routed_forward.restype = ctypes.c_int
+    lib.moe_ffn_routed_workspace.argtypes = [ctypes.POINTER(MoeFfnRoutedArgs)]
+    lib.moe_ffn_routed_workspace.restype = c_i64
     lib.moe_ffn_last_error.argtypes = [vp]
     lib.moe_ffn_last_error.restype = ctypes.c_char_p
     lib.moe_ffn_destroy.argtypes = [vp]

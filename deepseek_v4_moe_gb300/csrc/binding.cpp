@@ -1,4 +1,4 @@
-// Python binding of the dense feed-forward sublayer's C entry points (include/moe_ffn.h): checks of
+// Python binding of the C entry points without a handle (include/moe_ffn.h): checks of
 // the tensors, outputs and workspaces from PyTorch's allocator, the current stream, and the call.  The
 // checks take a few tenths of a microsecond here; through ctypes they took longer than a token's kernels.
 #include <ATen/ATen.h>
@@ -7,11 +7,13 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/python_variable.h>
 #include <torch/csrc/utils/pybind.h>
 
 #include <optional>
 #include <sstream>
 #include <string>
+#include <vector>
 
 #include "moe_ffn.h"
 
@@ -437,6 +439,212 @@ Tensor fp8_matmul(const Tensor &a, const Tensor &a_scale, const Tensor &b, const
   return *out;
 }
 
+// ---- 4-bit weights and the routed layer ----
+
+// Weights as the package's Int4 (codes, scales, zeros or None, group), or a plain tensor of values.
+struct Weights {
+  Tensor w, scales;
+  Maybe zeros;
+  int64_t group = 0;  // 0: values
+  int64_t dim() const { return w.dim(); }
+  int64_t n() const { return w.size(w.dim() - 2); }
+  int64_t k() const { return w.size(w.dim() - 1) * (group ? 2 : 1); }
+};
+Weights weights_of(const char *name, py::handle o) {
+  Weights r;
+  if (THPVariable_Check(o.ptr())) {
+    r.w = THPVariable_Unpack(o.ptr());
+  } else if (PyTuple_Check(o.ptr()) && PyTuple_GET_SIZE(o.ptr()) == 4) {
+    PyObject *item[4];
+    for (int i = 0; i < 4; ++i) item[i] = PyTuple_GET_ITEM(o.ptr(), i);
+    if (!THPVariable_Check(item[0]) || !THPVariable_Check(item[1]) || (item[2] != Py_None && !THPVariable_Check(item[2])))
+      throw py::type_error(std::string(name) + " must hold tensors: codes, scales and zeros (or None)");
+    r.w = THPVariable_Unpack(item[0]);
+    r.scales = THPVariable_Unpack(item[1]);
+    if (item[2] != Py_None) r.zeros = THPVariable_Unpack(item[2]);
+    r.group = py::cast<int64_t>(py::handle(item[3]));
+    if (r.group != 32 && r.group != 64 && r.group != 128) refuse(std::string(name) + " must have groups of 32, 64 or 128");
+  } else {
+    throw py::type_error(std::string(name) + " must be a torch.Tensor or an Int4");
+  }
+  if (r.w.dim() < 2) refuse(std::string(name) + " must be [..., rows, columns], got " + text(r.w.sizes()));
+  return r;
+}
+// Checks 4-bit weights of any leading sizes; type: of the scales.
+void check_codes(const Where &w, const char *name, const Weights &m, ScalarType type) {
+  const std::string s = name;
+  if (!m.group) refuse(s + " must be an Int4");
+  whole(w, (s + ".codes").c_str(), m.w, m.w.sizes(), ScalarType::Byte);
+  auto groups = m.w.sizes().vec();
+  groups.back() = (m.k() + m.group - 1) / m.group;
+  whole(w, (s + ".scales").c_str(), m.scales, groups, type);
+  if (m.zeros) whole(w, (s + ".zeros").c_str(), *m.zeros, groups, ScalarType::Byte);
+}
+uint8_t *zeros_of(const Weights &m) { return m.zeros ? static_cast<uint8_t *>(m.zeros->data_ptr()) : nullptr; }
+
+moe_ffn_int4_weights_args int4_args(const Weights &m) {
+  moe_ffn_int4_weights_args a = {};
+  a.n = size32("the number of rows", m.w.numel() / (m.w.size(-1) ? m.w.size(-1) : 1));
+  a.k = size32("the number of columns", m.k());
+  a.group = (int32_t)m.group;
+  a.scale_type = type_code(m.scales.scalar_type());
+  a.codes = static_cast<uint8_t *>(m.w.data_ptr());
+  a.scales = m.scales.data_ptr();
+  a.zeros = zeros_of(m);
+  return a;
+}
+
+py::tuple int4_quantise(const Tensor &w, int64_t group, bool zero_points, py::object scale_dtype) {
+  const Where at("w", w);
+  const ScalarType t = w.scalar_type();
+  const ScalarType st = scale_dtype.is_none() ? (t == ScalarType::Float ? ScalarType::BFloat16 : t) : dtype_of(scale_dtype);
+  if (type_code(t) < 0 || (st != ScalarType::BFloat16 && st != ScalarType::Half))
+    refuse("w must be float32, bfloat16 or float16, scale_dtype bfloat16 or float16");
+  if (group != 32 && group != 64 && group != 128) refuse("group must be 32, 64 or 128");
+  if (w.dim() < 2) refuse("w must be [..., rows, columns], got " + text(w.sizes()));
+  const int64_t k = w.size(-1);
+  if (w.dim() > 2 && !w.is_contiguous()) refuse("w of more than two dimensions must be contiguous");
+  const int64_t ld = w.dim() == 2 ? matrix(at, "w", w, w.sizes(), t) : k;
+  if (k % 32) refuse("w must have a multiple of 32 columns");
+  auto shape = w.sizes().vec();
+  Weights m;
+  m.group = group;
+  shape.back() = k / 2;
+  m.w = fresh(at, shape, ScalarType::Byte);
+  shape.back() = (k + group - 1) / group;
+  m.scales = fresh(at, shape, st);
+  if (zero_points) m.zeros = fresh(at, shape, ScalarType::Byte);
+  const moe_ffn_int4_weights_args a = int4_args(m);
+  check(moe_ffn_int4_quantise(&a, w.data_ptr(), type_code(t), ld, at.stream));
+  return py::make_tuple(m.w, m.scales, m.zeros ? py::cast(*m.zeros) : py::none(), group);
+}
+
+Tensor int4_widen(py::object o, Maybe out) {
+  const Weights m = weights_of("w", o);
+  const Where w("w.codes", m.w);
+  if (!m.group) refuse("w must be an Int4");
+  const ScalarType t = m.scales.scalar_type();
+  if (t != ScalarType::BFloat16 && t != ScalarType::Half) refuse("w.scales must be bfloat16 or float16");
+  check_codes(w, "w", m, t);
+  auto shape = m.w.sizes().vec();
+  shape.back() = m.k();
+  const Maybe given = out;
+  if (!out) out = fresh(w, shape, t);
+  int64_t ld = m.k();
+  if (shape.size() == 2) ld = matrix(w, "out", *out, shape, t);
+  else whole(w, "out", *out, shape, t);
+  const moe_ffn_int4_weights_args a = int4_args(m);
+  check(moe_ffn_int4_widen(&a, out->data_ptr(), ld, w.stream));
+  written(given);
+  return *out;
+}
+
+Tensor int4_matmul(const Tensor &x, py::object o, Maybe out) {
+  const Where w("x", x);
+  const ScalarType t = x.scalar_type();
+  if (t != ScalarType::BFloat16 && t != ScalarType::Half) refuse("x must be bfloat16 or float16");
+  two("x", x);
+  const Weights m = weights_of("w", o);
+  two("w.codes", m.w);
+  check_codes(w, "w", m, t);
+  const int64_t rows = x.size(0), n = m.n(), k = m.k();
+  moe_ffn_int4_matmul_args a = {};
+  a.rows = size32("rows", rows);
+  a.n = size32("n", n);
+  a.k = size32("k", k);
+  a.type = type_code(t);
+  a.group = (int32_t)m.group;
+  a.ld_x = matrix(w, "x", x, {rows, k}, t);
+  a.x = x.data_ptr();
+  a.codes = static_cast<uint8_t *>(m.w.data_ptr());
+  a.scales = m.scales.data_ptr();
+  a.zeros = zeros_of(m);
+  const Maybe given = out;
+  if (!out) out = fresh(w, {rows, n}, t);
+  a.ld_out = matrix(w, "out", *out, {rows, n}, t);
+  a.out = out->data_ptr();
+  check(moe_ffn_int4_matmul(&a, w.stream));
+  written(given);
+  return *out;
+}
+
+py::tuple routed_ffn(const Tensor &x, const Tensor &router, py::object w_gate, py::object w_up, py::object w_down, int64_t top_k,
+                     const Maybe &bias, int score, bool normalise, double route_scale, py::object shared, int activation, Maybe out) {
+  const Where w("x", x);
+  const ScalarType t = x.scalar_type();
+  if (t != ScalarType::BFloat16 && t != ScalarType::Half) refuse("x must be bfloat16 or float16");
+  two("x", x);
+  two("w_router", router);
+  const int64_t rows = x.size(0), hidden = x.size(1), experts = router.size(0);
+  const ScalarType tr = router.scalar_type();
+  if (tr != t && tr != ScalarType::Float) refuse("w_router must be float32 or of x's type");
+  Weights m[6];
+  const char *names[] = {"w_gate", "w_up", "w_down", "shared[0]", "shared[1]", "shared[2]"};
+  m[0] = weights_of(names[0], w_gate);
+  m[1] = weights_of(names[1], w_up);
+  m[2] = weights_of(names[2], w_down);
+  int64_t n_shared = 0;
+  if (!shared.is_none()) {
+    if (!PyTuple_Check(shared.ptr()) || PyTuple_GET_SIZE(shared.ptr()) != 3) refuse("shared must be three weights: gate, up and down");
+    for (int i = 0; i < 3; ++i) m[3 + i] = weights_of(names[3 + i], PyTuple_GET_ITEM(shared.ptr(), i));
+    n_shared = m[3].dim() == 2 ? 1 : m[3].w.size(0);
+    if (n_shared < 1) refuse("shared must hold at least one expert");
+  }
+  const int64_t inter = m[0].n(), group = m[0].group;
+  moe_ffn_routed_args a = {};
+  moe_ffn_matrices *to[] = {&a.gate, &a.up, &a.down, &a.shared_gate, &a.shared_up, &a.shared_down};
+  for (int i = 0; i < (n_shared ? 6 : 3); ++i) {
+    const int64_t count = i < 3 ? experts : n_shared, n = i % 3 == 2 ? hidden : inter, k = i % 3 == 2 ? inter : hidden;
+    if (m[i].group != group) refuse(std::string(names[i]) + " must be of w_gate's kind (values, or 4 bits with its group)");
+    std::vector<int64_t> shape = {count, n, group ? k / 2 : k};
+    if (i >= 3 && m[3].dim() == 2) shape.erase(shape.begin());
+    if (group) {
+      if (k % 32) refuse("hidden and inter must be multiples of 32 with 4-bit weights");
+      if (m[i].w.sizes() != at::IntArrayRef(shape))
+        refuse(std::string(names[i]) + ".codes must be of shape " + text(shape) + ", got " + text(m[i].w.sizes()));
+      check_codes(w, names[i], m[i], t);
+      to[i]->scales = m[i].scales.data_ptr();
+      to[i]->zeros = zeros_of(m[i]);
+    } else {
+      whole(w, names[i], m[i].w, shape, t);
+    }
+    to[i]->w = m[i].w.data_ptr();
+  }
+  a.rows = size32("rows", rows);
+  a.hidden = size32("hidden", hidden);
+  a.inter = size32("inter", inter);
+  a.experts = size32("experts", experts);
+  a.top_k = size32("top_k", top_k);
+  a.shared = size32("shared", n_shared);
+  a.type = type_code(t);
+  a.router_type = type_code(tr);
+  a.bits = group ? 4 : 16;
+  a.group = (int32_t)group;
+  a.score = score;
+  a.normalise = normalise;
+  a.activation = activation;
+  a.route_scale = (float)route_scale;
+  a.ld_x = matrix(w, "x", x, x.sizes(), t);
+  a.x = x.data_ptr();
+  a.router = whole(w, "w_router", router, {experts, hidden}, tr);
+  if (bias) a.bias = static_cast<float *>(whole(w, "bias", *bias, {experts}, ScalarType::Float));
+  const int64_t need = moe_ffn_routed_workspace(&a);
+  check(need);
+  const Maybe given = out;
+  if (!out) out = fresh(w, {rows, hidden}, t);
+  a.ld_y = matrix(w, "out", *out, {rows, hidden}, t);
+  a.y = out->data_ptr();
+  const Tensor indices = fresh(w, {rows, top_k}, ScalarType::Int), chosen = fresh(w, {rows, top_k}, ScalarType::Float);
+  a.indices = static_cast<int32_t *>(indices.data_ptr());
+  a.weights = static_cast<float *>(chosen.data_ptr());
+  const Tensor ws = fresh(w, {need}, ScalarType::Byte);
+  a.workspace = ws.data_ptr();
+  a.workspace_bytes = (size_t)need;
+  check(moe_ffn_routed_forward(&a, w.stream));
+  written(given);
+  return py::make_tuple(*out, indices, chosen);
+}
+
 }  // namespace
 
 // wrap_pybind_function: errors of PyTorch's own (a failed allocation) keep their Python types
@@ -449,5 +657,9 @@ PYBIND11_MODULE(_native, m) {
   m.def("gated_ffn", torch::wrap_pybind_function(&gated_ffn));
   m.def("gated_ffn_backward", torch::wrap_pybind_function(&gated_ffn_backward));
   m.def("fp8_quantise", torch::wrap_pybind_function(&fp8_quantise));
+  m.def("int4_quantise", torch::wrap_pybind_function(&int4_quantise));
+  m.def("int4_widen", torch::wrap_pybind_function(&int4_widen));
+  m.def("int4_matmul", torch::wrap_pybind_function(&int4_matmul));
+  m.def("routed_ffn", torch::wrap_pybind_function(&routed_ffn));
   m.def("fp8_matmul", torch::wrap_pybind_function(&fp8_matmul));
 }

@@ -1,0 +1,268 @@
+// C entry points of the products with 4-bit weights and of the routed layer without a handle: argument checks and
+// launches (include/moe_ffn.h documents each).
+#include "few.h"
+
+#include "entry.h"
+
+namespace {
+
+using namespace moe::entry;
+
+constexpr int kCodesMax = 1 << 20, kCodeRowsMax = 1 << 24;
+
+int check_group(const char *who, int group) {
+  if (group != 32 && group != 64 && group != 128) return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: group must be 32, 64 or 128", who);
+  return MOE_FFN_OK;
+}
+bool type16(int t) { return t == MOE_FFN_BF16 || t == MOE_FFN_F16; }
+
+int check_int4(const char *who, int64_t n, int64_t k, int group, const void *codes, const void *scales, const void *zeros) {
+  if (n < 1 || n > kCodeRowsMax || k < 32 || k % 32 || k > kCodesMax)
+    return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: n must be in 1..2^24, k a multiple of 32 in 32..2^20", who);
+  const int rc = check_group(who, group);
+  if (rc) return rc;
+  if (!codes || !scales) return fail(MOE_FFN_ERR_NULL_PTR, "%s: codes or scales is NULL", who);
+  if (!aligned(codes, 16) || !aligned(scales, 16) || !aligned(zeros, 16))
+    return fail(MOE_FFN_ERR_ALIGNMENT, "%s: codes, scales and zeros must be 16-byte aligned", who);
+  return MOE_FFN_OK;
+}
+
+int log2_of(int group) { return group == 32 ? 5 : group == 64 ? 6 : 7; }
+
+moe::FewMatrix matrix(const void *w, const void *scales, const uint8_t *zeros, int64_t n, int64_t k, int group) {
+  const int groups = (int)((k + group - 1) / group);
+  return moe::FewMatrix{w, static_cast<const uint16_t *>(scales), zeros, (int)n, (int)k, groups, log2_of(group)};
+}
+
+// rows of x or of a result in 16-byte pieces
+int check_rows16(const char *who, const char *name, const void *p, int64_t ld, int64_t cols) {
+  if (!p) return fail(MOE_FFN_ERR_NULL_PTR, "%s: %s is NULL", who, name);
+  if (ld < cols || ld % 8 || ld > kLdMax)
+    return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: the row stride of %s must be a multiple of 8, at least %lld", who, name, (long long)cols);
+  if (!aligned(p, 16)) return fail(MOE_FFN_ERR_ALIGNMENT, "%s: %s is not 16-byte aligned", who, name);
+  return MOE_FFN_OK;
+}
+// rows that are written value by value
+int check_rows2(const char *who, const char *name, const void *p, int64_t ld, int64_t cols) {
+  if (!p) return fail(MOE_FFN_ERR_NULL_PTR, "%s: %s is NULL", who, name);
+  if (ld < cols || ld > kLdMax) return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: the row stride of %s is below %lld", who, name, (long long)cols);
+  if (!aligned(p, 2)) return fail(MOE_FFN_ERR_ALIGNMENT, "%s: %s is misaligned", who, name);
+  return MOE_FFN_OK;
+}
+
+int check_weights(const char *who, const moe_ffn_int4_weights_args *a) {
+  if (!a) return fail(MOE_FFN_ERR_NULL_PTR, "%s: args is NULL", who);
+  int rc = check_int4(who, a->n, a->k, a->group, a->codes, a->scales, a->zeros);
+  if (rc) return rc;
+  if (!type16(a->scale_type)) return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: scale_type must be bf16 or f16", who);
+  return MOE_FFN_OK;
+}
+
+moe::Int4WeightParams weight_params(const moe_ffn_int4_weights_args *a) {
+  moe::Int4WeightParams p = {};
+  p.n = a->n;
+  p.k = a->k;
+  p.group = a->group;
+  p.codes = a->codes;
+  p.scales = a->scales;
+  p.zeros = a->zeros;
+  p.f16 = a->scale_type == MOE_FFN_F16;
+  return p;
+}
+
+int weight_spans(const moe_ffn_int4_weights_args *a, Span *s) {
+  const int64_t groups = (a->k + a->group - 1) / a->group;
+  s[0] = span("codes", a->codes, a->n, a->k / 2, a->k / 2, 1);
+  s[1] = span("scales", a->scales, a->n, groups, groups, 2);
+  s[2] = span("zeros", a->zeros, a->n, groups, groups, 1);
+  return 3;
+}
+
+}  // namespace
+
+extern "C" int moe_ffn_int4_quantise(const moe_ffn_int4_weights_args *a, const void *w, int32_t type, int64_t ld_w, void *stream) {
+  const char *who = "int4_quantise";
+  int rc = check_weights(who, a);
+  if (rc) return rc;
+  if (!is_type(type)) return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: unknown type", who);
+  if (!w) return fail(MOE_FFN_ERR_NULL_PTR, "%s: w is NULL", who);
+  if (ld_w < a->k || ld_w % 8 || ld_w > kLdMax)
+    return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: the row stride of w must be a multiple of 8, at least k", who);
+  const int bytes = type_bytes(type);
+  if (!aligned(w, 8 * bytes)) return fail(MOE_FFN_ERR_ALIGNMENT, "%s: w is not aligned to eight values", who);
+  Span outs[3];
+  const Span ins[] = {span("w", w, a->n, a->k, ld_w, bytes)};
+  if ((rc = check_overlaps(who, outs, weight_spans(a, outs), ins, 1, -1, -1))) return rc;
+  const int sms = current_sms();
+  if (sms < 0) return sms;
+  if ((rc = pending(who))) return rc;
+  moe::Int4WeightParams p = weight_params(a);
+  p.type = type;
+  p.w = w;
+  p.ld_w = ld_w;
+  return launched(who, moe::launch_int4_quantise(p, sms, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int moe_ffn_int4_widen(const moe_ffn_int4_weights_args *a, void *out, int64_t ld_out, void *stream) {
+  const char *who = "int4_widen";
+  int rc = check_weights(who, a);
+  if (rc) return rc;
+  if ((rc = check_rows16(who, "out", out, ld_out, a->k))) return rc;
+  Span ins[3];
+  const Span outs[] = {span("out", out, a->n, a->k, ld_out, 2)};
+  if ((rc = check_overlaps(who, outs, 1, ins, weight_spans(a, ins), -1, -1))) return rc;
+  const int sms = current_sms();
+  if (sms < 0) return sms;
+  if ((rc = pending(who))) return rc;
+  moe::Int4WeightParams p = weight_params(a);
+  p.out = out;
+  p.ld_out = ld_out;
+  return launched(who, moe::launch_int4_widen(p, sms, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int moe_ffn_int4_matmul(const moe_ffn_int4_matmul_args *a, void *stream) {
+  const char *who = "int4_matmul";
+  if (!a) return fail(MOE_FFN_ERR_NULL_PTR, "%s: args is NULL", who);
+  if (a->rows == 0) return fail(MOE_FFN_ERR_ROWS_ZERO, "%s: rows must be at least 1", who);
+  if (a->rows < 0 || a->rows > (1 << 16)) return fail(MOE_FFN_ERR_ROWS_RANGE, "%s: rows must be at most 2^16", who);
+  if (!type16(a->type)) return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: type must be bf16 or f16", who);
+  int rc = check_int4(who, a->n, a->k, a->group, a->codes, a->scales, a->zeros);
+  if (rc) return rc;
+  const int64_t R = a->rows, N = a->n, K = a->k, G = (K + a->group - 1) / a->group;
+  if ((rc = check_rows16(who, "x", a->x, a->ld_x, K)) || (rc = check_rows2(who, "out", a->out, a->ld_out, N))) return rc;
+  const Span ins[] = {span("x", a->x, R, K, a->ld_x, 2), span("codes", a->codes, N, K / 2, K / 2, 1),
+                      span("scales", a->scales, N, G, G, 2), span("zeros", a->zeros, N, G, G, 1)};
+  const Span outs[] = {span("out", a->out, R, N, a->ld_out, 2)};
+  if ((rc = check_overlaps(who, outs, 1, ins, 4, -1, -1))) return rc;
+  const int sms = current_sms();
+  if (sms < 0) return sms;
+  if ((rc = pending(who))) return rc;
+  moe::Int4MatmulParams p = {};
+  p.w = matrix(a->codes, a->scales, a->zeros, N, K, a->group);
+  p.rows = a->rows;
+  p.x = a->x;
+  p.ld_x = a->ld_x;
+  p.out = a->out;
+  p.ld_out = a->ld_out;
+  return launched(who, moe::launch_int4_matmul(p, a->type == MOE_FFN_F16, sms, static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+
+int check_routed(const char *who, const moe_ffn_routed_args *a) {
+  if (!a) return fail(MOE_FFN_ERR_NULL_PTR, "%s: args is NULL", who);
+  if (a->rows == 0) return fail(MOE_FFN_ERR_ROWS_ZERO, "%s: rows must be at least 1", who);
+  if (a->rows < 0 || a->rows > moe::kRoutedRows)
+    return fail(MOE_FFN_ERR_ROWS_RANGE, "%s: rows must be at most %d", who, moe::kRoutedRows);
+  if (a->bits != 4 && a->bits != 16) return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: bits must be 4 or 16", who);
+  const int step = a->bits == 4 ? 32 : 8;
+  if (a->hidden < step || a->hidden % step || a->hidden > 65536 || a->inter < step || a->inter % step || a->inter > 65536)
+    return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: hidden and inter must be multiples of %d, at most 65536", who, step);
+  if (a->experts < 1 || a->experts > moe::kRoutedExperts || a->top_k < 1 || a->top_k > moe::kRoutedTopK || a->top_k > a->experts ||
+      a->shared < 0 || a->shared > moe::kRoutedShared)
+    return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: experts must be in 1..%d, top_k in 1..%d and at most experts, shared in 0..%d", who,
+                moe::kRoutedExperts, moe::kRoutedTopK, moe::kRoutedShared);
+  if (!type16(a->type) || (a->router_type != MOE_FFN_F32 && a->router_type != a->type))
+    return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: type must be bf16 or f16, router_type f32 or type", who);
+  if (a->score != MOE_FFN_SCORE_SIGMOID && a->score != MOE_FFN_SCORE_SOFTMAX)
+    return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: unknown score", who);
+  if (a->activation != MOE_FFN_ACT_SILU && a->activation != MOE_FFN_ACT_GELU)
+    return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: unknown activation", who);
+  return a->bits == 4 ? check_group(who, a->group) : MOE_FFN_OK;
+}
+
+int64_t logits_bytes(const moe_ffn_routed_args *a) { return ((int64_t)a->rows * a->experts * 4 + 255) / 256 * 256; }
+int64_t routed_workspace(const moe_ffn_routed_args *a) {
+  return logits_bytes(a) + (int64_t)a->rows * (a->top_k + a->shared) * a->inter * 2;
+}
+
+}  // namespace
+
+extern "C" int64_t moe_ffn_routed_workspace(const moe_ffn_routed_args *a) {
+  const int rc = check_routed("routed_workspace", a);
+  return rc ? rc : routed_workspace(a);
+}
+
+extern "C" int moe_ffn_routed_forward(const moe_ffn_routed_args *a, void *stream) {
+  const char *who = "routed_forward";
+  int rc = check_routed(who, a);
+  if (rc) return rc;
+  const int64_t R = a->rows, H = a->hidden, I = a->inter, E = a->experts, S = a->shared, K = a->top_k;
+  if ((rc = check_rows16(who, "x", a->x, a->ld_x, H)) || (rc = check_rows2(who, "y", a->y, a->ld_y, H)) ||
+      (rc = check_rows16(who, "workspace", a->workspace, 8, 8)))
+    return rc;
+  if (!a->router) return fail(MOE_FFN_ERR_NULL_PTR, "%s: router is NULL", who);
+  const int rb = type_bytes(a->router_type);
+  if (!aligned(a->router, 8 * rb) || !aligned(a->bias, 4) || !aligned(a->indices, 4) || !aligned(a->weights, 4))
+    return fail(MOE_FFN_ERR_ALIGNMENT, "%s: router must be aligned to eight values, bias, indices and weights to one", who);
+  const moe_ffn_matrices *all[] = {&a->gate, &a->up, &a->down, &a->shared_gate, &a->shared_up, &a->shared_down};
+  const char *names[] = {"gate", "up", "down", "shared_gate", "shared_up", "shared_down"};
+  Span ins[3 + 18];
+  int n_ins = 0;
+  ins[n_ins++] = span("x", a->x, R, H, a->ld_x, 2);
+  ins[n_ins++] = span("router", a->router, E, H, H, rb);
+  ins[n_ins++] = span("bias", a->bias, 1, E, E, 4);
+  moe::FewMatrix m[6] = {};
+  for (int i = 0; i < 6; ++i) {
+    const int64_t count = i < 3 ? E : S, n = i % 3 == 2 ? H : I, k = i % 3 == 2 ? I : H;
+    if (!count) {
+      if (all[i]->w) return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: %s is given without shared experts", who, names[i]);
+      continue;
+    }
+    if (a->bits == 4) {
+      if ((rc = check_int4(names[i], n, k, a->group, all[i]->w, all[i]->scales, all[i]->zeros))) return rc;
+      const int64_t G = (k + a->group - 1) / a->group;
+      m[i] = matrix(all[i]->w, all[i]->scales, all[i]->zeros, n, k, a->group);
+      ins[n_ins++] = span(names[i], all[i]->w, count * n, k / 2, k / 2, 1);
+      ins[n_ins++] = span(names[i], all[i]->scales, count * n, G, G, 2);
+      ins[n_ins++] = span(names[i], all[i]->zeros, count * n, G, G, 1);
+    } else {
+      if ((rc = check_rows16(who, names[i], all[i]->w, k, k))) return rc;
+      if (all[i]->scales || all[i]->zeros) return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: %s in 16 bits has no scales", who, names[i]);
+      m[i] = moe::FewMatrix{all[i]->w, nullptr, nullptr, (int)n, (int)k, 0, 0};
+      ins[n_ins++] = span(names[i], all[i]->w, count * n, k, k, 2);
+    }
+  }
+  // zero points are read, or not, by the expert's matrix for the shared one's too
+  for (int i = 0; i < 3; ++i)
+    if (S && (m[i].zeros != nullptr) != (m[i + 3].zeros != nullptr))
+      return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: %s and %s must both have zero points or neither", who, names[i], names[i + 3]);
+  const int64_t need = routed_workspace(a);
+  if (a->workspace_bytes < (size_t)need)
+    return fail(MOE_FFN_ERR_NO_MEMORY, "%s: workspace of %zu bytes, needs %lld", who, a->workspace_bytes, (long long)need);
+  const Span outs[] = {span("y", a->y, R, H, a->ld_y, 2), span("indices", a->indices, R, K, K, 4),
+                       span("weights", a->weights, R, K, K, 4), span("workspace", a->workspace, 1, need, 0, 1)};
+  if ((rc = check_overlaps(who, outs, 4, ins, n_ins, -1, -1))) return rc;
+  const int sms = current_sms();
+  if (sms < 0) return sms;
+  if ((rc = pending(who))) return rc;
+  moe::RoutedParams p = {};
+  p.rows = a->rows;
+  p.hidden = a->hidden;
+  p.inter = a->inter;
+  p.experts = a->experts;
+  p.top_k = a->top_k;
+  p.shared = a->shared;
+  p.softmax = a->score == MOE_FFN_SCORE_SOFTMAX;
+  p.normalise = a->normalise != 0;
+  p.act = a->activation;
+  p.router_f32 = a->router_type == MOE_FFN_F32;
+  p.scale = a->route_scale;
+  p.x = a->x;
+  p.ld_x = a->ld_x;
+  p.router = a->router;
+  p.bias = a->bias;
+  p.gate = m[0];
+  p.up = m[1];
+  p.down = m[2];
+  p.s_gate = m[3];
+  p.s_up = m[4];
+  p.s_down = m[5];
+  p.y = a->y;
+  p.ld_y = a->ld_y;
+  p.indices = a->indices;
+  p.weights = a->weights;
+  p.logits = static_cast<float *>(a->workspace);
+  p.h = reinterpret_cast<uint16_t *>(static_cast<char *>(a->workspace) + logits_bytes(a));
+  return launched(who, moe::launch_routed(p, a->type == MOE_FFN_F16, a->bits == 4, sms, static_cast<cudaStream_t>(stream)));
+}

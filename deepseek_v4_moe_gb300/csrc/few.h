@@ -1,0 +1,69 @@
+// Host-side launchers of the kernels for a few rows: products with 4-bit weights, and the routed layer without a handle.
+#pragma once
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "dense.h"
+
+namespace moe {
+
+// A matrix [n, k] of weights, or several of them one after another (experts).  16-bit: values of the call's type, no
+// scales.  4-bit: codes [n, k / 2] (the even column in the low half), scales [n, groups] of the call's type, zero points
+// [n, groups] or none (8).
+struct FewMatrix {
+  const void *w;
+  const uint16_t *scales;
+  const uint8_t *zeros;
+  int n, k, groups, group_shift;
+};
+
+struct Int4MatmulParams {
+  FewMatrix w;
+  int rows;
+  const void *x;
+  void *out;
+  long long ld_x, ld_out;
+};
+cudaError_t launch_int4_matmul(const Int4MatmulParams &p, bool f16, int num_sms, cudaStream_t st);
+
+struct Int4WeightParams {
+  int n, k, group, type;      // type: of w, or of the widened matrix
+  const void *w;
+  long long ld_w;
+  uint8_t *codes;
+  void *scales;
+  uint8_t *zeros;             // or none
+  int f16;                    // of the scales
+  void *out;                  // widen
+  long long ld_out;
+};
+cudaError_t launch_int4_quantise(const Int4WeightParams &p, int num_sms, cudaStream_t st);
+cudaError_t launch_int4_widen(const Int4WeightParams &p, int num_sms, cudaStream_t st);
+
+// ---- the routed layer ----
+
+constexpr int kRoutedRows = 32;     // tokens of a call: a bit each in a group's mask
+constexpr int kRoutedExperts = 512;
+constexpr int kRoutedTopK = 8;
+constexpr int kRoutedShared = 8;
+
+struct RoutedParams {
+  int rows, hidden, inter, experts, top_k, shared;
+  int softmax, normalise, act, router_f32;
+  float scale;
+  const void *x;
+  long long ld_x;
+  const void *router;
+  const float *bias;
+  FewMatrix gate, up, down;            // the experts'
+  FewMatrix s_gate, s_up, s_down;      // the shared experts'
+  void *y;
+  long long ld_y;
+  int32_t *indices;                    // [rows, top_k] or none
+  float *weights;
+  float *logits;                       // workspace: [rows, experts]
+  uint16_t *h;                         // workspace: [rows, top_k + shared, inter]
+};
+cudaError_t launch_routed(const RoutedParams &p, bool f16, bool bits4, int num_sms, cudaStream_t st);
+
+}  // namespace moe

@@ -462,6 +462,88 @@ typedef struct moe_ffn_gated_quantise_args {
 /* The codes of moe_ffn_fp8_matmul. */
 int moe_ffn_gated_quantise(const moe_ffn_gated_quantise_args *a, const moe_ffn_fp8_out *o, void *stream);
 
+/* Weights in 4 bits with a scale for each group of columns:
+ *   w[j, k] = (code[j, k] - zero[j, k / group]) * scale[j, k / group]
+ * Codes 0..15 lie two to a byte, the even column in the low half.  Without zero points zero is 8. */
+typedef struct moe_ffn_int4_weights_args {
+  int32_t n, k;                  /* n at most 2^24, k a multiple of 32, at most 2^20 */
+  int32_t group;                 /* 32, 64 or 128; the last group of a row may be shorter */
+  int32_t scale_type;            /* MOE_FFN_BF16 or _F16 */
+  uint8_t *codes;                /* [n, k / 2], contiguous, 16-byte aligned, as the next two */
+  void *scales;                  /* [n, ceil(k / group)] */
+  uint8_t *zeros;                /* [n, ceil(k / group)], the low four bits of each, or NULL */
+} moe_ffn_int4_weights_args;
+
+/* Makes such weights of w [n, k] (type MOE_FFN_F32, _BF16 or _F16; aligned to eight values, ld a multiple of 8).
+ * Without zeros: scale = max|w| / 7 of the group, code = 8 + w / scale within 1..15.  With zeros:
+ * scale = (max(w, 0) - min(w, 0)) / 15, zero = -min(w, 0) / scale, code = zero + w / scale within 0..15.
+ * Quotients are f32, rounded to nearest even; they are by the scale as it is stored, which is 1 for a group of zeros and
+ * at least scale_type's smallest normal value.  A group with a NaN or an infinity, or whose scale leaves scale_type, has
+ * the scale infinity, and products with it are not finite. */
+int moe_ffn_int4_quantise(const moe_ffn_int4_weights_args *a, const void *w, int32_t type, int64_t ld_w, void *stream);
+
+/* The values of such weights, rounded to scale_type: out [n, k], 16-byte aligned, ld a multiple of 8.  For prompts, whose
+ * products the 16-bit entry points make. */
+int moe_ffn_int4_widen(const moe_ffn_int4_weights_args *a, void *out, int64_t ld_out, void *stream);
+
+/* Product of a few rows with such weights: out[i, j] = sum over k of x[i, k] * w[j, k].  Each group's products are summed
+ * in f32 and multiplied by its scale there.  Made for up to 32 rows; more are taken 32 at a time. */
+typedef struct moe_ffn_int4_matmul_args {
+  int32_t rows, n, k;            /* rows at most 2^16; n and k as above */
+  int32_t type;                  /* of x, scales and out: MOE_FFN_BF16 or _F16 */
+  int32_t group;
+  const void *x; int64_t ld_x;   /* [rows, k]; 16-byte aligned, ld a multiple of 8 */
+  const uint8_t *codes;          /* as above */
+  const void *scales;
+  const uint8_t *zeros;
+  void *out; int64_t ld_out;     /* [rows, n], any ld >= n; overlaps no input */
+} moe_ffn_int4_matmul_args;
+
+/* These three return MOE_FFN_OK, NULL_PTR, ROWS_ZERO, ROWS_RANGE, BAD_CONFIG, ALIGNMENT, ALIAS, UNSUPPORTED or CUDA. */
+int moe_ffn_int4_matmul(const moe_ffn_int4_matmul_args *a, void *stream);
+
+/* A whole mixture-of-experts layer on a plain residual stream, for a few tokens:
+ *   l = x router^T;  s = sigmoid(l) or softmax(l) over the experts
+ *   the top_k experts by s + bias (in f32; without a bias by l), slots in descending order, exact ties to the lower index,
+ *   NaN after everything else
+ *   weight = route_scale * s, or with normalise route_scale * s / (sum of the chosen s)
+ *   y = sum over the slots of weight * E(x) + sum over the shared experts of S(x), each a gated block
+ *       E(x) = (act(x gate^T) * (x up^T)) down^T
+ * weight * act(g) * u is rounded to the operand type before the down projection (a shared expert's without a weight). */
+#define MOE_FFN_SCORE_SIGMOID 0
+#define MOE_FFN_SCORE_SOFTMAX 1
+
+typedef struct moe_ffn_matrices {  /* the matrices of one projection, [count, n, k], contiguous, 16-byte aligned */
+  const void *w;                   /* bits 16: values; bits 4: codes as above */
+  const void *scales;              /* bits 4 */
+  const uint8_t *zeros;            /* bits 4, or NULL; the shared experts' given exactly when the experts' are */
+} moe_ffn_matrices;
+
+typedef struct moe_ffn_routed_args {
+  int32_t rows, hidden, inter;     /* rows at most 32; hidden and inter multiples of 8 (bits 4: 32), at most 65536 */
+  int32_t experts, top_k, shared;  /* at most 512, 8 (and experts) and 8 */
+  int32_t type;                    /* MOE_FFN_BF16 or _F16: x, y, 16-bit weights, scales */
+  int32_t router_type;             /* MOE_FFN_F32 or type */
+  int32_t bits, group;             /* 16, or 4 with group 32, 64 or 128 */
+  int32_t score, normalise, activation;
+  float route_scale;
+  const void *x; int64_t ld_x;     /* [rows, hidden]; 16-byte aligned, ld a multiple of 8 */
+  const void *router;              /* [experts, hidden], contiguous, aligned to eight values */
+  const float *bias;               /* [experts], or NULL */
+  moe_ffn_matrices gate, up, down;                       /* [experts, inter, hidden] twice, [experts, hidden, inter] */
+  moe_ffn_matrices shared_gate, shared_up, shared_down;  /* the same of the shared experts; all NULL with shared 0 */
+  void *y; int64_t ld_y;           /* [rows, hidden], any ld >= hidden */
+  int32_t *indices;                /* [rows, top_k], or NULL */
+  float *weights;                  /* [rows, top_k], or NULL */
+  void *workspace; size_t workspace_bytes;  /* at least moe_ffn_routed_workspace, 16-byte aligned */
+} moe_ffn_routed_args;
+
+/* The codes of moe_ffn_int4_matmul, and NO_MEMORY when the workspace is too small. */
+int moe_ffn_routed_forward(const moe_ffn_routed_args *a, void *stream);
+
+/* Bytes of workspace that the call needs; negative: an error code. */
+int64_t moe_ffn_routed_workspace(const moe_ffn_routed_args *a);
+
 /* Device status bits (MOE_FFN_DEV_TIMEOUT) that the dense sublayer's kernels set on the current device
  * since the previous call, after waiting for `stream` (which must not be under capture); then cleared.
  * Each set of bits is reported to one caller.  Or a negative code. */
