@@ -27,13 +27,9 @@ __global__ void take_status_kernel() { g_status_out = atomicExch(&g_status, 0); 
 std::atomic<int> g_inject{0};
 std::atomic<unsigned> g_wait_us{0};
 
-struct DeviceSide {
-  int *status;
-  uint64_t wait_ns;
-  int inject;
-};
+}  // namespace
 
-int device_side(const char *who, DeviceSide *d) {
+int moe::entry::device_side(const char *who, DeviceSide *d) {
   static std::atomic<int *> known[kMaxDevices];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
@@ -54,34 +50,7 @@ int device_side(const char *who, DeviceSide *d) {
   return MOE_FFN_OK;
 }
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn find_encode() {
-  void *p = nullptr;
-  cudaDriverEntryPointQueryResult q;
-  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-      q == cudaDriverEntryPointSuccess)
-    return reinterpret_cast<EncodeTiledFn>(p);
-  cudaGetLastError();
-  return nullptr;
-}
-
-// A row-major matrix [outer, inner] of 1- or 2-byte elements, rows `ld` elements apart, in boxes of 128
-// bytes x box_outer rows with the 128-byte swizzle; what lies past its ends reads as zeros.
-bool encode_map(CUtensorMap *m, const void *base, int bytes, int64_t inner, int64_t outer, int64_t ld, int box_outer) {
-  static const EncodeTiledFn enc = find_encode();
-  if (!enc) return false;
-  const cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
-  const cuuint64_t strides[1] = {(cuuint64_t)(ld * bytes)};
-  const cuuint32_t box[2] = {(cuuint32_t)(128 / bytes), (cuuint32_t)box_outer};
-  const cuuint32_t estr[2] = {1, 1};
-  return enc(m, bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
-             const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
+namespace {
 
 // ---- block_norm ----
 

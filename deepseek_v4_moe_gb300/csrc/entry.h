@@ -1,5 +1,6 @@
 // What the C entry points without a handle share: error texts, the device, checks of tensors' places.
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdarg.h>
 #include <stdint.h>
@@ -110,6 +111,45 @@ inline int check_stride(const char *who, const char *name, int64_t ld, int64_t r
 }
 
 constexpr int64_t kLdMax = (int64_t)1 << 36;  // a row stride in bytes stays below the tensor maps' 2^40
+
+// What the kernels with bounded waits get besides their arguments: where they report a wait that ran out, how long one
+// may last, and whether one is to run out for a test.
+struct DeviceSide {
+  int *status;
+  uint64_t wait_ns;
+  int inject;
+};
+int device_side(const char *who, DeviceSide *d);  // dense.cu
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+inline EncodeTiledFn find_encode() {
+  void *p = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+      q == cudaDriverEntryPointSuccess)
+    return reinterpret_cast<EncodeTiledFn>(p);
+  cudaGetLastError();
+  return nullptr;
+}
+
+// A row-major matrix [outer, inner] of 1- or 2-byte elements, rows `ld` elements apart, in boxes of 128 (or 64) bytes x
+// box_outer rows with the swizzle of that width; what lies past its ends reads as zeros.
+inline bool encode_map(CUtensorMap *m, const void *base, int bytes, int64_t inner, int64_t outer, int64_t ld, int box_outer,
+                       int box_bytes = 128) {
+  static const EncodeTiledFn enc = find_encode();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
+  const cuuint64_t strides[1] = {(cuuint64_t)(ld * bytes)};
+  const cuuint32_t box[2] = {(cuuint32_t)(box_bytes / bytes), (cuuint32_t)box_outer};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(m, bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+             const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             box_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 }  // namespace entry
 }  // namespace moe

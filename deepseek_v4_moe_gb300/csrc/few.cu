@@ -34,6 +34,11 @@ moe::FewMatrix matrix(const void *w, const void *scales, const uint8_t *zeros, i
   return moe::FewMatrix{w, static_cast<const uint16_t *>(scales), zeros, (int)n, (int)k, groups, log2_of(group)};
 }
 
+// boxes of 64 bytes x 16 rows over `count` matrices [n, k] one after another
+bool box_map(CUtensorMap *m, const moe::FewMatrix &w, int64_t count, int bits) {
+  return bits == 4 ? encode_map(m, w.w, 1, w.k / 2, count * w.n, w.k / 2, 16, 64) : encode_map(m, w.w, 2, w.k, count * w.n, w.k, 16, 64);
+}
+
 // rows of x or of a result in 16-byte pieces
 int check_rows16(const char *who, const char *name, const void *p, int64_t ld, int64_t cols) {
   if (!p) return fail(MOE_FFN_ERR_NULL_PTR, "%s: %s is NULL", who, name);
@@ -144,7 +149,12 @@ extern "C" int moe_ffn_int4_matmul(const moe_ffn_int4_matmul_args *a, void *stre
   p.ld_x = a->ld_x;
   p.out = a->out;
   p.ld_out = a->ld_out;
-  return launched(who, moe::launch_int4_matmul(p, a->type == MOE_FFN_F16, sms, static_cast<cudaStream_t>(stream)));
+  DeviceSide dev;
+  if ((rc = device_side(who, &dev))) return rc;
+  p.waits = moe::Waits{dev.status, dev.wait_ns, dev.inject};
+  CUtensorMap map;
+  if (!box_map(&map, p.w, 1, 4)) return fail(MOE_FFN_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", who);
+  return launched(who, moe::launch_int4_matmul(p, map, a->type == MOE_FFN_F16, sms, static_cast<cudaStream_t>(stream)));
 }
 
 namespace {
@@ -264,5 +274,15 @@ extern "C" int moe_ffn_routed_forward(const moe_ffn_routed_args *a, void *stream
   p.weights = a->weights;
   p.logits = static_cast<float *>(a->workspace);
   p.h = reinterpret_cast<uint16_t *>(static_cast<char *>(a->workspace) + logits_bytes(a));
-  return launched(who, moe::launch_routed(p, a->type == MOE_FFN_F16, a->bits == 4, sms, static_cast<cudaStream_t>(stream)));
+  DeviceSide dev;
+  if ((rc = device_side(who, &dev))) return rc;
+  p.waits = moe::Waits{dev.status, dev.wait_ns, dev.inject};
+  moe::RoutedMaps maps;
+  moe::RoutedDownMaps down;
+  CUtensorMap *to[] = {&maps.gate, &maps.up, &down.down, &maps.s_gate, &maps.s_up, &down.s_down};
+  for (int i = 0; i < 6; ++i) {
+    if (i >= 3 && !S) *to[i] = *to[i - 3];  // not read
+    else if (!box_map(to[i], m[i], i < 3 ? E : S, a->bits)) return fail(MOE_FFN_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", who);
+  }
+  return launched(who, moe::launch_routed(p, maps, down, a->type == MOE_FFN_F16, a->bits == 4, sms, static_cast<cudaStream_t>(stream)));
 }

@@ -1,5 +1,6 @@
 // Host-side launchers of the kernels for a few rows: products with 4-bit weights, and the routed layer without a handle.
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -17,14 +18,23 @@ struct FewMatrix {
   int n, k, groups, group_shift;
 };
 
+// what a kernel with bounded waits reports to, how long they last, and whether one is to run out
+struct Waits {
+  int *status;
+  uint64_t ns;
+  int inject;
+};
+
 struct Int4MatmulParams {
   FewMatrix w;
   int rows;
   const void *x;
   void *out;
   long long ld_x, ld_out;
+  Waits waits;
 };
-cudaError_t launch_int4_matmul(const Int4MatmulParams &p, bool f16, int num_sms, cudaStream_t st);
+// map: over the codes, boxes of 64 bytes x 16 rows
+cudaError_t launch_int4_matmul(const Int4MatmulParams &p, const CUtensorMap &map, bool f16, int num_sms, cudaStream_t st);
 
 struct Int4WeightParams {
   int n, k, group, type;      // type: of w, or of the widened matrix
@@ -63,7 +73,16 @@ struct RoutedParams {
   float *weights;
   float *logits;                       // workspace: [rows, experts]
   uint16_t *h;                         // workspace: [rows, top_k + shared, inter]
+  Waits waits;
 };
-cudaError_t launch_routed(const RoutedParams &p, bool f16, bool bits4, int num_sms, cudaStream_t st);
+// over all experts' rows of each matrix, boxes of 64 bytes x 16 rows
+struct RoutedMaps {
+  CUtensorMap gate, up, s_gate, s_up;
+};
+struct RoutedDownMaps {
+  CUtensorMap down, s_down;
+};
+cudaError_t launch_routed(const RoutedParams &p, const RoutedMaps &maps, const RoutedDownMaps &down, bool f16, bool bits4,
+                          int num_sms, cudaStream_t st);
 
 }  // namespace moe

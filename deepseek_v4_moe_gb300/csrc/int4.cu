@@ -17,63 +17,65 @@ namespace {
 template <typename T, int M, int NT>
 struct Int4Job {
   const Int4MatmulParams &p;
-  int units, tiles, sets, row_first, rows;
+  const CUtensorMap &map;
+  int units, segs, tiles, sets, row_first, rows;
   Tokens<NT> x;
+  int row_ahead;
+  Meta meta[M];
+  Tile<T, 4, M, NT> t;
   __device__ __forceinline__ int row0(int unit, int set) const { return (unit * sets + set) * (16 * M); }
   __device__ __forceinline__ void copies_begun() const {}
-  __device__ __forceinline__ void copy(uint32_t place, int unit, int set, int tile) const {
+  __device__ __forceinline__ void load_at(int unit, int set, int) { row_ahead = row0(unit, set); }
+  __device__ __forceinline__ void load(char *place, uint64_t *bar, int tile) const {
+    const int s = threadIdx.x & 31;
+    if (s < M) tma_load_2d(place + s * kBoxBytes, &map, bar, tile * 64, row_ahead + 16 * s);
+  }
+  __device__ __forceinline__ void use_at(int unit, int set, int) {
     const int r = row0(unit, set);
 #pragma unroll
-    for (int s = 0; s < M; ++s) copy_strip<4>(place + s * kStripBytes, p.w, 0, r + 16 * s, tile);
-    const int lane = threadIdx.x & 31;
-    if (lane < 16 * M) copy_meta(place + M * kStripBytes, p.w, 0, r, tile, lane);
+    for (int s = 0; s < M; ++s) meta[s].at(p.w, min(r + 16 * s, p.w.n - 1), p.w.n - r - 16 * s);
   }
-  __device__ __forceinline__ void multiply(uint32_t place, int unit, int set, int tile, float (&acc)[M][NT][4]) const {
-    FewMatrix m[M];
-    int e[M], r[M];
-#pragma unroll
-    for (int s = 0; s < M; ++s) {
-      m[s] = p.w;
-      e[s] = 0;
-      r[s] = row0(unit, set) + 16 * s;
-    }
-    multiply_tile<T, 4, M, NT>(place, m, e, r, tile, x, ~0u, acc);
+  __device__ __forceinline__ void fetch(int tile) {
+    t.fetch(x, tile * kTileK<4>, p.w.k);
+    t.fetch_meta(meta, tile * kTileK<4>, p.w.group_shift);
+  }
+  __device__ __forceinline__ void multiply(uint32_t place, float (&acc)[M][NT][4]) {
+    t.multiply(place, ~0u, acc, p.w.group_shift, p.w.zeros != nullptr);
   }
   template <typename Sum>
-  __device__ __forceinline__ void finish(int unit, int set, int thread, int threads, Sum sum) const {
-    const int r0 = row0(unit, set);
-    for (int i = thread; i < 16 * M * rows; i += threads) {
-      const int row = i % (16 * M), token = i / (16 * M);
-      if (r0 + row < p.w.n)
-        static_cast<T *>(p.out)[(row_first + token) * p.ld_out + r0 + row] = from_f32<T>(sum(row >> 4, row & 15, token));
+  __device__ __forceinline__ void finish(int unit, int set, int strip, int thread, int threads, Sum sum) const {
+    const int r0 = row0(unit, set) + 16 * strip;
+    for (int i = thread; i < 16 * rows; i += threads) {
+      const int row = i & 15, token = i >> 4;
+      if (r0 + row < p.w.n) static_cast<T *>(p.out)[(row_first + token) * p.ld_out + r0 + row] = from_f32<T>(sum(0, row, token));
     }
   }
 };
 
+constexpr size_t kAlign = 1024;  // of the ring, whose boxes' swizzle goes by the address
 template <int M>
-constexpr int kInt4Stages = M == 2 ? 2 : 4;
+constexpr int kInt4Stages = M == 4 ? 3 : M == 2 ? 5 : 6;
 
 template <typename T, int M, int NT>
-__global__ void __launch_bounds__(32 * kFewWarps, 2) int4_matmul_kernel(const __grid_constant__ Int4MatmulParams p, int log_kw) {
-  extern __shared__ __align__(128) char smem[];
-  constexpr int kPlace = kPlaceBytes<4, M>;
-  const int lane = threadIdx.x & 31;
-  Int4Job<T, M, NT> job{p, 0, (p.w.k + kTileK<4> - 1) / kTileK<4>, kFewWarps >> log_kw, (int)blockIdx.y * 8 * NT, 0, {}};
-  job.units = (p.w.n + 16 * M * job.sets - 1) / (16 * M * job.sets);
-  job.rows = min(8 * NT, p.rows - job.row_first);
+__global__ void __launch_bounds__(32 * kFewWarps, 2)
+    int4_matmul_kernel(const __grid_constant__ Int4MatmulParams p, const __grid_constant__ CUtensorMap map, int log_kw) {
+  extern __shared__ char smem[];
+  const int lane = threadIdx.x & 31, sets = kFewWarps >> log_kw, row_first = (int)blockIdx.y * 8 * NT;
+  Int4Job<T, M, NT> job{p, map, 0, 1, (p.w.k + kTileK<4> - 1) / kTileK<4>, sets, row_first, min(8 * NT, p.rows - row_first)};
+  job.units = (p.w.n + 16 * M * sets - 1) / (16 * M * sets);
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
     const int token = 8 * i + (lane >> 2);
-    job.x.row[i] = token < job.rows ? static_cast<const char *>(p.x) + (job.row_first + token) * p.ld_x * 2 : nullptr;
+    job.x.row[i] = token < job.rows ? static_cast<const char *>(p.x) + (row_first + token) * p.ld_x * 2 : nullptr;
   }
   pdl_wait();
-  stream_units<M, NT, kInt4Stages<M>, kPlace>(job, smem_u32(smem), reinterpret_cast<float *>(smem + kFewWarps * kInt4Stages<M> * kPlace),
-                                              log_kw);
+  char *ring = smem + (-smem_u32(smem) & (kAlign - 1));
+  stream_units<M, 1, NT, kInt4Stages<M>, M>(job, ring, log_kw, p.waits.status, p.waits.ns, p.waits.inject);
 }
 
 template <typename T, int M, int NT>
-cudaError_t int4_launch(const Int4MatmulParams &p, int num_sms, cudaStream_t st) {
-  constexpr size_t smem = kFewWarps * (kInt4Stages<M> * kPlaceBytes<4, M> + M * NT * kPartFloats * sizeof(float));
+cudaError_t int4_launch(const Int4MatmulParams &p, const CUtensorMap &map, int num_sms, cudaStream_t st) {
+  constexpr size_t smem = kFewWarps * (kInt4Stages<M> * M * kBoxBytes + NT * kPartFloats * sizeof(float)) + kAlign;
   static std::atomic<unsigned long long> done{0};
   const cudaError_t e = allow_smem((const void *)int4_matmul_kernel<T, M, NT>, smem, done);
   if (e != cudaSuccess) return e;
@@ -83,21 +85,16 @@ cudaError_t int4_launch(const Int4MatmulParams &p, int num_sms, cudaStream_t st)
   while (log_kw < 3 && (2 << log_kw) <= tiles && (strips << log_kw) < 4 * kFewWarps * num_sms) ++log_kw;
   const int units = (strips + (kFewWarps >> log_kw) - 1) / (kFewWarps >> log_kw);
   const int y = (p.rows + 8 * NT - 1) / (8 * NT), most = 2 * num_sms;
-  return launch_pdl(int4_matmul_kernel<T, M, NT>, dim3(units < most ? units : most, y), dim3(32 * kFewWarps), smem, st, p, log_kw);
-}
-
-template <typename T, int M>
-cudaError_t int4_rows(const Int4MatmulParams &p, int num_sms, cudaStream_t st) {
-  if (p.rows <= 8) return int4_launch<T, M, 1>(p, num_sms, st);
-  if (p.rows <= 16) return int4_launch<T, M, 2>(p, num_sms, st);
-  return int4_launch<T, M, 4>(p, num_sms, st);
+  return launch_pdl(int4_matmul_kernel<T, M, NT>, dim3(units < most ? units : most, y), dim3(32 * kFewWarps), smem, st, p, map, log_kw);
 }
 
 template <typename T>
-cudaError_t int4_typed(const Int4MatmulParams &p, int num_sms, cudaStream_t st) {
-  // two strips a warp share what is read of x, where there are enough of them
-  if (p.w.n >= 64 * num_sms) return int4_rows<T, 2>(p, num_sms, st);
-  return int4_rows<T, 1>(p, num_sms, st);
+cudaError_t int4_typed(const Int4MatmulParams &p, const CUtensorMap &map, int num_sms, cudaStream_t st) {
+  // several strips a warp share what is read of x, where there are enough of them
+  const bool many = p.w.n >= 64 * num_sms, some = p.w.n >= 32 * num_sms;
+  if (p.rows <= 8) return many ? int4_launch<T, 4, 1>(p, map, num_sms, st) : some ? int4_launch<T, 2, 1>(p, map, num_sms, st) : int4_launch<T, 1, 1>(p, map, num_sms, st);
+  if (p.rows <= 16) return many ? int4_launch<T, 4, 2>(p, map, num_sms, st) : some ? int4_launch<T, 2, 2>(p, map, num_sms, st) : int4_launch<T, 1, 2>(p, map, num_sms, st);
+  return some ? int4_launch<T, 2, 4>(p, map, num_sms, st) : int4_launch<T, 1, 4>(p, map, num_sms, st);
 }
 
 // ---- making and widening weights ----
@@ -184,8 +181,8 @@ cudaError_t quantise_launch(const Int4WeightParams &p, int num_sms, cudaStream_t
 
 }  // namespace
 
-cudaError_t launch_int4_matmul(const Int4MatmulParams &p, bool f16, int num_sms, cudaStream_t st) {
-  return f16 ? int4_typed<__half>(p, num_sms, st) : int4_typed<__nv_bfloat16>(p, num_sms, st);
+cudaError_t launch_int4_matmul(const Int4MatmulParams &p, const CUtensorMap &map, bool f16, int num_sms, cudaStream_t st) {
+  return f16 ? int4_typed<__half>(p, map, num_sms, st) : int4_typed<__nv_bfloat16>(p, map, num_sms, st);
 }
 
 cudaError_t launch_int4_quantise(const Int4WeightParams &p, int num_sms, cudaStream_t st) {

@@ -206,49 +206,76 @@ __device__ __forceinline__ int slot_of(const RoutedParams &p, const Choice &c, i
 
 // ---- gate and up ----
 
+constexpr size_t kAlign = 1024;  // of the ring, whose boxes' swizzle goes by the address
+
+// the n-th token of a mask, or -1
+__device__ __forceinline__ int token_at(uint32_t mask, int n) {
+  for (; n > 0 && mask; --n) mask &= mask - 1u;
+  return __ffs(mask) - 1;
+}
+
+// A unit: 16 rows of a group's gate and up matrices.  Column j of the right operand is the group's j-th token.
 template <typename T, int BITS, int NT>
 struct UpJob {
   const RoutedParams &p;
+  const RoutedMaps &maps;
   const Choice &c;
-  int units, tiles, strips;  // a unit: 16 rows of a group's gate and up matrices
+  int units, segs, tiles, strips;
+  int row_ahead;
+  bool shared_ahead;
+  unsigned some;
+  Tokens<NT> x;
+  Meta meta[2];
+  Tile<T, BITS, 2, NT> t;
   __device__ __forceinline__ void copies_begun() const {}
-  __device__ __forceinline__ void copy(uint32_t place, int unit, int, int tile) const {
-    const int group = unit / strips, r = (unit - group * strips) * 16, e = c.expert[group];
-    const bool shared = group >= c.routed;
-    const FewMatrix &g = shared ? p.s_gate : p.gate, &u = shared ? p.s_up : p.up;
-    copy_strip<BITS>(place, g, e, r, tile);
-    copy_strip<BITS>(place + kStripBytes, u, e, r, tile);
-    if constexpr (BITS == 4) {
-      const int lane = threadIdx.x & 31;
-      copy_meta(place + 2 * kStripBytes + (lane >> 4) * 16 * kMetaPitch, lane < 16 ? g : u, e, r, tile, lane & 15);
-    }
+  __device__ __forceinline__ void load_at(int unit, int, int) {
+    const int group = unit / strips;
+    row_ahead = c.expert[group] * p.inter + (unit - group * strips) * 16;
+    shared_ahead = group >= c.routed;
   }
-  __device__ __forceinline__ void multiply(uint32_t place, int unit, int, int tile, float (&acc)[2][NT][4]) const {
+  __device__ __forceinline__ void load(char *place, uint64_t *bar, int tile) const {
+    const int i = threadIdx.x & 31, box = i % kBoxes<BITS>;
+    if (i >= 2 * kBoxes<BITS>) return;
+    const CUtensorMap *gate = shared_ahead ? &maps.s_gate : &maps.gate, *up = shared_ahead ? &maps.s_up : &maps.up;
+    tma_load_2d(place + i * kBoxBytes, i < kBoxes<BITS> ? gate : up, bar, (tile * kBoxes<BITS> + box) * (BITS == 16 ? 32 : 64), row_ahead);
+  }
+  __device__ __forceinline__ void use_at(int unit, int, int) {
     const int group = unit / strips, r = (unit - group * strips) * 16, e = c.expert[group], lane = threadIdx.x & 31;
     const uint32_t mask = c.group_mask[group];
-    Tokens<NT> x;
-    unsigned some = 0;
+    some = 0;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      const int token = 8 * i + (lane >> 2);
-      x.row[i] = mask >> token & 1 ? static_cast<const char *>(p.x) + token * p.ld_x * 2 : nullptr;
-      some |= (mask >> (8 * i) & 255u ? 1u : 0u) << i;
+      const int token = token_at(mask, 8 * i + (lane >> 2));
+      x.row[i] = token >= 0 ? static_cast<const char *>(p.x) + token * p.ld_x * 2 : nullptr;
+      some |= (__popc(mask) > 8 * i ? 1u : 0u) << i;
     }
-    const FewMatrix m[2] = {p.gate, p.up};  // (the shared experts' are of the same shape)
-    const int es[2] = {e, e}, rs[2] = {r, r};
-    multiply_tile<T, BITS, 2, NT>(place, m, es, rs, tile, x, some, acc);
+    if constexpr (BITS == 4) {
+      const bool sh = group >= c.routed;
+      const long long row = (long long)e * p.inter + r;
+      meta[0].at(sh ? p.s_gate : p.gate, row, p.inter - r);
+      meta[1].at(sh ? p.s_up : p.up, row, p.inter - r);
+    }
+  }
+  __device__ __forceinline__ void fetch(int tile) {
+    t.fetch(x, tile * kTileK<BITS>, p.hidden);
+    if constexpr (BITS == 4) t.fetch_meta(meta, tile * kTileK<BITS>, p.gate.group_shift);
+  }
+  __device__ __forceinline__ void multiply(uint32_t place, float (&acc)[2][NT][4]) {
+    if constexpr (BITS == 4) t.multiply(place, some, acc, p.gate.group_shift, p.gate.zeros || p.up.zeros);
+    else t.multiply(place, some, acc);
   }
   template <typename Sum>
-  __device__ __forceinline__ void finish(int unit, int, int thread, int threads, Sum sum) const {
+  __device__ __forceinline__ void finish(int unit, int, int, int thread, int threads, Sum sum) const {
     const int group = unit / strips, r = (unit - group * strips) * 16;
     const uint32_t mask = c.group_mask[group];
-    for (int i = thread; i < 16 * p.rows; i += threads) {
-      const int row = i & 15, token = i >> 4;
-      if (!(mask >> token & 1) || r + row >= p.inter) continue;
+    const int count = __popc(mask);
+    for (int i = thread; i < 16 * count; i += threads) {
+      const int row = i & 15, column = i >> 4, token = token_at(mask, column);
+      if (r + row >= p.inter) continue;
       const int slot = slot_of(p, c, group, token);
       const float w = group < c.routed ? c.weight[token][slot] : 1.f;
       // rounded to 16 bits as the tensor cores' operand, as the gated block does
-      const T h = from_f32<T>(act_value(p.act, sum(0, row, token)) * sum(1, row, token) * w);
+      const T h = from_f32<T>(act_value(p.act, sum(0, row, column)) * sum(1, row, column) * w);
       p.h[((long long)token * (p.top_k + p.shared) + slot) * p.inter + r + row] = *reinterpret_cast<const uint16_t *>(&h);
     }
   }
@@ -256,26 +283,34 @@ struct UpJob {
 
 // ---- down ----
 
+// A unit: 16 rows of every group's matrix.  Column j of the right operand is token j for every group.
 template <typename T, int BITS, int NT>
 struct DownJob {
   const RoutedParams &p;
+  const RoutedDownMaps &maps;
   const Choice &c;
-  int units, tiles, per;  // a unit: 16 rows of every group's matrix; per: tiles of a group
+  int units, segs, tiles;
+  int row_ahead;
+  bool shared_ahead;
+  unsigned some;
+  Tokens<NT> x;
+  Meta meta[1];
+  Tile<T, BITS, 1, NT> t;
   __device__ __forceinline__ void copies_begun() const { pdl_wait(); }  // h comes from the kernel before
-  __device__ __forceinline__ void copy(uint32_t place, int unit, int, int tile) const {
-    const int group = tile / per, e = c.expert[group];
-    const FewMatrix &d = group >= c.routed ? p.s_down : p.down;
-    copy_strip<BITS>(place, d, e, unit * 16, tile - group * per);
-    if constexpr (BITS == 4) {
-      const int lane = threadIdx.x & 31;
-      if (lane < 16) copy_meta(place + kStripBytes, d, e, unit * 16, tile - group * per, lane);
-    }
+  __device__ __forceinline__ void load_at(int unit, int, int group) {
+    row_ahead = c.expert[group] * p.hidden + unit * 16;
+    shared_ahead = group >= c.routed;
   }
-  __device__ __forceinline__ void multiply(uint32_t place, int unit, int, int tile, float (&acc)[1][NT][4]) const {
-    const int group = tile / per, lane = threadIdx.x & 31;
+  __device__ __forceinline__ void load(char *place, uint64_t *bar, int tile) const {
+    const int i = threadIdx.x & 31;
+    if (i < kBoxes<BITS>)
+      tma_load_2d(place + i * kBoxBytes, shared_ahead ? &maps.s_down : &maps.down, bar,
+                  (tile * kBoxes<BITS> + i) * (BITS == 16 ? 32 : 64), row_ahead);
+  }
+  __device__ __forceinline__ void use_at(int unit, int, int group) {
+    const int e = c.expert[group], lane = threadIdx.x & 31;
     const uint32_t mask = c.group_mask[group];
-    Tokens<NT> x;
-    unsigned some = 0;
+    some = 0;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       const int token = 8 * i + (lane >> 2);
@@ -285,12 +320,18 @@ struct DownJob {
             p.h + ((long long)token * (p.top_k + p.shared) + slot_of(p, c, group, token)) * p.inter);
       some |= (mask >> (8 * i) & 255u ? 1u : 0u) << i;
     }
-    const FewMatrix m[1] = {p.down};
-    const int es[1] = {c.expert[group]}, rs[1] = {unit * 16};
-    multiply_tile<T, BITS, 1, NT>(place, m, es, rs, tile - group * per, x, some, acc);
+    if constexpr (BITS == 4) meta[0].at(group >= c.routed ? p.s_down : p.down, (long long)e * p.hidden + unit * 16, p.hidden - unit * 16);
+  }
+  __device__ __forceinline__ void fetch(int tile) {
+    t.fetch(x, tile * kTileK<BITS>, p.inter);
+    if constexpr (BITS == 4) t.fetch_meta(meta, tile * kTileK<BITS>, p.down.group_shift);
+  }
+  __device__ __forceinline__ void multiply(uint32_t place, float (&acc)[1][NT][4]) {
+    if constexpr (BITS == 4) t.multiply(place, some, acc, p.down.group_shift, p.down.zeros != nullptr);
+    else t.multiply(place, some, acc);
   }
   template <typename Sum>
-  __device__ __forceinline__ void finish(int unit, int, int thread, int threads, Sum sum) const {
+  __device__ __forceinline__ void finish(int unit, int, int, int thread, int threads, Sum sum) const {
     for (int i = thread; i < 16 * p.rows; i += threads) {
       const int row = i & 15, token = i >> 4;
       if (unit * 16 + row < p.hidden) static_cast<T *>(p.y)[token * p.ld_y + unit * 16 + row] = from_f32<T>(sum(0, row, token));
@@ -298,64 +339,70 @@ struct DownJob {
   }
 };
 
+template <bool UP, int BITS>
+constexpr int kRoutedStages = UP ? (BITS == 16 ? 2 : 4) : (BITS == 16 ? 5 : 8);
 template <bool UP, int BITS, int NT>
-constexpr int kRoutedStages = !UP ? 4 : BITS == 16 && NT == 1 ? 3 : 2;
+constexpr size_t kRoutedSmem =
+    kFewWarps * (kRoutedStages<UP, BITS> * (UP ? 2 : 1) * kBoxes<BITS> * kBoxBytes + (UP ? 2 : 1) * NT * kPartFloats * sizeof(float)) + kAlign;
 
-template <bool UP, typename T, int BITS, int NT>
-__global__ void __launch_bounds__(32 * kFewWarps, 2) routed_kernel(const __grid_constant__ RoutedParams p) {
-  constexpr int M = UP ? 2 : 1, kStages = kRoutedStages<UP, BITS, NT>, kPlace = kPlaceBytes<BITS, M>;
-  extern __shared__ __align__(128) char smem[];
+template <typename T, int BITS, int NT>
+__global__ void __launch_bounds__(32 * kFewWarps, 2)
+    routed_up_kernel(const __grid_constant__ RoutedParams p, const __grid_constant__ RoutedMaps maps) {
+  extern __shared__ char smem[];
   __shared__ Choice c;
-  float *parts = reinterpret_cast<float *>(smem + kFewWarps * kStages * kPlace);
-  if constexpr (UP) {
-    pdl_wait();
-    // The down kernel's CTAs may come, choose and fetch weights: not earlier, as they read the logits.
-    pdl_trigger();
-    choose(p, c, blockIdx.x == 0);
-    const int strips = (p.inter + 15) / 16;
-    UpJob<T, BITS, NT> job{p, c, c.groups * strips, (p.hidden + kTileK<BITS> - 1) / kTileK<BITS>, strips};
-    stream_units<M, NT, kStages, kPlace>(job, smem_u32(smem), parts, 3);
-  } else {
-    choose(p, c, false);
-    const int per = (p.inter + kTileK<BITS> - 1) / kTileK<BITS>;
-    DownJob<T, BITS, NT> job{p, c, (p.hidden + 15) / 16, c.groups * per, per};
-    stream_units<M, NT, kStages, kPlace>(job, smem_u32(smem), parts, 3);
-  }
-}
-
-template <bool UP, typename T, int BITS, int NT>
-cudaError_t part_launch(const RoutedParams &p, int num_sms, cudaStream_t st) {
-  constexpr int M = UP ? 2 : 1;
-  constexpr size_t smem = kFewWarps * (kRoutedStages<UP, BITS, NT> * kPlaceBytes<BITS, M> + M * NT * kPartFloats * sizeof(float));
-  static std::atomic<unsigned long long> done{0};
-  const cudaError_t e = allow_smem((const void *)routed_kernel<UP, T, BITS, NT>, smem, done);
-  if (e != cudaSuccess) return e;
-  const long long groups = (long long)(p.rows * p.top_k < p.experts ? p.rows * p.top_k : p.experts) + p.shared;
-  const long long units = UP ? groups * ((p.inter + 15) / 16) : (p.hidden + 15) / 16, most = 2ll * num_sms;
-  return launch_pdl(routed_kernel<UP, T, BITS, NT>, dim3((unsigned)(units < most ? units : most)), dim3(32 * kFewWarps), smem, st, p);
+  char *ring = smem + (-smem_u32(smem) & (kAlign - 1));
+  pdl_wait();
+  // The down kernel's CTAs may come, choose and fetch weights: not earlier, as they read the logits.
+  pdl_trigger();
+  choose(p, c, blockIdx.x == 0);
+  const int strips = (p.inter + 15) / 16;
+  UpJob<T, BITS, NT> job{p, maps, c, c.groups * strips, 1, (p.hidden + kTileK<BITS> - 1) / kTileK<BITS>, strips};
+  stream_units<2, 2, NT, kRoutedStages<true, BITS>, 2 * kBoxes<BITS>>(job, ring, 3, p.waits.status, p.waits.ns, p.waits.inject);
 }
 
 template <typename T, int BITS, int NT>
-cudaError_t layer_launch(const RoutedParams &p, int num_sms, cudaStream_t st) {
-  const dim3 grid((p.experts + kRouteExperts - 1) / kRouteExperts);
-  cudaError_t e = launch_pdl(p.router_f32 ? routed_logits_kernel<T, float> : routed_logits_kernel<T, T>, grid, dim3(256), 0, st, p);
-  if (e == cudaSuccess) e = part_launch<true, T, BITS, NT>(p, num_sms, st);
-  if (e == cudaSuccess) e = part_launch<false, T, BITS, NT>(p, num_sms, st);
+__global__ void __launch_bounds__(32 * kFewWarps, 2)
+    routed_down_kernel(const __grid_constant__ RoutedParams p, const __grid_constant__ RoutedDownMaps maps) {
+  extern __shared__ char smem[];
+  __shared__ Choice c;
+  char *ring = smem + (-smem_u32(smem) & (kAlign - 1));
+  choose(p, c, false);
+  DownJob<T, BITS, NT> job{p, maps, c, (p.hidden + 15) / 16, c.groups, (p.inter + kTileK<BITS> - 1) / kTileK<BITS>};
+  stream_units<1, 1, NT, kRoutedStages<false, BITS>, kBoxes<BITS>>(job, ring, 3, p.waits.status, p.waits.ns, p.waits.inject);
+}
+
+template <typename T, int BITS, int NT>
+cudaError_t layer_launch(const RoutedParams &p, const RoutedMaps &maps, const RoutedDownMaps &down, int num_sms, cudaStream_t st) {
+  constexpr size_t smem_up = kRoutedSmem<true, BITS, NT>, smem_down = kRoutedSmem<false, BITS, NT>;
+  static std::atomic<unsigned long long> done[2];
+  cudaError_t e = allow_smem((const void *)routed_up_kernel<T, BITS, NT>, smem_up, done[0]);
+  if (e == cudaSuccess) e = allow_smem((const void *)routed_down_kernel<T, BITS, NT>, smem_down, done[1]);
+  const dim3 threads(32 * kFewWarps);
+  if (e == cudaSuccess)
+    e = launch_pdl(p.router_f32 ? routed_logits_kernel<T, float> : routed_logits_kernel<T, T>,
+                   dim3((p.experts + kRouteExperts - 1) / kRouteExperts), dim3(256), 0, st, p);
+  const long long groups = (long long)(p.rows * p.top_k < p.experts ? p.rows * p.top_k : p.experts) + p.shared;
+  const long long units = groups * ((p.inter + 15) / 16), units_down = (p.hidden + 15) / 16, most = 2ll * num_sms;
+  if (e == cudaSuccess)
+    e = launch_pdl(routed_up_kernel<T, BITS, NT>, dim3((unsigned)(units < most ? units : most)), threads, smem_up, st, p, maps);
+  if (e == cudaSuccess)
+    e = launch_pdl(routed_down_kernel<T, BITS, NT>, dim3((unsigned)(units_down < most ? units_down : most)), threads, smem_down, st, p, down);
   return e;
 }
 
 template <typename T, int BITS>
-cudaError_t routed_rows(const RoutedParams &p, int num_sms, cudaStream_t st) {
-  if (p.rows <= 8) return layer_launch<T, BITS, 1>(p, num_sms, st);
-  if (p.rows <= 16) return layer_launch<T, BITS, 2>(p, num_sms, st);
-  return layer_launch<T, BITS, 4>(p, num_sms, st);
+cudaError_t routed_rows(const RoutedParams &p, const RoutedMaps &maps, const RoutedDownMaps &down, int num_sms, cudaStream_t st) {
+  if (p.rows <= 8) return layer_launch<T, BITS, 1>(p, maps, down, num_sms, st);
+  if (p.rows <= 16) return layer_launch<T, BITS, 2>(p, maps, down, num_sms, st);
+  return layer_launch<T, BITS, 4>(p, maps, down, num_sms, st);
 }
 
 }  // namespace
 
-cudaError_t launch_routed(const RoutedParams &p, bool f16, bool bits4, int num_sms, cudaStream_t st) {
-  if (f16) return bits4 ? routed_rows<__half, 4>(p, num_sms, st) : routed_rows<__half, 16>(p, num_sms, st);
-  return bits4 ? routed_rows<__nv_bfloat16, 4>(p, num_sms, st) : routed_rows<__nv_bfloat16, 16>(p, num_sms, st);
+cudaError_t launch_routed(const RoutedParams &p, const RoutedMaps &maps, const RoutedDownMaps &down, bool f16, bool bits4,
+                          int num_sms, cudaStream_t st) {
+  if (f16) return bits4 ? routed_rows<__half, 4>(p, maps, down, num_sms, st) : routed_rows<__half, 16>(p, maps, down, num_sms, st);
+  return bits4 ? routed_rows<__nv_bfloat16, 4>(p, maps, down, num_sms, st) : routed_rows<__nv_bfloat16, 16>(p, maps, down, num_sms, st);
 }
 
 }  // namespace moe
