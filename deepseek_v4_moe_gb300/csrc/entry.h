@@ -151,5 +151,18 @@ inline bool encode_map(CUtensorMap *m, const void *base, int bytes, int64_t inne
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A row-major matrix [rows, 32 * pieces] of 16-bit elements as pieces of 32 columns (64 bytes, in that swizzle), in boxes
+// of box_rows rows of box_pieces pieces, piece after piece; what lies past its ends reads as zeros.
+inline bool encode_pieces(CUtensorMap *m, const void *base, int64_t pieces, int64_t rows, int64_t ld, int box_rows, int box_pieces) {
+  static const EncodeTiledFn enc = find_encode();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {32, (cuuint64_t)rows, (cuuint64_t)pieces};
+  const cuuint64_t strides[2] = {(cuuint64_t)(ld * 2), 64};
+  const cuuint32_t box[3] = {32, (cuuint32_t)box_rows, (cuuint32_t)box_pieces}, estr[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace entry
 }  // namespace moe

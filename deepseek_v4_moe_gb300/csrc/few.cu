@@ -152,9 +152,12 @@ extern "C" int moe_ffn_int4_matmul(const moe_ffn_int4_matmul_args *a, void *stre
   DeviceSide dev;
   if ((rc = device_side(who, &dev))) return rc;
   p.waits = moe::Waits{dev.status, dev.wait_ns, dev.inject};
-  CUtensorMap map;
-  if (!box_map(&map, p.w, 1, 4)) return fail(MOE_FFN_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", who);
-  return launched(who, moe::launch_int4_matmul(p, map, a->type == MOE_FFN_F16, sms, static_cast<cudaStream_t>(stream)));
+  const moe::Int4Tiles t = moe::int4_pick_tiles(a->rows, a->n, a->k, sms);
+  moe::Int4Maps maps;
+  if (!encode_map(&maps.w, a->codes, 1, K / 2, N, K / 2, t.w_box(), 64) ||
+      !encode_pieces(&maps.x, a->x, K / 32, R, a->ld_x, t.box_rows, t.x_box_pieces()))
+    return fail(MOE_FFN_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", who);
+  return launched(who, moe::launch_int4_matmul(p, maps, t, a->type == MOE_FFN_F16, sms, static_cast<cudaStream_t>(stream)));
 }
 
 namespace {

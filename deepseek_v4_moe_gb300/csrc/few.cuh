@@ -6,10 +6,9 @@
 // left operand of 128 rows in shared or tensor memory: 4-bit weights would have to be written there in 16 bits, four
 // times the bytes that come from memory, and read again.)
 //
-// TMA brings 64 bytes of each of a strip's rows (32 columns in 16 bits, 128 in 4), into a ring that each warp has for
-// itself: no barrier is met in the loop, and one instruction takes the place of a lane's address arithmetic (with
-// cp.async and the addresses in every lane 16 tokens by 129280 x 4096 took 165 us, at 1.6 instructions a cycle).
-// What the weights are multiplied with comes through the L1.
+// TMA brings 64 bytes of each of a strip's rows (32 columns in 16 bits, 128 in 4) into a ring, and the tokens' columns
+// beside them: with the addresses in every lane 16 tokens by 129280 x 4096 took 165 us at 1.6 instructions a cycle, and
+// with the tokens read through the L1 their latency stopped the warps.
 // The order of k within a tile is free as long as both operands have the same one: lane 4 g + t of a warp holds columns
 // 32 c + 8 t .. + 7 of row g (and g + 8), as one 16-byte read of x gives them for token g.
 #pragma once
@@ -95,147 +94,174 @@ __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t at) {
                : "memory");
 }
 
-// The tokens that a lane reads the right operand of: token g of each eight, or null.
-template <int NT>
-struct Tokens {
-  const char *row[NT];
-  __device__ __forceinline__ uint4 get(int i, int k, int end) const {
-    return row[i] && k < end ? *reinterpret_cast<const uint4 *>(row[i] + 2 * (long long)k) : make_uint4(0u, 0u, 0u, 0u);
+// The right operand of a tile in shared memory: pieces of 32 columns, each `rows` tokens' 64 bytes one after another, in
+// the same swizzle as the weights.  A lane's 16 bytes of a piece for its token of eight i.  ROWS8: rows is a multiple of
+// 8, so that a piece is that many bytes from the one before.
+template <int PIECES, int NT, bool ROWS8>
+struct Operand {
+  uint32_t at[ROWS8 ? 1 : PIECES];
+  uint32_t pitch;  // of a piece
+  // first: the tile's first line (of 64 bytes, from an address that is a multiple of 512)
+  __device__ __forceinline__ void set(int first, int rows) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    pitch = rows * 64;
+#pragma unroll
+    for (int c = 0; c < (ROWS8 ? 1 : PIECES); ++c) {
+      const int line = first + c * rows + min(g, rows - 1);  // (a token that is none reads another's: nobody reads its sums)
+      at[c] = line * 64 + ((t ^ (line >> 1 & 3)) << 4);
+    }
+  }
+  __device__ __forceinline__ uint4 get(uint32_t base, int c, int i) const {
+    return ROWS8 ? lds128(base + at[0] + c * pitch + i * 512) : lds128(base + at[c % (ROWS8 ? 1 : PIECES)]);
   }
 };
 
-// A tile's right operand and scales in a lane's registers, and the strips' products.
-template <typename T, int BITS, int M, int NT>
+// The products of a tile's strips.  PIECES: of 32 columns in a group of 4-bit weights, at compile time, so that a tile's
+// products are one run of instructions in which the strips overlap.
+template <typename T, int BITS, int PIECES, int M, int NT, bool ROWS8>
 struct Tile;
 
-template <typename T, int M, int NT>
-struct Tile<T, 16, M, NT> {
-  uint4 b[kBoxes<16>][NT];
-  // x: tokens; k: first column of the tile
-  __device__ __forceinline__ void fetch(const Tokens<NT> &x, int k, int end) {
-    const int t = threadIdx.x & 3;
-#pragma unroll
-    for (int c = 0; c < kBoxes<16>; ++c)
-#pragma unroll
-      for (int i = 0; i < NT; ++i) b[c][i] = x.get(i, k + 32 * c + 8 * t, end);
-  }
+template <typename T, int M, int NT, bool ROWS8>
+struct Tile<T, 16, 0, M, NT, ROWS8> {
+  Operand<kBoxes<16>, NT, ROWS8> x;
   // some: bit i where eight i has tokens at all
-  __device__ __forceinline__ void multiply(uint32_t place, unsigned some, float (&acc)[M][NT][4]) const {
+  __device__ __forceinline__ void multiply(uint32_t place, uint32_t tokens, unsigned some, float (&acc)[M][NT][4]) const {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const uint32_t at = place + g * 64 + ((t ^ (g >> 1 & 3)) << 4);
 #pragma unroll
-    for (int s = 0; s < M; ++s)
+    for (int c = 0; c < kBoxes<16>; ++c) {
+      uint4 b[NT];
 #pragma unroll
-      for (int c = 0; c < kBoxes<16>; ++c) {
+      for (int i = 0; i < NT; ++i) b[i] = x.get(tokens, c, i);
+#pragma unroll
+      for (int s = 0; s < M; ++s) {
         const uint32_t box = at + (s * kBoxes<16> + c) * kBoxBytes;
         const uint4 lo = lds128(box), hi = lds128(box + 512);
 #pragma unroll
         for (int i = 0; i < NT; ++i)
           if (NT == 1 || some >> i & 1) {
-            mma16816<T, false>(acc[s][i], lo.x, hi.x, lo.y, hi.y, b[c][i].x, b[c][i].y);
-            mma16816<T, false>(acc[s][i], lo.z, hi.z, lo.w, hi.w, b[c][i].z, b[c][i].w);
+            mma16816<T, false>(acc[s][i], lo.x, hi.x, lo.y, hi.y, b[i].x, b[i].y);
+            mma16816<T, false>(acc[s][i], lo.z, hi.z, lo.w, hi.w, b[i].z, b[i].w);
           }
       }
+    }
   }
 };
 
-// A strip's scales and zero points: lane l reads row l & 15 of groups l >> 4, and + 2 (a tile has one, two or four).
-struct Meta {
+// A strip's scales and zero points of a tile.  Lane l reads row l & 15; groups l >> 4 of the tile, and + 2 where it has
+// four; where it has one, lanes from 16 on read that of this warp's next tile, and every other tile reads nothing.
+// They are read one reading ahead of their use.
+struct MetaRow {
   const uint16_t *scales;
   const uint8_t *zeros;
-  int groups;             // of a row
   __device__ __forceinline__ void at(const FewMatrix &m, long long row0, int rows_left) {
-    const int lane = threadIdx.x & 31, row = lane & 15;
+    const int row = threadIdx.x & 15;
     const long long first = (row0 + (row < rows_left ? row : 0)) * m.groups;
     scales = m.scales + first;
     zeros = m.zeros ? m.zeros + first : nullptr;
-    groups = m.groups;
   }
 };
-
-template <typename T, int M, int NT>
-struct Tile<T, 4, M, NT> {
-  uint4 b[4][NT];
-  uint32_t scale[M][2], zero[M][2];
-  __device__ __forceinline__ void fetch(const Tokens<NT> &x, int k, int end) {
-    const int t = threadIdx.x & 3;
+template <int PIECES, int M>
+struct Meta {
+  static constexpr int kGroups = 4 / PIECES, kEach = kGroups == 4 ? 2 : 1;
+  MetaRow row[M];
+  uint32_t now[M][kEach], next[M][kEach];  // scale in the low half, zero point in the high
+  int half, step, groups;                  // half: 16 in the tile that finds its scales read
+  __device__ __forceinline__ void read(int tile) {
+    const int lane = threadIdx.x & 31, g0 = kGroups == 1 ? tile + (lane >> 4) * step : tile * kGroups + (lane >> 4);
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
+    for (int h = 0; h < kEach; ++h) {
+      const int g = min(g0 + 2 * h, groups - 1);
 #pragma unroll
-      for (int i = 0; i < NT; ++i) b[c][i] = x.get(i, k + 32 * c + 8 * t, end);
+      for (int s = 0; s < M; ++s) next[s][h] = row[s].scales[g] | (row[s].zeros ? (row[s].zeros[g] & 15u) << 16 : 0u);
+    }
   }
-  __device__ __forceinline__ void fetch_meta(const Meta (&meta)[M], int k, int shift) {
-    const int lane = threadIdx.x & 31, g0 = (k >> shift) + (lane >> 4), last = meta[0].groups - 1;
+  // from a warp's first tile of a matrix on; its rows are set
+  __device__ __forceinline__ void begin(int tile, int step_, int groups_) {
+    step = step_;
+    groups = groups_;
+    half = 16;
+    read(tile);
+  }
+  __device__ __forceinline__ void advance(int tile) {
+    if constexpr (kGroups == 1) {
+      half ^= 16;
+      if (half) return;
+    }
 #pragma unroll
     for (int s = 0; s < M; ++s)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        if (h == 0 || shift == 5) {
-          const int g = min(g0 + 2 * h, last);
-          scale[s][h] = meta[s].scales[g];
-          zero[s][h] = meta[s].zeros ? meta[s].zeros[g] & 15u : 8u;
-        }
+      for (int h = 0; h < kEach; ++h) now[s][h] = next[s][h];
+    read(tile + (kGroups == 1 ? 2 * step : step));  // (past the end: the last group's again)
   }
-  __device__ __forceinline__ void order() {  // columns as the codes' pairs: 0 and 4, 1 and 5, 2 and 6, 3 and 7
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-#pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        const uint4 v = b[c][i];
-        b[c][i] = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
-                             __byte_perm(v.y, v.w, 0x7632));
-      }
+  // what row g, and g + 8 for eight = 8, of strip s has in group q
+  __device__ __forceinline__ uint32_t get(int s, int q, int eight) const {
+    return __shfl_sync(0xffffffffu, now[s][q / 2 % kEach], (kGroups == 1 ? half : (q & 1) * 16) + ((threadIdx.x & 31) >> 2) + eight);
   }
-  __device__ __forceinline__ void multiply(uint32_t place, unsigned some, float (&acc)[M][NT][4], int shift, bool zeros) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, r = (lane & 7) + (lane & 8), c0 = lane >> 4;
+};
+
+// columns in the order of the codes' pairs: 0 and 4, 1 and 5, 2 and 6, 3 and 7
+__device__ __forceinline__ uint4 in_pairs(const uint4 v) {
+  return make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
+                    __byte_perm(v.y, v.w, 0x7632));
+}
+
+template <typename T, int PIECES, int M, int NT, bool ROWS8>
+struct Tile<T, 4, PIECES, M, NT, ROWS8> {
+  static constexpr int kGroups = 4 / PIECES;
+  Operand<4, NT, ROWS8> x;
+  Meta<PIECES, M> meta;
+  __device__ __forceinline__ void multiply(uint32_t place, uint32_t tokens, unsigned some, float (&acc)[M][NT][4], bool zeros) const {
+    const int lane = threadIdx.x & 31, r = lane & 15, c0 = lane >> 4;
     const T *tag = nullptr;
     const uint32_t at = place + r * 64 + ((c0 ^ (r >> 1 & 3)) << 4);
-    const int per = 1 << (shift - 5);  // pieces of 32 columns in a group
-    order();
+    uint32_t w[M][4];
 #pragma unroll
-    for (int s = 0; s < M; ++s) {
-      uint32_t w[2][4];
-      ldmatrix4(w[0], at + s * kBoxBytes);
-      ldmatrix4(w[1], (at ^ 32) + s * kBoxBytes);
-      Zero<T> z[2] = {zero_of<T>(8u), zero_of<T>(8u)};
-      float part[NT][4];
+    for (int q = 0; q < kGroups; ++q) {
+      float part[M][NT][4];
+      uint32_t m0[M], m1[M];
+      Zero<T> z0[M], z1[M];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int group = c >> (shift - 5);
-        if (zeros && (c & (per - 1)) == 0) {
-          const uint32_t all = group < 2 ? zero[s][0] : zero[s][1];
-          z[0] = zero_of<T>(__shfl_sync(0xffffffffu, all, (group & 1) * 16 + g));
-          z[1] = zero_of<T>(__shfl_sync(0xffffffffu, all, (group & 1) * 16 + g + 8));
-        }
-        uint32_t lo[4], hi[4];
-        widen_codes<T>(w[c >> 1][2 * (c & 1)], z[0], lo);
-        widen_codes<T>(w[c >> 1][2 * (c & 1) + 1], z[1], hi);
-        const bool begins = (c & (per - 1)) == 0;
-        if (begins) {
+      for (int s = 0; s < M; ++s) {
+        m0[s] = meta.get(s, q, 0);
+        m1[s] = meta.get(s, q, 8);
+        z0[s] = zero_of<T>(zeros ? m0[s] >> 16 : 8u);
+        z1[s] = zero_of<T>(zeros ? m1[s] >> 16 : 8u);
+      }
 #pragma unroll
-          for (int i = 0; i < NT; ++i)
-            if (NT == 1 || some >> i & 1) mma16816<T, true>(part[i], lo[0], hi[0], lo[1], hi[1], b[c][i].x, b[c][i].y);
-        } else {
+      for (int j = 0; j < PIECES; ++j) {
+        const int c = q * PIECES + j;
+        uint4 b[NT];
 #pragma unroll
-          for (int i = 0; i < NT; ++i)
-            if (NT == 1 || some >> i & 1) mma16816<T, false>(part[i], lo[0], hi[0], lo[1], hi[1], b[c][i].x, b[c][i].y);
-        }
+        for (int i = 0; i < NT; ++i) b[i] = in_pairs(x.get(tokens, c, i));
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
-          if (NT == 1 || some >> i & 1) mma16816<T, false>(part[i], lo[2], hi[2], lo[3], hi[3], b[c][i].z, b[c][i].w);
-        if ((c & (per - 1)) == per - 1) {  // the group ends: its sums times its scale
-          const uint32_t all = group < 2 ? scale[s][0] : scale[s][1];
-          const float s0 = value16(__shfl_sync(0xffffffffu, all, (group & 1) * 16 + g), tag);
-          const float s1 = value16(__shfl_sync(0xffffffffu, all, (group & 1) * 16 + g + 8), tag);
+        for (int s = 0; s < M; ++s) {
+          if (c == 0) ldmatrix4(w[s], at + s * kBoxBytes);
+          if (c == 2) ldmatrix4(w[s], (at ^ 32) + s * kBoxBytes);
+          uint32_t lo[4], hi[4];
+          widen_codes<T>(w[s][2 * (c & 1)], z0[s], lo);
+          widen_codes<T>(w[s][2 * (c & 1) + 1], z1[s], hi);
 #pragma unroll
           for (int i = 0; i < NT; ++i)
-            if (NT == 1 || some >> i & 1) {
-              acc[s][i][0] = fmaf(part[i][0], s0, acc[s][i][0]);
-              acc[s][i][1] = fmaf(part[i][1], s0, acc[s][i][1]);
-              acc[s][i][2] = fmaf(part[i][2], s1, acc[s][i][2]);
-              acc[s][i][3] = fmaf(part[i][3], s1, acc[s][i][3]);
+            if (NT <= 2 || some >> i & 1) {
+              if (j == 0) mma16816<T, true>(part[s][i], lo[0], hi[0], lo[1], hi[1], b[i].x, b[i].y);
+              else mma16816<T, false>(part[s][i], lo[0], hi[0], lo[1], hi[1], b[i].x, b[i].y);
+              mma16816<T, false>(part[s][i], lo[2], hi[2], lo[3], hi[3], b[i].z, b[i].w);
             }
         }
+      }
+      // the groups' sums times their scales
+#pragma unroll
+      for (int s = 0; s < M; ++s) {
+        const float s0 = value16(m0[s], tag), s1 = value16(m1[s], tag);
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+          if (NT <= 2 || some >> i & 1) {
+            acc[s][i][0] = fmaf(part[s][i][0], s0, acc[s][i][0]);
+            acc[s][i][1] = fmaf(part[s][i][1], s0, acc[s][i][1]);
+            acc[s][i][2] = fmaf(part[s][i][2], s1, acc[s][i][2]);
+            acc[s][i][3] = fmaf(part[s][i][3], s1, acc[s][i][3]);
+          }
       }
     }
   }
@@ -252,118 +278,6 @@ __device__ __forceinline__ int part_at(int row, int token) {
 __device__ __forceinline__ void warps_meet(int first, int count) {  // `count` warps from warp `first` on, a power of two
   if (count == 1) __syncwarp();
   else asm volatile("bar.sync %0, %1;" ::"r"(1 + first / count), "r"(32 * count) : "memory");
-}
-
-// Streams a job's units, one after another, through the CTA's warps.  A unit is rows of the result with all tokens: `segs`
-// matrices of `tiles` tiles, dealt to 2^log_kw warps, whose sums meet in shared memory in the warps' order: the same bits
-// every run.  The CTA's 8 / 2^log_kw sets of warps take neighbouring parts of a unit.  Copies run ahead across units.
-//   M strips, P of them finished together;  int units, segs, tiles
-//   void load_at(unit, set, seg);  void load(place, barrier, tile)       the copies' side, M * kBoxes boxes a place
-//   void use_at(unit, set, seg);   void fetch(tile);  void multiply(place, acc)
-//   void finish(unit, set, strip, thread, threads, sum)                  sum(strip of P, row, token)
-template <int M, int P, int NT, int STAGES, int BOXES, typename Job>
-__device__ __forceinline__ void stream_units(Job &job, char *smem, int log_kw, int *status, uint64_t wait_ns, bool inject) {
-  constexpr int kPlace = BOXES * kBoxBytes;
-  __shared__ uint64_t full[kFewWarps][STAGES];
-  __shared__ uint64_t never;
-  __shared__ int abort_flag;
-  const int warp = threadIdx.x >> 5, kw = 1 << log_kw, set = warp >> log_kw, mine = warp & (kw - 1);
-  char *own = smem + warp * (STAGES * kPlace);
-  float *parts = reinterpret_cast<float *>(smem + kFewWarps * STAGES * kPlace);
-  if (threadIdx.x < kFewWarps * STAGES) mbar_init(&full[0][0] + threadIdx.x, 1);
-  if (threadIdx.x == 0) {
-    mbar_init(&never, 1);
-    abort_flag = 0;
-    fence_mbar_init();
-  }
-  if (threadIdx.x < kFewWarps * STAGES) fence_mbar_init();
-  __syncthreads();
-  // a place in the job's tiles that this warp has come to
-  struct Place {
-    int unit, seg, tile;
-  };
-  auto enter = [&](Place &p) {  // past the end of a matrix: the next one that has a tile for this warp
-    while (p.unit < job.units && p.tile >= job.tiles) {
-      p.tile -= job.tiles;
-      if (++p.seg == job.segs) {
-        p.seg = 0;
-        p.tile = mine;
-        p.unit += gridDim.x;
-        if (mine >= job.segs * job.tiles) p.unit = job.units;
-      }
-    }
-  };
-  Place ahead = {(int)blockIdx.x, 0, mine};
-  if (mine >= job.segs * job.tiles) ahead.unit = job.units;
-  enter(ahead);
-  if (ahead.unit < job.units) job.load_at(ahead.unit, set, ahead.seg);
-  int begun = 0, used = 0;  // copies
-  auto copy_next = [&](int stage) {
-    if (ahead.unit >= job.units) return;
-    if ((threadIdx.x & 31) == 0) mbar_arrive_expect_tx(&full[warp][stage], kPlace);
-    __syncwarp();
-    job.load(own + stage * kPlace, &full[warp][stage], ahead.tile);
-    ++begun;
-    ahead.tile += kw;
-    if (ahead.tile >= job.tiles) {
-      enter(ahead);
-      if (ahead.unit < job.units) job.load_at(ahead.unit, set, ahead.seg);
-    }
-  };
-#pragma unroll
-  for (int s = 0; s < STAGES; ++s) copy_next(s);
-  job.copies_begun();
-  if (inject && blockIdx.x == 0) wait_bounded(&never, 0, &abort_flag, status, wait_ns);  // test hook: a wait that runs out
-  int stage = 0, phase = 0;
-  for (int unit = blockIdx.x; unit < job.units; unit += gridDim.x) {
-    float acc[M][NT][4];
-#pragma unroll
-    for (int m = 0; m < M; ++m)
-#pragma unroll
-      for (int i = 0; i < NT; ++i) acc[m][i][0] = acc[m][i][1] = acc[m][i][2] = acc[m][i][3] = 0.f;
-    int tile = mine;
-    for (int seg = 0; seg < job.segs; ++seg, tile -= job.tiles) {
-      if (tile >= job.tiles) continue;
-      job.use_at(unit, set, seg);
-      for (; tile < job.tiles; tile += kw) {
-        job.fetch(tile);
-        // (the lanes agree: one that gave up takes the warp with it)
-        if (!__all_sync(0xffffffffu, wait_bounded(&full[warp][stage], phase, &abort_flag, status, wait_ns))) continue;
-        job.multiply(smem_u32(own) + stage * kPlace, acc);
-        __syncwarp();
-        ++used;
-        copy_next(stage);
-        if (++stage == STAGES) {
-          stage = 0;
-          phase ^= 1;
-        }
-      }
-    }
-    float *sums = parts + set * kw * (P * NT * kPartFloats);
-#pragma unroll
-    for (int m = 0; m < M; m += P) {
-#pragma unroll
-      for (int q = 0; q < P; ++q)
-#pragma unroll
-        for (int i = 0; i < NT; ++i) put_part(sums + ((mine * P + q) * NT + i) * kPartFloats, acc[m + q][i]);
-      warps_meet(set * kw, kw);
-      job.finish(unit, set, m, threadIdx.x & (32 * kw - 1), 32 * kw, [&](int q, int row, int token) {
-        const float *at = sums + (q * NT + (token >> 3)) * kPartFloats + part_at(row, token & 7);
-        float v = at[0];
-        for (int w = 1; w < kw; ++w) v += at[w * (P * NT * kPartFloats)];
-        return v;
-      });
-      warps_meet(set * kw, kw);
-    }
-  }
-  // after a wait that ran out: no copy may land in memory that the CTA has left
-  for (int nobody = 0; used < begun; ++used) {
-    mbar_wait_bounded(&full[warp][stage], phase, &nobody, status, wait_ns);
-    if (++stage == STAGES) {
-      stage = 0;
-      phase ^= 1;
-    }
-  }
 }
 
 }  // namespace moe

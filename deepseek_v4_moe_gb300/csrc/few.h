@@ -33,8 +33,19 @@ struct Int4MatmulParams {
   long long ld_x, ld_out;
   Waits waits;
 };
-// map: over the codes, boxes of 64 bytes x 16 rows
-cudaError_t launch_int4_matmul(const Int4MatmulParams &p, const CUtensorMap &map, bool f16, int num_sms, cudaStream_t st);
+// w: the codes, boxes of 64 bytes x the rows of a CTA's sets; x: pieces of 32 columns, boxes of those of a step's tiles
+struct Int4Maps {
+  CUtensorMap w, x;
+};
+// strips of 16 rows and eights of tokens of a warp, shares of k (2^log_kw), tokens of a copy of x
+struct Int4Tiles {
+  int strips, eights, log_kw, box_rows;
+  int w_box() const { return 16 * strips * (8 >> log_kw) < 256 ? 16 * strips * (8 >> log_kw) : 256; }  // rows; TMA's most
+  int x_box_pieces() const { return 4 << log_kw; }
+};
+Int4Tiles int4_pick_tiles(int rows, int n, int k, int num_sms);
+cudaError_t launch_int4_matmul(const Int4MatmulParams &p, const Int4Maps &maps, const Int4Tiles &t, bool f16, int num_sms,
+                               cudaStream_t st);
 
 struct Int4WeightParams {
   int n, k, group, type;      // type: of w, or of the widened matrix

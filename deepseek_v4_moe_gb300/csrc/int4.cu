@@ -14,87 +14,160 @@ namespace {
 
 // ---- product ----
 
-template <typename T, int M, int NT>
-struct Int4Job {
-  const Int4MatmulParams &p;
-  const CUtensorMap &map;
-  int units, segs, tiles, sets, row_first, rows;
-  Tokens<NT> x;
-  int row_ahead;
-  Meta meta[M];
-  Tile<T, 4, M, NT> t;
-  __device__ __forceinline__ int row0(int unit, int set) const { return (unit * sets + set) * (16 * M); }
-  __device__ __forceinline__ void copies_begun() const {}
-  __device__ __forceinline__ void load_at(int unit, int set, int) { row_ahead = row0(unit, set); }
-  __device__ __forceinline__ void load(char *place, uint64_t *bar, int tile) const {
-    const int s = threadIdx.x & 31;
-    if (s < M) tma_load_2d(place + s * kBoxBytes, &map, bar, tile * 64, row_ahead + 16 * s);
-  }
-  __device__ __forceinline__ void use_at(int unit, int set, int) {
-    const int r = row0(unit, set);
-#pragma unroll
-    for (int s = 0; s < M; ++s) meta[s].at(p.w, min(r + 16 * s, p.w.n - 1), p.w.n - r - 16 * s);
-  }
-  __device__ __forceinline__ void fetch(int tile) {
-    t.fetch(x, tile * kTileK<4>, p.w.k);
-    t.fetch_meta(meta, tile * kTileK<4>, p.w.group_shift);
-  }
-  __device__ __forceinline__ void multiply(uint32_t place, float (&acc)[M][NT][4]) {
-    t.multiply(place, ~0u, acc, p.w.group_shift, p.w.zeros != nullptr);
-  }
-  template <typename Sum>
-  __device__ __forceinline__ void finish(int unit, int set, int strip, int thread, int threads, Sum sum) const {
-    const int r0 = row0(unit, set) + 16 * strip;
-    for (int i = thread; i < 16 * rows; i += threads) {
-      const int row = i & 15, token = i >> 4;
-      if (r0 + row < p.w.n) static_cast<T *>(p.out)[(row_first + token) * p.ld_out + r0 + row] = from_f32<T>(sum(0, row, token));
-    }
-  }
+// A unit: 128 M / kw rows of the result.  The CTA's 8 warps are kw shares of k for each of 8 / kw sets of 16 M rows; a
+// step of the ring holds a tile of every set and share, and the tokens' columns of every share, so that what comes from
+// the L2 of x serves all sets.  The warp that is last to finish a step lets the copies of a later one into its place.
+// The shares' sums meet in shared memory in their order.
+
+constexpr int kInt4Stages = 8;             // at most
+constexpr size_t kInt4Smem = 112 * 1024;  // two CTAs on an SM
+struct Int4Plan {
+  int log_kw, stages, box_rows;  // box_rows: tokens of a copy
+  int steps, units;
+  int x_bytes, stage_bytes;
 };
 
-constexpr size_t kAlign = 1024;  // of the ring, whose boxes' swizzle goes by the address
-template <int M>
-constexpr int kInt4Stages = M == 4 ? 3 : M == 2 ? 5 : 6;
-
-template <typename T, int M, int NT>
+template <typename T, int PIECES, int M, int NT>
 __global__ void __launch_bounds__(32 * kFewWarps, 2)
-    int4_matmul_kernel(const __grid_constant__ Int4MatmulParams p, const __grid_constant__ CUtensorMap map, int log_kw) {
+    int4_matmul_kernel(const __grid_constant__ Int4MatmulParams p, const __grid_constant__ Int4Maps maps,
+                       const __grid_constant__ Int4Plan plan) {
   extern __shared__ char smem[];
-  const int lane = threadIdx.x & 31, sets = kFewWarps >> log_kw, row_first = (int)blockIdx.y * 8 * NT;
-  Int4Job<T, M, NT> job{p, map, 0, 1, (p.w.k + kTileK<4> - 1) / kTileK<4>, sets, row_first, min(8 * NT, p.rows - row_first)};
-  job.units = (p.w.n + 16 * M * sets - 1) / (16 * M * sets);
-#pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    const int token = 8 * i + (lane >> 2);
-    job.x.row[i] = token < job.rows ? static_cast<const char *>(p.x) + (row_first + token) * p.ld_x * 2 : nullptr;
+  __shared__ uint64_t full[kInt4Stages], never;
+  __shared__ unsigned left[kInt4Stages], fills[kInt4Stages];
+  __shared__ int abort_flag;
+  constexpr int kWeights = kFewWarps * M * kBoxBytes;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int kw = 1 << plan.log_kw, sets = kFewWarps >> plan.log_kw, set = warp >> plan.log_kw, share = warp & (kw - 1);
+  const int row_first = blockIdx.y * 8 * NT, rows = min(8 * NT, p.rows - row_first), set_rows = 16 * M;
+  char *ring = smem + (-smem_u32(smem) & 1023u);
+  float *parts = reinterpret_cast<float *>(ring + plan.stages * plan.stage_bytes);
+  if (threadIdx.x < kInt4Stages) {
+    mbar_init(&full[threadIdx.x], 1);
+    left[threadIdx.x] = fills[threadIdx.x] = 0u;
+    if (threadIdx.x == 0) {
+      mbar_init(&never, 1);
+      abort_flag = 0;
+    }
+    fence_mbar_init();
   }
+  __syncthreads();
   pdl_wait();
-  char *ring = smem + (-smem_u32(smem) & (kAlign - 1));
-  stream_units<M, 1, NT, kInt4Stages<M>, M>(job, ring, log_kw, p.waits.status, p.waits.ns, p.waits.inject);
+  // a step's copies, by one thread
+  auto fill = [&](int stage, int unit, int step) {
+    char *place = ring + stage * plan.stage_bytes;
+    mbar_arrive_expect_tx(&full[stage], kWeights + plan.x_bytes);
+    for (int j = 0; j < kw; ++j)
+      for (int r = 0; r < sets * set_rows; r += 256)  // (a copy's most rows)
+        tma_load_2d(place + (j * sets * set_rows + r) * 64, &maps.w, &full[stage], (step * kw + j) * 64, unit * sets * set_rows + r);
+    tma_load_3d(place + kWeights, &maps.x, &full[stage], 0, row_first, step * kw * 4);
+    fills[stage] += 1;
+  };
+  auto onwards = [&](int &unit, int &step, int by) {
+    for (step += by; step >= plan.steps; step -= plan.steps) unit += gridDim.x;
+  };
+  if (threadIdx.x == 0) {
+    int unit = blockIdx.x, step = 0;
+    for (int s = 0; s < plan.stages && unit < plan.units; ++s, onwards(unit, step, 1)) fill(s, unit, step);
+  }
+  if (p.waits.inject && blockIdx.x == 0) wait_bounded(&never, 0, &abort_flag, p.waits.status, p.waits.ns);  // test hook
+  Tile<T, 4, PIECES, M, NT, (NT > 1)> t;
+  t.x.set(share * 4 * plan.box_rows, plan.box_rows);
+  const uint32_t w_at = smem_u32(ring) + (share * sets + set) * M * kBoxBytes, x_at = smem_u32(ring) + kWeights;
+  int stage = 0, phase = 0;
+  for (int unit = blockIdx.x; unit < plan.units; unit += gridDim.x) {
+    const int row0 = (unit * sets + set) * set_rows;
+#pragma unroll
+    for (int s = 0; s < M; ++s) t.meta.row[s].at(p.w, min(row0 + 16 * s, p.w.n - 1), p.w.n - row0 - 16 * s);
+    t.meta.begin(share, kw, p.w.groups);
+    float acc[M][NT][4];
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+      for (int i = 0; i < NT; ++i) acc[m][i][0] = acc[m][i][1] = acc[m][i][2] = acc[m][i][3] = 0.f;
+    for (int step = 0; step < plan.steps; ++step) {
+      t.meta.advance(step * kw + share);
+      // (the lanes agree: one that gave up takes the warp with it)
+      if (!__all_sync(0xffffffffu, wait_bounded(&full[stage], phase, &abort_flag, p.waits.status, p.waits.ns))) break;
+      t.multiply(w_at + stage * plan.stage_bytes, x_at + stage * plan.stage_bytes, ~0u, acc, p.w.zeros != nullptr);
+      __syncwarp();
+      if (lane == 0) {
+        unsigned before;
+        asm volatile("atom.acq_rel.cta.shared::cta.inc.u32 %0, [%1], %2;"
+                     : "=r"(before)
+                     : "r"(smem_u32(&left[stage])), "r"(kFewWarps - 1u)
+                     : "memory");
+        if (before == kFewWarps - 1) {
+          int u = unit, s = step;
+          onwards(u, s, plan.stages);
+          if (u < plan.units) fill(stage, u, s);
+        }
+      }
+      if (++stage == plan.stages) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+    float *sums = parts + set * kw * (NT * kPartFloats);
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+#pragma unroll
+      for (int i = 0; i < NT; ++i) put_part(sums + (share * NT + i) * kPartFloats, acc[m][i]);
+      warps_meet(set * kw, kw);
+      const int r0 = row0 + 16 * m;
+      for (int i = threadIdx.x & (32 * kw - 1); i < 16 * rows; i += 32 * kw) {
+        const int row = i & 15, token = i >> 4;
+        if (r0 + row >= p.w.n) continue;
+        const float *at = sums + (token >> 3) * kPartFloats + part_at(row, token & 7);
+        float v = at[0];
+        for (int w = 1; w < kw; ++w) v += at[w * (NT * kPartFloats)];
+        static_cast<T *>(p.out)[(row_first + token) * p.ld_out + r0 + row] = from_f32<T>(v);
+      }
+      warps_meet(set * kw, kw);
+    }
+  }
+  // after a wait that ran out: no copy may land in memory that the CTA has left
+  __syncthreads();
+  if (abort_flag && threadIdx.x == 0)
+    for (int s = 0, nobody = 0; s < plan.stages; ++s)
+      if (fills[s]) mbar_wait_bounded(&full[s], (fills[s] - 1) & 1, &nobody, p.waits.status, p.waits.ns);
 }
 
-template <typename T, int M, int NT>
-cudaError_t int4_launch(const Int4MatmulParams &p, const CUtensorMap &map, int num_sms, cudaStream_t st) {
-  constexpr size_t smem = kFewWarps * (kInt4Stages<M> * M * kBoxBytes + NT * kPartFloats * sizeof(float)) + kAlign;
+template <typename T, int PIECES, int M, int NT>
+cudaError_t int4_launch(const Int4MatmulParams &p, const Int4Maps &maps, const Int4Plan &plan, int y, int num_sms, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
-  const cudaError_t e = allow_smem((const void *)int4_matmul_kernel<T, M, NT>, smem, done);
+  const cudaError_t e = allow_smem((const void *)int4_matmul_kernel<T, PIECES, M, NT>, kInt4Smem, done);
   if (e != cudaSuccess) return e;
-  const int tiles = (p.w.k + kTileK<4> - 1) / kTileK<4>, strips = (p.w.n + 16 * M - 1) / (16 * M);
-  // warps that share a strip: as many as there are tiles, unless the strips alone keep every warp busy
-  int log_kw = 0;
-  while (log_kw < 3 && (2 << log_kw) <= tiles && (strips << log_kw) < 4 * kFewWarps * num_sms) ++log_kw;
-  const int units = (strips + (kFewWarps >> log_kw) - 1) / (kFewWarps >> log_kw);
-  const int y = (p.rows + 8 * NT - 1) / (8 * NT), most = 2 * num_sms;
-  return launch_pdl(int4_matmul_kernel<T, M, NT>, dim3(units < most ? units : most, y), dim3(32 * kFewWarps), smem, st, p, map, log_kw);
+  const size_t smem = plan.stages * (size_t)plan.stage_bytes + kFewWarps * NT * kPartFloats * sizeof(float) + 1024;
+  const int most = 2 * num_sms / y > 1 ? 2 * num_sms / y : 1;
+  return launch_pdl(int4_matmul_kernel<T, PIECES, M, NT>, dim3(plan.units < most ? plan.units : most, y), dim3(32 * kFewWarps), smem,
+                    st, p, maps, plan);
 }
 
-template <typename T>
-cudaError_t int4_typed(const Int4MatmulParams &p, const CUtensorMap &map, int num_sms, cudaStream_t st) {
-  // several strips a warp share what is read of x, where there are enough of them
-  const bool many = p.w.n >= 64 * num_sms, some = p.w.n >= 32 * num_sms;
-  if (p.rows <= 8) return many ? int4_launch<T, 4, 1>(p, map, num_sms, st) : some ? int4_launch<T, 2, 1>(p, map, num_sms, st) : int4_launch<T, 1, 1>(p, map, num_sms, st);
-  if (p.rows <= 16) return many ? int4_launch<T, 4, 2>(p, map, num_sms, st) : some ? int4_launch<T, 2, 2>(p, map, num_sms, st) : int4_launch<T, 1, 2>(p, map, num_sms, st);
-  return some ? int4_launch<T, 2, 4>(p, map, num_sms, st) : int4_launch<T, 1, 4>(p, map, num_sms, st);
+template <typename T, int PIECES>
+cudaError_t int4_tiles(const Int4MatmulParams &p, const Int4Maps &maps, const Int4Tiles &t, int num_sms, cudaStream_t st) {
+  Int4Plan plan;
+  const int tiles = (p.w.k + kTileK<4> - 1) / kTileK<4>, set_rows = 16 * t.strips, sets = kFewWarps >> t.log_kw;
+  plan.log_kw = t.log_kw;
+  plan.box_rows = t.box_rows;
+  plan.steps = (tiles + (1 << t.log_kw) - 1) >> t.log_kw;
+  plan.units = (p.w.n + sets * set_rows - 1) / (sets * set_rows);
+  plan.x_bytes = (4 << t.log_kw) * t.box_rows * 64;
+  plan.stage_bytes = (kFewWarps * t.strips * kBoxBytes + plan.x_bytes + 1023) / 1024 * 1024;
+  const int room = (int)kInt4Smem - 1024 - kFewWarps * t.eights * kPartFloats * 4;
+  plan.stages = room / plan.stage_bytes < kInt4Stages ? room / plan.stage_bytes : kInt4Stages;
+  const int y = (p.rows + 8 * t.eights - 1) / (8 * t.eights);
+#define MOE_INT4(M, NT) \
+  if (t.strips == M && t.eights == NT) return int4_launch<T, PIECES, M, NT>(p, maps, plan, y, num_sms, st)
+  MOE_INT4(1, 1);
+  MOE_INT4(2, 1);
+  MOE_INT4(4, 1);
+  MOE_INT4(1, 2);
+  MOE_INT4(2, 2);
+  MOE_INT4(4, 2);
+  MOE_INT4(1, 4);
+  MOE_INT4(2, 4);
+#undef MOE_INT4
+  return cudaErrorInvalidValue;
 }
 
 // ---- making and widening weights ----
@@ -181,8 +254,30 @@ cudaError_t quantise_launch(const Int4WeightParams &p, int num_sms, cudaStream_t
 
 }  // namespace
 
-cudaError_t launch_int4_matmul(const Int4MatmulParams &p, const CUtensorMap &map, bool f16, int num_sms, cudaStream_t st) {
-  return f16 ? int4_typed<__half>(p, map, num_sms, st) : int4_typed<__nv_bfloat16>(p, map, num_sms, st);
+// Strips: as many to a warp as the matrix's rows can spare (they share what is read of x).  Shares of k: as many as k has
+// tiles, unless sets of rows alone keep every warp of the GPU busy.
+Int4Tiles int4_pick_tiles(int rows, int n, int k, int num_sms) {
+  Int4Tiles t;
+  t.eights = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+  t.strips = t.eights <= 2 && n >= 64 * num_sms ? 4 : t.eights == 4 && n >= 32 * num_sms ? 2 : 1;
+  const int tiles = (k + kTileK<4> - 1) / kTileK<4>, strips = (n + 16 * t.strips - 1) / (16 * t.strips);
+  t.log_kw = 0;
+  const int most = t.eights == 1 ? 3 : t.eights == 2 ? 2 : 1;  // each share has its own columns of x in a step
+  while (t.log_kw < most && (2 << t.log_kw) <= tiles && (strips << t.log_kw) < 2 * kFewWarps * num_sms) ++t.log_kw;
+  t.box_rows = t.eights > 1 ? 8 * t.eights : rows <= 1 ? 1 : rows <= 2 ? 2 : rows <= 4 ? 4 : 8;
+  return t;
+}
+
+template <typename T>
+cudaError_t launch_int4_typed(const Int4MatmulParams &p, const Int4Maps &maps, const Int4Tiles &t, int num_sms, cudaStream_t st) {
+  if (p.w.group_shift == 5) return int4_tiles<T, 1>(p, maps, t, num_sms, st);
+  if (p.w.group_shift == 6) return int4_tiles<T, 2>(p, maps, t, num_sms, st);
+  return int4_tiles<T, 4>(p, maps, t, num_sms, st);
+}
+
+cudaError_t launch_int4_matmul(const Int4MatmulParams &p, const Int4Maps &maps, const Int4Tiles &t, bool f16, int num_sms,
+                               cudaStream_t st) {
+  return f16 ? launch_int4_typed<__half>(p, maps, t, num_sms, st) : launch_int4_typed<__nv_bfloat16>(p, maps, t, num_sms, st);
 }
 
 cudaError_t launch_int4_quantise(const Int4WeightParams &p, int num_sms, cudaStream_t st) {

@@ -66,13 +66,19 @@ __global__ void __launch_bounds__(256) routed_logits_kernel(const __grid_constan
 
 // ---- choice ----
 
-constexpr int kGroupsMax = kRoutedRows * kRoutedTopK + kRoutedShared;
+// The experts' tokens, eight at a time, which are the columns of the tensor cores' right operand.  Gate and up take any
+// eight tokens of an expert together; down takes tokens 8 j .. 8 j + 7 for every expert, so that its accumulators may add
+// all experts' products.  An expert with more tokens, or tokens of several eights, comes several times, one after
+// another: its weights then come from the L2.  Shared experts have the numbers from `experts` on, and come last.
+constexpr int kEightsMax = kRoutedRows / 8, kUpMax = kRoutedRows * kRoutedTopK + kRoutedShared * kEightsMax;
+constexpr int kDownMax = 8 * kRoutedTopK + kRoutedShared;
 
 struct Choice {
-  int groups, routed;                              // experts with tokens, the shared ones last
+  int up, down[kEightsMax];                        // entries
   uint32_t mask[kRoutedExperts];                   // each expert's tokens
-  uint32_t group_mask[kGroupsMax];
-  uint16_t expert[kGroupsMax];
+  uint32_t up_mask[kUpMax];
+  uint16_t up_expert[kUpMax];
+  uint16_t down_expert[kEightsMax][kDownMax];
   uint16_t index[kRoutedRows][kRoutedTopK];
   float weight[kRoutedRows][kRoutedTopK];
 };
@@ -171,181 +177,348 @@ __device__ __forceinline__ void choose(const RoutedParams &p, Choice &c, bool wr
   }
   __syncthreads();
   if (warp == 0) {
-    int n = 0;
-    for (int e0 = 0; e0 < p.experts; e0 += 32) {
-      const uint32_t mask = e0 + lane < p.experts ? c.mask[e0 + lane] : 0u;
-      const uint32_t has = __ballot_sync(0xffffffffu, mask != 0u);
-      if (mask) {
-        const int at = n + __popc(has & ((1u << lane) - 1u));
-        c.expert[at] = (uint16_t)(e0 + lane);
-        c.group_mask[at] = mask;
+    const int all = p.experts + p.shared;
+    int up = 0, down[kEightsMax] = {};
+    for (int e0 = 0; e0 < all; e0 += 32) {
+      const int e = e0 + lane;
+      uint32_t mask = e < p.experts ? c.mask[e] : e < all ? 0xFFFFFFFFu >> (32 - p.rows) : 0u;
+#pragma unroll
+      for (int j = 0; j < kEightsMax; ++j) {
+        const uint32_t has = __ballot_sync(0xffffffffu, mask >> (8 * j) & 255u);
+        if (mask >> (8 * j) & 255u) c.down_expert[j][down[j] + __popc(has & ((1u << lane) - 1u))] = (uint16_t)e;
+        down[j] += __popc(has);
       }
-      n += __popc(has);
-    }
-    if (lane < p.shared) {
-      c.expert[n + lane] = (uint16_t)lane;
-      c.group_mask[n + lane] = 0xFFFFFFFFu >> (32 - p.rows);
+      const int passes = (__popc(mask) + 7) / 8;
+      int at = passes;  // the entries of the lanes up to this one
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, at, o);
+        if (lane >= o) at += v;
+      }
+      const int added = __shfl_sync(0xffffffffu, at, 31);
+      at += up - passes;
+      up += added;
+      for (; mask; ++at) {  // eight tokens at a time
+        uint32_t rest = mask;
+        for (int i = 0; i < 8 && rest; ++i) rest &= rest - 1u;
+        c.up_expert[at] = (uint16_t)e;
+        c.up_mask[at] = mask ^ rest;
+        mask = rest;
+      }
     }
     if (lane == 0) {
-      c.routed = n;
-      c.groups = n + p.shared;
+      c.up = up;
+#pragma unroll
+      for (int j = 0; j < kEightsMax; ++j) c.down[j] = down[j];
     }
   }
   __syncthreads();
 }
 
-// the place of a group among a token's, which has chosen it: that of its row of h
-__device__ __forceinline__ int slot_of(const RoutedParams &p, const Choice &c, int group, int token) {
-  const int e = c.expert[group];
-  if (group >= c.routed) return p.top_k + e;
+// the place of expert e among token's, which has chosen it: that of its row of h
+__device__ __forceinline__ int slot_of(const RoutedParams &p, const Choice &c, int e, int token) {
+  if (e >= p.experts) return p.top_k + e - p.experts;
   int slot = 0;
   for (int s = 1; s < p.top_k; ++s)
     if (c.index[token][s] == e) slot = s;
   return slot;
 }
-
-// ---- gate and up ----
-
-constexpr size_t kAlign = 1024;  // of the ring, whose boxes' swizzle goes by the address
-
+__device__ __forceinline__ uint16_t *h_row(const RoutedParams &p, const Choice &c, int e, int token) {
+  return p.h + ((long long)token * (p.top_k + p.shared) + slot_of(p, c, e, token)) * p.inter;
+}
 // the n-th token of a mask, or -1
 __device__ __forceinline__ int token_at(uint32_t mask, int n) {
   for (; n > 0 && mask; --n) mask &= mask - 1u;
   return __ffs(mask) - 1;
 }
 
-// A unit: 16 rows of a group's gate and up matrices.  Column j of the right operand is the group's j-th token.
-template <typename T, int BITS, int NT>
+// ---- the weights' way through a warp ----
+//
+// A unit is 16 rows of the result; its `segs` matrices of `tiles` tiles each are dealt to the CTA's 8 warps, whose sums
+// meet in shared memory in the warps' order.  Each warp has a ring of its own, filled across units: a place holds a tile of
+// M strips, brought by TMA, and the tokens' columns, brought by the lanes (cp.async), of which there may be few.  Both
+// arrive on one barrier, and no barrier of several warps is met before a unit ends.
+
+// place: M strips, then the tokens' columns
+template <int BITS, int M>
+struct Place {
+  static constexpr int kWeights = M * kBoxes<BITS> * kBoxBytes, kPieces = BITS == 16 ? 2 : 4, kTokens = kPieces * 8 * 64;
+  static constexpr int kBytes = kWeights + kTokens;
+};
+
+// Copies a lane's part of the tokens' columns: row g's 16 bytes t of each piece; zeros where there are none.
+template <int PIECES>
+__device__ __forceinline__ void copy_tokens(uint32_t dst, const uint16_t *row, const void *any, int k, int end) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int c = 0; c < PIECES; ++c) {
+    const int col = k + 32 * c + 8 * t, line = 8 * c + g;
+    const bool in = row && col < end;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst + line * 64 + ((t ^ (line >> 1 & 3)) << 4)),
+                 "l"(in ? static_cast<const void *>(row + col) : any), "r"(in ? 16 : 0)
+                 : "memory");
+  }
+}
+
+//   int units, tiles, k;  int segs(unit)
+//   void weights_at(unit, seg);  void weights(place, barrier, tile)      by one lane
+//   void tokens_at(unit, seg)    sets `row`, the lane's token
+//   void use_at(unit, seg);  void multiply(place, tile, acc);  void finish(unit, thread, sum)
+template <int BITS, int M, int STAGES, typename Job>
+__device__ __forceinline__ void stream_units(Job &job, char *smem, const Waits &waits) {
+  using P = Place<BITS, M>;
+  constexpr int kw = kFewWarps;
+  __shared__ uint64_t full[kFewWarps][STAGES], never;
+  __shared__ int abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  char *own = smem + warp * (STAGES * P::kBytes);
+  float *parts = reinterpret_cast<float *>(smem + kw * STAGES * P::kBytes);
+  if (threadIdx.x < kw * STAGES) mbar_init(&full[0][0] + threadIdx.x, 1 + 32);
+  if (threadIdx.x == 0) {
+    mbar_init(&never, 1);
+    abort_flag = 0;
+  }
+  if (threadIdx.x < kw * STAGES) fence_mbar_init();
+  __syncthreads();
+  // a place in the job's tiles that this warp has come to
+  struct At {
+    int unit, seg, tile, segs;
+  };
+  auto settle = [&](At &a) {  // past the end of a matrix: the next one that has a tile for this warp
+    while (a.unit < job.units && a.tile >= job.tiles) {
+      a.tile -= job.tiles;
+      if (++a.seg >= a.segs) {
+        a.unit += gridDim.x;
+        a.seg = 0;
+        a.tile = warp;
+        if (a.unit < job.units) a.segs = job.segs(a.unit);
+      }
+    }
+  };
+  auto start = [&] {
+    At a = {(int)blockIdx.x, 0, warp, 0};
+    if (a.unit < job.units) a.segs = job.segs(a.unit);
+    settle(a);
+    return a;
+  };
+  auto weights = [&](At &a, int stage) {
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&full[warp][stage], P::kWeights);
+      job.weights(own + stage * P::kBytes, &full[warp][stage], a.tile);
+    }
+  };
+  auto tokens = [&](At &a, int stage) {
+    copy_tokens<P::kPieces>(smem_u32(own) + stage * P::kBytes + P::kWeights, job.row, job.p.x, a.tile * kTileK<BITS>, job.k);
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&full[warp][stage])) : "memory");
+  };
+  int begun = 0, used = 0;
+  // the first weights need not wait for what makes the tokens' columns
+  At ahead = start();
+  if (ahead.unit < job.units) job.weights_at(ahead.unit, ahead.seg);
+  for (int s = 0; s < STAGES && ahead.unit < job.units; ++s) {
+    weights(ahead, s);
+    ahead.tile += kw;
+    if (ahead.tile >= job.tiles) {
+      settle(ahead);
+      if (ahead.unit < job.units) job.weights_at(ahead.unit, ahead.seg);
+    }
+  }
+  job.tokens_ready();
+  ahead = start();
+  if (ahead.unit < job.units) job.tokens_at(ahead.unit, ahead.seg);
+  for (; begun < STAGES && ahead.unit < job.units; ++begun) {
+    tokens(ahead, begun);
+    ahead.tile += kw;
+    if (ahead.tile >= job.tiles) {
+      settle(ahead);
+      if (ahead.unit < job.units) job.tokens_at(ahead.unit, ahead.seg);
+    }
+  }
+  if (waits.inject && blockIdx.x == 0) wait_bounded(&never, 0, &abort_flag, waits.status, waits.ns);  // test hook: a wait that runs out
+  int stage = 0, phase = 0;
+  for (int unit = blockIdx.x; unit < job.units; unit += gridDim.x) {
+    float acc[M][1][4];
+#pragma unroll
+    for (int m = 0; m < M; ++m) acc[m][0][0] = acc[m][0][1] = acc[m][0][2] = acc[m][0][3] = 0.f;
+    const int segs = job.segs(unit);
+    int tile = warp;
+    for (int seg = 0; seg < segs; ++seg, tile -= job.tiles) {
+      if (tile >= job.tiles) continue;
+      job.use_at(unit, seg, tile);
+      for (; tile < job.tiles; tile += kw) {
+        job.meta_at(tile);
+        // (the lanes agree: one that gave up takes the warp with it)
+        if (!__all_sync(0xffffffffu, wait_bounded(&full[warp][stage], phase, &abort_flag, waits.status, waits.ns))) continue;
+        const uint32_t place = smem_u32(own) + stage * P::kBytes;
+        job.multiply(place, place + P::kWeights, acc);
+        __syncwarp();
+        ++used;
+        if (ahead.unit < job.units) {
+          weights(ahead, stage);
+          tokens(ahead, stage);
+          ++begun;
+          ahead.tile += kw;
+          if (ahead.tile >= job.tiles) {
+            settle(ahead);
+            if (ahead.unit < job.units) {
+              job.weights_at(ahead.unit, ahead.seg);
+              job.tokens_at(ahead.unit, ahead.seg);
+            }
+          }
+        }
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < M; ++m) put_part(parts + (warp * M + m) * kPartFloats, acc[m][0]);
+    __syncthreads();
+    if (threadIdx.x < 128)
+      job.finish(unit, threadIdx.x & 15, threadIdx.x >> 4, [&](int m) {
+        const float *at = parts + m * kPartFloats + part_at(threadIdx.x & 15, threadIdx.x >> 4);
+        float v = at[0];
+#pragma unroll
+        for (int w = 1; w < kw; ++w) v += at[w * M * kPartFloats];
+        return v;
+      });
+    __syncthreads();
+  }
+  // after a wait that ran out: no copy may land in memory that the CTA has left
+  for (int nobody = 0; used < begun; ++used) {
+    mbar_wait_bounded(&full[warp][stage], phase, &nobody, waits.status, waits.ns);
+    if (++stage == STAGES) {
+      stage = 0;
+      phase ^= 1;
+    }
+  }
+}
+
+// ---- gate and up ----
+
+constexpr size_t kAlign = 512;  // of the ring, whose boxes' swizzle goes by the address
+
+// A unit: 16 rows of an entry's gate and up matrices.
+template <typename T, int BITS, int PIECES>
 struct UpJob {
   const RoutedParams &p;
   const RoutedMaps &maps;
   const Choice &c;
-  int units, segs, tiles, strips;
-  int row_ahead;
+  int units, tiles, k, strips;
+  int map_row;
   bool shared_ahead;
-  unsigned some;
-  Tokens<NT> x;
-  Meta meta[2];
-  Tile<T, BITS, 2, NT> t;
-  __device__ __forceinline__ void copies_begun() const {}
-  __device__ __forceinline__ void load_at(int unit, int, int) {
-    const int group = unit / strips;
-    row_ahead = c.expert[group] * p.inter + (unit - group * strips) * 16;
-    shared_ahead = group >= c.routed;
+  const uint16_t *row;
+  Tile<T, BITS, PIECES, 2, 1, false> t;
+  __device__ __forceinline__ int segs(int) const { return 1; }
+  __device__ __forceinline__ void weights_at(int unit, int) {
+    const int entry = unit / strips, e = c.up_expert[entry];
+    shared_ahead = e >= p.experts;
+    map_row = (shared_ahead ? e - p.experts : e) * p.inter + (unit - entry * strips) * 16;
   }
-  __device__ __forceinline__ void load(char *place, uint64_t *bar, int tile) const {
-    const int i = threadIdx.x & 31, box = i % kBoxes<BITS>;
-    if (i >= 2 * kBoxes<BITS>) return;
+  __device__ __forceinline__ void weights(char *place, uint64_t *bar, int tile) const {
     const CUtensorMap *gate = shared_ahead ? &maps.s_gate : &maps.gate, *up = shared_ahead ? &maps.s_up : &maps.up;
-    tma_load_2d(place + i * kBoxBytes, i < kBoxes<BITS> ? gate : up, bar, (tile * kBoxes<BITS> + box) * (BITS == 16 ? 32 : 64), row_ahead);
-  }
-  __device__ __forceinline__ void use_at(int unit, int, int) {
-    const int group = unit / strips, r = (unit - group * strips) * 16, e = c.expert[group], lane = threadIdx.x & 31;
-    const uint32_t mask = c.group_mask[group];
-    some = 0;
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const int token = token_at(mask, 8 * i + (lane >> 2));
-      x.row[i] = token >= 0 ? static_cast<const char *>(p.x) + token * p.ld_x * 2 : nullptr;
-      some |= (__popc(mask) > 8 * i ? 1u : 0u) << i;
+    for (int b = 0; b < kBoxes<BITS>; ++b) {
+      const int x = (tile * kBoxes<BITS> + b) * (BITS == 16 ? 32 : 64);
+      tma_load_2d(place + b * kBoxBytes, gate, bar, x, map_row);
+      tma_load_2d(place + (kBoxes<BITS> + b) * kBoxBytes, up, bar, x, map_row);
     }
+  }
+  __device__ __forceinline__ void tokens_ready() const {}
+  __device__ __forceinline__ void tokens_at(int unit, int) {
+    const int token = token_at(c.up_mask[unit / strips], (threadIdx.x & 31) >> 2);
+    row = token >= 0 ? static_cast<const uint16_t *>(p.x) + token * p.ld_x : nullptr;
+  }
+  __device__ __forceinline__ void use_at(int unit, int, int tile) {
     if constexpr (BITS == 4) {
-      const bool sh = group >= c.routed;
-      const long long row = (long long)e * p.inter + r;
-      meta[0].at(sh ? p.s_gate : p.gate, row, p.inter - r);
-      meta[1].at(sh ? p.s_up : p.up, row, p.inter - r);
+      const int entry = unit / strips, r = (unit - entry * strips) * 16, e = c.up_expert[entry];
+      const bool sh = e >= p.experts;
+      const long long first = (long long)(sh ? e - p.experts : e) * p.inter + r;
+      t.meta.row[0].at(sh ? p.s_gate : p.gate, first, p.inter - r);
+      t.meta.row[1].at(sh ? p.s_up : p.up, first, p.inter - r);
+      t.meta.begin(tile, kFewWarps, p.gate.groups);
     }
   }
-  __device__ __forceinline__ void fetch(int tile) {
-    t.fetch(x, tile * kTileK<BITS>, p.hidden);
-    if constexpr (BITS == 4) t.fetch_meta(meta, tile * kTileK<BITS>, p.gate.group_shift);
+  __device__ __forceinline__ void meta_at(int tile) {
+    if constexpr (BITS == 4) t.meta.advance(tile);
   }
-  __device__ __forceinline__ void multiply(uint32_t place, float (&acc)[2][NT][4]) {
-    if constexpr (BITS == 4) t.multiply(place, some, acc, p.gate.group_shift, p.gate.zeros || p.up.zeros);
-    else t.multiply(place, some, acc);
+  __device__ __forceinline__ void multiply(uint32_t place, uint32_t tokens, float (&acc)[2][1][4]) {
+    if constexpr (BITS == 4) t.multiply(place, tokens, 1u, acc, p.gate.zeros || p.up.zeros);
+    else t.multiply(place, tokens, 1u, acc);
   }
   template <typename Sum>
-  __device__ __forceinline__ void finish(int unit, int, int, int thread, int threads, Sum sum) const {
-    const int group = unit / strips, r = (unit - group * strips) * 16;
-    const uint32_t mask = c.group_mask[group];
-    const int count = __popc(mask);
-    for (int i = thread; i < 16 * count; i += threads) {
-      const int row = i & 15, column = i >> 4, token = token_at(mask, column);
-      if (r + row >= p.inter) continue;
-      const int slot = slot_of(p, c, group, token);
-      const float w = group < c.routed ? c.weight[token][slot] : 1.f;
-      // rounded to 16 bits as the tensor cores' operand, as the gated block does
-      const T h = from_f32<T>(act_value(p.act, sum(0, row, column)) * sum(1, row, column) * w);
-      p.h[((long long)token * (p.top_k + p.shared) + slot) * p.inter + r + row] = *reinterpret_cast<const uint16_t *>(&h);
-    }
+  __device__ __forceinline__ void finish(int unit, int r, int column, Sum sum) const {
+    const int entry = unit / strips, at = (unit - entry * strips) * 16 + r, e = c.up_expert[entry];
+    const int token = token_at(c.up_mask[entry], column);
+    if (token < 0 || at >= p.inter) return;
+    const float w = e < p.experts ? c.weight[token][slot_of(p, c, e, token)] : 1.f;
+    // rounded to 16 bits as the tensor cores' operand, as the gated block does
+    const T h = from_f32<T>(act_value(p.act, sum(0)) * sum(1) * w);
+    h_row(p, c, e, token)[at] = *reinterpret_cast<const uint16_t *>(&h);
   }
 };
 
 // ---- down ----
 
-// A unit: 16 rows of every group's matrix.  Column j of the right operand is token j for every group.
-template <typename T, int BITS, int NT>
+// A unit: 16 rows of every expert's matrix that one of eight tokens has chosen.
+template <typename T, int BITS, int PIECES>
 struct DownJob {
   const RoutedParams &p;
   const RoutedDownMaps &maps;
   const Choice &c;
-  int units, segs, tiles;
-  int row_ahead;
+  int units, tiles, k, eights;
+  int map_row;
   bool shared_ahead;
-  unsigned some;
-  Tokens<NT> x;
-  Meta meta[1];
-  Tile<T, BITS, 1, NT> t;
-  __device__ __forceinline__ void copies_begun() const { pdl_wait(); }  // h comes from the kernel before
-  __device__ __forceinline__ void load_at(int unit, int, int group) {
-    row_ahead = c.expert[group] * p.hidden + unit * 16;
-    shared_ahead = group >= c.routed;
+  const uint16_t *row;
+  Tile<T, BITS, PIECES, 1, 1, false> t;
+  __device__ __forceinline__ int segs(int unit) const { return c.down[unit % eights]; }
+  __device__ __forceinline__ void weights_at(int unit, int seg) {
+    const int e = c.down_expert[unit % eights][seg];
+    shared_ahead = e >= p.experts;
+    map_row = (shared_ahead ? e - p.experts : e) * p.hidden + unit / eights * 16;
   }
-  __device__ __forceinline__ void load(char *place, uint64_t *bar, int tile) const {
-    const int i = threadIdx.x & 31;
-    if (i < kBoxes<BITS>)
-      tma_load_2d(place + i * kBoxBytes, shared_ahead ? &maps.s_down : &maps.down, bar,
-                  (tile * kBoxes<BITS> + i) * (BITS == 16 ? 32 : 64), row_ahead);
-  }
-  __device__ __forceinline__ void use_at(int unit, int, int group) {
-    const int e = c.expert[group], lane = threadIdx.x & 31;
-    const uint32_t mask = c.group_mask[group];
-    some = 0;
+  __device__ __forceinline__ void weights(char *place, uint64_t *bar, int tile) const {
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const int token = 8 * i + (lane >> 2);
-      x.row[i] = nullptr;
-      if (mask >> token & 1)
-        x.row[i] = reinterpret_cast<const char *>(
-            p.h + ((long long)token * (p.top_k + p.shared) + slot_of(p, c, group, token)) * p.inter);
-      some |= (mask >> (8 * i) & 255u ? 1u : 0u) << i;
+    for (int b = 0; b < kBoxes<BITS>; ++b)
+      tma_load_2d(place + b * kBoxBytes, shared_ahead ? &maps.s_down : &maps.down, bar, (tile * kBoxes<BITS> + b) * (BITS == 16 ? 32 : 64),
+                  map_row);
+  }
+  __device__ __forceinline__ void tokens_ready() const { pdl_wait(); }  // h comes from the kernel before
+  __device__ __forceinline__ void tokens_at(int unit, int seg) {
+    const int eight = unit % eights, e = c.down_expert[eight][seg], token = 8 * eight + ((threadIdx.x & 31) >> 2);
+    const uint32_t mask = e >= p.experts ? 0xFFFFFFFFu >> (32 - p.rows) : c.mask[e];
+    row = mask >> token & 1 ? h_row(p, c, e, token) : nullptr;
+  }
+  __device__ __forceinline__ void use_at(int unit, int seg, int tile) {
+    if constexpr (BITS == 4) {
+      const int e = c.down_expert[unit % eights][seg], r = unit / eights * 16;
+      const bool sh = e >= p.experts;
+      t.meta.row[0].at(sh ? p.s_down : p.down, (long long)(sh ? e - p.experts : e) * p.hidden + r, p.hidden - r);
+      t.meta.begin(tile, kFewWarps, p.down.groups);
     }
-    if constexpr (BITS == 4) meta[0].at(group >= c.routed ? p.s_down : p.down, (long long)e * p.hidden + unit * 16, p.hidden - unit * 16);
   }
-  __device__ __forceinline__ void fetch(int tile) {
-    t.fetch(x, tile * kTileK<BITS>, p.inter);
-    if constexpr (BITS == 4) t.fetch_meta(meta, tile * kTileK<BITS>, p.down.group_shift);
+  __device__ __forceinline__ void meta_at(int tile) {
+    if constexpr (BITS == 4) t.meta.advance(tile);
   }
-  __device__ __forceinline__ void multiply(uint32_t place, float (&acc)[1][NT][4]) {
-    if constexpr (BITS == 4) t.multiply(place, some, acc, p.down.group_shift, p.down.zeros != nullptr);
-    else t.multiply(place, some, acc);
+  __device__ __forceinline__ void multiply(uint32_t place, uint32_t tokens, float (&acc)[1][1][4]) {
+    if constexpr (BITS == 4) t.multiply(place, tokens, 1u, acc, p.down.zeros != nullptr);
+    else t.multiply(place, tokens, 1u, acc);
   }
   template <typename Sum>
-  __device__ __forceinline__ void finish(int unit, int, int, int thread, int threads, Sum sum) const {
-    for (int i = thread; i < 16 * p.rows; i += threads) {
-      const int row = i & 15, token = i >> 4;
-      if (unit * 16 + row < p.hidden) static_cast<T *>(p.y)[token * p.ld_y + unit * 16 + row] = from_f32<T>(sum(0, row, token));
-    }
+  __device__ __forceinline__ void finish(int unit, int r, int column, Sum sum) const {
+    const int at = unit / eights * 16 + r, token = unit % eights * 8 + column;
+    if (token < p.rows && at < p.hidden) static_cast<T *>(p.y)[token * p.ld_y + at] = from_f32<T>(sum(0));
   }
 };
 
 template <bool UP, int BITS>
-constexpr int kRoutedStages = UP ? (BITS == 16 ? 2 : 4) : (BITS == 16 ? 5 : 8);
-template <bool UP, int BITS, int NT>
+constexpr int kRoutedStages = UP ? (BITS == 16 ? 2 : 3) : 4;
+template <bool UP, int BITS>
 constexpr size_t kRoutedSmem =
-    kFewWarps * (kRoutedStages<UP, BITS> * (UP ? 2 : 1) * kBoxes<BITS> * kBoxBytes + (UP ? 2 : 1) * NT * kPartFloats * sizeof(float)) + kAlign;
+    kFewWarps * (kRoutedStages<UP, BITS> * Place<BITS, UP ? 2 : 1>::kBytes + (UP ? 2 : 1) * kPartFloats * sizeof(float)) + kAlign;
 
-template <typename T, int BITS, int NT>
+template <typename T, int BITS, int PIECES>
 __global__ void __launch_bounds__(32 * kFewWarps, 2)
     routed_up_kernel(const __grid_constant__ RoutedParams p, const __grid_constant__ RoutedMaps maps) {
   extern __shared__ char smem[];
@@ -356,53 +529,59 @@ __global__ void __launch_bounds__(32 * kFewWarps, 2)
   pdl_trigger();
   choose(p, c, blockIdx.x == 0);
   const int strips = (p.inter + 15) / 16;
-  UpJob<T, BITS, NT> job{p, maps, c, c.groups * strips, 1, (p.hidden + kTileK<BITS> - 1) / kTileK<BITS>, strips};
-  stream_units<2, 2, NT, kRoutedStages<true, BITS>, 2 * kBoxes<BITS>>(job, ring, 3, p.waits.status, p.waits.ns, p.waits.inject);
+  UpJob<T, BITS, PIECES> job{p, maps, c, c.up * strips, (p.hidden + kTileK<BITS> - 1) / kTileK<BITS>, p.hidden, strips};
+  job.t.x.set(0, 8);
+  stream_units<BITS, 2, kRoutedStages<true, BITS>>(job, ring, p.waits);
 }
 
-template <typename T, int BITS, int NT>
+template <typename T, int BITS, int PIECES>
 __global__ void __launch_bounds__(32 * kFewWarps, 2)
     routed_down_kernel(const __grid_constant__ RoutedParams p, const __grid_constant__ RoutedDownMaps maps) {
   extern __shared__ char smem[];
   __shared__ Choice c;
   char *ring = smem + (-smem_u32(smem) & (kAlign - 1));
   choose(p, c, false);
-  DownJob<T, BITS, NT> job{p, maps, c, (p.hidden + 15) / 16, c.groups, (p.inter + kTileK<BITS> - 1) / kTileK<BITS>};
-  stream_units<1, 1, NT, kRoutedStages<false, BITS>, kBoxes<BITS>>(job, ring, 3, p.waits.status, p.waits.ns, p.waits.inject);
+  const int eights = (p.rows + 7) / 8;
+  DownJob<T, BITS, PIECES> job{p, maps, c, (p.hidden + 15) / 16 * eights, (p.inter + kTileK<BITS> - 1) / kTileK<BITS>, p.inter, eights};
+  job.t.x.set(0, 8);
+  stream_units<BITS, 1, kRoutedStages<false, BITS>>(job, ring, p.waits);
 }
 
-template <typename T, int BITS, int NT>
+template <typename T, int BITS, int PIECES>
 cudaError_t layer_launch(const RoutedParams &p, const RoutedMaps &maps, const RoutedDownMaps &down, int num_sms, cudaStream_t st) {
-  constexpr size_t smem_up = kRoutedSmem<true, BITS, NT>, smem_down = kRoutedSmem<false, BITS, NT>;
+  constexpr size_t smem_up = kRoutedSmem<true, BITS>, smem_down = kRoutedSmem<false, BITS>;
   static std::atomic<unsigned long long> done[2];
-  cudaError_t e = allow_smem((const void *)routed_up_kernel<T, BITS, NT>, smem_up, done[0]);
-  if (e == cudaSuccess) e = allow_smem((const void *)routed_down_kernel<T, BITS, NT>, smem_down, done[1]);
+  cudaError_t e = allow_smem((const void *)routed_up_kernel<T, BITS, PIECES>, smem_up, done[0]);
+  if (e == cudaSuccess) e = allow_smem((const void *)routed_down_kernel<T, BITS, PIECES>, smem_down, done[1]);
   const dim3 threads(32 * kFewWarps);
   if (e == cudaSuccess)
     e = launch_pdl(p.router_f32 ? routed_logits_kernel<T, float> : routed_logits_kernel<T, T>,
                    dim3((p.experts + kRouteExperts - 1) / kRouteExperts), dim3(256), 0, st, p);
-  const long long groups = (long long)(p.rows * p.top_k < p.experts ? p.rows * p.top_k : p.experts) + p.shared;
-  const long long units = groups * ((p.inter + 15) / 16), units_down = (p.hidden + 15) / 16, most = 2ll * num_sms;
+  const int eights = (p.rows + 7) / 8;
+  const long long entries = p.rows * p.top_k + p.shared * eights;  // at most
+  const long long units = entries * ((p.inter + 15) / 16), units_down = (long long)eights * ((p.hidden + 15) / 16), most = 2ll * num_sms;
   if (e == cudaSuccess)
-    e = launch_pdl(routed_up_kernel<T, BITS, NT>, dim3((unsigned)(units < most ? units : most)), threads, smem_up, st, p, maps);
+    e = launch_pdl(routed_up_kernel<T, BITS, PIECES>, dim3((unsigned)(units < most ? units : most)), threads, smem_up, st, p, maps);
   if (e == cudaSuccess)
-    e = launch_pdl(routed_down_kernel<T, BITS, NT>, dim3((unsigned)(units_down < most ? units_down : most)), threads, smem_down, st, p, down);
+    e = launch_pdl(routed_down_kernel<T, BITS, PIECES>, dim3((unsigned)(units_down < most ? units_down : most)), threads, smem_down,
+                   st, p, down);
   return e;
 }
 
-template <typename T, int BITS>
-cudaError_t routed_rows(const RoutedParams &p, const RoutedMaps &maps, const RoutedDownMaps &down, int num_sms, cudaStream_t st) {
-  if (p.rows <= 8) return layer_launch<T, BITS, 1>(p, maps, down, num_sms, st);
-  if (p.rows <= 16) return layer_launch<T, BITS, 2>(p, maps, down, num_sms, st);
-  return layer_launch<T, BITS, 4>(p, maps, down, num_sms, st);
+template <typename T>
+cudaError_t routed_typed(const RoutedParams &p, const RoutedMaps &maps, const RoutedDownMaps &down, bool bits4, int num_sms,
+                         cudaStream_t st) {
+  if (!bits4) return layer_launch<T, 16, 0>(p, maps, down, num_sms, st);
+  if (p.gate.group_shift == 5) return layer_launch<T, 4, 1>(p, maps, down, num_sms, st);
+  if (p.gate.group_shift == 6) return layer_launch<T, 4, 2>(p, maps, down, num_sms, st);
+  return layer_launch<T, 4, 4>(p, maps, down, num_sms, st);
 }
 
 }  // namespace
 
 cudaError_t launch_routed(const RoutedParams &p, const RoutedMaps &maps, const RoutedDownMaps &down, bool f16, bool bits4,
                           int num_sms, cudaStream_t st) {
-  if (f16) return bits4 ? routed_rows<__half, 4>(p, maps, down, num_sms, st) : routed_rows<__half, 16>(p, maps, down, num_sms, st);
-  return bits4 ? routed_rows<__nv_bfloat16, 4>(p, maps, down, num_sms, st) : routed_rows<__nv_bfloat16, 16>(p, maps, down, num_sms, st);
+  return f16 ? routed_typed<__half>(p, maps, down, bits4, num_sms, st) : routed_typed<__nv_bfloat16>(p, maps, down, bits4, num_sms, st);
 }
 
 }  // namespace moe
