@@ -236,10 +236,9 @@ extern "C" int moe_ffn_routed_forward(const moe_ffn_routed_args *a, void *stream
       ins[n_ins++] = span(names[i], all[i]->w, count * n, k, k, 2);
     }
   }
-  // zero points are read, or not, by the expert's matrix for the shared one's too
-  for (int i = 0; i < 3; ++i)
-    if (S && (m[i].zeros != nullptr) != (m[i + 3].zeros != nullptr))
-      return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: %s and %s must both have zero points or neither", who, names[i], names[i + 3]);
+  for (int i = 1; i < (S ? 6 : 3); ++i)  // one kernel reads several matrices, with zero points or without
+    if ((m[i].zeros != nullptr) != (m[0].zeros != nullptr))
+      return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: %s and %s must both have zero points or neither", who, names[0], names[i]);
   const int64_t need = routed_workspace(a);
   if (a->workspace_bytes < (size_t)need)
     return fail(MOE_FFN_ERR_NO_MEMORY, "%s: workspace of %zu bytes, needs %lld", who, a->workspace_bytes, (long long)need);

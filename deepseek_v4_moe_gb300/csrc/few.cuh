@@ -116,13 +116,13 @@ struct Operand {
   }
 };
 
-// The products of a tile's strips.  PIECES: of 32 columns in a group of 4-bit weights, at compile time, so that a tile's
-// products are one run of instructions in which the strips overlap.
-template <typename T, int BITS, int PIECES, int M, int NT, bool ROWS8>
+// The products of a tile's strips.  PIECES: of 32 columns in a group of 4-bit weights, and ZP: they have zero
+// points, at compile time, so that a tile's products are one run of instructions in which the strips overlap.
+template <typename T, int BITS, int PIECES, bool ZP, int M, int NT, bool ROWS8>
 struct Tile;
 
 template <typename T, int M, int NT, bool ROWS8>
-struct Tile<T, 16, 0, M, NT, ROWS8> {
+struct Tile<T, 16, 0, false, M, NT, ROWS8> {
   Operand<kBoxes<16>, NT, ROWS8> x;
   // some: bit i where eight i has tokens at all
   __device__ __forceinline__ void multiply(uint32_t place, uint32_t tokens, unsigned some, float (&acc)[M][NT][4]) const {
@@ -158,10 +158,10 @@ struct MetaRow {
     const int row = threadIdx.x & 15;
     const long long first = (row0 + (row < rows_left ? row : 0)) * m.groups;
     scales = m.scales + first;
-    zeros = m.zeros ? m.zeros + first : nullptr;
+    zeros = m.zeros + first;  // (read with zero points only)
   }
 };
-template <int PIECES, int M>
+template <int PIECES, int M, bool ZP>
 struct Meta {
   static constexpr int kGroups = 4 / PIECES, kEach = kGroups == 4 ? 2 : 1;
   MetaRow row[M];
@@ -173,7 +173,7 @@ struct Meta {
     for (int h = 0; h < kEach; ++h) {
       const int g = min(g0 + 2 * h, groups - 1);
 #pragma unroll
-      for (int s = 0; s < M; ++s) next[s][h] = row[s].scales[g] | (row[s].zeros ? (row[s].zeros[g] & 15u) << 16 : 0u);
+      for (int s = 0; s < M; ++s) next[s][h] = row[s].scales[g] | (ZP ? (row[s].zeros[g] & 15u) << 16 : 0u);
     }
   }
   // from a warp's first tile of a matrix on; its rows are set
@@ -206,12 +206,12 @@ __device__ __forceinline__ uint4 in_pairs(const uint4 v) {
                     __byte_perm(v.y, v.w, 0x7632));
 }
 
-template <typename T, int PIECES, int M, int NT, bool ROWS8>
-struct Tile<T, 4, PIECES, M, NT, ROWS8> {
+template <typename T, int PIECES, bool ZP, int M, int NT, bool ROWS8>
+struct Tile<T, 4, PIECES, ZP, M, NT, ROWS8> {
   static constexpr int kGroups = 4 / PIECES;
   Operand<4, NT, ROWS8> x;
-  Meta<PIECES, M> meta;
-  __device__ __forceinline__ void multiply(uint32_t place, uint32_t tokens, unsigned some, float (&acc)[M][NT][4], bool zeros) const {
+  Meta<PIECES, M, ZP> meta;
+  __device__ __forceinline__ void multiply(uint32_t place, uint32_t tokens, unsigned some, float (&acc)[M][NT][4]) const {
     const int lane = threadIdx.x & 31, r = lane & 15, c0 = lane >> 4;
     const T *tag = nullptr;
     const uint32_t at = place + r * 64 + ((c0 ^ (r >> 1 & 3)) << 4);
@@ -225,8 +225,8 @@ struct Tile<T, 4, PIECES, M, NT, ROWS8> {
       for (int s = 0; s < M; ++s) {
         m0[s] = meta.get(s, q, 0);
         m1[s] = meta.get(s, q, 8);
-        z0[s] = zero_of<T>(zeros ? m0[s] >> 16 : 8u);
-        z1[s] = zero_of<T>(zeros ? m1[s] >> 16 : 8u);
+        z0[s] = zero_of<T>(ZP ? m0[s] >> 16 : 8u);
+        z1[s] = zero_of<T>(ZP ? m1[s] >> 16 : 8u);
       }
 #pragma unroll
       for (int j = 0; j < PIECES; ++j) {

@@ -27,7 +27,7 @@ struct Int4Plan {
   int x_bytes, stage_bytes;
 };
 
-template <typename T, int PIECES, int M, int NT>
+template <typename T, int PIECES, bool ZP, int M, int NT>
 __global__ void __launch_bounds__(32 * kFewWarps, 2)
     int4_matmul_kernel(const __grid_constant__ Int4MatmulParams p, const __grid_constant__ Int4Maps maps,
                        const __grid_constant__ Int4Plan plan) {
@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, 2)
     for (int s = 0; s < plan.stages && unit < plan.units; ++s, onwards(unit, step, 1)) fill(s, unit, step);
   }
   if (p.waits.inject && blockIdx.x == 0) wait_bounded(&never, 0, &abort_flag, p.waits.status, p.waits.ns);  // test hook
-  Tile<T, 4, PIECES, M, NT, (NT > 1)> t;
+  Tile<T, 4, PIECES, ZP, M, NT, (NT > 1)> t;
   t.x.set(share * 4 * plan.box_rows, plan.box_rows);
   const uint32_t w_at = smem_u32(ring) + (share * sets + set) * M * kBoxBytes, x_at = smem_u32(ring) + kWeights;
   int stage = 0, phase = 0;
@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, 2)
       t.meta.advance(step * kw + share);
       // (the lanes agree: one that gave up takes the warp with it)
       if (!__all_sync(0xffffffffu, wait_bounded(&full[stage], phase, &abort_flag, p.waits.status, p.waits.ns))) break;
-      t.multiply(w_at + stage * plan.stage_bytes, x_at + stage * plan.stage_bytes, ~0u, acc, p.w.zeros != nullptr);
+      t.multiply(w_at + stage * plan.stage_bytes, x_at + stage * plan.stage_bytes, ~0u, acc);
       __syncwarp();
       if (lane == 0) {
         unsigned before;
@@ -132,18 +132,18 @@ __global__ void __launch_bounds__(32 * kFewWarps, 2)
       if (fills[s]) mbar_wait_bounded(&full[s], (fills[s] - 1) & 1, &nobody, p.waits.status, p.waits.ns);
 }
 
-template <typename T, int PIECES, int M, int NT>
+template <typename T, int PIECES, bool ZP, int M, int NT>
 cudaError_t int4_launch(const Int4MatmulParams &p, const Int4Maps &maps, const Int4Plan &plan, int y, int num_sms, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
-  const cudaError_t e = allow_smem((const void *)int4_matmul_kernel<T, PIECES, M, NT>, kInt4Smem, done);
+  const cudaError_t e = allow_smem((const void *)int4_matmul_kernel<T, PIECES, ZP, M, NT>, kInt4Smem, done);
   if (e != cudaSuccess) return e;
   const size_t smem = plan.stages * (size_t)plan.stage_bytes + kFewWarps * NT * kPartFloats * sizeof(float) + 1024;
   const int most = 2 * num_sms / y > 1 ? 2 * num_sms / y : 1;
-  return launch_pdl(int4_matmul_kernel<T, PIECES, M, NT>, dim3(plan.units < most ? plan.units : most, y), dim3(32 * kFewWarps), smem,
+  return launch_pdl(int4_matmul_kernel<T, PIECES, ZP, M, NT>, dim3(plan.units < most ? plan.units : most, y), dim3(32 * kFewWarps), smem,
                     st, p, maps, plan);
 }
 
-template <typename T, int PIECES>
+template <typename T, int PIECES, bool ZP>
 cudaError_t int4_tiles(const Int4MatmulParams &p, const Int4Maps &maps, const Int4Tiles &t, int num_sms, cudaStream_t st) {
   Int4Plan plan;
   const int tiles = (p.w.k + kTileK<4> - 1) / kTileK<4>, set_rows = 16 * t.strips, sets = kFewWarps >> t.log_kw;
@@ -157,13 +157,11 @@ cudaError_t int4_tiles(const Int4MatmulParams &p, const Int4Maps &maps, const In
   plan.stages = room / plan.stage_bytes < kInt4Stages ? room / plan.stage_bytes : kInt4Stages;
   const int y = (p.rows + 8 * t.eights - 1) / (8 * t.eights);
 #define MOE_INT4(M, NT) \
-  if (t.strips == M && t.eights == NT) return int4_launch<T, PIECES, M, NT>(p, maps, plan, y, num_sms, st)
+  if (t.strips == M && t.eights == NT) return int4_launch<T, PIECES, ZP, M, NT>(p, maps, plan, y, num_sms, st)
   MOE_INT4(1, 1);
-  MOE_INT4(2, 1);
   MOE_INT4(4, 1);
   MOE_INT4(1, 2);
   MOE_INT4(2, 2);
-  MOE_INT4(4, 2);
   MOE_INT4(1, 4);
   MOE_INT4(2, 4);
 #undef MOE_INT4
@@ -259,7 +257,7 @@ cudaError_t quantise_launch(const Int4WeightParams &p, int num_sms, cudaStream_t
 Int4Tiles int4_pick_tiles(int rows, int n, int k, int num_sms) {
   Int4Tiles t;
   t.eights = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
-  t.strips = t.eights <= 2 && n >= 64 * num_sms ? 4 : t.eights == 4 && n >= 32 * num_sms ? 2 : 1;
+  t.strips = t.eights == 1 && n >= 64 * num_sms ? 4 : t.eights >= 2 && n >= 32 * num_sms ? 2 : 1;
   const int tiles = (k + kTileK<4> - 1) / kTileK<4>, strips = (n + 16 * t.strips - 1) / (16 * t.strips);
   t.log_kw = 0;
   const int most = t.eights == 1 ? 3 : t.eights == 2 ? 2 : 1;  // each share has its own columns of x in a step
@@ -270,9 +268,9 @@ Int4Tiles int4_pick_tiles(int rows, int n, int k, int num_sms) {
 
 template <typename T>
 cudaError_t launch_int4_typed(const Int4MatmulParams &p, const Int4Maps &maps, const Int4Tiles &t, int num_sms, cudaStream_t st) {
-  if (p.w.group_shift == 5) return int4_tiles<T, 1>(p, maps, t, num_sms, st);
-  if (p.w.group_shift == 6) return int4_tiles<T, 2>(p, maps, t, num_sms, st);
-  return int4_tiles<T, 4>(p, maps, t, num_sms, st);
+  if (p.w.group_shift == 5) return p.w.zeros ? int4_tiles<T, 1, true>(p, maps, t, num_sms, st) : int4_tiles<T, 1, false>(p, maps, t, num_sms, st);
+  if (p.w.group_shift == 6) return p.w.zeros ? int4_tiles<T, 2, true>(p, maps, t, num_sms, st) : int4_tiles<T, 2, false>(p, maps, t, num_sms, st);
+  return p.w.zeros ? int4_tiles<T, 4, true>(p, maps, t, num_sms, st) : int4_tiles<T, 4, false>(p, maps, t, num_sms, st);
 }
 
 cudaError_t launch_int4_matmul(const Int4MatmulParams &p, const Int4Maps &maps, const Int4Tiles &t, bool f16, int num_sms,

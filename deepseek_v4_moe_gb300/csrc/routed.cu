@@ -400,7 +400,7 @@ __device__ __forceinline__ void stream_units(Job &job, char *smem, const Waits &
 constexpr size_t kAlign = 512;  // of the ring, whose boxes' swizzle goes by the address
 
 // A unit: 16 rows of an entry's gate and up matrices.
-template <typename T, int BITS, int PIECES>
+template <typename T, int BITS, int PIECES, bool ZP>
 struct UpJob {
   const RoutedParams &p;
   const RoutedMaps &maps;
@@ -409,7 +409,7 @@ struct UpJob {
   int map_row;
   bool shared_ahead;
   const uint16_t *row;
-  Tile<T, BITS, PIECES, 2, 1, false> t;
+  Tile<T, BITS, PIECES, ZP, 2, 1, false> t;
   __device__ __forceinline__ int segs(int) const { return 1; }
   __device__ __forceinline__ void weights_at(int unit, int) {
     const int entry = unit / strips, e = c.up_expert[entry];
@@ -444,8 +444,7 @@ struct UpJob {
     if constexpr (BITS == 4) t.meta.advance(tile);
   }
   __device__ __forceinline__ void multiply(uint32_t place, uint32_t tokens, float (&acc)[2][1][4]) {
-    if constexpr (BITS == 4) t.multiply(place, tokens, 1u, acc, p.gate.zeros || p.up.zeros);
-    else t.multiply(place, tokens, 1u, acc);
+    t.multiply(place, tokens, 1u, acc);
   }
   template <typename Sum>
   __device__ __forceinline__ void finish(int unit, int r, int column, Sum sum) const {
@@ -462,7 +461,7 @@ struct UpJob {
 // ---- down ----
 
 // A unit: 16 rows of every expert's matrix that one of eight tokens has chosen.
-template <typename T, int BITS, int PIECES>
+template <typename T, int BITS, int PIECES, bool ZP>
 struct DownJob {
   const RoutedParams &p;
   const RoutedDownMaps &maps;
@@ -471,7 +470,7 @@ struct DownJob {
   int map_row;
   bool shared_ahead;
   const uint16_t *row;
-  Tile<T, BITS, PIECES, 1, 1, false> t;
+  Tile<T, BITS, PIECES, ZP, 1, 1, false> t;
   __device__ __forceinline__ int segs(int unit) const { return c.down[unit % eights]; }
   __device__ __forceinline__ void weights_at(int unit, int seg) {
     const int e = c.down_expert[unit % eights][seg];
@@ -502,8 +501,7 @@ struct DownJob {
     if constexpr (BITS == 4) t.meta.advance(tile);
   }
   __device__ __forceinline__ void multiply(uint32_t place, uint32_t tokens, float (&acc)[1][1][4]) {
-    if constexpr (BITS == 4) t.multiply(place, tokens, 1u, acc, p.down.zeros != nullptr);
-    else t.multiply(place, tokens, 1u, acc);
+    t.multiply(place, tokens, 1u, acc);
   }
   template <typename Sum>
   __device__ __forceinline__ void finish(int unit, int r, int column, Sum sum) const {
@@ -518,7 +516,7 @@ template <bool UP, int BITS>
 constexpr size_t kRoutedSmem =
     kFewWarps * (kRoutedStages<UP, BITS> * Place<BITS, UP ? 2 : 1>::kBytes + (UP ? 2 : 1) * kPartFloats * sizeof(float)) + kAlign;
 
-template <typename T, int BITS, int PIECES>
+template <typename T, int BITS, int PIECES, bool ZP>
 __global__ void __launch_bounds__(32 * kFewWarps, 2)
     routed_up_kernel(const __grid_constant__ RoutedParams p, const __grid_constant__ RoutedMaps maps) {
   extern __shared__ char smem[];
@@ -529,12 +527,12 @@ __global__ void __launch_bounds__(32 * kFewWarps, 2)
   pdl_trigger();
   choose(p, c, blockIdx.x == 0);
   const int strips = (p.inter + 15) / 16;
-  UpJob<T, BITS, PIECES> job{p, maps, c, c.up * strips, (p.hidden + kTileK<BITS> - 1) / kTileK<BITS>, p.hidden, strips};
+  UpJob<T, BITS, PIECES, ZP> job{p, maps, c, c.up * strips, (p.hidden + kTileK<BITS> - 1) / kTileK<BITS>, p.hidden, strips};
   job.t.x.set(0, 8);
   stream_units<BITS, 2, kRoutedStages<true, BITS>>(job, ring, p.waits);
 }
 
-template <typename T, int BITS, int PIECES>
+template <typename T, int BITS, int PIECES, bool ZP>
 __global__ void __launch_bounds__(32 * kFewWarps, 2)
     routed_down_kernel(const __grid_constant__ RoutedParams p, const __grid_constant__ RoutedDownMaps maps) {
   extern __shared__ char smem[];
@@ -542,17 +540,17 @@ __global__ void __launch_bounds__(32 * kFewWarps, 2)
   char *ring = smem + (-smem_u32(smem) & (kAlign - 1));
   choose(p, c, false);
   const int eights = (p.rows + 7) / 8;
-  DownJob<T, BITS, PIECES> job{p, maps, c, (p.hidden + 15) / 16 * eights, (p.inter + kTileK<BITS> - 1) / kTileK<BITS>, p.inter, eights};
+  DownJob<T, BITS, PIECES, ZP> job{p, maps, c, (p.hidden + 15) / 16 * eights, (p.inter + kTileK<BITS> - 1) / kTileK<BITS>, p.inter, eights};
   job.t.x.set(0, 8);
   stream_units<BITS, 1, kRoutedStages<false, BITS>>(job, ring, p.waits);
 }
 
-template <typename T, int BITS, int PIECES>
+template <typename T, int BITS, int PIECES, bool ZP>
 cudaError_t layer_launch(const RoutedParams &p, const RoutedMaps &maps, const RoutedDownMaps &down, int num_sms, cudaStream_t st) {
   constexpr size_t smem_up = kRoutedSmem<true, BITS>, smem_down = kRoutedSmem<false, BITS>;
   static std::atomic<unsigned long long> done[2];
-  cudaError_t e = allow_smem((const void *)routed_up_kernel<T, BITS, PIECES>, smem_up, done[0]);
-  if (e == cudaSuccess) e = allow_smem((const void *)routed_down_kernel<T, BITS, PIECES>, smem_down, done[1]);
+  cudaError_t e = allow_smem((const void *)routed_up_kernel<T, BITS, PIECES, ZP>, smem_up, done[0]);
+  if (e == cudaSuccess) e = allow_smem((const void *)routed_down_kernel<T, BITS, PIECES, ZP>, smem_down, done[1]);
   const dim3 threads(32 * kFewWarps);
   if (e == cudaSuccess)
     e = launch_pdl(p.router_f32 ? routed_logits_kernel<T, float> : routed_logits_kernel<T, T>,
@@ -561,9 +559,9 @@ cudaError_t layer_launch(const RoutedParams &p, const RoutedMaps &maps, const Ro
   const long long entries = p.rows * p.top_k + p.shared * eights;  // at most
   const long long units = entries * ((p.inter + 15) / 16), units_down = (long long)eights * ((p.hidden + 15) / 16), most = 2ll * num_sms;
   if (e == cudaSuccess)
-    e = launch_pdl(routed_up_kernel<T, BITS, PIECES>, dim3((unsigned)(units < most ? units : most)), threads, smem_up, st, p, maps);
+    e = launch_pdl(routed_up_kernel<T, BITS, PIECES, ZP>, dim3((unsigned)(units < most ? units : most)), threads, smem_up, st, p, maps);
   if (e == cudaSuccess)
-    e = launch_pdl(routed_down_kernel<T, BITS, PIECES>, dim3((unsigned)(units_down < most ? units_down : most)), threads, smem_down,
+    e = launch_pdl(routed_down_kernel<T, BITS, PIECES, ZP>, dim3((unsigned)(units_down < most ? units_down : most)), threads, smem_down,
                    st, p, down);
   return e;
 }
@@ -571,10 +569,13 @@ cudaError_t layer_launch(const RoutedParams &p, const RoutedMaps &maps, const Ro
 template <typename T>
 cudaError_t routed_typed(const RoutedParams &p, const RoutedMaps &maps, const RoutedDownMaps &down, bool bits4, int num_sms,
                          cudaStream_t st) {
-  if (!bits4) return layer_launch<T, 16, 0>(p, maps, down, num_sms, st);
-  if (p.gate.group_shift == 5) return layer_launch<T, 4, 1>(p, maps, down, num_sms, st);
-  if (p.gate.group_shift == 6) return layer_launch<T, 4, 2>(p, maps, down, num_sms, st);
-  return layer_launch<T, 4, 4>(p, maps, down, num_sms, st);
+  if (!bits4) return layer_launch<T, 16, 0, false>(p, maps, down, num_sms, st);
+  const bool zp = p.gate.zeros != nullptr;
+  if (p.gate.group_shift == 5)
+    return zp ? layer_launch<T, 4, 1, true>(p, maps, down, num_sms, st) : layer_launch<T, 4, 1, false>(p, maps, down, num_sms, st);
+  if (p.gate.group_shift == 6)
+    return zp ? layer_launch<T, 4, 2, true>(p, maps, down, num_sms, st) : layer_launch<T, 4, 2, false>(p, maps, down, num_sms, st);
+  return zp ? layer_launch<T, 4, 4, true>(p, maps, down, num_sms, st) : layer_launch<T, 4, 4, false>(p, maps, down, num_sms, st);
 }
 
 }  // namespace

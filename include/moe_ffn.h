@@ -516,7 +516,7 @@ int moe_ffn_int4_matmul(const moe_ffn_int4_matmul_args *a, void *stream);
 typedef struct moe_ffn_matrices {  /* the matrices of one projection, [count, n, k], contiguous, 16-byte aligned */
   const void *w;                   /* bits 16: values; bits 4: codes as above */
   const void *scales;              /* bits 4 */
-  const uint8_t *zeros;            /* bits 4, or NULL; the shared experts' given exactly when the experts' are */
+  const uint8_t *zeros;            /* bits 4: given for all projections, or for none */
 } moe_ffn_matrices;
 
 typedef struct moe_ffn_routed_args {
