@@ -140,70 +140,54 @@ __device__ __forceinline__ Pairs gate_set(const NormParams &p, int row, int gate
 
 // (Single values: 64 registers and 32 warps on an SM, some of them spilled, in place of 124 and 16 warps: 2000 x 4001
 // bf16 39 -> 28 us, 4096 x 3001 f32 57 -> 44.)
-// Writes y as FP8 codes with a scale for each block of 128 columns, of its f32 values.  VEC: a block of a set is 16
-// neighbouring lanes' eight columns each.  Otherwise (columns t + n e) a warp's columns of one e lie in one block,
-// several warps' in the same one: their maxima meet in shared memory (`amax`, one word for each block, zeros on entry
-// and on return), by integer atomics, whose order changes nothing.
-template <bool VEC>
-__device__ __forceinline__ void store_codes(const NormParams &p, size_t r, bool in, int t, int n, uint32_t *amax, const Pairs (&y)[kSets]) {
+// Writes y as FP8 codes with a scale for each block of 128 columns, of its f32 values, without wide accesses: a warp's
+// columns of one e (t + n e) lie in one block, several warps' in the same one, and their maxima meet in shared memory
+// (`amax`, one word for each block, zeros on entry and on return; `by`: what the blocks are divided by) by integer atomics, whose order changes nothing.
+__device__ __forceinline__ void store_codes(const NormParams &p, size_t r, bool in, int t, int n, uint32_t *amax, float2 *by,
+                                            const Pairs (&y)[kSets]) {
   const int blocks = (p.hidden + kScaleBlock - 1) / kScaleBlock;
   uint8_t *codes = p.codes + r * p.ld_codes;
   float *scales = p.scales + r * blocks;
-  if constexpr (VEC) {
-    uint32_t m[kSets];
+  auto meet = [&] {  // the group's threads
+    if (n == 32) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(1 + threadIdx.x / n), "r"(n) : "memory");
+  };
 #pragma unroll
-    for (int v = 0; v < kSets; ++v) m[v] = largest(flat(y[v]));
+  for (int v = 0; v < kSets; ++v)
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1)
-#pragma unroll
-      for (int v = 0; v < kSets; ++v) m[v] = max(m[v], __shfl_xor_sync(0xffffffffu, m[v], o));
-#pragma unroll
-    for (int v = 0; v < kSets; ++v) {
-      const int col = 8 * (v * n + t);
-      if (!in || col >= p.hidden) continue;
-      const float s = block_scale(m[v], p.e5m2, p.pow2);
-      const Divisor d = divisor(s);
-      *reinterpret_cast<uint2 *>(codes + col) = make_uint2(codes4(flat(y[v]), d, p.e5m2), codes4(flat(y[v]) + 4, d, p.e5m2));
-      if (t % 16 == 0) scales[col / kScaleBlock] = s;
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(flat(y[v])[e]) & 0x7FFFFFFFu);
+      const int col = (8 * v + e) * n + (t & ~31);
+      if (t % 32 == 0 && col < p.hidden) atomicMax(&amax[col / kScaleBlock], m);
     }
-  } else {
-    auto meet = [&] {  // the group's threads
-      if (n == 32) __syncwarp();
-      else asm volatile("bar.sync %0, %1;" ::"r"(1 + threadIdx.x / n), "r"(n) : "memory");
-    };
-#pragma unroll
-    for (int v = 0; v < kSets; ++v)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(flat(y[v])[e]) & 0x7FFFFFFFu);
-        const int col = (8 * v + e) * n + (t & ~31);
-        if (t % 32 == 0 && col < p.hidden) atomicMax(&amax[col / kScaleBlock], m);
-      }
-    meet();
-    if (in) {
-#pragma unroll
-      for (int v = 0; v < kSets; ++v)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int col = (8 * v + e) * n + t;
-          if (col >= p.hidden) continue;
-          const float s = block_scale(amax[col / kScaleBlock], p.e5m2, p.pow2);
-          codes[col] = (uint8_t)codes2(flat(y[v])[e], 0.f, divisor(s), p.e5m2);
-          if (col % kScaleBlock == 0) scales[col / kScaleBlock] = s;
-        }
-    }
-    meet();
-    for (int b = t; b < blocks; b += n) amax[b] = 0u;
-    meet();
+  meet();
+  for (int b = t; b < blocks; b += n) {  // a block's scale and its reciprocal, once
+    const float s = block_scale(amax[b], p.e5m2, p.pow2);
+    const Divisor d = divisor(s);
+    by[b] = make_float2(d.r, d.s);
+    amax[b] = 0u;
+    if (in) scales[b] = s;
   }
+  meet();
+  if (!in) return;
+#pragma unroll
+  for (int v = 0; v < kSets; ++v)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int col = (8 * v + e) * n + t;
+      if (col >= p.hidden) continue;
+      const float2 d = by[col / kScaleBlock];
+      codes[col] = (uint8_t)codes2(flat(y[v])[e], 0.f, Divisor{d.x, d.y}, p.e5m2);
+    }
 }
 
-// OUT8: y goes out as FP8 codes and scales.
+// OUT8: y goes out as FP8 codes and scales (without wide accesses).
 template <typename TS, typename TB, bool VEC, bool OUT8>
 __global__ void __launch_bounds__(512, VEC ? 1 : 2) block_norm_kernel(const __grid_constant__ NormParams p, int n) {
   __shared__ float buf[2 * 16];
-  __shared__ uint32_t amax[OUT8 && !VEC ? kNormHiddenMax / kScaleBlock : 1];
-  if constexpr (OUT8 && !VEC) {
+  __shared__ uint32_t amax[OUT8 ? kNormHiddenMax / kScaleBlock : 1];
+  __shared__ float2 by[OUT8 ? kNormHiddenMax / kScaleBlock : 1];
+  if constexpr (OUT8) {
     for (int i = threadIdx.x; i < (int)(sizeof amax / sizeof *amax); i += blockDim.x) amax[i] = 0u;
     __syncthreads();
   }
@@ -259,7 +243,85 @@ __global__ void __launch_bounds__(512, VEC ? 1 : 2) block_norm_kernel(const __gr
         else if (in) store_set<TB, VEC>(static_cast<TB *>(p.y) + r * p.ld_y, v, t, n, p.hidden, mul(w, mul(s[v], rs)));
       }
       // a group's blocks: of all groups together at most kNormHiddenMax / kScaleBlock
-      if constexpr (OUT8) store_codes<VEC>(p, r, in, t, n, amax + group * (n * 8 * kSets / kScaleBlock), s);
+      if constexpr (OUT8) store_codes(p, r, in, t, n, amax + group * (n * 8 * kSets / kScaleBlock), by + group * (n * 8 * kSets / kScaleBlock), s);
+    }
+  }
+}
+
+// y as codes, rows in wide accesses.  A thread holds SETS sets of a row and has the next row's loads in flight meanwhile:
+// 4096 x 4096 (f32 stream, bf16 block) took 43.7 us as an instance of the kernel above, whose 82 registers left the SMs
+// 16 warps, each of which loaded, reduced and stored in turn.
+template <typename TS, typename TB, int SETS>
+__global__ void __launch_bounds__(512, 2) block_norm_fp8_kernel(const __grid_constant__ NormParams p, int n) {
+  __shared__ float buf[2 * 16];
+  const int t = threadIdx.x & (n - 1), group = threadIdx.x / n, groups = blockDim.x / n;
+  const int blocks = (p.hidden + kScaleBlock - 1) / kScaleBlock, step = gridDim.x * groups;
+  const float inv = 1.f / (float)p.hidden;
+  int turn = 0;
+  Eight<TS, true> es[SETS];
+  Eight<TB, true> ef[SETS];
+  auto fetch = [&](int row) {
+    const size_t r = row < p.rows ? row : 0;  // a group without a row reads the first one and stores nothing
+#pragma unroll
+    for (int v = 0; v < SETS; ++v) {
+      es[v].load(static_cast<const TS *>(p.state) + r * p.ld_state, v * n + t, n, p.hidden);
+      if (p.f) ef[v].load(static_cast<const TB *>(p.f) + r * p.ld_f, v * n + t, n, p.hidden);
+    }
+  };
+  pdl_wait();
+  int row = blockIdx.x * groups + group;
+  fetch(row);
+  for (int base = blockIdx.x * groups; base < p.rows; base += step, row += step) {
+    const bool in = row < p.rows;
+    const size_t r = in ? row : 0;
+    Pairs s[SETS], f[SETS];
+#pragma unroll
+    for (int v = 0; v < SETS; ++v) {
+      es[v].get(flat(s[v]));
+      if (p.f) ef[v].get(flat(f[v]));
+    }
+    if (base + step < p.rows) fetch(row + step);
+    if (p.f) {
+      float scale = p.scale;
+      if (p.w_post) {
+        float2 ss = pair(0.f);
+#pragma unroll
+        for (int v = 0; v < SETS; ++v) dot(f[v], f[v], ss);
+        float sums[1] = {ss.x + ss.y};
+        group_sums(sums, n, buf, turn);
+        scale *= rsqrtf(fmaf(sums[0], inv, p.eps));
+      }
+      const int gate_row = p.gate_kind == kGateVector ? (int)r / p.rows_per_gate : 0;
+#pragma unroll
+      for (int v = 0; v < SETS; ++v) {
+        Pairs w = gate_set<TB, true>(p, (int)r, gate_row, v, t, n);
+        if (p.w_post) w = mul(w, load_set<float, true>(p.w_post, v, t, n, p.hidden));
+        s[v] = fma(mul(w, scale), f[v], s[v]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) flat(s[v])[e] = to_f32(from_f32<TS>(flat(s[v])[e]));
+        if (in) store_set<TS, true>(static_cast<TS *>(p.out) + r * p.ld_out, v, t, n, p.hidden, s[v]);
+      }
+    }
+    float2 ss = pair(0.f);
+#pragma unroll
+    for (int v = 0; v < SETS; ++v) dot(s[v], s[v], ss);
+    float sums[1] = {ss.x + ss.y};
+    group_sums(sums, n, buf, turn);
+    const float rs = rsqrtf(fmaf(sums[0], inv, p.eps));
+    uint8_t *codes = p.codes + r * p.ld_codes;
+    float *scales = p.scales + r * blocks;
+#pragma unroll
+    for (int v = 0; v < SETS; ++v) {
+      const Pairs y = mul(load_set<float, true>(p.w_next, v, t, n, p.hidden), mul(s[v], rs));
+      uint32_t m = largest(flat(y));  // a block: 16 neighbouring lanes' eight columns each
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const int col = 8 * (v * n + t);
+      if (!in || col >= p.hidden) continue;
+      const float scale = block_scale(m, p.e5m2, p.pow2);
+      const Divisor d = divisor(scale);
+      *reinterpret_cast<uint2 *>(codes + col) = make_uint2(codes4(flat(y), d, p.e5m2), codes4(flat(y) + 4, d, p.e5m2));
+      if (t % 16 == 0) scales[col / kScaleBlock] = scale;
     }
   }
 }
@@ -706,8 +768,17 @@ cudaError_t forward_typed(const NormParams &p, int num_sms, cudaStream_t st) {
   const int blocks = (p.rows + groups - 1) / groups, most = num_sms * (1024 / threads);
   const int grid = blocks < most ? blocks : most;
   const bool vec = all_wide(p);
-  auto kernel = p.codes ? (vec ? block_norm_kernel<TS, TB, true, true> : block_norm_kernel<TS, TB, false, true>)
-                        : (vec ? block_norm_kernel<TS, TB, true, false> : block_norm_kernel<TS, TB, false, false>);
+  if (p.codes && vec) {
+    const bool one = p.hidden <= 4096;  // a set of each thread's row: twice the threads a row
+    const int n8 = one && p.hidden > 256 ? 2 * n : n;
+    const int threads8 = n8 < 256 ? 256 : n8, groups8 = threads8 / n8, blocks8 = (p.rows + groups8 - 1) / groups8;
+    const int most8 = num_sms * (1024 / threads8);
+    return launch_pdl(one ? block_norm_fp8_kernel<TS, TB, 1> : block_norm_fp8_kernel<TS, TB, 2>, dim3(blocks8 < most8 ? blocks8 : most8),
+                      dim3(threads8), 0, st, p, n8);
+  }
+  auto kernel = p.codes ? block_norm_kernel<TS, TB, false, true>
+                : vec   ? block_norm_kernel<TS, TB, true, false>
+                        : block_norm_kernel<TS, TB, false, false>;
   return launch_pdl(kernel, dim3(grid), dim3(threads), 0, st, p, n);
 }
 

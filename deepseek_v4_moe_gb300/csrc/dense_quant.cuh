@@ -33,6 +33,11 @@ struct Divisor {
 __device__ __forceinline__ Divisor divisor(float scale) {
   return Divisor{__frcp_rn(scale), __float_as_uint(scale) == 0x7F800000u ? 0.f : scale};
 }
+// x over the scale in f32, rounded to nearest even
+__device__ __forceinline__ float quotient(float x, const Divisor &d) {
+  const float q = x * d.r;
+  return fmaf(fmaf(q, d.s, -x), -d.r, q);
+}
 __device__ __forceinline__ uint32_t codes2(float a, float b, const Divisor &d, bool e5m2) {
   const float2 q = __fmul2_rn(make_float2(a, b), make_float2(d.r, d.r));
   const float2 rest = __ffma2_rn(q, make_float2(d.s, d.s), make_float2(-a, -b));

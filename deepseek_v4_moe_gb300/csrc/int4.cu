@@ -6,6 +6,7 @@
 // in f32; a group's sum is multiplied by its scale in f32 once.  (Weights multiplied by their scales before the product
 // would be rounded to 16 bits each.)
 // Bound by the codes' way from memory; the conversion, 11 instructions for 8 codes, comes second.
+#include "dense_quant.cuh"
 #include "few.cuh"
 #include "kernels.h"
 
@@ -175,79 +176,136 @@ cudaError_t int4_tiles(const Int4MatmulParams &p, const Int4Maps &maps, const In
 // to their type first, and are 1 for zeros and at least its smallest normal value.  Eight values a lane, a group's in
 // 4, 8 or 16 lanes; bound by the weights' bytes.
 
-template <typename TS>
-__device__ __forceinline__ uint32_t bits_of(TS v) {
-  return *reinterpret_cast<const uint16_t *>(&v);
-}
+// A warp's next kChunks neighbouring chunks of CHUNK columns of a row: row and first chunk, from its number on.
+template <int CHUNK, int KCHUNKS>
+struct RowChunks {
+  long long row;
+  int at, per_row, rows_on, at_on;
+  __device__ __forceinline__ RowChunks(int k) {
+    const int warps = blockDim.x >> 5;
+    const long long first = (long long)blockIdx.x * warps + (threadIdx.x >> 5);
+    const long long step = (long long)gridDim.x * warps;
+    per_row = (k + CHUNK * KCHUNKS - 1) / (CHUNK * KCHUNKS);
+    row = first / per_row;
+    at = (int)(first - row * per_row);
+    rows_on = (int)(step / per_row);
+    at_on = (int)(step % per_row);
+  }
+  __device__ __forceinline__ int column() const { return at * (CHUNK * KCHUNKS); }
+  __device__ __forceinline__ void next() {
+    row += rows_on;
+    at += at_on;
+    if (at >= per_row) {
+      at -= per_row;
+      ++row;
+    }
+  }
+};
 
-template <typename T, typename TS>
+// The quotients are those of dense_quant.cuh, without a division for each value (all of them divided, with a 64-bit
+// division for a lane's place besides: 4096 x 2048 made and widened 22.9 us).
+template <typename T, typename TS, int PER>  // PER: lanes of a group
 __global__ void __launch_bounds__(256) int4_quantise_kernel(const __grid_constant__ Int4WeightParams p) {
-  const int lane = threadIdx.x & 31, eights = p.k / 8, per = p.group / 8;
-  const int groups = (p.k + p.group - 1) / p.group, row_lanes = groups * per;  // the last group's lanes may have no columns
-  const long long all = (long long)p.n * row_lanes;
+  constexpr int kChunks = sizeof(T) == 4 ? 1 : 2;
   constexpr float kLeast = std::is_same<TS, __half>::value ? 6.103515625e-05f : 1.17549435e-38f;
+  const int lane = threadIdx.x & 31, groups = (p.k + 8 * PER - 1) / (8 * PER);
+  RowChunks<256, kChunks> c(p.k);
   pdl_wait();
-  for (long long i0 = ((long long)blockIdx.x * 256 + threadIdx.x) - lane; i0 < all; i0 += (long long)gridDim.x * 256) {
-    const long long i = i0 + lane, row = i / row_lanes;
-    const int at = (int)(i - row * row_lanes);
-    const bool in = i < all && at < eights;
-    float v[8];
+  for (; c.row < p.n; c.next()) {
+    float v[kChunks][8], lo[kChunks], hi[kChunks];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = 0.f;
-    if (in) load_eight<T, true>(static_cast<const T *>(p.w) + row * p.ld_w + 8 * at, 0, 1, 8, v);
-    float lo = 0.f, hi = 0.f;
-    bool bad = false;  // a NaN, which minima and maxima pass over
+    for (int i = 0; i < kChunks; ++i) {
+      const int col = c.column() + 256 * i + 8 * lane;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      lo = fminf(lo, v[e]);
-      hi = fmaxf(hi, v[e]);
-      bad |= v[e] != v[e];
+      for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
+      if (col < p.k) load_eight<T, true>(static_cast<const T *>(p.w) + c.row * p.ld_w + col, 0, 1, 8, v[i]);
     }
-    if (bad) hi = __int_as_float(0x7F800000);
-    for (int o = per >> 1; o > 0; o >>= 1) {
-      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-    }
-    float s = p.zeros ? __fdiv_rn(__fsub_rn(hi, lo), 15.f) : __fdiv_rn(fmaxf(hi, -lo), 7.f);
-    s = s == 0.f ? 1.f : fmaxf(s, kLeast);
-    const TS stored = from_f32<TS>(s);
-    s = to_f32(stored);
-    const float zero = p.zeros ? fminf(fmaxf(rintf(__fdiv_rn(-lo, s)), 0.f), 15.f) : 8.f, least = p.zeros ? 0.f : 1.f;
-    uint32_t w = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      w |= (uint32_t)fminf(fmaxf(rintf(__fdiv_rn(v[e], s)) + zero, least), 15.f) << (4 * e);
-    if (in) *reinterpret_cast<uint32_t *>(p.codes + row * (p.k / 2) + 4 * at) = w;
-    if (i < all && at % per == 0) {
-      static_cast<TS *>(p.scales)[row * groups + at / per] = stored;
-      if (p.zeros) p.zeros[row * groups + at / per] = (uint8_t)zero;
+    for (int i = 0; i < kChunks; ++i) {
+      lo[i] = hi[i] = 0.f;
+      bool bad = false;  // a NaN, which minima and maxima pass over
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        lo[i] = fminf(lo[i], v[i][e]);
+        hi[i] = fmaxf(hi[i], v[i][e]);
+        bad |= v[i][e] != v[i][e];
+      }
+      if (bad) hi[i] = __int_as_float(0x7F800000);
+    }
+#pragma unroll
+    for (int o = PER >> 1; o > 0; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) {
+        lo[i] = fminf(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], o));
+        hi[i] = fmaxf(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], o));
+      }
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+      const int col = c.column() + 256 * i + 8 * lane;
+      float s = p.zeros ? __fdiv_rn(__fsub_rn(hi[i], lo[i]), 15.f) : __fdiv_rn(fmaxf(hi[i], -lo[i]), 7.f);
+      s = s == 0.f ? 1.f : fmaxf(s, kLeast);
+      const TS stored = from_f32<TS>(s);
+      const Divisor d = divisor(to_f32(stored));
+      const float zero = p.zeros ? fminf(fmaxf(rintf(quotient(-lo[i], d)), 0.f), 15.f) : 8.f, least = p.zeros ? 0.f : 1.f;
+      uint32_t w = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        // a whole number of 0 .. 15 as the low bits of 2^23 and it
+        const float code = fminf(fmaxf(rintf(quotient(v[i][e], d)) + zero, least), 15.f) + 8388608.f;
+        w |= (__float_as_uint(code) & 15u) << (4 * e);
+      }
+      if (col < p.k) *reinterpret_cast<uint32_t *>(p.codes + c.row * (p.k / 2) + col / 2) = w;
+      const int group = col / (8 * PER);
+      if (lane % PER == 0 && group < groups) {
+        static_cast<TS *>(p.scales)[c.row * groups + group] = stored;
+        if (p.zeros) p.zeros[c.row * groups + group] = (uint8_t)zero;
+      }
     }
   }
 }
 
+// Sixteen values a lane: code less zero point, exact in T, times the scale, rounded once.
 template <typename T>
 __global__ void __launch_bounds__(256) int4_widen_kernel(const __grid_constant__ Int4WeightParams p) {
-  const int eights = p.k / 8, groups = (p.k + p.group - 1) / p.group;
-  const long long all = (long long)p.n * eights;
+  const int lane = threadIdx.x & 31, groups = (p.k + p.group - 1) / p.group, shift = p.group == 32 ? 5 : p.group == 64 ? 6 : 7;
+  RowChunks<512, 1> c(p.k);
   pdl_wait();
-  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < all; i += (long long)gridDim.x * 256) {
-    const long long row = i / eights;
-    const int at = (int)(i - row * eights);
-    const long long g = row * groups + at * 8 / p.group;
-    const uint32_t w = *reinterpret_cast<const uint32_t *>(p.codes + row * (p.k / 2) + 4 * at);
-    const float s = to_f32(static_cast<const T *>(p.scales)[g]), zero = p.zeros ? (float)(p.zeros[g] & 15) : 8.f;
-    float v[8];
+  for (; c.row < p.n; c.next()) {
+    const int col = c.column() + 16 * lane;
+    if (col >= p.k) continue;
+    const uint2 w = *reinterpret_cast<const uint2 *>(p.codes + c.row * (p.k / 2) + col / 2);
+    const long long g = c.row * groups + (col >> shift);
+    const uint32_t scale = static_cast<const uint16_t *>(p.scales)[g] * 0x10001u;
+    const Zero<T> z = zero_of<T>(p.zeros ? p.zeros[g] & 15u : 8u);
+    uint32_t o[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = ((float)(w >> (4 * e) & 15u) - zero) * s;
-    Eight<T, true>::store(static_cast<T *>(p.out) + row * p.ld_out + 8 * at, 0, 1, 8, v);
+    for (int h = 0; h < 2; ++h) {
+      uint32_t v[4];
+      widen_codes<T>(h ? w.y : w.x, z, v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (std::is_same<T, __half>::value) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(v[i]) : "r"(scale));
+        else asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(v[i]) : "r"(scale));
+      }
+      // from pairs of columns i and i + 4 to neighbours
+      o[4 * h] = __byte_perm(v[0], v[1], 0x5410);
+      o[4 * h + 1] = __byte_perm(v[2], v[3], 0x5410);
+      o[4 * h + 2] = __byte_perm(v[0], v[1], 0x7632);
+      o[4 * h + 3] = __byte_perm(v[2], v[3], 0x7632);
+    }
+    uint4 *out = reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + c.row * p.ld_out + col);
+    out[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    out[1] = make_uint4(o[4], o[5], o[6], o[7]);
   }
 }
 
 template <typename T, typename TS>
 cudaError_t quantise_launch(const Int4WeightParams &p, int num_sms, cudaStream_t st) {
-  const long long lanes = (long long)p.n * ((p.k + p.group - 1) / p.group) * (p.group / 8);
-  const long long ctas = (lanes + 255) / 256, most = 8ll * num_sms;
-  return launch_pdl(int4_quantise_kernel<T, TS>, dim3((unsigned)(ctas < most ? ctas : most)), dim3(256), 0, st, p);
+  const int columns = sizeof(T) == 4 ? 256 : 512;  // of a warp
+  const long long ctas = ((long long)p.n * ((p.k + columns - 1) / columns) + 7) / 8, most = 4ll * num_sms;
+  const dim3 grid((unsigned)(ctas < most ? ctas : most));
+  auto kernel = p.group == 32 ? int4_quantise_kernel<T, TS, 4> : p.group == 64 ? int4_quantise_kernel<T, TS, 8> : int4_quantise_kernel<T, TS, 16>;
+  return launch_pdl(kernel, grid, dim3(256), 0, st, p);
 }
 
 }  // namespace
@@ -288,7 +346,7 @@ cudaError_t launch_int4_quantise(const Int4WeightParams &p, int num_sms, cudaStr
 }
 
 cudaError_t launch_int4_widen(const Int4WeightParams &p, int num_sms, cudaStream_t st) {
-  const long long ctas = ((long long)p.n * (p.k / 8) + 255) / 256, most = 8ll * num_sms;
+  const long long ctas = ((long long)p.n * ((p.k + 511) / 512) + 7) / 8, most = 8ll * num_sms;
   const dim3 grid((unsigned)(ctas < most ? ctas : most));
   return launch_pdl(p.f16 ? int4_widen_kernel<__half> : int4_widen_kernel<__nv_bfloat16>, grid, dim3(256), 0, st, p);
 }
