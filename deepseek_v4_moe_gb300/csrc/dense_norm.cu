@@ -248,81 +248,114 @@ __global__ void __launch_bounds__(512, VEC ? 1 : 2) block_norm_kernel(const __gr
   }
 }
 
+// Sums a value over a group of n threads, as group_sums: the warps' sums are read by every thread, four at a time, in
+// their order.
+__device__ __forceinline__ float group_sum(float v, int n, float *buf, int &turn) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (n == 32) return v;
+  const int warp = threadIdx.x >> 5, per = n >> 5, first = warp & ~(per - 1);
+  float *b = buf + turn * 16;
+  turn ^= 1;
+  if ((threadIdx.x & 31) == 0) b[warp] = v;
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + threadIdx.x / n), "r"(n) : "memory");
+  if (per == 2) return b[first] + b[first + 1];
+  const float4 *q = reinterpret_cast<const float4 *>(b + first);
+  float4 a = q[0];
+  if (per >= 8) {
+    const float4 c = q[1];
+    a = make_float4(a.x + c.x, a.y + c.y, a.z + c.z, a.w + c.w);
+  }
+  if (per == 16) {
+    const float4 c = q[2], e = q[3];
+    a = make_float4(a.x + c.x + e.x, a.y + c.y + e.y, a.z + c.z + e.z, a.w + c.w + e.w);
+  }
+  return (a.x + a.y) + (a.z + a.w);
+}
+
 // y as codes, rows in wide accesses.  A thread holds SETS sets of a row and has the next row's loads in flight meanwhile:
 // 4096 x 4096 (f32 stream, bf16 block) took 43.7 us as an instance of the kernel above, whose 82 registers left the SMs
-// 16 warps, each of which loaded, reduced and stored in turn.
-template <typename TS, typename TB, int SETS>
-__global__ void __launch_bounds__(512, 2) block_norm_fp8_kernel(const __grid_constant__ NormParams p, int n) {
-  __shared__ float buf[2 * 16];
+// 16 warps, each of which loaded, reduced and stored in turn, and 38.4 at 429 instructions for a warp's 256 columns.
+template <typename TS, typename TB, int SETS, bool E5M2, bool GATE>
+__global__ void __launch_bounds__(512, SETS == 1 ? 2 : 1) block_norm_fp8_kernel(const __grid_constant__ NormParams p, int n) {
+  __shared__ __align__(16) float buf[2 * 16];
   const int t = threadIdx.x & (n - 1), group = threadIdx.x / n, groups = blockDim.x / n;
   const int blocks = (p.hidden + kScaleBlock - 1) / kScaleBlock, step = gridDim.x * groups;
   const float inv = 1.f / (float)p.hidden;
   int turn = 0;
   Eight<TS, true> es[SETS];
   Eight<TB, true> ef[SETS];
-  auto fetch = [&](int row) {
-    const size_t r = row < p.rows ? row : 0;  // a group without a row reads the first one and stores nothing
+  int row = blockIdx.x * groups + group;
+  // this row's places, and by how much they move on; a group without a row reads the first one and stores nothing
+  const TS *state = static_cast<const TS *>(p.state) + (row < p.rows ? row : 0) * p.ld_state;
+  const TB *f_row = static_cast<const TB *>(p.f) + (row < p.rows ? row : 0) * p.ld_f;
+  TS *out = static_cast<TS *>(p.out) + row * p.ld_out;
+  uint8_t *codes = p.codes + row * p.ld_codes + 8 * t;
+  float *scales = p.scales + (long long)row * blocks + t / 16;
+  auto fetch = [&] {
 #pragma unroll
     for (int v = 0; v < SETS; ++v) {
-      es[v].load(static_cast<const TS *>(p.state) + r * p.ld_state, v * n + t, n, p.hidden);
-      if (p.f) ef[v].load(static_cast<const TB *>(p.f) + r * p.ld_f, v * n + t, n, p.hidden);
+      es[v].load(state, v * n + t, n, p.hidden);
+      if (p.f) ef[v].load(f_row, v * n + t, n, p.hidden);
     }
   };
   pdl_wait();
-  int row = blockIdx.x * groups + group;
-  fetch(row);
-  for (int base = blockIdx.x * groups; base < p.rows; base += step, row += step) {
+  fetch();
+  for (int base = blockIdx.x * groups; base < p.rows; base += step) {
     const bool in = row < p.rows;
-    const size_t r = in ? row : 0;
     Pairs s[SETS], f[SETS];
 #pragma unroll
     for (int v = 0; v < SETS; ++v) {
       es[v].get(flat(s[v]));
       if (p.f) ef[v].get(flat(f[v]));
     }
-    if (base + step < p.rows) fetch(row + step);
+    if (base + step < p.rows) {
+      if (row + step < p.rows) {
+        state += step * p.ld_state;
+        f_row += step * p.ld_f;
+      }
+      fetch();
+    }
     if (p.f) {
       float scale = p.scale;
       if (p.w_post) {
         float2 ss = pair(0.f);
 #pragma unroll
         for (int v = 0; v < SETS; ++v) dot(f[v], f[v], ss);
-        float sums[1] = {ss.x + ss.y};
-        group_sums(sums, n, buf, turn);
-        scale *= rsqrtf(fmaf(sums[0], inv, p.eps));
+        scale *= rsqrtf(fmaf(group_sum(ss.x + ss.y, n, buf, turn), inv, p.eps));
       }
-      const int gate_row = p.gate_kind == kGateVector ? (int)r / p.rows_per_gate : 0;
 #pragma unroll
       for (int v = 0; v < SETS; ++v) {
-        Pairs w = gate_set<TB, true>(p, (int)r, gate_row, v, t, n);
-        if (p.w_post) w = mul(w, load_set<float, true>(p.w_post, v, t, n, p.hidden));
-        s[v] = fma(mul(w, scale), f[v], s[v]);
+        Pairs w = splat(scale);
+        if (p.w_post) w = mul(load_set<float, true>(p.w_post, v, t, n, p.hidden), scale);
+        if constexpr (GATE) w = mul(w, gate_set<TB, true>(p, in ? row : 0, p.gate_kind == kGateVector && in ? row / p.rows_per_gate : 0, v, t, n));
+        s[v] = fma(w, f[v], s[v]);
+        if constexpr (sizeof(TS) < 4)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) flat(s[v])[e] = to_f32(from_f32<TS>(flat(s[v])[e]));
-        if (in) store_set<TS, true>(static_cast<TS *>(p.out) + r * p.ld_out, v, t, n, p.hidden, s[v]);
+          for (int e = 0; e < 8; ++e) flat(s[v])[e] = to_f32(from_f32<TS>(flat(s[v])[e]));
+        if (in) store_set<TS, true>(out, v, t, n, p.hidden, s[v]);
       }
     }
     float2 ss = pair(0.f);
 #pragma unroll
     for (int v = 0; v < SETS; ++v) dot(s[v], s[v], ss);
-    float sums[1] = {ss.x + ss.y};
-    group_sums(sums, n, buf, turn);
-    const float rs = rsqrtf(fmaf(sums[0], inv, p.eps));
-    uint8_t *codes = p.codes + r * p.ld_codes;
-    float *scales = p.scales + r * blocks;
+    const float rs = rsqrtf(fmaf(group_sum(ss.x + ss.y, n, buf, turn), inv, p.eps));
 #pragma unroll
     for (int v = 0; v < SETS; ++v) {
       const Pairs y = mul(load_set<float, true>(p.w_next, v, t, n, p.hidden), mul(s[v], rs));
       uint32_t m = largest(flat(y));  // a block: 16 neighbouring lanes' eight columns each
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const int col = 8 * (v * n + t);
-      if (!in || col >= p.hidden) continue;
-      const float scale = block_scale(m, p.e5m2, p.pow2);
+      if (!in || 8 * (v * n + t) >= p.hidden) continue;
+      const float scale = block_scale<E5M2>(m, p.pow2);
       const Divisor d = divisor(scale);
-      *reinterpret_cast<uint2 *>(codes + col) = make_uint2(codes4(flat(y), d, p.e5m2), codes4(flat(y) + 4, d, p.e5m2));
-      if (t % 16 == 0) scales[col / kScaleBlock] = scale;
+      *reinterpret_cast<uint2 *>(codes + 8 * v * n) = make_uint2(codes4<E5M2>(flat(y), d), codes4<E5M2>(flat(y) + 4, d));
+      if (t % 16 == 0) scales[v * n / 16] = scale;
     }
+    row += step;
+    out += step * p.ld_out;
+    codes += step * p.ld_codes;
+    scales += (long long)step * blocks;
   }
 }
 
@@ -772,8 +805,14 @@ cudaError_t forward_typed(const NormParams &p, int num_sms, cudaStream_t st) {
     const bool one = p.hidden <= 4096;  // a set of each thread's row: twice the threads a row
     const int n8 = one && p.hidden > 256 ? 2 * n : n;
     const int threads8 = n8 < 256 ? 256 : n8, groups8 = threads8 / n8, blocks8 = (p.rows + groups8 - 1) / groups8;
-    const int most8 = num_sms * (1024 / threads8);
-    return launch_pdl(one ? block_norm_fp8_kernel<TS, TB, 1> : block_norm_fp8_kernel<TS, TB, 2>, dim3(blocks8 < most8 ? blocks8 : most8),
+    const int most8 = num_sms * ((one ? 1024 : 512) / threads8);
+    const bool gate = p.gate_kind != kGateNone;
+    auto pick = [&](auto e5m2) {
+      constexpr bool E = decltype(e5m2)::value;
+      return one ? (gate ? block_norm_fp8_kernel<TS, TB, 1, E, true> : block_norm_fp8_kernel<TS, TB, 1, E, false>)
+                 : (gate ? block_norm_fp8_kernel<TS, TB, 2, E, true> : block_norm_fp8_kernel<TS, TB, 2, E, false>);
+    };
+    return launch_pdl(p.e5m2 ? pick(std::true_type()) : pick(std::false_type()), dim3(blocks8 < most8 ? blocks8 : most8),
                       dim3(threads8), 0, st, p, n8);
   }
   auto kernel = p.codes ? block_norm_kernel<TS, TB, false, true>

@@ -26,6 +26,18 @@ __device__ __forceinline__ float block_scale(uint32_t amax, bool e5m2, bool pow2
   return s;
 }
 
+// The same with the format known at compile time and, for magnitudes of 2^-90 to infinity, the quotient by the largest
+// code from its reciprocal (as `quotient` below): a division's instructions are a tenth of what a row's values take.
+template <bool E5M2>
+__device__ __forceinline__ float block_scale(uint32_t amax, bool pow2) {
+  constexpr float kMost = E5M2 ? 57344.f : 448.f, kInverse = 1.f / kMost;
+  if (amax - 0x12800000u >= 0x6D000000u) return block_scale(amax, E5M2, pow2);
+  const float x = __uint_as_float(amax), q = x * kInverse;
+  const float s = fmaf(fmaf(q, kMost, -x), -kInverse, q);
+  const uint32_t u = __float_as_uint(s);
+  return pow2 && u & 0x7FFFFFu ? __uint_as_float((u & 0x7F800000u) + 0x800000u) : s;
+}
+
 struct Divisor {
   float r, s;
 };
@@ -48,6 +60,17 @@ __device__ __forceinline__ uint32_t codes4(const float *v, const Divisor &d, boo
   return codes2(v[0], v[1], d, e5m2) | codes2(v[2], v[3], d, e5m2) << 16;
 }
 
+template <bool E5M2>
+__device__ __forceinline__ uint32_t codes4(const float *v, const Divisor &d) {
+  uint32_t o[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float2 x = make_float2(v[2 * i], v[2 * i + 1]), q = __fmul2_rn(x, make_float2(d.r, d.r));
+    const float2 rest = __ffma2_rn(q, make_float2(d.s, d.s), make_float2(-x.x, -x.y));
+    o[i] = __nv_cvt_float2_to_fp8x2(__ffma2_rn(rest, make_float2(-d.r, -d.r), q), __NV_SATFINITE, E5M2 ? __NV_E5M2 : __NV_E4M3);
+  }
+  return o[0] | o[1] << 16;
+}
 __device__ __forceinline__ uint32_t largest(const float (&v)[8]) {
   uint32_t m = 0u;
 #pragma unroll
