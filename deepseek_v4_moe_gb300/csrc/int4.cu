@@ -203,63 +203,58 @@ struct RowChunks {
 };
 
 // The quotients are those of dense_quant.cuh, without a division for each value (all of them divided, with a 64-bit
-// division for a lane's place besides: 4096 x 2048 made and widened 22.9 us).
-template <typename T, typename TS, int PER>  // PER: lanes of a group
-__global__ void __launch_bounds__(256) int4_quantise_kernel(const __grid_constant__ Int4WeightParams p) {
-  constexpr int kChunks = sizeof(T) == 4 ? 1 : 2;
+// division for a lane's place besides: 4096 x 2048 made and widened 22.9 us); a warp has its next columns' loads in flight.
+template <typename T, typename TS, int PER, bool ZP>  // PER: lanes of a group
+__global__ void __launch_bounds__(256, 4) int4_quantise_kernel(const __grid_constant__ Int4WeightParams p) {
   constexpr float kLeast = std::is_same<TS, __half>::value ? 6.103515625e-05f : 1.17549435e-38f;
+  constexpr float kInteger = 12582912.f;  // 1.5 2^23: a sum with it has the whole number nearest in its low bits
   const int lane = threadIdx.x & 31, groups = (p.k + 8 * PER - 1) / (8 * PER);
-  RowChunks<256, kChunks> c(p.k);
+  RowChunks<256, 1> c(p.k);
+  Eight<T, true> ahead;
+  auto load = [&] {
+    const int col = c.column() + 8 * lane;
+    ahead.load(static_cast<const T *>(p.w) + c.row * p.ld_w + col, 0, 1, c.row < p.n && col < p.k ? 8 : 0);
+  };
   pdl_wait();
-  for (; c.row < p.n; c.next()) {
-    float v[kChunks][8], lo[kChunks], hi[kChunks];
+  load();
+  while (c.row < p.n) {
+    float v[8];
+    ahead.get(v);
+    const int col = c.column() + 8 * lane;
+    const long long row = c.row;
+    c.next();
+    load();
+    float lo = 0.f, hi = 0.f, bad = 0.f;  // bad: not 0 where a value is no number, which minima and maxima pass over
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
-      const int col = c.column() + 256 * i + 8 * lane;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
-      if (col < p.k) load_eight<T, true>(static_cast<const T *>(p.w) + c.row * p.ld_w + col, 0, 1, 8, v[i]);
+    for (int e = 0; e < 8; ++e) {
+      if (ZP) lo = fminf(lo, v[e]);
+      hi = fmaxf(hi, ZP ? v[e] : fabsf(v[e]));
+      bad = fmaf(v[e], 0.f, bad);
     }
+    if (bad != 0.f) hi = __int_as_float(0x7F800000);
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
-      lo[i] = hi[i] = 0.f;
-      bool bad = false;  // a NaN, which minima and maxima pass over
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        lo[i] = fminf(lo[i], v[i][e]);
-        hi[i] = fmaxf(hi[i], v[i][e]);
-        bad |= v[i][e] != v[i][e];
-      }
-      if (bad) hi[i] = __int_as_float(0x7F800000);
+    for (int o = PER >> 1; o > 0; o >>= 1) {
+      if (ZP) lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
     }
+    float s = __fdiv_rn(ZP ? __fsub_rn(hi, lo) : hi, ZP ? 15.f : 7.f);
+    s = s == 0.f ? 1.f : fmaxf(s, kLeast);
+    const TS stored = from_f32<TS>(s);
+    const Divisor d = divisor(to_f32(stored));
+    const float zero = ZP ? fminf(fmaxf(rintf(quotient(-lo, d)), 0.f), 15.f) : 8.f, least = (ZP ? 0.f : 1.f) - zero, most = 15.f - zero;
+    const uint32_t z = (uint32_t)zero;
+    uint32_t w = 0;
 #pragma unroll
-    for (int o = PER >> 1; o > 0; o >>= 1)
-#pragma unroll
-      for (int i = 0; i < kChunks; ++i) {
-        lo[i] = fminf(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], o));
-        hi[i] = fmaxf(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], o));
-      }
-#pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
-      const int col = c.column() + 256 * i + 8 * lane;
-      float s = p.zeros ? __fdiv_rn(__fsub_rn(hi[i], lo[i]), 15.f) : __fdiv_rn(fmaxf(hi[i], -lo[i]), 7.f);
-      s = s == 0.f ? 1.f : fmaxf(s, kLeast);
-      const TS stored = from_f32<TS>(s);
-      const Divisor d = divisor(to_f32(stored));
-      const float zero = p.zeros ? fminf(fmaxf(rintf(quotient(-lo[i], d)), 0.f), 15.f) : 8.f, least = p.zeros ? 0.f : 1.f;
-      uint32_t w = 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        // a whole number of 0 .. 15 as the low bits of 2^23 and it
-        const float code = fminf(fmaxf(rintf(quotient(v[i][e], d)) + zero, least), 15.f) + 8388608.f;
-        w |= (__float_as_uint(code) & 15u) << (4 * e);
-      }
-      if (col < p.k) *reinterpret_cast<uint32_t *>(p.codes + c.row * (p.k / 2) + col / 2) = w;
-      const int group = col / (8 * PER);
-      if (lane % PER == 0 && group < groups) {
-        static_cast<TS *>(p.scales)[c.row * groups + group] = stored;
-        if (p.zeros) p.zeros[c.row * groups + group] = (uint8_t)zero;
-      }
+    for (int e = 7; e >= 0; --e) {
+      // rounded after the cut, whose ends are whole numbers; and not with the zero point, which would turn ties
+      const float q = fminf(fmaxf(quotient(v[e], d), least), most);
+      w = w << 4 | (__float_as_uint(q + kInteger) + z & 15u);
+    }
+    if (col < p.k) *reinterpret_cast<uint32_t *>(p.codes + row * (p.k / 2) + col / 2) = w;
+    const int group = col / (8 * PER);
+    if (lane % PER == 0 && group < groups) {
+      static_cast<TS *>(p.scales)[row * groups + group] = stored;
+      if (ZP) p.zeros[row * groups + group] = (uint8_t)z;
     }
   }
 }
@@ -301,11 +296,15 @@ __global__ void __launch_bounds__(256) int4_widen_kernel(const __grid_constant__
 
 template <typename T, typename TS>
 cudaError_t quantise_launch(const Int4WeightParams &p, int num_sms, cudaStream_t st) {
-  const int columns = sizeof(T) == 4 ? 256 : 512;  // of a warp
-  const long long ctas = ((long long)p.n * ((p.k + columns - 1) / columns) + 7) / 8, most = 4ll * num_sms;
+  const long long ctas = ((long long)p.n * ((p.k + 255) / 256) + 7) / 8, most = 4ll * num_sms;
   const dim3 grid((unsigned)(ctas < most ? ctas : most));
-  auto kernel = p.group == 32 ? int4_quantise_kernel<T, TS, 4> : p.group == 64 ? int4_quantise_kernel<T, TS, 8> : int4_quantise_kernel<T, TS, 16>;
-  return launch_pdl(kernel, grid, dim3(256), 0, st, p);
+  auto pick = [&](auto zp) {
+    constexpr bool ZP = decltype(zp)::value;
+    return p.group == 32   ? int4_quantise_kernel<T, TS, 4, ZP>
+           : p.group == 64 ? int4_quantise_kernel<T, TS, 8, ZP>
+                           : int4_quantise_kernel<T, TS, 16, ZP>;
+  };
+  return launch_pdl(p.zeros ? pick(std::true_type()) : pick(std::false_type()), grid, dim3(256), 0, st, p);
 }
 
 }  // namespace
