@@ -34,11 +34,6 @@ moe::FewMatrix matrix(const void *w, const void *scales, const uint8_t *zeros, i
   return moe::FewMatrix{w, static_cast<const uint16_t *>(scales), zeros, (int)n, (int)k, groups, log2_of(group)};
 }
 
-// boxes of 64 bytes x 16 rows over `count` matrices [n, k] one after another
-bool box_map(CUtensorMap *m, const moe::FewMatrix &w, int64_t count, int bits) {
-  return bits == 4 ? encode_map(m, w.w, 1, w.k / 2, count * w.n, w.k / 2, 16, 64) : encode_map(m, w.w, 2, w.k, count * w.n, w.k, 16, 64);
-}
-
 // rows of x or of a result in 16-byte pieces
 int check_rows16(const char *who, const char *name, const void *p, int64_t ld, int64_t cols) {
   if (!p) return fail(MOE_FFN_ERR_NULL_PTR, "%s: %s is NULL", who, name);
@@ -185,8 +180,15 @@ int check_routed(const char *who, const moe_ffn_routed_args *a) {
 }
 
 int64_t logits_bytes(const moe_ffn_routed_args *a) { return ((int64_t)a->rows * a->experts * 4 + 255) / 256 * 256; }
+// experts with tokens, at most
+int64_t routed_groups(const moe_ffn_routed_args *a) {
+  return (a->rows * a->top_k < a->experts ? a->rows * a->top_k : a->experts) + a->shared;
+}
 int64_t routed_workspace(const moe_ffn_routed_args *a) {
-  return logits_bytes(a) + (int64_t)a->rows * (a->top_k + a->shared) * a->inter * 2;
+  // h: a row for each token of each expert that it has chosen; with 16-bit weights for every token, and tokens up to a
+  // multiple of 8
+  const int64_t rows = a->bits == 4 ? (int64_t)a->rows * (a->top_k + a->shared) : routed_groups(a) * ((a->rows + 7) / 8 * 8);
+  return logits_bytes(a) + rows * a->inter * 2;
 }
 
 }  // namespace
@@ -279,12 +281,19 @@ extern "C" int moe_ffn_routed_forward(const moe_ffn_routed_args *a, void *stream
   DeviceSide dev;
   if ((rc = device_side(who, &dev))) return rc;
   p.waits = moe::Waits{dev.status, dev.wait_ns, dev.inject};
-  moe::RoutedMaps maps;
-  moe::RoutedDownMaps down;
-  CUtensorMap *to[] = {&maps.gate, &maps.up, &down.down, &maps.s_gate, &maps.s_up, &down.s_down};
-  for (int i = 0; i < 6; ++i) {
-    if (i >= 3 && !S) *to[i] = *to[i - 3];  // not read
-    else if (!box_map(to[i], m[i], i < 3 ? E : S, a->bits)) return fail(MOE_FFN_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", who);
+  moe::RoutedMaps maps = {}, down = {};
+  CUtensorMap *to[] = {&maps.gate, &maps.up, &down.gate, &maps.s_gate, &maps.s_up, &down.s_gate};
+  bool ok = true;
+  for (int i = 0; i < (S ? 6 : 3); ++i) {
+    const int64_t count = i < 3 ? E : S, n = m[i].n, k = m[i].k;
+    ok = ok && (a->bits == 4 ? encode_map(to[i], m[i].w, 1, k / 2, count * n, k / 2, 16, 64)
+                             : encode_map(to[i], m[i].w, 2, k, count * n, k, i % 3 == 2 ? 128 : 64));
   }
+  if (a->bits == 16) {
+    const int64_t R8 = (R + 7) / 8 * 8;
+    ok = ok && encode_map(&maps.tokens, a->x, 2, H, R, a->ld_x, (int)R8) &&
+         encode_map(&down.tokens, p.h, 2, I, routed_groups(a) * R8, I, (int)R8);
+  }
+  if (!ok) return fail(MOE_FFN_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", who);
   return launched(who, moe::launch_routed(p, maps, down, a->type == MOE_FFN_F16, a->bits == 4, sms, static_cast<cudaStream_t>(stream)));
 }

@@ -86,14 +86,13 @@ struct RoutedParams {
   uint16_t *h;                         // workspace: [rows, top_k + shared, inter]
   Waits waits;
 };
-// over all experts' rows of each matrix, boxes of 64 bytes x 16 rows
+// over all experts' rows of each matrix; of the down kernels gate and s_gate are down and s_down.  4 bits: boxes of 64
+// bytes x 16 rows.  16 bits: boxes of 128 bytes x 64 rows (down: 128), and tokens: x, or h, boxes of 128 bytes x the
+// tokens up to a multiple of 8.
 struct RoutedMaps {
-  CUtensorMap gate, up, s_gate, s_up;
+  CUtensorMap gate, up, s_gate, s_up, tokens;
 };
-struct RoutedDownMaps {
-  CUtensorMap down, s_down;
-};
-cudaError_t launch_routed(const RoutedParams &p, const RoutedMaps &maps, const RoutedDownMaps &down, bool f16, bool bits4,
+cudaError_t launch_routed(const RoutedParams &p, const RoutedMaps &maps, const RoutedMaps &down, bool f16, bool bits4,
                           int num_sms, cudaStream_t st);
 
 }  // namespace moe

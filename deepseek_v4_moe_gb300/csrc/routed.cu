@@ -73,8 +73,13 @@ __global__ void __launch_bounds__(256) routed_logits_kernel(const __grid_constan
 constexpr int kEightsMax = kRoutedRows / 8, kUpMax = kRoutedRows * kRoutedTopK + kRoutedShared * kEightsMax;
 constexpr int kDownMax = 8 * kRoutedTopK + kRoutedShared;
 
+constexpr int kGroupsMax = kRoutedRows * kRoutedTopK + kRoutedShared;
+
 struct Choice {
   int up, down[kEightsMax];                        // entries
+  int groups;                                      // experts with tokens, each once
+  uint16_t group_expert[kGroupsMax];
+  uint32_t group_mask[kGroupsMax];
   uint32_t mask[kRoutedExperts];                   // each expert's tokens
   uint32_t up_mask[kUpMax];
   uint16_t up_expert[kUpMax];
@@ -178,7 +183,7 @@ __device__ __forceinline__ void choose(const RoutedParams &p, Choice &c, bool wr
   __syncthreads();
   if (warp == 0) {
     const int all = p.experts + p.shared;
-    int up = 0, down[kEightsMax] = {};
+    int up = 0, down[kEightsMax] = {}, groups = 0;
     for (int e0 = 0; e0 < all; e0 += 32) {
       const int e = e0 + lane;
       uint32_t mask = e < p.experts ? c.mask[e] : e < all ? 0xFFFFFFFFu >> (32 - p.rows) : 0u;
@@ -188,6 +193,13 @@ __device__ __forceinline__ void choose(const RoutedParams &p, Choice &c, bool wr
         if (mask >> (8 * j) & 255u) c.down_expert[j][down[j] + __popc(has & ((1u << lane) - 1u))] = (uint16_t)e;
         down[j] += __popc(has);
       }
+      const uint32_t any = __ballot_sync(0xffffffffu, mask != 0u);
+      if (mask) {
+        const int g = groups + __popc(any & ((1u << lane) - 1u));
+        c.group_expert[g] = (uint16_t)e;
+        c.group_mask[g] = mask;
+      }
+      groups += __popc(any);
       const int passes = (__popc(mask) + 7) / 8;
       int at = passes;  // the entries of the lanes up to this one
 #pragma unroll
@@ -208,6 +220,7 @@ __device__ __forceinline__ void choose(const RoutedParams &p, Choice &c, bool wr
     }
     if (lane == 0) {
       c.up = up;
+      c.groups = groups;
 #pragma unroll
       for (int j = 0; j < kEightsMax; ++j) c.down[j] = down[j];
     }
@@ -464,7 +477,7 @@ struct UpJob {
 template <typename T, int BITS, int PIECES, bool ZP>
 struct DownJob {
   const RoutedParams &p;
-  const RoutedDownMaps &maps;
+  const RoutedMaps &maps;
   const Choice &c;
   int units, tiles, k, eights;
   int map_row;
@@ -480,7 +493,7 @@ struct DownJob {
   __device__ __forceinline__ void weights(char *place, uint64_t *bar, int tile) const {
 #pragma unroll
     for (int b = 0; b < kBoxes<BITS>; ++b)
-      tma_load_2d(place + b * kBoxBytes, shared_ahead ? &maps.s_down : &maps.down, bar, (tile * kBoxes<BITS> + b) * (BITS == 16 ? 32 : 64),
+      tma_load_2d(place + b * kBoxBytes, shared_ahead ? &maps.s_gate : &maps.gate, bar, (tile * kBoxes<BITS> + b) * (BITS == 16 ? 32 : 64),
                   map_row);
   }
   __device__ __forceinline__ void tokens_ready() const { pdl_wait(); }  // h comes from the kernel before
@@ -510,6 +523,269 @@ struct DownJob {
   }
 };
 
+// ---- 16-bit weights: tcgen05 ----
+//
+// The weights are the left operand as they lie (128 rows x 64 columns a step, K-major, by TMA), all tokens' columns the
+// right one, so that nothing but copies and one instruction for 16 columns is left: the kernels run at the pace of memory.
+// (On mma.sync, a warp's strips of 16 rows as above, one token of 256 experts of 4096 x 2048 took 72 to 83 us: copies of
+// 16 rows x 64 bytes do not come faster than 3.2 TB/s.)
+//
+// Up: a tile is 64 rows of gate and 64 of up; two accumulators in TMEM, so that a tile's epilogue runs beside the next
+// tile's products.  h lies by experts, [expert's place among the chosen][tokens, up to a multiple of 8][inter], with zeros
+// for the tokens that have not chosen it: the down kernel's right operand, as it needs it.
+// Down: a tile is 128 rows; the experts' steps are shared by the CTAs of a cluster, whose sums meet in shared memory.
+
+constexpr int kTcThreads = 192, kTcRows = 128, kTcW = kTcRows * 128;
+template <int NC>
+constexpr int kTcStage = kTcW + NC * 128;
+template <int NC>
+constexpr int kTcRing = NC == 16 ? 11 : 9;
+template <int NC>
+constexpr size_t kTcSmem = kTcRing<NC> * kTcStage<NC> + 1024;
+
+// NC columns of this thread's lane of an accumulator
+template <int NC>
+__device__ __forceinline__ void read_accumulator(uint32_t at, float (&v)[NC]) {
+#pragma unroll
+  for (int i = 0; i < NC; i += 16) tmem_ld16(at + i, reinterpret_cast<float(&)[16]>(v[i]));
+}
+
+template <bool UP, typename T, int NC>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    routed_tc_kernel(const __grid_constant__ RoutedParams p, const __grid_constant__ RoutedMaps maps, int splits) {
+  constexpr int kTcStages = kTcRing<NC>;
+  extern __shared__ char smem[];
+  __shared__ Choice c;
+  __shared__ __align__(8) uint64_t full[kTcStages], empty[kTcStages], tfull[2], tempty[2], mma_done, never;
+  __shared__ uint32_t tmem_base;
+  __shared__ int abort_flag, issued;
+  __shared__ float sums[UP ? 2 : 1][NC * (UP ? 64 : kTcRows)];
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  char *ring = smem + (-smem_u32(smem) & 1023u);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kTcStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], 4);
+    }
+    mbar_init(&mma_done, 1);
+    mbar_init(&never, 1);
+    abort_flag = 0;
+    issued = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc(&tmem_base, 64);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base;
+  if constexpr (UP) {
+    pdl_wait();
+    // The down kernel's CTAs may come, choose and fetch weights: not earlier, as they read the logits.
+    pdl_trigger();
+  }
+  choose(p, c, UP && blockIdx.x == 0);
+  volatile int *abort_p = &abort_flag;
+  const Waits &w = p.waits;
+  const int rows8 = (p.rows + 7) / 8 * 8, depth = UP ? p.hidden : p.inter, steps = (depth + 63) / 64;
+  const int tiles = UP ? (p.inter + 63) / 64 : 1;  // of an expert
+  // UP: units of an expert's tile, one after another; otherwise one tile, and this CTA's share of all experts' steps
+  const int rank = UP ? 0 : blockIdx.x % splits, tile_down = UP ? 0 : blockIdx.x / splits;
+  const int units = UP ? c.groups * tiles : 1, unit0 = UP ? blockIdx.x : 0, unit_step = UP ? gridDim.x : 1;
+  const long long all = (long long)c.groups * steps;
+  const int first = UP ? 0 : (int)(all * rank / splits), end = UP ? steps : (int)(all * (rank + 1) / splits);
+
+  if (warp == 0) {
+    // ---------------- copies ----------------
+    const uint32_t ring0 = smem_u32(ring), bytes = kTcW + rows8 * 128;
+    RingPos<kTcStages> pos;
+    int j = 0, group = UP ? 0 : first / steps, k = UP ? 0 : first % steps, unit = unit0, step = first;
+    auto weights = [&](int s) {
+      const uint32_t at = ring0 + s * kTcStage<NC>, bar = smem_u32(&full[s]);
+      mbar_expect_one(bar, bytes);
+      const int e = c.group_expert[group];
+      const bool shared = e >= p.experts;
+      const int row = (shared ? e - p.experts : e) * (UP ? p.inter : p.hidden);
+      if constexpr (UP) {
+        const int r = row + (unit - group * tiles) * 64;
+        tma_load_2d_one<false>(at, shared ? &maps.s_gate : &maps.gate, bar, k * 64, r);
+        tma_load_2d_one<false>(at + 64 * 128, shared ? &maps.s_up : &maps.up, bar, k * 64, r);
+      } else {
+        tma_load_2d_one<false>(at, shared ? &maps.s_gate : &maps.gate, bar, k * 64, row + tile_down * kTcRows);
+      }
+    };
+    auto tokens = [&](int s, int g, int kk) {
+      tma_load_2d_one<false>(ring0 + s * kTcStage<NC> + kTcW, &maps.tokens, smem_u32(&full[s]), kk * 64, UP ? 0 : g * rows8);
+    };
+    auto next = [&] {
+      ++step;
+      if (++k == steps) {
+        k = 0;
+        if (!UP) ++group;
+      }
+      if (UP && step == end) {
+        step = 0;
+        unit += unit_step;
+        group = unit / tiles;
+      }
+    };
+    if (UP) group = unit / tiles;
+    bool ok = true;
+    if constexpr (!UP) {  // the first weights need not wait for h
+      const int g0 = group, k0 = k;
+      for (; j < kTcStages && step < end; ++j, next()) weights(j);
+      pdl_wait();
+      int g = g0, kk = k0;
+      for (int i = 0; i < j; ++i) {
+        tokens(i, g, kk);
+        if (++kk == steps) {
+          kk = 0;
+          ++g;
+        }
+      }
+      for (int i = 0; i < j; ++i) pos.next();
+    }
+    for (; unit < units && step < end; ++j, pos.next(), next()) {
+      if (!warp_wait(&empty[pos.slot], pos.round ^ 1u, abort_p, w.status, w.ns)) {
+        ok = false;
+        break;
+      }
+      weights(pos.slot);
+      tokens(pos.slot, group, k);
+    }
+    (void)ok;
+    if (lane == 0) issued = j;
+  } else if (warp == 1) {
+    // ---------------- products ----------------
+    if (w.inject && blockIdx.x == 0) (void)warp_wait(&never, 0u, abort_p, w.status, w.ns);  // test hook: a wait that runs out
+    const uint32_t idesc = std::is_same<T, __half>::value ? idesc_f16_f32(kTcRows, NC) : idesc_bf16_f32(kTcRows, NC);
+    const uint64_t a0 = smem_desc_sw128(smem_u32(ring)), b0 = a0 + (kTcW >> 4);
+    RingPos<kTcStages> pos;
+    RingPos<2> acc;
+    bool ok = true;
+    for (int unit = unit0; ok && unit < units; unit += unit_step, acc.next()) {
+      if (!warp_wait(&tempty[acc.slot], acc.round ^ 1u, abort_p, w.status, w.ns)) break;
+      for (int step = first; step < end; ++step, pos.next()) {
+        if (!warp_wait(&full[pos.slot], pos.round, abort_p, w.status, w.ns)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t at = pos.slot * (kTcStage<NC> >> 4), d = tmem + acc.slot * 32;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          tc_mma_one<false, false>(d, a0 + (at + k * 2), b0 + (at + k * 2), idesc, step > first || k > 0 ? 1u : 0u);
+        tc_commit_one<false>(smem_u32(&empty[pos.slot]));
+      }
+      if (ok) tc_commit_one<false>(smem_u32(&tfull[acc.slot]));
+    }
+    // every MMA this warp issued completes before TMEM is freed
+    tc_commit_one<false>(smem_u32(&mma_done));
+    int no_abort = 0;
+    (void)wait_bounded(&mma_done, 0u, &no_abort, w.status, w.ns);
+  } else {
+    // ---------------- results ----------------
+    const int q = warp & 3, row = q * 32 + lane;
+    RingPos<2> acc;
+    for (int unit = unit0; unit < units; unit += unit_step, acc.next()) {
+      float v[NC];
+      const bool ok = (UP || first < end) && warp_wait(&tfull[acc.slot], acc.round, abort_p, w.status, w.ns);
+      if (ok) {
+        tc_fence_after();
+        read_accumulator<NC>(tmem + ((uint32_t)(q * 32) << 16) + acc.slot * 32, v);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tempty[acc.slot]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < NC; ++i) v[i] = 0.f;
+      }
+      if constexpr (UP) {
+        float *u = sums[acc.slot];
+        if (q >= 2)
+#pragma unroll
+          for (int t = 0; t < NC; ++t)
+            if (t < p.rows) u[t * 64 + row - 64] = v[t];
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        const int group = unit / tiles, at = (unit - group * tiles) * 64 + row, e = c.group_expert[group];
+        const uint32_t mask = c.group_mask[group];
+        if (q < 2 && at < p.inter) {
+          uint16_t *h = p.h + (long long)group * rows8 * p.inter + at;
+#pragma unroll
+          for (int t = 0; t < NC; ++t) {
+            if (t >= p.rows) break;
+            T out = from_f32<T>(0.f);
+            if (mask >> t & 1) {
+              const float weight = e < p.experts ? c.weight[t][slot_of(p, c, e, t)] : 1.f;
+              // rounded to 16 bits as the tensor cores' operand, as the gated block does
+              out = from_f32<T>(act_value(p.act, v[t]) * u[t * 64 + row] * weight);
+            }
+            h[(long long)t * p.inter] = *reinterpret_cast<const uint16_t *>(&out);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int t = 0; t < NC; ++t)
+          if (t < p.rows) sums[0][t * kTcRows + row] = v[t];
+      }
+    }
+  }
+  // Copies still in flight after an abort land before the CTA may leave (bounded; in a normal run each has landed).
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int no_abort = 0;
+    for (int s = 0; s < kTcStages; ++s) {
+      const int n = issued / kTcStages + (s < issued % kTcStages ? 1 : 0);
+      if (n > 0) (void)wait_bounded(&full[s], (uint32_t)((n - 1) & 1), &no_abort, w.status, w.ns);
+    }
+  }
+  if constexpr (!UP) {
+    // the CTAs' sums in the order of their ranks, a part of the rows by each
+    if (splits > 1) cluster_sync();
+    const int part = kTcRows / splits, row0 = rank * part;
+    for (int i = threadIdx.x; i < part * p.rows; i += kTcThreads) {
+      const int row = row0 + i % part, t = i / part, at = tile_down * kTcRows + row;
+      float v = 0.f;
+      for (int r = 0; r < splits; ++r) {
+        float x;
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(in_cta(&sums[0][t * kTcRows + row], r)) : "memory");
+        v += x;
+      }
+      if (at < p.hidden) static_cast<T *>(p.y)[t * p.ld_y + at] = from_f32<T>(v);
+    }
+    if (splits > 1) cluster_sync();
+  } else {
+    __syncthreads();
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 64);
+  }
+}
+
+template <typename T, int NC>
+cudaError_t tc_launch(const RoutedParams &p, const RoutedMaps &maps, const RoutedMaps &down, int num_sms, cudaStream_t st) {
+  static std::atomic<unsigned long long> done[2];
+  cudaError_t e = allow_smem((const void *)routed_tc_kernel<true, T, NC>, kTcSmem<NC>, done[0]);
+  if (e == cudaSuccess)
+    e = launch_pdl(p.router_f32 ? routed_logits_kernel<T, float> : routed_logits_kernel<T, T>,
+                   dim3((p.experts + kRouteExperts - 1) / kRouteExperts), dim3(256), 0, st, p);
+  const long long groups = (p.rows * p.top_k < p.experts ? p.rows * p.top_k : p.experts) + p.shared;
+  const long long units = groups * ((p.inter + 63) / 64);
+  if (e == cudaSuccess)
+    e = launch_pdl(routed_tc_kernel<true, T, NC>, dim3((unsigned)(units < num_sms ? units : num_sms)), dim3(kTcThreads), kTcSmem<NC>, st, p,
+                   maps, 1);
+  if (e != cudaSuccess) return e;
+  // as many CTAs to a tile as run at one time (of clusters of 8, 4 and 2 on 152 SMs 16, 36 and 75)
+  const int tiles = (p.hidden + kTcRows - 1) / kTcRows;
+  const int splits = tiles <= num_sms * 16 / 152 ? 8 : tiles <= num_sms * 36 / 152 ? 4 : tiles <= num_sms * 75 / 152 ? 2 : 1;
+  return launch_clusters(routed_tc_kernel<false, T, NC>, kTcSmem<NC>, done[1], tiles, splits, kTcThreads, st, p, down, splits);
+}
+
 template <bool UP, int BITS>
 constexpr int kRoutedStages = UP ? (BITS == 16 ? 2 : 3) : 4;
 template <bool UP, int BITS>
@@ -534,7 +810,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, 2)
 
 template <typename T, int BITS, int PIECES, bool ZP>
 __global__ void __launch_bounds__(32 * kFewWarps, 2)
-    routed_down_kernel(const __grid_constant__ RoutedParams p, const __grid_constant__ RoutedDownMaps maps) {
+    routed_down_kernel(const __grid_constant__ RoutedParams p, const __grid_constant__ RoutedMaps maps) {
   extern __shared__ char smem[];
   __shared__ Choice c;
   char *ring = smem + (-smem_u32(smem) & (kAlign - 1));
@@ -546,7 +822,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, 2)
 }
 
 template <typename T, int BITS, int PIECES, bool ZP>
-cudaError_t layer_launch(const RoutedParams &p, const RoutedMaps &maps, const RoutedDownMaps &down, int num_sms, cudaStream_t st) {
+cudaError_t layer_launch(const RoutedParams &p, const RoutedMaps &maps, const RoutedMaps &down, int num_sms, cudaStream_t st) {
   constexpr size_t smem_up = kRoutedSmem<true, BITS>, smem_down = kRoutedSmem<false, BITS>;
   static std::atomic<unsigned long long> done[2];
   cudaError_t e = allow_smem((const void *)routed_up_kernel<T, BITS, PIECES, ZP>, smem_up, done[0]);
@@ -567,9 +843,9 @@ cudaError_t layer_launch(const RoutedParams &p, const RoutedMaps &maps, const Ro
 }
 
 template <typename T>
-cudaError_t routed_typed(const RoutedParams &p, const RoutedMaps &maps, const RoutedDownMaps &down, bool bits4, int num_sms,
+cudaError_t routed_typed(const RoutedParams &p, const RoutedMaps &maps, const RoutedMaps &down, bool bits4, int num_sms,
                          cudaStream_t st) {
-  if (!bits4) return layer_launch<T, 16, 0, false>(p, maps, down, num_sms, st);
+  if (!bits4) return p.rows <= 16 ? tc_launch<T, 16>(p, maps, down, num_sms, st) : tc_launch<T, 32>(p, maps, down, num_sms, st);
   const bool zp = p.gate.zeros != nullptr;
   if (p.gate.group_shift == 5)
     return zp ? layer_launch<T, 4, 1, true>(p, maps, down, num_sms, st) : layer_launch<T, 4, 1, false>(p, maps, down, num_sms, st);
@@ -580,7 +856,7 @@ cudaError_t routed_typed(const RoutedParams &p, const RoutedMaps &maps, const Ro
 
 }  // namespace
 
-cudaError_t launch_routed(const RoutedParams &p, const RoutedMaps &maps, const RoutedDownMaps &down, bool f16, bool bits4,
+cudaError_t launch_routed(const RoutedParams &p, const RoutedMaps &maps, const RoutedMaps &down, bool f16, bool bits4,
                           int num_sms, cudaStream_t st) {
   return f16 ? routed_typed<__half>(p, maps, down, bits4, num_sms, st) : routed_typed<__nv_bfloat16>(p, maps, down, bits4, num_sms, st);
 }
