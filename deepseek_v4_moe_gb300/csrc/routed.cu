@@ -78,6 +78,7 @@ constexpr int kGroupsMax = kRoutedRows * kRoutedTopK + kRoutedShared;
 struct Choice {
   int up, down[kEightsMax];                        // entries
   int groups;                                      // experts with tokens, each once
+  int count[(kRoutedExperts + kRoutedShared + 31) / 32];
   uint16_t group_expert[kGroupsMax];
   uint32_t group_mask[kGroupsMax];
   uint32_t mask[kRoutedExperts];                   // each expert's tokens
@@ -94,9 +95,9 @@ __device__ __forceinline__ uint32_t rank_of(float v) {
   return v != v ? 1u : u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// A warp for each token: lane l holds experts l, l + 32, ...  Every thread of the CTA.
-__device__ __forceinline__ void choose(const RoutedParams &p, Choice &c, bool write) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+// A warp for each token: lane l holds experts l, l + 32, ...  Every thread of the CTA; ends with a barrier.
+__device__ __forceinline__ void choose_tokens(const RoutedParams &p, Choice &c, bool write) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5, each = (p.experts + 31) >> 5;
   constexpr int kEach = kRoutedExperts / 32;
   for (int e = threadIdx.x; e < p.experts; e += blockDim.x) c.mask[e] = 0u;
   __syncthreads();
@@ -105,15 +106,22 @@ __device__ __forceinline__ void choose(const RoutedParams &p, Choice &c, bool wr
     uint32_t key[kEach];
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
-      l[i] = 32 * i + lane < p.experts ? __ldcg(p.logits + t * p.experts + 32 * i + lane) : -INFINITY;
-      top = fmaxf(top, l[i]);
+      l[i] = -INFINITY;
+      if (i < each && 32 * i + lane < p.experts) l[i] = __ldcg(p.logits + t * p.experts + 32 * i + lane);
     }
     if (p.softmax) {
 #pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        if (i >= each) break;
+        top = fmaxf(top, l[i]);
+      }
+#pragma unroll
       for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
 #pragma unroll
-      for (int i = 0; i < kEach; ++i)
-        if (32 * i < p.experts) total += expf(l[i] - top);
+      for (int i = 0; i < kEach; ++i) {
+        if (i >= each) break;
+        total += expf(l[i] - top);
+      }
       total = warp_sum(total);
     }
     // without a bias the scores' order is the logits'
@@ -121,41 +129,37 @@ __device__ __forceinline__ void choose(const RoutedParams &p, Choice &c, bool wr
     for (int i = 0; i < kEach; ++i) {
       key[i] = 0u;
       const int e = 32 * i + lane;
-      if (e < p.experts) {
+      if (i < each && e < p.experts) {
         float v = l[i];
         if (p.bias) v = (p.softmax ? expf(v - top) / total : sigmoidf_(v)) + p.bias[e];
         key[i] = rank_of(v);
       }
     }
-    float mine = 0.f;  // lane s: the s-th choice's logit
-    int which = 0;
+    int which = 0;  // lane s: the s-th choice
     for (int s = 0; s < p.top_k; ++s) {
       uint32_t best = 0u;
       int at = 0;
 #pragma unroll
-      for (int i = 0; i < kEach; ++i)
+      for (int i = 0; i < kEach; ++i) {
+        if (i >= each) break;
         if (key[i] > best) {
           best = key[i];
           at = i;
         }
+      }
       const uint32_t most = __reduce_max_sync(0xffffffffu, best);
       const int e = (int)__reduce_min_sync(0xffffffffu, best == most ? (uint32_t)(32 * at + lane) : 0xFFFFFFFFu);
-      float logit = 0.f;
 #pragma unroll
-      for (int i = 0; i < kEach; ++i)
-        if (32 * i + lane == e) {
-          key[i] = 0u;
-          logit = l[i];
-        }
-      logit = __shfl_sync(0xffffffffu, logit, e & 31);
-      if (lane == s) {
-        mine = logit;
-        which = e;
+      for (int i = 0; i < kEach; ++i) {
+        if (i >= each) break;
+        if (32 * i + lane == e) key[i] = 0u;
       }
+      if (lane == s) which = e;
     }
+    const bool in = lane < p.top_k;
+    const float mine = in ? __ldcg(p.logits + t * p.experts + which) : 0.f;
     // The chosen scores over their sum.  Both are scaled by exp(-m), m the largest of min(l, 0) (or of l): far out
     // every score may be 0 in f32 where their ratios are not.
-    const bool in = lane < p.top_k;
     float w;
     if (p.normalise) {
       float m = in ? (p.softmax ? mine : fminf(mine, 0.f)) : -INFINITY;
@@ -181,9 +185,39 @@ __device__ __forceinline__ void choose(const RoutedParams &p, Choice &c, bool wr
     }
   }
   __syncthreads();
+}
+
+// The experts with tokens, each once, in the order of their numbers.  A warp for each 32 of them.
+__device__ __forceinline__ void choose_groups(const RoutedParams &p, Choice &c, bool write) {
+  choose_tokens(p, c, write);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const int all = p.experts + p.shared, parts = (all + 31) >> 5;
+  auto tokens_of = [&](int e) { return e < p.experts ? c.mask[e] : e < all ? 0xFFFFFFFFu >> (32 - p.rows) : 0u; };
+  for (int i = warp; i < parts; i += warps) {
+    const uint32_t has = __ballot_sync(0xffffffffu, tokens_of(32 * i + lane) != 0u);
+    if (lane == 0) c.count[i] = __popc(has);
+  }
+  __syncthreads();
+  for (int i = warp; i < parts; i += warps) {
+    const uint32_t mask = tokens_of(32 * i + lane), has = __ballot_sync(0xffffffffu, mask != 0u);
+    const int before = __reduce_add_sync(0xffffffffu, lane < i ? c.count[lane] : 0);
+    if (mask) {
+      const int g = before + __popc(has & ((1u << lane) - 1u));
+      c.group_expert[g] = (uint16_t)(32 * i + lane);
+      c.group_mask[g] = mask;
+    }
+    if (i == parts - 1 && lane == 0) c.groups = before + __popc(has);
+  }
+  __syncthreads();
+}
+
+// The same as lists of eights of tokens.
+__device__ __forceinline__ void choose(const RoutedParams &p, Choice &c, bool write) {
+  choose_tokens(p, c, write);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == 0) {
     const int all = p.experts + p.shared;
-    int up = 0, down[kEightsMax] = {}, groups = 0;
+    int up = 0, down[kEightsMax] = {};
     for (int e0 = 0; e0 < all; e0 += 32) {
       const int e = e0 + lane;
       uint32_t mask = e < p.experts ? c.mask[e] : e < all ? 0xFFFFFFFFu >> (32 - p.rows) : 0u;
@@ -193,13 +227,6 @@ __device__ __forceinline__ void choose(const RoutedParams &p, Choice &c, bool wr
         if (mask >> (8 * j) & 255u) c.down_expert[j][down[j] + __popc(has & ((1u << lane) - 1u))] = (uint16_t)e;
         down[j] += __popc(has);
       }
-      const uint32_t any = __ballot_sync(0xffffffffu, mask != 0u);
-      if (mask) {
-        const int g = groups + __popc(any & ((1u << lane) - 1u));
-        c.group_expert[g] = (uint16_t)e;
-        c.group_mask[g] = mask;
-      }
-      groups += __popc(any);
       const int passes = (__popc(mask) + 7) / 8;
       int at = passes;  // the entries of the lanes up to this one
 #pragma unroll
@@ -220,7 +247,6 @@ __device__ __forceinline__ void choose(const RoutedParams &p, Choice &c, bool wr
     }
     if (lane == 0) {
       c.up = up;
-      c.groups = groups;
 #pragma unroll
       for (int j = 0; j < kEightsMax; ++j) c.down[j] = down[j];
     }
@@ -587,7 +613,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // The down kernel's CTAs may come, choose and fetch weights: not earlier, as they read the logits.
     pdl_trigger();
   }
-  choose(p, c, UP && blockIdx.x == 0);
+  choose_groups(p, c, UP && blockIdx.x == 0);
   volatile int *abort_p = &abort_flag;
   const Waits &w = p.waits;
   const int rows8 = (p.rows + 7) / 8 * 8, depth = UP ? p.hidden : p.inter, steps = (depth + 63) / 64;
@@ -733,10 +759,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
     }
   }
-  // Copies still in flight after an abort land before the CTA may leave (bounded; in a normal run each has landed).
+  // Copies still in flight after an abort land before the CTA may leave (bounded; otherwise each has landed).
   tc_fence_before();
   __syncthreads();
-  if (threadIdx.x == 0) {
+  if (abort_flag && threadIdx.x == 0) {
     int no_abort = 0;
     for (int s = 0; s < kTcStages; ++s) {
       const int n = issued / kTcStages + (s < issued % kTcStages ? 1 : 0);
@@ -749,12 +775,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int part = kTcRows / splits, row0 = rank * part;
     for (int i = threadIdx.x; i < part * p.rows; i += kTcThreads) {
       const int row = row0 + i % part, t = i / part, at = tile_down * kTcRows + row;
-      float v = 0.f;
-      for (int r = 0; r < splits; ++r) {
-        float x;
-        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(in_cta(&sums[0][t * kTcRows + row], r)) : "memory");
-        v += x;
-      }
+      float v = 0.f, x[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r)  // all loads before the first sum
+        if (r < splits)
+          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x[r]) : "r"(in_cta(&sums[0][t * kTcRows + row], r)) : "memory");
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        if (r < splits) v += x[r];
       if (at < p.hidden) static_cast<T *>(p.y)[t * p.ld_y + at] = from_f32<T>(v);
     }
     if (splits > 1) cluster_sync();
