@@ -95,69 +95,59 @@ __device__ __forceinline__ uint32_t rank_of(float v) {
   return v != v ? 1u : u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// A warp for each token: lane l holds experts l, l + 32, ...  Every thread of the CTA; ends with a barrier.
-__device__ __forceinline__ void choose_tokens(const RoutedParams &p, Choice &c, bool write) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5, each = (p.experts + 31) >> 5;
-  constexpr int kEach = kRoutedExperts / 32;
+// A warp for each token.  Every thread of the CTA; ends with a barrier.  keys: 512 words of shared memory for each warp.
+// The loops are kept short: a kernel runs this code once, and its way into the instruction caches took most of its time
+// while the experts were held in registers (16 of them a lane, each loop unrolled: 8.7 us of one token of 256 experts).
+__device__ __forceinline__ void choose_tokens(const RoutedParams &p, Choice &c, uint32_t *keys, bool write) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  uint32_t *key = keys + warp * kRoutedExperts;
   for (int e = threadIdx.x; e < p.experts; e += blockDim.x) c.mask[e] = 0u;
   __syncthreads();
+#pragma unroll 1
   for (int t = warp; t < p.rows; t += warps) {
-    float l[kEach], top = -INFINITY, total = 0.f;
-    uint32_t key[kEach];
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      l[i] = -INFINITY;
-      if (i < each && 32 * i + lane < p.experts) l[i] = __ldcg(p.logits + t * p.experts + 32 * i + lane);
-    }
-    if (p.softmax) {
-#pragma unroll
-      for (int i = 0; i < kEach; ++i) {
-        if (i >= each) break;
-        top = fmaxf(top, l[i]);
-      }
+    const float *logits = p.logits + t * p.experts;
+    float top = -INFINITY, total = 0.f;
+    if (p.softmax && (p.bias || !p.normalise)) {  // a score itself is wanted, not ratios or the order alone
+#pragma unroll 4
+      for (int e = lane; e < p.experts; e += 32) top = fmaxf(top, __ldcg(logits + e));
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-#pragma unroll
-      for (int i = 0; i < kEach; ++i) {
-        if (i >= each) break;
-        total += expf(l[i] - top);
-      }
+#pragma unroll 1
+      for (int e = lane; e < p.experts; e += 32) total += expf(__ldcg(logits + e) - top);
       total = warp_sum(total);
     }
-    // without a bias the scores' order is the logits'
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      key[i] = 0u;
-      const int e = 32 * i + lane;
-      if (i < each && e < p.experts) {
-        float v = l[i];
-        if (p.bias) v = (p.softmax ? expf(v - top) / total : sigmoidf_(v)) + p.bias[e];
-        key[i] = rank_of(v);
+    if (p.bias) {
+#pragma unroll 1
+      for (int e = lane; e < p.experts; e += 32) {
+        const float l = __ldcg(logits + e);
+        key[e] = rank_of((p.softmax ? expf(l - top) / total : sigmoidf_(l)) + p.bias[e]);
       }
+    } else {  // the scores' order is the logits'
+#pragma unroll 8
+      for (int e = lane; e < p.experts; e += 32) key[e] = rank_of(__ldcg(logits + e));
     }
+    __syncwarp();
     int which = 0;  // lane s: the s-th choice
+#pragma unroll 1
     for (int s = 0; s < p.top_k; ++s) {
       uint32_t best = 0u;
-      int at = 0;
-#pragma unroll
-      for (int i = 0; i < kEach; ++i) {
-        if (i >= each) break;
-        if (key[i] > best) {
-          best = key[i];
-          at = i;
+      int at = 0x7FFFFFFF;
+#pragma unroll 8
+      for (int e = lane; e < p.experts; e += 32) {
+        const uint32_t k = key[e];
+        if (k > best) {
+          best = k;
+          at = e;
         }
       }
       const uint32_t most = __reduce_max_sync(0xffffffffu, best);
-      const int e = (int)__reduce_min_sync(0xffffffffu, best == most ? (uint32_t)(32 * at + lane) : 0xFFFFFFFFu);
-#pragma unroll
-      for (int i = 0; i < kEach; ++i) {
-        if (i >= each) break;
-        if (32 * i + lane == e) key[i] = 0u;
-      }
+      const int e = (int)__reduce_min_sync(0xffffffffu, best == most ? (uint32_t)at : 0xFFFFFFFFu);
+      if (lane == (e & 31)) key[e] = 0u;
+      __syncwarp();
       if (lane == s) which = e;
     }
     const bool in = lane < p.top_k;
-    const float mine = in ? __ldcg(p.logits + t * p.experts + which) : 0.f;
+    const float mine = in ? __ldcg(logits + which) : 0.f;
     // The chosen scores over their sum.  Both are scaled by exp(-m), m the largest of min(l, 0) (or of l): far out
     // every score may be 0 in f32 where their ratios are not.
     float w;
@@ -165,7 +155,8 @@ __device__ __forceinline__ void choose_tokens(const RoutedParams &p, Choice &c, 
       float m = in ? (p.softmax ? mine : fminf(mine, 0.f)) : -INFINITY;
 #pragma unroll
       for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      w = !in ? 0.f : p.softmax ? expf(mine - m) : expf(fminf(mine, 0.f) - m) / (1.f + expf(-fabsf(mine)));
+      w = !in ? 0.f : expf((p.softmax ? mine : fminf(mine, 0.f)) - m);
+      if (!p.softmax) w /= 1.f + expf(-fabsf(mine));
       float sum = w;
 #pragma unroll
       for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -188,8 +179,8 @@ __device__ __forceinline__ void choose_tokens(const RoutedParams &p, Choice &c, 
 }
 
 // The experts with tokens, each once, in the order of their numbers.  A warp for each 32 of them.
-__device__ __forceinline__ void choose_groups(const RoutedParams &p, Choice &c, bool write) {
-  choose_tokens(p, c, write);
+__device__ __forceinline__ void choose_groups(const RoutedParams &p, Choice &c, uint32_t *keys, bool write) {
+  choose_tokens(p, c, keys, write);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int all = p.experts + p.shared, parts = (all + 31) >> 5;
   auto tokens_of = [&](int e) { return e < p.experts ? c.mask[e] : e < all ? 0xFFFFFFFFu >> (32 - p.rows) : 0u; };
@@ -212,8 +203,8 @@ __device__ __forceinline__ void choose_groups(const RoutedParams &p, Choice &c, 
 }
 
 // The same as lists of eights of tokens.
-__device__ __forceinline__ void choose(const RoutedParams &p, Choice &c, bool write) {
-  choose_tokens(p, c, write);
+__device__ __forceinline__ void choose(const RoutedParams &p, Choice &c, uint32_t *keys, bool write) {
+  choose_tokens(p, c, keys, write);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == 0) {
     const int all = p.experts + p.shared;
@@ -565,7 +556,7 @@ constexpr int kTcThreads = 192, kTcRows = 128, kTcW = kTcRows * 128;
 template <int NC>
 constexpr int kTcStage = kTcW + NC * 128;
 template <int NC>
-constexpr int kTcRing = NC == 16 ? 11 : 9;
+constexpr int kTcRing = NC == 16 ? 5 : 4;  // two CTAs on an SM: the down kernel's come while the up kernel's end
 template <int NC>
 constexpr size_t kTcSmem = kTcRing<NC> * kTcStage<NC> + 1024;
 
@@ -577,7 +568,7 @@ __device__ __forceinline__ void read_accumulator(uint32_t at, float (&v)[NC]) {
 }
 
 template <bool UP, typename T, int NC>
-__global__ void __launch_bounds__(kTcThreads, 1)
+__global__ void __launch_bounds__(kTcThreads, 2)
     routed_tc_kernel(const __grid_constant__ RoutedParams p, const __grid_constant__ RoutedMaps maps, int splits) {
   constexpr int kTcStages = kTcRing<NC>;
   extern __shared__ char smem[];
@@ -613,7 +604,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // The down kernel's CTAs may come, choose and fetch weights: not earlier, as they read the logits.
     pdl_trigger();
   }
-  choose_groups(p, c, UP && blockIdx.x == 0);
+  choose_groups(p, c, reinterpret_cast<uint32_t *>(ring), UP && blockIdx.x == 0);  // (the ring is not in use yet)
   volatile int *abort_p = &abort_flag;
   const Waits &w = p.waits;
   const int rows8 = (p.rows + 7) / 8 * 8, depth = UP ? p.hidden : p.inter, steps = (depth + 63) / 64;
@@ -664,6 +655,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int g0 = group, k0 = k;
       for (; j < kTcStages && step < end; ++j, next()) weights(j);
       pdl_wait();
+      pdl_trigger();
       int g = g0, kk = k0;
       for (int i = 0; i < j; ++i) {
         tokens(i, g, kk);
@@ -805,12 +797,12 @@ cudaError_t tc_launch(const RoutedParams &p, const RoutedMaps &maps, const Route
   const long long groups = (p.rows * p.top_k < p.experts ? p.rows * p.top_k : p.experts) + p.shared;
   const long long units = groups * ((p.inter + 63) / 64);
   if (e == cudaSuccess)
-    e = launch_pdl(routed_tc_kernel<true, T, NC>, dim3((unsigned)(units < num_sms ? units : num_sms)), dim3(kTcThreads), kTcSmem<NC>, st, p,
+    e = launch_pdl(routed_tc_kernel<true, T, NC>, dim3((unsigned)(units < 2 * num_sms ? units : 2 * num_sms)), dim3(kTcThreads), kTcSmem<NC>, st, p,
                    maps, 1);
   if (e != cudaSuccess) return e;
-  // as many CTAs to a tile as run at one time (of clusters of 8, 4 and 2 on 152 SMs 16, 36 and 75)
+  // as many CTAs to a tile as run at one time, two on an SM (of clusters of 8, 4 and 2 on 152 SMs 32, 72 and 150)
   const int tiles = (p.hidden + kTcRows - 1) / kTcRows;
-  const int splits = tiles <= num_sms * 16 / 152 ? 8 : tiles <= num_sms * 36 / 152 ? 4 : tiles <= num_sms * 75 / 152 ? 2 : 1;
+  const int splits = tiles <= num_sms * 32 / 152 ? 8 : tiles <= num_sms * 72 / 152 ? 4 : tiles <= num_sms * 150 / 152 ? 2 : 1;
   return launch_clusters(routed_tc_kernel<false, T, NC>, kTcSmem<NC>, done[1], tiles, splits, kTcThreads, st, p, down, splits);
 }
 
@@ -829,7 +821,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, 2)
   pdl_wait();
   // The down kernel's CTAs may come, choose and fetch weights: not earlier, as they read the logits.
   pdl_trigger();
-  choose(p, c, blockIdx.x == 0);
+  choose(p, c, reinterpret_cast<uint32_t *>(ring), blockIdx.x == 0);
   const int strips = (p.inter + 15) / 16;
   UpJob<T, BITS, PIECES, ZP> job{p, maps, c, c.up * strips, (p.hidden + kTileK<BITS> - 1) / kTileK<BITS>, p.hidden, strips};
   job.t.x.set(0, 8);
@@ -842,7 +834,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, 2)
   extern __shared__ char smem[];
   __shared__ Choice c;
   char *ring = smem + (-smem_u32(smem) & (kAlign - 1));
-  choose(p, c, false);
+  choose(p, c, reinterpret_cast<uint32_t *>(ring), false);
   const int eights = (p.rows + 7) / 8;
   DownJob<T, BITS, PIECES, ZP> job{p, maps, c, (p.hidden + 15) / 16 * eights, (p.inter + kTileK<BITS> - 1) / kTileK<BITS>, p.inter, eights};
   job.t.x.set(0, 8);
