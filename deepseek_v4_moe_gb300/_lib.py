@@ -104,7 +104,8 @@ class MoeFfnInt4WeightsArgs(ctypes.Structure):
 
 class MoeFfnInt4MatmulArgs(ctypes.Structure):
     _fields_ = [("rows", c_i32), ("n", c_i32), ("k", c_i32), ("type", c_i32), ("group", c_i32), ("x", c_vp),
-                ("ld_x", c_i64), ("codes", c_vp), ("scales", c_vp), ("zeros", c_vp), ("out", c_vp), ("ld_out", c_i64)]
+                ("ld_x", c_i64), ("codes", c_vp), ("scales", c_vp), ("zeros", c_vp), ("out", c_vp), ("ld_out", c_i64),
+                ("workspace", c_vp), ("workspace_bytes", c_sz)]
 
 
 SCORES = {"sigmoid": 0, "softmax": 1}
@@ -221,6 +222,8 @@ def load(build: bool = True):
     lib.moe_ffn_int4_widen.restype = ctypes.c_int
     lib.moe_ffn_int4_matmul.argtypes = [ctypes.POINTER(MoeFfnInt4MatmulArgs), vp]
     lib.moe_ffn_int4_matmul.restype = ctypes.c_int
+    lib.moe_ffn_int4_matmul_workspace.argtypes = [ctypes.POINTER(MoeFfnInt4MatmulArgs)]
+    lib.moe_ffn_int4_matmul_workspace.restype = c_i64
     lib.moe_ffn_routed_forward.argtypes = [ctypes.POINTER(MoeFfnRoutedArgs), vp]
     lib.moe_ffn_routed_forward.restype = ctypes.c_int
     lib.moe_ffn_routed_workspace.argtypes = [ctypes.POINTER(MoeFfnRoutedArgs)]

@@ -563,6 +563,14 @@ Tensor int4_matmul(const Tensor &x, py::object o, Maybe out) {
   if (!out) out = fresh(w, {rows, n}, t);
   a.ld_out = matrix(w, "out", *out, {rows, n}, t);
   a.out = out->data_ptr();
+  const int64_t need = moe_ffn_int4_matmul_workspace(&a);
+  check(need);
+  Tensor ws;
+  if (need) {
+    ws = fresh(w, {need}, ScalarType::Byte);
+    a.workspace = ws.data_ptr();
+    a.workspace_bytes = (size_t)need;
+  }
   check(moe_ffn_int4_matmul(&a, w.stream));
   written(given);
   return *out;

@@ -16,10 +16,14 @@ int check_group(const char *who, int group) {
 }
 bool type16(int t) { return t == MOE_FFN_BF16 || t == MOE_FFN_F16; }
 
-int check_int4(const char *who, int64_t n, int64_t k, int group, const void *codes, const void *scales, const void *zeros) {
+int check_int4_sizes(const char *who, int64_t n, int64_t k, int group) {
   if (n < 1 || n > kCodeRowsMax || k < 32 || k % 32 || k > kCodesMax)
     return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: n must be in 1..2^24, k a multiple of 32 in 32..2^20", who);
-  const int rc = check_group(who, group);
+  return check_group(who, group);
+}
+
+int check_int4(const char *who, int64_t n, int64_t k, int group, const void *codes, const void *scales, const void *zeros) {
+  const int rc = check_int4_sizes(who, n, k, group);
   if (rc) return rc;
   if (!codes || !scales) return fail(MOE_FFN_ERR_NULL_PTR, "%s: codes or scales is NULL", who);
   if (!aligned(codes, 16) || !aligned(scales, 16) || !aligned(zeros, 16))
@@ -120,20 +124,58 @@ extern "C" int moe_ffn_int4_widen(const moe_ffn_int4_weights_args *a, void *out,
   return launched(who, moe::launch_int4_widen(p, sms, static_cast<cudaStream_t>(stream)));
 }
 
-extern "C" int moe_ffn_int4_matmul(const moe_ffn_int4_matmul_args *a, void *stream) {
-  const char *who = "int4_matmul";
+namespace {
+
+// where the parts of the FP8 form lie in the workspace
+struct Int4Space {
+  int64_t sums, back, bytes;
+  int groups, rows;  // rows of the planes
+};
+Int4Space int4_space(const moe_ffn_int4_matmul_args *a, int tokens) {
+  Int4Space s;
+  const int planes = a->type == MOE_FFN_F16 ? 3 : 2;
+  const int64_t blocks = (a->rows + tokens - 1) / tokens;
+  s.groups = (int)((a->k + 127) / 128 * (128 / a->group));
+  s.rows = (int)(blocks * planes * tokens);
+  s.sums = ((int64_t)s.rows * a->k + 255) / 256 * 256;
+  s.back = s.sums + (blocks * s.groups * tokens * 4 + 255) / 256 * 256;
+  s.bytes = s.back + (int64_t)a->rows * 4;
+  return s;
+}
+
+int check_int4_matmul(const char *who, const moe_ffn_int4_matmul_args *a) {
   if (!a) return fail(MOE_FFN_ERR_NULL_PTR, "%s: args is NULL", who);
   if (a->rows == 0) return fail(MOE_FFN_ERR_ROWS_ZERO, "%s: rows must be at least 1", who);
   if (a->rows < 0 || a->rows > (1 << 16)) return fail(MOE_FFN_ERR_ROWS_RANGE, "%s: rows must be at most 2^16", who);
   if (!type16(a->type)) return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: type must be bf16 or f16", who);
-  int rc = check_int4(who, a->n, a->k, a->group, a->codes, a->scales, a->zeros);
+  return check_int4_sizes(who, a->n, a->k, a->group);
+}
+
+}  // namespace
+
+extern "C" int64_t moe_ffn_int4_matmul_workspace(const moe_ffn_int4_matmul_args *a) {
+  const int rc = check_int4_matmul("int4_matmul_workspace", a);
+  if (rc) return rc;
+  const int sms = current_sms();
+  if (sms < 0) return sms;
+  const int tokens = moe::int4_tc_tokens(a->rows, a->n, a->k, a->type == MOE_FFN_F16, sms);
+  return tokens ? int4_space(a, tokens).bytes : 0;
+}
+
+extern "C" int moe_ffn_int4_matmul(const moe_ffn_int4_matmul_args *a, void *stream) {
+  const char *who = "int4_matmul";
+  int rc = check_int4_matmul(who, a);
+  if (rc) return rc;
+  rc = check_int4(who, a->n, a->k, a->group, a->codes, a->scales, a->zeros);
   if (rc) return rc;
   const int64_t R = a->rows, N = a->n, K = a->k, G = (K + a->group - 1) / a->group;
   if ((rc = check_rows16(who, "x", a->x, a->ld_x, K)) || (rc = check_rows2(who, "out", a->out, a->ld_out, N))) return rc;
   const Span ins[] = {span("x", a->x, R, K, a->ld_x, 2), span("codes", a->codes, N, K / 2, K / 2, 1),
                       span("scales", a->scales, N, G, G, 2), span("zeros", a->zeros, N, G, G, 1)};
-  const Span outs[] = {span("out", a->out, R, N, a->ld_out, 2)};
-  if ((rc = check_overlaps(who, outs, 1, ins, 4, -1, -1))) return rc;
+  if (!aligned(a->workspace, 256)) return fail(MOE_FFN_ERR_ALIGNMENT, "%s: workspace is not 256-byte aligned", who);
+  const Span outs[] = {span("out", a->out, R, N, a->ld_out, 2),
+                       span("workspace", a->workspace, 1, (int64_t)a->workspace_bytes, 0, 1)};
+  if ((rc = check_overlaps(who, outs, 2, ins, 4, -1, -1))) return rc;
   const int sms = current_sms();
   if (sms < 0) return sms;
   if ((rc = pending(who))) return rc;
@@ -147,12 +189,29 @@ extern "C" int moe_ffn_int4_matmul(const moe_ffn_int4_matmul_args *a, void *stre
   DeviceSide dev;
   if ((rc = device_side(who, &dev))) return rc;
   p.waits = moe::Waits{dev.status, dev.wait_ns, dev.inject};
-  const moe::Int4Tiles t = moe::int4_pick_tiles(a->rows, a->n, a->k, sms);
+  const bool f16 = a->type == MOE_FFN_F16;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
   moe::Int4Maps maps;
+  if (const int tokens = moe::int4_tc_tokens(a->rows, a->n, a->k, f16, sms)) {
+    const Int4Space space = int4_space(a, tokens);
+    if (!a->workspace) return fail(MOE_FFN_ERR_NULL_PTR, "%s: workspace is NULL", who);
+    if (a->workspace_bytes < (size_t)space.bytes)
+      return fail(MOE_FFN_ERR_NO_MEMORY, "%s: workspace of %zu bytes, needs %lld", who, a->workspace_bytes, (long long)space.bytes);
+    char *ws = static_cast<char *>(a->workspace);
+    p.planes = reinterpret_cast<uint2 *>(ws);
+    p.sums = reinterpret_cast<float *>(ws + space.sums);
+    p.back = reinterpret_cast<float *>(ws + space.back);
+    p.sum_groups = space.groups;
+    if (!encode_map(&maps.w, a->codes, 1, K / 2, N, K / 2, 128, 64) ||
+        !encode_map(&maps.x, ws, 1, K, space.rows, K, tokens * (f16 ? 3 : 2)))
+      return fail(MOE_FFN_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", who);
+    return launched(who, moe::launch_int4_tc(p, maps, tokens, f16, sms, st));
+  }
+  const moe::Int4Tiles t = moe::int4_pick_tiles(a->rows, a->n, a->k, sms);
   if (!encode_map(&maps.w, a->codes, 1, K / 2, N, K / 2, t.w_box(), 64) ||
       !encode_pieces(&maps.x, a->x, K / 32, R, a->ld_x, t.box_rows, t.x_box_pieces()))
     return fail(MOE_FFN_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", who);
-  return launched(who, moe::launch_int4_matmul(p, maps, t, a->type == MOE_FFN_F16, sms, static_cast<cudaStream_t>(stream)));
+  return launched(who, moe::launch_int4_matmul(p, maps, t, f16, sms, st));
 }
 
 namespace {

@@ -32,11 +32,20 @@ struct Int4MatmulParams {
   void *out;
   long long ld_x, ld_out;
   Waits waits;
+  // Workspace of the FP8 tensor cores' form: x as planes of codes [blocks of tokens][planes][tokens][k], the groups' sums
+  // [blocks][sum_groups][tokens], what the rows' sums are multiplied by.
+  uint2 *planes;
+  float *sums, *back;
+  int sum_groups;  // groups of a row, up to a whole tile of 128 columns
 };
-// w: the codes, boxes of 64 bytes x the rows of a CTA's sets; x: pieces of 32 columns, boxes of those of a step's tiles
+// tokens of a block in that form, for so many rows; 0: the other form serves the call
+int int4_tc_tokens(int rows, int n, int k, bool f16, int num_sms);
+// w: the codes, boxes of 64 bytes x the rows of a CTA's sets; x: pieces of 32 columns, boxes of those of a step's tiles.  FP8
+// form: w the codes, boxes of 64 bytes x 128 rows; x the planes, boxes of 128 bytes x a block's rows
 struct Int4Maps {
   CUtensorMap w, x;
 };
+cudaError_t launch_int4_tc(const Int4MatmulParams &p, const Int4Maps &maps, int tokens, bool f16, int num_sms, cudaStream_t st);
 // strips of 16 rows and eights of tokens of a warp, shares of k (2^log_kw), tokens of a copy of x
 struct Int4Tiles {
   int strips, eights, log_kw, box_rows;

@@ -1,0 +1,386 @@
+// 4-bit weights on the FP8 tensor cores (sm_103a): the pipeline that the product of a few rows and the routed layer share.
+//
+// A code 0 .. 15 in a byte is the E4M3 number code 2^-9: its first eight are the subnormal numbers, the next eight have the
+// smallest exponent, and both count in steps of 2^-9.  So three instructions (a mask, a shift, a mask) make eight codes an
+// operand of the tensor cores, where sixteen-bit ones take 11, and the weights come from memory, through registers, into
+// TMEM as the left operand.  (On mma.sync in 16 bits 16 tokens by 129280 x 4096 took 93 us, at 25 instructions for eight
+// codes; mma.sync's FP8 form is made of 16-bit products, with a conversion of either operand each time: 146 us.)
+//
+// The right operand is split beforehand: scaled by a power of two, so that its largest magnitude lies in [128, 256), into
+// p0 = e4m3(x), p1 = e4m3(32 (x - p0)) and, for f16, p2 = e4m3(32 (32 (x - p0) - p1)).  Each plane takes four significant
+// bits, so that two are a bf16 number and three an f16 one: exactly down to 2^-14 of the largest magnitude, below that to
+// 2^-22 of it (f16: 2^-27).  The planes are columns of their own; a group's products are joined in f32, its zero point is
+// applied to its sum of x, and its scale to the result, once for each group:
+//   acc += scale (sum(code p0) + sum(code p1) / 32 + .. - zero sum(x))
+//
+// Roles: a warp copies (TMA), one issues the products, eight make codes operands (two sets of four, every other tile: a
+// thread has a row of 128 columns), four join the groups (a thread has a row, its sums of all tokens in registers).
+#pragma once
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "dense_tc.cuh"
+#include "dense_vec.cuh"
+#include "few.h"
+
+namespace moe {
+
+constexpr int kCodeThreads = 32 * 14, kCodeRows = 128, kCodeTile = 128;  // rows, and columns, of a tile
+constexpr int kCodeW = kCodeRows * 64;                                   // its bytes
+constexpr int kCodeA = 4, kCodeD = 4;                                    // slots in TMEM of left operands and of sums
+constexpr float kPlane = 0.03125f;
+
+// TOKENS: 8, 16 or 32; PLANES: 2 or 3; GROUPS of a tile: 1, 2 or 4
+template <int TOKENS, int PLANES, int GROUPS>
+struct CodeCfg {
+  static constexpr int kRows = TOKENS * PLANES;                 // of the right operand
+  static constexpr int kN = (kRows + 15) / 16 * 16;             // columns of the sums
+  static constexpr int kB = kN * 128, kSums = GROUPS * TOKENS * 4;
+  static constexpr int kStage = kCodeW + kB + (kSums + 1023) / 1024 * 1024;
+  static constexpr int kStages = 180 * 1024 / kStage < 12 ? 180 * 1024 / kStage : 12;
+  static constexpr int kRing = kStages * kStage;
+  static constexpr uint32_t kBytes = kCodeW + kRows * 128 + kSums;
+  static constexpr int kTmem = 512;
+  static_assert(kCodeA * 32 + kCodeD * kN <= kTmem, "TMEM");
+};
+
+// A row's power of two: what is split is x 2^e; max: the largest magnitude's bits as f32.  (Values below 2^-119 count as
+// that: the sums' way back has to be a normal number.)
+__device__ __forceinline__ int plane_exponent(uint32_t max) {
+  const int e = 7 + 127 - (int)(max >> 23);
+  return e > 126 ? 126 : e;
+}
+__device__ __forceinline__ float two_to(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+
+__device__ __forceinline__ float2 e4m3_pair(uint32_t c) {
+  uint32_t f;
+  asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %1;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n}" : "=r"(f) : "r"(c));
+  return __half22float2(*reinterpret_cast<const __half2 *>(&f));
+}
+// the planes' codes of two scaled values, in the low 16 bits of o[plane]; returns the sum of what they stand for
+template <int PLANES>
+__device__ __forceinline__ float split2(float a, float b, uint32_t (&o)[PLANES]) {
+  float sum = 0.f, unit = 1.f;
+#pragma unroll
+  for (int i = 0; i < PLANES; ++i) {
+    o[i] = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    const float2 v = e4m3_pair(o[i]);
+    sum = fmaf(v.x + v.y, unit, sum);
+    a = (a - v.x) * 32.f;
+    b = (b - v.y) * 32.f;
+    unit *= kPlane;
+  }
+  return sum;
+}
+// Eight values' codes of each plane as they stand in the operand: even columns, then odd ones, as a word's codes leave them.
+template <int PLANES>
+__device__ __forceinline__ float split8(const float (&v)[8], float scale, uint2 (&o)[PLANES]) {
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < PLANES; ++i) o[i] = make_uint2(0u, 0u);
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      uint32_t c[PLANES];
+      sum += split2<PLANES>(v[4 * j + h] * scale, v[4 * j + 2 + h] * scale, c);
+#pragma unroll
+      for (int i = 0; i < PLANES; ++i) (h ? o[i].y : o[i].x) |= c[i] << (16 * j);
+    }
+  return sum;
+}
+
+// instruction descriptor, kind::f8f6f4: E4M3 operands (K-major), f32 sums, M x N
+__device__ __forceinline__ uint32_t idesc_e4m3(int M, int N) { return 1u << 4 | (uint32_t)(N >> 3) << 17 | (uint32_t)(M >> 4) << 24; }
+
+// D (+)= A B^T, A (128 rows x 32 columns, a byte each) in TMEM, B from shared memory; by one lane of a converged warp
+__device__ __forceinline__ void mma_codes_one(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// 32 columns of this thread's TMEM lane
+__device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
+      "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]),
+      "r"(r[31])
+      : "memory");
+}
+// N columns of this thread's lane in sixteens `apart` columns from one another, waited for
+template <int N>
+__device__ __forceinline__ void tmem_columns(uint32_t at, int apart, float (&v)[N]) {
+  if (apart < 16) apart = 16;  // eight tokens: their planes side by side
+#pragma unroll
+  for (int i = 0; i < N; i += 16)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];"
+        : "=f"(v[i]), "=f"(v[i + 1]), "=f"(v[i + 2]), "=f"(v[i + 3]), "=f"(v[i + 4]), "=f"(v[i + 5]), "=f"(v[i + 6]),
+          "=f"(v[i + 7]), "=f"(v[i + 8]), "=f"(v[i + 9]), "=f"(v[i + 10]), "=f"(v[i + 11]), "=f"(v[i + 12]), "=f"(v[i + 13]),
+          "=f"(v[i + 14]), "=f"(v[i + 15])
+        : "r"(at + i / 16 * apart));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
+}
+// a piece of memory into this CTA's shared memory, by one lane of a converged warp (bytes a multiple of 16)
+__device__ __forceinline__ void tma_bulk_one(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n\t}" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+struct CodeBars {
+  uint64_t full[12], empty[12], afull[kCodeA], aempty[kCodeA], dfull[kCodeD], dempty[kCodeD], mma_done, never;
+  uint32_t tmem;
+  int abort_flag, issued;
+};
+
+// The kernel's body.  A job gives this CTA's tiles, the same to every role:
+//   Place begin();  place.more(), place.next()               a tile, one after another through the CTA's units
+//   bool ends(place)                                         a unit's last tile
+//   void weights(place, at, bar)                             its codes' copy, by the converged warp
+//   void ready();  void tokens(place, at, sums, bar)         what the tokens' copies wait for; they, and their groups' sums
+//   Row; void row_at(row, place, r); void take(row, place, scale, zero)   row r's scales and zero points, a tile ahead
+//   kFactors; void factors(sums, group, token, f)            what four tokens' sums of the group are multiplied by
+//   void finish(place, r, acc, ok)
+template <typename C, int TOKENS, int PLANES, int GROUPS, typename Job>
+__device__ __forceinline__ void code_pipeline(Job &job, char *ring, CodeBars &b, const Waits &w) {
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  constexpr int S = C::kStages;
+  volatile int *abort_p = &b.abort_flag;
+  const uint32_t ring0 = smem_u32(ring), tmem = b.tmem, tmem_d = tmem + kCodeA * 32;
+  if (warp == 0) {
+    // ---------------- copies ----------------
+    RingPos<S> pos;
+    int j = 0;
+    auto weights = [&](const auto &p, int s) {
+      mbar_expect_one(smem_u32(&b.full[s]), C::kBytes);
+      job.weights(p, ring0 + s * C::kStage, smem_u32(&b.full[s]));
+    };
+    auto tokens = [&](const auto &p, int s) {
+      job.tokens(p, ring0 + s * C::kStage + kCodeW, ring0 + s * C::kStage + kCodeW + C::kB, smem_u32(&b.full[s]));
+    };
+    auto p = job.begin(), early = p;
+    for (; j < S && p.more(); ++j, p.next()) weights(p, j);  // these need not wait for the tokens
+    job.ready();
+    for (int i = 0; i < j; ++i, early.next(), pos.next()) tokens(early, i);
+    for (; p.more(); ++j, pos.next(), p.next()) {
+      if (!warp_wait(&b.empty[pos.slot], pos.round ^ 1u, abort_p, w.status, w.ns)) break;
+      weights(p, pos.slot);
+      tokens(p, pos.slot);
+    }
+    if (lane == 0) b.issued = j;
+  } else if (warp == 1) {
+    // ---------------- products ----------------
+    if (w.inject && blockIdx.x == 0) (void)warp_wait(&b.never, 0u, abort_p, w.status, w.ns);  // test hook: a wait that runs out
+    const uint32_t idesc = idesc_e4m3(kCodeRows, C::kN);
+    const uint64_t b0 = smem_desc_sw128(ring0 + kCodeW);
+    RingPos<S> pos;
+    RingPos<kCodeA> a;
+    RingPos<kCodeD> d;
+    bool ok = true;
+    for (auto p = job.begin(); ok && p.more(); p.next(), pos.next(), a.next()) {
+      ok = warp_wait(&b.full[pos.slot], pos.round, abort_p, w.status, w.ns) &&
+           warp_wait(&b.afull[a.slot], a.round, abort_p, w.status, w.ns);
+      if (!ok) break;
+#pragma unroll
+      for (int q = 0; q < GROUPS; ++q, d.next()) {
+        if (!warp_wait(&b.dempty[d.slot], d.round ^ 1u, abort_p, w.status, w.ns)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < 4 / GROUPS; ++k) {
+          const int at = q * (4 / GROUPS) + k;
+          mma_codes_one(tmem_d + d.slot * C::kN, tmem + a.slot * 32 + at * 8, b0 + (pos.slot * (C::kStage >> 4) + at * 2), idesc, k ? 1u : 0u);
+        }
+        tc_commit_one<false>(smem_u32(&b.dfull[d.slot]));
+      }
+      if (!ok) break;
+      tc_commit_one<false>(smem_u32(&b.empty[pos.slot]));
+      tc_commit_one<false>(smem_u32(&b.aempty[a.slot]));
+    }
+    // every MMA this warp issued completes before TMEM is freed
+    tc_commit_one<false>(smem_u32(&b.mma_done));
+    int no_abort = 0;
+    (void)wait_bounded(&b.mma_done, 0u, &no_abort, w.status, w.ns);
+  } else if (warp >= 6) {
+    // ---------------- codes to operands ----------------
+    const int set = (warp - 6) >> 2, q = warp & 3, row = q * 32 + lane;
+    RingPos<S> pos;
+    RingPos<kCodeA> a;
+    int i = 0;
+    for (auto p = job.begin(); p.more(); p.next(), pos.next(), a.next(), ++i) {
+      if ((i & 1) != set) continue;
+      if (!warp_wait(&b.full[pos.slot], pos.round, abort_p, w.status, w.ns) ||
+          !warp_wait(&b.aempty[a.slot], a.round ^ 1u, abort_p, w.status, w.ns))
+        break;
+      tc_fence_after();  // the products that read this slot before are complete
+      const uint32_t at = ring0 + pos.slot * C::kStage + row * 64;
+      uint4 c[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) c[j] = lds128(at + ((j ^ (row >> 1 & 3)) << 4));
+      uint32_t v[32];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t x[4] = {c[j].x, c[j].y, c[j].z, c[j].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[8 * j + 2 * e] = x[e] & 0x0F0F0F0Fu;
+          v[8 * j + 2 * e + 1] = x[e] >> 4 & 0x0F0F0F0Fu;
+        }
+      }
+      tmem_store32(tmem + ((uint32_t)(q * 32) << 16) + a.slot * 32, v);
+      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&b.afull[a.slot]);
+        mbar_arrive(&b.empty[pos.slot]);
+      }
+    }
+  } else {
+    // ---------------- groups' sums ----------------
+    const int q = warp & 3;
+    RingPos<S> pos;
+    RingPos<kCodeD> d;
+    float acc[TOKENS];
+#pragma unroll
+    for (int t = 0; t < TOKENS; ++t) acc[t] = 0.f;
+    auto p = job.begin();
+    typename Job::Row row;
+    if (p.more()) job.row_at(row, p, q * 32 + lane);
+    bool ok = true;
+    for (; p.more(); p.next(), pos.next()) {
+      float scale[GROUPS], zero[GROUPS];
+      job.take(row, p, scale, zero);  // read one tile ahead
+      ok = ok && warp_wait(&b.full[pos.slot], pos.round, abort_p, w.status, w.ns);
+      const uint32_t sums = ring0 + pos.slot * C::kStage + kCodeW + C::kB;
+#pragma unroll
+      for (int g = 0; g < GROUPS; ++g, d.next()) {
+        ok = ok && warp_wait(&b.dfull[d.slot], d.round, abort_p, w.status, w.ns);
+        if (!ok) continue;
+        tc_fence_after();
+        // sixteen tokens' sums at a time (of eight tokens all planes' lie in one or two sixteens)
+        constexpr int kChunk = TOKENS < 16 ? TOKENS : 16, kCols = TOKENS < 16 ? C::kN : 16 * PLANES;
+        const uint32_t from = tmem_d + ((uint32_t)(q * 32) << 16) + d.slot * C::kN;
+#pragma unroll
+        for (int t0 = 0; t0 < TOKENS; t0 += kChunk) {
+          float v[kCols];
+          tmem_columns<kCols>(from + t0, TOKENS, v);
+          if (t0 + kChunk == TOKENS) {  // everything is in registers: the slot is free
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&b.dempty[d.slot]);
+          }
+#pragma unroll
+          for (int t4 = 0; t4 < kChunk; t4 += 4) {
+            const uint4 x4 = lds128(sums + (g * TOKENS + t0 + t4) * 4);
+            const float x[4] = {__uint_as_float(x4.x), __uint_as_float(x4.y), __uint_as_float(x4.z), __uint_as_float(x4.w)};
+            float f[4];
+            if constexpr (Job::kFactors) job.factors(sums, g, t0 + t4, f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int t = t4 + i;
+              float s = v[(PLANES - 1) * kChunk + t];
+#pragma unroll
+              for (int k = PLANES - 2; k >= 0; --k) s = fmaf(s, kPlane, v[k * kChunk + t]);
+              s = fmaf(-zero[g], x[i], s);
+              if constexpr (Job::kFactors) acc[t0 + t] = fmaf(s, scale[g] * f[i], acc[t0 + t]);
+              else acc[t0 + t] = fmaf(s, scale[g], acc[t0 + t]);
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&b.empty[pos.slot]);
+      if (job.ends(p)) {
+        job.finish(p, q * 32 + lane, acc, ok);
+#pragma unroll
+        for (int t = 0; t < TOKENS; ++t) acc[t] = 0.f;
+        auto after = p;
+        after.next();
+        if (after.more()) job.row_at(row, after, q * 32 + lane);
+      }
+    }
+  }
+  // Copies still in flight after an abort land before the CTA may leave (bounded; otherwise each has landed).
+  tc_fence_before();
+  __syncthreads();
+  if (b.abort_flag && threadIdx.x == 0) {
+    int no_abort = 0;
+    for (int s = 0; s < S; ++s) {
+      const int n = b.issued / S + (s < b.issued % S ? 1 : 0);
+      if (n > 0) (void)wait_bounded(&b.full[s], (uint32_t)((n - 1) & 1), &no_abort, w.status, w.ns);
+    }
+  }
+}
+
+// before the pipeline, by every thread
+__device__ __forceinline__ void code_setup(CodeBars &b, int stages) {
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(&b.full[s], 1);
+      mbar_init(&b.empty[s], 4 + 1 + 4);  // the codes' warps, the products, the sums' warps
+    }
+    for (int s = 0; s < kCodeA; ++s) {
+      mbar_init(&b.afull[s], 4);
+      mbar_init(&b.aempty[s], 1);
+    }
+    for (int s = 0; s < kCodeD; ++s) {
+      mbar_init(&b.dfull[s], 1);
+      mbar_init(&b.dempty[s], 4);
+    }
+    mbar_init(&b.mma_done, 1);
+    mbar_init(&b.never, 1);
+    b.abort_flag = 0;
+    b.issued = 0;
+    fence_mbar_init();
+  }
+  if (threadIdx.x >> 5 == 1) tmem_alloc(&b.tmem, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+}
+__device__ __forceinline__ void code_end(CodeBars &b) {
+  __syncthreads();
+  if (threadIdx.x >> 5 == 1) {
+    tc_fence_after();
+    tmem_dealloc(b.tmem, 512);
+  }
+}
+
+// Launches clusters of `ctas` CTAs along x.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_code_clusters(void (*kernel)(KArgs...), size_t smem, std::atomic<unsigned long long> &done, dim3 grid, int ctas,
+                                 cudaStream_t st, const Args &...args) {
+  const cudaError_t e = allow_smem((const void *)kernel, smem, done);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {(unsigned)ctas, 1u, 1u};
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kCodeThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+}  // namespace moe

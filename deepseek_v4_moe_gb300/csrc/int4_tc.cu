@@ -1,0 +1,201 @@
+// The product of 4-bit weights and a few rows on the FP8 tensor cores (sm_103a): see few_tc.cuh.
+//
+// A tile is 128 rows of the weights and 128 columns.  Where the matrix has more row tiles than the GPU has SMs, a CTA takes
+// one row tile after another; otherwise the CTAs of a cluster share the columns of one, and their sums meet in shared
+// memory in the order of their ranks.
+#include <stdlib.h>
+#include "few_tc.cuh"
+#include "kernels.h"
+
+namespace moe {
+namespace {
+
+// x as planes and groups' sums: a CTA takes a row (its largest magnitude first).
+template <typename T, int PLANES>
+__global__ void __launch_bounds__(256) int4_planes_kernel(const __grid_constant__ Int4MatmulParams p, int tokens) {
+  __shared__ uint32_t most[8];
+  const int row = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k8 = p.w.k / 8, per = 1 << (p.w.group_shift - 3);
+  const T *x = static_cast<const T *>(p.x) + row * p.ld_x;
+  pdl_wait();
+  // The product may come and fetch weights: not earlier, as what the wait was for may write them.
+  pdl_trigger();
+  uint32_t m = 0;
+  for (int i = threadIdx.x; i < k8; i += 256) {
+    float v[8];
+    load_eight<T, true>(x + 8 * i, 0, 1, 8, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+  }
+  m = __reduce_max_sync(0xffffffffu, m);
+  if (lane == 0) most[warp] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, most[i]);
+  const int e = plane_exponent(m), block = row / tokens, token = row % tokens;
+  // what a row's sums are multiplied by; a row that is not finite gives NaN
+  if (threadIdx.x == 0) p.back[row] = m >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : two_to(-e);
+  const float scale = two_to(e);
+  const int all = p.sum_groups * per;  // up to whole groups: their sums are of all their columns
+  for (int i0 = warp * 32; i0 < all; i0 += 256) {
+    const int i = i0 + lane;
+    float sum = 0.f;
+    if (i < k8) {
+      float v[8];
+      load_eight<T, true>(x + 8 * i, 0, 1, 8, v);
+      uint2 o[PLANES];
+      sum = split8<PLANES>(v, scale, o);
+#pragma unroll
+      for (int k = 0; k < PLANES; ++k) p.planes[(((size_t)block * PLANES + k) * tokens + token) * k8 + i] = o[k];
+    }
+    for (int o = per >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (i < all && i % per == 0) p.sums[((size_t)block * p.sum_groups + i / per) * tokens + token] = sum * 0x1p-9f;
+  }
+}
+
+template <typename T, int TOKENS, int PLANES, int GROUPS, bool ZP>
+struct MatmulJob {
+  static constexpr bool kFactors = false;
+  const Int4MatmulParams &p;
+  const Int4Maps &maps;
+  float *sums;                    // the cluster's sums meet in it, [TOKENS][128]
+  int splits, first, end, units, unit0, unit_step, block;
+  struct Place {
+    int unit, tile, units, first, end, unit_step;
+    __device__ __forceinline__ bool more() const { return unit < units; }
+    __device__ __forceinline__ void next() {
+      if (++tile == end) {
+        tile = first;
+        unit += unit_step;
+      }
+    }
+  };
+  __device__ __forceinline__ Place begin() const { return Place{first < end ? unit0 : units, first, units, first, end, unit_step}; }
+  __device__ __forceinline__ bool ends(const Place &a) const { return a.tile == end - 1; }
+  __device__ __forceinline__ void weights(const Place &a, uint32_t at, uint32_t bar) const {
+    tma_load_2d_one<false>(at, &maps.w, bar, a.tile * 64, a.unit * kCodeRows);
+  }
+  __device__ __forceinline__ void ready() const { pdl_wait(); }
+  __device__ __forceinline__ void tokens(const Place &a, uint32_t at, uint32_t to, uint32_t bar) const {
+    tma_load_2d_one<false>(at, &maps.x, bar, a.tile * 128, block * (TOKENS * PLANES));
+    tma_bulk_one(to, p.sums + ((size_t)block * p.sum_groups + a.tile * GROUPS) * TOKENS, GROUPS * TOKENS * 4, bar);
+  }
+  struct Row {
+    const uint16_t *scales;
+    const uint8_t *zeros;
+    uint32_t next[GROUPS];
+  };
+  __device__ __forceinline__ void read(Row &r, int tile) const {
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g) {
+      const int at = min(tile * GROUPS + g, p.w.groups - 1);
+      r.next[g] = r.scales[at] | (ZP ? (r.zeros[at] & 15u) << 16 : 8u << 16);
+    }
+  }
+  __device__ __forceinline__ void row_at(Row &r, const Place &a, int row) const {
+    const long long at = (long long)min(a.unit * kCodeRows + row, p.w.n - 1) * p.w.groups;
+    r.scales = p.w.scales + at;
+    r.zeros = p.w.zeros + at;
+    read(r, a.tile);
+  }
+  __device__ __forceinline__ void take(Row &r, const Place &a, float (&scale)[GROUPS], float (&zero)[GROUPS]) const {
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g) {
+      const uint16_t s = (uint16_t)r.next[g];
+      scale[g] = to_f32(*reinterpret_cast<const T *>(&s));
+      zero[g] = (float)(r.next[g] >> 16);
+    }
+    read(r, a.tile + 1);
+  }
+  __device__ __forceinline__ void finish(const Place &a, int row, const float (&acc)[TOKENS], bool) const {
+    const int n = a.unit * kCodeRows + row, rows = min(TOKENS, p.rows - block * TOKENS);
+#pragma unroll
+    for (int t = 0; t < TOKENS; ++t) {
+      if (t >= rows) break;
+      if (splits > 1) sums[t * kCodeRows + row] = acc[t];
+      else if (n < p.w.n) store(n, t, acc[t]);
+    }
+  }
+  __device__ __forceinline__ void store(int n, int t, float v) const {
+    const int token = block * TOKENS + t;
+    static_cast<T *>(p.out)[token * p.ld_out + n] = from_f32<T>(v * 512.f * p.back[token]);
+  }
+};
+
+template <typename T, int TOKENS, int PLANES, int GROUPS, bool ZP>
+__global__ void __launch_bounds__(kCodeThreads, 1)
+    int4_tc_kernel(const __grid_constant__ Int4MatmulParams p, const __grid_constant__ Int4Maps maps, int splits) {
+  using C = CodeCfg<TOKENS, PLANES, GROUPS>;
+  extern __shared__ char smem[];
+  __shared__ __align__(8) CodeBars bars;
+  __shared__ float sums[TOKENS * kCodeRows];
+  char *ring = smem + (-smem_u32(smem) & 1023u);
+  code_setup(bars, C::kStages);
+  const int tiles = (p.w.k + kCodeTile - 1) / kCodeTile, rank = blockIdx.x % splits;
+  MatmulJob<T, TOKENS, PLANES, GROUPS, ZP> job{p, maps, sums, splits, (int)((long long)tiles * rank / splits),
+                                               (int)((long long)tiles * (rank + 1) / splits),
+                                               (p.w.n + kCodeRows - 1) / kCodeRows, (int)blockIdx.x / splits, (int)gridDim.x / splits,
+                                               (int)blockIdx.y};
+  if (splits > 1 && job.first == job.end)
+    for (int i = threadIdx.x; i < TOKENS * kCodeRows; i += kCodeThreads) sums[i] = 0.f;
+  code_pipeline<C, TOKENS, PLANES, GROUPS>(job, ring, bars, p.waits);
+  if (splits > 1) {  // one row tile, whose sums meet: a part of the rows by each CTA
+    cluster_sync();
+    const int part = kCodeRows / splits, row0 = rank * part, rows = min(TOKENS, p.rows - job.block * TOKENS);
+    for (int i = threadIdx.x; i < part * rows; i += kCodeThreads) {
+      const int row = row0 + i % part, t = i / part, n = job.unit0 * kCodeRows + row;
+      float v = 0.f, x[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r)  // all loads before the first sum
+        if (r < splits)
+          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x[r]) : "r"(in_cta(&sums[t * kCodeRows + row], r)) : "memory");
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        if (r < splits) v += x[r];
+      if (n < p.w.n) job.store(n, t, v);
+    }
+    cluster_sync();
+  }
+  code_end(bars);
+}
+
+template <typename T, int TOKENS, int GROUPS, bool ZP>
+cudaError_t tc_launch(const Int4MatmulParams &p, const Int4Maps &maps, int num_sms, cudaStream_t st) {
+  constexpr int PLANES = std::is_same<T, __half>::value ? 3 : 2;
+  using C = CodeCfg<TOKENS, PLANES, GROUPS>;
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = launch_pdl(int4_planes_kernel<T, PLANES>, dim3(p.rows), dim3(256), 0, st, p, TOKENS);
+  if (e != cudaSuccess) return e;
+  const int tiles = (p.w.n + kCodeRows - 1) / kCodeRows, blocks = (p.rows + TOKENS - 1) / TOKENS;
+  // as many CTAs to a row tile as run at one time (of clusters of 8, 4 and 2 on 152 SMs 16, 36 and 75)
+  const int splits = tiles <= num_sms * 16 / 152 ? 8 : tiles <= num_sms * 36 / 152 ? 4 : tiles <= num_sms * 75 / 152 ? 2 : 1;
+  const int busy = splits > 1 || tiles < num_sms ? tiles : num_sms;
+  return launch_code_clusters(int4_tc_kernel<T, TOKENS, PLANES, GROUPS, ZP>, C::kRing + 1024, done, dim3(busy * splits, blocks), splits, st, p,
+                              maps, splits);
+}
+
+template <typename T, int GROUPS, bool ZP>
+cudaError_t tc_rows(const Int4MatmulParams &p, const Int4Maps &maps, int tokens, int num_sms, cudaStream_t st) {
+  if (tokens == 8) return tc_launch<T, 8, GROUPS, ZP>(p, maps, num_sms, st);
+  if (tokens == 16) return tc_launch<T, 16, GROUPS, ZP>(p, maps, num_sms, st);
+  return tc_launch<T, 32, GROUPS, ZP>(p, maps, num_sms, st);
+}
+
+template <typename T>
+cudaError_t tc_typed(const Int4MatmulParams &p, const Int4Maps &maps, int tokens, int num_sms, cudaStream_t st) {
+  if (p.w.group_shift == 5) return p.w.zeros ? tc_rows<T, 4, true>(p, maps, tokens, num_sms, st) : tc_rows<T, 4, false>(p, maps, tokens, num_sms, st);
+  if (p.w.group_shift == 6) return p.w.zeros ? tc_rows<T, 2, true>(p, maps, tokens, num_sms, st) : tc_rows<T, 2, false>(p, maps, tokens, num_sms, st);
+  return p.w.zeros ? tc_rows<T, 1, true>(p, maps, tokens, num_sms, st) : tc_rows<T, 1, false>(p, maps, tokens, num_sms, st);
+}
+
+}  // namespace
+
+int int4_tc_tokens(int rows, int n, int k, bool f16, int num_sms) {
+  if (getenv("X0")) return 0;
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+}
+
+cudaError_t launch_int4_tc(const Int4MatmulParams &p, const Int4Maps &maps, int tokens, bool f16, int num_sms, cudaStream_t st) {
+  return f16 ? tc_typed<__half>(p, maps, tokens, num_sms, st) : tc_typed<__nv_bfloat16>(p, maps, tokens, num_sms, st);
+}
+
+}  // namespace moe

@@ -497,9 +497,15 @@ typedef struct moe_ffn_int4_matmul_args {
   const void *scales;
   const uint8_t *zeros;
   void *out; int64_t ld_out;     /* [rows, n], any ld >= n; overlaps no input */
+  void *workspace; size_t workspace_bytes;  /* at least moe_ffn_int4_matmul_workspace, 256-byte aligned */
 } moe_ffn_int4_matmul_args;
 
-/* These three return MOE_FFN_OK, NULL_PTR, ROWS_ZERO, ROWS_RANGE, BAD_CONFIG, ALIGNMENT, ALIAS, UNSUPPORTED or CUDA. */
+/* Bytes of workspace that the call needs on the current device (pointers are not read), 0 for none; negative: an error
+ * code. */
+int64_t moe_ffn_int4_matmul_workspace(const moe_ffn_int4_matmul_args *a);
+
+/* These three return MOE_FFN_OK, NULL_PTR, ROWS_ZERO, ROWS_RANGE, BAD_CONFIG, ALIGNMENT, ALIAS, UNSUPPORTED or CUDA,
+ * int4_matmul NO_MEMORY too when the workspace is too small. */
 int moe_ffn_int4_matmul(const moe_ffn_int4_matmul_args *a, void *stream);
 
 /* A whole mixture-of-experts layer on a plain residual stream, for a few tokens:
