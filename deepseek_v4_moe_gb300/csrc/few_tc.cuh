@@ -26,23 +26,31 @@
 
 namespace moe {
 
-constexpr int kCodeThreads = 32 * 14, kCodeRows = 128, kCodeTile = 128;  // rows, and columns, of a tile
+constexpr int kCodeRows = 128, kCodeTile = 128;  // rows, and columns, of a tile
 constexpr int kCodeW = kCodeRows * 64;                                   // its bytes
-constexpr int kCodeA = 4, kCodeD = 4;                                    // slots in TMEM of left operands and of sums
+constexpr int kCodeSlotsMax = 8;
 constexpr float kPlane = 0.03125f;
 
 // TOKENS: 8, 16 or 32; PLANES: 2 or 3; GROUPS of a tile: 1, 2 or 4
 template <int TOKENS, int PLANES, int GROUPS>
 struct CodeCfg {
+  static constexpr int kTokens = TOKENS;
   static constexpr int kRows = TOKENS * PLANES;                 // of the right operand
   static constexpr int kN = (kRows + 15) / 16 * 16;             // columns of the sums
   static constexpr int kB = kN * 128, kSums = GROUPS * TOKENS * 4;
   static constexpr int kStage = kCodeW + kB + (kSums + 1023) / 1024 * 1024;
-  static constexpr int kStages = 180 * 1024 / kStage < 12 ? 180 * 1024 / kStage : 12;
-  static constexpr int kRing = kStages * kStage;
   static constexpr uint32_t kBytes = kCodeW + kRows * 128 + kSums;
-  static constexpr int kTmem = 512;
-  static_assert(kCodeA * 32 + kCodeD * kN <= kTmem, "TMEM");
+  // Slots in TMEM of a tile's sums (all its groups') and of left operands.  Warps that issue products, and sets of four
+  // that make operands and that join groups: each takes tiles in turn.  A set sees a barrier's every round only if no
+  // other set uses its slot, so the numbers of slots and stages are multiples of the sets'.
+  static constexpr int kD = GROUPS * kN <= 64 ? 4 : GROUPS * kN <= 192 ? 2 : 1;
+  static constexpr int kIssue = kD > 1 ? 2 : 1, kJoin = TOKENS <= 16 && kD > 1 ? 2 : 1, kSets = 2;
+  static constexpr int kFit = 180 * 1024 / kStage < 12 ? 180 * 1024 / kStage : 12, kStages = kFit / 2 * 2;
+  static constexpr int kRoom = (512 - kD * GROUPS * kN) / 32, kA = (kRoom < 8 ? kRoom : 8) / 2 * 2;
+  static constexpr int kFirstJoin = 1 + kIssue + (1 + kIssue) % 2, kFirstMake = kFirstJoin + 4 * kJoin;  // their first warps
+  static constexpr int kRing = kStages * kStage;
+  static constexpr int kThreads = 32 * (kFirstMake + 4 * kSets);
+  static_assert(kA >= 2 && kA <= kCodeSlotsMax && kStages >= 2, "slots");
 };
 
 // A row's power of two: what is split is x 2^e; max: the largest magnitude's bits as f32.  (Values below 2^-119 count as
@@ -140,8 +148,10 @@ __device__ __forceinline__ void tma_bulk_one(uint32_t dst, const void *src, uint
       : "memory");
 }
 
+template <typename C>
 struct CodeBars {
-  uint64_t full[12], empty[12], afull[kCodeA], aempty[kCodeA], dfull[kCodeD], dempty[kCodeD], mma_done, never;
+  float join[C::kJoin > 1 ? C::kTokens * kCodeRows : 1];
+  uint64_t full[12], empty[12], afull[kCodeSlotsMax], aempty[kCodeSlotsMax], dfull[kCodeSlotsMax], dempty[kCodeSlotsMax], mma_done[2], never;
   uint32_t tmem;
   int abort_flag, issued;
 };
@@ -151,15 +161,15 @@ struct CodeBars {
 //   bool ends(place)                                         a unit's last tile
 //   void weights(place, at, bar)                             its codes' copy, by the converged warp
 //   void ready();  void tokens(place, at, sums, bar)         what the tokens' copies wait for; they, and their groups' sums
-//   Row; void row_at(row, place, r); void take(row, place, scale, zero)   row r's scales and zero points, a tile ahead
+//   Row; void row_at(row, place, r); void scales(row, place, scale, zero)   row r's scales and zero points
 //   kFactors; void factors(sums, group, token, f)            what four tokens' sums of the group are multiplied by
 //   void finish(place, r, acc, ok)
 template <typename C, int TOKENS, int PLANES, int GROUPS, typename Job>
-__device__ __forceinline__ void code_pipeline(Job &job, char *ring, CodeBars &b, const Waits &w) {
+__device__ __forceinline__ void code_pipeline(Job &job, char *ring, CodeBars<C> &b, const Waits &w) {
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   constexpr int S = C::kStages;
   volatile int *abort_p = &b.abort_flag;
-  const uint32_t ring0 = smem_u32(ring), tmem = b.tmem, tmem_d = tmem + kCodeA * 32;
+  const uint32_t ring0 = smem_u32(ring), tmem = b.tmem, tmem_d = tmem + C::kA * 32;
   if (warp == 0) {
     // ---------------- copies ----------------
     RingPos<S> pos;
@@ -181,49 +191,40 @@ __device__ __forceinline__ void code_pipeline(Job &job, char *ring, CodeBars &b,
       tokens(p, pos.slot);
     }
     if (lane == 0) b.issued = j;
-  } else if (warp == 1) {
+  } else if (warp <= C::kIssue) {
     // ---------------- products ----------------
     if (w.inject && blockIdx.x == 0) (void)warp_wait(&b.never, 0u, abort_p, w.status, w.ns);  // test hook: a wait that runs out
     const uint32_t idesc = idesc_e4m3(kCodeRows, C::kN);
     const uint64_t b0 = smem_desc_sw128(ring0 + kCodeW);
     RingPos<S> pos;
-    RingPos<kCodeA> a;
-    RingPos<kCodeD> d;
-    bool ok = true;
-    for (auto p = job.begin(); ok && p.more(); p.next(), pos.next(), a.next()) {
-      ok = warp_wait(&b.full[pos.slot], pos.round, abort_p, w.status, w.ns) &&
-           warp_wait(&b.afull[a.slot], a.round, abort_p, w.status, w.ns);
-      if (!ok) break;
+    RingPos<C::kA> a;
+    RingPos<C::kD> d;
+    int i = 0;
+    for (auto p = job.begin(); p.more(); p.next(), pos.next(), a.next(), d.next(), ++i) {
+      if (i % C::kIssue != warp - 1) continue;
+      if (!warp_wait(&b.dempty[d.slot], d.round ^ 1u, abort_p, w.status, w.ns) ||
+          !warp_wait(&b.full[pos.slot], pos.round, abort_p, w.status, w.ns) ||
+          !warp_wait(&b.afull[a.slot], a.round, abort_p, w.status, w.ns))
+        break;
+      tc_fence_after();
 #pragma unroll
-      for (int q = 0; q < GROUPS; ++q, d.next()) {
-        if (!warp_wait(&b.dempty[d.slot], d.round ^ 1u, abort_p, w.status, w.ns)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-#pragma unroll
-        for (int k = 0; k < 4 / GROUPS; ++k) {
-          const int at = q * (4 / GROUPS) + k;
-          mma_codes_one(tmem_d + d.slot * C::kN, tmem + a.slot * 32 + at * 8, b0 + (pos.slot * (C::kStage >> 4) + at * 2), idesc, k ? 1u : 0u);
-        }
-        tc_commit_one<false>(smem_u32(&b.dfull[d.slot]));
-      }
-      if (!ok) break;
-      tc_commit_one<false>(smem_u32(&b.empty[pos.slot]));
-      tc_commit_one<false>(smem_u32(&b.aempty[a.slot]));
+      for (int k = 0; k < 4; ++k)
+        mma_codes_one(tmem_d + (d.slot * GROUPS + k * GROUPS / 4) * C::kN, tmem + a.slot * 32 + k * 8,
+                      b0 + (pos.slot * (C::kStage >> 4) + k * 2), idesc, k % (4 / GROUPS) ? 1u : 0u);
+      tc_commit_one<false>(smem_u32(&b.dfull[d.slot]));
     }
     // every MMA this warp issued completes before TMEM is freed
-    tc_commit_one<false>(smem_u32(&b.mma_done));
+    tc_commit_one<false>(smem_u32(&b.mma_done[warp - 1]));
     int no_abort = 0;
-    (void)wait_bounded(&b.mma_done, 0u, &no_abort, w.status, w.ns);
-  } else if (warp >= 6) {
+    (void)wait_bounded(&b.mma_done[warp - 1], 0u, &no_abort, w.status, w.ns);
+  } else if (warp >= C::kFirstMake) {
     // ---------------- codes to operands ----------------
-    const int set = (warp - 6) >> 2, q = warp & 3, row = q * 32 + lane;
+    const int set = (warp - C::kFirstMake) >> 2, q = warp & 3, row = q * 32 + lane;
     RingPos<S> pos;
-    RingPos<kCodeA> a;
+    RingPos<C::kA> a;
     int i = 0;
     for (auto p = job.begin(); p.more(); p.next(), pos.next(), a.next(), ++i) {
-      if ((i & 1) != set) continue;
+      if (i % C::kSets != set) continue;
       if (!warp_wait(&b.full[pos.slot], pos.round, abort_p, w.status, w.ns) ||
           !warp_wait(&b.aempty[a.slot], a.round ^ 1u, abort_p, w.status, w.ns))
         break;
@@ -251,11 +252,14 @@ __device__ __forceinline__ void code_pipeline(Job &job, char *ring, CodeBars &b,
         mbar_arrive(&b.empty[pos.slot]);
       }
     }
-  } else {
+  } else if (warp >= C::kFirstJoin) {
     // ---------------- groups' sums ----------------
-    const int q = warp & 3;
+    // Sets take every other tile; at a unit's end the first one adds the others' sums to its own.
+    const int q = warp & 3, set = (warp - C::kFirstJoin) >> 2;
     RingPos<S> pos;
-    RingPos<kCodeD> d;
+    RingPos<C::kA> a;
+    RingPos<C::kD> d;
+    int i = 0;
     float acc[TOKENS];
 #pragma unroll
     for (int t = 0; t < TOKENS; ++t) acc[t] = 0.f;
@@ -263,27 +267,31 @@ __device__ __forceinline__ void code_pipeline(Job &job, char *ring, CodeBars &b,
     typename Job::Row row;
     if (p.more()) job.row_at(row, p, q * 32 + lane);
     bool ok = true;
-    for (; p.more(); p.next(), pos.next()) {
+    for (; p.more(); p.next(), pos.next(), a.next(), d.next(), ++i) {
+      if (i % C::kJoin == set) {
       float scale[GROUPS], zero[GROUPS];
-      job.take(row, p, scale, zero);  // read one tile ahead
+      job.scales(row, p, scale, zero);
       ok = ok && warp_wait(&b.full[pos.slot], pos.round, abort_p, w.status, w.ns);
       const uint32_t sums = ring0 + pos.slot * C::kStage + kCodeW + C::kB;
+      ok = ok && warp_wait(&b.dfull[d.slot], d.round, abort_p, w.status, w.ns);
+      tc_fence_after();
 #pragma unroll
-      for (int g = 0; g < GROUPS; ++g, d.next()) {
-        ok = ok && warp_wait(&b.dfull[d.slot], d.round, abort_p, w.status, w.ns);
+      for (int g = 0; g < GROUPS; ++g) {
         if (!ok) continue;
-        tc_fence_after();
         // sixteen tokens' sums at a time (of eight tokens all planes' lie in one or two sixteens)
         constexpr int kChunk = TOKENS < 16 ? TOKENS : 16, kCols = TOKENS < 16 ? C::kN : 16 * PLANES;
-        const uint32_t from = tmem_d + ((uint32_t)(q * 32) << 16) + d.slot * C::kN;
+        const uint32_t from = tmem_d + ((uint32_t)(q * 32) << 16) + (d.slot * GROUPS + g) * C::kN;
 #pragma unroll
         for (int t0 = 0; t0 < TOKENS; t0 += kChunk) {
           float v[kCols];
           tmem_columns<kCols>(from + t0, TOKENS, v);
-          if (t0 + kChunk == TOKENS) {  // everything is in registers: the slot is free
+          if (g == GROUPS - 1 && t0 + kChunk == TOKENS) {  // everything is in registers: the tile's slots are free
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&b.dempty[d.slot]);
+            if (lane == 0) {
+              mbar_arrive(&b.dempty[d.slot]);
+              mbar_arrive(&b.aempty[a.slot]);
+            }
           }
 #pragma unroll
           for (int t4 = 0; t4 < kChunk; t4 += 4) {
@@ -306,8 +314,19 @@ __device__ __forceinline__ void code_pipeline(Job &job, char *ring, CodeBars &b,
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&b.empty[pos.slot]);
+      }
       if (job.ends(p)) {
-        job.finish(p, q * 32 + lane, acc, ok);
+        if constexpr (C::kJoin > 1) {
+          if (set == 1)
+#pragma unroll
+            for (int t = 0; t < TOKENS; ++t) b.join[t * kCodeRows + q * 32 + lane] = acc[t];
+          asm volatile("bar.sync 2, %0;" ::"n"(128 * C::kJoin) : "memory");
+          if (set == 0)
+#pragma unroll
+            for (int t = 0; t < TOKENS; ++t) acc[t] += b.join[t * kCodeRows + q * 32 + lane];
+          asm volatile("bar.sync 2, %0;" ::"n"(128 * C::kJoin) : "memory");
+        }
+        if (set == 0) job.finish(p, q * 32 + lane, acc, ok);
 #pragma unroll
         for (int t = 0; t < TOKENS; ++t) acc[t] = 0.f;
         auto after = p;
@@ -329,21 +348,22 @@ __device__ __forceinline__ void code_pipeline(Job &job, char *ring, CodeBars &b,
 }
 
 // before the pipeline, by every thread
-__device__ __forceinline__ void code_setup(CodeBars &b, int stages) {
+template <typename C>
+__device__ __forceinline__ void code_setup(CodeBars<C> &b) {
   if (threadIdx.x == 0) {
-    for (int s = 0; s < stages; ++s) {
+    for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&b.full[s], 1);
-      mbar_init(&b.empty[s], 4 + 1 + 4);  // the codes' warps, the products, the sums' warps
+      mbar_init(&b.empty[s], 4 + 4);  // the warps that made its operand, and that joined its groups after the products
     }
-    for (int s = 0; s < kCodeA; ++s) {
+    for (int s = 0; s < C::kA; ++s) {
       mbar_init(&b.afull[s], 4);
-      mbar_init(&b.aempty[s], 1);
+      mbar_init(&b.aempty[s], 4);
     }
-    for (int s = 0; s < kCodeD; ++s) {
+    for (int s = 0; s < C::kD; ++s) {
       mbar_init(&b.dfull[s], 1);
       mbar_init(&b.dempty[s], 4);
     }
-    mbar_init(&b.mma_done, 1);
+    for (int s = 0; s < 2; ++s) mbar_init(&b.mma_done[s], 1);
     mbar_init(&b.never, 1);
     b.abort_flag = 0;
     b.issued = 0;
@@ -354,7 +374,8 @@ __device__ __forceinline__ void code_setup(CodeBars &b, int stages) {
   __syncthreads();
   tc_fence_after();
 }
-__device__ __forceinline__ void code_end(CodeBars &b) {
+template <typename C>
+__device__ __forceinline__ void code_end(CodeBars<C> &b) {
   __syncthreads();
   if (threadIdx.x >> 5 == 1) {
     tc_fence_after();
@@ -364,8 +385,8 @@ __device__ __forceinline__ void code_end(CodeBars &b) {
 
 // Launches clusters of `ctas` CTAs along x.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_code_clusters(void (*kernel)(KArgs...), size_t smem, std::atomic<unsigned long long> &done, dim3 grid, int ctas,
-                                 cudaStream_t st, const Args &...args) {
+cudaError_t launch_code_clusters(void (*kernel)(KArgs...), size_t smem, std::atomic<unsigned long long> &done, dim3 grid, int threads,
+                                 int ctas, cudaStream_t st, const Args &...args) {
   const cudaError_t e = allow_smem((const void *)kernel, smem, done);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
@@ -375,7 +396,7 @@ cudaError_t launch_code_clusters(void (*kernel)(KArgs...), size_t smem, std::ato
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(kCodeThreads);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = attr;

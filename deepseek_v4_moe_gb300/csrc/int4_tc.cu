@@ -82,29 +82,19 @@ struct MatmulJob {
   struct Row {
     const uint16_t *scales;
     const uint8_t *zeros;
-    uint32_t next[GROUPS];
   };
-  __device__ __forceinline__ void read(Row &r, int tile) const {
-#pragma unroll
-    for (int g = 0; g < GROUPS; ++g) {
-      const int at = min(tile * GROUPS + g, p.w.groups - 1);
-      r.next[g] = r.scales[at] | (ZP ? (r.zeros[at] & 15u) << 16 : 8u << 16);
-    }
-  }
   __device__ __forceinline__ void row_at(Row &r, const Place &a, int row) const {
     const long long at = (long long)min(a.unit * kCodeRows + row, p.w.n - 1) * p.w.groups;
     r.scales = p.w.scales + at;
     r.zeros = p.w.zeros + at;
-    read(r, a.tile);
   }
-  __device__ __forceinline__ void take(Row &r, const Place &a, float (&scale)[GROUPS], float (&zero)[GROUPS]) const {
+  __device__ __forceinline__ void scales(const Row &r, const Place &a, float (&scale)[GROUPS], float (&zero)[GROUPS]) const {
 #pragma unroll
     for (int g = 0; g < GROUPS; ++g) {
-      const uint16_t s = (uint16_t)r.next[g];
-      scale[g] = to_f32(*reinterpret_cast<const T *>(&s));
-      zero[g] = (float)(r.next[g] >> 16);
+      const int at = min(a.tile * GROUPS + g, p.w.groups - 1);
+      scale[g] = to_f32(reinterpret_cast<const T *>(r.scales)[at]);
+      zero[g] = ZP ? (float)(r.zeros[at] & 15u) : 8.f;
     }
-    read(r, a.tile + 1);
   }
   __device__ __forceinline__ void finish(const Place &a, int row, const float (&acc)[TOKENS], bool) const {
     const int n = a.unit * kCodeRows + row, rows = min(TOKENS, p.rows - block * TOKENS);
@@ -122,26 +112,26 @@ struct MatmulJob {
 };
 
 template <typename T, int TOKENS, int PLANES, int GROUPS, bool ZP>
-__global__ void __launch_bounds__(kCodeThreads, 1)
+__global__ void __launch_bounds__(CodeCfg<TOKENS, PLANES, GROUPS>::kThreads, 1)
     int4_tc_kernel(const __grid_constant__ Int4MatmulParams p, const __grid_constant__ Int4Maps maps, int splits) {
   using C = CodeCfg<TOKENS, PLANES, GROUPS>;
   extern __shared__ char smem[];
-  __shared__ __align__(8) CodeBars bars;
+  __shared__ __align__(8) CodeBars<C> bars;
   __shared__ float sums[TOKENS * kCodeRows];
   char *ring = smem + (-smem_u32(smem) & 1023u);
-  code_setup(bars, C::kStages);
+  code_setup<C>(bars);
   const int tiles = (p.w.k + kCodeTile - 1) / kCodeTile, rank = blockIdx.x % splits;
   MatmulJob<T, TOKENS, PLANES, GROUPS, ZP> job{p, maps, sums, splits, (int)((long long)tiles * rank / splits),
                                                (int)((long long)tiles * (rank + 1) / splits),
                                                (p.w.n + kCodeRows - 1) / kCodeRows, (int)blockIdx.x / splits, (int)gridDim.x / splits,
                                                (int)blockIdx.y};
   if (splits > 1 && job.first == job.end)
-    for (int i = threadIdx.x; i < TOKENS * kCodeRows; i += kCodeThreads) sums[i] = 0.f;
+    for (int i = threadIdx.x; i < TOKENS * kCodeRows; i += C::kThreads) sums[i] = 0.f;
   code_pipeline<C, TOKENS, PLANES, GROUPS>(job, ring, bars, p.waits);
   if (splits > 1) {  // one row tile, whose sums meet: a part of the rows by each CTA
     cluster_sync();
     const int part = kCodeRows / splits, row0 = rank * part, rows = min(TOKENS, p.rows - job.block * TOKENS);
-    for (int i = threadIdx.x; i < part * rows; i += kCodeThreads) {
+    for (int i = threadIdx.x; i < part * rows; i += C::kThreads) {
       const int row = row0 + i % part, t = i / part, n = job.unit0 * kCodeRows + row;
       float v = 0.f, x[8];
 #pragma unroll
@@ -169,7 +159,7 @@ cudaError_t tc_launch(const Int4MatmulParams &p, const Int4Maps &maps, int num_s
   // as many CTAs to a row tile as run at one time (of clusters of 8, 4 and 2 on 152 SMs 16, 36 and 75)
   const int splits = tiles <= num_sms * 16 / 152 ? 8 : tiles <= num_sms * 36 / 152 ? 4 : tiles <= num_sms * 75 / 152 ? 2 : 1;
   const int busy = splits > 1 || tiles < num_sms ? tiles : num_sms;
-  return launch_code_clusters(int4_tc_kernel<T, TOKENS, PLANES, GROUPS, ZP>, C::kRing + 1024, done, dim3(busy * splits, blocks), splits, st, p,
+  return launch_code_clusters(int4_tc_kernel<T, TOKENS, PLANES, GROUPS, ZP>, C::kRing + 1024, done, dim3(busy * splits, blocks), C::kThreads, splits, st, p,
                               maps, splits);
 }
 
