@@ -135,7 +135,8 @@ Int4Space int4_space(const moe_ffn_int4_matmul_args *a, int tokens) {
   Int4Space s;
   const int planes = a->type == MOE_FFN_F16 ? 3 : 2;
   const int64_t blocks = (a->rows + tokens - 1) / tokens;
-  s.groups = (int)((a->k + 127) / 128 * (128 / a->group));
+  const int columns = 128 * moe::code_halves(tokens, planes, 128 / a->group);  // of a tile
+  s.groups = (int)((a->k + columns - 1) / columns * (columns / a->group));
   s.rows = (int)(blocks * planes * tokens);
   s.sums = ((int64_t)s.rows * a->k + 255) / 256 * 256;
   s.back = s.sums + (blocks * s.groups * tokens * 4 + 255) / 256 * 256;
@@ -202,7 +203,7 @@ extern "C" int moe_ffn_int4_matmul(const moe_ffn_int4_matmul_args *a, void *stre
     p.sums = reinterpret_cast<float *>(ws + space.sums);
     p.back = reinterpret_cast<float *>(ws + space.back);
     p.sum_groups = space.groups;
-    if (!encode_map(&maps.w, a->codes, 1, K / 2, N, K / 2, 128, 64) ||
+    if (!encode_map(&maps.w, a->codes, 1, K / 2, N, K / 2, 128, 64 * moe::code_halves(tokens, f16 ? 3 : 2, 128 / a->group)) ||
         !encode_map(&maps.x, ws, 1, K, space.rows, K, tokens * (f16 ? 3 : 2)))
       return fail(MOE_FFN_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", who);
     return launched(who, moe::launch_int4_tc(p, maps, tokens, f16, sms, st));

@@ -18,6 +18,10 @@ struct FewMatrix {
   int n, k, groups, group_shift;
 };
 
+// Halves of 128 columns that a tile of the FP8 tensor cores' form has: one where two halves' sums of all groups leave no
+// room in TMEM.  groups: of 128 columns.
+constexpr int code_halves(int tokens, int planes, int groups) { return 2 * groups * ((tokens * planes + 15) / 16 * 16) <= 384 ? 2 : 1; }
+
 // what a kernel with bounded waits reports to, how long they last, and whether one is to run out
 struct Waits {
   int *status;
@@ -36,12 +40,12 @@ struct Int4MatmulParams {
   // [blocks][sum_groups][tokens], what the rows' sums are multiplied by.
   uint2 *planes;
   float *sums, *back;
-  int sum_groups;  // groups of a row, up to a whole tile of 128 columns
+  int sum_groups;  // groups of a row, up to a whole tile
 };
 // tokens of a block in that form, for so many rows; 0: the other form serves the call
 int int4_tc_tokens(int rows, int n, int k, bool f16, int num_sms);
 // w: the codes, boxes of 64 bytes x the rows of a CTA's sets; x: pieces of 32 columns, boxes of those of a step's tiles.  FP8
-// form: w the codes, boxes of 64 bytes x 128 rows; x the planes, boxes of 128 bytes x a block's rows
+// form: w the codes, boxes of 64 bytes for each half of a tile x 128 rows; x the planes, boxes of 128 bytes x a block's rows
 struct Int4Maps {
   CUtensorMap w, x;
 };

@@ -14,7 +14,7 @@
 //   acc += scale (sum(code p0) + sum(code p1) / 32 + .. - zero sum(x))
 //
 // Roles: a warp copies (TMA), one issues the products, eight make codes operands (two sets of four, every other tile: a
-// thread has a row of 128 columns), four join the groups (a thread has a row, its sums of all tokens in registers).
+// thread has a row), four join the groups (a thread has a row, its sums of all tokens in registers).
 #pragma once
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -26,27 +26,28 @@
 
 namespace moe {
 
-constexpr int kCodeRows = 128, kCodeTile = 128;  // rows, and columns, of a tile
-constexpr int kCodeW = kCodeRows * 64;                                   // its bytes
+constexpr int kCodeRows = 128;  // of a tile; it has 256 columns, or 128 (code_halves)
 constexpr int kCodeSlotsMax = 8;
 constexpr float kPlane = 0.03125f;
 
-// TOKENS: 8, 16 or 32; PLANES: 2 or 3; GROUPS of a tile: 1, 2 or 4
+// TOKENS: 8, 16 or 32; PLANES: 2 or 3; GROUPS of 128 columns: 1, 2 or 4
 template <int TOKENS, int PLANES, int GROUPS>
 struct CodeCfg {
   static constexpr int kTokens = TOKENS;
   static constexpr int kRows = TOKENS * PLANES;                 // of the right operand
   static constexpr int kN = (kRows + 15) / 16 * 16;             // columns of the sums
-  static constexpr int kB = kN * 128, kSums = GROUPS * TOKENS * 4;
-  static constexpr int kStage = kCodeW + kB + (kSums + 1023) / 1024 * 1024;
-  static constexpr uint32_t kBytes = kCodeW + kRows * 128 + kSums;
+  static constexpr int kHalves = code_halves(TOKENS, PLANES, GROUPS), kAll = kHalves * GROUPS;  // of 128 columns; groups
+  static constexpr int kW = kCodeRows * 64 * kHalves;           // bytes of codes
+  static constexpr int kB = kN * 128, kSums = kAll * TOKENS * 4;
+  static constexpr int kStage = kW + kHalves * kB + (kSums + 1023) / 1024 * 1024;
+  static constexpr uint32_t kBytes = kW + kHalves * kRows * 128 + kSums;
   // Slots in TMEM of a tile's sums (all its groups') and of left operands.  Warps that issue products, and sets of four
   // that make operands and that join groups: each takes tiles in turn.  A set sees a barrier's every round only if no
   // other set uses its slot, so the numbers of slots and stages are multiples of the sets'.
-  static constexpr int kD = GROUPS * kN <= 64 ? 4 : GROUPS * kN <= 192 ? 2 : 1;
+  static constexpr int kD = kAll * kN <= 64 ? 4 : kAll * kN <= 192 ? 2 : 1;
   static constexpr int kIssue = kD > 1 ? 2 : 1, kJoin = TOKENS <= 16 && kD > 1 ? 2 : 1, kSets = 2;
   static constexpr int kFit = 180 * 1024 / kStage < 12 ? 180 * 1024 / kStage : 12, kStages = kFit / 2 * 2;
-  static constexpr int kRoom = (512 - kD * GROUPS * kN) / 32, kA = (kRoom < 8 ? kRoom : 8) / 2 * 2;
+  static constexpr int kRoom = (512 - kD * kAll * kN) / (32 * kHalves), kA = (kRoom < 8 ? kRoom : 8) / 2 * 2;
   static constexpr int kFirstJoin = 1 + kIssue + (1 + kIssue) % 2, kFirstMake = kFirstJoin + 4 * kJoin;  // their first warps
   static constexpr int kRing = kStages * kStage;
   static constexpr int kThreads = 32 * (kFirstMake + 4 * kSets);
@@ -169,7 +170,7 @@ __device__ __forceinline__ void code_pipeline(Job &job, char *ring, CodeBars<C> 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   constexpr int S = C::kStages;
   volatile int *abort_p = &b.abort_flag;
-  const uint32_t ring0 = smem_u32(ring), tmem = b.tmem, tmem_d = tmem + C::kA * 32;
+  const uint32_t ring0 = smem_u32(ring), tmem = b.tmem, tmem_d = tmem + C::kA * C::kHalves * 32;
   if (warp == 0) {
     // ---------------- copies ----------------
     RingPos<S> pos;
@@ -179,7 +180,8 @@ __device__ __forceinline__ void code_pipeline(Job &job, char *ring, CodeBars<C> 
       job.weights(p, ring0 + s * C::kStage, smem_u32(&b.full[s]));
     };
     auto tokens = [&](const auto &p, int s) {
-      job.tokens(p, ring0 + s * C::kStage + kCodeW, ring0 + s * C::kStage + kCodeW + C::kB, smem_u32(&b.full[s]));
+      const uint32_t at = ring0 + s * C::kStage + C::kW;
+      job.tokens(p, at, at + C::kHalves * C::kB, smem_u32(&b.full[s]));
     };
     auto p = job.begin(), early = p;
     for (; j < S && p.more(); ++j, p.next()) weights(p, j);  // these need not wait for the tokens
@@ -195,7 +197,7 @@ __device__ __forceinline__ void code_pipeline(Job &job, char *ring, CodeBars<C> 
     // ---------------- products ----------------
     if (w.inject && blockIdx.x == 0) (void)warp_wait(&b.never, 0u, abort_p, w.status, w.ns);  // test hook: a wait that runs out
     const uint32_t idesc = idesc_e4m3(kCodeRows, C::kN);
-    const uint64_t b0 = smem_desc_sw128(ring0 + kCodeW);
+    const uint64_t b0 = smem_desc_sw128(ring0 + C::kW);
     RingPos<S> pos;
     RingPos<C::kA> a;
     RingPos<C::kD> d;
@@ -208,9 +210,9 @@ __device__ __forceinline__ void code_pipeline(Job &job, char *ring, CodeBars<C> 
         break;
       tc_fence_after();
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        mma_codes_one(tmem_d + (d.slot * GROUPS + k * GROUPS / 4) * C::kN, tmem + a.slot * 32 + k * 8,
-                      b0 + (pos.slot * (C::kStage >> 4) + k * 2), idesc, k % (4 / GROUPS) ? 1u : 0u);
+      for (int k = 0; k < 4 * C::kHalves; ++k)
+        mma_codes_one(tmem_d + (d.slot * C::kAll + k * GROUPS / 4) * C::kN, tmem + a.slot * (C::kHalves * 32) + k * 8,
+                      b0 + (pos.slot * (C::kStage >> 4) + k / 4 * (C::kB >> 4) + k % 4 * 2), idesc, k % (4 / GROUPS) ? 1u : 0u);
       tc_commit_one<false>(smem_u32(&b.dfull[d.slot]));
     }
     // every MMA this warp issued completes before TMEM is freed
@@ -229,21 +231,25 @@ __device__ __forceinline__ void code_pipeline(Job &job, char *ring, CodeBars<C> 
           !warp_wait(&b.aempty[a.slot], a.round ^ 1u, abort_p, w.status, w.ns))
         break;
       tc_fence_after();  // the products that read this slot before are complete
-      const uint32_t at = ring0 + pos.slot * C::kStage + row * 64;
-      uint4 c[4];
+      const uint32_t at = ring0 + pos.slot * C::kStage + row * (64 * C::kHalves);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) c[j] = lds128(at + ((j ^ (row >> 1 & 3)) << 4));
-      uint32_t v[32];
+      for (int h = 0; h < C::kHalves; ++h) {
+        uint4 c[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t x[4] = {c[j].x, c[j].y, c[j].z, c[j].w};
+        for (int j = 0; j < 4; ++j)
+          c[j] = lds128(at + ((C::kHalves == 2 ? (4 * h + j) ^ (row & 7) : j ^ (row >> 1 & 3)) << 4));
+        uint32_t v[32];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          v[8 * j + 2 * e] = x[e] & 0x0F0F0F0Fu;
-          v[8 * j + 2 * e + 1] = x[e] >> 4 & 0x0F0F0F0Fu;
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t x[4] = {c[j].x, c[j].y, c[j].z, c[j].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            v[8 * j + 2 * e] = x[e] & 0x0F0F0F0Fu;
+            v[8 * j + 2 * e + 1] = x[e] >> 4 & 0x0F0F0F0Fu;
+          }
         }
+        tmem_store32(tmem + ((uint32_t)(q * 32) << 16) + (a.slot * C::kHalves + h) * 32, v);
       }
-      tmem_store32(tmem + ((uint32_t)(q * 32) << 16) + a.slot * 32, v);
       asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
       tc_fence_before();
       __syncwarp();
@@ -269,23 +275,23 @@ __device__ __forceinline__ void code_pipeline(Job &job, char *ring, CodeBars<C> 
     bool ok = true;
     for (; p.more(); p.next(), pos.next(), a.next(), d.next(), ++i) {
       if (i % C::kJoin == set) {
-      float scale[GROUPS], zero[GROUPS];
+      float scale[C::kAll], zero[C::kAll];
       job.scales(row, p, scale, zero);
       ok = ok && warp_wait(&b.full[pos.slot], pos.round, abort_p, w.status, w.ns);
-      const uint32_t sums = ring0 + pos.slot * C::kStage + kCodeW + C::kB;
+      const uint32_t sums = ring0 + pos.slot * C::kStage + C::kW + C::kHalves * C::kB;
       ok = ok && warp_wait(&b.dfull[d.slot], d.round, abort_p, w.status, w.ns);
       tc_fence_after();
 #pragma unroll
-      for (int g = 0; g < GROUPS; ++g) {
+      for (int g = 0; g < C::kAll; ++g) {
         if (!ok) continue;
         // sixteen tokens' sums at a time (of eight tokens all planes' lie in one or two sixteens)
         constexpr int kChunk = TOKENS < 16 ? TOKENS : 16, kCols = TOKENS < 16 ? C::kN : 16 * PLANES;
-        const uint32_t from = tmem_d + ((uint32_t)(q * 32) << 16) + (d.slot * GROUPS + g) * C::kN;
+        const uint32_t from = tmem_d + ((uint32_t)(q * 32) << 16) + (d.slot * C::kAll + g) * C::kN;
 #pragma unroll
         for (int t0 = 0; t0 < TOKENS; t0 += kChunk) {
           float v[kCols];
           tmem_columns<kCols>(from + t0, TOKENS, v);
-          if (g == GROUPS - 1 && t0 + kChunk == TOKENS) {  // everything is in registers: the tile's slots are free
+          if (g == C::kAll - 1 && t0 + kChunk == TOKENS) {  // everything is in registers: the tile's slots are free
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {

@@ -54,6 +54,7 @@ __global__ void __launch_bounds__(256) int4_planes_kernel(const __grid_constant_
 
 template <typename T, int TOKENS, int PLANES, int GROUPS, bool ZP>
 struct MatmulJob {
+  using C = CodeCfg<TOKENS, PLANES, GROUPS>;
   static constexpr bool kFactors = false;
   const Int4MatmulParams &p;
   const Int4Maps &maps;
@@ -72,12 +73,14 @@ struct MatmulJob {
   __device__ __forceinline__ Place begin() const { return Place{first < end ? unit0 : units, first, units, first, end, unit_step}; }
   __device__ __forceinline__ bool ends(const Place &a) const { return a.tile == end - 1; }
   __device__ __forceinline__ void weights(const Place &a, uint32_t at, uint32_t bar) const {
-    tma_load_2d_one<false>(at, &maps.w, bar, a.tile * 64, a.unit * kCodeRows);
+    tma_load_2d_one<false>(at, &maps.w, bar, a.tile * (64 * C::kHalves), a.unit * kCodeRows);
   }
   __device__ __forceinline__ void ready() const { pdl_wait(); }
   __device__ __forceinline__ void tokens(const Place &a, uint32_t at, uint32_t to, uint32_t bar) const {
-    tma_load_2d_one<false>(at, &maps.x, bar, a.tile * 128, block * (TOKENS * PLANES));
-    tma_bulk_one(to, p.sums + ((size_t)block * p.sum_groups + a.tile * GROUPS) * TOKENS, GROUPS * TOKENS * 4, bar);
+#pragma unroll
+    for (int h = 0; h < C::kHalves; ++h)
+      tma_load_2d_one<false>(at + h * C::kB, &maps.x, bar, (a.tile * C::kHalves + h) * 128, block * C::kRows);
+    tma_bulk_one(to, p.sums + ((size_t)block * p.sum_groups + a.tile * C::kAll) * TOKENS, C::kSums, bar);
   }
   struct Row {
     const uint16_t *scales;
@@ -88,10 +91,10 @@ struct MatmulJob {
     r.scales = p.w.scales + at;
     r.zeros = p.w.zeros + at;
   }
-  __device__ __forceinline__ void scales(const Row &r, const Place &a, float (&scale)[GROUPS], float (&zero)[GROUPS]) const {
+  __device__ __forceinline__ void scales(const Row &r, const Place &a, float (&scale)[C::kAll], float (&zero)[C::kAll]) const {
 #pragma unroll
-    for (int g = 0; g < GROUPS; ++g) {
-      const int at = min(a.tile * GROUPS + g, p.w.groups - 1);
+    for (int g = 0; g < C::kAll; ++g) {
+      const int at = min(a.tile * C::kAll + g, p.w.groups - 1);
       scale[g] = to_f32(reinterpret_cast<const T *>(r.scales)[at]);
       zero[g] = ZP ? (float)(r.zeros[at] & 15u) : 8.f;
     }
@@ -120,7 +123,7 @@ __global__ void __launch_bounds__(CodeCfg<TOKENS, PLANES, GROUPS>::kThreads, 1)
   __shared__ float sums[TOKENS * kCodeRows];
   char *ring = smem + (-smem_u32(smem) & 1023u);
   code_setup<C>(bars);
-  const int tiles = (p.w.k + kCodeTile - 1) / kCodeTile, rank = blockIdx.x % splits;
+  const int tiles = (p.w.k + 128 * C::kHalves - 1) / (128 * C::kHalves), rank = blockIdx.x % splits;
   MatmulJob<T, TOKENS, PLANES, GROUPS, ZP> job{p, maps, sums, splits, (int)((long long)tiles * rank / splits),
                                                (int)((long long)tiles * (rank + 1) / splits),
                                                (p.w.n + kCodeRows - 1) / kCodeRows, (int)blockIdx.x / splits, (int)gridDim.x / splits,
