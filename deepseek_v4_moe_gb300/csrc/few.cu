@@ -157,9 +157,7 @@ int check_int4_matmul(const char *who, const moe_ffn_int4_matmul_args *a) {
 extern "C" int64_t moe_ffn_int4_matmul_workspace(const moe_ffn_int4_matmul_args *a) {
   const int rc = check_int4_matmul("int4_matmul_workspace", a);
   if (rc) return rc;
-  const int sms = current_sms();
-  if (sms < 0) return sms;
-  const int tokens = moe::int4_tc_tokens(a->rows, a->n, a->k, a->type == MOE_FFN_F16, sms);
+  const int tokens = moe::int4_tc_tokens(a->rows, a->n, a->k, a->group);
   return tokens ? int4_space(a, tokens).bytes : 0;
 }
 
@@ -193,7 +191,7 @@ extern "C" int moe_ffn_int4_matmul(const moe_ffn_int4_matmul_args *a, void *stre
   const bool f16 = a->type == MOE_FFN_F16;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   moe::Int4Maps maps;
-  if (const int tokens = moe::int4_tc_tokens(a->rows, a->n, a->k, f16, sms)) {
+  if (const int tokens = moe::int4_tc_tokens(a->rows, a->n, a->k, a->group)) {
     const Int4Space space = int4_space(a, tokens);
     if (!a->workspace) return fail(MOE_FFN_ERR_NULL_PTR, "%s: workspace is NULL", who);
     if (a->workspace_bytes < (size_t)space.bytes)

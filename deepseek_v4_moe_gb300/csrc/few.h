@@ -43,7 +43,7 @@ struct Int4MatmulParams {
   int sum_groups;  // groups of a row, up to a whole tile
 };
 // tokens of a block in that form, for so many rows; 0: the other form serves the call
-int int4_tc_tokens(int rows, int n, int k, bool f16, int num_sms);
+int int4_tc_tokens(int rows, int n, int k, int group);
 // w: the codes, boxes of 64 bytes x the rows of a CTA's sets; x: pieces of 32 columns, boxes of those of a step's tiles.  FP8
 // form: w the codes, boxes of 64 bytes for each half of a tile x 128 rows; x the planes, boxes of 128 bytes x a block's rows
 struct Int4Maps {

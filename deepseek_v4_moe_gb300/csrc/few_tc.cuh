@@ -123,7 +123,7 @@ __device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t (&r)[32
       "r"(r[31])
       : "memory");
 }
-// N columns of this thread's lane in sixteens `apart` columns from one another, waited for
+// N columns of this thread's lane in sixteens `apart` columns from one another; they have arrived after tmem_arrived
 template <int N>
 __device__ __forceinline__ void tmem_columns(uint32_t at, int apart, float (&v)[N]) {
   if (apart < 16) apart = 16;  // eight tokens: their planes side by side
@@ -136,6 +136,9 @@ __device__ __forceinline__ void tmem_columns(uint32_t at, int apart, float (&v)[
           "=f"(v[i + 7]), "=f"(v[i + 8]), "=f"(v[i + 9]), "=f"(v[i + 10]), "=f"(v[i + 11]), "=f"(v[i + 12]), "=f"(v[i + 13]),
           "=f"(v[i + 14]), "=f"(v[i + 15])
         : "r"(at + i / 16 * apart));
+}
+template <int N>
+__device__ __forceinline__ void tmem_arrived(float (&v)[N]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
   for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
@@ -281,42 +284,48 @@ __device__ __forceinline__ void code_pipeline(Job &job, char *ring, CodeBars<C> 
       const uint32_t sums = ring0 + pos.slot * C::kStage + C::kW + C::kHalves * C::kB;
       ok = ok && warp_wait(&b.dfull[d.slot], d.round, abort_p, w.status, w.ns);
       tc_fence_after();
-#pragma unroll
-      for (int g = 0; g < C::kAll; ++g) {
-        if (!ok) continue;
-        // sixteen tokens' sums at a time (of eight tokens all planes' lie in one or two sixteens)
+      if (ok) {
+        // Sixteen tokens' sums of a group at a time (of eight tokens all planes' lie in one or two sixteens), of several
+        // groups where registers allow it, so that their way is waited for once.
         constexpr int kChunk = TOKENS < 16 ? TOKENS : 16, kCols = TOKENS < 16 ? C::kN : 16 * PLANES;
-        const uint32_t from = tmem_d + ((uint32_t)(q * 32) << 16) + (d.slot * C::kAll + g) * C::kN;
+        constexpr int kBatch = TOKENS > 16 ? 1 : C::kAll * kCols <= 64 ? C::kAll : 64 / kCols;
+        const uint32_t from = tmem_d + ((uint32_t)(q * 32) << 16) + d.slot * (C::kAll * C::kN);
 #pragma unroll
-        for (int t0 = 0; t0 < TOKENS; t0 += kChunk) {
-          float v[kCols];
-          tmem_columns<kCols>(from + t0, TOKENS, v);
-          if (g == C::kAll - 1 && t0 + kChunk == TOKENS) {  // everything is in registers: the tile's slots are free
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(&b.dempty[d.slot]);
-              mbar_arrive(&b.aempty[a.slot]);
+        for (int g0 = 0; g0 < C::kAll; g0 += kBatch)
+#pragma unroll
+          for (int t0 = 0; t0 < TOKENS; t0 += kChunk) {
+            float v[kBatch][kCols];
+#pragma unroll
+            for (int g = 0; g < kBatch; ++g) tmem_columns<kCols>(from + (g0 + g) * C::kN + t0, TOKENS, v[g]);
+            tmem_arrived(reinterpret_cast<float(&)[kBatch * kCols]>(v));
+            if (g0 + kBatch >= C::kAll && t0 + kChunk == TOKENS) {  // everything is in registers: the tile's slots are free
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) {
+                mbar_arrive(&b.dempty[d.slot]);
+                mbar_arrive(&b.aempty[a.slot]);
+              }
             }
+#pragma unroll
+            for (int g = 0; g < kBatch; ++g)
+#pragma unroll
+              for (int t4 = 0; t4 < kChunk; t4 += 4) {
+                const uint4 x4 = lds128(sums + ((g0 + g) * TOKENS + t0 + t4) * 4);
+                const float x[4] = {__uint_as_float(x4.x), __uint_as_float(x4.y), __uint_as_float(x4.z), __uint_as_float(x4.w)};
+                float f[4];
+                if constexpr (Job::kFactors) job.factors(sums, g0 + g, t0 + t4, f);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const int t = t4 + i;
+                  float s = v[g][(PLANES - 1) * kChunk + t];
+#pragma unroll
+                  for (int k = PLANES - 2; k >= 0; --k) s = fmaf(s, kPlane, v[g][k * kChunk + t]);
+                  s = fmaf(-zero[g0 + g], x[i], s);
+                  if constexpr (Job::kFactors) acc[t0 + t] = fmaf(s, scale[g0 + g] * f[i], acc[t0 + t]);
+                  else acc[t0 + t] = fmaf(s, scale[g0 + g], acc[t0 + t]);
+                }
+              }
           }
-#pragma unroll
-          for (int t4 = 0; t4 < kChunk; t4 += 4) {
-            const uint4 x4 = lds128(sums + (g * TOKENS + t0 + t4) * 4);
-            const float x[4] = {__uint_as_float(x4.x), __uint_as_float(x4.y), __uint_as_float(x4.z), __uint_as_float(x4.w)};
-            float f[4];
-            if constexpr (Job::kFactors) job.factors(sums, g, t0 + t4, f);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int t = t4 + i;
-              float s = v[(PLANES - 1) * kChunk + t];
-#pragma unroll
-              for (int k = PLANES - 2; k >= 0; --k) s = fmaf(s, kPlane, v[k * kChunk + t]);
-              s = fmaf(-zero[g], x[i], s);
-              if constexpr (Job::kFactors) acc[t0 + t] = fmaf(s, scale[g] * f[i], acc[t0 + t]);
-              else acc[t0 + t] = fmaf(s, scale[g], acc[t0 + t]);
-            }
-          }
-        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&b.empty[pos.slot]);

@@ -163,8 +163,10 @@ cudaError_t int4_tiles(const Int4MatmulParams &p, const Int4Maps &maps, const In
   MOE_INT4(4, 1);
   MOE_INT4(1, 2);
   MOE_INT4(2, 2);
-  MOE_INT4(1, 4);
-  MOE_INT4(2, 4);
+  if constexpr (PIECES == 1) {  // (more than 16 tokens come here in groups of 32 only: int4_tc_tokens)
+    MOE_INT4(1, 4);
+    MOE_INT4(2, 4);
+  }
 #undef MOE_INT4
   return cudaErrorInvalidValue;
 }

@@ -3,7 +3,6 @@
 // A tile is 128 rows of the weights and 128 columns.  Where the matrix has more row tiles than the GPU has SMs, a CTA takes
 // one row tile after another; otherwise the CTAs of a cluster share the columns of one, and their sums meet in shared
 // memory in the order of their ranks.
-#include <stdlib.h>
 #include "few_tc.cuh"
 #include "kernels.h"
 
@@ -160,7 +159,8 @@ cudaError_t tc_launch(const Int4MatmulParams &p, const Int4Maps &maps, int num_s
   if (e != cudaSuccess) return e;
   const int tiles = (p.w.n + kCodeRows - 1) / kCodeRows, blocks = (p.rows + TOKENS - 1) / TOKENS;
   // as many CTAs to a row tile as run at one time (of clusters of 8, 4 and 2 on 152 SMs 16, 36 and 75)
-  const int splits = tiles <= num_sms * 16 / 152 ? 8 : tiles <= num_sms * 36 / 152 ? 4 : tiles <= num_sms * 75 / 152 ? 2 : 1;
+  const long long all = (long long)tiles * blocks;
+  const int splits = all <= num_sms * 16 / 152 ? 8 : all <= num_sms * 36 / 152 ? 4 : all <= num_sms * 75 / 152 ? 2 : 1;
   const int busy = splits > 1 || tiles < num_sms ? tiles : num_sms;
   return launch_code_clusters(int4_tc_kernel<T, TOKENS, PLANES, GROUPS, ZP>, C::kRing + 1024, done, dim3(busy * splits, blocks), C::kThreads, splits, st, p,
                               maps, splits);
@@ -168,8 +168,10 @@ cudaError_t tc_launch(const Int4MatmulParams &p, const Int4Maps &maps, int num_s
 
 template <typename T, int GROUPS, bool ZP>
 cudaError_t tc_rows(const Int4MatmulParams &p, const Int4Maps &maps, int tokens, int num_sms, cudaStream_t st) {
-  if (tokens == 8) return tc_launch<T, 8, GROUPS, ZP>(p, maps, num_sms, st);
-  if (tokens == 16) return tc_launch<T, 16, GROUPS, ZP>(p, maps, num_sms, st);
+  if constexpr (GROUPS < 4) {  // (see int4_tc_tokens)
+    if (tokens == 8) return tc_launch<T, 8, GROUPS, ZP>(p, maps, num_sms, st);
+    if (tokens == 16) return tc_launch<T, 16, GROUPS, ZP>(p, maps, num_sms, st);
+  }
   return tc_launch<T, 32, GROUPS, ZP>(p, maps, num_sms, st);
 }
 
@@ -182,9 +184,18 @@ cudaError_t tc_typed(const Int4MatmulParams &p, const Int4Maps &maps, int tokens
 
 }  // namespace
 
-int int4_tc_tokens(int rows, int n, int k, bool f16, int num_sms) {
-  if (getenv("X0")) return 0;
-  return rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+// Splitting x takes a launch (4096 x 4096 in groups of 128: 7.3 us for a token, 8.1 for 16, by mma.sync 6.0 and 7.7), which
+// large matrices have time for (16384 x 2048: 7.3 and 8.6 for 7.6 and 8.8; 8192 x 8192: 14.3 and 16.5 for 18.4 and 18.1;
+// 129280 x 4096: 49 and 58 for 68 and 93), in groups of 64 larger ones (16384 x 2048: 8.2 for 7.7, 8192 x 8192: 16.6 for 18.7).
+// In groups of 32 the joining of eight groups a tile takes what the conversion saves (129280 x 4096: 100 and 142 for 96 and
+// 111).  Beyond 16 tokens mma.sync's registers leave it behind (4096 x 4096, 32 tokens: 9.7 for 16.4; 1031 x 2016: 7.3 for
+// 9.3), but for groups of 32 of many rows (8192 x 8192: 40 for 51, 16384 x 2048: 21 for 16; 64 tokens, twice 32 here,
+// 2048 x 8192: 23 for 32, 4096 x 4096: 23 for 17.5).
+int int4_tc_tokens(int rows, int n, int k, int group) {
+  const long long blocks = (rows + 31) / 32;
+  if (group == 32) return rows > 16 && n * blocks * blocks <= 12000 ? 32 : 0;
+  if (rows > 16) return 32;
+  return (long long)n * k >= (group == 128 ? 1 << 25 : 1 << 26) ? (rows <= 8 ? 8 : 16) : 0;
 }
 
 cudaError_t launch_int4_tc(const Int4MatmulParams &p, const Int4Maps &maps, int tokens, bool f16, int num_sms, cudaStream_t st) {

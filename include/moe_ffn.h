@@ -500,8 +500,7 @@ typedef struct moe_ffn_int4_matmul_args {
   void *workspace; size_t workspace_bytes;  /* at least moe_ffn_int4_matmul_workspace, 256-byte aligned */
 } moe_ffn_int4_matmul_args;
 
-/* Bytes of workspace that the call needs on the current device (pointers are not read), 0 for none; negative: an error
- * code. */
+/* Bytes of workspace that the call needs (pointers are not read), 0 for none; negative: an error code. */
 int64_t moe_ffn_int4_matmul_workspace(const moe_ffn_int4_matmul_args *a);
 
 /* These three return MOE_FFN_OK, NULL_PTR, ROWS_ZERO, ROWS_RANGE, BAD_CONFIG, ALIGNMENT, ALIAS, UNSUPPORTED or CUDA,
