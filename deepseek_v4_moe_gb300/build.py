@@ -29,7 +29,7 @@ NATIVE_KEY = os.path.join(BUILD, "native.key")
 NATIVE_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden"]
 SOURCES = ["moe_ffn.cu", "prelude.cu", "decode.cu", "decode_tc.cu", "dispatch.cu", "gemm_tc.cu", "splitgemm.cu",
            "noalloc.cu", "dense.cu", "dense_norm.cu", "dense_gemm.cu",
-           "dense_fp8.cu", "dense_gemv.cu", "few.cu", "int4.cu", "int4_tc.cu", "routed.cu"]
+           "dense_fp8.cu", "dense_gemv.cu", "few.cu", "int4.cu", "int4_tc.cu", "routed.cu", "routed_int4.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

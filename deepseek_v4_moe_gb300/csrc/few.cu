@@ -237,23 +237,49 @@ int check_routed(const char *who, const moe_ffn_routed_args *a) {
   return a->bits == 4 ? check_group(who, a->group) : MOE_FFN_OK;
 }
 
-int64_t logits_bytes(const moe_ffn_routed_args *a) { return ((int64_t)a->rows * a->experts * 4 + 255) / 256 * 256; }
 // experts with tokens, at most
 int64_t routed_groups(const moe_ffn_routed_args *a) {
   return (a->rows * a->top_k < a->experts ? a->rows * a->top_k : a->experts) + a->shared;
 }
-int64_t routed_workspace(const moe_ffn_routed_args *a) {
-  // h: a row for each token of each expert that it has chosen; with 16-bit weights for every token, and tokens up to a
-  // multiple of 8
-  const int64_t rows = a->bits == 4 ? (int64_t)a->rows * (a->top_k + a->shared) : routed_groups(a) * ((a->rows + 7) / 8 * 8);
-  return logits_bytes(a) + rows * a->inter * 2;
+// Offsets of the workspace's parts, each a multiple of 256, and sizes of 4-bit weights' parts.
+struct RoutedSpace {
+  int64_t h, x_planes, h_planes, x_sums, h_sums, back, h_max, masks, bytes;
+  int tokens, planes, x_groups, h_groups;
+};
+RoutedSpace routed_space(const moe_ffn_routed_args *a) {
+  RoutedSpace s = {};
+  int64_t at = 0;
+  auto part = [&](int64_t bytes) {
+    const int64_t from = at;
+    at += (bytes + 255) / 256 * 256;
+    return from;
+  };
+  const int64_t R = a->rows, I = a->inter, H = a->hidden, G = routed_groups(a);
+  part(R * a->experts * 4);  // the logits
+  s.h = part(G * (a->bits == 4 ? R : (R + 7) / 8 * 8) * I * 2);
+  if (a->bits == 4) {
+    s.tokens = moe::routed_code_tokens(a->rows);
+    s.planes = a->type == MOE_FFN_F16 ? 3 : 2;
+    const int columns = 128 * moe::code_halves(s.tokens, s.planes, 128 / a->group);  // of a tile
+    s.x_groups = (int)((H + columns - 1) / columns * (columns / a->group));
+    s.h_groups = (int)((I + columns - 1) / columns * (columns / a->group));
+    s.x_planes = part(s.planes * s.tokens * H);
+    s.h_planes = part(G * s.planes * s.tokens * I);
+    s.x_sums = part((int64_t)s.x_groups * s.tokens * 4);
+    s.h_sums = part(G * s.h_groups * s.tokens * 4);
+    s.back = part(R * 4);
+    s.h_max = part(R * 4);
+    s.masks = part(G * 4);
+  }
+  s.bytes = at;
+  return s;
 }
 
 }  // namespace
 
 extern "C" int64_t moe_ffn_routed_workspace(const moe_ffn_routed_args *a) {
   const int rc = check_routed("routed_workspace", a);
-  return rc ? rc : routed_workspace(a);
+  return rc ? rc : routed_space(a).bytes;
 }
 
 extern "C" int moe_ffn_routed_forward(const moe_ffn_routed_args *a, void *stream) {
@@ -299,7 +325,8 @@ extern "C" int moe_ffn_routed_forward(const moe_ffn_routed_args *a, void *stream
   for (int i = 1; i < (S ? 6 : 3); ++i)  // one kernel reads several matrices, with zero points or without
     if ((m[i].zeros != nullptr) != (m[0].zeros != nullptr))
       return fail(MOE_FFN_ERR_BAD_CONFIG, "%s: %s and %s must both have zero points or neither", who, names[0], names[i]);
-  const int64_t need = routed_workspace(a);
+  const RoutedSpace space = routed_space(a);
+  const int64_t need = space.bytes;
   if (a->workspace_bytes < (size_t)need)
     return fail(MOE_FFN_ERR_NO_MEMORY, "%s: workspace of %zu bytes, needs %lld", who, a->workspace_bytes, (long long)need);
   const Span outs[] = {span("y", a->y, R, H, a->ld_y, 2), span("indices", a->indices, R, K, K, 4),
@@ -334,24 +361,44 @@ extern "C" int moe_ffn_routed_forward(const moe_ffn_routed_args *a, void *stream
   p.ld_y = a->ld_y;
   p.indices = a->indices;
   p.weights = a->weights;
-  p.logits = static_cast<float *>(a->workspace);
-  p.h = reinterpret_cast<uint16_t *>(static_cast<char *>(a->workspace) + logits_bytes(a));
+  char *ws = static_cast<char *>(a->workspace);
+  p.logits = reinterpret_cast<float *>(ws);
+  p.h = reinterpret_cast<uint16_t *>(ws + space.h);
+  p.groups = (int)routed_groups(a);
   DeviceSide dev;
   if ((rc = device_side(who, &dev))) return rc;
   p.waits = moe::Waits{dev.status, dev.wait_ns, dev.inject};
   moe::RoutedMaps maps = {}, down = {};
   CUtensorMap *to[] = {&maps.gate, &maps.up, &down.gate, &maps.s_gate, &maps.s_up, &down.s_gate};
   bool ok = true;
+  const int halves = a->bits == 4 ? moe::code_halves(space.tokens, space.planes, 128 / a->group) : 0;
   for (int i = 0; i < (S ? 6 : 3); ++i) {
     const int64_t count = i < 3 ? E : S, n = m[i].n, k = m[i].k;
-    ok = ok && (a->bits == 4 ? encode_map(to[i], m[i].w, 1, k / 2, count * n, k / 2, 16, 64)
-                             : encode_map(to[i], m[i].w, 2, k, count * n, k, i % 3 == 2 ? 128 : 64));
+    const int box = i % 3 == 2 ? 128 : 64;
+    ok = ok && (a->bits == 4 ? encode_map(to[i], m[i].w, 1, k / 2, count * n, k / 2, box, 64 * halves)
+                             : encode_map(to[i], m[i].w, 2, k, count * n, k, box));
   }
+  const bool f16 = a->type == MOE_FFN_F16;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (a->bits == 16) {
     const int64_t R8 = (R + 7) / 8 * 8;
-    ok = ok && encode_map(&maps.tokens, a->x, 2, H, R, a->ld_x, (int)R8) &&
-         encode_map(&down.tokens, p.h, 2, I, routed_groups(a) * R8, I, (int)R8);
+    if (!ok || !encode_map(&maps.tokens, a->x, 2, H, R, a->ld_x, (int)R8) ||
+        !encode_map(&down.tokens, p.h, 2, I, p.groups * R8, I, (int)R8))
+      return fail(MOE_FFN_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", who);
+    return launched(who, moe::launch_routed(p, maps, down, f16, sms, st));
   }
-  if (!ok) return fail(MOE_FFN_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", who);
-  return launched(who, moe::launch_routed(p, maps, down, a->type == MOE_FFN_F16, a->bits == 4, sms, static_cast<cudaStream_t>(stream)));
+  p.x_planes = reinterpret_cast<uint2 *>(ws + space.x_planes);
+  p.h_planes = reinterpret_cast<uint2 *>(ws + space.h_planes);
+  p.x_sums = reinterpret_cast<float *>(ws + space.x_sums);
+  p.h_sums = reinterpret_cast<float *>(ws + space.h_sums);
+  p.back = reinterpret_cast<float *>(ws + space.back);
+  p.h_max = reinterpret_cast<uint32_t *>(ws + space.h_max);
+  p.masks = reinterpret_cast<uint32_t *>(ws + space.masks);
+  p.x_groups = space.x_groups;
+  p.h_groups = space.h_groups;
+  const int rows = space.planes * space.tokens;
+  if (!ok || !encode_map(&maps.tokens, p.x_planes, 1, H, rows, H, rows) ||
+      !encode_map(&down.tokens, p.h_planes, 1, I, (int64_t)p.groups * rows, I, rows))
+    return fail(MOE_FFN_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", who);
+  return launched(who, moe::launch_routed_int4(p, maps, down, f16, sms, st));
 }

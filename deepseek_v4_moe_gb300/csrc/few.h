@@ -22,6 +22,12 @@ struct FewMatrix {
 // room in TMEM.  groups: of 128 columns.
 constexpr int code_halves(int tokens, int planes, int groups) { return 2 * groups * ((tokens * planes + 15) / 16 * 16) <= 384 ? 2 : 1; }
 
+// CTAs of a cluster that share a row tile's columns: as many as run at one time (of clusters of 8, 4 and 2 with an SM for
+// each CTA, 12, 36 and 75 on 152 SMs: 16 tiles of 2048 x 8192 by 32 tokens took 18 us in eights, 12.5 in fours)
+inline int code_splits(long long tiles, int num_sms) {
+  return tiles <= num_sms * 12 / 152 ? 8 : tiles <= num_sms * 36 / 152 ? 4 : tiles <= num_sms * 75 / 152 ? 2 : 1;
+}
+
 // what a kernel with bounded waits reports to, how long they last, and whether one is to run out
 struct Waits {
   int *status;
@@ -96,16 +102,26 @@ struct RoutedParams {
   int32_t *indices;                    // [rows, top_k] or none
   float *weights;
   float *logits;                       // workspace: [rows, experts]
-  uint16_t *h;                         // workspace: [rows, top_k + shared, inter]
+  uint16_t *h;                         // workspace: of 16-bit weights [groups, rows up to a multiple of 8, inter], of 4-bit
+                                       // ones [groups, rows, inter]; a group is an expert with tokens
+  int groups;                          // at most
+  // Workspace of 4-bit weights: x and h as planes [1 or groups][planes][tokens][k], their groups' sums [1 or groups]
+  // [x_groups or h_groups][tokens], what products of x are multiplied by, the largest |h| of a token, groups' tokens.
+  uint2 *x_planes, *h_planes;
+  float *x_sums, *h_sums, *back;
+  uint32_t *h_max, *masks;
+  int x_groups, h_groups;              // of a row, up to a whole tile
   Waits waits;
 };
-// over all experts' rows of each matrix; of the down kernels gate and s_gate are down and s_down.  4 bits: boxes of 64
-// bytes x 16 rows.  16 bits: boxes of 128 bytes x 64 rows (down: 128), and tokens: x, or h, boxes of 128 bytes x the
-// tokens up to a multiple of 8.
+// Over all experts' rows of each matrix; of the down kernels gate and s_gate are down and s_down; boxes of 64 rows (down:
+// 128).  16 bits: boxes of 128 bytes, and tokens: x, or h, boxes of 128 bytes x the tokens up to a multiple of 8.  4 bits:
+// boxes of 64 bytes for each half of a tile, and tokens: planes, boxes of 128 bytes x routed_code_tokens' of each.
 struct RoutedMaps {
   CUtensorMap gate, up, s_gate, s_up, tokens;
 };
-cudaError_t launch_routed(const RoutedParams &p, const RoutedMaps &maps, const RoutedMaps &down, bool f16, bool bits4,
-                          int num_sms, cudaStream_t st);
+cudaError_t launch_routed(const RoutedParams &p, const RoutedMaps &maps, const RoutedMaps &down, bool f16, int num_sms, cudaStream_t st);
+inline int routed_code_tokens(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
+cudaError_t launch_routed_int4(const RoutedParams &p, const RoutedMaps &maps, const RoutedMaps &down, bool f16, int num_sms,
+                               cudaStream_t st);
 
 }  // namespace moe

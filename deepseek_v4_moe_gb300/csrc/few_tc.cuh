@@ -100,6 +100,51 @@ __device__ __forceinline__ float split8(const float (&v)[8], float scale, uint2 
   return sum;
 }
 
+// A row's planes (out, `apart` between two planes) and groups' sums, by a CTA of 256: k8 eights of columns of x, scaled;
+// `groups` of `per` eights up to the last tile's, each sum `tokens` floats from the one before.  x none: zeros.
+template <typename T, int PLANES>
+__device__ __forceinline__ void split_row(const T *x, float scale, int k8, int groups, int per, uint2 *out, size_t apart, float *sums, int tokens) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, all = groups * per;
+  for (int i0 = warp * 32; i0 < all; i0 += 256) {
+    const int i = i0 + lane;
+    float sum = 0.f;
+    if (i < k8) {
+      uint2 o[PLANES] = {};
+      if (x) {
+        float v[8];
+        load_eight<T, true>(x + 8 * i, 0, 1, 8, v);
+        sum = split8<PLANES>(v, scale, o);
+      }
+#pragma unroll
+      for (int k = 0; k < PLANES; ++k) out[k * apart + i] = o[k];
+    }
+    for (int o = per >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (i < all && i % per == 0) sums[i / per * tokens] = sum * 0x1p-9f;
+  }
+}
+// the bits of a row's largest magnitude, by a CTA of 256
+template <typename T>
+__device__ __forceinline__ uint32_t row_max(const T *x, int k8) {
+  __shared__ uint32_t most[8];
+  uint32_t m = 0;
+  for (int i = threadIdx.x; i < k8; i += 256) {
+    float v[8];
+    load_eight<T, true>(x + 8 * i, 0, 1, 8, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+  }
+  m = __reduce_max_sync(0xffffffffu, m);
+  if (threadIdx.x % 32 == 0) most[threadIdx.x >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, most[i]);
+  return m;
+}
+// what a row's sums are multiplied by; a row that is not finite gives NaN
+__device__ __forceinline__ float way_back(uint32_t max) {
+  return max >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : two_to(-plane_exponent(max));
+}
+
 // instruction descriptor, kind::f8f6f4: E4M3 operands (K-major), f32 sums, M x N
 __device__ __forceinline__ uint32_t idesc_e4m3(int M, int N) { return 1u << 4 | (uint32_t)(N >> 3) << 17 | (uint32_t)(M >> 4) << 24; }
 

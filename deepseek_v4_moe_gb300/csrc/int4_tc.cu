@@ -9,46 +9,19 @@
 namespace moe {
 namespace {
 
-// x as planes and groups' sums: a CTA takes a row (its largest magnitude first).
+// x as planes and groups' sums: a CTA takes a row.
 template <typename T, int PLANES>
 __global__ void __launch_bounds__(256) int4_planes_kernel(const __grid_constant__ Int4MatmulParams p, int tokens) {
-  __shared__ uint32_t most[8];
-  const int row = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k8 = p.w.k / 8, per = 1 << (p.w.group_shift - 3);
+  const int row = blockIdx.x, k8 = p.w.k / 8, block = row / tokens, token = row % tokens;
   const T *x = static_cast<const T *>(p.x) + row * p.ld_x;
   pdl_wait();
   // The product may come and fetch weights: not earlier, as what the wait was for may write them.
   pdl_trigger();
-  uint32_t m = 0;
-  for (int i = threadIdx.x; i < k8; i += 256) {
-    float v[8];
-    load_eight<T, true>(x + 8 * i, 0, 1, 8, v);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(v[e]) & 0x7FFFFFFFu);
-  }
-  m = __reduce_max_sync(0xffffffffu, m);
-  if (lane == 0) most[warp] = m;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, most[i]);
-  const int e = plane_exponent(m), block = row / tokens, token = row % tokens;
-  // what a row's sums are multiplied by; a row that is not finite gives NaN
-  if (threadIdx.x == 0) p.back[row] = m >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : two_to(-e);
-  const float scale = two_to(e);
-  const int all = p.sum_groups * per;  // up to whole groups: their sums are of all their columns
-  for (int i0 = warp * 32; i0 < all; i0 += 256) {
-    const int i = i0 + lane;
-    float sum = 0.f;
-    if (i < k8) {
-      float v[8];
-      load_eight<T, true>(x + 8 * i, 0, 1, 8, v);
-      uint2 o[PLANES];
-      sum = split8<PLANES>(v, scale, o);
-#pragma unroll
-      for (int k = 0; k < PLANES; ++k) p.planes[(((size_t)block * PLANES + k) * tokens + token) * k8 + i] = o[k];
-    }
-    for (int o = per >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (i < all && i % per == 0) p.sums[((size_t)block * p.sum_groups + i / per) * tokens + token] = sum * 0x1p-9f;
-  }
+  const uint32_t most = row_max(x, k8);
+  if (threadIdx.x == 0) p.back[row] = way_back(most);
+  split_row<T, PLANES>(x, two_to(plane_exponent(most)), k8, p.sum_groups, 1 << (p.w.group_shift - 3),
+                       p.planes + ((size_t)block * PLANES * tokens + token) * k8, (size_t)tokens * k8,
+                       p.sums + (size_t)block * p.sum_groups * tokens + token, tokens);
 }
 
 template <typename T, int TOKENS, int PLANES, int GROUPS, bool ZP>
@@ -158,9 +131,7 @@ cudaError_t tc_launch(const Int4MatmulParams &p, const Int4Maps &maps, int num_s
   const cudaError_t e = launch_pdl(int4_planes_kernel<T, PLANES>, dim3(p.rows), dim3(256), 0, st, p, TOKENS);
   if (e != cudaSuccess) return e;
   const int tiles = (p.w.n + kCodeRows - 1) / kCodeRows, blocks = (p.rows + TOKENS - 1) / TOKENS;
-  // as many CTAs to a row tile as run at one time (of clusters of 8, 4 and 2 on 152 SMs 16, 36 and 75)
-  const long long all = (long long)tiles * blocks;
-  const int splits = all <= num_sms * 16 / 152 ? 8 : all <= num_sms * 36 / 152 ? 4 : all <= num_sms * 75 / 152 ? 2 : 1;
+  const int splits = code_splits((long long)tiles * blocks, num_sms);
   const int busy = splits > 1 || tiles < num_sms ? tiles : num_sms;
   return launch_code_clusters(int4_tc_kernel<T, TOKENS, PLANES, GROUPS, ZP>, C::kRing + 1024, done, dim3(busy * splits, blocks), C::kThreads, splits, st, p,
                               maps, splits);

@@ -1,0 +1,264 @@
+// The routed layer with 4-bit weights on the FP8 tensor cores (sm_103a; few_tc.cuh), in four kernels:
+//
+//   route   l = x Wr^T, and x as planes
+//   up      each CTA chooses the experts from l; h = weight act(x Wg_e^T) (x Wu_e^T), in 16 bits
+//   split   h as planes
+//   down    y = sum over the experts of h Wd_e^T
+//
+// Bound by the chosen experts' codes on their way from memory and through registers into operands: each is read once, for
+// all tokens, which are the right operand's columns for every expert.  So the down kernel, whose operand is zero where a
+// token has not chosen an expert, adds all experts' products in its registers, in one order.
+//
+// A token's h has one power of two for all of its experts, from the largest magnitude among them (an atomic maximum: of
+// any order the same), so that their products can be added as they are: what is lost of an expert's h is below 2^-22 of
+// the token's largest (f16: 2^-27), and the sum that it goes to holds that one.
+#include "few_tc.cuh"
+#include "kernels.h"
+#include "routed.cuh"
+
+namespace moe {
+namespace {
+
+// CTAs from route_ctas on: a row of x each
+template <typename T, typename TR, int PLANES>
+__global__ void __launch_bounds__(256) routed_planes_kernel(const __grid_constant__ RoutedParams p, int tokens) {
+  const int n = route_ctas(p), row = blockIdx.x - n, k8 = p.hidden / 8;
+  pdl_wait();
+  pdl_trigger();
+  if (row < 0) {
+    route_logits<T, TR>(p, blockIdx.x * kRouteExperts);
+    return;
+  }
+  const T *x = static_cast<const T *>(p.x) + row * p.ld_x;
+  const uint32_t most = row_max(x, k8);
+  if (threadIdx.x == 0) {
+    p.back[row] = way_back(most);
+    p.h_max[row] = 0u;
+  }
+  split_row<T, PLANES>(x, two_to(plane_exponent(most)), k8, p.x_groups, 1 << (p.gate.group_shift - 3), p.x_planes + (size_t)row * k8,
+                       (size_t)tokens * k8, p.x_sums + row, tokens);
+}
+
+// a CTA for each row of h: a token of an expert; zeros where it has not chosen it
+template <typename T, int PLANES>
+__global__ void __launch_bounds__(256) routed_split_kernel(const __grid_constant__ RoutedParams p, int tokens) {
+  const int token = blockIdx.x, group = blockIdx.y, k8 = p.inter / 8;
+  pdl_wait();
+  // The down kernel's CTAs may come, choose and fetch weights.
+  pdl_trigger();
+  const uint32_t mask = p.masks[group];
+  if (!mask) return;  // no such group
+  const T *h = reinterpret_cast<const T *>(p.h) + ((size_t)group * p.rows + token) * p.inter;
+  split_row<T, PLANES>(mask >> token & 1 ? h : nullptr, two_to(plane_exponent(__ldcg(p.h_max + token))), k8, p.h_groups,
+                       1 << (p.gate.group_shift - 3), p.h_planes + ((size_t)group * PLANES * tokens + token) * k8, (size_t)tokens * k8,
+                       p.h_sums + (size_t)group * p.h_groups * tokens + token, tokens);
+}
+
+// Up: a unit is 64 rows of a group's gate and 64 of its up matrix.  Down: one unit, 128 rows of all groups' matrices, whose
+// tiles the CTAs of a cluster share.
+template <bool UP, typename T, int TOKENS, int PLANES, int GROUPS>
+struct LayerJob {
+  using C = CodeCfg<TOKENS, PLANES, GROUPS>;
+  static constexpr bool kFactors = false;
+  const RoutedParams &p;
+  const RoutedMaps &maps;
+  const Choice &c;
+  float *sums;                    // up: [2][TOKENS][64]; down: [TOKENS][128]
+  int tiles, strips;              // of a group; up: units of a group
+  int row_tile, first, end;       // down
+  mutable int turn;
+  struct Place {
+    int unit, group, tile, left, tiles, strips, step;
+    __device__ __forceinline__ bool more() const { return left > 0; }
+    __device__ __forceinline__ void next() {
+      if constexpr (!UP) --left;
+      if (++tile == tiles) {
+        tile = 0;
+        if constexpr (UP) {
+          left -= step;
+          unit += step;
+          group = unit / strips;
+        } else {
+          ++group;
+        }
+      }
+    }
+  };
+  __device__ __forceinline__ Place begin() const {
+    if constexpr (UP)
+      return Place{(int)blockIdx.x, (int)blockIdx.x / strips, 0, c.groups * strips - (int)blockIdx.x, tiles, strips, (int)gridDim.x};
+    else return Place{0, first / tiles, first % tiles, end - first, tiles, 1, 1};
+  }
+  __device__ __forceinline__ bool ends(const Place &a) const { return UP ? a.tile == tiles - 1 : a.left == 1; }
+  // the group's matrix among its kind's
+  __device__ __forceinline__ int matrix_of(const Place &a, bool &shared) const {
+    const int e = c.group_expert[a.group];
+    shared = e >= p.experts;
+    return shared ? e - p.experts : e;
+  }
+  __device__ __forceinline__ void weights(const Place &a, uint32_t at, uint32_t bar) const {
+    bool shared;
+    const int e = matrix_of(a, shared), x = a.tile * (64 * C::kHalves);
+    if constexpr (UP) {
+      const int r = e * p.inter + (a.unit - a.group * strips) * 64;
+      tma_load_2d_one<false>(at, shared ? &maps.s_gate : &maps.gate, bar, x, r);
+      tma_load_2d_one<false>(at + C::kW / 2, shared ? &maps.s_up : &maps.up, bar, x, r);
+    } else {
+      tma_load_2d_one<false>(at, shared ? &maps.s_gate : &maps.gate, bar, x, e * p.hidden + row_tile * kCodeRows);
+    }
+  }
+  __device__ __forceinline__ void ready() const {
+    if constexpr (!UP) pdl_wait();
+  }
+  __device__ __forceinline__ void tokens(const Place &a, uint32_t at, uint32_t to, uint32_t bar) const {
+#pragma unroll
+    for (int h = 0; h < C::kHalves; ++h)
+      tma_load_2d_one<false>(at + h * C::kB, &maps.tokens, bar, (a.tile * C::kHalves + h) * 128, UP ? 0 : a.group * C::kRows);
+    const float *from = UP ? p.x_sums : p.h_sums + (size_t)a.group * p.h_groups * TOKENS;
+    tma_bulk_one(to, from + a.tile * (C::kAll * TOKENS), C::kSums, bar);
+  }
+  struct Row {
+    int row;
+  };
+  __device__ __forceinline__ void row_at(Row &r, const Place &a, int row) const {
+    if constexpr (UP) r.row = min((a.unit - a.group * strips) * 64 + row % 64, p.inter - 1) | (row >= 64 ? 1 << 30 : 0);
+    else r.row = min(row_tile * kCodeRows + row, p.hidden - 1);
+  }
+  __device__ __forceinline__ void scales(const Row &r, const Place &a, float (&scale)[C::kAll], float (&zero)[C::kAll]) const {
+    bool shared;
+    const int e = matrix_of(a, shared);
+    const bool up = UP && r.row >> 30;
+    const FewMatrix &m = UP ? (shared ? (up ? p.s_up : p.s_gate) : up ? p.up : p.gate) : shared ? p.s_down : p.down;
+    const long long at = ((long long)e * (UP ? p.inter : p.hidden) + (r.row & 0x3FFFFFFF)) * m.groups;
+#pragma unroll
+    for (int g = 0; g < C::kAll; ++g) {
+      const int i = min(a.tile * C::kAll + g, m.groups - 1);
+      scale[g] = to_f32(reinterpret_cast<const T *>(m.scales)[at + i]);
+      zero[g] = m.zeros ? (float)(m.zeros[at + i] & 15u) : 8.f;
+    }
+  }
+  __device__ __forceinline__ void finish(const Place &a, int row, const float (&acc)[TOKENS], bool) const {
+    if constexpr (UP) {
+      float *u = sums + turn * (TOKENS * 64);
+      turn ^= 1;
+      if (row >= 64)
+#pragma unroll
+        for (int t = 0; t < TOKENS; ++t)
+          if (t < p.rows) u[t * 64 + row - 64] = acc[t];
+      asm volatile("bar.sync 3, 128;" ::: "memory");
+      if (row >= 64) return;
+      const int at = (a.unit - a.group * strips) * 64 + row, e = c.group_expert[a.group];
+      const uint32_t mask = c.group_mask[a.group];
+      uint16_t *h = p.h + (size_t)a.group * p.rows * p.inter + at;
+#pragma unroll
+      for (int t = 0; t < TOKENS; ++t) {
+        if (t >= p.rows) break;
+        if (!(mask >> t & 1)) continue;
+        uint32_t size = 0u;
+        if (at < p.inter) {
+          const float back = 512.f * p.back[t];
+          // rounded to 16 bits as the 16-bit layer does
+          const T out = from_f32<T>(act_value(p.act, acc[t] * back) * (u[t * 64 + row] * back) * weight_of(p, c, e, t));
+          h[(size_t)t * p.inter] = *reinterpret_cast<const uint16_t *>(&out);
+          size = __float_as_uint(to_f32(out)) & 0x7FFFFFFFu;
+        }
+        size = __reduce_max_sync(0xffffffffu, size);
+        if (row % 32 == 0) atomicMax(p.h_max + t, size);
+      }
+    } else {
+#pragma unroll
+      for (int t = 0; t < TOKENS; ++t)
+        if (t < p.rows) sums[t * kCodeRows + row] = acc[t];
+    }
+  }
+};
+
+template <bool UP, typename T, int TOKENS, int PLANES, int GROUPS>
+__global__ void __launch_bounds__(CodeCfg<TOKENS, PLANES, GROUPS>::kThreads, 1)
+    routed_codes_kernel(const __grid_constant__ RoutedParams p, const __grid_constant__ RoutedMaps maps, int splits) {
+  using C = CodeCfg<TOKENS, PLANES, GROUPS>;
+  extern __shared__ char smem[];
+  __shared__ __align__(8) CodeBars<C> bars;
+  __shared__ Choice c;
+  __shared__ float sums[TOKENS * kCodeRows];
+  char *ring = smem + (-smem_u32(smem) & 1023u);
+  code_setup<C>(bars);
+  if constexpr (UP) {
+    pdl_wait();
+    pdl_trigger();
+  }
+  choose_groups(p, c, reinterpret_cast<uint32_t *>(ring), UP && blockIdx.x == 0);  // (the ring is not in use yet)
+  const int tiles = ((UP ? p.hidden : p.inter) + 128 * C::kHalves - 1) / (128 * C::kHalves), strips = (p.inter + 63) / 64;
+  const int rank = UP ? 0 : blockIdx.x % splits, row_tile = UP ? 0 : blockIdx.x / splits;
+  const long long all = (long long)c.groups * tiles;
+  if (UP && blockIdx.x == 0)
+    for (int g = threadIdx.x; g < p.groups; g += C::kThreads) p.masks[g] = g < c.groups ? c.group_mask[g] : 0u;
+  const LayerJob<UP, T, TOKENS, PLANES, GROUPS> job{p, maps, c, sums, tiles, strips, row_tile, (int)(all * rank / splits),
+                                                    (int)(all * (rank + 1) / splits), 0};
+  if (!UP && job.first == job.end)
+    for (int i = threadIdx.x; i < TOKENS * kCodeRows; i += C::kThreads) sums[i] = 0.f;
+  code_pipeline<C, TOKENS, PLANES, GROUPS>(job, ring, bars, p.waits);
+  if constexpr (!UP) {  // the CTAs' sums in the order of their ranks, a part of the rows by each
+    if (splits > 1) cluster_sync();
+    const int part = kCodeRows / splits, row0 = rank * part;
+    for (int i = threadIdx.x; i < part * p.rows; i += C::kThreads) {
+      const int row = row0 + i % part, t = i / part, n = row_tile * kCodeRows + row;
+      float v = 0.f, x[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r)  // all loads before the first sum
+        if (r < splits)
+          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x[r]) : "r"(in_cta(&sums[t * kCodeRows + row], r)) : "memory");
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        if (r < splits) v += x[r];
+      if (n < p.hidden) static_cast<T *>(p.y)[t * p.ld_y + n] = from_f32<T>(v * 512.f * way_back(__ldcg(p.h_max + t)));
+    }
+    if (splits > 1) cluster_sync();
+  }
+  code_end(bars);
+}
+
+template <typename T, int TOKENS, int GROUPS>
+cudaError_t codes_launch(const RoutedParams &p, const RoutedMaps &maps, const RoutedMaps &down, int num_sms, cudaStream_t st) {
+  constexpr int PLANES = std::is_same<T, __half>::value ? 3 : 2;
+  using C = CodeCfg<TOKENS, PLANES, GROUPS>;
+  constexpr size_t smem = C::kRing + 1024;
+  static std::atomic<unsigned long long> done[2];
+  cudaError_t e = allow_smem((const void *)routed_codes_kernel<true, T, TOKENS, PLANES, GROUPS>, smem, done[0]);
+  if (e == cudaSuccess)
+    e = launch_pdl(p.router_f32 ? routed_planes_kernel<T, float, PLANES> : routed_planes_kernel<T, T, PLANES>, dim3(route_ctas(p) + p.rows),
+                   dim3(256), 0, st, p, TOKENS);
+  const long long units = (long long)p.groups * ((p.inter + 63) / 64);
+  if (e == cudaSuccess)
+    e = launch_pdl(routed_codes_kernel<true, T, TOKENS, PLANES, GROUPS>, dim3((unsigned)(units < num_sms ? units : num_sms)),
+                   dim3(C::kThreads), smem, st, p, maps, 1);
+  if (e == cudaSuccess) e = launch_pdl(routed_split_kernel<T, PLANES>, dim3(p.rows, p.groups), dim3(256), 0, st, p, TOKENS);
+  if (e != cudaSuccess) return e;
+  const int tiles = (p.hidden + kCodeRows - 1) / kCodeRows, splits = code_splits(tiles, num_sms);
+  return launch_code_clusters(routed_codes_kernel<false, T, TOKENS, PLANES, GROUPS>, smem, done[1], dim3(tiles * splits), C::kThreads, splits,
+                              st, p, down, splits);
+}
+
+template <typename T, int GROUPS>
+cudaError_t codes_tokens(const RoutedParams &p, const RoutedMaps &maps, const RoutedMaps &down, int num_sms, cudaStream_t st) {
+  const int tokens = routed_code_tokens(p.rows);
+  if (tokens == 8) return codes_launch<T, 8, GROUPS>(p, maps, down, num_sms, st);
+  if (tokens == 16) return codes_launch<T, 16, GROUPS>(p, maps, down, num_sms, st);
+  return codes_launch<T, 32, GROUPS>(p, maps, down, num_sms, st);
+}
+template <typename T>
+cudaError_t codes_typed(const RoutedParams &p, const RoutedMaps &maps, const RoutedMaps &down, int num_sms, cudaStream_t st) {
+  const int shift = p.gate.group_shift;
+  if (shift == 7) return codes_tokens<T, 1>(p, maps, down, num_sms, st);
+  if (shift == 6) return codes_tokens<T, 2>(p, maps, down, num_sms, st);
+  return codes_tokens<T, 4>(p, maps, down, num_sms, st);
+}
+
+}  // namespace
+
+cudaError_t launch_routed_int4(const RoutedParams &p, const RoutedMaps &maps, const RoutedMaps &down, bool f16, int num_sms,
+                               cudaStream_t st) {
+  return f16 ? codes_typed<__half>(p, maps, down, num_sms, st) : codes_typed<__nv_bfloat16>(p, maps, down, num_sms, st);
+}
+
+}  // namespace moe
