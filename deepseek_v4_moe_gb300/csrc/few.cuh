@@ -1,13 +1,11 @@
-// What the kernels for a few rows share (sm_103a): strips of 16 rows of a weight matrix streamed through a warp and
-// multiplied with up to 32 tokens.
+// 4-bit weights on mma.sync (sm_103a): strips of 16 rows of the matrix streamed through a warp and multiplied with up to
+// 32 tokens.
 //
 // The weights are the left operand of mma.m16n8k16, the tokens its eight columns: a few tokens cost the tensor cores as
-// much as one, the sums are f32, and the work left to the CUDA cores is the 4-bit weights' conversion.  (tcgen05 wants its
-// left operand of 128 rows in shared or tensor memory: 4-bit weights would have to be written there in 16 bits, four
-// times the bytes that come from memory, and read again.)
+// much as one, the sums are f32, and the work left to the CUDA cores is the codes' conversion to 16 bits, in registers.
+// It takes x as it is, so that a product is one launch; where the conversion bounds it, few_tc.cuh's form is faster.
 //
-// TMA brings 64 bytes of each of a strip's rows (32 columns in 16 bits, 128 in 4) into a ring, and the tokens' columns
-// beside them: with the addresses in every lane 16 tokens by 129280 x 4096 took 165 us at 1.6 instructions a cycle, and
+// TMA brings 64 bytes (128 columns) of each of a strip's rows into a ring, and the tokens' columns beside them: with the addresses in every lane 16 tokens by 129280 x 4096 took 165 us at 1.6 instructions a cycle, and
 // with the tokens read through the L1 their latency stopped the warps.
 // The order of k within a tile is free as long as both operands have the same one: lane 4 g + t of a warp holds columns
 // 32 c + 8 t .. + 7 of row g (and g + 8), as one 16-byte read of x gives them for token g.
@@ -28,11 +26,7 @@ constexpr int kFewWarps = 8;
 constexpr int kBoxBytes = 16 * 64;       // 64 bytes of each of a strip's rows
 constexpr int kPartFloats = 8 * 20;      // a strip's sums with 8 tokens, rows of 16 padded to 20 against conflicts
 
-// boxes of a strip in a tile, and a tile's columns
-template <int BITS>
-constexpr int kBoxes = BITS == 16 ? 2 : 1;
-template <int BITS>
-constexpr int kTileK = kBoxes<BITS> * 512 / BITS;
+constexpr int kTileK = 128;              // columns of a tile: a box
 
 template <typename T, bool ZERO>
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -116,38 +110,6 @@ struct Operand {
   }
 };
 
-// The products of a tile's strips.  PIECES: of 32 columns in a group of 4-bit weights, and ZP: they have zero
-// points, at compile time, so that a tile's products are one run of instructions in which the strips overlap.
-template <typename T, int BITS, int PIECES, bool ZP, int M, int NT, bool ROWS8>
-struct Tile;
-
-template <typename T, int M, int NT, bool ROWS8>
-struct Tile<T, 16, 0, false, M, NT, ROWS8> {
-  Operand<kBoxes<16>, NT, ROWS8> x;
-  // some: bit i where eight i has tokens at all
-  __device__ __forceinline__ void multiply(uint32_t place, uint32_t tokens, unsigned some, float (&acc)[M][NT][4]) const {
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const uint32_t at = place + g * 64 + ((t ^ (g >> 1 & 3)) << 4);
-#pragma unroll
-    for (int c = 0; c < kBoxes<16>; ++c) {
-      uint4 b[NT];
-#pragma unroll
-      for (int i = 0; i < NT; ++i) b[i] = x.get(tokens, c, i);
-#pragma unroll
-      for (int s = 0; s < M; ++s) {
-        const uint32_t box = at + (s * kBoxes<16> + c) * kBoxBytes;
-        const uint4 lo = lds128(box), hi = lds128(box + 512);
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-          if (NT == 1 || some >> i & 1) {
-            mma16816<T, false>(acc[s][i], lo.x, hi.x, lo.y, hi.y, b[i].x, b[i].y);
-            mma16816<T, false>(acc[s][i], lo.z, hi.z, lo.w, hi.w, b[i].z, b[i].w);
-          }
-      }
-    }
-  }
-};
-
 // A strip's scales and zero points of a tile.  Lane l reads row l & 15; groups l >> 4 of the tile, and + 2 where it has
 // four; where it has one, lanes from 16 on read that of this warp's next tile, and every other tile reads nothing.
 // They are read one reading ahead of their use.
@@ -206,12 +168,14 @@ __device__ __forceinline__ uint4 in_pairs(const uint4 v) {
                     __byte_perm(v.y, v.w, 0x7632));
 }
 
+// The products of a tile's strips.  PIECES: of 32 columns in a group, and ZP: there are zero points, at compile time, so
+// that a tile's products are one run of instructions in which the strips overlap.
 template <typename T, int PIECES, bool ZP, int M, int NT, bool ROWS8>
-struct Tile<T, 4, PIECES, ZP, M, NT, ROWS8> {
+struct Tile {
   static constexpr int kGroups = 4 / PIECES;
   Operand<4, NT, ROWS8> x;
   Meta<PIECES, M, ZP> meta;
-  __device__ __forceinline__ void multiply(uint32_t place, uint32_t tokens, unsigned some, float (&acc)[M][NT][4]) const {
+  __device__ __forceinline__ void multiply(uint32_t place, uint32_t tokens, float (&acc)[M][NT][4]) const {
     const int lane = threadIdx.x & 31, r = lane & 15, c0 = lane >> 4;
     const T *tag = nullptr;
     const uint32_t at = place + r * 64 + ((c0 ^ (r >> 1 & 3)) << 4);
@@ -242,12 +206,11 @@ struct Tile<T, 4, PIECES, ZP, M, NT, ROWS8> {
           widen_codes<T>(w[s][2 * (c & 1)], z0[s], lo);
           widen_codes<T>(w[s][2 * (c & 1) + 1], z1[s], hi);
 #pragma unroll
-          for (int i = 0; i < NT; ++i)
-            if (NT <= 2 || some >> i & 1) {
-              if (j == 0) mma16816<T, true>(part[s][i], lo[0], hi[0], lo[1], hi[1], b[i].x, b[i].y);
-              else mma16816<T, false>(part[s][i], lo[0], hi[0], lo[1], hi[1], b[i].x, b[i].y);
-              mma16816<T, false>(part[s][i], lo[2], hi[2], lo[3], hi[3], b[i].z, b[i].w);
-            }
+          for (int i = 0; i < NT; ++i) {
+            if (j == 0) mma16816<T, true>(part[s][i], lo[0], hi[0], lo[1], hi[1], b[i].x, b[i].y);
+            else mma16816<T, false>(part[s][i], lo[0], hi[0], lo[1], hi[1], b[i].x, b[i].y);
+            mma16816<T, false>(part[s][i], lo[2], hi[2], lo[3], hi[3], b[i].z, b[i].w);
+          }
         }
       }
       // the groups' sums times their scales
@@ -255,13 +218,12 @@ struct Tile<T, 4, PIECES, ZP, M, NT, ROWS8> {
       for (int s = 0; s < M; ++s) {
         const float s0 = value16(m0[s], tag), s1 = value16(m1[s], tag);
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
-          if (NT <= 2 || some >> i & 1) {
-            acc[s][i][0] = fmaf(part[s][i][0], s0, acc[s][i][0]);
-            acc[s][i][1] = fmaf(part[s][i][1], s0, acc[s][i][1]);
-            acc[s][i][2] = fmaf(part[s][i][2], s1, acc[s][i][2]);
-            acc[s][i][3] = fmaf(part[s][i][3], s1, acc[s][i][3]);
-          }
+        for (int i = 0; i < NT; ++i) {
+          acc[s][i][0] = fmaf(part[s][i][0], s0, acc[s][i][0]);
+          acc[s][i][1] = fmaf(part[s][i][1], s0, acc[s][i][1]);
+          acc[s][i][2] = fmaf(part[s][i][2], s1, acc[s][i][2]);
+          acc[s][i][3] = fmaf(part[s][i][3], s1, acc[s][i][3]);
+        }
       }
     }
   }

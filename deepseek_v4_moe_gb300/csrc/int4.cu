@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, 2)
     for (int s = 0; s < plan.stages && unit < plan.units; ++s, onwards(unit, step, 1)) fill(s, unit, step);
   }
   if (p.waits.inject && blockIdx.x == 0) wait_bounded(&never, 0, &abort_flag, p.waits.status, p.waits.ns);  // test hook
-  Tile<T, 4, PIECES, ZP, M, NT, (NT > 1)> t;
+  Tile<T, PIECES, ZP, M, NT, (NT > 1)> t;
   t.x.set(share * 4 * plan.box_rows, plan.box_rows);
   const uint32_t w_at = smem_u32(ring) + (share * sets + set) * M * kBoxBytes, x_at = smem_u32(ring) + kWeights;
   int stage = 0, phase = 0;
@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, 2)
       t.meta.advance(step * kw + share);
       // (the lanes agree: one that gave up takes the warp with it)
       if (!__all_sync(0xffffffffu, wait_bounded(&full[stage], phase, &abort_flag, p.waits.status, p.waits.ns))) break;
-      t.multiply(w_at + stage * plan.stage_bytes, x_at + stage * plan.stage_bytes, ~0u, acc);
+      t.multiply(w_at + stage * plan.stage_bytes, x_at + stage * plan.stage_bytes, acc);
       __syncwarp();
       if (lane == 0) {
         unsigned before;
@@ -147,7 +147,7 @@ cudaError_t int4_launch(const Int4MatmulParams &p, const Int4Maps &maps, const I
 template <typename T, int PIECES, bool ZP>
 cudaError_t int4_tiles(const Int4MatmulParams &p, const Int4Maps &maps, const Int4Tiles &t, int num_sms, cudaStream_t st) {
   Int4Plan plan;
-  const int tiles = (p.w.k + kTileK<4> - 1) / kTileK<4>, set_rows = 16 * t.strips, sets = kFewWarps >> t.log_kw;
+  const int tiles = (p.w.k + kTileK - 1) / kTileK, set_rows = 16 * t.strips, sets = kFewWarps >> t.log_kw;
   plan.log_kw = t.log_kw;
   plan.box_rows = t.box_rows;
   plan.steps = (tiles + (1 << t.log_kw) - 1) >> t.log_kw;
@@ -317,7 +317,7 @@ Int4Tiles int4_pick_tiles(int rows, int n, int k, int num_sms) {
   Int4Tiles t;
   t.eights = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
   t.strips = t.eights == 1 && n >= 64 * num_sms ? 4 : t.eights >= 2 && n >= 32 * num_sms ? 2 : 1;
-  const int tiles = (k + kTileK<4> - 1) / kTileK<4>, strips = (n + 16 * t.strips - 1) / (16 * t.strips);
+  const int tiles = (k + kTileK - 1) / kTileK, strips = (n + 16 * t.strips - 1) / (16 * t.strips);
   t.log_kw = 0;
   const int most = t.eights == 1 ? 3 : t.eights == 2 ? 2 : 1;  // each share has its own columns of x in a step
   while (t.log_kw < most && (2 << t.log_kw) <= tiles && (strips << t.log_kw) < 2 * kFewWarps * num_sms) ++t.log_kw;
