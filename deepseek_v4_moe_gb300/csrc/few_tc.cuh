@@ -199,7 +199,7 @@ __device__ __forceinline__ void tma_bulk_one(uint32_t dst, const void *src, uint
 
 template <typename C>
 struct CodeBars {
-  float join[C::kJoin > 1 ? C::kTokens * kCodeRows : 1];
+  float join[2][C::kJoin > 1 ? C::kTokens * kCodeRows : 1];
   uint64_t full[12], empty[12], afull[kCodeSlotsMax], aempty[kCodeSlotsMax], dfull[kCodeSlotsMax], dempty[kCodeSlotsMax], mma_done[2], never;
   uint32_t tmem;
   int abort_flag, issued;
@@ -211,8 +211,7 @@ struct CodeBars {
 //   void weights(place, at, bar)                             its codes' copy, by the converged warp
 //   void ready();  void tokens(place, at, sums, bar)         what the tokens' copies wait for; they, and their groups' sums
 //   Row; void row_at(row, place, r); void scales(row, place, scale, zero)   row r's scales and zero points
-//   kFactors; void factors(sums, group, token, f)            what four tokens' sums of the group are multiplied by
-//   void finish(place, r, acc, ok)
+//   void finish(place, r, turn, acc)                         by 128 threads; turn: 0 and 1, unit after unit
 template <typename C, int TOKENS, int PLANES, int GROUPS, typename Job>
 __device__ __forceinline__ void code_pipeline(Job &job, char *ring, CodeBars<C> &b, const Waits &w) {
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -308,12 +307,12 @@ __device__ __forceinline__ void code_pipeline(Job &job, char *ring, CodeBars<C> 
     }
   } else if (warp >= C::kFirstJoin) {
     // ---------------- groups' sums ----------------
-    // Sets take every other tile; at a unit's end the first one adds the others' sums to its own.
+    // Sets take every other tile; at the units' ends they take turns in adding the other's sums to their own and finishing.
     const int q = warp & 3, set = (warp - C::kFirstJoin) >> 2;
     RingPos<S> pos;
     RingPos<C::kA> a;
     RingPos<C::kD> d;
-    int i = 0;
+    int i = 0, turn = 0;
     float acc[TOKENS];
 #pragma unroll
     for (int t = 0; t < TOKENS; ++t) acc[t] = 0.f;
@@ -357,8 +356,6 @@ __device__ __forceinline__ void code_pipeline(Job &job, char *ring, CodeBars<C> 
               for (int t4 = 0; t4 < kChunk; t4 += 4) {
                 const uint4 x4 = lds128(sums + ((g0 + g) * TOKENS + t0 + t4) * 4);
                 const float x[4] = {__uint_as_float(x4.x), __uint_as_float(x4.y), __uint_as_float(x4.z), __uint_as_float(x4.w)};
-                float f[4];
-                if constexpr (Job::kFactors) job.factors(sums, g0 + g, t0 + t4, f);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                   const int t = t4 + i;
@@ -366,8 +363,7 @@ __device__ __forceinline__ void code_pipeline(Job &job, char *ring, CodeBars<C> 
 #pragma unroll
                   for (int k = PLANES - 2; k >= 0; --k) s = fmaf(s, kPlane, v[g][k * kChunk + t]);
                   s = fmaf(-zero[g0 + g], x[i], s);
-                  if constexpr (Job::kFactors) acc[t0 + t] = fmaf(s, scale[g0 + g] * f[i], acc[t0 + t]);
-                  else acc[t0 + t] = fmaf(s, scale[g0 + g], acc[t0 + t]);
+                  acc[t0 + t] = fmaf(s, scale[g0 + g], acc[t0 + t]);
                 }
               }
           }
@@ -377,16 +373,17 @@ __device__ __forceinline__ void code_pipeline(Job &job, char *ring, CodeBars<C> 
       }
       if (job.ends(p)) {
         if constexpr (C::kJoin > 1) {
-          if (set == 1)
+          float *other = b.join[turn] + q * 32 + lane;
+          if (set != turn)
 #pragma unroll
-            for (int t = 0; t < TOKENS; ++t) b.join[t * kCodeRows + q * 32 + lane] = acc[t];
+            for (int t = 0; t < TOKENS; ++t) other[t * kCodeRows] = acc[t];
           asm volatile("bar.sync 2, %0;" ::"n"(128 * C::kJoin) : "memory");
-          if (set == 0)
+          if (set == turn)
 #pragma unroll
-            for (int t = 0; t < TOKENS; ++t) acc[t] += b.join[t * kCodeRows + q * 32 + lane];
-          asm volatile("bar.sync 2, %0;" ::"n"(128 * C::kJoin) : "memory");
+            for (int t = 0; t < TOKENS; ++t) acc[t] += other[t * kCodeRows];
         }
-        if (set == 0) job.finish(p, q * 32 + lane, acc, ok);
+        if (C::kJoin == 1 || set == turn) job.finish(p, q * 32 + lane, turn, acc);
+        turn ^= 1;
 #pragma unroll
         for (int t = 0; t < TOKENS; ++t) acc[t] = 0.f;
         auto after = p;

@@ -27,7 +27,6 @@ __global__ void __launch_bounds__(256) int4_planes_kernel(const __grid_constant_
 template <typename T, int TOKENS, int PLANES, int GROUPS, bool ZP>
 struct MatmulJob {
   using C = CodeCfg<TOKENS, PLANES, GROUPS>;
-  static constexpr bool kFactors = false;
   const Int4MatmulParams &p;
   const Int4Maps &maps;
   float *sums;                    // the cluster's sums meet in it, [TOKENS][128]
@@ -71,7 +70,7 @@ struct MatmulJob {
       zero[g] = ZP ? (float)(r.zeros[at] & 15u) : 8.f;
     }
   }
-  __device__ __forceinline__ void finish(const Place &a, int row, const float (&acc)[TOKENS], bool) const {
+  __device__ __forceinline__ void finish(const Place &a, int row, int, const float (&acc)[TOKENS]) const {
     const int n = a.unit * kCodeRows + row, rows = min(TOKENS, p.rows - block * TOKENS);
 #pragma unroll
     for (int t = 0; t < TOKENS; ++t) {

@@ -19,7 +19,7 @@ template <typename T, typename TR>
 __global__ void __launch_bounds__(256) routed_logits_kernel(const __grid_constant__ RoutedParams p) {
   pdl_wait();
   pdl_trigger();
-  route_logits<T, TR>(p, blockIdx.x * kRouteExperts);
+  route_logits<T, TR>(p, blockIdx.x * kRouteExperts, blockIdx.y * kRouteTokens);
 }
 
 // The weights are the left operand as they lie (128 rows x 64 columns a step, K-major, by TMA), all tokens' columns the
@@ -210,18 +210,16 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         asm volatile("bar.sync 1, 128;" ::: "memory");
         const int group = unit / tiles, at = (unit - group * tiles) * 64 + row, e = c.group_expert[group];
         const uint32_t mask = c.group_mask[group];
-        if (q < 2 && at < p.inter) {
+        const float weight = weight_of(p, c, e, lane);  // this lane's token's
+        if (q < 2) {
           uint16_t *h = p.h + (long long)group * rows8 * p.inter + at;
 #pragma unroll
           for (int t = 0; t < NC; ++t) {
             if (t >= p.rows) break;
             T out = from_f32<T>(0.f);
-            if (mask >> t & 1) {
-              const float weight = weight_of(p, c, e, t);
-              // rounded to 16 bits as the tensor cores' operand, as the gated block does
-              out = from_f32<T>(act_value(p.act, v[t]) * u[t * 64 + row] * weight);
-            }
-            h[(long long)t * p.inter] = *reinterpret_cast<const uint16_t *>(&out);
+            if (mask >> t & 1)  // rounded to 16 bits as the tensor cores' operand, as the gated block does
+              out = from_f32<T>(act_value(p.act, v[t]) * u[t * 64 + row] * __shfl_sync(0xffffffffu, weight, t));
+            if (at < p.inter) h[(long long)t * p.inter] = *reinterpret_cast<const uint16_t *>(&out);
           }
         }
       } else {
@@ -273,7 +271,7 @@ cudaError_t tc_launch(const RoutedParams &p, const RoutedMaps &maps, const Route
   cudaError_t e = allow_smem((const void *)routed_tc_kernel<true, T, NC>, kTcSmem<NC>, done[0]);
   if (e == cudaSuccess)
     e = launch_pdl(p.router_f32 ? routed_logits_kernel<T, float> : routed_logits_kernel<T, T>,
-                   dim3(route_ctas(p)), dim3(256), 0, st, p);
+                   dim3(route_ctas(p), route_turns(p)), dim3(256), 0, st, p);
   const long long groups = (p.rows * p.top_k < p.experts ? p.rows * p.top_k : p.experts) + p.shared;
   const long long units = groups * ((p.inter + 63) / 64);
   if (e == cudaSuccess)

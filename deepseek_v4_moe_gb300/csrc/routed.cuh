@@ -11,49 +11,49 @@ namespace moe {
 
 // ---- router ----
 
-constexpr int kRouteExperts = 2, kRouteTokens = 8;  // of a CTA, and of a turn
+// of a CTA
+constexpr int kRouteExperts = 2, kRouteTokens = 4;
 __host__ __device__ inline int route_ctas(const RoutedParams &p) { return (p.experts + kRouteExperts - 1) / kRouteExperts; }
+inline int route_turns(const RoutedParams &p) { return (p.rows + kRouteTokens - 1) / kRouteTokens; }
 
-// by a CTA of 256
+// by a CTA of 256: experts from e0 on, tokens from t0 on
 template <typename T, typename TR>
-__device__ __forceinline__ void route_logits(const RoutedParams &p, int e0) {
+__device__ __forceinline__ void route_logits(const RoutedParams &p, int e0, int t0) {
   __shared__ float sums[8][kRouteExperts * kRouteTokens];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int t0 = 0; t0 < p.rows; t0 += kRouteTokens) {
-    float acc[kRouteExperts][kRouteTokens] = {};
-    for (int k = warp * 256 + lane * 8; k < p.hidden; k += 8 * 256) {
-      float w[kRouteExperts][8];
-#pragma unroll
-      for (int e = 0; e < kRouteExperts; ++e)
-        load_eight<TR, true>(static_cast<const TR *>(p.router) + (long long)min(e0 + e, p.experts - 1) * p.hidden + k, 0, 1, 8, w[e]);
-#pragma unroll
-      for (int t = 0; t < kRouteTokens; ++t)
-        if (t0 + t < p.rows) {
-          float x[8];
-          load_eight<T, true>(static_cast<const T *>(p.x) + (t0 + t) * p.ld_x + k, 0, 1, 8, x);
-#pragma unroll
-          for (int e = 0; e < kRouteExperts; ++e)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) acc[e][t] = fmaf(w[e][i], x[i], acc[e][t]);
-        }
-    }
+  float acc[kRouteExperts][kRouteTokens] = {};
+#pragma unroll 2
+  for (int k = warp * 256 + lane * 8; k < p.hidden; k += 8 * 256) {
+    float w[kRouteExperts][8];
 #pragma unroll
     for (int e = 0; e < kRouteExperts; ++e)
+      load_eight<TR, true>(static_cast<const TR *>(p.router) + (long long)min(e0 + e, p.experts - 1) * p.hidden + k, 0, 1, 8, w[e]);
 #pragma unroll
-      for (int t = 0; t < kRouteTokens; ++t) {
-        if (t0 + t >= p.rows) continue;
-        const float s = warp_sum(acc[e][t]);
-        if (lane == 0) sums[warp][e * kRouteTokens + t] = s;
+    for (int t = 0; t < kRouteTokens; ++t)
+      if (t0 + t < p.rows) {
+        float x[8];
+        load_eight<T, true>(static_cast<const T *>(p.x) + (t0 + t) * p.ld_x + k, 0, 1, 8, x);
+#pragma unroll
+        for (int e = 0; e < kRouteExperts; ++e)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc[e][t] = fmaf(w[e][i], x[i], acc[e][t]);
       }
-    __syncthreads();
-    const int e = threadIdx.x / kRouteTokens, t = threadIdx.x % kRouteTokens;
-    if (e < kRouteExperts && e0 + e < p.experts && t0 + t < p.rows) {
-      float s = sums[0][threadIdx.x];
+  }
 #pragma unroll
-      for (int w = 1; w < 8; ++w) s += sums[w][threadIdx.x];
-      p.logits[(t0 + t) * p.experts + e0 + e] = s;
+  for (int e = 0; e < kRouteExperts; ++e)
+#pragma unroll
+    for (int t = 0; t < kRouteTokens; ++t) {
+      if (t0 + t >= p.rows) continue;
+      const float s = warp_sum(acc[e][t]);
+      if (lane == 0) sums[warp][e * kRouteTokens + t] = s;
     }
-    __syncthreads();
+  __syncthreads();
+  const int e = threadIdx.x / kRouteTokens, t = threadIdx.x % kRouteTokens;
+  if (e < kRouteExperts && e0 + e < p.experts && t0 + t < p.rows) {
+    float s = sums[0][threadIdx.x];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) s += sums[w][threadIdx.x];
+    p.logits[(t0 + t) * p.experts + e0 + e] = s;
   }
 }
 
@@ -68,7 +68,7 @@ struct Choice {
   uint16_t group_expert[kGroupsMax];
   uint32_t group_mask[kGroupsMax];
   uint32_t mask[kRoutedExperts];                   // each expert's tokens
-  uint16_t index[kRoutedRows][kRoutedTopK];
+  __align__(16) uint16_t index[kRoutedRows][kRoutedTopK];
   float weight[kRoutedRows][kRoutedTopK];
 };
 
@@ -185,12 +185,15 @@ __device__ __forceinline__ void choose_groups(const RoutedParams &p, Choice &c, 
   __syncthreads();
 }
 
-// expert e's weight for a token that has chosen it
+// expert e's weight for a token, if it has chosen it (otherwise anything)
 __device__ __forceinline__ float weight_of(const RoutedParams &p, const Choice &c, int e, int token) {
   if (e >= p.experts) return 1.f;
+  const uint4 v = *reinterpret_cast<const uint4 *>(c.index[token]);
+  const uint32_t x[4] = {v.x, v.y, v.z, v.w};
   int slot = 0;
-  for (int s = 1; s < p.top_k; ++s)
-    if (c.index[token][s] == e) slot = s;
+#pragma unroll
+  for (int s = 0; s < kRoutedTopK; ++s)
+    if (s < p.top_k && (x[s / 2] >> (16 * (s % 2)) & 0xFFFFu) == (uint32_t)e) slot = s;
   return c.weight[token][slot];
 }
 

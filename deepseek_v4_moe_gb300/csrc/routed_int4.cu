@@ -19,16 +19,17 @@
 namespace moe {
 namespace {
 
-// CTAs from route_ctas on: a row of x each
+// CTAs from route_ctas on: a row of x each, those of the tokens that the others have
 template <typename T, typename TR, int PLANES>
 __global__ void __launch_bounds__(256) routed_planes_kernel(const __grid_constant__ RoutedParams p, int tokens) {
-  const int n = route_ctas(p), row = blockIdx.x - n, k8 = p.hidden / 8;
+  const int n = route_ctas(p), row = blockIdx.y * kRouteTokens + blockIdx.x - n, k8 = p.hidden / 8;
   pdl_wait();
   pdl_trigger();
-  if (row < 0) {
-    route_logits<T, TR>(p, blockIdx.x * kRouteExperts);
+  if (blockIdx.x < n) {
+    route_logits<T, TR>(p, blockIdx.x * kRouteExperts, blockIdx.y * kRouteTokens);
     return;
   }
+  if (row >= p.rows) return;
   const T *x = static_cast<const T *>(p.x) + row * p.ld_x;
   const uint32_t most = row_max(x, k8);
   if (threadIdx.x == 0) {
@@ -59,14 +60,13 @@ __global__ void __launch_bounds__(256) routed_split_kernel(const __grid_constant
 template <bool UP, typename T, int TOKENS, int PLANES, int GROUPS>
 struct LayerJob {
   using C = CodeCfg<TOKENS, PLANES, GROUPS>;
-  static constexpr bool kFactors = false;
   const RoutedParams &p;
   const RoutedMaps &maps;
   const Choice &c;
   float *sums;                    // up: [2][TOKENS][64]; down: [TOKENS][128]
   int tiles, strips;              // of a group; up: units of a group
   int row_tile, first, end;       // down
-  mutable int turn;
+  float back;                     // up: what this lane's token's products are multiplied by
   struct Place {
     int unit, group, tile, left, tiles, strips, step;
     __device__ __forceinline__ bool more() const { return left > 0; }
@@ -137,28 +137,28 @@ struct LayerJob {
       zero[g] = m.zeros ? (float)(m.zeros[at + i] & 15u) : 8.f;
     }
   }
-  __device__ __forceinline__ void finish(const Place &a, int row, const float (&acc)[TOKENS], bool) const {
+  __device__ __forceinline__ void finish(const Place &a, int row, int turn, const float (&acc)[TOKENS]) const {
     if constexpr (UP) {
       float *u = sums + turn * (TOKENS * 64);
-      turn ^= 1;
       if (row >= 64)
 #pragma unroll
         for (int t = 0; t < TOKENS; ++t)
           if (t < p.rows) u[t * 64 + row - 64] = acc[t];
-      asm volatile("bar.sync 3, 128;" ::: "memory");
+      asm volatile("bar.sync %0, 128;" ::"r"(3 + turn) : "memory");
       if (row >= 64) return;
       const int at = (a.unit - a.group * strips) * 64 + row, e = c.group_expert[a.group];
       const uint32_t mask = c.group_mask[a.group];
       uint16_t *h = p.h + (size_t)a.group * p.rows * p.inter + at;
+      const float weight = weight_of(p, c, e, threadIdx.x & 31);  // this lane's token's
 #pragma unroll
       for (int t = 0; t < TOKENS; ++t) {
         if (t >= p.rows) break;
         if (!(mask >> t & 1)) continue;
+        const float by = __shfl_sync(0xffffffffu, back, t), w = __shfl_sync(0xffffffffu, weight, t);
         uint32_t size = 0u;
         if (at < p.inter) {
-          const float back = 512.f * p.back[t];
           // rounded to 16 bits as the 16-bit layer does
-          const T out = from_f32<T>(act_value(p.act, acc[t] * back) * (u[t * 64 + row] * back) * weight_of(p, c, e, t));
+          const T out = from_f32<T>(act_value(p.act, acc[t] * by) * (u[t * 64 + row] * by) * w);
           h[(size_t)t * p.inter] = *reinterpret_cast<const uint16_t *>(&out);
           size = __float_as_uint(to_f32(out)) & 0x7FFFFFFFu;
         }
@@ -194,7 +194,8 @@ __global__ void __launch_bounds__(CodeCfg<TOKENS, PLANES, GROUPS>::kThreads, 1)
   if (UP && blockIdx.x == 0)
     for (int g = threadIdx.x; g < p.groups; g += C::kThreads) p.masks[g] = g < c.groups ? c.group_mask[g] : 0u;
   const LayerJob<UP, T, TOKENS, PLANES, GROUPS> job{p, maps, c, sums, tiles, strips, row_tile, (int)(all * rank / splits),
-                                                    (int)(all * (rank + 1) / splits), 0};
+                                                    (int)(all * (rank + 1) / splits),
+                                                    UP && threadIdx.x % 32 < p.rows ? 512.f * __ldcg(p.back + threadIdx.x % 32) : 0.f};
   if (!UP && job.first == job.end)
     for (int i = threadIdx.x; i < TOKENS * kCodeRows; i += C::kThreads) sums[i] = 0.f;
   code_pipeline<C, TOKENS, PLANES, GROUPS>(job, ring, bars, p.waits);
@@ -226,7 +227,7 @@ cudaError_t codes_launch(const RoutedParams &p, const RoutedMaps &maps, const Ro
   static std::atomic<unsigned long long> done[2];
   cudaError_t e = allow_smem((const void *)routed_codes_kernel<true, T, TOKENS, PLANES, GROUPS>, smem, done[0]);
   if (e == cudaSuccess)
-    e = launch_pdl(p.router_f32 ? routed_planes_kernel<T, float, PLANES> : routed_planes_kernel<T, T, PLANES>, dim3(route_ctas(p) + p.rows),
+    e = launch_pdl(p.router_f32 ? routed_planes_kernel<T, float, PLANES> : routed_planes_kernel<T, T, PLANES>, dim3(route_ctas(p) + kRouteTokens, route_turns(p)),
                    dim3(256), 0, st, p, TOKENS);
   const long long units = (long long)p.groups * ((p.inter + 63) / 64);
   if (e == cudaSuccess)
