@@ -210,7 +210,8 @@ struct CodeBars {
 //   bool ends(place)                                         a unit's last tile
 //   void weights(place, at, bar)                             its codes' copy, by the converged warp
 //   void ready();  void tokens(place, at, sums, bar)         what the tokens' copies wait for; they, and their groups' sums
-//   Row; void row_at(row, place, r); void scales(row, place, scale, zero)   row r's scales and zero points
+//   Row; void row_at(row, place, r); void scales(row, place, scale, zero)   row r's scales and zero points; row_at: at the
+//                                                            beginning of a unit, and fetches the next one's into the L2
 //   void finish(place, r, turn, acc)                         by 128 threads; turn: 0 and 1, unit after unit
 template <typename C, int TOKENS, int PLANES, int GROUPS, typename Job>
 __device__ __forceinline__ void code_pipeline(Job &job, char *ring, CodeBars<C> &b, const Waits &w) {
@@ -402,6 +403,11 @@ __device__ __forceinline__ void code_pipeline(Job &job, char *ring, CodeBars<C> 
       if (n > 0) (void)wait_bounded(&b.full[s], (uint32_t)((n - 1) & 1), &no_abort, w.status, w.ns);
     }
   }
+}
+
+// bytes of memory into the L2
+__device__ __forceinline__ void fetch_lines(const void *at, int bytes) {
+  for (int i = 0; i < bytes; i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char *>(at) + i));
 }
 
 // before the pipeline, by every thread

@@ -61,6 +61,11 @@ struct MatmulJob {
     const long long at = (long long)min(a.unit * kCodeRows + row, p.w.n - 1) * p.w.groups;
     r.scales = p.w.scales + at;
     r.zeros = p.w.zeros + at;
+    if (a.unit + unit_step < units) {
+      const long long to = (long long)min((a.unit + unit_step) * kCodeRows + row, p.w.n - 1) * p.w.groups;
+      fetch_lines(p.w.scales + to, 2 * p.w.groups);
+      if (ZP) fetch_lines(p.w.zeros + to, p.w.groups);
+    }
   }
   __device__ __forceinline__ void scales(const Row &r, const Place &a, float (&scale)[C::kAll], float (&zero)[C::kAll]) const {
 #pragma unroll

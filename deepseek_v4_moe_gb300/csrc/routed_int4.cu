@@ -118,23 +118,52 @@ struct LayerJob {
     tma_bulk_one(to, from + a.tile * (C::kAll * TOKENS), C::kSums, bar);
   }
   struct Row {
-    int row;
+    const uint16_t *scales;
+    const uint8_t *zeros;
+    int row, group, groups;
   };
-  __device__ __forceinline__ void row_at(Row &r, const Place &a, int row) const {
-    if constexpr (UP) r.row = min((a.unit - a.group * strips) * 64 + row % 64, p.inter - 1) | (row >= 64 ? 1 << 30 : 0);
-    else r.row = min(row_tile * kCodeRows + row, p.hidden - 1);
-  }
-  __device__ __forceinline__ void scales(const Row &r, const Place &a, float (&scale)[C::kAll], float (&zero)[C::kAll]) const {
-    bool shared;
-    const int e = matrix_of(a, shared);
-    const bool up = UP && r.row >> 30;
+  // row r of a group's matrices; up: 64 rows of gate, then 64 of up
+  __device__ __forceinline__ void find(Row &r, int group, int strip) const {
+    const int e0 = c.group_expert[group];
+    const bool shared = e0 >= p.experts, up = UP && r.row >= 64;
     const FewMatrix &m = UP ? (shared ? (up ? p.s_up : p.s_gate) : up ? p.up : p.gate) : shared ? p.s_down : p.down;
-    const long long at = ((long long)e * (UP ? p.inter : p.hidden) + (r.row & 0x3FFFFFFF)) * m.groups;
+    const int row = UP ? min(strip * 64 + r.row % 64, p.inter - 1) : min(row_tile * kCodeRows + r.row, p.hidden - 1);
+    const long long at = ((long long)(shared ? e0 - p.experts : e0) * (UP ? p.inter : p.hidden) + row) * m.groups;
+    r.group = group;
+    r.groups = m.groups;
+    r.scales = m.scales + at;
+    r.zeros = m.zeros ? m.zeros + at : nullptr;
+  }
+  __device__ __forceinline__ void fetch(const Row &r) const {
+    fetch_lines(r.scales, 2 * r.groups);
+    if (r.zeros) fetch_lines(r.zeros, r.groups);
+  }
+  __device__ __forceinline__ void row_at(Row &r, const Place &a, int row) const {
+    r.row = row;
+    if constexpr (UP) {
+      const int next = a.unit + a.step, group = next / strips;
+      if (group < c.groups) {
+        find(r, group, next - group * strips);
+        fetch(r);
+      }
+      find(r, a.group, a.unit - a.group * strips);
+    } else {
+      r.group = -1;
+    }
+  }
+  __device__ __forceinline__ void scales(Row &r, const Place &a, float (&scale)[C::kAll], float (&zero)[C::kAll]) const {
+    if (!UP && r.group != a.group) {
+      if (a.group + 1 < c.groups) {
+        find(r, a.group + 1, 0);
+        fetch(r);
+      }
+      find(r, a.group, 0);
+    }
 #pragma unroll
     for (int g = 0; g < C::kAll; ++g) {
-      const int i = min(a.tile * C::kAll + g, m.groups - 1);
-      scale[g] = to_f32(reinterpret_cast<const T *>(m.scales)[at + i]);
-      zero[g] = m.zeros ? (float)(m.zeros[at + i] & 15u) : 8.f;
+      const int i = min(a.tile * C::kAll + g, r.groups - 1);
+      scale[g] = to_f32(reinterpret_cast<const T *>(r.scales)[i]);
+      zero[g] = r.zeros ? (float)(r.zeros[i] & 15u) : 8.f;
     }
   }
   __device__ __forceinline__ void finish(const Place &a, int row, int turn, const float (&acc)[TOKENS]) const {
