@@ -161,11 +161,13 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
 // a ring position: slot and the parity of its round
 template <int SLOTS>
 struct RingPos {
-  int slot = 0;
+  int slot;
   uint32_t round = 0;
-  __device__ __forceinline__ void next() {
-    if (++slot == SLOTS) {
-      slot = 0;
+  __device__ __forceinline__ RingPos(int first = 0) : slot(first) {}
+  __device__ __forceinline__ void next(int by = 1) {  // (SLOTS is a multiple of `by`)
+    slot += by;
+    if (slot >= SLOTS) {
+      slot -= SLOTS;
       round ^= 1u;
     }
   }

@@ -188,6 +188,18 @@ __device__ __forceinline__ void tmem_arrived(float (&v)[N]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
 }
+// two f32 multiply-adds in one instruction
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+  return v;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
 // a piece of memory into this CTA's shared memory, by one lane of a converged warp (bytes a multiple of 16)
 __device__ __forceinline__ void tma_bulk_one(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
   asm volatile(
@@ -206,12 +218,13 @@ struct CodeBars {
 };
 
 // The kernel's body.  A job gives this CTA's tiles, the same to every role:
-//   Place begin();  place.more(), place.next()               a tile, one after another through the CTA's units
+//   int count();  Place begin();  place.more(), place.tile;  next(place)    its tiles, one after another through its units
 //   bool ends(place)                                         a unit's last tile
 //   void weights(place, at, bar)                             its codes' copy, by the converged warp
 //   void ready();  void tokens(place, at, sums, bar)         what the tokens' copies wait for; they, and their groups' sums
-//   Row; void row_at(row, place, r); void scales(row, place, scale, zero)   row r's scales and zero points; row_at: at the
-//                                                            beginning of a unit, and fetches the next one's into the L2
+//   Row; void row_at(row, place, r)                          row r's scales, at the beginning of a unit; the next one's
+//                                                            are fetched into the L2
+//   Scales; void scales(row, place, ahead, s); last(place)   those of the tile `ahead` tiles on; the end of such tiles
 //   void finish(place, r, turn, acc)                         by 128 threads; turn: 0 and 1, unit after unit
 template <typename C, int TOKENS, int PLANES, int GROUPS, typename Job>
 __device__ __forceinline__ void code_pipeline(Job &job, char *ring, CodeBars<C> &b, const Waits &w) {
@@ -232,10 +245,10 @@ __device__ __forceinline__ void code_pipeline(Job &job, char *ring, CodeBars<C> 
       job.tokens(p, at, at + C::kHalves * C::kB, smem_u32(&b.full[s]));
     };
     auto p = job.begin(), early = p;
-    for (; j < S && p.more(); ++j, p.next()) weights(p, j);  // these need not wait for the tokens
+    for (; j < S && p.more(); ++j, job.next(p)) weights(p, j);  // these need not wait for the tokens
     job.ready();
-    for (int i = 0; i < j; ++i, early.next(), pos.next()) tokens(early, i);
-    for (; p.more(); ++j, pos.next(), p.next()) {
+    for (int i = 0; i < j; ++i, job.next(early), pos.next()) tokens(early, i);
+    for (; p.more(); ++j, pos.next(), job.next(p)) {
       if (!warp_wait(&b.empty[pos.slot], pos.round ^ 1u, abort_p, w.status, w.ns)) break;
       weights(p, pos.slot);
       tokens(p, pos.slot);
@@ -246,12 +259,10 @@ __device__ __forceinline__ void code_pipeline(Job &job, char *ring, CodeBars<C> 
     if (w.inject && blockIdx.x == 0) (void)warp_wait(&b.never, 0u, abort_p, w.status, w.ns);  // test hook: a wait that runs out
     const uint32_t idesc = idesc_e4m3(kCodeRows, C::kN);
     const uint64_t b0 = smem_desc_sw128(ring0 + C::kW);
-    RingPos<S> pos;
-    RingPos<C::kA> a;
-    RingPos<C::kD> d;
-    int i = 0;
-    for (auto p = job.begin(); p.more(); p.next(), pos.next(), a.next(), d.next(), ++i) {
-      if (i % C::kIssue != warp - 1) continue;
+    RingPos<S> pos(warp - 1);
+    RingPos<C::kA> a(warp - 1);
+    RingPos<C::kD> d(warp - 1);
+    for (int i = warp - 1, tiles = job.count(); i < tiles; i += C::kIssue, pos.next(C::kIssue), a.next(C::kIssue), d.next(C::kIssue)) {
       if (!warp_wait(&b.dempty[d.slot], d.round ^ 1u, abort_p, w.status, w.ns) ||
           !warp_wait(&b.full[pos.slot], pos.round, abort_p, w.status, w.ns) ||
           !warp_wait(&b.afull[a.slot], a.round, abort_p, w.status, w.ns))
@@ -270,11 +281,9 @@ __device__ __forceinline__ void code_pipeline(Job &job, char *ring, CodeBars<C> 
   } else if (warp >= C::kFirstMake) {
     // ---------------- codes to operands ----------------
     const int set = (warp - C::kFirstMake) >> 2, q = warp & 3, row = q * 32 + lane;
-    RingPos<S> pos;
-    RingPos<C::kA> a;
-    int i = 0;
-    for (auto p = job.begin(); p.more(); p.next(), pos.next(), a.next(), ++i) {
-      if (i % C::kSets != set) continue;
+    RingPos<S> pos(set);
+    RingPos<C::kA> a(set);
+    for (int i = set, tiles = job.count(); i < tiles; i += C::kSets, pos.next(C::kSets), a.next(C::kSets)) {
       if (!warp_wait(&b.full[pos.slot], pos.round, abort_p, w.status, w.ns) ||
           !warp_wait(&b.aempty[a.slot], a.round ^ 1u, abort_p, w.status, w.ns))
         break;
@@ -309,86 +318,101 @@ __device__ __forceinline__ void code_pipeline(Job &job, char *ring, CodeBars<C> 
   } else if (warp >= C::kFirstJoin) {
     // ---------------- groups' sums ----------------
     // Sets take every other tile; at the units' ends they take turns in adding the other's sums to their own and finishing.
+    // What a set does for a tile bounded the pipeline once (2050 cycles, one step waiting for another): so a tile's scales
+    // are read during the one before, and two multiply-adds are one instruction.
     const int q = warp & 3, set = (warp - C::kFirstJoin) >> 2;
-    RingPos<S> pos;
-    RingPos<C::kA> a;
-    RingPos<C::kD> d;
+    RingPos<S> pos(set);
+    RingPos<C::kA> a(set);
+    RingPos<C::kD> d(set);
     int i = 0, turn = 0;
-    float acc[TOKENS];
+    uint64_t acc[TOKENS / 2];
 #pragma unroll
-    for (int t = 0; t < TOKENS; ++t) acc[t] = 0.f;
+    for (int t = 0; t < TOKENS / 2; ++t) acc[t] = 0u;
     auto p = job.begin();
     typename Job::Row row;
     if (p.more()) job.row_at(row, p, q * 32 + lane);
-    bool ok = true;
-    for (; p.more(); p.next(), pos.next(), a.next(), d.next(), ++i) {
+    bool ok = true, read = false;  // read: the scales are those of the next tile
+    typename Job::Scales now, next;
+    for (; p.more(); job.next(p), ++i) {
       if (i % C::kJoin == set) {
-      float scale[C::kAll], zero[C::kAll];
-      job.scales(row, p, scale, zero);
-      ok = ok && warp_wait(&b.full[pos.slot], pos.round, abort_p, w.status, w.ns);
-      const uint32_t sums = ring0 + pos.slot * C::kStage + C::kW + C::kHalves * C::kB;
-      ok = ok && warp_wait(&b.dfull[d.slot], d.round, abort_p, w.status, w.ns);
-      tc_fence_after();
-      if (ok) {
-        // Sixteen tokens' sums of a group at a time (of eight tokens all planes' lie in one or two sixteens), of several
-        // groups where registers allow it, so that their way is waited for once.
-        constexpr int kChunk = TOKENS < 16 ? TOKENS : 16, kCols = TOKENS < 16 ? C::kN : 16 * PLANES;
-        constexpr int kBatch = TOKENS > 16 ? 1 : C::kAll * kCols <= 64 ? C::kAll : 64 / kCols;
-        const uint32_t from = tmem_d + ((uint32_t)(q * 32) << 16) + d.slot * (C::kAll * C::kN);
+        if (!read) job.scales(row, p, 0, now);
+        read = p.tile + C::kJoin < job.last(p);  // (of the same rows)
+        if (read) job.scales(row, p, C::kJoin, next);
+        ok = ok && warp_wait(&b.full[pos.slot], pos.round, abort_p, w.status, w.ns);
+        const uint32_t sums = ring0 + pos.slot * C::kStage + C::kW + C::kHalves * C::kB;
+        ok = ok && warp_wait(&b.dfull[d.slot], d.round, abort_p, w.status, w.ns);
+        tc_fence_after();
+        if (ok) {
+          // Sixteen tokens' sums of a group at a time (of eight tokens all planes' lie in one or two sixteens), of several
+          // groups where registers allow it, so that their way is waited for once.
+          constexpr int kChunk = TOKENS < 16 ? TOKENS : 16, kCols = TOKENS < 16 ? C::kN : 16 * PLANES;
+          constexpr int kBatch = C::kAll * kCols <= 32 ? C::kAll : kCols <= 16 ? 2 : 1;
+          const uint32_t from = tmem_d + ((uint32_t)(q * 32) << 16) + d.slot * (C::kAll * C::kN);
+          const uint64_t plane = pair(kPlane, kPlane);
 #pragma unroll
-        for (int g0 = 0; g0 < C::kAll; g0 += kBatch)
+          for (int g0 = 0; g0 < C::kAll; g0 += kBatch)
 #pragma unroll
-          for (int t0 = 0; t0 < TOKENS; t0 += kChunk) {
-            float v[kBatch][kCols];
+            for (int t0 = 0; t0 < TOKENS; t0 += kChunk) {
+              float v[kBatch][kCols];
 #pragma unroll
-            for (int g = 0; g < kBatch; ++g) tmem_columns<kCols>(from + (g0 + g) * C::kN + t0, TOKENS, v[g]);
-            tmem_arrived(reinterpret_cast<float(&)[kBatch * kCols]>(v));
-            if (g0 + kBatch >= C::kAll && t0 + kChunk == TOKENS) {  // everything is in registers: the tile's slots are free
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) {
-                mbar_arrive(&b.dempty[d.slot]);
-                mbar_arrive(&b.aempty[a.slot]);
-              }
-            }
-#pragma unroll
-            for (int g = 0; g < kBatch; ++g)
-#pragma unroll
-              for (int t4 = 0; t4 < kChunk; t4 += 4) {
-                const uint4 x4 = lds128(sums + ((g0 + g) * TOKENS + t0 + t4) * 4);
-                const float x[4] = {__uint_as_float(x4.x), __uint_as_float(x4.y), __uint_as_float(x4.z), __uint_as_float(x4.w)};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const int t = t4 + i;
-                  float s = v[g][(PLANES - 1) * kChunk + t];
-#pragma unroll
-                  for (int k = PLANES - 2; k >= 0; --k) s = fmaf(s, kPlane, v[g][k * kChunk + t]);
-                  s = fmaf(-zero[g0 + g], x[i], s);
-                  acc[t0 + t] = fmaf(s, scale[g0 + g], acc[t0 + t]);
+              for (int g = 0; g < kBatch; ++g) tmem_columns<kCols>(from + (g0 + g) * C::kN + t0, TOKENS, v[g]);
+              tmem_arrived(reinterpret_cast<float(&)[kBatch * kCols]>(v));
+              if (g0 + kBatch >= C::kAll && t0 + kChunk == TOKENS) {  // everything is in registers: the tile's slots are free
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                  mbar_arrive(&b.dempty[d.slot]);
+                  mbar_arrive(&b.aempty[a.slot]);
                 }
               }
-          }
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&b.empty[pos.slot]);
+#pragma unroll
+              for (int g = 0; g < kBatch; ++g) {
+                const float zero = -now.zero(g0 + g), scale = now.scale(g0 + g);
+                const uint64_t z = pair(zero, zero), m = pair(scale, scale);
+#pragma unroll
+                for (int t4 = 0; t4 < kChunk; t4 += 4) {
+                  const uint4 x4 = lds128(sums + ((g0 + g) * TOKENS + t0 + t4) * 4);
+                  const uint64_t x[2] = {pair(__uint_as_float(x4.x), __uint_as_float(x4.y)), pair(__uint_as_float(x4.z), __uint_as_float(x4.w))};
+#pragma unroll
+                  for (int i = 0; i < 2; ++i) {
+                    const int t = t4 + 2 * i;
+                    const float *at = &v[g][(PLANES - 1) * kChunk + t];
+                    uint64_t s = pair(at[0], at[1]);
+#pragma unroll
+                    for (int k = PLANES - 2; k >= 0; --k) s = fma2(s, plane, pair(v[g][k * kChunk + t], v[g][k * kChunk + t + 1]));
+                    acc[(t0 + t) / 2] = fma2(fma2(z, x[i], s), m, acc[(t0 + t) / 2]);
+                  }
+                }
+              }
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b.empty[pos.slot]);
+        now = next;
+        pos.next(C::kJoin);
+        a.next(C::kJoin);
+        d.next(C::kJoin);
       }
       if (job.ends(p)) {
+        float sum[TOKENS];
+#pragma unroll
+        for (int t = 0; t < TOKENS; t += 2) unpair(acc[t / 2], sum[t], sum[t + 1]);
         if constexpr (C::kJoin > 1) {
           float *other = b.join[turn] + q * 32 + lane;
           if (set != turn)
 #pragma unroll
-            for (int t = 0; t < TOKENS; ++t) other[t * kCodeRows] = acc[t];
+            for (int t = 0; t < TOKENS; ++t) other[t * kCodeRows] = sum[t];
           asm volatile("bar.sync 2, %0;" ::"n"(128 * C::kJoin) : "memory");
           if (set == turn)
 #pragma unroll
-            for (int t = 0; t < TOKENS; ++t) acc[t] += other[t * kCodeRows];
+            for (int t = 0; t < TOKENS; ++t) sum[t] += other[t * kCodeRows];
         }
-        if (C::kJoin == 1 || set == turn) job.finish(p, q * 32 + lane, turn, acc);
+        if (C::kJoin == 1 || set == turn) job.finish(p, q * 32 + lane, turn, sum);
         turn ^= 1;
 #pragma unroll
-        for (int t = 0; t < TOKENS; ++t) acc[t] = 0.f;
+        for (int t = 0; t < TOKENS / 2; ++t) acc[t] = 0u;
         auto after = p;
-        after.next();
+        job.next(after);
         if (after.more()) job.row_at(row, after, q * 32 + lane);
       }
     }

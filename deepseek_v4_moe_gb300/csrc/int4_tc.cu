@@ -32,16 +32,19 @@ struct MatmulJob {
   float *sums;                    // the cluster's sums meet in it, [TOKENS][128]
   int splits, first, end, units, unit0, unit_step, block;
   struct Place {
-    int unit, tile, units, first, end, unit_step;
+    int unit, tile, units;
     __device__ __forceinline__ bool more() const { return unit < units; }
-    __device__ __forceinline__ void next() {
-      if (++tile == end) {
-        tile = first;
-        unit += unit_step;
-      }
-    }
   };
-  __device__ __forceinline__ Place begin() const { return Place{first < end ? unit0 : units, first, units, first, end, unit_step}; }
+  __device__ __forceinline__ void next(Place &a) const {
+    if (++a.tile == end) {
+      a.tile = first;
+      a.unit += unit_step;
+    }
+  }
+  __device__ __forceinline__ int count() const {
+    return unit0 < units ? (end - first) * ((units - unit0 + unit_step - 1) / unit_step) : 0;
+  }
+  __device__ __forceinline__ Place begin() const { return Place{first < end ? unit0 : units, first, units}; }
   __device__ __forceinline__ bool ends(const Place &a) const { return a.tile == end - 1; }
   __device__ __forceinline__ void weights(const Place &a, uint32_t at, uint32_t bar) const {
     tma_load_2d_one<false>(at, &maps.w, bar, a.tile * (64 * C::kHalves), a.unit * kCodeRows);
@@ -67,12 +70,19 @@ struct MatmulJob {
       if (ZP) fetch_lines(p.w.zeros + to, p.w.groups);
     }
   }
-  __device__ __forceinline__ void scales(const Row &r, const Place &a, float (&scale)[C::kAll], float (&zero)[C::kAll]) const {
+  struct Scales {
+    uint16_t scales[C::kAll];
+    uint8_t zeros[C::kAll];
+    __device__ __forceinline__ float scale(int g) const { return to_f32(reinterpret_cast<const T *>(scales)[g]); }
+    __device__ __forceinline__ float zero(int g) const { return ZP ? (float)(zeros[g] & 15u) : 8.f; }
+  };
+  __device__ __forceinline__ int last(const Place &) const { return end; }
+  __device__ __forceinline__ void scales(const Row &r, const Place &a, int ahead, Scales &s) const {
 #pragma unroll
     for (int g = 0; g < C::kAll; ++g) {
-      const int at = min(a.tile * C::kAll + g, p.w.groups - 1);
-      scale[g] = to_f32(reinterpret_cast<const T *>(r.scales)[at]);
-      zero[g] = ZP ? (float)(r.zeros[at] & 15u) : 8.f;
+      const int at = min((a.tile + ahead) * C::kAll + g, p.w.groups - 1);
+      s.scales[g] = r.scales[at];
+      if (ZP) s.zeros[g] = r.zeros[at];
     }
   }
   __device__ __forceinline__ void finish(const Place &a, int row, int, const float (&acc)[TOKENS]) const {

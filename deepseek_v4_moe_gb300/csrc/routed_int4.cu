@@ -68,26 +68,28 @@ struct LayerJob {
   int row_tile, first, end;       // down
   float back;                     // up: what this lane's token's products are multiplied by
   struct Place {
-    int unit, group, tile, left, tiles, strips, step;
+    int unit, group, tile, left;  // left: tiles; up: units
     __device__ __forceinline__ bool more() const { return left > 0; }
-    __device__ __forceinline__ void next() {
-      if constexpr (!UP) --left;
-      if (++tile == tiles) {
-        tile = 0;
-        if constexpr (UP) {
-          left -= step;
-          unit += step;
-          group = unit / strips;
-        } else {
-          ++group;
-        }
-      }
-    }
   };
+  __device__ __forceinline__ void next(Place &a) const {
+    if (!UP) --a.left;
+    if (++a.tile < tiles) return;
+    a.tile = 0;
+    if (UP) {
+      a.left -= gridDim.x;
+      a.unit += gridDim.x;
+      a.group = a.unit / strips;
+    } else {
+      ++a.group;
+    }
+  }
+  __device__ __forceinline__ int count() const {
+    const int units = c.groups * strips, at = blockIdx.x, step = gridDim.x;
+    return !UP ? end - first : at < units ? tiles * ((units - at + step - 1) / step) : 0;
+  }
   __device__ __forceinline__ Place begin() const {
-    if constexpr (UP)
-      return Place{(int)blockIdx.x, (int)blockIdx.x / strips, 0, c.groups * strips - (int)blockIdx.x, tiles, strips, (int)gridDim.x};
-    else return Place{0, first / tiles, first % tiles, end - first, tiles, 1, 1};
+    if (UP) return Place{(int)blockIdx.x, (int)blockIdx.x / strips, 0, c.groups * strips - (int)blockIdx.x};
+    return Place{0, first / tiles, first % tiles, end - first};
   }
   __device__ __forceinline__ bool ends(const Place &a) const { return UP ? a.tile == tiles - 1 : a.left == 1; }
   // the group's matrix among its kind's
@@ -141,7 +143,7 @@ struct LayerJob {
   __device__ __forceinline__ void row_at(Row &r, const Place &a, int row) const {
     r.row = row;
     if constexpr (UP) {
-      const int next = a.unit + a.step, group = next / strips;
+      const int next = a.unit + gridDim.x, group = next / strips;
       if (group < c.groups) {
         find(r, group, next - group * strips);
         fetch(r);
@@ -151,7 +153,14 @@ struct LayerJob {
       r.group = -1;
     }
   }
-  __device__ __forceinline__ void scales(Row &r, const Place &a, float (&scale)[C::kAll], float (&zero)[C::kAll]) const {
+  struct Scales {
+    uint16_t scales[C::kAll];
+    uint8_t zeros[C::kAll];
+    __device__ __forceinline__ float scale(int g) const { return to_f32(reinterpret_cast<const T *>(scales)[g]); }
+    __device__ __forceinline__ float zero(int g) const { return (float)(zeros[g] & 15u); }
+  };
+  __device__ __forceinline__ int last(const Place &a) const { return UP || a.left > tiles - a.tile ? tiles : a.tile + a.left; }
+  __device__ __forceinline__ void scales(Row &r, const Place &a, int ahead, Scales &s) const {
     if (!UP && r.group != a.group) {
       if (a.group + 1 < c.groups) {
         find(r, a.group + 1, 0);
@@ -161,9 +170,10 @@ struct LayerJob {
     }
 #pragma unroll
     for (int g = 0; g < C::kAll; ++g) {
-      const int i = min(a.tile * C::kAll + g, r.groups - 1);
-      scale[g] = to_f32(reinterpret_cast<const T *>(r.scales)[i]);
-      zero[g] = r.zeros ? (float)(r.zeros[i] & 15u) : 8.f;
+      const int i = min((a.tile + ahead) * C::kAll + g, r.groups - 1);
+      s.scales[g] = r.scales[i];
+      s.zeros[g] = 8u;
+      if (r.zeros) s.zeros[g] = r.zeros[i];
     }
   }
   __device__ __forceinline__ void finish(const Place &a, int row, int turn, const float (&acc)[TOKENS]) const {
