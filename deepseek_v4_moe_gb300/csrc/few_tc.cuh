@@ -219,11 +219,11 @@ struct CodeBars {
 
 // The kernel's body.  A job gives this CTA's tiles, the same to every role:
 //   int count();  Place begin();  place.more(), place.tile;  next(place)    its tiles, one after another through its units
-//   bool ends(place)                                         a unit's last tile
 //   void weights(place, at, bar)                             its codes' copy, by the converged warp
 //   void ready();  void tokens(place, at, sums, bar)         what the tokens' copies wait for; they, and their groups' sums
-//   Row; void row_at(row, place, r)                          row r's scales, at the beginning of a unit; the next one's
-//                                                            are fetched into the L2
+//   next_unit(place);  int unit_tiles();  bool skip(place, tiles)   on within the unit: whether there is such a tile
+//   Row; void row_at(row, place, r);  next_row(row, place)   where row r of a unit, and of the one after it, has its scales;
+//                                                            the next ones are fetched into the L2
 //   Scales; void scales(row, place, ahead, s); last(place)   those of the tile `ahead` tiles on; the end of such tiles
 //   void finish(place, r, turn, acc)                         by 128 threads; turn: 0 and 1, unit after unit
 template <typename C, int TOKENS, int PLANES, int GROUPS, typename Job>
@@ -320,23 +320,26 @@ __device__ __forceinline__ void code_pipeline(Job &job, char *ring, CodeBars<C> 
     // Sets take every other tile; at the units' ends they take turns in adding the other's sums to their own and finishing.
     // What a set does for a tile bounded the pipeline once (2050 cycles, one step waiting for another): so a tile's scales
     // are read during the one before, and two multiply-adds are one instruction.
+    constexpr bool kAhead = TOKENS < 32;  // (there are no registers for it)
     const int q = warp & 3, set = (warp - C::kFirstJoin) >> 2;
     RingPos<S> pos(set);
     RingPos<C::kA> a(set);
     RingPos<C::kD> d(set);
-    int i = 0, turn = 0;
+    int turn = 0, skipped = set;  // tiles before this set's first in a unit
     uint64_t acc[TOKENS / 2];
-#pragma unroll
-    for (int t = 0; t < TOKENS / 2; ++t) acc[t] = 0u;
-    auto p = job.begin();
+    auto unit = job.begin();
     typename Job::Row row;
-    if (p.more()) job.row_at(row, p, q * 32 + lane);
-    bool ok = true, read = false;  // read: the scales are those of the next tile
     typename Job::Scales now, next;
-    for (; p.more(); job.next(p), ++i) {
-      if (i % C::kJoin == set) {
+    if (unit.more()) job.row_at(row, unit, q * 32 + lane);
+    bool ok = true;
+    for (; unit.more(); job.next_unit(unit)) {
+#pragma unroll
+      for (int t = 0; t < TOKENS / 2; ++t) acc[t] = 0u;
+      auto p = unit;
+      bool in = job.skip(p, skipped), read = false;  // read: the scales are those of the next tile
+      for (; in; in = job.skip(p, C::kJoin)) {
         if (!read) job.scales(row, p, 0, now);
-        read = p.tile + C::kJoin < job.last(p);  // (of the same rows)
+        read = kAhead && p.tile + C::kJoin < job.last(p);  // (of the same rows)
         if (read) job.scales(row, p, C::kJoin, next);
         ok = ok && warp_wait(&b.full[pos.slot], pos.round, abort_p, w.status, w.ns);
         const uint32_t sums = ring0 + pos.slot * C::kStage + C::kW + C::kHalves * C::kB;
@@ -393,28 +396,23 @@ __device__ __forceinline__ void code_pipeline(Job &job, char *ring, CodeBars<C> 
         a.next(C::kJoin);
         d.next(C::kJoin);
       }
-      if (job.ends(p)) {
-        float sum[TOKENS];
+      skipped = (skipped + C::kJoin - job.unit_tiles() % C::kJoin) % C::kJoin;
+      float sum[TOKENS];
 #pragma unroll
-        for (int t = 0; t < TOKENS; t += 2) unpair(acc[t / 2], sum[t], sum[t + 1]);
-        if constexpr (C::kJoin > 1) {
-          float *other = b.join[turn] + q * 32 + lane;
-          if (set != turn)
+      for (int t = 0; t < TOKENS; t += 2) unpair(acc[t / 2], sum[t], sum[t + 1]);
+      if constexpr (C::kJoin > 1) {
+        float *other = b.join[turn] + q * 32 + lane;
+        if (set != turn)
 #pragma unroll
-            for (int t = 0; t < TOKENS; ++t) other[t * kCodeRows] = sum[t];
-          asm volatile("bar.sync 2, %0;" ::"n"(128 * C::kJoin) : "memory");
-          if (set == turn)
+          for (int t = 0; t < TOKENS; ++t) other[t * kCodeRows] = sum[t];
+        asm volatile("bar.sync 2, %0;" ::"n"(128 * C::kJoin) : "memory");
+        if (set == turn)
 #pragma unroll
-            for (int t = 0; t < TOKENS; ++t) sum[t] += other[t * kCodeRows];
-        }
-        if (C::kJoin == 1 || set == turn) job.finish(p, q * 32 + lane, turn, sum);
-        turn ^= 1;
-#pragma unroll
-        for (int t = 0; t < TOKENS / 2; ++t) acc[t] = 0u;
-        auto after = p;
-        job.next(after);
-        if (after.more()) job.row_at(row, after, q * 32 + lane);
+          for (int t = 0; t < TOKENS; ++t) sum[t] += other[t * kCodeRows];
       }
+      if (C::kJoin == 1 || set == turn) job.finish(unit, q * 32 + lane, turn, sum);
+      turn ^= 1;
+      job.next_row(row, unit);
     }
   }
   // Copies still in flight after an abort land before the CTA may leave (bounded; otherwise each has landed).

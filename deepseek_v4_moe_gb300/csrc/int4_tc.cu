@@ -45,7 +45,9 @@ struct MatmulJob {
     return unit0 < units ? (end - first) * ((units - unit0 + unit_step - 1) / unit_step) : 0;
   }
   __device__ __forceinline__ Place begin() const { return Place{first < end ? unit0 : units, first, units}; }
-  __device__ __forceinline__ bool ends(const Place &a) const { return a.tile == end - 1; }
+  __device__ __forceinline__ void next_unit(Place &a) const { a.unit += unit_step; }
+  __device__ __forceinline__ int unit_tiles() const { return end - first; }
+  __device__ __forceinline__ bool skip(Place &a, int by) const { return (a.tile += by) < end; }
   __device__ __forceinline__ void weights(const Place &a, uint32_t at, uint32_t bar) const {
     tma_load_2d_one<false>(at, &maps.w, bar, a.tile * (64 * C::kHalves), a.unit * kCodeRows);
   }
@@ -59,16 +61,27 @@ struct MatmulJob {
   struct Row {
     const uint16_t *scales;
     const uint8_t *zeros;
+    int row;
   };
   __device__ __forceinline__ void row_at(Row &r, const Place &a, int row) const {
-    const long long at = (long long)min(a.unit * kCodeRows + row, p.w.n - 1) * p.w.groups;
+    r.row = row;
+    find(r, a.unit);
+    fetch(r, a.unit);
+  }
+  __device__ __forceinline__ void next_row(Row &r, const Place &a) const {
+    find(r, a.unit + unit_step);
+    fetch(r, a.unit + unit_step);
+  }
+  __device__ __forceinline__ void find(Row &r, int unit) const {
+    const long long at = (long long)min(unit * kCodeRows + r.row, p.w.n - 1) * p.w.groups;
     r.scales = p.w.scales + at;
     r.zeros = p.w.zeros + at;
-    if (a.unit + unit_step < units) {
-      const long long to = (long long)min((a.unit + unit_step) * kCodeRows + row, p.w.n - 1) * p.w.groups;
-      fetch_lines(p.w.scales + to, 2 * p.w.groups);
-      if (ZP) fetch_lines(p.w.zeros + to, p.w.groups);
-    }
+  }
+  __device__ __forceinline__ void fetch(const Row &r, int unit) const {  // those of the unit after it
+    if (unit + unit_step >= units) return;
+    const int by = min((unit + unit_step) * kCodeRows + r.row, p.w.n - 1) - (unit * kCodeRows + r.row);
+    fetch_lines(r.scales + (long long)by * p.w.groups, 2 * p.w.groups);
+    if (ZP) fetch_lines(r.zeros + (long long)by * p.w.groups, p.w.groups);
   }
   struct Scales {
     uint16_t scales[C::kAll];

@@ -91,7 +91,26 @@ struct LayerJob {
     if (UP) return Place{(int)blockIdx.x, (int)blockIdx.x / strips, 0, c.groups * strips - (int)blockIdx.x};
     return Place{0, first / tiles, first % tiles, end - first};
   }
-  __device__ __forceinline__ bool ends(const Place &a) const { return UP ? a.tile == tiles - 1 : a.left == 1; }
+  __device__ __forceinline__ void next_unit(Place &a) const {
+    if (UP) {
+      a.left -= gridDim.x;
+      a.unit += gridDim.x;
+      a.group = a.unit / strips;
+    } else {
+      a.left = 0;
+    }
+  }
+  __device__ __forceinline__ int unit_tiles() const { return UP ? tiles : end - first; }
+  __device__ __forceinline__ bool skip(Place &a, int by) const {
+    a.tile += by;
+    if (UP) return a.tile < tiles;
+    a.left -= by;
+    while (a.tile >= tiles) {
+      a.tile -= tiles;
+      ++a.group;
+    }
+    return a.left > 0;
+  }
   // the group's matrix among its kind's
   __device__ __forceinline__ int matrix_of(const Place &a, bool &shared) const {
     const int e = c.group_expert[a.group];
@@ -119,39 +138,41 @@ struct LayerJob {
     const float *from = UP ? p.x_sums : p.h_sums + (size_t)a.group * p.h_groups * TOKENS;
     tma_bulk_one(to, from + a.tile * (C::kAll * TOKENS), C::kSums, bar);
   }
-  struct Row {
+  struct Lines {
     const uint16_t *scales;
     const uint8_t *zeros;
-    int row, group, groups;
+  };
+  struct Row {
+    Lines now, next;
+    int row, group;
   };
   // row r of a group's matrices; up: 64 rows of gate, then 64 of up
-  __device__ __forceinline__ void find(Row &r, int group, int strip) const {
+  __device__ __forceinline__ Lines find(int r, int group, int strip) const {
     const int e0 = c.group_expert[group];
-    const bool shared = e0 >= p.experts, up = UP && r.row >= 64;
+    const bool shared = e0 >= p.experts, up = UP && r >= 64;
     const FewMatrix &m = UP ? (shared ? (up ? p.s_up : p.s_gate) : up ? p.up : p.gate) : shared ? p.s_down : p.down;
-    const int row = UP ? min(strip * 64 + r.row % 64, p.inter - 1) : min(row_tile * kCodeRows + r.row, p.hidden - 1);
-    const long long at = ((long long)(shared ? e0 - p.experts : e0) * (UP ? p.inter : p.hidden) + row) * m.groups;
-    r.group = group;
-    r.groups = m.groups;
-    r.scales = m.scales + at;
-    r.zeros = m.zeros ? m.zeros + at : nullptr;
+    const int row = UP ? min(strip * 64 + r % 64, p.inter - 1) : min(row_tile * kCodeRows + r, p.hidden - 1);
+    const long long at = ((long long)(shared ? e0 - p.experts : e0) * (UP ? p.inter : p.hidden) + row) * groups();
+    return Lines{m.scales + at, m.zeros ? m.zeros + at : nullptr};
   }
-  __device__ __forceinline__ void fetch(const Row &r) const {
-    fetch_lines(r.scales, 2 * r.groups);
-    if (r.zeros) fetch_lines(r.zeros, r.groups);
+  __device__ __forceinline__ int groups() const { return UP ? p.gate.groups : p.down.groups; }
+  // what comes after a unit (up) or a group (down)
+  __device__ __forceinline__ void look_ahead(Row &r, int next) const {
+    const int group = UP ? next / strips : next;
+    if (group >= c.groups) return;
+    r.next = find(r.row, group, UP ? next - group * strips : 0);
+    fetch_lines(r.next.scales, 2 * groups());
+    if (r.next.zeros) fetch_lines(r.next.zeros, groups());
   }
   __device__ __forceinline__ void row_at(Row &r, const Place &a, int row) const {
     r.row = row;
-    if constexpr (UP) {
-      const int next = a.unit + gridDim.x, group = next / strips;
-      if (group < c.groups) {
-        find(r, group, next - group * strips);
-        fetch(r);
-      }
-      find(r, a.group, a.unit - a.group * strips);
-    } else {
-      r.group = -1;
-    }
+    r.group = a.group;
+    r.now = find(row, a.group, UP ? a.unit - a.group * strips : 0);
+    look_ahead(r, UP ? a.unit + gridDim.x : a.group + 1);
+  }
+  __device__ __forceinline__ void next_row(Row &r, const Place &a) const {
+    r.now = r.next;
+    look_ahead(r, a.unit + 2 * gridDim.x);
   }
   struct Scales {
     uint16_t scales[C::kAll];
@@ -162,18 +183,16 @@ struct LayerJob {
   __device__ __forceinline__ int last(const Place &a) const { return UP || a.left > tiles - a.tile ? tiles : a.tile + a.left; }
   __device__ __forceinline__ void scales(Row &r, const Place &a, int ahead, Scales &s) const {
     if (!UP && r.group != a.group) {
-      if (a.group + 1 < c.groups) {
-        find(r, a.group + 1, 0);
-        fetch(r);
-      }
-      find(r, a.group, 0);
+      r.now = a.group == r.group + 1 ? r.next : find(r.row, a.group, 0);
+      r.group = a.group;
+      look_ahead(r, a.group + 1);
     }
 #pragma unroll
     for (int g = 0; g < C::kAll; ++g) {
-      const int i = min((a.tile + ahead) * C::kAll + g, r.groups - 1);
-      s.scales[g] = r.scales[i];
+      const int i = min((a.tile + ahead) * C::kAll + g, groups() - 1);
+      s.scales[g] = r.now.scales[i];
       s.zeros[g] = 8u;
-      if (r.zeros) s.zeros[g] = r.zeros[i];
+      if (r.now.zeros) s.zeros[g] = r.now.zeros[i];
     }
   }
   __device__ __forceinline__ void finish(const Place &a, int row, int turn, const float (&acc)[TOKENS]) const {
