@@ -182,18 +182,20 @@ cudaError_t tc_typed(const Int4MatmulParams &p, const Int4Maps &maps, int tokens
 
 }  // namespace
 
-// Splitting x takes a launch (4096 x 4096 in groups of 128: 7.3 us for a token, 8.1 for 16, by mma.sync 6.0 and 7.7), which
-// large matrices have time for (16384 x 2048: 7.3 and 8.6 for 7.6 and 8.8; 8192 x 8192: 14.3 and 16.5 for 18.4 and 18.1;
-// 129280 x 4096: 49 and 58 for 68 and 93), in groups of 64 larger ones (16384 x 2048: 8.2 for 7.7, 8192 x 8192: 16.6 for 18.7).
-// In groups of 32 the joining of eight groups a tile takes what the conversion saves (129280 x 4096: 100 and 142 for 96 and
-// 111).  Beyond 16 tokens mma.sync's registers leave it behind (4096 x 4096, 32 tokens: 9.7 for 16.4; 1031 x 2016: 7.3 for
-// 9.3), but for groups of 32 of many rows (8192 x 8192: 40 for 51, 16384 x 2048: 21 for 16; 64 tokens, twice 32 here,
-// 2048 x 8192: 23 for 32, 4096 x 4096: 23 for 17.5).
+// Splitting x takes a launch (4096 x 4096 in groups of 128: 7.1 us for a token, 7.7 for 16, by mma.sync 6.0 and 7.7), which
+// large matrices have time for (16384 x 2048: 7.0 and 8.1 for 7.6 and 8.8; 8192 x 8192: 13.7 and 15.6 for 18.4 and 18.1;
+// 129280 x 4096: 46 and 54 for 68 and 93), in groups of 64 larger ones (16384 x 2048 in f16: 7.7 and 9.9 for 7.4 and 8.7,
+// 8192 x 8192: 15.7 and 19.7 for 18.1 and 18.7), and long rows of more than eight tokens (512 x 8192, 16 tokens: 8.6 for
+// 13.3, groups of 64: 9.0 for 13.4).  In groups of 32 the joining of eight groups a tile takes what the conversion saves
+// (129280 x 4096: 97 and 133 for 96 and 112).  Beyond 16 tokens mma.sync's registers leave it behind (4096 x 4096, 32 tokens:
+// 9.9 for 16.4; 1031 x 2016: 7.6 for 9.3), but for groups of 32 of many rows (8192 x 8192: 37 for 51, 16384 x 2048: 20 for
+// 16; 64 tokens, twice 32 here, 2048 x 8192: 22 for 32, 4096 x 4096: 22 for 17.5).
 int int4_tc_tokens(int rows, int n, int k, int group) {
   const long long blocks = (rows + 31) / 32;
   if (group == 32) return rows > 16 && n * blocks * blocks <= 12000 ? 32 : 0;
   if (rows > 16) return 32;
-  return (long long)n * k >= (group == 128 ? 1 << 25 : 1 << 26) ? (rows <= 8 ? 8 : 16) : 0;
+  const bool large = (long long)n * k >= (group == 128 ? 1 << 25 : 1 << 26), deep = rows > 8 && k >= 8192;
+  return large || deep ? (rows <= 8 ? 8 : 16) : 0;
 }
 
 cudaError_t launch_int4_tc(const Int4MatmulParams &p, const Int4Maps &maps, int tokens, bool f16, int num_sms, cudaStream_t st) {
