@@ -8,13 +8,15 @@
 //
 // The right operand is split beforehand: scaled by a power of two, so that its largest magnitude lies in [128, 256), into
 // p0 = e4m3(x), p1 = e4m3(32 (x - p0)) and, for f16, p2 = e4m3(32 (32 (x - p0) - p1)).  Each plane takes four significant
-// bits, so that two are a bf16 number and three an f16 one: exactly down to 2^-14 of the largest magnitude, below that to
-// 2^-22 of it (f16: 2^-27).  The planes are columns of their own; a group's products are joined in f32, its zero point is
-// applied to its sum of x, and its scale to the result, once for each group:
+// bits, so that two are a bf16 number and three an f16 one: exactly down to 2^-14 of the largest magnitude (f16: 2^-16),
+// below that to 2^-22 of it (2^-27; two planes without the 32: 2^-17).  The planes are columns of their own; a group's
+// products are joined in f32, its zero point is applied to its sum of x, and its scale to the result, once for each group:
 //   acc += scale (sum(code p0) + sum(code p1) / 32 + .. - zero sum(x))
 //
-// Roles: a warp copies (TMA), one issues the products, eight make codes operands (two sets of four, every other tile: a
-// thread has a row), four join the groups (a thread has a row, its sums of all tokens in registers).
+// Roles: a warp copies (TMA), one or two issue the products, eight make codes operands (two sets of four, every other tile:
+// a thread has a row), four or eight join the groups (a thread has a row, its sums of all tokens in registers).
+// Joining is what comes before the memory: every role's warp has about 900 cycles for a tile of 128 rows x 256 columns at
+// 5 TB/s, and a set of joining warps took 2050 for two.
 #pragma once
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -318,8 +320,8 @@ __device__ __forceinline__ void code_pipeline(Job &job, char *ring, CodeBars<C> 
   } else if (warp >= C::kFirstJoin) {
     // ---------------- groups' sums ----------------
     // Sets take every other tile; at the units' ends they take turns in adding the other's sums to their own and finishing.
-    // What a set does for a tile bounded the pipeline once (2050 cycles, one step waiting for another): so a tile's scales
-    // are read during the one before, and two multiply-adds are one instruction.
+    // What a set does for a tile bounded the pipeline (2050 cycles, one step waiting for another): so a tile's scales are
+    // read during the one before, and two multiply-adds are one instruction.
     constexpr bool kAhead = TOKENS < 32;  // (there are no registers for it)
     const int q = warp & 3, set = (warp - C::kFirstJoin) >> 2;
     RingPos<S> pos(set);

@@ -1,8 +1,8 @@
 // The product of 4-bit weights and a few rows on the FP8 tensor cores (sm_103a): see few_tc.cuh.
 //
-// A tile is 128 rows of the weights and 128 columns.  Where the matrix has more row tiles than the GPU has SMs, a CTA takes
-// one row tile after another; otherwise the CTAs of a cluster share the columns of one, and their sums meet in shared
-// memory in the order of their ranks.
+// Where the matrix has more row tiles than the GPU has SMs, a CTA takes one row tile after another; otherwise the CTAs of a
+// cluster share the columns of one, and their sums meet in shared memory in the order of their ranks.
+// 16 tokens by 129280 x 4096 in groups of 128: 54 us, 5.1 TB/s (41 at the copy's rate); one token 46.
 #include "few_tc.cuh"
 #include "kernels.h"
 

@@ -60,6 +60,9 @@ def int4_matmul(x: torch.Tensor, w: Int4, out: Optional[torch.Tensor] = None,
     """x w^T for a few rows: ``x`` [rows, k] bfloat16 or float16 (16-byte aligned, row strides multiples of 8), ``w``
     [n, k] in 4 bits with scales of x's type.  Each group's products are summed in float32 and multiplied by its scale
     there; the result [rows, n] is of x's type.  Made for up to 32 rows; more are taken 32 at a time.
+
+    Large products and those of more rows take x in FP8 planes: exact down to 2^-14 of a row's largest magnitude (float16:
+    2^-16), off by at most 2^-22 (2^-27) of it below that; a row that is not finite gives NaN there.
     """
     if stream is not None:
         with _on(x, stream):
@@ -82,7 +85,8 @@ def routed_ffn(x: torch.Tensor, w_router: torch.Tensor, w_gate: Weights, w_up: W
     [experts]; ``w_gate``, ``w_up`` [experts, inter, hidden] and ``w_down`` [experts, hidden, inter], tensors of x's type
     or all :class:`Int4` of one group; ``shared``: the same three of the shared experts, [inter, hidden] for one or
     [count, inter, hidden].  hidden and inter are multiples of 8 (32 with Int4).  Without ``normalise`` the weight is
-    route_scale * s.  Returns (y [rows, hidden], indices int32 [rows, top_k], weights float32 [rows, top_k]).
+    route_scale * s.  4-bit experts take x and their hidden values in planes as :func:`int4_matmul` does; a token's hidden
+    values have one power of two for all of its experts.  Returns (y [rows, hidden], indices int32 [rows, top_k], weights float32 [rows, top_k]).
     """
     if score not in SCORES:
         raise ValueError(f"score must be one of {sorted(SCORES)}")

@@ -487,7 +487,10 @@ int moe_ffn_int4_quantise(const moe_ffn_int4_weights_args *a, const void *w, int
 int moe_ffn_int4_widen(const moe_ffn_int4_weights_args *a, void *out, int64_t ld_out, void *stream);
 
 /* Product of a few rows with such weights: out[i, j] = sum over k of x[i, k] * w[j, k].  Each group's products are summed
- * in f32 and multiplied by its scale there.  Made for up to 32 rows; more are taken 32 at a time. */
+ * in f32 and multiplied by its scale there.  Made for up to 32 rows; more are taken 32 at a time.
+ * Where the call needs a workspace, x goes through it as a row's values over a power of two in FP8 planes: exact down to
+ * 2^-14 of the row's largest magnitude, below that off by at most 2^-22 of it (f16: 2^-16 and 2^-27); magnitudes below
+ * 2^-119 count as that in this.  There a row with a NaN or an infinity gives NaN throughout. */
 typedef struct moe_ffn_int4_matmul_args {
   int32_t rows, n, k;            /* rows at most 2^16; n and k as above */
   int32_t type;                  /* of x, scales and out: MOE_FFN_BF16 or _F16 */
@@ -514,7 +517,10 @@ int moe_ffn_int4_matmul(const moe_ffn_int4_matmul_args *a, void *stream);
  *   weight = route_scale * s, or with normalise route_scale * s / (sum of the chosen s)
  *   y = sum over the slots of weight * E(x) + sum over the shared experts of S(x), each a gated block
  *       E(x) = (act(x gate^T) * (x up^T)) down^T
- * weight * act(g) * u is rounded to the operand type before the down projection (a shared expert's without a weight). */
+ * weight * act(g) * u is rounded to the operand type before the down projection (a shared expert's without a weight).
+ * With bits 4 both operands go through planes as int4_matmul's do; those of the down projection have one power of two for
+ * all of a token's experts.  A token that is not finite, or whose hidden values are not, gives NaN; the others do not
+ * see it. */
 #define MOE_FFN_SCORE_SIGMOID 0
 #define MOE_FFN_SCORE_SOFTMAX 1
 
@@ -549,13 +555,13 @@ int moe_ffn_routed_forward(const moe_ffn_routed_args *a, void *stream);
 /* Bytes of workspace that the call needs; negative: an error code. */
 int64_t moe_ffn_routed_workspace(const moe_ffn_routed_args *a);
 
-/* Device status bits (MOE_FFN_DEV_TIMEOUT) that the dense sublayer's kernels set on the current device
+/* Device status bits (MOE_FFN_DEV_TIMEOUT) that the kernels of the calls without a handle set on the current device
  * since the previous call, after waiting for `stream` (which must not be under capture); then cleared.
  * Each set of bits is reported to one caller.  Or a negative code. */
 int moe_ffn_dense_status(void *stream);
 
 /* Test hook for failure detection, as moe_ffn_set_fault_injection: with enable != 0, CTA 0 of each
- * tensor-core kernel of the dense sublayer that the process launches from now on first waits for
+ * tensor-core kernel of these calls that the process launches from now on first waits for
  * something that never comes, and wait_limit_us (0: 2 s) bounds every wait. */
 int moe_ffn_dense_fault_injection(int32_t enable, uint32_t wait_limit_us);
 
