@@ -138,11 +138,10 @@ __device__ __forceinline__ Pairs gate_set(const NormParams &p, int row, int gate
   return splat(x);
 }
 
-// (Single values: 64 registers and 32 warps on an SM, some of them spilled, in place of 124 and 16 warps: 2000 x 4001
-// bf16 39 -> 28 us, 4096 x 3001 f32 57 -> 44.)
 // Writes y as FP8 codes with a scale for each block of 128 columns, of its f32 values, without wide accesses: a warp's
 // columns of one e (t + n e) lie in one block, several warps' in the same one, and their maxima meet in shared memory
-// (`amax`, one word for each block, zeros on entry and on return; `by`: what the blocks are divided by) by integer atomics, whose order changes nothing.
+// (`amax`, one word for each block, zeros on entry and on return; `by`: what the blocks are divided by) by integer
+// atomics, whose order changes nothing.
 __device__ __forceinline__ void store_codes(const NormParams &p, size_t r, bool in, int t, int n, uint32_t *amax, float2 *by,
                                             const Pairs (&y)[kSets]) {
   const int blocks = (p.hidden + kScaleBlock - 1) / kScaleBlock;
@@ -181,6 +180,8 @@ __device__ __forceinline__ void store_codes(const NormParams &p, size_t r, bool 
     }
 }
 
+// (Single values: 64 registers and 32 warps on an SM, some of them spilled, in place of 124 and 16 warps: 2000 x 4001
+// bf16 39 -> 28 us, 4096 x 3001 f32 57 -> 44.)
 // OUT8: y goes out as FP8 codes and scales (without wide accesses).
 template <typename TS, typename TB, bool VEC, bool OUT8>
 __global__ void __launch_bounds__(512, VEC ? 1 : 2) block_norm_kernel(const __grid_constant__ NormParams p, int n) {

@@ -14,7 +14,7 @@
 //   acc += scale (sum(code p0) + sum(code p1) / 32 + .. - zero sum(x))
 //
 // Roles: a warp copies (TMA), one or two issue the products, eight make codes operands (two sets of four, every other tile:
-// a thread has a row), four or eight join the groups (a thread has a row, its sums of all tokens in registers).
+// a thread has a row), four or eight join the groups (a thread has a row, its sums of the tokens in registers).
 // Joining is what comes before the memory: every role's warp has about 900 cycles for a tile of 128 rows x 256 columns at
 // 5 TB/s, and a set of joining warps took 2050 for two.
 #pragma once
@@ -47,7 +47,12 @@ struct CodeCfg {
   // that make operands and that join groups: each takes tiles in turn.  A set sees a barrier's every round only if no
   // other set uses its slot, so the numbers of slots and stages are multiples of the sets'.
   static constexpr int kD = kAll * kN <= 64 ? 4 : kAll * kN <= 192 ? 2 : 1;
-  static constexpr int kIssue = kD > 1 ? 2 : 1, kJoin = TOKENS <= 16 && kD > 1 ? 2 : 1, kSets = 2;
+  static constexpr int kIssue = kD > 1 ? 2 : 1, kSets = 2;
+  // Sets that join take every other tile, of 32 tokens 16 each of every tile: all of them in one set have no registers for
+  // the next scales (32 tokens by 129280 x 4096 in groups of 128: 80.9 us, 73.3 so; f16 79.7 and 76.0).  Two planes in
+  // groups of 32 have one set, as every step is another's wait there (8192 x 8192: 37.1, in two 41.0; f16 42.4 and 41.2).
+  static constexpr int kHalf = TOKENS > 16 && (GROUPS < 4 || PLANES > 2) ? 2 : 1, kTurns = kHalf == 1 && kD > 1 ? 2 : 1;
+  static constexpr int kJoin = kHalf * kTurns, kMine = TOKENS / kHalf;
   static constexpr int kFit = 180 * 1024 / kStage < 12 ? 180 * 1024 / kStage : 12, kStages = kFit / 2 * 2;
   static constexpr int kRoom = (512 - kD * kAll * kN) / (32 * kHalves), kA = (kRoom < 8 ? kRoom : 8) / 2 * 2;
   static constexpr int kFirstJoin = 1 + kIssue + (1 + kIssue) % 2, kFirstMake = kFirstJoin + 4 * kJoin;  // their first warps
@@ -213,7 +218,7 @@ __device__ __forceinline__ void tma_bulk_one(uint32_t dst, const void *src, uint
 
 template <typename C>
 struct CodeBars {
-  float join[2][C::kJoin > 1 ? C::kTokens * kCodeRows : 1];
+  float join[2][C::kTurns > 1 ? C::kTokens * kCodeRows : 1];
   uint64_t full[12], empty[12], afull[kCodeSlotsMax], aempty[kCodeSlotsMax], dfull[kCodeSlotsMax], dempty[kCodeSlotsMax], mma_done[2], never;
   uint32_t tmem;
   int abort_flag, issued;
@@ -227,7 +232,8 @@ struct CodeBars {
 //   Row; void row_at(row, place, r);  next_row(row, place)   where row r of a unit, and of the one after it, has its scales;
 //                                                            the next ones are fetched into the L2
 //   Scales; void scales(row, place, ahead, s); last(place)   those of the tile `ahead` tiles on; the end of such tiles
-//   void finish(place, r, turn, acc)                         by 128 threads; turn: 0 and 1, unit after unit
+//   void finish(place, r, turn, barrier, t0, acc)            by 128 threads with a barrier for them, of tokens from t0 on;
+//                                                            turn: 0 and 1, unit after unit
 template <typename C, int TOKENS, int PLANES, int GROUPS, typename Job>
 __device__ __forceinline__ void code_pipeline(Job &job, char *ring, CodeBars<C> &b, const Waits &w) {
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -322,13 +328,15 @@ __device__ __forceinline__ void code_pipeline(Job &job, char *ring, CodeBars<C> 
     // Sets take every other tile; at the units' ends they take turns in adding the other's sums to their own and finishing.
     // What a set does for a tile bounded the pipeline (2050 cycles, one step waiting for another): so a tile's scales are
     // read during the one before, and two multiply-adds are one instruction.
-    constexpr bool kAhead = TOKENS < 32;  // (there are no registers for it)
     const int q = warp & 3, set = (warp - C::kFirstJoin) >> 2;
-    RingPos<S> pos(set);
-    RingPos<C::kA> a(set);
-    RingPos<C::kD> d(set);
-    int turn = 0, skipped = set;  // tiles before this set's first in a unit
-    uint64_t acc[TOKENS / 2];
+    const int late = C::kTurns > 1 ? set : 0, t_first = C::kHalf > 1 ? set * C::kMine : 0;  // its first tile and token
+    constexpr int kMine = C::kMine;
+    constexpr bool kAhead = kMine < 32;  // (there are no registers for it otherwise)
+    RingPos<S> pos(late);
+    RingPos<C::kA> a(late);
+    RingPos<C::kD> d(late);
+    int turn = 0, skipped = late;  // tiles before this set's first in a unit
+    uint64_t acc[kMine / 2];
     auto unit = job.begin();
     typename Job::Row row;
     typename Job::Scales now, next;
@@ -336,13 +344,13 @@ __device__ __forceinline__ void code_pipeline(Job &job, char *ring, CodeBars<C> 
     bool ok = true;
     for (; unit.more(); job.next_unit(unit)) {
 #pragma unroll
-      for (int t = 0; t < TOKENS / 2; ++t) acc[t] = 0u;
+      for (int t = 0; t < kMine / 2; ++t) acc[t] = 0u;
       auto p = unit;
       bool in = job.skip(p, skipped), read = false;  // read: the scales are those of the next tile
-      for (; in; in = job.skip(p, C::kJoin)) {
+      for (; in; in = job.skip(p, C::kTurns)) {
         if (!read) job.scales(row, p, 0, now);
-        read = kAhead && p.tile + C::kJoin < job.last(p);  // (of the same rows)
-        if (read) job.scales(row, p, C::kJoin, next);
+        read = kAhead && p.tile + C::kTurns < job.last(p);  // (of the same rows)
+        if (read) job.scales(row, p, C::kTurns, next);
         ok = ok && warp_wait(&b.full[pos.slot], pos.round, abort_p, w.status, w.ns);
         const uint32_t sums = ring0 + pos.slot * C::kStage + C::kW + C::kHalves * C::kB;
         ok = ok && warp_wait(&b.dfull[d.slot], d.round, abort_p, w.status, w.ns);
@@ -350,19 +358,19 @@ __device__ __forceinline__ void code_pipeline(Job &job, char *ring, CodeBars<C> 
         if (ok) {
           // Sixteen tokens' sums of a group at a time (of eight tokens all planes' lie in one or two sixteens), of several
           // groups where registers allow it, so that their way is waited for once.
-          constexpr int kChunk = TOKENS < 16 ? TOKENS : 16, kCols = TOKENS < 16 ? C::kN : 16 * PLANES;
+          constexpr int kChunk = kMine < 16 ? kMine : 16, kCols = TOKENS < 16 ? C::kN : 16 * PLANES;
           constexpr int kBatch = C::kAll * kCols <= 32 ? C::kAll : kCols <= 16 ? 2 : 1;
           const uint32_t from = tmem_d + ((uint32_t)(q * 32) << 16) + d.slot * (C::kAll * C::kN);
           const uint64_t plane = pair(kPlane, kPlane);
 #pragma unroll
           for (int g0 = 0; g0 < C::kAll; g0 += kBatch)
 #pragma unroll
-            for (int t0 = 0; t0 < TOKENS; t0 += kChunk) {
+            for (int t0 = 0; t0 < kMine; t0 += kChunk) {
               float v[kBatch][kCols];
 #pragma unroll
-              for (int g = 0; g < kBatch; ++g) tmem_columns<kCols>(from + (g0 + g) * C::kN + t0, TOKENS, v[g]);
+              for (int g = 0; g < kBatch; ++g) tmem_columns<kCols>(from + (g0 + g) * C::kN + t_first + t0, TOKENS, v[g]);
               tmem_arrived(reinterpret_cast<float(&)[kBatch * kCols]>(v));
-              if (g0 + kBatch >= C::kAll && t0 + kChunk == TOKENS) {  // everything is in registers: the tile's slots are free
+              if (g0 + kBatch >= C::kAll && t0 + kChunk == kMine) {  // everything is in registers: the tile's slots are free
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
@@ -376,7 +384,7 @@ __device__ __forceinline__ void code_pipeline(Job &job, char *ring, CodeBars<C> 
                 const uint64_t z = pair(zero, zero), m = pair(scale, scale);
 #pragma unroll
                 for (int t4 = 0; t4 < kChunk; t4 += 4) {
-                  const uint4 x4 = lds128(sums + ((g0 + g) * TOKENS + t0 + t4) * 4);
+                  const uint4 x4 = lds128(sums + ((g0 + g) * TOKENS + t_first + t0 + t4) * 4);
                   const uint64_t x[2] = {pair(__uint_as_float(x4.x), __uint_as_float(x4.y)), pair(__uint_as_float(x4.z), __uint_as_float(x4.w))};
 #pragma unroll
                   for (int i = 0; i < 2; ++i) {
@@ -394,25 +402,25 @@ __device__ __forceinline__ void code_pipeline(Job &job, char *ring, CodeBars<C> 
         __syncwarp();
         if (lane == 0) mbar_arrive(&b.empty[pos.slot]);
         now = next;
-        pos.next(C::kJoin);
-        a.next(C::kJoin);
-        d.next(C::kJoin);
+        pos.next(C::kTurns);
+        a.next(C::kTurns);
+        d.next(C::kTurns);
       }
-      skipped = (skipped + C::kJoin - job.unit_tiles() % C::kJoin) % C::kJoin;
-      float sum[TOKENS];
+      skipped = (skipped + C::kTurns - job.unit_tiles() % C::kTurns) % C::kTurns;
+      float sum[kMine];
 #pragma unroll
-      for (int t = 0; t < TOKENS; t += 2) unpair(acc[t / 2], sum[t], sum[t + 1]);
-      if constexpr (C::kJoin > 1) {
+      for (int t = 0; t < kMine; t += 2) unpair(acc[t / 2], sum[t], sum[t + 1]);
+      if constexpr (C::kTurns > 1) {
         float *other = b.join[turn] + q * 32 + lane;
-        if (set != turn)
+        if (late != turn)
 #pragma unroll
-          for (int t = 0; t < TOKENS; ++t) other[t * kCodeRows] = sum[t];
-        asm volatile("bar.sync 2, %0;" ::"n"(128 * C::kJoin) : "memory");
-        if (set == turn)
+          for (int t = 0; t < kMine; ++t) other[t * kCodeRows] = sum[t];
+        asm volatile("bar.sync 2, %0;" ::"n"(128 * C::kTurns) : "memory");
+        if (late == turn)
 #pragma unroll
-          for (int t = 0; t < TOKENS; ++t) sum[t] += other[t * kCodeRows];
+          for (int t = 0; t < kMine; ++t) sum[t] += other[t * kCodeRows];
       }
-      if (C::kJoin == 1 || set == turn) job.finish(unit, q * 32 + lane, turn, sum);
+      if (C::kTurns == 1 || late == turn) job.finish(unit, q * 32 + lane, turn, 3 + (C::kHalf > 1 ? set : turn), t_first, sum);
       turn ^= 1;
       job.next_row(row, unit);
     }
@@ -440,15 +448,15 @@ __device__ __forceinline__ void code_setup(CodeBars<C> &b) {
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&b.full[s], 1);
-      mbar_init(&b.empty[s], 4 + 4);  // the warps that made its operand, and that joined its groups after the products
+      mbar_init(&b.empty[s], 4 + 4 * C::kHalf);  // the warps that made its operand, and that joined its groups after the products
     }
     for (int s = 0; s < C::kA; ++s) {
       mbar_init(&b.afull[s], 4);
-      mbar_init(&b.aempty[s], 4);
+      mbar_init(&b.aempty[s], 4 * C::kHalf);
     }
     for (int s = 0; s < C::kD; ++s) {
       mbar_init(&b.dfull[s], 1);
-      mbar_init(&b.dempty[s], 4);
+      mbar_init(&b.dempty[s], 4 * C::kHalf);
     }
     for (int s = 0; s < 2; ++s) mbar_init(&b.mma_done[s], 1);
     mbar_init(&b.never, 1);

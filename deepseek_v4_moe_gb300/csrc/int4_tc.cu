@@ -98,13 +98,13 @@ struct MatmulJob {
       if (ZP) s.zeros[g] = r.zeros[at];
     }
   }
-  __device__ __forceinline__ void finish(const Place &a, int row, int, const float (&acc)[TOKENS]) const {
+  __device__ __forceinline__ void finish(const Place &a, int row, int, int, int t0, const float (&acc)[C::kMine]) const {
     const int n = a.unit * kCodeRows + row, rows = min(TOKENS, p.rows - block * TOKENS);
 #pragma unroll
-    for (int t = 0; t < TOKENS; ++t) {
-      if (t >= rows) break;
-      if (splits > 1) sums[t * kCodeRows + row] = acc[t];
-      else if (n < p.w.n) store(n, t, acc[t]);
+    for (int t = 0; t < C::kMine; ++t) {
+      if (t0 + t >= rows) break;
+      if (splits > 1) sums[(t0 + t) * kCodeRows + row] = acc[t];
+      else if (n < p.w.n) store(n, t0 + t, acc[t]);
     }
   }
   __device__ __forceinline__ void store(int n, int t, float v) const {

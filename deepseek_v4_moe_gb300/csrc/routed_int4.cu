@@ -10,8 +10,7 @@
 // token has not chosen an expert, adds all experts' products in its registers, in one order.
 // 16 tokens through 256 experts of 4096 x 2048 and a shared one, six each, in groups of 128: 226 us, 4.7 TB/s (157 at the
 // copy's rate; on mma.sync, each expert's tokens eight at a time, 577); one token 46 us (13.7), of which the four kernels'
-// latencies are the most: gate and up have 224 strips for 152 SMs.  32 tokens 551 us (263): the sums of 32 tokens leave
-// the joining warps no registers to read a tile's scales ahead.
+// latencies are the most: gate and up have 224 strips for 152 SMs.  32 tokens 537 us (263).
 //
 // A token's h has one power of two for all of its experts, from the largest magnitude among them (an atomic maximum: of
 // any order the same), so that their products can be added as they are: what is lost of an expert's h is below 2^-22 of
@@ -199,24 +198,24 @@ struct LayerJob {
       if (r.now.zeros) s.zeros[g] = r.now.zeros[i];
     }
   }
-  __device__ __forceinline__ void finish(const Place &a, int row, int turn, const float (&acc)[TOKENS]) const {
+  __device__ __forceinline__ void finish(const Place &a, int row, int turn, int barrier, int t0, const float (&acc)[C::kMine]) const {
     if constexpr (UP) {
-      float *u = sums + turn * (TOKENS * 64);
+      float *u = sums + turn * (TOKENS * 64) + t0 * 64;
       if (row >= 64)
 #pragma unroll
-        for (int t = 0; t < TOKENS; ++t)
-          if (t < p.rows) u[t * 64 + row - 64] = acc[t];
-      asm volatile("bar.sync %0, 128;" ::"r"(3 + turn) : "memory");
+        for (int t = 0; t < C::kMine; ++t)
+          if (t0 + t < p.rows) u[t * 64 + row - 64] = acc[t];
+      asm volatile("bar.sync %0, 128;" ::"r"(barrier) : "memory");
       if (row >= 64) return;
       const int at = (a.unit - a.group * strips) * 64 + row, e = c.group_expert[a.group];
-      const uint32_t mask = c.group_mask[a.group];
-      uint16_t *h = p.h + (size_t)a.group * p.rows * p.inter + at;
+      const uint32_t mask = c.group_mask[a.group] >> t0;
+      uint16_t *h = p.h + ((size_t)a.group * p.rows + t0) * p.inter + at;
       const float weight = weight_of(p, c, e, threadIdx.x & 31);  // this lane's token's
 #pragma unroll
-      for (int t = 0; t < TOKENS; ++t) {
-        if (t >= p.rows) break;
+      for (int t = 0; t < C::kMine; ++t) {
+        if (t0 + t >= p.rows) break;
         if (!(mask >> t & 1)) continue;
-        const float by = __shfl_sync(0xffffffffu, back, t), w = __shfl_sync(0xffffffffu, weight, t);
+        const float by = __shfl_sync(0xffffffffu, back, t0 + t), w = __shfl_sync(0xffffffffu, weight, t0 + t);
         uint32_t size = 0u;
         if (at < p.inter) {
           // rounded to 16 bits as the 16-bit layer does
@@ -225,12 +224,12 @@ struct LayerJob {
           size = __float_as_uint(to_f32(out)) & 0x7FFFFFFFu;
         }
         size = __reduce_max_sync(0xffffffffu, size);
-        if (row % 32 == 0) atomicMax(p.h_max + t, size);
+        if (row % 32 == 0) atomicMax(p.h_max + t0 + t, size);
       }
     } else {
 #pragma unroll
-      for (int t = 0; t < TOKENS; ++t)
-        if (t < p.rows) sums[t * kCodeRows + row] = acc[t];
+      for (int t = 0; t < C::kMine; ++t)
+        if (t0 + t < p.rows) sums[(t0 + t) * kCodeRows + row] = acc[t];
     }
   }
 };

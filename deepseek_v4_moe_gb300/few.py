@@ -86,7 +86,8 @@ def routed_ffn(x: torch.Tensor, w_router: torch.Tensor, w_gate: Weights, w_up: W
     or all :class:`Int4` of one group; ``shared``: the same three of the shared experts, [inter, hidden] for one or
     [count, inter, hidden].  hidden and inter are multiples of 8 (32 with Int4).  Without ``normalise`` the weight is
     route_scale * s.  4-bit experts take x and their hidden values in planes as :func:`int4_matmul` does; a token's hidden
-    values have one power of two for all of its experts.  Returns (y [rows, hidden], indices int32 [rows, top_k], weights float32 [rows, top_k]).
+    values have one power of two for all of its experts.  Weights are finite: what is not in a chosen expert's reaches all
+    tokens of the call.  Returns (y [rows, hidden], indices int32 [rows, top_k], weights float32 [rows, top_k]).
     """
     if score not in SCORES:
         raise ValueError(f"score must be one of {sorted(SCORES)}")

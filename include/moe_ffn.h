@@ -520,7 +520,7 @@ int moe_ffn_int4_matmul(const moe_ffn_int4_matmul_args *a, void *stream);
  * weight * act(g) * u is rounded to the operand type before the down projection (a shared expert's without a weight).
  * With bits 4 both operands go through planes as int4_matmul's do; those of the down projection have one power of two for
  * all of a token's experts.  A token that is not finite, or whose hidden values are not, gives NaN; the others do not
- * see it. */
+ * see it.  Weights are finite: an infinity or a NaN of a chosen expert reaches all tokens of the call. */
 #define MOE_FFN_SCORE_SIGMOID 0
 #define MOE_FFN_SCORE_SOFTMAX 1
 
