@@ -207,7 +207,7 @@ struct RowChunks {
 
 // The quotients are those of dense_quant.cuh, without a division for each value (all of them divided, with a 64-bit
 // division for a lane's place besides: 4096 x 2048 made and widened 22.9 us, now 14.0, of which 8.9 and 5.1); a warp has its
-// next columns' loads in flight, 16 KB on an SM, which bounds it at 2.4 TB/s.
+// next columns' loads in flight (two ahead changed nothing).  Bound by its instructions, some 150 for eight values.
 template <typename T, typename TS, int PER, bool ZP>  // PER: lanes of a group
 __global__ void __launch_bounds__(256, 4) int4_quantise_kernel(const __grid_constant__ Int4WeightParams p) {
   constexpr float kLeast = std::is_same<TS, __half>::value ? 6.103515625e-05f : 1.17549435e-38f;
