@@ -19,8 +19,12 @@ struct FewMatrix {
 };
 
 // Halves of 128 columns that a tile of the FP8 tensor cores' form has: one where two halves' sums of all groups leave no
-// room in TMEM.  groups: of 128 columns.
-constexpr int code_halves(int tokens, int planes, int groups) { return 2 * groups * ((tokens * planes + 15) / 16 * 16) <= 384 ? 2 : 1; }
+// room for a second tile's in TMEM (16 tokens of the routed layer in groups of 32: 566 us, 510 so; f16 599 and 559), or, of
+// 32 tokens, not even for one's (in groups of 64 one half would take 937 us for 789: the tiles' fixed costs count for both
+// joining sets).  groups: of 128 columns.
+constexpr int code_halves(int tokens, int planes, int groups) {
+  return 2 * groups * ((tokens * planes + 15) / 16 * 16) <= (tokens > 16 ? 384 : 192) ? 2 : 1;
+}
 
 // CTAs of a cluster that share a row tile's columns: as many as run at one time (of clusters of 8, 4 and 2 with an SM for
 // each CTA, 12, 36 and 75 on 152 SMs: 16 tiles of 2048 x 8192 by 32 tokens took 18 us in eights, 12.5 in fours)

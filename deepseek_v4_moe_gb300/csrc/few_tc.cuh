@@ -13,8 +13,8 @@
 // products are joined in f32, its zero point is applied to its sum of x, and its scale to the result, once for each group:
 //   acc += scale (sum(code p0) + sum(code p1) / 32 + .. - zero sum(x))
 //
-// Roles: a warp copies (TMA), one or two issue the products, eight make codes operands (two sets of four, every other tile:
-// a thread has a row), four or eight join the groups (a thread has a row, its sums of the tokens in registers).
+// Roles: a warp copies (TMA), one or two issue the products, four or eight make codes operands and four or eight join the
+// groups (in sets of four, of which a thread has a row; its sums of the tokens stay in registers).
 // Joining is what comes before the memory: every role's warp has about 900 cycles for a tile of 128 rows x 256 columns at
 // 5 TB/s, and a set of joining warps took 2050 for two.
 #pragma once
@@ -44,10 +44,14 @@ struct CodeCfg {
   static constexpr int kStage = kW + kHalves * kB + (kSums + 1023) / 1024 * 1024;
   static constexpr uint32_t kBytes = kW + kHalves * kRows * 128 + kSums;
   // Slots in TMEM of a tile's sums (all its groups') and of left operands.  Warps that issue products, and sets of four
-  // that make operands and that join groups: each takes tiles in turn.  A set sees a barrier's every round only if no
-  // other set uses its slot, so the numbers of slots and stages are multiples of the sets'.
+  // that make operands and that join groups, take tiles in turn.  A set sees a barrier's every round only if no other set
+  // uses its slot, so the numbers of slots and stages are multiples of the sets'.
   static constexpr int kD = kAll * kN <= 64 ? 4 : kAll * kN <= 192 ? 2 : 1;
-  static constexpr int kIssue = kD > 1 ? 2 : 1, kSets = 2;
+  static constexpr int kIssue = kD > 1 ? 2 : 1;
+  // Two sets make operands where little else is done (one token through the routed layer in groups of 128 40.8 us, with one
+  // set 42.2); otherwise their instructions are missed where groups are joined (16 tokens in groups of 32 510 us, with one
+  // set 487, of 128 220 and 218).
+  static constexpr int kSets = TOKENS == 8 && GROUPS == 1 ? 2 : 1;
   // Sets that join take every other tile, of 32 tokens 16 each of every tile: all of them in one set have no registers for
   // the next scales (32 tokens by 129280 x 4096 in groups of 128: 80.9 us, 73.3 so; f16 79.7 and 76.0).  Two planes in
   // groups of 32 have one set, as every step is another's wait there (8192 x 8192: 37.1, in two 41.0; f16 42.4 and 41.2).

@@ -182,14 +182,15 @@ cudaError_t tc_typed(const Int4MatmulParams &p, const Int4Maps &maps, int tokens
 
 }  // namespace
 
-// Splitting x takes a launch (4096 x 4096 in groups of 128: 7.1 us for a token, 7.7 for 16, by mma.sync 6.0 and 7.7), which
-// large matrices have time for (16384 x 2048: 7.0 and 8.1 for 7.6 and 8.8; 8192 x 8192: 13.7 and 15.6 for 18.4 and 18.1;
-// 129280 x 4096: 46 and 54 for 68 and 93), in groups of 64 larger ones (16384 x 2048 in f16: 7.7 and 9.9 for 7.4 and 8.7,
-// 8192 x 8192: 15.7 and 19.7 for 18.1 and 18.7), and long rows of more than eight tokens (512 x 8192, 16 tokens: 8.6 for
-// 13.3, groups of 64: 9.0 for 13.4).  In groups of 32 the joining of eight groups a tile takes what the conversion saves
-// (129280 x 4096: 97 and 133 for 96 and 112).  Beyond 16 tokens mma.sync's registers leave it behind (4096 x 4096, 32 tokens:
-// 9.9 for 16.4; 1031 x 2016: 7.6 for 9.3), but for groups of 32 of many rows (8192 x 8192: 37 for 51, 16384 x 2048: 20 for
-// 16; 64 tokens, twice 32 here, 2048 x 8192: 22 for 32, 4096 x 4096: 22 for 17.5).
+// Splitting x takes a launch (4096 x 4096 in groups of 128: 7.1 us for a token, 7.9 for 16, by mma.sync 6.0 and 7.7), which
+// large matrices have time for (16384 x 2048: 7.0 and 8.4 for 7.6 and 8.8; 8192 x 8192: 13.7 and 16.0 for 18.4 and 18.3;
+// 129280 x 4096: 46 and 54 for 68 and 93), in groups of 64 larger ones (16384 x 2048 in f16: 7.7 and 10.1 for 7.4 and 8.8,
+// 8192 x 8192: 15.9 and 20.2 for 18.1 and 18.9, in bf16 15.5 and 17.3 for 18.6 and 18.9), and long rows of more than eight
+// tokens (512 x 8192, 16 tokens: 8.7 for 13.3, groups of 64: 8.8 for 13.4).  In groups of 32 the joining of eight groups
+// takes what the conversion saves (129280 x 4096: 91 and 115 for 96 and 111).  Beyond 16 tokens mma.sync's registers leave
+// it behind (4096 x 4096, 32 tokens: 9.2 for 16.5; 1031 x 2016: 7.0 for 9.3), but for groups of 32 of many rows
+// (8192 x 8192: 32 for 51, 16384 x 2048: 17 for 16; 64 tokens, twice 32 here, 2048 x 8192: 19 for 32, 4096 x 4096: 19 for
+// 17.5).
 int int4_tc_tokens(int rows, int n, int k, int group) {
   const long long blocks = (rows + 31) / 32;
   if (group == 32) return rows > 16 && n * blocks * blocks <= 12000 ? 32 : 0;
