@@ -78,7 +78,8 @@ __device__ __forceinline__ uint32_t rank_of(float v) {
   return v != v ? 1u : u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// A warp for each token.  Every thread of the CTA; ends with a barrier.  keys: 1024 words of shared memory for each warp.
+// A warp for each token.  Every thread of the CTA; ends with a barrier.  keys: 1024 words of shared memory for each warp,
+// whose use by TMA afterwards needs a proxy fence by every thread and a barrier (choose_groups).
 // The loops are kept short: a kernel runs this code once, and its way into the instruction caches took most of its time
 // while the experts were held in registers (16 of them a lane, each loop unrolled: 8.7 us of one token of 256 experts).
 // But the loads have one of their own, with all of them on their way (one token of 256 experts in 16 bits: 69.9 -> 65.5 us).
@@ -174,6 +175,9 @@ __device__ __forceinline__ void choose_groups(const RoutedParams &p, Choice &c, 
   choose_tokens(p, c, keys, write);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int all = p.experts + p.shared, parts = (all + 31) >> 5;
+  // The keys' place is TMA's next: their loads and stores (behind choose_tokens' last barrier) come before its writes, which
+  // no barrier alone orders after them.
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   auto tokens_of = [&](int e) { return e < p.experts ? c.mask[e] : e < all ? 0xFFFFFFFFu >> (32 - p.rows) : 0u; };
   for (int i = warp; i < parts; i += warps) {
     const uint32_t has = __ballot_sync(0xffffffffu, tokens_of(32 * i + lane) != 0u);
