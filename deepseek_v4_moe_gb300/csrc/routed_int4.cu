@@ -69,7 +69,8 @@ struct LayerJob {
   float *sums;                    // up: [2][TOKENS][64]; down: [TOKENS][128]
   int tiles, strips;              // of a group; up: units of a group
   int row_tile, first, end;       // down
-  float back;                     // up: what this lane's token's products are multiplied by
+  float back;                     // up: what this lane's token's products are multiplied by, after 512 (2^119 at most: together
+                                  // they may leave f32)
   struct Place {
     int unit, group, tile, left;  // left: tiles; up: units
     __device__ __forceinline__ bool more() const { return left > 0; }
@@ -219,7 +220,7 @@ struct LayerJob {
         uint32_t size = 0u;
         if (at < p.inter) {
           // rounded to 16 bits as the 16-bit layer does
-          const T out = from_f32<T>(act_value(p.act, acc[t] * by) * (u[t * 64 + row] * by) * w);
+          const T out = from_f32<T>(act_value(p.act, acc[t] * 512.f * by) * (u[t * 64 + row] * 512.f * by) * w);
           h[(size_t)t * p.inter] = *reinterpret_cast<const uint16_t *>(&out);
           size = __float_as_uint(to_f32(out)) & 0x7FFFFFFFu;
         }
@@ -256,7 +257,7 @@ __global__ void __launch_bounds__(CodeCfg<TOKENS, PLANES, GROUPS>::kThreads, 1)
     for (int g = threadIdx.x; g < p.groups; g += C::kThreads) p.masks[g] = g < c.groups ? c.group_mask[g] : 0u;
   const LayerJob<UP, T, TOKENS, PLANES, GROUPS> job{p, maps, c, sums, tiles, strips, row_tile, (int)(all * rank / splits),
                                                     (int)(all * (rank + 1) / splits),
-                                                    UP && threadIdx.x % 32 < p.rows ? 512.f * __ldcg(p.back + threadIdx.x % 32) : 0.f};
+                                                    UP && threadIdx.x % 32 < p.rows ? __ldcg(p.back + threadIdx.x % 32) : 0.f};
   if (!UP && job.first == job.end)
     for (int i = threadIdx.x; i < TOKENS * kCodeRows; i += C::kThreads) sums[i] = 0.f;
   code_pipeline<C, TOKENS, PLANES, GROUPS>(job, ring, bars, p.waits);
