@@ -174,6 +174,18 @@ constexpr float kGelu2 = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 __device__ __forceinline__ float act_value(int act, float g) {
   return g * fast_sigmoid(act == kSilu ? g : kGelu2 * fmaf(0.044715f * g * g, g, g));
 }
+// The same to a few units of 2^-23, wherever it lies: for products that go on in more than 16 bits.  (Near -80 the form
+// above is off by 2^-17.)  1 + e lies in [1, 2], where a step of Newton's method leaves its reciprocal a unit off at most.
+__device__ __forceinline__ float sigmoid_f32(float x) {
+  const float e = expf(-fabsf(x)), d = 1.f + e;
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+  r = fmaf(r, fmaf(-d, r, 1.f), r);
+  return x < 0.f ? e * r : r;
+}
+__device__ __forceinline__ float act_f32(int act, float g) {
+  return g * sigmoid_f32(act == kSilu ? g : kGelu2 * fmaf(0.044715f * g * g, g, g));
+}
 __device__ __forceinline__ void act_both(int act, float g, float &a, float &da) {
   const float s = fast_sigmoid(act == kSilu ? g : kGelu2 * fmaf(0.044715f * g * g, g, g));
   // (finite: past 4e19, where its square leaves f32, what it is multiplied by is 0)

@@ -256,7 +256,7 @@ RoutedSpace routed_space(const moe_ffn_routed_args *a) {
   };
   const int64_t R = a->rows, I = a->inter, H = a->hidden, G = routed_groups(a);
   part(R * a->experts * 4);  // the logits
-  s.h = part(G * (a->bits == 4 ? R : (R + 7) / 8 * 8) * I * 2);
+  s.h = part(G * (a->bits == 4 ? R : (R + 7) / 8 * 16) * I * 2);
   if (a->bits == 4) {
     s.tokens = moe::routed_code_tokens(a->rows);
     s.planes = a->type == MOE_FFN_F16 ? 3 : 2;
@@ -383,7 +383,7 @@ extern "C" int moe_ffn_routed_forward(const moe_ffn_routed_args *a, void *stream
   if (a->bits == 16) {
     const int64_t R8 = (R + 7) / 8 * 8;
     if (!ok || !encode_map(&maps.tokens, a->x, 2, H, R, a->ld_x, (int)R8) ||
-        !encode_map(&down.tokens, p.h, 2, I, p.groups * R8, I, (int)R8))
+        !encode_map(&down.tokens, p.h, 2, I, p.groups * 2 * R8, I, (int)(2 * R8)))
       return fail(MOE_FFN_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", who);
     return launched(who, moe::launch_routed(p, maps, down, f16, sms, st));
   }

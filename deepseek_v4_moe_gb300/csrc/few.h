@@ -106,8 +106,8 @@ struct RoutedParams {
   int32_t *indices;                    // [rows, top_k] or none
   float *weights;
   float *logits;                       // workspace: [rows, experts]
-  uint16_t *h;                         // workspace: of 16-bit weights [groups, rows up to a multiple of 8, inter], of 4-bit
-                                       // ones [groups, rows, inter]; a group is an expert with tokens
+  uint16_t *h;                         // workspace: of 16-bit weights [groups, 2 parts, rows up to a multiple of 8, inter],
+                                       // of 4-bit ones [groups, rows, inter]; a group is an expert with tokens
   int groups;                          // at most
   // Workspace of 4-bit weights: x and h as planes [1 or groups][planes][tokens][k], their groups' sums [1 or groups]
   // [x_groups or h_groups][tokens], what products of x are multiplied by, the largest |h| of a token, groups' tokens.
@@ -118,7 +118,7 @@ struct RoutedParams {
   Waits waits;
 };
 // Over all experts' rows of each matrix; of the down kernels gate and s_gate are down and s_down; boxes of 64 rows (down:
-// 128).  16 bits: boxes of 128 bytes, and tokens: x, or h, boxes of 128 bytes x the tokens up to a multiple of 8.  4 bits:
+// 128).  16 bits: boxes of 128 bytes, and tokens: x, or h, boxes of 128 bytes x the tokens up to a multiple of 8 (h: twice).  4 bits:
 // boxes of 64 bytes for each half of a tile, and tokens: planes, boxes of 128 bytes x routed_code_tokens' of each.
 struct RoutedMaps {
   CUtensorMap gate, up, s_gate, s_up, tokens;

@@ -36,12 +36,17 @@ __global__ void __launch_bounds__(256) routed_logits_kernel(const __grid_constan
 // Down: a tile is 128 rows; the experts' steps are shared by the CTAs of a cluster, whose sums meet in shared memory.
 
 constexpr int kTcThreads = 192, kTcRows = 128, kTcW = kTcRows * 128;
+// NC: columns of the right operand, tokens in gate and up, two for each in down
 template <int NC>
 constexpr int kTcStage = kTcW + NC * 128;
 template <int NC>
-constexpr int kTcRing = NC == 16 ? 5 : 4;  // two CTAs on an SM: the down kernel's come while the up kernel's end
+constexpr int kTcRing = NC == 16 ? 5 : NC == 32 ? 4 : 3;  // two CTAs on an SM: the down kernel's come while the up kernel's end
 template <int NC>
 constexpr size_t kTcSmem = kTcRing<NC> * kTcStage<NC> + 1024;
+
+// what the second part of a hidden value is multiplied by, so that it is a normal number where the first one is
+template <typename T>
+constexpr float kLow = std::is_same<T, __half>::value ? 0x1p11f : 0x1p8f;
 
 // NC columns of this thread's lane of an accumulator
 template <int NC>
@@ -59,7 +64,8 @@ __global__ void __launch_bounds__(kTcThreads, 2)
   __shared__ __align__(8) uint64_t full[kTcStages], empty[kTcStages], tfull[2], tempty[2], mma_done, never;
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag, issued;
-  __shared__ float sums[UP ? 2 : 1][NC * (UP ? 64 : kTcRows)];
+  constexpr int kTokens = UP ? NC : NC / 2;
+  __shared__ float sums[UP ? 2 : 1][kTokens * (UP ? 64 : kTcRows)];
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   char *ring = smem + (-smem_u32(smem) & 1023u);
   if (threadIdx.x == 0) {
@@ -90,7 +96,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
   choose_groups(p, c, reinterpret_cast<uint32_t *>(ring), UP && blockIdx.x == 0);  // (the ring is not in use yet)
   volatile int *abort_p = &abort_flag;
   const Waits &w = p.waits;
-  const int rows8 = (p.rows + 7) / 8 * 8, depth = UP ? p.hidden : p.inter, steps = (depth + 63) / 64;
+  const int rows8 = (p.rows + 7) / 8 * 8, columns = UP ? rows8 : 2 * rows8, depth = UP ? p.hidden : p.inter, steps = (depth + 63) / 64;
   const int tiles = UP ? (p.inter + 63) / 64 : 1;  // of an expert
   // UP: units of an expert's tile, one after another; otherwise one tile, and this CTA's share of all experts' steps
   const int rank = UP ? 0 : blockIdx.x % splits, tile_down = UP ? 0 : blockIdx.x / splits;
@@ -100,7 +106,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
 
   if (warp == 0) {
     // ---------------- copies ----------------
-    const uint32_t ring0 = smem_u32(ring), bytes = kTcW + rows8 * 128;
+    const uint32_t ring0 = smem_u32(ring), bytes = kTcW + columns * 128;
     RingPos<kTcStages> pos;
     int j = 0, group = UP ? 0 : first / steps, k = UP ? 0 : first % steps, unit = unit0, step = first;
     auto weights = [&](int s) {
@@ -118,7 +124,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       }
     };
     auto tokens = [&](int s, int g, int kk) {
-      tma_load_2d_one<false>(ring0 + s * kTcStage<NC> + kTcW, &maps.tokens, smem_u32(&full[s]), kk * 64, UP ? 0 : g * rows8);
+      tma_load_2d_one<false>(ring0 + s * kTcStage<NC> + kTcW, &maps.tokens, smem_u32(&full[s]), kk * 64, UP ? 0 : g * columns);
     };
     auto next = [&] {
       ++step;
@@ -192,17 +198,34 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     const int q = warp & 3, row = q * 32 + lane;
     RingPos<2> acc;
     for (int unit = unit0; unit < units; unit += unit_step, acc.next()) {
-      float v[NC];
+      float v[kTokens];
       const bool ok = (UP || first < end) && warp_wait(&tfull[acc.slot], acc.round, abort_p, w.status, w.ns);
       if (ok) {
         tc_fence_after();
-        read_accumulator<NC>(tmem + ((uint32_t)(q * 32) << 16) + acc.slot * 32, v);
+        const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + acc.slot * 32;
+        if constexpr (UP) {
+          read_accumulator<NC>(at, v);
+        } else if constexpr (NC == 16) {  // eight tokens: both parts in one reading
+          float both[16];
+          read_accumulator<16>(at, both);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = fmaf(both[8 + i], 1.f / kLow<T>, both[i]);
+        } else {
+          read_accumulator<kTokens>(at, v);
+#pragma unroll
+          for (int i = 0; i < kTokens; i += 16) {
+            float low[16];
+            read_accumulator<16>(at + rows8 + i, low);  // (past the last token what nobody reads)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[i + j] = fmaf(low[j], 1.f / kLow<T>, v[i + j]);
+          }
+        }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&tempty[acc.slot]);
       } else {
 #pragma unroll
-        for (int i = 0; i < NC; ++i) v[i] = 0.f;
+        for (int i = 0; i < kTokens; ++i) v[i] = 0.f;
       }
       if constexpr (UP) {
         float *u = sums[acc.slot];
@@ -215,19 +238,26 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         const uint32_t mask = c.group_mask[group];
         const float weight = weight_of(p, c, e, lane);  // this lane's token's
         if (q < 2) {
-          uint16_t *h = p.h + (long long)group * rows8 * p.inter + at;
+          uint16_t *h = p.h + (long long)group * (2 * rows8) * p.inter + at;
 #pragma unroll
           for (int t = 0; t < NC; ++t) {
             if (t >= p.rows) break;
-            T out = from_f32<T>(0.f);
-            if (mask >> t & 1)  // rounded to 16 bits as the tensor cores' operand, as the gated block does
-              out = from_f32<T>(act_value(p.act, v[t]) * u[t * 64 + row] * __shfl_sync(0xffffffffu, weight, t));
-            if (at < p.inter) h[(long long)t * p.inter] = *reinterpret_cast<const uint16_t *>(&out);
+            T out = from_f32<T>(0.f), low = out;
+            if (mask >> t & 1) {
+              const float x = act_f32(p.act, v[t]) * u[t * 64 + row] * __shfl_sync(0xffffffffu, weight, t);
+              out = from_f32<T>(x);
+              const float rest = x - to_f32(out);  // (an infinity has none)
+              if (fabsf(rest) < INFINITY) low = from_f32<T>(rest * kLow<T>);
+            }
+            if (at < p.inter) {
+              h[(long long)t * p.inter] = *reinterpret_cast<const uint16_t *>(&out);
+              h[(long long)(rows8 + t) * p.inter] = *reinterpret_cast<const uint16_t *>(&low);
+            }
           }
         }
       } else {
 #pragma unroll
-        for (int t = 0; t < NC; ++t)
+        for (int t = 0; t < kTokens; ++t)
           if (t < p.rows) sums[0][t * kTcRows + row] = v[t];
       }
     }
@@ -268,7 +298,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
   }
 }
 
-template <typename T, int NC>
+template <typename T, int NC, int DOWN>
 cudaError_t tc_launch(const RoutedParams &p, const RoutedMaps &maps, const RoutedMaps &down, int num_sms, cudaStream_t st) {
   static std::atomic<unsigned long long> done[2];
   cudaError_t e = allow_smem((const void *)routed_tc_kernel<true, T, NC>, kTcSmem<NC>, done[0]);
@@ -284,12 +314,13 @@ cudaError_t tc_launch(const RoutedParams &p, const RoutedMaps &maps, const Route
   // as many CTAs to a tile as run at one time, two on an SM (of clusters of 8, 4 and 2 on 152 SMs 32, 72 and 150)
   const int tiles = (p.hidden + kTcRows - 1) / kTcRows;
   const int splits = tiles <= num_sms * 32 / 152 ? 8 : tiles <= num_sms * 72 / 152 ? 4 : tiles <= num_sms * 150 / 152 ? 2 : 1;
-  return launch_clusters(routed_tc_kernel<false, T, NC>, kTcSmem<NC>, done[1], tiles, splits, kTcThreads, st, p, down, splits);
+  return launch_clusters(routed_tc_kernel<false, T, DOWN>, kTcSmem<DOWN>, done[1], tiles, splits, kTcThreads, st, p, down, splits);
 }
 
 template <typename T>
 cudaError_t routed_typed(const RoutedParams &p, const RoutedMaps &maps, const RoutedMaps &down, int num_sms, cudaStream_t st) {
-  return p.rows <= 16 ? tc_launch<T, 16>(p, maps, down, num_sms, st) : tc_launch<T, 32>(p, maps, down, num_sms, st);
+  if (p.rows <= 8) return tc_launch<T, 16, 16>(p, maps, down, num_sms, st);
+  return p.rows <= 16 ? tc_launch<T, 16, 32>(p, maps, down, num_sms, st) : tc_launch<T, 32, 64>(p, maps, down, num_sms, st);
 }
 
 }  // namespace

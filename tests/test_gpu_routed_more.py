@@ -37,3 +37,65 @@ def test_tokens_of_any_magnitude(power, inverse):
     if power + inverse == 0:  # every step is exact up to the powers
         assert all(torch.equal(a, b) for a, b in zip(got, m.routed_ffn(x, router, *ws, 3, bias=bias)))
     tr.check(got, x * 2.0 ** power, router, ws2, 3, None, "silu", bias)
+
+
+def fine_layer(rows, bits, dtype, down=1.0, inter=32):
+    """Small sums, so that what the hidden values lose shows: one expert of each token."""
+    x, router, ws, _, _ = tr.layer(rows, 64, inter, 8, 0, bits, 32, True, dtype, True, False, seed=3)
+    if bits == 16:
+        return x, router, [*ws[:2], ws[2] * down]
+    return x, router, [*ws[:2], ws[2]._replace(scales=ws[2].scales * down)]
+
+
+def fine_room(x, router, ws, index, weight, lost):
+    """y in 64 bits, and the room that its parts leave: lost(h, the token's largest |h|) of the hidden values.  Sums of 64
+    exact products in f32, four steps of 16 with a unit of 2^-23 each and as much again where planes and groups are joined:
+    2^-20 of the sum of magnitudes."""
+    want = torch.zeros(len(x), ws[2].scales.shape[1] if isinstance(ws[2], m.Int4) else ws[2].shape[1], device="cuda",
+                       dtype=torch.float64)
+    room, xd = torch.zeros_like(want), x.double()
+    for e in index.unique().tolist():
+        g, u, d = ((t4.values((w.codes[e], w.scales[e], w.zeros[e] if w.zeros is not None else None), w.group)
+                    if isinstance(w, m.Int4) else w[e].double()) for w in ws)
+        by = (weight.double() * (index == e)).sum(1, keepdim=True)
+        a, b = xd @ g.T, xd @ u.T
+        da, db = (2.0 ** -20 * (xd.abs() @ v.abs().T) for v in (g, u))
+        s = torch.nn.functional.silu(a)
+        h = by * s * b
+        dh = by * (1.13 * b.abs() * da + (s.abs() + 1.13 * da) * db) + 2.0 ** -19 * h.abs()
+        dh = dh + lost(h.abs() + dh, (h.abs() + dh).amax(1, keepdim=True))
+        want += h @ d.T
+        room += (dh + 2.0 ** -20 * h.abs()) @ d.abs().T
+    return want, (room + torch.finfo(x.dtype).eps / 2 * want.abs()) * (1 + 2.0 ** -10)
+
+
+# What the hidden values lose: as 16-bit numbers of two parts half a step of the second, 2^-18 of a value (f16: 2^-22, and
+# of subnormal numbers 2^-25 2^-11); as three planes half a step of the third, 2^-12 of a value or 2^-27 of the largest.
+LOST = {(16, BF16): lambda h, most: 2.0 ** -18 * h, (16, F16): lambda h, most: 2.0 ** -22 * h + 2.0 ** -36,
+        (4, BF16): lambda h, most: torch.maximum(2.0 ** -12 * h, 2.0 ** -27 * most),
+        (4, F16): lambda h, most: torch.maximum(2.0 ** -12 * h, 2.0 ** -27 * most)}
+
+
+@pytest.mark.parametrize("rows", [1, 7, 8, 9, 16, 17, 23, 24, 25, 32])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("bits", [16])
+def test_hidden_values_keep_more_than_the_type(bits, dtype, rows):
+    x, router, ws = fine_layer(rows, bits, dtype)
+    y, index, weight = m.routed_ffn(x, router, *ws, 1)
+    want, room = fine_room(x, router, ws, index, weight, LOST[bits, dtype])
+    assert ((y.double() - want).abs() <= room + (2.0 ** -25 if dtype == F16 else 0)).all()
+
+
+@pytest.mark.parametrize("bits", [16])
+def test_hidden_values_below_f16s_normal_numbers(bits):
+    """Unnormalised weights of 0.004 take the hidden values to 10^-5, where a number of f16 has a few bits; large down
+    matrices bring them back."""
+    x, router, ws = fine_layer(20, bits, F16, down=64.0)
+    x, router = x / 16, torch.cat([router[:8] * 0.01, torch.zeros(248, 64, device="cuda")])
+    many = [torch.cat([w] * 32) if bits == 16 else w._replace(codes=torch.cat([w.codes] * 32), scales=torch.cat([w.scales] * 32),
+                                                              zeros=torch.cat([w.zeros] * 32)) for w in ws]
+    y, index, weight = m.routed_ffn(x, router, *many, 1, score="softmax", normalise=False)
+    assert (weight < 0.005).all()
+    want, room = fine_room(x, router, many, index, weight, LOST[bits, F16])
+    assert want.abs().mean() > 2.0 ** -14  # (normal numbers again)
+    assert ((y.double() - want).abs() <= room + 2.0 ** -25).all()
