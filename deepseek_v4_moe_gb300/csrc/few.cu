@@ -245,6 +245,7 @@ int64_t routed_groups(const moe_ffn_routed_args *a) {
 struct RoutedSpace {
   int64_t h, x_planes, h_planes, x_sums, h_sums, back, h_max, masks, bytes;
   int tokens, planes, x_groups, h_groups;
+  int x_halves, h_halves;  // of a tile
 };
 RoutedSpace routed_space(const moe_ffn_routed_args *a) {
   RoutedSpace s = {};
@@ -256,15 +257,17 @@ RoutedSpace routed_space(const moe_ffn_routed_args *a) {
   };
   const int64_t R = a->rows, I = a->inter, H = a->hidden, G = routed_groups(a);
   part(R * a->experts * 4);  // the logits
-  s.h = part(G * (a->bits == 4 ? R : (R + 7) / 8 * 16) * I * 2);
+  s.h = part(a->bits == 4 ? G * R * I * 4 : G * ((R + 7) / 8 * 16) * I * 2);
   if (a->bits == 4) {
     s.tokens = moe::routed_code_tokens(a->rows);
     s.planes = a->type == MOE_FFN_F16 ? 3 : 2;
-    const int columns = 128 * moe::code_halves(s.tokens, s.planes, 128 / a->group);  // of a tile
-    s.x_groups = (int)((H + columns - 1) / columns * (columns / a->group));
-    s.h_groups = (int)((I + columns - 1) / columns * (columns / a->group));
+    s.x_halves = moe::code_halves(s.tokens, s.planes, 128 / a->group);
+    s.h_halves = moe::code_halves(s.tokens, moe::kHiddenPlanes, 128 / a->group);
+    auto groups = [&](int64_t k, int columns) { return (int)((k + columns - 1) / columns * (columns / a->group)); };
+    s.x_groups = groups(H, 128 * s.x_halves);
+    s.h_groups = groups(I, 128 * s.h_halves);
     s.x_planes = part(s.planes * s.tokens * H);
-    s.h_planes = part(G * s.planes * s.tokens * I);
+    s.h_planes = part(G * moe::kHiddenPlanes * s.tokens * I);
     s.x_sums = part((int64_t)s.x_groups * s.tokens * 4);
     s.h_sums = part(G * s.h_groups * s.tokens * 4);
     s.back = part(R * 4);
@@ -364,6 +367,7 @@ extern "C" int moe_ffn_routed_forward(const moe_ffn_routed_args *a, void *stream
   char *ws = static_cast<char *>(a->workspace);
   p.logits = reinterpret_cast<float *>(ws);
   p.h = reinterpret_cast<uint16_t *>(ws + space.h);
+  p.h32 = reinterpret_cast<float *>(ws + space.h);
   p.groups = (int)routed_groups(a);
   DeviceSide dev;
   if ((rc = device_side(who, &dev))) return rc;
@@ -371,10 +375,9 @@ extern "C" int moe_ffn_routed_forward(const moe_ffn_routed_args *a, void *stream
   moe::RoutedMaps maps = {}, down = {};
   CUtensorMap *to[] = {&maps.gate, &maps.up, &down.gate, &maps.s_gate, &maps.s_up, &down.s_gate};
   bool ok = true;
-  const int halves = a->bits == 4 ? moe::code_halves(space.tokens, space.planes, 128 / a->group) : 0;
   for (int i = 0; i < (S ? 6 : 3); ++i) {
     const int64_t count = i < 3 ? E : S, n = m[i].n, k = m[i].k;
-    const int box = i % 3 == 2 ? 128 : 64;
+    const int box = i % 3 == 2 ? 128 : 64, halves = i % 3 == 2 ? space.h_halves : space.x_halves;
     ok = ok && (a->bits == 4 ? encode_map(to[i], m[i].w, 1, k / 2, count * n, k / 2, box, 64 * halves)
                              : encode_map(to[i], m[i].w, 2, k, count * n, k, box));
   }
@@ -396,9 +399,9 @@ extern "C" int moe_ffn_routed_forward(const moe_ffn_routed_args *a, void *stream
   p.masks = reinterpret_cast<uint32_t *>(ws + space.masks);
   p.x_groups = space.x_groups;
   p.h_groups = space.h_groups;
-  const int rows = space.planes * space.tokens;
+  const int rows = space.planes * space.tokens, h_rows = moe::kHiddenPlanes * space.tokens;
   if (!ok || !encode_map(&maps.tokens, p.x_planes, 1, H, rows, H, rows) ||
-      !encode_map(&down.tokens, p.h_planes, 1, I, (int64_t)p.groups * rows, I, rows))
+      !encode_map(&down.tokens, p.h_planes, 1, I, (int64_t)p.groups * h_rows, I, h_rows))
     return fail(MOE_FFN_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed", who);
   return launched(who, moe::launch_routed_int4(p, maps, down, f16, sms, st));
 }

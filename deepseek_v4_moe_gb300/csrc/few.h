@@ -90,6 +90,7 @@ constexpr int kRoutedRows = 32;     // tokens of a call: a bit each in a group's
 constexpr int kRoutedExperts = 512;
 constexpr int kRoutedTopK = 8;
 constexpr int kRoutedShared = 8;
+constexpr int kHiddenPlanes = 3;    // of the 4-bit layer's hidden values, in either type
 
 struct RoutedParams {
   int rows, hidden, inter, experts, top_k, shared;
@@ -106,10 +107,11 @@ struct RoutedParams {
   int32_t *indices;                    // [rows, top_k] or none
   float *weights;
   float *logits;                       // workspace: [rows, experts]
-  uint16_t *h;                         // workspace: of 16-bit weights [groups, 2 parts, rows up to a multiple of 8, inter],
-                                       // of 4-bit ones [groups, rows, inter]; a group is an expert with tokens
+  // The hidden values, of groups: experts with tokens.
+  uint16_t *h;                         // workspace: of 16-bit weights [groups, 2 parts, rows up to a multiple of 8, inter]
+  float *h32;                          // workspace: of 4-bit weights [groups, rows, inter]
   int groups;                          // at most
-  // Workspace of 4-bit weights: x and h as planes [1 or groups][planes][tokens][k], their groups' sums [1 or groups]
+  // Workspace of 4-bit weights: x and h32 as planes [1 or groups][planes][tokens][k], their groups' sums [1 or groups]
   // [x_groups or h_groups][tokens], what products of x are multiplied by, the largest |h| of a token, groups' tokens.
   uint2 *x_planes, *h_planes;
   float *x_sums, *h_sums, *back;

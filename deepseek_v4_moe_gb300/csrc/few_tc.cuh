@@ -111,6 +111,17 @@ __device__ __forceinline__ float split8(const float (&v)[8], float scale, uint2 
   return sum;
 }
 
+// eight values in 16-byte pieces (a workspace is aligned to those)
+template <typename T>
+__device__ __forceinline__ void load_pieces(const T *x, float (&v)[8]) {
+  if constexpr (std::is_same<T, float>::value) {
+    const float4 a = reinterpret_cast<const float4 *>(x)[0], b = reinterpret_cast<const float4 *>(x)[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else {
+    load_eight<T, true>(x, 0, 1, 8, v);
+  }
+}
+
 // A row's planes (out, `apart` between two planes) and groups' sums, by a CTA of 256: k8 eights of columns of x, scaled;
 // `groups` of `per` eights up to the last tile's, each sum `tokens` floats from the one before.  x none: zeros.
 template <typename T, int PLANES>
@@ -123,7 +134,7 @@ __device__ __forceinline__ void split_row(const T *x, float scale, int k8, int g
       uint2 o[PLANES] = {};
       if (x) {
         float v[8];
-        load_eight<T, true>(x + 8 * i, 0, 1, 8, v);
+        load_pieces(x + 8 * i, v);
         sum = split8<PLANES>(v, scale, o);
       }
 #pragma unroll
@@ -140,7 +151,7 @@ __device__ __forceinline__ uint32_t row_max(const T *x, int k8) {
   uint32_t m = 0;
   for (int i = threadIdx.x; i < k8; i += 256) {
     float v[8];
-    load_eight<T, true>(x + 8 * i, 0, 1, 8, v);
+    load_pieces(x + 8 * i, v);
 #pragma unroll
     for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(v[e]) & 0x7FFFFFFFu);
   }

@@ -1,8 +1,8 @@
 // The routed layer with 4-bit weights on the FP8 tensor cores (sm_103a; few_tc.cuh), in four kernels:
 //
 //   route   l = x Wr^T, and x as planes
-//   up      each CTA chooses the experts from l; h = weight act(x Wg_e^T) (x Wu_e^T), in 16 bits
-//   split   h as planes
+//   up      each CTA chooses the experts from l; h = weight act(x Wg_e^T) (x Wu_e^T), in f32
+//   split   h as planes: three, so that 12 significant bits are left of either type's products
 //   down    y = sum over the experts of h Wd_e^T
 //
 // Bound by the chosen experts' codes on their way from memory and through registers into operands: each is read once, for
@@ -13,8 +13,10 @@
 // latencies are the most: gate and up have 224 strips for 152 SMs.  32 tokens 491 us (263).
 //
 // A token's h has one power of two for all of its experts, from the largest magnitude among them (an atomic maximum: of
-// any order the same), so that their products can be added as they are: what is lost of an expert's h is below 2^-22 of
-// the token's largest (f16: 2^-27), and the sum that it goes to holds that one.
+// any order the same), so that their products can be added as they are: what is lost of an expert's h is below 2^-12 of it
+// or 2^-27 of the token's largest, and the sum that it goes to holds that one.  It has three planes in bf16 too: h rounded
+// to 16 bits, in two planes, left the layer off by 0.0024 in 2-norm where y's rounding leaves 0.0017 (16 tokens 230 us for
+// 231, 32 tokens in groups of 32 1210 for 1440).
 #include "few_tc.cuh"
 #include "kernels.h"
 #include "routed.cuh"
@@ -44,7 +46,6 @@ __global__ void __launch_bounds__(256) routed_planes_kernel(const __grid_constan
 }
 
 // a CTA for each row of h: a token of an expert; zeros where it has not chosen it
-template <typename T, int PLANES>
 __global__ void __launch_bounds__(256) routed_split_kernel(const __grid_constant__ RoutedParams p, int tokens) {
   const int token = blockIdx.x, group = blockIdx.y, k8 = p.inter / 8;
   pdl_wait();
@@ -52,10 +53,10 @@ __global__ void __launch_bounds__(256) routed_split_kernel(const __grid_constant
   pdl_trigger();
   const uint32_t mask = p.masks[group];
   if (!mask) return;  // no such group
-  const T *h = reinterpret_cast<const T *>(p.h) + ((size_t)group * p.rows + token) * p.inter;
-  split_row<T, PLANES>(mask >> token & 1 ? h : nullptr, two_to(plane_exponent(__ldcg(p.h_max + token))), k8, p.h_groups,
-                       1 << (p.gate.group_shift - 3), p.h_planes + ((size_t)group * PLANES * tokens + token) * k8, (size_t)tokens * k8,
-                       p.h_sums + (size_t)group * p.h_groups * tokens + token, tokens);
+  const float *h = p.h32 + ((size_t)group * p.rows + token) * p.inter;
+  split_row<float, kHiddenPlanes>(mask >> token & 1 ? h : nullptr, two_to(plane_exponent(__ldcg(p.h_max + token))), k8, p.h_groups,
+                                  1 << (p.gate.group_shift - 3), p.h_planes + ((size_t)group * kHiddenPlanes * tokens + token) * k8,
+                                  (size_t)tokens * k8, p.h_sums + (size_t)group * p.h_groups * tokens + token, tokens);
 }
 
 // Up: a unit is 64 rows of a group's gate and 64 of its up matrix.  Down: one unit, 128 rows of all groups' matrices, whose
@@ -210,7 +211,7 @@ struct LayerJob {
       if (row >= 64) return;
       const int at = (a.unit - a.group * strips) * 64 + row, e = c.group_expert[a.group];
       const uint32_t mask = c.group_mask[a.group] >> t0;
-      uint16_t *h = p.h + ((size_t)a.group * p.rows + t0) * p.inter + at;
+      float *h = p.h32 + ((size_t)a.group * p.rows + t0) * p.inter + at;
       const float weight = weight_of(p, c, e, threadIdx.x & 31);  // this lane's token's
 #pragma unroll
       for (int t = 0; t < C::kMine; ++t) {
@@ -219,10 +220,9 @@ struct LayerJob {
         const float by = __shfl_sync(0xffffffffu, back, t0 + t), w = __shfl_sync(0xffffffffu, weight, t0 + t);
         uint32_t size = 0u;
         if (at < p.inter) {
-          // rounded to 16 bits as the 16-bit layer does
-          const T out = from_f32<T>(act_value(p.act, acc[t] * 512.f * by) * (u[t * 64 + row] * 512.f * by) * w);
-          h[(size_t)t * p.inter] = *reinterpret_cast<const uint16_t *>(&out);
-          size = __float_as_uint(to_f32(out)) & 0x7FFFFFFFu;
+          const float out = act_value(p.act, acc[t] * 512.f * by) * (u[t * 64 + row] * 512.f * by) * w;
+          h[(size_t)t * p.inter] = out;
+          size = __float_as_uint(out) & 0x7FFFFFFFu;
         }
         size = __reduce_max_sync(0xffffffffu, size);
         if (row % 32 == 0) atomicMax(p.h_max + t0 + t, size);
@@ -285,21 +285,21 @@ template <typename T, int TOKENS, int GROUPS>
 cudaError_t codes_launch(const RoutedParams &p, const RoutedMaps &maps, const RoutedMaps &down, int num_sms, cudaStream_t st) {
   constexpr int PLANES = std::is_same<T, __half>::value ? 3 : 2;
   using C = CodeCfg<TOKENS, PLANES, GROUPS>;
-  constexpr size_t smem = C::kRing + 1024;
+  using D = CodeCfg<TOKENS, kHiddenPlanes, GROUPS>;  // of the down kernel
   static std::atomic<unsigned long long> done[2];
-  cudaError_t e = allow_smem((const void *)routed_codes_kernel<true, T, TOKENS, PLANES, GROUPS>, smem, done[0]);
+  cudaError_t e = allow_smem((const void *)routed_codes_kernel<true, T, TOKENS, PLANES, GROUPS>, C::kRing + 1024, done[0]);
   if (e == cudaSuccess)
     e = launch_pdl(p.router_f32 ? routed_planes_kernel<T, float, PLANES> : routed_planes_kernel<T, T, PLANES>, dim3(route_ctas(p) + kRouteTokens, route_turns(p)),
                    dim3(256), 0, st, p, TOKENS);
   const long long units = (long long)p.groups * ((p.inter + 63) / 64);
   if (e == cudaSuccess)
     e = launch_pdl(routed_codes_kernel<true, T, TOKENS, PLANES, GROUPS>, dim3((unsigned)(units < num_sms ? units : num_sms)),
-                   dim3(C::kThreads), smem, st, p, maps, 1);
-  if (e == cudaSuccess) e = launch_pdl(routed_split_kernel<T, PLANES>, dim3(p.rows, p.groups), dim3(256), 0, st, p, TOKENS);
+                   dim3(C::kThreads), C::kRing + 1024, st, p, maps, 1);
+  if (e == cudaSuccess) e = launch_pdl(routed_split_kernel, dim3(p.rows, p.groups), dim3(256), 0, st, p, TOKENS);
   if (e != cudaSuccess) return e;
   const int tiles = (p.hidden + kCodeRows - 1) / kCodeRows, splits = code_splits(tiles, num_sms);
-  return launch_code_clusters(routed_codes_kernel<false, T, TOKENS, PLANES, GROUPS>, smem, done[1], dim3(tiles * splits), C::kThreads, splits,
-                              st, p, down, splits);
+  return launch_code_clusters(routed_codes_kernel<false, T, TOKENS, kHiddenPlanes, GROUPS>, D::kRing + 1024, done[1], dim3(tiles * splits),
+                              D::kThreads, splits, st, p, down, splits);
 }
 
 template <typename T, int GROUPS>

@@ -85,9 +85,10 @@ def routed_ffn(x: torch.Tensor, w_router: torch.Tensor, w_gate: Weights, w_up: W
     [experts]; ``w_gate``, ``w_up`` [experts, inter, hidden] and ``w_down`` [experts, hidden, inter], tensors of x's type
     or all :class:`Int4` of one group; ``shared``: the same three of the shared experts, [inter, hidden] for one or
     [count, inter, hidden].  hidden and inter are multiples of 8 (32 with Int4).  Without ``normalise`` the weight is
-    route_scale * s.  4-bit experts take x and their hidden values in planes as :func:`int4_matmul` does; a token's hidden
-    values have one power of two for all of its experts.  Weights are finite: what is not in a chosen expert's reaches all
-    tokens of the call.  Returns (y [rows, hidden], indices int32 [rows, top_k], weights float32 [rows, top_k]).
+    route_scale * s.  The hidden values go into the down projection as two numbers of x's type; with 4-bit experts x goes
+    through planes as :func:`int4_matmul`'s does and the hidden values through three, 12 significant bits, with one power
+    of two for all of a token's experts.  Weights are finite: what is not in a chosen expert's reaches all tokens of the
+    call.  Returns (y [rows, hidden], indices int32 [rows, top_k], weights float32 [rows, top_k]).
     """
     if score not in SCORES:
         raise ValueError(f"score must be one of {sorted(SCORES)}")

@@ -519,8 +519,9 @@ int moe_ffn_int4_matmul(const moe_ffn_int4_matmul_args *a, void *stream);
  *       E(x) = (act(x gate^T) * (x up^T)) down^T
  * weight * act(g) * u (a shared expert's without a weight) goes into the down projection as two numbers of the operand type:
  * 16 significant bits (f16: 22, but no more than 2^-36, and its range).
- * With bits 4 it is rounded to the operand type, and both operands go through planes as int4_matmul's do; those of the down
- * projection have one power of two for all of a token's experts.  A token that is not finite, or whose hidden values are not, gives NaN; the others do not
+ * With bits 4 x goes through planes as int4_matmul's does, and the hidden values from f32 into three: 12 significant bits down
+ * to 2^-15 of the largest, those of a token's experts together, and off by at most 2^-27 of it below.
+ * A token that is not finite, or whose hidden values are not, gives NaN; the others do not
  * see it.  Weights are finite: an infinity or a NaN of a chosen expert reaches all tokens of the call. */
 #define MOE_FFN_SCORE_SIGMOID 0
 #define MOE_FFN_SCORE_SOFTMAX 1

@@ -1,5 +1,6 @@
 """The routed layer without a handle, further: the choice's place in shared memory, magnitudes at the types' ends, the
 precision of the hidden values, weights that are not finite, and the choice of every token."""
+import ctypes
 import math
 
 import pytest
@@ -8,6 +9,7 @@ import torch
 import deepseek_v4_moe_gb300 as m
 import test_gpu_int4 as t4
 import test_gpu_routed as tr
+from deepseek_v4_moe_gb300 import _lib
 
 pytestmark = pytest.mark.gpu
 
@@ -78,7 +80,7 @@ LOST = {(16, BF16): lambda h, most: 2.0 ** -18 * h, (16, F16): lambda h, most: 2
 
 @pytest.mark.parametrize("rows", [1, 7, 8, 9, 16, 17, 23, 24, 25, 32])
 @pytest.mark.parametrize("dtype", [BF16, F16])
-@pytest.mark.parametrize("bits", [16])
+@pytest.mark.parametrize("bits", [16, 4])
 def test_hidden_values_keep_more_than_the_type(bits, dtype, rows):
     x, router, ws = fine_layer(rows, bits, dtype)
     y, index, weight = m.routed_ffn(x, router, *ws, 1)
@@ -86,7 +88,7 @@ def test_hidden_values_keep_more_than_the_type(bits, dtype, rows):
     assert ((y.double() - want).abs() <= room + (2.0 ** -25 if dtype == F16 else 0)).all()
 
 
-@pytest.mark.parametrize("bits", [16])
+@pytest.mark.parametrize("bits", [16, 4])
 def test_hidden_values_below_f16s_normal_numbers(bits):
     """Unnormalised weights of 0.004 take the hidden values to 10^-5, where a number of f16 has a few bits; large down
     matrices bring them back."""
@@ -99,3 +101,23 @@ def test_hidden_values_below_f16s_normal_numbers(bits):
     want, room = fine_room(x, router, many, index, weight, LOST[bits, F16])
     assert want.abs().mean() > 2.0 ** -14  # (normal numbers again)
     assert ((y.double() - want).abs() <= room + 2.0 ** -25).all()
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+def test_a_workspace_aligned_to_16_bytes(cuda_lib, bits):
+    rows, hidden, inter, experts = 9, 256, 96, 10
+    x, router, ws, _, _ = tr.layer(rows, hidden, inter, experts, 0, bits, 32, True, BF16, False, False)
+    want = m.routed_ffn(x, router, *ws, 3)
+    y, index = torch.empty_like(x), torch.empty(rows, 3, device="cuda", dtype=torch.int32)
+    mats = [_lib.MoeFfnMatrices(*(t.data_ptr() for t in w[:3])) if bits == 4 else _lib.MoeFfnMatrices(w.data_ptr(), None, None)
+            for w in ws]
+    a = _lib.MoeFfnRoutedArgs(rows=rows, hidden=hidden, inter=inter, experts=experts, top_k=3, shared=0, type=_lib.TYPE_BF16,
+                              router_type=_lib.TYPE_BF16, bits=bits, group=32, score=_lib.SCORES["sigmoid"], normalise=1,
+                              activation=0, route_scale=1.0, x=x.data_ptr(), ld_x=hidden, router=router.data_ptr(),
+                              gate=mats[0], up=mats[1], down=mats[2], y=y.data_ptr(), ld_y=hidden, indices=index.data_ptr())
+    need = cuda_lib.moe_ffn_routed_workspace(ctypes.byref(a))
+    space = torch.empty(need + 272, device="cuda", dtype=torch.uint8)
+    a.workspace, a.workspace_bytes = (space.data_ptr() + 255) // 256 * 256 + 16, need
+    stream = torch.cuda.current_stream().cuda_stream
+    assert cuda_lib.moe_ffn_routed_forward(ctypes.byref(a), stream) == 0, cuda_lib.moe_ffn_last_error(None)
+    assert torch.equal(y, want[0]) and torch.equal(index, want[1])
