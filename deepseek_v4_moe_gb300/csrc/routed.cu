@@ -55,6 +55,37 @@ __device__ __forceinline__ void read_accumulator(uint32_t at, float (&v)[NC]) {
   for (int i = 0; i < NC; i += 16) tmem_ld16(at + i, reinterpret_cast<float(&)[16]>(v[i]));
 }
 
+// A result from the token's own experts alone, by a warp: see the down kernel's end.  (32 tokens of 64 experts of 4096 x 2048
+// with a NaN in each row of the shared expert's matrix, so that every result comes here and stays NaN: 3.2 ms, for 0.48.)
+template <typename T>
+__device__ __noinline__ float own_experts(const RoutedParams &p, const Choice &c, int rows8, int token, int n) {
+  auto eight = [](const T *at, float (&v)[8]) {
+    const uint4 w = __ldcg(reinterpret_cast<const uint4 *>(at));
+    unpack2(w.x, v[0], v[1], at);
+    unpack2(w.y, v[2], v[3], at);
+    unpack2(w.z, v[4], v[5], at);
+    unpack2(w.w, v[6], v[7], at);
+  };
+  float sum = 0.f;
+  for (int g = 0; g < c.groups; ++g) {
+    if (!(c.group_mask[g] >> token & 1)) continue;
+    const int e = c.group_expert[g];
+    const FewMatrix &m = e >= p.experts ? p.s_down : p.down;
+    const T *w = static_cast<const T *>(m.w) + ((long long)(e >= p.experts ? e - p.experts : e) * p.hidden + n) * p.inter;
+    const T *h = reinterpret_cast<const T *>(p.h) + ((long long)g * (2 * rows8) + token) * p.inter;
+    for (int k = threadIdx.x % 32 * 8; k < p.inter; k += 256) {
+      float a[8], b[8], low[8];
+      eight(w + k, a);
+      eight(h + k, b);
+      eight(h + (long long)rows8 * p.inter + k, low);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum = fmaf(a[i], fmaf(low[i], 1.f / kLow<T>, b[i]), sum);
+    }
+    if (__any_sync(0xffffffffu, sum != sum)) break;  // its own
+  }
+  return warp_sum(sum);
+}
+
 template <bool UP, typename T, int NC>
 __global__ void __launch_bounds__(kTcThreads, 2)
     routed_tc_kernel(const __grid_constant__ RoutedParams p, const __grid_constant__ RoutedMaps maps, int splits) {
@@ -275,18 +306,26 @@ __global__ void __launch_bounds__(kTcThreads, 2)
   if constexpr (!UP) {
     // the CTAs' sums in the order of their ranks, a part of the rows by each
     if (splits > 1) cluster_sync();
-    const int part = kTcRows / splits, row0 = rank * part;
-    for (int i = threadIdx.x; i < part * p.rows; i += kTcThreads) {
-      const int row = row0 + i % part, t = i / part, at = tile_down * kTcRows + row;
+    // An infinity or a NaN of an expert's matrix is NaN as 0 times it for the tokens that have not chosen it: such results
+    // are formed again.  (Without one this is a comparison for each result.)
+    const int part = kTcRows / splits, row0 = rank * part, count = part * p.rows;
+    for (int i0 = 0; i0 < count; i0 += kTcThreads) {
+      const int i = i0 + threadIdx.x, row = row0 + i % part, t = i / part, at = tile_down * kTcRows + row;
+      const bool in = i < count && at < p.hidden;
       float v = 0.f, x[8];
 #pragma unroll
       for (int r = 0; r < 8; ++r)  // all loads before the first sum
-        if (r < splits)
+        if (in && r < splits)
           asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x[r]) : "r"(in_cta(&sums[0][t * kTcRows + row], r)) : "memory");
 #pragma unroll
       for (int r = 0; r < 8; ++r)
-        if (r < splits) v += x[r];
-      if (at < p.hidden) static_cast<T *>(p.y)[t * p.ld_y + at] = from_f32<T>(v);
+        if (in && r < splits) v += x[r];
+      for (unsigned again = __ballot_sync(0xffffffffu, v != v); again; again &= again - 1) {
+        const int from = __ffs(again) - 1;
+        const float own = own_experts<T>(p, c, rows8, __shfl_sync(0xffffffffu, t, from), __shfl_sync(0xffffffffu, at, from));
+        if (lane == from) v = own;
+      }
+      if (in) static_cast<T *>(p.y)[t * p.ld_y + at] = from_f32<T>(v);
     }
     if (splits > 1) cluster_sync();
   } else {

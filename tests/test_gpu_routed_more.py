@@ -121,3 +121,48 @@ def test_a_workspace_aligned_to_16_bytes(cuda_lib, bits):
     stream = torch.cuda.current_stream().cuda_stream
     assert cuda_lib.moe_ffn_routed_forward(ctypes.byref(a), stream) == 0, cuda_lib.moe_ffn_last_error(None)
     assert torch.equal(y, want[0]) and torch.equal(index, want[1])
+
+
+def spoil(w, e, row, column, value):
+    """A value of expert e's matrix, or in 4 bits the scale of its group."""
+    if isinstance(w, m.Int4):
+        w.scales[e, row, column // w.group] = value
+    else:
+        w[e, row, column] = value
+
+
+@pytest.mark.parametrize("rows,hidden,inter,shared", [(20, 256, 160, 1), (5, 4096, 64, 0), (32, 544, 96, 2), (2, 32, 32, 1)])
+@pytest.mark.parametrize("bits", [16])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_weights_that_are_not_finite_reach_the_tokens_that_chose_them(rows, hidden, inter, shared, bits, dtype):
+    """Infinities and NaN in one expert: tokens of the others are as without them, up to the order of their sums."""
+    x, router, ws, sh, _ = tr.layer(rows, hidden, inter, 6, shared, bits, 32, True, dtype, False, False)
+    clean = m.routed_ffn(x, router, *ws, 2, shared=sh)
+    bad = clean[1][0, 0].item()
+    has = (clean[1] == bad).any(1)
+    others = [w._replace(scales=w.scales.clone()) if bits == 4 else w.clone() for w in ws]
+    spoil(others[2], bad, 3, 5, math.inf)
+    spoil(others[2], bad, hidden - 1, inter - 1, math.nan)
+    y, index, weight = m.routed_ffn(x, router, *others, 2, shared=sh)
+    assert torch.equal(index, clean[1]) and torch.equal(weight, clean[2])
+    assert not torch.isfinite(y[has][:, [3, hidden - 1]]).any() and has.any()
+    rest = [c for c in range(hidden) if c not in (3, hidden - 1)]
+    assert torch.equal(y[:, rest], clean[0][:, rest])
+    if (~has).any():
+        tr.check((y[~has], index[~has], weight[~has]), x[~has], router, ws, 2, sh, "silu")
+    # a row of gate or up: all of y, of the expert's tokens alone
+    spoil(others[1], bad, 7, 9, -math.inf)
+    y, _, _ = m.routed_ffn(x, router, *others, 2, shared=sh)
+    assert not torch.isfinite(y[has]).any()
+    if (~has).any():
+        tr.check((y[~has], index[~has], weight[~has]), x[~has], router, ws, 2, sh, "silu")
+
+
+def test_weights_that_are_not_finite_in_a_shared_expert_reach_all():
+    for bits in (16, 4):
+        x, router, ws, sh, _ = tr.layer(9, 256, 96, 6, 1, bits, 64, False, BF16, False, False)
+        clean = m.routed_ffn(x, router, *ws, 2, shared=sh)[0]
+        spoil(sh[2], 0, 100, 50, math.nan)
+        y = m.routed_ffn(x, router, *ws, 2, shared=sh)[0]
+        rest = [c for c in range(256) if c != 100]
+        assert torch.isnan(y[:, 100]).all() and torch.equal(y[:, rest], clean[:, rest])
