@@ -235,6 +235,34 @@ struct LayerJob {
   }
 };
 
+// A result from the token's own experts alone, by a warp: see the down kernel's end.
+template <typename T>
+__device__ __noinline__ float own_experts(const RoutedParams &p, const Choice &c, int token, int n) {
+  float sum = 0.f;
+  for (int g = 0; g < c.groups; ++g) {
+    if (!(c.group_mask[g] >> token & 1)) continue;
+    const int e = c.group_expert[g];
+    const FewMatrix &m = e >= p.experts ? p.s_down : p.down;
+    const long long row = (long long)(e >= p.experts ? e - p.experts : e) * p.hidden + n;
+    const uint32_t *codes = static_cast<const uint32_t *>(m.w) + row * (p.inter / 8);
+    const T *scales = reinterpret_cast<const T *>(m.scales) + row * m.groups;
+    const float4 *h = reinterpret_cast<const float4 *>(p.h32 + ((size_t)g * p.rows + token) * p.inter);
+    for (int i = threadIdx.x % 32; i < p.inter / 8; i += 32) {
+      const int group = 8 * i >> m.group_shift;
+      const float zero = m.zeros ? (float)(m.zeros[row * m.groups + group] & 15u) : 8.f;
+      const uint32_t w = codes[i];
+      const float4 lo = __ldcg(h + 2 * i), hi = __ldcg(h + 2 * i + 1);
+      const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+      float part = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) part = fmaf((float)(w >> (4 * k) & 15u) - zero, v[k], part);
+      sum = fmaf(part, to_f32(scales[group]), sum);
+    }
+    if (__any_sync(0xffffffffu, sum != sum)) break;  // its own
+  }
+  return warp_sum(sum);
+}
+
 template <bool UP, typename T, int TOKENS, int PLANES, int GROUPS>
 __global__ void __launch_bounds__(CodeCfg<TOKENS, PLANES, GROUPS>::kThreads, 1)
     routed_codes_kernel(const __grid_constant__ RoutedParams p, const __grid_constant__ RoutedMaps maps, int splits) {
@@ -263,18 +291,29 @@ __global__ void __launch_bounds__(CodeCfg<TOKENS, PLANES, GROUPS>::kThreads, 1)
   code_pipeline<C, TOKENS, PLANES, GROUPS>(job, ring, bars, p.waits);
   if constexpr (!UP) {  // the CTAs' sums in the order of their ranks, a part of the rows by each
     if (splits > 1) cluster_sync();
-    const int part = kCodeRows / splits, row0 = rank * part;
-    for (int i = threadIdx.x; i < part * p.rows; i += C::kThreads) {
-      const int row = row0 + i % part, t = i / part, n = row_tile * kCodeRows + row;
-      float v = 0.f, x[8];
+    // A scale that is not finite is NaN as 0 times it for the tokens that have not chosen its expert: such results are formed
+    // again.  (Without one this is a comparison for each result; a token that is not finite itself is NaN throughout.)
+    const int part = kCodeRows / splits, row0 = rank * part, count = part * p.rows;
+    for (int i0 = 0; i0 < count; i0 += C::kThreads) {
+      const int i = i0 + threadIdx.x, row = row0 + i % part, t = i / part, n = row_tile * kCodeRows + row;
+      const bool in = i < count && n < p.hidden;
+      float v = 0.f, back = 0.f, x[8];
 #pragma unroll
       for (int r = 0; r < 8; ++r)  // all loads before the first sum
-        if (r < splits)
+        if (in && r < splits)
           asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x[r]) : "r"(in_cta(&sums[t * kCodeRows + row], r)) : "memory");
+      if (in) back = way_back(__ldcg(p.h_max + t));
 #pragma unroll
       for (int r = 0; r < 8; ++r)
-        if (r < splits) v += x[r];
-      if (n < p.hidden) static_cast<T *>(p.y)[t * p.ld_y + n] = from_f32<T>(v * 512.f * way_back(__ldcg(p.h_max + t)));
+        if (in && r < splits) v += x[r];
+      const bool bad = v != v && back == back;
+      v = v * 512.f * back;
+      for (unsigned again = __ballot_sync(0xffffffffu, bad); again; again &= again - 1) {
+        const int from = __ffs(again) - 1;
+        const float own = own_experts<T>(p, c, __shfl_sync(0xffffffffu, t, from), __shfl_sync(0xffffffffu, n, from));
+        if (threadIdx.x % 32 == from) v = own;
+      }
+      if (in) static_cast<T *>(p.y)[t * p.ld_y + n] = from_f32<T>(v);
     }
     if (splits > 1) cluster_sync();
   }

@@ -87,8 +87,8 @@ def routed_ffn(x: torch.Tensor, w_router: torch.Tensor, w_gate: Weights, w_up: W
     [count, inter, hidden].  hidden and inter are multiples of 8 (32 with Int4).  Without ``normalise`` the weight is
     route_scale * s.  The hidden values go into the down projection as two numbers of x's type; with 4-bit experts x goes
     through planes as :func:`int4_matmul`'s does and the hidden values through three, 12 significant bits, with one power
-    of two for all of a token's experts, and scales of w_down are finite: what is not in a chosen expert's reaches all
-    tokens of the call.  Returns (y [rows, hidden], indices int32 [rows, top_k], weights float32 [rows, top_k]).
+    of two for all of a token's experts.  What is not finite in a token or an expert reaches that token, or the tokens that
+    have chosen the expert, alone.  Returns (y [rows, hidden], indices int32 [rows, top_k], weights float32 [rows, top_k]).
     """
     if score not in SCORES:
         raise ValueError(f"score must be one of {sorted(SCORES)}")

@@ -522,8 +522,7 @@ int moe_ffn_int4_matmul(const moe_ffn_int4_matmul_args *a, void *stream);
  * With bits 4 x goes through planes as int4_matmul's does, and the hidden values from f32 into three: 12 significant bits down
  * to 2^-15 of the largest, those of a token's experts together, and off by at most 2^-27 of it below.
  * A token that is not finite, or whose hidden values are not, gives results that are not (with bits 4 NaN); the others do
- * not see it.  An infinity or a NaN of an expert's matrix reaches the tokens that have chosen it, with bits 4 one of down
- * all tokens of the call. */
+ * not see it.  An infinity or a NaN of an expert's matrix (with bits 4: scale) reaches the tokens that have chosen it alone. */
 #define MOE_FFN_SCORE_SIGMOID 0
 #define MOE_FFN_SCORE_SOFTMAX 1
 

@@ -132,7 +132,7 @@ def spoil(w, e, row, column, value):
 
 
 @pytest.mark.parametrize("rows,hidden,inter,shared", [(20, 256, 160, 1), (5, 4096, 64, 0), (32, 544, 96, 2), (2, 32, 32, 1)])
-@pytest.mark.parametrize("bits", [16])
+@pytest.mark.parametrize("bits", [16, 4])
 @pytest.mark.parametrize("dtype", [BF16, F16])
 def test_weights_that_are_not_finite_reach_the_tokens_that_chose_them(rows, hidden, inter, shared, bits, dtype):
     """Infinities and NaN in one expert: tokens of the others are as without them, up to the order of their sums."""
