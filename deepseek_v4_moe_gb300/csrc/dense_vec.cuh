@@ -159,8 +159,9 @@ __device__ __forceinline__ ScalePair scales_apart(float a, float b) {
 }
 
 // 1 / (1 + exp(-x)) by the approximate base-2 exponential and reciprocal: a few units of 2^-22, and |x| 2^-23
-// more where it is small, as the exponent's rounding counts (2^-17 at -80); well below the 16-bit types that what is
-// made of it is rounded to; 0 and 1 far out, where exp(-x) overflows or vanishes.  (With subnormals, which change nothing here, each takes several instructions more.)
+// more where it is small, as the exponent's rounding counts (2^-17 at -80); well below the 16 bits, or three planes of
+// FP8, that what is made of it is rounded to; 0 and 1 far out, where exp(-x) overflows or vanishes.  (With subnormals,
+// which change nothing here, each takes several instructions more.)
 __device__ __forceinline__ float fast_sigmoid(float x) {
   float e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
@@ -174,17 +175,30 @@ constexpr float kGelu2 = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 __device__ __forceinline__ float act_value(int act, float g) {
   return g * fast_sigmoid(act == kSilu ? g : kGelu2 * fmaf(0.044715f * g * g, g, g));
 }
-// The same to a few units of 2^-23, wherever it lies: for products that go on in more than 16 bits.  (Near -80 the form
-// above is off by 2^-17.)  1 + e lies in [1, 2], where a step of Newton's method leaves its reciprocal a unit off at most.
-__device__ __forceinline__ float sigmoid_f32(float x) {
-  const float e = expf(-fabsf(x)), d = 1.f + e;
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
-  r = fmaf(r, fmaf(-d, r, 1.f), r);
-  return x < 0.f ? e * r : r;
+// Two of the same within 2^-21 of the value, wherever it lies, for products that go on in more than 16 bits.  (Near -80
+// the form above is off by 2^-17.)  With t = -x log2(e) rounded, exp(-x) = 2^t exp(p), where p = -x - t ln 2 takes two
+// multiply-adds (ln 2 in two parts; t times the first is exact there), lies below 2^-16 and so stands for exp(p) - 1.
+// Within [-88.4, 40] nothing overflows, and past the ends the result is 0 or 1.
+__device__ __forceinline__ float2 sigmoids_f32(float2 x) {
+  const float2 y = make_float2(fmaxf(fminf(-x.x, 88.4f), -40.f), fmaxf(fminf(-x.y, 88.4f), -40.f));
+  const float2 t = __fmul2_rn(y, make_float2(1.44269504f, 1.44269504f));
+  float2 p = __ffma2_rn(t, make_float2(-0.693147182f, -0.693147182f), y);
+  p = __ffma2_rn(t, make_float2(1.9046543e-9f, 1.9046543e-9f), p);
+  float2 e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+  e = __fadd2_rn(__ffma2_rn(e, p, e), make_float2(1.f, 1.f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(e.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(e.y));
+  return r;
 }
-__device__ __forceinline__ float act_f32(int act, float g) {
-  return g * sigmoid_f32(act == kSilu ? g : kGelu2 * fmaf(0.044715f * g * g, g, g));
+__device__ __forceinline__ float2 acts_f32(int act, float2 g) {
+  float2 z = g;
+  if (act != kSilu) {
+    const float2 q = __fmul2_rn(__fmul2_rn(make_float2(0.044715f, 0.044715f), g), g);
+    z = __fmul2_rn(make_float2(kGelu2, kGelu2), __ffma2_rn(q, g, g));
+  }
+  return __fmul2_rn(g, sigmoids_f32(z));
 }
 __device__ __forceinline__ void act_both(int act, float g, float &a, float &da) {
   const float s = fast_sigmoid(act == kSilu ? g : kGelu2 * fmaf(0.044715f * g * g, g, g));

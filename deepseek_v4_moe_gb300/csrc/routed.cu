@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             if (t >= p.rows) break;
             T out = from_f32<T>(0.f), low = out;
             if (mask >> t & 1) {
-              const float x = act_f32(p.act, v[t]) * u[t * 64 + row] * __shfl_sync(0xffffffffu, weight, t);
+              const float x = acts_f32(p.act, make_float2(v[t], v[t])).x * u[t * 64 + row] * __shfl_sync(0xffffffffu, weight, t);
               out = from_f32<T>(x);
               const float rest = x - to_f32(out);  // (an infinity has none)
               if (fabsf(rest) < INFINITY) low = from_f32<T>(rest * kLow<T>);
