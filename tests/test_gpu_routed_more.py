@@ -166,3 +166,76 @@ def test_weights_that_are_not_finite_in_a_shared_expert_reach_all():
         y = m.routed_ffn(x, router, *ws, 2, shared=sh)[0]
         rest = [c for c in range(256) if c != 100]
         assert torch.isnan(y[:, 100]).all() and torch.equal(y[:, rest], clean[:, rest])
+
+
+@pytest.mark.parametrize("rows,hidden,experts,top_k", [(1, 4096, 256, 6), (32, 4096, 256, 8), (32, 1024, 512, 8), (31, 96, 33, 7),
+                                                       (17, 32, 8, 8), (9, 65536, 5, 2), (26, 512, 64, 1)])
+@pytest.mark.parametrize("score,with_bias,router_f32", [("sigmoid", True, False), ("sigmoid", False, True), ("softmax", True, True),
+                                                        ("softmax", False, False)])
+@pytest.mark.parametrize("bits", [16, 4])
+def test_the_choice_of_every_token(bits, score, with_bias, router_f32, rows, hidden, experts, top_k):
+    """Also of tokens whose experts lie so close that 32 bits may order them otherwise: no chosen expert is worse than one left
+    out, and no slot than the next, by more than the logits' errors."""
+    x, router, ws, _, bias = tr.layer(rows, hidden, 32, experts, 0, bits, 32, False, BF16, router_f32, with_bias, seed=11)
+    _, index, weight = m.routed_ffn(x, router, *ws, top_k, bias=bias, score=score)
+    i = index.long()
+    assert ((i >= 0) & (i < experts)).all()
+    assert all(len(set(row)) == top_k for row in i.tolist())
+    l = x.double() @ router.double().T
+    # a lane's sums of hidden / 256 values, then 13 levels: of 65536 values below 2^-15.9 of the magnitudes
+    off = 2.0 ** -15.9 * (x.double().abs() @ router.double().abs().T).amax(1, keepdim=True)
+    s = torch.sigmoid(l) if score == "sigmoid" else l.softmax(1)
+    rank = l
+    if with_bias:  # scores move by less than logits do, and by three roundings of their own
+        rank, off = s + bias.double(), off + 2.0 ** -20
+    got = rank.gather(1, i)
+    left_out = rank.scatter(1, i, -math.inf).amax(1, keepdim=True)
+    assert (got >= left_out - 2 * off).all()
+    assert (got[:, :-1] >= got[:, 1:] - 2 * off).all()
+    w = s.gather(1, i)
+    w = w / w.sum(1, keepdim=True)
+    off = 2.0 ** -15.9 * (x.double().abs() @ router.double().abs().T).amax(1, keepdim=True)
+    assert ((weight.double() - w).abs() <= (4 * off + 2.0 ** -20) * w).all()  # a ratio of exponentials of two logits
+    alone = torch.cat([m.routed_ffn(x[t:t + 1], router, *ws, top_k, bias=bias, score=score)[1] for t in range(rows)])
+    assert torch.equal(alone, index)  # a token's choice does not depend on the others
+
+
+# a bf16 layer of up to eight tokens in groups of 32: tiles of eight groups, two at a time; hidden and inter that end inside
+# a tile of 256 columns, and more units than SMs
+SHORT = [(1, 4128, 160, 40, 6, 1, 32, False, BF16, "sigmoid", True, False, "silu"),
+         (5, 1056, 1312, 24, 4, 0, 32, True, BF16, "softmax", False, True, "gelu"),
+         (8, 288, 2080, 30, 8, 2, 32, True, BF16, "sigmoid", False, False, "silu"),
+         (8, 32, 64, 8, 2, 1, 32, False, BF16, "sigmoid", True, False, "silu")]
+
+
+@pytest.mark.parametrize("case", SHORT, ids=[f"{c[0]}x{c[1]}x{c[2]}" for c in SHORT])
+def test_few_tokens_in_short_groups(case, cuda_lib):
+    rows, hidden, inter, experts, top_k, shared, group, zeros, dtype, score, bias, router_f32, act = case
+    x, router, ws, sh, b = tr.layer(rows, hidden, inter, experts, shared, 4, group, zeros, dtype, router_f32, bias, seed=7)
+
+    def call():
+        return m.routed_ffn(x, router, *ws, top_k, bias=b, score=score, shared=sh, activation=act)
+
+    want = call()
+    tr.check(want, x, router, ws, top_k, sh, act, b, score)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(3):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append(call())
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kept = call()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, c) for g in [*got, kept] for a, c in zip(g, want))
+    assert cuda_lib.moe_ffn_dense_fault_injection(1, 20000) == 0
+    try:
+        call()
+        assert m.dense_status() == 8
+    finally:
+        cuda_lib.moe_ffn_dense_fault_injection(0, 0)
+    assert all(torch.equal(a, c) for a, c in zip(call(), want)) and m.dense_status() == 0
