@@ -5,8 +5,9 @@
 // much as one, the sums are f32, and the work left to the CUDA cores is the codes' conversion to 16 bits, in registers.
 // It takes x as it is, so that a product is one launch; where the conversion bounds it, few_tc.cuh's form is faster.
 //
-// TMA brings 64 bytes (128 columns) of each of a strip's rows into a ring, and the tokens' columns beside them: with the addresses in every lane 16 tokens by 129280 x 4096 took 165 us at 1.6 instructions a cycle, and
-// with the tokens read through the L1 their latency stopped the warps.
+// TMA brings 64 bytes (128 columns) of each of a strip's rows into a ring, and the tokens' columns beside them: with the
+// addresses in every lane 16 tokens by 129280 x 4096 took 165 us at 1.6 instructions a cycle, and with the tokens read through
+// the L1 their latency stopped the warps.
 // The order of k within a tile is free as long as both operands have the same one: lane 4 g + t of a warp holds columns
 // 32 c + 8 t .. + 7 of row g (and g + 8), as one 16-byte read of x gives them for token g.
 #pragma once
@@ -43,7 +44,9 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
 }
 
 // Pairs of code - zero in T from a word's codes: nibbles i and i + 4, for i = 0 .. 3.  A code in the low mantissa bits of
-// 128 (bf16) or 1024 (f16) is that number plus the code; the difference to the same number plus the zero point is exact.
+// 128 (bf16) or 1024 (f16) is that number plus the code; the difference to the same number plus the zero point is exact
+// (widening codes so, without conversions: Y. J. Kim, R. Henry, R. Fahim and H. H. Awadalla, "Who Says Elephants Can't Run:
+// Bringing Large Scale MoE Models into Cloud Scale Production", 2022).
 // f16 has mantissa bits for a code four places up as well, which is sixteen times the code: (1024 + 16 c) / 16 - (64 + z)
 // in one multiply-add, so that two of three shifts are saved.
 template <typename T>
@@ -91,7 +94,7 @@ __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t at) {
 // The right operand of a tile in shared memory: pieces of 32 columns, each `rows` tokens' 64 bytes one after another, in
 // the same swizzle as the weights.  A lane's 16 bytes of a piece for its token of eight i.  ROWS8: rows is a multiple of
 // 8, so that a piece is that many bytes from the one before.
-template <int PIECES, int NT, bool ROWS8>
+template <int PIECES, bool ROWS8>
 struct Operand {
   uint32_t at[ROWS8 ? 1 : PIECES];
   uint32_t pitch;  // of a piece
@@ -173,7 +176,7 @@ __device__ __forceinline__ uint4 in_pairs(const uint4 v) {
 template <typename T, int PIECES, bool ZP, int M, int NT, bool ROWS8>
 struct Tile {
   static constexpr int kGroups = 4 / PIECES;
-  Operand<4, NT, ROWS8> x;
+  Operand<4, ROWS8> x;
   Meta<PIECES, M, ZP> meta;
   __device__ __forceinline__ void multiply(uint32_t place, uint32_t tokens, float (&acc)[M][NT][4]) const {
     const int lane = threadIdx.x & 31, r = lane & 15, c0 = lane >> 4;

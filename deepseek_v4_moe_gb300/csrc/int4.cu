@@ -179,8 +179,8 @@ cudaError_t int4_tiles(const Int4MatmulParams &p, const Int4Maps &maps, const In
 // to their type first, and are 1 for zeros and at least its smallest normal value.  Eight values a lane, a group's in
 // 4, 8 or 16 lanes; bound by the weights' bytes.
 
-// A warp's next kChunks neighbouring chunks of CHUNK columns of a row: row and first chunk, from its number on.
-template <int CHUNK, int KCHUNKS>
+// A warp's chunks of CHUNK columns of a row: row and chunk, from its number on.
+template <int CHUNK>
 struct RowChunks {
   long long row;
   int at, per_row, rows_on, at_on;
@@ -188,13 +188,13 @@ struct RowChunks {
     const int warps = blockDim.x >> 5;
     const long long first = (long long)blockIdx.x * warps + (threadIdx.x >> 5);
     const long long step = (long long)gridDim.x * warps;
-    per_row = (k + CHUNK * KCHUNKS - 1) / (CHUNK * KCHUNKS);
+    per_row = (k + CHUNK - 1) / CHUNK;
     row = first / per_row;
     at = (int)(first - row * per_row);
     rows_on = (int)(step / per_row);
     at_on = (int)(step % per_row);
   }
-  __device__ __forceinline__ int column() const { return at * (CHUNK * KCHUNKS); }
+  __device__ __forceinline__ int column() const { return at * CHUNK; }
   __device__ __forceinline__ void next() {
     row += rows_on;
     at += at_on;
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(256, 4) int4_quantise_kernel(const __grid_cons
   constexpr float kLeast = std::is_same<TS, __half>::value ? 6.103515625e-05f : 1.17549435e-38f;
   constexpr float kInteger = 12582912.f;  // 1.5 2^23: a sum with it has the whole number nearest in its low bits
   const int lane = threadIdx.x & 31, groups = (p.k + 8 * PER - 1) / (8 * PER);
-  RowChunks<256, 1> c(p.k);
+  RowChunks<256> c(p.k);
   Eight<T, true> ahead;
   auto load = [&] {
     const int col = c.column() + 8 * lane;
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(256, 4) int4_quantise_kernel(const __grid_cons
 template <typename T>
 __global__ void __launch_bounds__(256) int4_widen_kernel(const __grid_constant__ Int4WeightParams p) {
   const int lane = threadIdx.x & 31, groups = (p.k + p.group - 1) / p.group, shift = p.group == 32 ? 5 : p.group == 64 ? 6 : 7;
-  RowChunks<512, 1> c(p.k);
+  RowChunks<512> c(p.k);
   pdl_wait();
   for (; c.row < p.n; c.next()) {
     const int col = c.column() + 16 * lane;

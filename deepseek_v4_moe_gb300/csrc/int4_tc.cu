@@ -182,15 +182,20 @@ cudaError_t tc_typed(const Int4MatmulParams &p, const Int4Maps &maps, int tokens
 
 }  // namespace
 
-// Splitting x takes a launch (4096 x 4096 in groups of 128: 7.1 us for a token, 7.9 for 16, by mma.sync 6.0 and 7.7), which
-// large matrices have time for (16384 x 2048: 7.0 and 8.4 for 7.6 and 8.8; 8192 x 8192: 13.7 and 16.0 for 18.4 and 18.3;
-// 129280 x 4096: 46 and 54 for 68 and 93), in groups of 64 larger ones (16384 x 2048 in f16: 7.7 and 10.1 for 7.4 and 8.8,
-// 8192 x 8192: 15.9 and 20.2 for 18.1 and 18.9, in bf16 15.5 and 17.3 for 18.6 and 18.9), and long rows of more than eight
-// tokens (512 x 8192, 16 tokens: 8.7 for 13.3, groups of 64: 8.8 for 13.4).  In groups of 32 the joining of eight groups
-// takes what the conversion saves (129280 x 4096: 91 and 115 for 96 and 111).  Beyond 16 tokens mma.sync's registers leave
-// it behind (4096 x 4096, 32 tokens: 9.2 for 16.5; 1031 x 2016: 7.0 for 9.3), but for groups of 32 of many rows
-// (8192 x 8192: 32 for 51, 16384 x 2048: 17 for 16; 64 tokens, twice 32 here, 2048 x 8192: 19 for 32, 4096 x 4096: 19 for
-// 17.5).
+// Which form serves a call, measured on weights that come from memory (bf16, us, planes and mma.sync; n of 512 to 65536, k of
+// 512 to 16384):
+//   Up to 16 tokens splitting x takes a launch (4096 x 4096 in groups of 128: 7.9 and 6.0 for a token, 8.9 and 7.7 for 16),
+//   which large matrices have time for (8192 x 8192: 12.8 and 18.5, 15.3 and 17.8; 65536 x 4096: 28 and 39, 34 and 50; about
+//   even at 2^25: 8192 x 4096 9.9 and 10.9, 11.0 and 10.0, 16384 x 2048 8.4 and 8.1, 9.6 and 9.0), in groups of 64 larger ones
+//   (8192 x 4096: 10.9 and 11.1, 11.8 and 10.6; 8192 x 8192: 15.0 and 18.6, 16.3 and 18.7), and so have long rows of more than
+//   eight tokens (512 x 8192, 16 tokens: 8.8 and 13.2; with one 7.7 and 8.2).  In groups of 32 the joining of eight groups
+//   takes what the conversion saves (65536 x 4096: 55 and 49, 69 and 59; 8192 x 8192: 18.8 and 20.2, 23 and 20).
+//   Beyond 16 tokens mma.sync's registers leave it behind (32 tokens by 4096 x 4096: 10.0 and 15.8; 65536 x 4096: 42 and 72),
+//   but for groups of 32 of many rows (8192 x 4096: 19.7 and 28; 16384 x 4096: 29.3 and 28.3; 65536 x 4096: 100 and 89; 64
+//   tokens, twice 32 here, by 2048 x 4096: 13.1 and 17.5, by 4096 x 4096: 19.2 and 17.6).
+// Where it is not the faster one: beyond 16 tokens at k below about 1024 in groups of 128 and 64, 2048 in groups of 32
+// (4096 x 512: 7.0 and 4.0, 4096 x 1024: 7.1 and 5.8), up to 16 tokens at k of 16384 and few rows (512 x 16384, a token: 10.7
+// and 14.3; 16 in groups of 32 15.4 and 25.9), and in f16 of 16 tokens in groups of 64 (65536 x 1024: 20.9 and 17.2).
 int int4_tc_tokens(int rows, int n, int k, int group) {
   const long long blocks = (rows + 31) / 32;
   if (group == 32) return rows > 16 && n * blocks * blocks <= 12000 ? 32 : 0;

@@ -27,7 +27,7 @@ __global__ void __launch_bounds__(256) routed_logits_kernel(const __grid_constan
 
 // The weights are the left operand as they lie (128 rows x 64 columns a step, K-major, by TMA), all tokens' columns the
 // right one, so that nothing but copies and one instruction for 16 columns is left: the kernels run at the pace of memory.
-// (On mma.sync, a warp's strips of 16 rows as above, one token of 256 experts of 4096 x 2048 took 72 to 83 us: copies of
+// (On mma.sync, a strip of 16 rows to a warp, one token of 256 experts of 4096 x 2048 took 72 to 83 us: copies of
 // 16 rows x 64 bytes do not come faster than 3.2 TB/s.)
 //
 // Up: a tile is 64 rows of gate and 64 of up; two accumulators in TMEM, so that a tile's epilogue runs beside the next
@@ -170,7 +170,6 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       }
     };
     if (UP) group = unit / tiles;
-    bool ok = true;
     if constexpr (!UP) {  // the first weights need not wait for h
       const int g0 = group, k0 = k;
       for (; j < kTcStages && step < end; ++j, next()) weights(j);
@@ -187,14 +186,10 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       for (int i = 0; i < j; ++i) pos.next();
     }
     for (; unit < units && step < end; ++j, pos.next(), next()) {
-      if (!warp_wait(&empty[pos.slot], pos.round ^ 1u, abort_p, w.status, w.ns)) {
-        ok = false;
-        break;
-      }
+      if (!warp_wait(&empty[pos.slot], pos.round ^ 1u, abort_p, w.status, w.ns)) break;
       weights(pos.slot);
       tokens(pos.slot, group, k);
     }
-    (void)ok;
     if (lane == 0) issued = j;
   } else if (warp == 1) {
     // ---------------- products ----------------
