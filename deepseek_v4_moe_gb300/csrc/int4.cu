@@ -177,7 +177,7 @@ cudaError_t int4_tiles(const Int4MatmulParams &p, const Int4Maps &maps, const In
 // Symmetric: scale = max|w| / 7, code = 8 + w / scale in 1..15.  With zero points: scale = (max(w, 0) - min(w, 0)) / 15,
 // zero = -min(w, 0) / scale, code = zero + w / scale in 0..15.  Quotients are rounded to nearest even; scales are rounded
 // to their type first, and are 1 for zeros and at least its smallest normal value.  Eight values a lane, a group's in
-// 4, 8 or 16 lanes; bound by the weights' bytes.
+// 4, 8 or 16 lanes.
 
 // A warp's chunks of CHUNK columns of a row: row and chunk, from its number on.
 template <int CHUNK>
@@ -206,8 +206,9 @@ struct RowChunks {
 };
 
 // The quotients are those of dense_quant.cuh, without a division for each value (all of them divided, with a 64-bit
-// division for a lane's place besides: 4096 x 2048 made and widened 22.9 us, now 14.0, of which 8.9 and 5.1); a warp has its
-// next columns' loads in flight (two ahead changed nothing).  Bound by its instructions, some 150 for eight values.
+// division for a lane's place besides: 4096 x 2048 made and widened 22.9 us, now 14.1; each by itself, from memory, 8.9 and
+// 6.1, for 3.1); a warp has its next columns' loads in flight (two ahead changed nothing).  Bound by its instructions, some
+// 150 for eight values.
 template <typename T, typename TS, int PER, bool ZP>  // PER: lanes of a group
 __global__ void __launch_bounds__(256, 4) int4_quantise_kernel(const __grid_constant__ Int4WeightParams p) {
   constexpr float kLeast = std::is_same<TS, __half>::value ? 6.103515625e-05f : 1.17549435e-38f;

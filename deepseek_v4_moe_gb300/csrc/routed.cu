@@ -8,8 +8,8 @@
 // Bound by the chosen experts' weights on their way from memory: each is read once, for all of its tokens.  Column j of
 // the tensor cores' right operand is token j for every expert (zeros where it did not choose it), so the down kernel adds
 // all experts' products in its accumulators: no partial results in memory, and one order of every sum.
-// One token through 256 experts of 4096 x 2048 and a shared one, six each: 65.5 us, 5.4 TB/s (52 at the copy's rate): gate and
-// up read at 5.7 TB/s once they know the experts.  5 tokens through 60 experts of 1000 x 424: 22.3 us (6.6), three kernels'
+// One token through 256 experts of 4096 x 2048 and a shared one, six each: 65.6 us, 5.4 TB/s (52 at the copy's rate): gate and
+// up read at 5.7 TB/s once they know the experts.  5 tokens through 60 experts of 1000 x 424: 22.7 us (6.6), three kernels'
 // latencies.
 #include "dense_tc.cuh"
 #include "kernels.h"

@@ -2,18 +2,18 @@
 //
 //   route   l = x Wr^T, and x as planes
 //   up      each CTA chooses the experts from l; h = weight act(x Wg_e^T) (x Wu_e^T), in f32
-//   split   h as planes: three, so that 12 significant bits are left of either type's products
+//   split   h as planes: three, in either type
 //   down    y = sum over the experts of h Wd_e^T
 //
 // Bound by the chosen experts' codes on their way from memory and through registers into operands: each is read once, for
 // all tokens, which are the right operand's columns for every expert.  So the down kernel, whose operand is zero where a
 // token has not chosen an expert, adds all experts' products in its registers, in one order.
-// 16 tokens through 256 experts of 4096 x 2048 and a shared one, six each, in groups of 128: 217 us, 4.9 TB/s (157 at the
-// copy's rate; on mma.sync, each expert's tokens eight at a time, 577); one token 40 us (13.7), of which the four kernels'
-// latencies are the most: gate and up have 224 strips for 152 SMs.  32 tokens 491 us (263).
+// 16 tokens through 256 experts of 4096 x 2048 and a shared one, six each, in groups of 128: 221 us, 4.8 TB/s (157 at the
+// copy's rate; on mma.sync, each expert's tokens eight at a time, 577); one token 41 us (13.7), of which the four kernels'
+// latencies are the most: gate and up have 224 strips for 152 SMs.  32 tokens 500 us (263).
 //
 // A token's h has one power of two for all of its experts, from the largest magnitude among them (an atomic maximum: of
-// any order the same), so that their products can be added as they are: what is lost of an expert's h is below 2^-12 of it
+// any order the same), so that their products can be added as they are: what is lost of an expert's h is at most 2^-14 of it
 // or 2^-27 of the token's largest, and the sum that it goes to holds that one.  It has three planes in bf16 too: h rounded
 // to 16 bits, in two planes, left the layer off by 0.0024 in 2-norm where y's rounding leaves 0.0017 (16 tokens 230 us for
 // 231, 32 tokens in groups of 32 1210 for 1440).

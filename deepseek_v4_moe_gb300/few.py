@@ -62,7 +62,8 @@ def int4_matmul(x: torch.Tensor, w: Int4, out: Optional[torch.Tensor] = None,
     there; the result [rows, n] is of x's type.  Made for up to 32 rows; more are taken 32 at a time.
 
     Large products and those of more rows take x in FP8 planes: exact down to 2^-14 of a row's largest magnitude (float16:
-    2^-16), off by at most 2^-22 (2^-27) of it below that; a row that is not finite gives NaN there.
+    2^-16), off by at most 2^-22 (2^-27) of it below that.  A row that is not finite gives no finite result: NaN there,
+    infinities among them elsewhere.
     """
     if stream is not None:
         with _on(x, stream):
@@ -86,8 +87,8 @@ def routed_ffn(x: torch.Tensor, w_router: torch.Tensor, w_gate: Weights, w_up: W
     or all :class:`Int4` of one group; ``shared``: the same three of the shared experts, [inter, hidden] for one or
     [count, inter, hidden].  hidden and inter are multiples of 8 (32 with Int4).  Without ``normalise`` the weight is
     route_scale * s.  The hidden values go into the down projection as two numbers of x's type; with 4-bit experts x goes
-    through planes as :func:`int4_matmul`'s does and the hidden values through three, 12 significant bits, with one power
-    of two for all of a token's experts.  What is not finite in a token or an expert reaches that token, or the tokens that
+    through planes as :func:`int4_matmul`'s does and the hidden values through three, off by at most 2^-14 of a value or
+    2^-27 of the token's largest.  What is not finite in a token or an expert reaches that token, or the tokens that
     have chosen the expert, alone.  Returns (y [rows, hidden], indices int32 [rows, top_k], weights float32 [rows, top_k]).
     """
     if score not in SCORES:

@@ -490,7 +490,10 @@ int moe_ffn_int4_widen(const moe_ffn_int4_weights_args *a, void *out, int64_t ld
  * in f32 and multiplied by its scale there.  Made for up to 32 rows; more are taken 32 at a time.
  * Where the call needs a workspace, x goes through it as a row's values over a power of two in FP8 planes: exact down to
  * 2^-14 of the row's largest magnitude, below that off by at most 2^-22 of it (f16: 2^-16 and 2^-27); magnitudes below
- * 2^-119 count as that in this.  There a row with a NaN or an infinity gives NaN throughout. */
+ * 2^-119 count as that in this, and sums are taken over that power of two before they are multiplied by scales, which
+ * have to leave them in f32's range (as scales between 2^-100 and 2^100 do).
+ * A row with a NaN or an infinity gives no finite result: NaN where the call needs a workspace, the products' infinities and
+ * NaN where it needs none. */
 typedef struct moe_ffn_int4_matmul_args {
   int32_t rows, n, k;            /* rows at most 2^16; n and k as above */
   int32_t type;                  /* of x, scales and out: MOE_FFN_BF16 or _F16 */
@@ -519,8 +522,8 @@ int moe_ffn_int4_matmul(const moe_ffn_int4_matmul_args *a, void *stream);
  *       E(x) = (act(x gate^T) * (x up^T)) down^T
  * weight * act(g) * u (a shared expert's without a weight) goes into the down projection as two numbers of the operand type:
  * 16 significant bits (f16: 22, but no more than 2^-36, and its range).
- * With bits 4 x goes through planes as int4_matmul's does, and the hidden values from f32 into three: 12 significant bits down
- * to 2^-15 of the largest, those of a token's experts together, and off by at most 2^-27 of it below.
+ * With bits 4 x goes through planes as int4_matmul's does, and the hidden values from f32 into three: off by at most 2^-14 of
+ * a value, or 2^-27 of the largest of all of the token's experts.
  * A token that is not finite, or whose hidden values are not, gives results that are not (with bits 4 NaN); the others do
  * not see it.  An infinity or a NaN of an expert's matrix (with bits 4: scale) reaches the tokens that have chosen it alone. */
 #define MOE_FFN_SCORE_SIGMOID 0
