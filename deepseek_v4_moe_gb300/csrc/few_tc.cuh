@@ -7,9 +7,10 @@
 // codes; mma.sync's FP8 form is made of 16-bit products, with a conversion of either operand each time: 146 us.)
 //
 // The right operand is split beforehand: scaled by a power of two, so that its largest magnitude lies in [128, 256), into
-// p0 = e4m3(x), p1 = e4m3(32 (x - p0)) and, for f16, p2 = e4m3(32 (32 (x - p0) - p1)).  Each plane takes four significant
-// bits, so that two are a bf16 number and three an f16 one: exactly down to 2^-14 of the largest magnitude (f16: 2^-16),
-// below that to 2^-22 of it (2^-27; two planes without the 32: 2^-17).  The planes are columns of their own; a group's
+// p0 = e4m3(x), p1 = e4m3(32 (x - p0)) and, for f16 and the routed layer's hidden values, p2 = e4m3(32 (32 (x - p0) - p1)).
+// Each plane takes four significant bits, so that two are a bf16 number and three an f16 one: exactly down to 2^-14 of the
+// largest magnitude (f16: 2^-16), below that to 2^-22 of it (2^-27; two planes without the 32: 2^-17).  Half a step of three
+// is 2^-14 of an f32 value.  The planes are columns of their own; a group's
 // products are joined in f32, its zero point is applied to its sum of x, and its scale to the result, once for each group:
 //   acc += scale (sum(code p0) + sum(code p1) / 32 + .. - zero sum(x))
 //
